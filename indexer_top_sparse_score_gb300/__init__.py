@@ -22,7 +22,7 @@ _CSRC = os.path.join(_HERE, "csrc")
 _INCLUDE = os.path.join(os.path.dirname(_HERE), "include")
 _BUILD = os.path.join(_HERE, "_build")
 LIB_PATH = os.path.join(_BUILD, "libsmla.so")
-SOURCES = ["api.cu", "indexer.cu", "mla.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "indexer.cu", "mla.cu", "noalloc.cu", "prefix.cu", "serve.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC"]
 
@@ -51,7 +51,8 @@ def _stale() -> bool:
     if not os.path.exists(LIB_PATH):
         return True
     t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(_CSRC, f) for f in os.listdir(_CSRC)] + [os.path.join(_INCLUDE, "smla.h")]
+    deps = [os.path.join(_CSRC, f) for f in os.listdir(_CSRC)] + [os.path.join(_INCLUDE, f)
+                                                                  for f in os.listdir(_INCLUDE)]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -111,6 +112,26 @@ _SIGS = {
     "smla_read_status": (ctypes.c_int, [_vp, _vp, ctypes.POINTER(ctypes.c_uint32)]),
 }
 
+class RopeTable(ctypes.Structure):
+    """smla_rope: cos_sin [max_pos][64] and the pairing of the rotated values."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int32), ("kv_interleaved", ctypes.c_int32),
+                ("idx_interleaved", ctypes.c_int32)]
+
+
+_i64 = ctypes.c_int64
+# include/smla_serve.h
+_SERVE_SIGS = {
+    "smla_build_tables": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                         _vp, _sz, _vp]),
+    "smla_cache_append": (ctypes.c_int, [_vp, _vp, _i32, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _f32, _vp,
+                                         _sz, _vp]),
+    "smla_query_prep": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp,
+                                       _f32, _vp, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "smla_shared_prefix_fwd_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "smla_shared_prefix_fwd": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _f32, _vp, _vp,
+                                              _vp, _sz, _vp]),
+}
+
 
 def lib(build_if_missing: bool = False):
     """The loaded libsmla.so. Raises if it has not been built (no fallback)."""
@@ -123,7 +144,7 @@ def lib(build_if_missing: bool = False):
                 raise RuntimeError(f"libsmla.so is not built ({LIB_PATH}); run "
                                    "indexer_top_sparse_score_gb300.build() first")
             L = ctypes.CDLL(LIB_PATH)
-            for name, (res, args) in _SIGS.items():
+            for name, (res, args) in {**_SIGS, **_SERVE_SIGS}.items():
                 f = getattr(L, name)
                 f.restype = res
                 f.argtypes = args
@@ -377,6 +398,152 @@ def sparse_mla_decode(cache, page_tables, seq_lens, max_seq_len, q_per_seq, q, q
                                   _stream(stream))
     _check(rc, "smla_sparse_mla_decode")
     return out, lse, out_idx, ws
+
+
+# ---------------------------------------------------------------------------- serving steps
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def build_tables(ctx_lens, new_lens, page_tables, free_pages, max_new, *, seq_lens=None, cu_new=None,
+                 positions=None, slots=None, row_seq=None, pages_used=None, ws=None, stream=None):
+    """Pages and slots of every request's next tokens (see smla_build_tables);
+    page_tables is updated in place. Returns (seq_lens, cu_new, positions, slots,
+    row_seq, pages_used, ws)."""
+    L = lib()
+    n, max_pages = page_tables.shape
+    dev = page_tables.device
+    for t in (ctx_lens, new_lens, page_tables, free_pages, seq_lens, cu_new, positions, slots, row_seq, pages_used):
+        _need(t is None or (t.dtype == torch.int32 and t.is_contiguous()), "lengths, tables and maps are contiguous int32")
+    _need(ctx_lens.numel() == n and new_lens.numel() == n, "one length per row of page_tables")
+
+    def out(t, k):
+        _need(t is None or t.numel() >= k, "an output is too small")
+        return torch.empty(k, dtype=torch.int32, device=dev) if t is None else t
+
+    seq_lens, cu_new, pages_used = out(seq_lens, n), out(cu_new, n + 1), out(pages_used, 1)
+    positions, slots, row_seq = out(positions, max_new), out(slots, max_new), out(row_seq, max_new)
+    if ws is None:
+        ws = workspace(STATUS_BYTES, dev)
+    rc = L.smla_build_tables(_p(ctx_lens), _p(new_lens), n, _p(page_tables), max_pages, _p(free_pages),
+                             0 if free_pages is None else free_pages.numel(), max_new, _p(seq_lens), _p(cu_new),
+                             _p(positions), _p(slots), _p(row_seq), _p(pages_used), _p(ws), ws.numel(),
+                             _stream(stream))
+    _check(rc, "smla_build_tables")
+    return seq_lens, cu_new, positions, slots, row_seq, pages_used, ws
+
+
+def _rope(table, kv_interleaved, idx_interleaved) -> RopeTable:
+    _need(table.dtype == torch.float32 and table.dim() == 2 and table.shape[1] == 64 and table.is_contiguous(),
+          "rope is a contiguous fp32 [max_pos, 64] table")
+    return RopeTable(_p(table), table.shape[0], int(kv_interleaved), int(idx_interleaved))
+
+
+def cache_append(cache, slots, positions, rope, *, ckv=None, kv_norm=None, k_idx=None, idx_norm=None, idx_bias=None,
+                 eps=1e-6, kv_interleaved=True, idx_interleaved=False, ws=None, stream=None):
+    """Norm, rotation, quantisation and paged write of new latent rows (ckv
+    [rows, 576] bf16) and indexer keys (k_idx [rows, d_idx] bf16) into `cache`
+    (see smla_cache_append). Rows may be strided. Returns ws."""
+    L = lib()
+    rows = slots.numel()
+    _need(slots.dtype == torch.int32 and positions.dtype == torch.int32 and positions.numel() == rows,
+          "slots and positions are int32, one per row")
+    for x, d in ((ckv, D_QK), (k_idx, cache.k_idx.shape[-1])):
+        _need(x is None or (x.dtype == torch.bfloat16 and x.shape == (rows, d) and x.stride(1) == 1),
+              "rows are bf16 [rows, width] with values next to each other")
+    for t, d in ((kv_norm, D_V), (idx_norm, cache.k_idx.shape[-1]), (idx_bias, cache.k_idx.shape[-1])):
+        _need(t is None or (t.dtype == torch.float32 and t.numel() == d and t.is_contiguous()), "norm weights are fp32")
+    if ws is None:
+        ws = workspace(STATUS_BYTES, slots.device)
+    c, r = make_cache(cache), _rope(rope, kv_interleaved, idx_interleaved)
+    rc = L.smla_cache_append(ctypes.byref(c), ctypes.byref(r), rows, _p(slots), _p(positions), _p(ckv),
+                             0 if ckv is None else ckv.stride(0), _p(kv_norm), _p(k_idx),
+                             0 if k_idx is None else k_idx.stride(0), _p(idx_norm), _p(idx_bias), float(eps), _p(ws),
+                             ws.numel(), _stream(stream))
+    _check(rc, "smla_cache_append")
+    return ws
+
+
+def query_prep(positions, rope, *, q_pe=None, q=None, q_idx_raw=None, w=None, idx_dtype="fp8", idx_norm=None,
+               eps=1e-6, w_scale=1.0, kv_interleaved=True, idx_interleaved=False, q_idx=None, w_out=None, ws=None,
+               stream=None):
+    """Rotation of the attention queries' 64 rope values (q_pe [rows, H, 64],
+    strided) into the last 64 values of q [rows, H, 576], and norm, rotation and
+    quantisation of the indexer queries q_idx_raw [rows, h_idx, d_idx] with the
+    scale folded into the head weights (see smla_query_prep). Returns (q, q_idx,
+    w_out, ws)."""
+    L = lib()
+    rows = positions.numel()
+    _need(positions.dtype == torch.int32, "positions are int32")
+    n_heads = h_idx = d_idx = pe_row = pe_head = raw_row = 0
+    if q_pe is not None:
+        n_heads = q_pe.shape[1]
+        _need(q_pe.dtype == torch.bfloat16 and q_pe.shape == (rows, n_heads, D_QK - D_V) and q_pe.stride(2) == 1,
+              "q_pe is bf16 [rows, heads, 64] with values next to each other")
+        if q is None:
+            q = torch.empty((rows, n_heads, D_QK), dtype=torch.bfloat16, device=q_pe.device)
+        _need(q.dtype == torch.bfloat16 and q.shape == (rows, n_heads, D_QK) and q.is_contiguous(),
+              "q is contiguous bf16 [rows, heads, 576]")
+        pe_row, pe_head = q_pe.stride(0), q_pe.stride(1)
+    if q_idx_raw is not None:
+        h_idx, d_idx = q_idx_raw.shape[1:]
+        _need(q_idx_raw.dtype == torch.bfloat16 and q_idx_raw.shape[0] == rows and q_idx_raw.stride(2) == 1
+              and q_idx_raw.stride(1) == d_idx, "q_idx_raw is bf16 [rows, h_idx, d_idx], each row dense")
+        _need(w is not None and w.dtype == torch.float32 and w.shape == (rows, h_idx) and w.is_contiguous(),
+              "w is contiguous fp32 [rows, h_idx]")
+        raw_row = q_idx_raw.stride(0)
+        if q_idx is None:
+            q_idx = torch.empty((rows, h_idx, d_idx), device=w.device,
+                                dtype=torch.bfloat16 if idx_dtype == "bf16" else torch.uint8)
+        _need(q_idx.shape == (rows, h_idx, d_idx) and q_idx.is_contiguous()
+              and q_idx.element_size() == (2 if idx_dtype == "bf16" else 1), "q_idx does not fit idx_dtype")
+        if w_out is None:
+            w_out = torch.empty_like(w)
+        _need(w_out.dtype == torch.float32 and w_out.shape == w.shape and w_out.is_contiguous(), "w_out is like w")
+        _need(idx_norm is None or (idx_norm.dtype == torch.float32 and idx_norm.numel() == d_idx
+                                   and idx_norm.is_contiguous()), "idx_norm is fp32 [d_idx]")
+    if ws is None:
+        ws = workspace(STATUS_BYTES, positions.device)
+    r = _rope(rope, kv_interleaved, idx_interleaved)
+    rc = L.smla_query_prep(ctypes.byref(r), rows, _p(positions), _p(q_pe), pe_row, pe_head, n_heads, _p(q),
+                           _p(q_idx_raw), raw_row, h_idx, d_idx, _dtype_code(idx_dtype), _p(idx_norm), float(eps),
+                           _p(w), float(w_scale), _p(q_idx), _p(w_out), _p(ws), ws.numel(), _stream(stream))
+    _check(rc, "smla_query_prep")
+    return q, q_idx, w_out, ws
+
+
+def shared_prefix_workspace_bytes(n_seqs, max_seq_len, shared_len, q_per_seq, n_heads) -> int:
+    return lib().smla_shared_prefix_fwd_workspace_size(n_seqs, max_seq_len, shared_len, q_per_seq, n_heads)
+
+
+def shared_prefix_fwd(cache, page_tables, seq_lens, max_seq_len, shared_len, q_per_seq, q, sm_scale, *, out=None,
+                      lse=None, ws=None, stream=None):
+    """Attention of a batch whose requests share their first shared_len tokens:
+    the shared part is read once for all query rows (see smla_shared_prefix_fwd).
+    Returns (out, lse, ws)."""
+    L = lib()
+    n_seqs, max_pages = page_tables.shape
+    rows, H, _ = q.shape
+    _need(q.dtype == torch.bfloat16 and q.is_contiguous() and q.shape[2] == D_QK and rows == n_seqs * q_per_seq,
+          "q is contiguous bf16 [n_seqs * q_per_seq, heads, 576]")
+    _need(page_tables.dtype == torch.int32 and page_tables.is_contiguous() and seq_lens.dtype == torch.int32
+          and seq_lens.numel() == n_seqs and seq_lens.is_contiguous(), "page_tables and seq_lens are contiguous int32")
+    if out is None:
+        out = torch.empty((rows, H, D_V), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((rows, H), dtype=torch.float32, device=q.device)
+    _need(out.dtype == torch.bfloat16 and out.shape == (rows, H, D_V) and out.is_contiguous()
+          and lse.dtype == torch.float32 and lse.shape == (rows, H) and lse.is_contiguous(),
+          "out is contiguous bf16 [rows, heads, 512], lse fp32 [rows, heads]")
+    if ws is None:
+        ws = workspace(shared_prefix_workspace_bytes(n_seqs, max_seq_len, shared_len, q_per_seq, H), q.device)
+    c = make_cache(cache)
+    rc = L.smla_shared_prefix_fwd(ctypes.byref(c), _p(page_tables), max_pages, n_seqs, _p(seq_lens), max_seq_len,
+                                  shared_len, q_per_seq, _p(q), H, float(sm_scale), _p(out), _p(lse), _p(ws),
+                                  ws.numel(), _stream(stream))
+    _check(rc, "smla_shared_prefix_fwd")
+    return out, lse, ws
 
 
 def read_status(ws: torch.Tensor, stream=None):

@@ -33,6 +33,16 @@ EncodeTiledFn encode_fn() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool valid_h_idx(int h) { return h == 4 || h == 8 || h == 16 || h == 32 || h == 64; }
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+int reset_status(void* ws, cudaStream_t st) {
+  return cudaMemsetAsync(ws, 0, 4, st) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+}  // namespace
+
 int check_cache(const smla_paged_cache* c, bool need_kv, bool need_idx) {
   if (!c) return SMLA_ERR_INVALID_ARG;
   if (c->page_size != kPage || c->num_pages <= 0) return c->page_size != kPage && c->page_size > 0
@@ -54,16 +64,6 @@ int check_cache(const smla_paged_cache* c, bool need_kv, bool need_idx) {
   }
   return SMLA_OK;
 }
-
-bool valid_h_idx(int h) { return h == 4 || h == 8 || h == 16 || h == 32 || h == 64; }
-
-size_t round256(size_t b) { return (b + 255) / 256 * 256; }
-
-int reset_status(void* ws, cudaStream_t st) {
-  return cudaMemsetAsync(ws, 0, 4, st) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
-}
-
-}  // namespace
 
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner_elems,
                uint64_t rows, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows,

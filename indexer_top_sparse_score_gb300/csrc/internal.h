@@ -83,6 +83,9 @@ size_t mla_shadow_bytes(int32_t n_keys, int32_t kv_dtype);
 // Fills the shadow from the pool through the page table (one sequence).
 int launch_shadow_convert(const MlaLaunch& L);
 
+// Argument checks of a cache whose latent rows / indexer keys the call uses.
+int check_cache(const smla_paged_cache* c, bool need_kv, bool need_idx);
+
 // Whether the indexer runs token groups over the full key range (prefill) or
 // splits each sequence's keys into blocks merged afterwards (decode).
 bool indexer_split_mode(int32_t q_per_seq, int32_t h_idx);
