@@ -1,5 +1,39 @@
 // Attention of a batch over a shared prompt and each request's own tokens
-// (smla_shared_prefix_fwd).
+// (smla_shared_prefix_fwd): out = softmax(sm_scale q K^T) K[:, 0:512] over every
+// key a token sees, in one pass over the keys with a running maximum and sum.
+//
+// Rows of the problem are (token, head) pairs: the latent row of a key serves
+// every head of every token, so the shared prompt is ONE product with
+// n_seqs * q_per_seq * n_heads rows, and a request's own tokens one with
+// q_per_seq * n_heads rows. Both are cut into segments of 128 rows (row block)
+// x a range of keys, walked in tiles of 128 keys (two pages).
+//
+// Why a CTA pair. A row's output has 512 fp32 values, so 128 rows fill all 512
+// columns of an SM's tensor memory and leave none for the logits. A cluster of
+// two CTAs therefore shares a block of 128 rows:
+//   CTA c computes the logits of page c of each tile (QK over 576 values) and
+//   the output values 256 c .. 256 c + 255 (PV over both pages of the tile).
+// Every product is one M = 128 tcgen05.mma per 16 values, no logit is computed
+// twice, and what crosses the pair per tile is the row maxima (512 B) and the
+// probabilities of the other page (16 KB), both sent through distributed shared
+// memory with their bytes counted on the receiver's barrier.
+//
+// Tensor memory (512 columns): O 256 | S 64 | Q values 0..383 (192). Shared
+// memory (216 KB + barriers): Q values 384..575, the keys of one tile in flight
+// in QK and one in PV as 17 slots of 64 keys x 64 values, and both halves of P:
+//   KO  own page, the 5 chunks that only QK reads     (1 tile)
+//   KV  own page, the 4 chunks of this CTA's output   (2 tiles)
+//   VO  other page, the 4 chunks of this CTA's output (1 tile)
+// Warp roles: 0-3 softmax (a thread per row) and results, 4 TMA loads of BF16
+// rows, 5 MMA issue, 6-13 (FP8 caches) load and widen the rows instead of TMA.
+// The issue order QK(t + 1), PV(t) keeps the tensor pipe busy during softmax(t).
+//
+// The work is cut evenly: segment after segment on one line (a tile costs 1, a
+// segment's start kOverhead more), and pair i of P walks the i-th of P equal
+// stretches. A segment that is cut leaves several partial results (fp32 O with
+// its maximum and sums) that merge_kernel joins; no pair waits for another.
+#include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -12,136 +46,967 @@
 namespace smla {
 namespace {
 
+constexpr int kRows = 128;       // rows of a block (MMA M)
+constexpr int kOverhead = 2;     // cost of starting a segment, in tiles
+constexpr int kChunk = 64 * 128; // 64 keys x 64 values
+constexpr int kQChunk = kRows * 128;
+constexpr int kQTmemChunks = 6;  // Q chunks in tensor memory; the other 3 in shared memory
+constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
+constexpr int kOffQ = 0, kOffKO = 3 * kQChunk, kOffKV = kOffKO + 5 * kChunk, kOffVO = kOffKV + 8 * kChunk,
+              kOffP = kOffVO + 4 * kChunk, kOffMeta = kOffP + 2 * kQChunk;
+constexpr float kRaise = 8.0f;   // log2: the reference maximum is raised only when exceeded by this much
+constexpr int kMaxPairs = 128;
+constexpr int kMaxPieces = kMaxPairs + 2;  // of a row: its two segments are walked by distinct pairs, but for one at each border
+constexpr int kTileRowBytes = 656, kTileRope = 528;
+constexpr int kConvWarps = 8;
+
+enum { kBf16 = 0, kTokenFp8 = 1, kTileFp8 = 2 };
+
 struct PrefixParams {
   const uint8_t* kv;
   const float* kv_scale;
-  int32_t kv_dtype, num_pages;
+  int32_t num_pages;
   const int32_t* page_tables;
   int32_t max_pages, n_seqs;
   const int32_t* seq_lens;
-  int32_t max_seq_len, shared_len, q_per_seq;
+  int32_t max_seq_len, shared_len, q_per_seq, hshift;  // heads = 1 << hshift
   const uint16_t* q;
-  float sm_scale;
+  float scale_log2;
   uint16_t* out;
   float* lse;
   uint32_t* status;
+  int32_t n_rows;     // tokens * heads
+  int32_t n_rb, n_pt; // row blocks and tiles of the shared part (n_rb = 0: nothing shared)
+  int32_t rb_s;       // row blocks of one request
+  int32_t n_seg, pairs;
+  long long* seg_off; // [0] length of the line, [1 + i] where own segment i starts
+  float* part_m;      // [slot][128]
+  float* part_l;      // [slot][2][128]
+  float4* part_o;     // [slot][2][64][128]: four output values of a row
 };
 
-constexpr int kTile = 32;
-constexpr int kThreads = 256;
-
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(c)));
-  return __half2float(__ushort_as_half(static_cast<uint16_t>(r)));
+// ------------------------------------------------------------------ the line of work
+__device__ __forceinline__ int length_of(const PrefixParams& p, int b) {
+  return max(0, min(__ldg(p.seq_lens + b), p.max_seq_len));
 }
-
-__device__ __forceinline__ float kv_value(const PrefixParams& p, long long row, int d) {
-  if (p.kv_dtype == SMLA_BF16)
-    return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p.kv)[row * kDqk + d]) << 16);
-  if (p.kv_dtype == SMLA_FP8_E4M3) return e4m3_value(p.kv[row * kDqk + d]) * p.kv_scale[row];
-  const uint8_t* r = p.kv + row * 656;
-  if (d < kDv) return e4m3_value(r[d]) * reinterpret_cast<const float*>(r + kDv)[d >> 7];
-  return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(r + 528)[d - kDv]) << 16);
+// Keys that the last token of own segment i sees.
+__device__ __forceinline__ int own_end(const PrefixParams& p, int i) {
+  const int b = i / p.rb_s, rb = i - b * p.rb_s;
+  const int j = min(p.q_per_seq - 1, (rb * kRows + kRows - 1) >> p.hshift);
+  return length_of(p, b) - p.q_per_seq + j + 1;
 }
+__device__ __forceinline__ int own_tiles(const PrefixParams& p, int i) {
+  const int end = own_end(p, i);
+  if (end <= p.shared_len) return 0;
+  return ((end + kPage - 1) / kPage - p.shared_len / kPage + 1) >> 1;
+}
+__device__ __forceinline__ int seg_tiles(const PrefixParams& p, int s) {
+  return s < p.n_rb ? p.n_pt : own_tiles(p, s - p.n_rb);
+}
+__device__ __forceinline__ int seg_cost(int tiles) { return tiles > 0 ? tiles + kOverhead : 0; }
 
-// One block per new token: its heads' queries and 32 keys at a time in shared
-// memory, running maximum and sum per head, two output columns per thread.
-template <int H>
-__global__ void __launch_bounds__(kThreads) prefix_simple_kernel(const PrefixParams p) {
-  extern __shared__ float sm[];
-  float* sq = sm;                   // [H][576]
-  float* sk = sq + H * kDqk;        // [32][577]
-  float* sp = sk + kTile * (kDqk + 1);  // [H][32]
-  float* sa = sp + H * kTile;       // [H] rescale
-  const int t = threadIdx.x, row = blockIdx.x, b = row / p.q_per_seq;
-  int len = p.seq_lens[b];
-  if (len > p.max_seq_len) {
-    len = p.max_seq_len;
-    if (t == 0) set_status(p.status, kStatusBounds);
-  }
-  const int n = max(0, len - p.q_per_seq + row - b * p.q_per_seq + 1);
-  for (int i = t; i < H * kDqk; i += kThreads)
-    sq[i] = __uint_as_float(static_cast<uint32_t>(p.q[static_cast<long long>(row) * H * kDqk + i]) << 16) * p.sm_scale;
-  float acc[2 * H];
-#pragma unroll
-  for (int i = 0; i < 2 * H; ++i) acc[i] = 0.0f;
-  float m = -INFINITY, l = 0.0f;  // of head t (t < H)
-  for (int k0 = 0; k0 < n; k0 += kTile) {
-    __syncthreads();
-    for (int i = t; i < kTile * kDqk; i += kThreads) {
-      const int k = i / kDqk, d = i - k * kDqk, key = k0 + k;
-      float v = 0.0f;
-      if (key < n) {
-        const int page = p.page_tables[static_cast<long long>(key < p.shared_len ? 0 : b) * p.max_pages + key / kPage];
-        if (page >= 0 && page < p.num_pages) v = kv_value(p, static_cast<long long>(page) * kPage + key % kPage, d);
-        else if (d == 0) set_status(p.status, kStatusBounds);
-      }
-      sk[k * (kDqk + 1) + d] = v;
+struct Line {  // a pair's stretch [x, y) and where it stands: segment s starts at a
+  long long x, y, a;
+  int s;
+};
+struct Piece {
+  int s, t0, t1;  // tiles [t0, t1) of segment s
+};
+
+__device__ __forceinline__ bool next_piece(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
+  while (L.s < p.n_seg && L.a < L.y) {
+    const int tiles = seg_tiles(p, L.s), cost = seg_cost(tiles);
+    const int s = L.s++;
+    const long long a = L.a;
+    if (cost == 0) continue;
+    if (writer && s >= p.n_rb && a >= L.x) p.seg_off[1 + s - p.n_rb] = a;
+    L.a += cost;
+    const long long t0 = max(L.x - a - kOverhead, 0LL), t1 = min(L.y - a - kOverhead, static_cast<long long>(tiles));
+    if (t1 > t0) {
+      pc.s = s;
+      pc.t0 = static_cast<int>(t0);
+      pc.t1 = static_cast<int>(t1);
+      return true;
     }
+  }
+  return false;
+}
+
+// The tiles of a pair's pieces one after another, with the tile's page ids.
+struct Tiles {
+  Line line;
+  Piece pc;
+  int t;
+  const int32_t* table;
+  int first_page, end_page;  // of the segment
+  int own, other;            // pool pages of the tile's page `rank` and of the other one, -1: none
+  bool bad;                  // a table entry is outside the pool
+
+  __device__ __forceinline__ int page(const PrefixParams& p, int i) {
+    if (i >= end_page) return -1;
+    const int v = __ldg(table + i);
+    if (v >= 0 && v < p.num_pages) return v;
+    bad = true;
+    return -1;
+  }
+  __device__ __forceinline__ bool next(const PrefixParams& p, int rank, bool fresh) {
+    if (fresh || ++t >= pc.t1) {
+      if (!next_piece(p, line, pc, false)) return false;
+      t = pc.t0;
+      if (pc.s < p.n_rb) {
+        table = p.page_tables;
+        first_page = 0;
+        end_page = (p.shared_len + kPage - 1) / kPage;
+      } else {
+        const int i = pc.s - p.n_rb;
+        table = p.page_tables + static_cast<long long>(i / p.rb_s) * p.max_pages;
+        first_page = p.shared_len / kPage;
+        end_page = (own_end(p, i) + kPage - 1) / kPage;
+      }
+    }
+    bad = false;
+    own = page(p, first_page + 2 * t + rank);
+    other = page(p, first_page + 2 * t + (rank ^ 1));
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------ cluster helpers
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// one float into the peer's shared memory, its 4 bytes counted on the peer's barrier
+__device__ __forceinline__ void send_float(uint32_t dst, float v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst),
+               "r"(__float_as_uint(v)), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void send_bulk(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// Bounded wait that also acquires what the other CTA of the cluster sent.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((it & 15u) == 0) {
+      if (*abort) return false;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        set_status(status, kStatusTimeout);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+// A from tensor memory
+__device__ __forceinline__ void mma_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrives on the barrier at this address in both CTAs of the pair
+__device__ __forceinline__ void commit_pair_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {  // relative error about 2^-22; 2^-inf = 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
+  if (f16) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// four e4m3 codes -> four floats
+__device__ __forceinline__ void e4m3x4(uint32_t c, float* f) {
+  uint32_t lo, hi;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(c)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(c >> 16)));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+}
+__device__ __forceinline__ uint32_t piece_off(int row, int j) {  // 16-byte piece j of a 128-byte swizzled row
+  return static_cast<uint32_t>(row * 128 + ((j ^ (row & 7)) << 4));
+}
+// bf16 pair -> f16 pair; `over`: a value outside f16's range
+__device__ __forceinline__ uint32_t to_f16(uint32_t w, bool& over) {
+  over |= ((w & 0x7FFFu) > 0x477Fu && (w & 0x7FFFu) < 0x7F80u) || ((w & 0x7FFF0000u) > 0x477F0000u && (w & 0x7FFF0000u) < 0x7F800000u);
+  return pack2(bf_lo(w), bf_hi(w), true);
+}
+
+struct Meta {
+  float mx[2][kRows];         // the other CTA's row maxima
+  float ks[4][2][64];         // per softmax warp: scales of the own page (per-token FP8)
+  uint64_t q_full, ko_full, kv_full[2], vo_full, ko_free, kv_free[2], vo_free;
+  uint64_t s_full, s_free, p_own, p_other, pv_done, o_free;
+  uint64_t mx_full[2][4];
+  long long scan[34];
+  long long start_a;
+  int start_s;
+  uint32_t tmem_slot;
+  int abort_flag;
+};
+constexpr size_t kSmemBytes = kOffMeta + sizeof(Meta);
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+// Keys [lo, hi) that a row sees in its segment; over the block's rows that see
+// any, the smallest and largest hi.
+struct Limits {
+  int lo, hi, min_hi, max_hi;
+};
+__device__ __forceinline__ Limits limits(const PrefixParams& p, int s, int row) {
+  Limits m;
+  m.hi = 0, m.min_hi = INT_MAX, m.max_hi = 0;
+  const bool shared = s < p.n_rb;
+  const int i = s - p.n_rb, b0 = shared ? 0 : i / p.rb_s;
+  const int r0 = (shared ? s : i - b0 * p.rb_s) * kRows;
+  const int last = shared ? p.n_rows >> p.hshift : p.q_per_seq;  // tokens of the batch or of the request
+  m.lo = shared ? 0 : p.shared_len;
+  const int mine = (r0 + row) >> p.hshift;
+  for (int k = r0 >> p.hshift; k < min(last, (r0 + kRows) >> p.hshift); ++k) {
+    const int b = shared ? k / p.q_per_seq : b0, j = shared ? k - b * p.q_per_seq : k;
+    int hi = max(0, length_of(p, b) - p.q_per_seq + j + 1);
+    if (shared) hi = min(hi, p.shared_len);
+    if (hi > m.lo) {
+      m.min_hi = min(m.min_hi, hi);
+      m.max_hi = max(m.max_hi, hi);
+    }
+    if (k == mine) m.hi = hi;
+  }
+  return m;
+}
+
+template <int FMT>
+constexpr int kThreadsOf = FMT == kBf16 ? 192 : 192 + 32 * kConvWarps;
+
+template <int FMT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefixParams p) {
+  constexpr bool F16 = FMT == kTileFp8;  // operand type of the MMAs
+  constexpr uint32_t kFmt = F16 ? kFmtF16 : kFmtBF16;
+  constexpr int kThreads = kThreadsOf<FMT>;
+  constexpr uint32_t kFills = FMT == kBf16 ? 1 : kConvWarps;  // arrivals that fill a slot group
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Meta& M = *reinterpret_cast<Meta*>(smem + kOffMeta);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int pair = blockIdx.x >> 1;
+  const bool aligned = (smem_u32(smem) & 1023u) == 0;
+
+  if (tid == 0) {
+    mbar_init(&M.q_full, 4);
+    mbar_init(&M.ko_full, kFills);
+    mbar_init(&M.vo_full, kFills);
+    mbar_init(&M.ko_free, 1);
+    mbar_init(&M.vo_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&M.kv_full[i], kFills);
+      mbar_init(&M.kv_free[i], 1);
+      for (int w = 0; w < 4; ++w) mbar_init(&M.mx_full[i][w], 1);
+    }
+    mbar_init(&M.s_full, 1);
+    mbar_init(&M.s_free, 4);
+    mbar_init(&M.p_own, 4);
+    mbar_init(&M.p_other, 1);
+    mbar_init(&M.pv_done, 2);
+    mbar_init(&M.o_free, 4);
+    M.abort_flag = 0;
+    M.start_s = p.n_seg;
+    M.start_a = 0;
+    fence_mbar_init();
+    if (!aligned) set_status(p.status, kStatusSetup);
+  }
+  if (warp == 4) {
+    tmem_alloc(&M.tmem_slot, 512);
+    tmem_relinquish();
+  }
+
+  // ---- the length of the line, this pair's stretch, and the segment it begins in
+  Line line;
+  {
+    const int n_own = p.n_seg - p.n_rb;
+    const long long shared_cost = static_cast<long long>(p.n_rb) * seg_cost(p.n_pt);
+    long long sum = 0;
+    for (int i = tid; i < n_own; i += kThreads) sum += seg_cost(own_tiles(p, i));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (lane == 0) M.scan[warp] = sum;
+    if (pair == 0 && rank == 0)
+      for (int b = tid; b < p.n_seqs; b += kThreads)
+        if (__ldg(p.seq_lens + b) > p.max_seq_len) set_status(p.status, kStatusBounds);
     __syncthreads();
-    for (int i = t; i < H * kTile; i += kThreads) {
-      const int h = i / kTile, k = i % kTile, key = k0 + k;
-      float s = -INFINITY;
-      if (key < n) {
-        const int page = p.page_tables[static_cast<long long>(key < p.shared_len ? 0 : b) * p.max_pages + key / kPage];
-        if (page >= 0 && page < p.num_pages) {
-          s = 0.0f;
-          for (int d = 0; d < kDqk; ++d) s += sq[h * kDqk + d] * sk[k * (kDqk + 1) + d];
+    long long total = shared_cost;
+    for (int w = 0; w < kThreads / 32; ++w) total += M.scan[w];
+    line.x = total * pair / p.pairs;
+    line.y = total * (pair + 1) / p.pairs;
+    if (pair == 0 && rank == 0 && tid == 0) p.seg_off[0] = total;
+    if (line.x < line.y) {
+      if (line.x < shared_cost) {
+        if (tid == 0) {
+          M.start_s = static_cast<int>(line.x / seg_cost(p.n_pt));
+          M.start_a = static_cast<long long>(M.start_s) * seg_cost(p.n_pt);
+        }
+      } else {
+        long long before = shared_cost;
+        for (int c0 = 0; c0 < n_own && before <= line.x; c0 += kThreads) {
+          const int i = c0 + tid;
+          const long long cost = i < n_own ? seg_cost(own_tiles(p, i)) : 0;
+          long long v = cost;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const long long o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+            if (lane >= d) v += o;
+          }
+          __syncthreads();
+          if (lane == 31) M.scan[warp] = v;
+          __syncthreads();
+          long long all = 0;
+          for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) v += M.scan[w];
+            all += M.scan[w];
+          }
+          if (before + v - cost <= line.x && line.x < before + v) {
+            M.start_s = p.n_rb + i;
+            M.start_a = before + v - cost;
+          }
+          before += all;
         }
       }
-      sp[i] = s;
-    }
-    __syncthreads();
-    if (t < H) {
-      float top = m;
-      for (int k = 0; k < kTile; ++k) top = fmaxf(top, sp[t * kTile + k]);
-      const float ref = top == -INFINITY ? 0.0f : top;
-      const float a = expf(m - ref);
-      l *= a;
-      for (int k = 0; k < kTile; ++k) {
-        const float e = expf(sp[t * kTile + k] - ref);
-        sp[t * kTile + k] = e;
-        l += e;
-      }
-      m = top;
-      sa[t] = a;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      float a0 = acc[2 * h] * sa[h], a1 = acc[2 * h + 1] * sa[h];
-#pragma unroll 4
-      for (int k = 0; k < kTile; ++k) {
-        const float e = sp[h * kTile + k];
-        a0 += e * sk[k * (kDqk + 1) + t];
-        a1 += e * sk[k * (kDqk + 1) + 256 + t];
-      }
-      acc[2 * h] = a0, acc[2 * h + 1] = a1;
     }
   }
+  tc_fence_before();
   __syncthreads();
-  if (t < H) {
-    sa[t] = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    if (p.lse) p.lse[static_cast<long long>(row) * H + t] = l == 0.0f ? -INFINITY : m + logf(l);
-  }
-  __syncthreads();
+  cluster_sync();  // the pair's barriers are set up before either CTA sends to the other
+  tc_fence_after();
+  line.s = aligned ? M.start_s : p.n_seg;
+  line.a = M.start_a;
+  const uint32_t tmem = M.tmem_slot;
+  const uint32_t sbase = smem_u32(smem);
+  volatile int* abort_v = &M.abort_flag;
+
+  if (warp < 4) {
+    // -------------------------------------------------------------- softmax, results
+    const int row = tid;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t peer_mx = peer_addr(smem_u32(&M.mx[0][0]), rank ^ 1);
+    const uint32_t peer_mxbar = peer_addr(smem_u32(&M.mx_full[0][0]), rank ^ 1);
+    const uint32_t peer_p = peer_addr(sbase + kOffP + kQChunk, rank ^ 1);
+    const uint32_t peer_pbar = peer_addr(smem_u32(&M.p_other), rank ^ 1);
+    const bool writer = rank == 0 && tid == 0;
+    bool over = false;
+    // a thread's row of Q: chunks 0-5 into its lane of tensor memory, 6-8 into shared memory
+    auto load_q = [&](int s) {
+      const bool shared = s < p.n_rb;
+      const int i = s - p.n_rb, b = shared ? 0 : i / p.rb_s;
+      const int r = (shared ? s : i - b * p.rb_s) * kRows + row;
+      const int limit = shared ? p.n_rows : p.q_per_seq << p.hshift;
+      const long long flat = (static_cast<long long>(b) * p.q_per_seq << p.hshift) + r;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + flat * kDqk);
 #pragma unroll
-  for (int h = 0; h < H; ++h)
+      for (int c = 0; c < kDqk / 64; ++c) {
+        uint4 v[8];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const __nv_bfloat16 o = __float2bfloat16(sa[h] == 0.0f ? 0.0f : acc[2 * h + j] * sa[h]);
-      p.out[(static_cast<long long>(row) * H + h) * kDv + 256 * j + t] = *reinterpret_cast<const uint16_t*>(&o);
+        for (int j = 0; j < 8; ++j) v[j] = r < limit ? __ldg(src + 8 * c + j) : make_uint4(0, 0, 0, 0);
+        if (F16) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[j] = make_uint4(to_f16(v[j].x, over), to_f16(v[j].y, over), to_f16(v[j].z, over), to_f16(v[j].w, over));
+        }
+        if (c < kQTmemChunks) {
+          tmem_st_32x32b_x32(tmem + lanes + kColQ + 32 * c, reinterpret_cast<const uint32_t*>(v));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(smem + kOffQ + (c - kQTmemChunks) * kQChunk + piece_off(row, j)) = v[j];
+        }
+      }
+      tmem_wait_st();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&M.q_full);
+    };
+
+    Line wline = line;
+    Piece pc;
+    bool have = next_piece(p, wline, pc, writer);
+    if (have) load_q(pc.s);
+    Tiles cur;
+    cur.line = line;
+    bool more = cur.next(p, rank, true);
+    uint32_t g = 0;
+    bool ok = true;
+    while (have && ok) {
+      const Limits lim = limits(p, pc.s, row);
+      float m = -INFINITY, l = 0.0f;
+      for (int t = pc.t0; t < pc.t1; ++t, ++g) {
+        const int tile_k = (cur.first_page + 2 * t) * kPage, key0 = tile_k + rank * kPage;
+        const int own = cur.own;
+        const float* ks = M.ks[warp][g & 1];
+        if (FMT == kTokenFp8) {  // scales of the own page, a copy per warp
+          const float2 sc = own >= 0 ? __ldg(reinterpret_cast<const float2*>(p.kv_scale + static_cast<long long>(own) * kPage) + lane)
+                                     : make_float2(0.0f, 0.0f);
+          *reinterpret_cast<float2*>(&M.ks[warp][g & 1][2 * lane]) = sc;
+          __syncwarp();
+        }
+        if (more) more = cur.next(p, rank, false);
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_spin(&M.s_full, g & 1, abort_v, p.status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float x[64];
+        tmem_ld_32x32b_x32(tmem + lanes + kColS, reinterpret_cast<uint32_t*>(x));
+        tmem_ld_32x32b_x32(tmem + lanes + kColS + 32, reinterpret_cast<uint32_t*>(x) + 32);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&M.s_free);
+        const bool edge = own < 0 || key0 < lim.lo || key0 + kPage > lim.min_hi;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) x[i] *= FMT == kTokenFp8 ? ks[i] * p.scale_log2 : p.scale_log2;
+        if (edge) {
+          const int hi = own < 0 ? 0 : lim.hi;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) x[i] = key0 + i >= lim.lo && key0 + i < hi ? x[i] : -INFINITY;
+        }
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 64; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], x[i]);
+        const float mine = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        // the row's maximum over the other CTA's page: both CTAs scale P and O by the same reference
+        const uint32_t par = g & 1;
+        send_float(peer_mx + (par * kRows + row) * 4, mine, peer_mxbar + (par * 4 + warp) * 8);
+        if (lane == 0) mbar_arrive_expect_tx(&M.mx_full[par][warp], 32 * 4);
+        if (!__all_sync(0xFFFFFFFFu, wait_cluster(&M.mx_full[par][warp], (g >> 1) & 1, abort_v, p.status))) {
+          ok = false;
+          break;
+        }
+        const float top = fmaxf(mine, *reinterpret_cast<volatile float*>(&M.mx[par][row]));
+        const bool raise = top > m + kRaise || (m == -INFINITY && top > -INFINITY);
+        float alpha = 1.0f;
+        if (raise) {
+          alpha = m == -INFINITY ? 0.0f : exp2_fast(m - top);
+          m = top;
+          l *= alpha;
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        uint32_t pk[32];
+        float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          float a = exp2_fast(x[i] - ref), b = exp2_fast(x[i + 1] - ref);
+          l4[(i >> 1) & 3] += a + b;
+          if (FMT == kTokenFp8) {
+            a *= ks[i], b *= ks[i + 1];
+            if (edge) {  // a masked key's scale may be anything
+              if (x[i] == -INFINITY) a = 0.0f;
+              if (x[i + 1] == -INFINITY) b = 0.0f;
+            }
+          }
+          // P is rounded to the operands' type (bf16: 2^-9 of a probability at most); the sum l is not
+          pk[i >> 1] = pack2(a, b, F16);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        // both CTAs are done with the previous tile's P, and O holds it
+        if (g > 0 && !__all_sync(0xFFFFFFFFu, wait_cluster(&M.pv_done, (g - 1) & 1, abort_v, p.status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (t > pc.t0 && __any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tmem + lanes + kColO + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st_32x32b_x32(tmem + lanes + kColO + 32 * c, o);
+          }
+          tmem_wait_st();
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(smem + kOffP + piece_off(row, j)) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        // 0 * NaN: V rows that no row of the block sees are zeroed, and rows that
+        // only some see are zeroed if they hold a value that is not finite (those
+        // that see it have a logit that is not finite either)
+        if (tile_k < lim.lo || tile_k + 2 * kPage > lim.min_hi) {
+          const bool w_ok = mbar_wait(&M.kv_full[g & 1], (g >> 1) & 1, abort_v, p.status) &&
+                            mbar_wait(&M.vo_full, g & 1, abort_v, p.status);
+          if (!__all_sync(0xFFFFFFFFu, w_ok)) {
+            ok = false;
+            break;
+          }
+          const bool oth = row >= kPage;
+          const int r = row & (kPage - 1), key = tile_k + (oth ? rank ^ 1 : rank) * kPage + r;
+          uint8_t* v = smem + (oth ? kOffVO : kOffKV + static_cast<int>(g & 1) * 4 * kChunk);
+          bool zero = key < lim.lo || key >= lim.max_hi;
+          if (!zero && key >= lim.min_hi) {
+            constexpr uint32_t inf = F16 ? 0x7C00u : 0x7F80u;
+            for (int j = 0; j < 32; ++j) {
+              const uint4 u = *reinterpret_cast<const uint4*>(v + (j >> 3) * kChunk + piece_off(r, j & 7));
+              const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+              for (int k = 0; k < 4; ++k) zero |= (e[k] & inf) == inf || (e[k] & (inf << 16)) == inf << 16;
+            }
+          }
+          if (zero)
+            for (int j = 0; j < 32; ++j)
+              *reinterpret_cast<uint4*>(v + (j >> 3) * kChunk + piece_off(r, j & 7)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          send_bulk(peer_p + warp * 4096, sbase + kOffP + warp * 4096, 4096, peer_pbar);
+          mbar_arrive(&M.p_own);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      // the next piece's Q while the last product runs, then this piece's results
+      const int slot = pc.s + pair;
+      have = next_piece(p, wline, pc, writer);
+      if (have) load_q(pc.s);
+      if (!__all_sync(0xFFFFFFFFu, wait_cluster(&M.pv_done, (g - 1) & 1, abort_v, p.status))) break;
+      tc_fence_after();
+      float4* o = p.part_o + (static_cast<long long>(slot) * 2 + rank) * 64 * kRows + row;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        float v[32];
+        tmem_ld_32x32b_x32(tmem + lanes + kColO + 32 * c, reinterpret_cast<uint32_t*>(v));
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[(8 * c + j) * kRows] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&M.o_free);
+      // a row that sees none of the segment's keys took part in the unmasked tiles: dropped here
+      if (lim.hi <= lim.lo) l = 0.0f;
+      if (rank == 0) p.part_m[static_cast<long long>(slot) * kRows + row] = m;
+      p.part_l[(static_cast<long long>(slot) * 2 + rank) * kRows + row] = l;
     }
+    if (over) set_status(p.status, kStatusOverflow);
+  } else if (warp == 4) {
+    // -------------------------------------------------------------- TMA loads
+    if (FMT == kBf16 && lane == 0) {
+      const int v0 = 256 * rank, k0 = 256 * (rank ^ 1);
+      Tiles cur;
+      cur.line = line;
+      bool more = cur.next(p, rank, true);
+      int last_other = 0;
+      // a page that is missing reads as zeros: a box wholly before the pool
+      auto y = [](int page) { return page >= 0 ? page * kPage : -kPage; };
+      auto load_vo = [&](uint32_t h, int page) {
+        if (h > 0 && !mbar_wait(&M.vo_free, (h - 1) & 1, abort_v, p.status)) return false;
+        mbar_arrive_expect_tx(&M.vo_full, 4 * kChunk);
+        for (int i = 0; i < 4; ++i) tma_load_2d(smem + kOffVO + i * kChunk, &kv_map, &M.vo_full, v0 + 64 * i, y(page));
+        return true;
+      };
+      uint32_t g = 0;
+      bool ok = true;
+      for (; more && ok; ++g) {
+        const int own = cur.own, other = cur.other;
+        if (cur.bad) set_status(p.status, kStatusBounds);
+        more = cur.next(p, rank, false);
+        if (g > 0 && !mbar_wait(&M.ko_free, (g - 1) & 1, abort_v, p.status)) { ok = false; break; }
+        mbar_arrive_expect_tx(&M.ko_full, 5 * kChunk);
+        for (int i = 0; i < 5; ++i)
+          tma_load_2d(smem + kOffKO + i * kChunk, &kv_map, &M.ko_full, i < 4 ? k0 + 64 * i : kDv, y(own));
+        const int buf = g & 1;
+        if (g > 1 && !mbar_wait(&M.kv_free[buf], ((g >> 1) - 1) & 1, abort_v, p.status)) { ok = false; break; }
+        mbar_arrive_expect_tx(&M.kv_full[buf], 4 * kChunk);
+        for (int i = 0; i < 4; ++i)
+          tma_load_2d(smem + kOffKV + (4 * buf + i) * kChunk, &kv_map, &M.kv_full[buf], v0 + 64 * i, y(own));
+        if (g > 0) ok = load_vo(g - 1, last_other);
+        last_other = other;
+      }
+      if (g > 0 && ok) load_vo(g - 1, last_other);
+    }
+  } else if (warp == 5) {
+    // -------------------------------------------------------------- MMA issue
+    constexpr uint32_t id_qk = instr_desc(128, 64, kFmt, kFmt, false, false);
+    constexpr uint32_t id_pv = instr_desc(128, 256, kFmt, kFmt, false, true);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const uint32_t sb = __shfl_sync(0xFFFFFFFFu, sbase, 0);
+    const int rk = __shfl_sync(0xFFFFFFFFu, rank, 0);
+    const uint64_t q_desc = smem_desc(sb + kOffQ, 16, 1024);
+    const uint64_t ko_desc = smem_desc(sb + kOffKO, 16, 1024);
+    const uint64_t kv_desc = smem_desc(sb + kOffKV, 16, 1024);
+    const uint64_t v_desc = smem_desc(sb + kOffKV, kChunk, 1024);   // the same chunks read as V: values x keys
+    const uint64_t vo_desc = smem_desc(sb + kOffVO, kChunk, 1024);
+    const uint64_t p_desc = smem_desc(sb + kOffP, 16, 1024);
+    const uint64_t po_desc = smem_desc(sb + kOffP + kQChunk, 16, 1024);
+    // logits of one chunk of 64 values: Q chunk c (tensor or shared memory) with the keys at `k`
+    auto qk = [&](int c, uint64_t k, bool first) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint64_t b = k + static_cast<uint64_t>(2 * kk);
+        const uint32_t acc = !first || kk != 0;
+        if (c < kQTmemChunks)
+          mma_ts_warp(tm + kColS, tm + kColQ + 32 * c + 8 * kk, b, id_qk, acc);
+        else
+          mma_f16_warp(tm + kColS, q_desc + static_cast<uint64_t>(((c - kQTmemChunks) * kQChunk >> 4) + 2 * kk), b, id_qk, acc);
+      }
+    };
+    Line wline = line;
+    Piece pc;
+    uint32_t g = 0, n = 0;
+    bool ok = true;
+    auto all = [](bool v) { return __all_sync(0xFFFFFFFFu, v); };
+    // O (+)= P V of tile h, own page first (its V slots are the next to be refilled)
+    auto pv = [&](uint32_t h, bool first) {
+      bool w = mbar_wait_spin(&M.p_own, h & 1, abort_v, p.status);
+      if (first && n > 0) w = w && mbar_wait(&M.o_free, (n - 1) & 1, abort_v, p.status);
+      if (!all(w)) return false;
+      tc_fence_after();
+      const uint64_t v = v_desc + static_cast<uint64_t>((h & 1) * (4 * kChunk >> 4));
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_f16_warp(tm + kColO, p_desc + static_cast<uint64_t>(2 * kk), v + static_cast<uint64_t>(kk * 2048 >> 4), id_pv,
+                     !first || kk != 0);
+      mma_commit_warp(&M.kv_free[h & 1]);
+      if (lane == 0) mbar_arrive_expect_tx(&M.p_other, kQChunk);
+      w = wait_cluster(&M.p_other, h & 1, abort_v, p.status) && mbar_wait_spin(&M.vo_full, h & 1, abort_v, p.status);
+      if (!all(w)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_f16_warp(tm + kColO, po_desc + static_cast<uint64_t>(2 * kk), vo_desc + static_cast<uint64_t>(kk * 2048 >> 4), id_pv, 1);
+      mma_commit_warp(&M.vo_free);
+      commit_pair_warp(&M.pv_done);
+      return true;
+    };
+    while (ok && next_piece(p, wline, pc, false)) {
+      if (!all(mbar_wait(&M.q_full, n & 1, abort_v, p.status))) break;
+      for (int t = pc.t0; t < pc.t1; ++t, ++g) {
+        const bool w = mbar_wait_spin(&M.ko_full, g & 1, abort_v, p.status) &&
+                       (g == 0 || mbar_wait_spin(&M.s_free, (g - 1) & 1, abort_v, p.status));
+        if (!all(w)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // Q chunk of slot i: 4 (1 - rank) + i
+          if (rk == 0) qk(4 + i, ko_desc + static_cast<uint64_t>(i * kChunk >> 4), i == 0);
+          else qk(i, ko_desc + static_cast<uint64_t>(i * kChunk >> 4), i == 0);
+        }
+        qk(8, ko_desc + static_cast<uint64_t>(4 * kChunk >> 4), false);
+        mma_commit_warp(&M.ko_free);
+        if (!all(mbar_wait_spin(&M.kv_full[g & 1], (g >> 1) & 1, abort_v, p.status))) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t kd = kv_desc + static_cast<uint64_t>((g & 1) * (4 * kChunk >> 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (rk == 0) qk(i, kd + static_cast<uint64_t>(i * kChunk >> 4), false);
+          else qk(4 + i, kd + static_cast<uint64_t>(i * kChunk >> 4), false);
+        }
+        mma_commit_warp(&M.s_full);
+        if (t > pc.t0 && !pv(g - 1, t - 1 == pc.t0)) { ok = false; break; }
+      }
+      if (!ok || !pv(g - 1, pc.t1 - 1 == pc.t0)) break;
+      ++n;
+    }
+  } else if (FMT != kBf16) {
+    // -------------------------------------------------------------- FP8 rows: load, widen, store
+    // Thread u takes 16 codes of row u / 4 in every chunk. Codes are exact in
+    // bf16 (per-token scales multiply the logits and P in fp32); tile-scaled
+    // values (code * scale) are rounded to f16.
+    const int u = tid - 192, r = u >> 2, pcs = u & 3;
+    constexpr int kRowBytes = FMT == kTokenFp8 ? kDqk : kTileRowBytes;
+    const int kc0 = 4 * (rank ^ 1), vc0 = 4 * rank;
+    bool over = false;
+    struct Group {
+      uint4 v[5];
+      uint4 rope;  // second half of a tile-scaled row's rope piece
+      float4 sc;
+    };
+    auto fetch = [&](Group& gr, int page, int c0, int n) {
+      const uint8_t* src = p.kv + (static_cast<long long>(max(page, 0)) * kPage + r) * kRowBytes;
+      const bool live = page >= 0;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        if (i >= n) continue;
+        const int off = i < 4 ? (c0 + i) * 64 + pcs * 16 : FMT == kTokenFp8 ? kDv + pcs * 16 : kTileRope + pcs * 32;
+        gr.v[i] = live ? __ldg(reinterpret_cast<const uint4*>(src + off)) : make_uint4(0, 0, 0, 0);
+      }
+      if (FMT == kTileFp8) {
+        if (n == 5) gr.rope = live ? __ldg(reinterpret_cast<const uint4*>(src + kTileRope + pcs * 32 + 16)) : make_uint4(0, 0, 0, 0);
+        gr.sc = live ? __ldg(reinterpret_cast<const float4*>(src + kDv)) : make_float4(0, 0, 0, 0);
+      }
+    };
+    auto store = [&](const Group& gr, int off, int c0, int n) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        if (i >= n) continue;
+        uint8_t* dst = smem + off + i * kChunk;
+        if (FMT == kTileFp8 && i == 4) {  // bf16 rope -> f16
+          const uint4 a = gr.v[4], b = gr.rope;
+          *reinterpret_cast<uint4*>(dst + piece_off(r, 2 * pcs)) =
+              make_uint4(to_f16(a.x, over), to_f16(a.y, over), to_f16(a.z, over), to_f16(a.w, over));
+          *reinterpret_cast<uint4*>(dst + piece_off(r, 2 * pcs + 1)) =
+              make_uint4(to_f16(b.x, over), to_f16(b.y, over), to_f16(b.z, over), to_f16(b.w, over));
+          continue;
+        }
+        float s = 1.0f;
+        if (FMT == kTileFp8) {
+          const int tile = (c0 + i) >> 1;
+          s = tile == 0 ? gr.sc.x : tile == 1 ? gr.sc.y : tile == 2 ? gr.sc.z : gr.sc.w;
+        }
+        const uint32_t w[4] = {gr.v[i].x, gr.v[i].y, gr.v[i].z, gr.v[i].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float f[4];
+          e4m3x4(w[k], f);
+          if (FMT == kTileFp8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[e] *= s;
+              over |= fabsf(f[e]) > 65504.0f && fabsf(f[e]) < INFINITY;
+            }
+          }
+          o[2 * k] = pack2(f[0], f[1], F16);
+          o[2 * k + 1] = pack2(f[2], f[3], F16);
+        }
+        *reinterpret_cast<uint4*>(dst + piece_off(r, 2 * pcs)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + piece_off(r, 2 * pcs + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    };
+    auto filled = [&](uint64_t* bar) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_v, p.status)); };
+    Tiles cur;
+    cur.line = line;
+    bool more = cur.next(p, rank, true);
+    Group ko, kv, vo;  // each group's next load is in flight while the others are stored
+    if (more) {
+      fetch(ko, cur.own, kc0, 5);
+      fetch(kv, cur.own, vc0, 4);
+    }
+    uint32_t g = 0;
+    bool ok = true;
+    for (; more && ok; ++g) {
+      const int other = cur.other;
+      if (cur.bad && lane == 0) set_status(p.status, kStatusBounds);
+      more = cur.next(p, rank, false);
+      if (g > 0 && !wait(&M.ko_free, (g - 1) & 1)) { ok = false; break; }
+      store(ko, kOffKO, kc0, 5);
+      filled(&M.ko_full);
+      if (more) fetch(ko, cur.own, kc0, 5);
+      const int buf = g & 1;
+      if (g > 1 && !wait(&M.kv_free[buf], ((g >> 1) - 1) & 1)) { ok = false; break; }
+      store(kv, kOffKV + 4 * buf * kChunk, vc0, 4);
+      filled(&M.kv_full[buf]);
+      if (more) fetch(kv, cur.own, vc0, 4);
+      if (g > 0) {
+        if (g > 1 && !wait(&M.vo_free, (g - 2) & 1)) { ok = false; break; }
+        store(vo, kOffVO, vc0, 4);
+        filled(&M.vo_full);
+      }
+      fetch(vo, other, vc0, 4);
+    }
+    if (ok && g > 0 && (g == 1 || wait(&M.vo_free, (g - 2) & 1))) {
+      store(vo, kOffVO, vc0, 4);
+      filled(&M.vo_full);
+    }
+    if (over) set_status(p.status, kStatusOverflow);
+  }
+
+  __syncwarp();
+  if (*abort_v) {  // a wait gave up: let copies that are still under way land before the memory goes
+    const long long t0 = clock64();
+    while (clock64() - t0 < 4000000) __nanosleep(1000);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer may still read or signal this CTA's shared memory until here
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
-template <int H>
-int launch_simple(const PrefixParams& p, cudaStream_t st) {
-  const size_t smem = (static_cast<size_t>(H) * kDqk + kTile * (kDqk + 1) + H * kTile + H) * 4;
-  if (cudaFuncSetAttribute(prefix_simple_kernel<H>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return SMLA_ERR_CUDA;
-  prefix_simple_kernel<H><<<p.n_seqs * p.q_per_seq, kThreads, smem, st>>>(p);
+// ------------------------------------------------------------------ joining the pieces
+// A block joins 16 rows (one token's or part of one's heads): the pieces of
+// their shared segment and of their own one, weighted by 2^(m - largest m).
+constexpr int kMergeRows = 16, kMergeThreads = 256;
+
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams p) {
+  __shared__ int slots[kMaxPieces];       // slot * 128 + the rows' place in the block
+  __shared__ float wgt[kMaxPieces][kMergeRows];
+  __shared__ float inv[kMergeRows];
+  __shared__ __align__(16) uint16_t o[kMergeRows][kDv];
+  __shared__ int s_n;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int r0 = blockIdx.x * kMergeRows;
+  const long long total = p.seg_off[0];
+  if (tid < 32) {
+    int n = 0;
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+      int s, at;
+      long long a;
+      if (part == 0) {
+        if (p.n_rb == 0) continue;
+        s = r0 / kRows;
+        at = r0 % kRows;
+        a = static_cast<long long>(s) * seg_cost(p.n_pt);
+      } else {
+        const int per = p.q_per_seq << p.hshift, b = r0 / per, in = r0 - b * per;
+        s = p.n_rb + b * p.rb_s + in / kRows;
+        at = in % kRows;
+        a = 0;
+      }
+      const int tiles = seg_tiles(p, s);
+      if (tiles == 0) continue;
+      if (part == 1) a = p.seg_off[1 + s - p.n_rb];
+      const long long t0 = a + kOverhead, t1 = t0 + tiles;
+      for (int base = 0; base < p.pairs; base += 32) {
+        const int q = base + lane;
+        const bool in = q < p.pairs && max(total * q / p.pairs, t0) < min(total * (q + 1) / p.pairs, t1);
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, in);
+        const int at_n = n + __popc(mask & ((1u << lane) - 1));
+        if (in && at_n < kMaxPieces) slots[at_n] = (s + q) * kRows + at;
+        n += __popc(mask);
+      }
+    }
+    if (lane == 0) s_n = min(n, kMaxPieces);
+  }
+  __syncthreads();
+  const int n = s_n;
+  {  // 16 threads per row
+    const int row = tid >> 4, k = tid & 15;
+    float top = -INFINITY;
+    for (int i = k; i < n; i += 16) {
+      const int slot = slots[i] / kRows, at = slots[i] % kRows + row;
+      const float l = p.part_l[(static_cast<long long>(slot) * 2) * kRows + at] + p.part_l[(static_cast<long long>(slot) * 2 + 1) * kRows + at];
+      if (l != 0.0f) top = fmaxf(top, p.part_m[static_cast<long long>(slot) * kRows + at]);
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    float sum = 0.0f;
+    for (int i = k; i < n; i += 16) {
+      const int slot = slots[i] / kRows, at = slots[i] % kRows + row;
+      const float l = p.part_l[(static_cast<long long>(slot) * 2) * kRows + at] + p.part_l[(static_cast<long long>(slot) * 2 + 1) * kRows + at];
+      // a row that saw nothing in a piece (l = 0) has nothing there, whatever its O holds; -1 marks it
+      const float w = l != 0.0f ? exp2_fast(p.part_m[static_cast<long long>(slot) * kRows + at] - top) : -1.0f;
+      wgt[i][row] = w;
+      if (l != 0.0f) sum += w * l;
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (k == 0) {
+      inv[row] = sum != 0.0f ? 1.0f / sum : 0.0f;
+      if (p.lse) p.lse[r0 + row] = sum != 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    }
+  }
+  __syncthreads();
+  const int row = tid & 15, c0 = tid >> 4;
+  float4 acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = make_float4(0, 0, 0, 0);
+  for (int i = 0; i < n; ++i) {
+    const float w = wgt[i][row];
+    if (w == -1.0f) continue;
+    const int slot = slots[i] / kRows, at = slots[i] % kRows + row;
+    const float4* src = p.part_o + static_cast<long long>(slot) * 2 * 64 * kRows + at;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 v = src[(c0 + 16 * j) * kRows];
+      acc[j].x += w * v.x, acc[j].y += w * v.y, acc[j].z += w * v.z, acc[j].w += w * v.w;
+    }
+  }
+  const float f = inv[row];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint2*>(&o[row][4 * (c0 + 16 * j)]) =
+        make_uint2(pack2(acc[j].x * f, acc[j].y * f, false), pack2(acc[j].z * f, acc[j].w * f, false));
+  __syncthreads();
+  for (int i = tid; i < kMergeRows * kDv / 8; i += kMergeThreads)
+    reinterpret_cast<uint4*>(p.out + static_cast<long long>(r0) * kDv)[i] = reinterpret_cast<const uint4*>(&o[0][0])[i];
+}
+
+template <int FMT>
+int launch(const CUtensorMap& map, const PrefixParams& p, cudaStream_t st) {
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(prefix_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+  if (attr != cudaSuccess) return SMLA_ERR_CUDA;
+  prefix_kernel<FMT><<<2 * p.pairs, kThreadsOf<FMT>, kSmemBytes, st>>>(map, p);
+  if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
+  merge_kernel<<<p.n_rows / kMergeRows, kMergeThreads, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+int pairs_of_device() { return std::max(1, std::min(num_sms() / 2, kMaxPairs)); }
+
+// Row blocks and segments; false: more than 32-bit counts hold.
+bool plan(PrefixParams& p) {
+  const int64_t rows = static_cast<int64_t>(p.n_seqs) * p.q_per_seq << p.hshift;
+  const int64_t rb_s = ((static_cast<int64_t>(p.q_per_seq) << p.hshift) + kRows - 1) / kRows;
+  const int64_t n_rb = p.shared_len > 0 ? (rows + kRows - 1) / kRows : 0;
+  const int64_t n_seg = n_rb + rb_s * p.n_seqs;
+  if (rows > INT32_MAX - kRows || (n_seg + kMaxPieces) * kRows > INT32_MAX) return false;
+  p.n_rows = static_cast<int32_t>(rows);
+  p.rb_s = static_cast<int32_t>(rb_s);
+  p.n_rb = static_cast<int32_t>(n_rb);
+  p.n_seg = static_cast<int32_t>(n_seg);
+  p.n_pt = (p.shared_len + 2 * kPage - 1) / (2 * kPage);
+  p.pairs = pairs_of_device();
+  return true;
+}
+
+size_t layout(PrefixParams& p, uint8_t* ws) {
+  const size_t slots = static_cast<size_t>(p.n_seg) + p.pairs;
+  size_t at = kStatusBytes;
+  p.seg_off = reinterpret_cast<long long*>(ws + at);
+  at += up256((static_cast<size_t>(p.n_seg - p.n_rb) + 1) * 8);
+  p.part_m = reinterpret_cast<float*>(ws + at);
+  at += slots * kRows * 4;
+  p.part_l = reinterpret_cast<float*>(ws + at);
+  at += slots * 2 * kRows * 4;
+  p.part_o = reinterpret_cast<float4*>(ws + at);
+  return at + slots * 2 * 64 * kRows * 16;
 }
 
 }  // namespace
@@ -151,7 +1016,14 @@ using namespace smla;
 
 extern "C" {
 
-size_t smla_shared_prefix_fwd_workspace_size(int32_t, int32_t, int32_t, int32_t, int32_t) { return kStatusBytes; }
+size_t smla_shared_prefix_fwd_workspace_size(int32_t n_seqs, int32_t max_seq_len, int32_t shared_len,
+                                             int32_t q_per_seq, int32_t n_heads) {
+  if (n_seqs <= 0 || q_per_seq <= 0 || max_seq_len <= 0 || shared_len < 0 || (n_heads != 16 && n_heads != 64)) return kStatusBytes;
+  PrefixParams p{};
+  p.n_seqs = n_seqs, p.q_per_seq = q_per_seq, p.shared_len = shared_len, p.hshift = n_heads == 64 ? 6 : 4;
+  if (!plan(p)) return kStatusBytes;
+  return layout(p, nullptr);
+}
 
 int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_tables, int32_t max_pages,
                            int32_t n_seqs, const int32_t* seq_lens, int32_t max_seq_len, int32_t shared_len,
@@ -165,15 +1037,28 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
   if (n_seqs <= 0 || q_per_seq <= 0 || max_pages <= 0 || max_seq_len <= 0 || shared_len < 0 || shared_len > max_seq_len)
     return SMLA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(max_pages) * kPage < max_seq_len || !(sm_scale == sm_scale)) return SMLA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(n_seqs) * q_per_seq * n_heads > INT32_MAX) return SMLA_ERR_UNSUPPORTED;
   if (n_heads != 16 && n_heads != 64) return SMLA_ERR_UNSUPPORTED;
-  if (!workspace || !al(workspace, 16) || workspace_bytes < kStatusBytes) return SMLA_ERR_WORKSPACE;
+  if (max_seq_len > INT32_MAX - 4 * kPage) return SMLA_ERR_UNSUPPORTED;  // key positions of a tile are int32
+  PrefixParams p{};
+  p.n_seqs = n_seqs, p.q_per_seq = q_per_seq, p.shared_len = shared_len, p.hshift = n_heads == 64 ? 6 : 4;
+  if (!plan(p)) return SMLA_ERR_UNSUPPORTED;
+  if (!workspace || !al(workspace, 16) || workspace_bytes < layout(p, static_cast<uint8_t*>(workspace))) return SMLA_ERR_WORKSPACE;
+  p.kv = static_cast<const uint8_t*>(cache->kv), p.kv_scale = cache->kv_scale, p.num_pages = cache->num_pages;
+  p.page_tables = page_tables, p.max_pages = max_pages, p.seq_lens = seq_lens, p.max_seq_len = max_seq_len;
+  p.q = static_cast<const uint16_t*>(q);
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.out = static_cast<uint16_t*>(out), p.lse = lse;
+  p.status = static_cast<uint32_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
-  PrefixParams p{static_cast<const uint8_t*>(cache->kv), cache->kv_scale, cache->kv_dtype, cache->num_pages, page_tables, max_pages,
-                 n_seqs, seq_lens, max_seq_len, shared_len, q_per_seq, static_cast<const uint16_t*>(q), sm_scale,
-                 static_cast<uint16_t*>(out), lse, static_cast<uint32_t*>(workspace)};
-  return n_heads == 64 ? launch_simple<64>(p, st) : launch_simple<16>(p, st);
+  CUtensorMap map{};
+  if (cache->kv_dtype == SMLA_BF16) {
+    if (!encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cache->kv, kDqk, static_cast<uint64_t>(cache->num_pages) * kPage, kDqk * 2,
+                   64, kPage, CU_TENSOR_MAP_SWIZZLE_128B))
+      return SMLA_ERR_CUDA;
+    return launch<kBf16>(map, p, st);
+  }
+  return cache->kv_dtype == SMLA_FP8_E4M3 ? launch<kTokenFp8>(map, p, st) : launch<kTileFp8>(map, p, st);
 }
 
 }  // extern "C"
