@@ -78,6 +78,18 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, ui
             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint32_t width, uint32_t chunks) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {64, rows, width / 64};
+  cuuint64_t strides[2] = {width * 2, 128};
+  cuuint32_t box[3] = {64, kPage, chunks};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t prefill_min_workspace(int32_t n_tokens, int32_t topk) {
   if (n_tokens <= 0 || topk <= 0) return kStatusBytes;
   return kStatusBytes + (static_cast<size_t>(n_tokens) * topk * 4 + 255) / 256 * 256;

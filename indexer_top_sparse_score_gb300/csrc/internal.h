@@ -108,6 +108,10 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, ui
                uint64_t rows, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows,
                CUtensorMapSwizzle swizzle);
 
+// Rows of `width` 16-bit values as [width / 64 chunks][rows][64 values], loaded in
+// boxes of one page (64 rows) and `chunks` chunks, each chunk 128-byte swizzled.
+bool encode_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint32_t width, uint32_t chunks);
+
 int num_sms();
 
 }  // namespace smla

@@ -18,8 +18,8 @@
 // probabilities of the other page (16 KB), both sent through distributed shared
 // memory with their bytes counted on the receiver's barrier.
 //
-// Tensor memory (512 columns): O 256 | S 64 | Q values 0..383 (192). Shared
-// memory (216 KB + barriers): Q values 384..575, the keys of one tile in flight
+// Tensor memory (512 columns): O 256 | S 64 | six of Q's nine chunks (192). Shared
+// memory (216 KB + barriers): Q's other chunks, the keys of one tile in flight
 // in QK and one in PV as 17 slots of 64 keys x 64 values, and both halves of P:
 //   KO  own page, the 5 chunks that only QK reads     (1 tile)
 //   KV  own page, the 4 chunks of this CTA's output   (2 tiles)
@@ -35,6 +35,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <mutex>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,10 +48,12 @@ namespace smla {
 namespace {
 
 constexpr int kRows = 128;       // rows of a block (MMA M)
-constexpr int kOverhead = 2;     // cost of starting a segment, in tiles
+constexpr int kOverhead = 6;     // cost of starting a segment (Q in, results out), in tiles
 constexpr int kChunk = 64 * 128; // 64 keys x 64 values
 constexpr int kQChunk = kRows * 128;
-constexpr int kQTmemChunks = 6;  // Q chunks in tensor memory; the other 3 in shared memory
+// Q chunks follow the key slots they meet (KO 0-4, KV 0-3, below): those of KO 0-3
+// and KV 0-1 are in tensor memory, those of KO 4 and KV 2-3 in shared memory.
+constexpr int kQTmemChunks = 6;
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 constexpr int kOffQ = 0, kOffKO = 3 * kQChunk, kOffKV = kOffKO + 5 * kChunk, kOffVO = kOffKV + 8 * kChunk,
               kOffP = kOffVO + 4 * kChunk, kOffMeta = kOffP + 2 * kQChunk;
@@ -113,7 +116,7 @@ struct Piece {
   int s, t0, t1;  // tiles [t0, t1) of segment s
 };
 
-__device__ __forceinline__ bool next_piece(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
+__device__ __noinline__ bool next_piece(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
   while (L.s < p.n_seg && L.a < L.y) {
     const int tiles = seg_tiles(p, L.s), cost = seg_cost(tiles);
     const int s = L.s++;
@@ -139,34 +142,35 @@ struct Tiles {
   int t;
   const int32_t* table;
   int first_page, end_page;  // of the segment
-  int own, other;            // pool pages of the tile's page `rank` and of the other one, -1: none
-  bool bad;                  // a table entry is outside the pool
+  int own_id, other_id;      // table entries of the tile's page `rank` and of the other one (kNoPage past the end);
+                             // loaded a tile ahead and looked at when the tile is
+  static constexpr int kNoPage = INT_MIN;
 
-  __device__ __forceinline__ int page(const PrefixParams& p, int i) {
-    if (i >= end_page) return -1;
-    const int v = __ldg(table + i);
-    if (v >= 0 && v < p.num_pages) return v;
-    bad = true;
-    return -1;
+  __device__ __forceinline__ int entry(int i) const { return i < end_page ? __ldg(table + i) : kNoPage; }
+  // pool page of an entry, -1: none
+  static __device__ __forceinline__ int pool_page(const PrefixParams& p, int id) { return id >= 0 && id < p.num_pages ? id : -1; }
+  __device__ __forceinline__ bool bad(const PrefixParams& p) const {
+    return (own_id != kNoPage && pool_page(p, own_id) < 0) || (other_id != kNoPage && pool_page(p, other_id) < 0);
+  }
+  __device__ __noinline__ bool next_segment(const PrefixParams& p) {
+    if (!next_piece(p, line, pc, false)) return false;
+    t = pc.t0;
+    if (pc.s < p.n_rb) {
+      table = p.page_tables;
+      first_page = 0;
+      end_page = (p.shared_len + kPage - 1) / kPage;
+    } else {
+      const int i = pc.s - p.n_rb;
+      table = p.page_tables + static_cast<long long>(i / p.rb_s) * p.max_pages;
+      first_page = p.shared_len / kPage;
+      end_page = (own_end(p, i) + kPage - 1) / kPage;
+    }
+    return true;
   }
   __device__ __forceinline__ bool next(const PrefixParams& p, int rank, bool fresh) {
-    if (fresh || ++t >= pc.t1) {
-      if (!next_piece(p, line, pc, false)) return false;
-      t = pc.t0;
-      if (pc.s < p.n_rb) {
-        table = p.page_tables;
-        first_page = 0;
-        end_page = (p.shared_len + kPage - 1) / kPage;
-      } else {
-        const int i = pc.s - p.n_rb;
-        table = p.page_tables + static_cast<long long>(i / p.rb_s) * p.max_pages;
-        first_page = p.shared_len / kPage;
-        end_page = (own_end(p, i) + kPage - 1) / kPage;
-      }
-    }
-    bad = false;
-    own = page(p, first_page + 2 * t + rank);
-    other = page(p, first_page + 2 * t + (rank ^ 1));
+    if ((fresh || ++t >= pc.t1) && !next_segment(p)) return false;
+    own_id = entry(first_page + 2 * t + rank);
+    other_id = entry(first_page + 2 * t + (rank ^ 1));
     return true;
   }
 };
@@ -196,19 +200,35 @@ __device__ __forceinline__ void send_bulk(uint32_t dst, uint32_t src, uint32_t b
                "r"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-// Bounded wait that also acquires what the other CTA of the cluster sent.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
-  const long long t0 = clock64();
-  for (uint32_t it = 1;; ++it) {
-    uint32_t ok;
+// Bounded waits. The first try is inline, the rest a call: the kernel's loops have
+// to stay small (114 KB of code ran at 5,800 cycles a tile, most of it waiting for
+// instructions). kCluster: also acquires what the other CTA sent.
+template <bool kCluster>
+__device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if (kCluster)
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(bar), "r"(parity)
         : "memory");
-    if (ok) return true;
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  return ok != 0;
+}
+template <bool kCluster>
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (try_bar<kCluster>(bar, parity)) return true;
     if ((it & 15u) == 0) {
       if (*abort) return false;
       if (clock64() - t0 > kWaitLimitCycles) {
@@ -219,19 +239,72 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, vol
     }
   }
 }
-// A from tensor memory
-__device__ __forceinline__ void mma_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  const uint32_t a = smem_u32(bar);
+  return try_bar<false>(a, parity) || wait_long<false>(a, parity, abort, status);
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  const uint32_t a = smem_u32(bar);
+  return try_bar<true>(a, parity) || wait_long<true>(a, parity, abort, status);
+}
+// Bounded wait without a call, for the MMA role (a call takes its descriptors out of
+// the uniform registers). It polls and never suspends: a try_wait with a time
+// hint took some 300 cycles even on a phase that was complete, seven times a
+// tile. About four seconds of polls at most.
+template <bool kCluster>
+__device__ __forceinline__ bool wait_poll(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  for (uint32_t it = 0; it < (1u << 28); ++it) {
+    uint32_t ok;
+    if (kCluster)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(a), "r"(parity)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(a), "r"(parity)
+          : "memory");
+    if (ok) return true;
+    if ((it & 63u) == 63u && *abort) return false;
+  }
+  *abort = 2;  // reported as a timeout by the end of the kernel
+  return false;
+}
+// true in one thread of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// chunks z .. of a page (box 64 values x 64 keys x chunks: one 8 KB slot per chunk)
+__device__ __forceinline__ void tma_chunks(void* dst, const CUtensorMap* map, uint64_t* bar, int y, int z) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(y), "r"(z)
+      : "memory");
+}
+// A from tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // arrives on the barrier at this address in both CTAs of the pair
-__device__ __forceinline__ void commit_pair_warp(uint64_t* bar) {
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
           smem_u32(bar))
       : "memory");
 }
@@ -288,7 +361,7 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 struct Limits {
   int lo, hi, min_hi, max_hi;
 };
-__device__ __forceinline__ Limits limits(const PrefixParams& p, int s, int row) {
+__device__ __noinline__ Limits limits(const PrefixParams& p, int s, int row) {
   Limits m;
   m.hi = 0, m.min_hi = INT_MAX, m.max_hi = 0;
   const bool shared = s < p.n_rb;
@@ -315,7 +388,7 @@ constexpr int kThreadsOf = FMT == kBf16 ? 192 : 192 + 32 * kConvWarps;
 
 template <int FMT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
-    prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const PrefixParams p) {
+    prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map, const PrefixParams p) {
   constexpr bool F16 = FMT == kTileFp8;  // operand type of the MMAs
   constexpr uint32_t kFmt = F16 ? kFmtF16 : kFmtBF16;
   constexpr int kThreads = kThreadsOf<FMT>;
@@ -428,7 +501,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     const uint32_t peer_pbar = peer_addr(smem_u32(&M.p_other), rank ^ 1);
     const bool writer = rank == 0 && tid == 0;
     bool over = false;
-    // a thread's row of Q: chunks 0-5 into its lane of tensor memory, 6-8 into shared memory
+    // a thread's row of Q: six chunks into its lane of tensor memory, three into shared memory
     auto load_q = [&](int s) {
       const bool shared = s < p.n_rb;
       const int i = s - p.n_rb, b = shared ? 0 : i / p.rb_s;
@@ -436,11 +509,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       const int limit = shared ? p.n_rows : p.q_per_seq << p.hshift;
       const long long flat = (static_cast<long long>(b) * p.q_per_seq << p.hshift) + r;
       const uint4* src = reinterpret_cast<const uint4*>(p.q + flat * kDqk);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < kDqk / 64; ++c) {
+        // c < 6: KO 0-3, KV 0-1; then KO 4, KV 2-3
+        const int chunk = c < 4 ? 4 * (rank ^ 1) + c : c < 6 ? 4 * rank + c - 4 : c == 6 ? 8 : 4 * rank + c - 5;
         uint4 v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = r < limit ? __ldg(src + 8 * c + j) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 8; ++j) v[j] = r < limit ? __ldg(src + 8 * chunk + j) : make_uint4(0, 0, 0, 0);
         if (F16) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -462,20 +537,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     };
 
     Line wline = line;
-    Piece pc;
-    bool have = next_piece(p, wline, pc, writer);
-    if (have) load_q(pc.s);
+    Piece pc, nx;
+    nx.s = 0;
+    bool have = next_piece(p, wline, nx, writer), started = false;
     Tiles cur;
     cur.line = line;
     bool more = cur.next(p, rank, true);
     uint32_t g = 0;
     bool ok = true;
-    while (have && ok) {
-      const Limits lim = limits(p, pc.s, row);
-      float m = -INFINITY, l = 0.0f;
+    Limits lim;
+    float m = 0.0f, l = 0.0f;
+    while (ok) {
+      // the next piece's Q while the last product of this one runs, then this one's results
+      if (have) load_q(nx.s);
+      if (started) {
+        if (!__all_sync(0xFFFFFFFFu, wait_cluster(&M.pv_done, (g - 1) & 1, abort_v, p.status))) break;
+        tc_fence_after();
+        const int slot = pc.s + pair;
+        float4* o = p.part_o + (static_cast<long long>(slot) * 2 + rank) * 64 * kRows + row;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          float v[32];
+          tmem_ld_32x32b_x32(tmem + lanes + kColO + 32 * c, reinterpret_cast<uint32_t*>(v));
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[(8 * c + j) * kRows] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&M.o_free);
+        // a row that sees none of the segment's keys took part in the unmasked tiles: dropped here
+        if (lim.hi <= lim.lo) l = 0.0f;
+        if (rank == 0) p.part_m[static_cast<long long>(slot) * kRows + row] = m;
+        p.part_l[(static_cast<long long>(slot) * 2 + rank) * kRows + row] = l;
+      }
+      if (!have) break;
+      started = true;
+      pc = nx;
+      lim = limits(p, pc.s, row);
+      m = -INFINITY, l = 0.0f;
       for (int t = pc.t0; t < pc.t1; ++t, ++g) {
         const int tile_k = (cur.first_page + 2 * t) * kPage, key0 = tile_k + rank * kPage;
-        const int own = cur.own;
+        const int own = Tiles::pool_page(p, cur.own_id);
         const float* ks = M.ks[warp][g & 1];
         if (FMT == kTokenFp8) {  // scales of the own page, a copy per warp
           const float2 sc = own >= 0 ? __ldg(reinterpret_cast<const float2*>(p.kv_scale + static_cast<long long>(own) * kPage) + lane)
@@ -484,7 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
           __syncwarp();
         }
         if (more) more = cur.next(p, rank, false);
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_spin(&M.s_full, g & 1, abort_v, p.status))) {
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(&M.s_full, g & 1, abort_v, p.status))) {
           ok = false;
           break;
         }
@@ -567,8 +670,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         // only some see are zeroed if they hold a value that is not finite (those
         // that see it have a logit that is not finite either)
         if (tile_k < lim.lo || tile_k + 2 * kPage > lim.min_hi) {
-          const bool w_ok = mbar_wait(&M.kv_full[g & 1], (g >> 1) & 1, abort_v, p.status) &&
-                            mbar_wait(&M.vo_full, g & 1, abort_v, p.status);
+          const bool w_ok = wait_bar(&M.kv_full[g & 1], (g >> 1) & 1, abort_v, p.status) &&
+                            wait_bar(&M.vo_full, g & 1, abort_v, p.status);
           if (!__all_sync(0xFFFFFFFFu, w_ok)) {
             ok = false;
             break;
@@ -598,35 +701,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         }
         __syncwarp();
       }
-      if (!ok) break;
-      // the next piece's Q while the last product runs, then this piece's results
-      const int slot = pc.s + pair;
-      have = next_piece(p, wline, pc, writer);
-      if (have) load_q(pc.s);
-      if (!__all_sync(0xFFFFFFFFu, wait_cluster(&M.pv_done, (g - 1) & 1, abort_v, p.status))) break;
-      tc_fence_after();
-      float4* o = p.part_o + (static_cast<long long>(slot) * 2 + rank) * 64 * kRows + row;
-#pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        float v[32];
-        tmem_ld_32x32b_x32(tmem + lanes + kColO + 32 * c, reinterpret_cast<uint32_t*>(v));
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[(8 * c + j) * kRows] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&M.o_free);
-      // a row that sees none of the segment's keys took part in the unmasked tiles: dropped here
-      if (lim.hi <= lim.lo) l = 0.0f;
-      if (rank == 0) p.part_m[static_cast<long long>(slot) * kRows + row] = m;
-      p.part_l[(static_cast<long long>(slot) * 2 + rank) * kRows + row] = l;
+      if (ok) have = next_piece(p, wline, nx, writer);
     }
     if (over) set_status(p.status, kStatusOverflow);
   } else if (warp == 4) {
     // -------------------------------------------------------------- TMA loads
-    if (FMT == kBf16 && lane == 0) {
-      const int v0 = 256 * rank, k0 = 256 * (rank ^ 1);
+    if (FMT == kBf16 && elect_one()) {
+      const int v0 = 4 * rank, k0 = 4 * (rank ^ 1);  // first chunk of this CTA's output values, of the others
       Tiles cur;
       cur.line = line;
       bool more = cur.next(p, rank, true);
@@ -634,26 +715,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       // a page that is missing reads as zeros: a box wholly before the pool
       auto y = [](int page) { return page >= 0 ? page * kPage : -kPage; };
       auto load_vo = [&](uint32_t h, int page) {
-        if (h > 0 && !mbar_wait(&M.vo_free, (h - 1) & 1, abort_v, p.status)) return false;
+        if (h > 0 && !wait_bar(&M.vo_free, (h - 1) & 1, abort_v, p.status)) return false;
         mbar_arrive_expect_tx(&M.vo_full, 4 * kChunk);
-        for (int i = 0; i < 4; ++i) tma_load_2d(smem + kOffVO + i * kChunk, &kv_map, &M.vo_full, v0 + 64 * i, y(page));
+        tma_chunks(smem + kOffVO, &kv_map, &M.vo_full, y(page), v0);
         return true;
       };
       uint32_t g = 0;
       bool ok = true;
       for (; more && ok; ++g) {
-        const int own = cur.own, other = cur.other;
-        if (cur.bad) set_status(p.status, kStatusBounds);
+        const int own = Tiles::pool_page(p, cur.own_id), other = Tiles::pool_page(p, cur.other_id);
+        if (cur.bad(p)) set_status(p.status, kStatusBounds);
         more = cur.next(p, rank, false);
-        if (g > 0 && !mbar_wait(&M.ko_free, (g - 1) & 1, abort_v, p.status)) { ok = false; break; }
+        if (g > 0 && !wait_bar(&M.ko_free, (g - 1) & 1, abort_v, p.status)) { ok = false; break; }
         mbar_arrive_expect_tx(&M.ko_full, 5 * kChunk);
-        for (int i = 0; i < 5; ++i)
-          tma_load_2d(smem + kOffKO + i * kChunk, &kv_map, &M.ko_full, i < 4 ? k0 + 64 * i : kDv, y(own));
+        tma_chunks(smem + kOffKO, &kv_map, &M.ko_full, y(own), k0);
+        tma_chunks(smem + kOffKO + 4 * kChunk, &rope_map, &M.ko_full, y(own), 8);
         const int buf = g & 1;
-        if (g > 1 && !mbar_wait(&M.kv_free[buf], ((g >> 1) - 1) & 1, abort_v, p.status)) { ok = false; break; }
+        if (g > 1 && !wait_bar(&M.kv_free[buf], ((g >> 1) - 1) & 1, abort_v, p.status)) { ok = false; break; }
         mbar_arrive_expect_tx(&M.kv_full[buf], 4 * kChunk);
-        for (int i = 0; i < 4; ++i)
-          tma_load_2d(smem + kOffKV + (4 * buf + i) * kChunk, &kv_map, &M.kv_full[buf], v0 + 64 * i, y(own));
+        tma_chunks(smem + kOffKV + 4 * buf * kChunk, &kv_map, &M.kv_full[buf], y(own), v0);
         if (g > 0) ok = load_vo(g - 1, last_other);
         last_other = other;
       }
@@ -661,11 +741,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     }
   } else if (warp == 5) {
     // -------------------------------------------------------------- MMA issue
+    // tcgen05.mma takes its descriptors from uniform registers. So the loop runs
+    // warp-wide on warp-uniform values, each batch of MMAs is unrolled with constant
+    // offsets and issued by one thread chosen with elect.sync (the compiler then
+    // knows that one thread is active), and no call or wait stands inside a batch.
+    // Measured on the issue alone, a tile's 44 MMAs: 2,376 cycles (back to back) in
+    // this form; 4,185 under `if (lane == 0)`, where each MMA becomes a loop over
+    // the active threads; about 3,300 with waits inside the batches.
     constexpr uint32_t id_qk = instr_desc(128, 64, kFmt, kFmt, false, false);
     constexpr uint32_t id_pv = instr_desc(128, 256, kFmt, kFmt, false, true);
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const uint32_t sb = __shfl_sync(0xFFFFFFFFu, sbase, 0);
-    const int rk = __shfl_sync(0xFFFFFFFFu, rank, 0);
     const uint64_t q_desc = smem_desc(sb + kOffQ, 16, 1024);
     const uint64_t ko_desc = smem_desc(sb + kOffKO, 16, 1024);
     const uint64_t kv_desc = smem_desc(sb + kOffKV, 16, 1024);
@@ -673,73 +759,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     const uint64_t vo_desc = smem_desc(sb + kOffVO, kChunk, 1024);
     const uint64_t p_desc = smem_desc(sb + kOffP, 16, 1024);
     const uint64_t po_desc = smem_desc(sb + kOffP + kQChunk, 16, 1024);
-    // logits of one chunk of 64 values: Q chunk c (tensor or shared memory) with the keys at `k`
-    auto qk = [&](int c, uint64_t k, bool first) {
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint64_t b = k + static_cast<uint64_t>(2 * kk);
-        const uint32_t acc = !first || kk != 0;
-        if (c < kQTmemChunks)
-          mma_ts_warp(tm + kColS, tm + kColQ + 32 * c + 8 * kk, b, id_qk, acc);
-        else
-          mma_f16_warp(tm + kColS, q_desc + static_cast<uint64_t>(((c - kQTmemChunks) * kQChunk >> 4) + 2 * kk), b, id_qk, acc);
-      }
-    };
     Line wline = line;
     Piece pc;
     uint32_t g = 0, n = 0;
     bool ok = true;
-    auto all = [](bool v) { return __all_sync(0xFFFFFFFFu, v); };
-    // O (+)= P V of tile h, own page first (its V slots are the next to be refilled)
-    auto pv = [&](uint32_t h, bool first) {
-      bool w = mbar_wait_spin(&M.p_own, h & 1, abort_v, p.status);
-      if (first && n > 0) w = w && mbar_wait(&M.o_free, (n - 1) & 1, abort_v, p.status);
-      if (!all(w)) return false;
-      tc_fence_after();
-      const uint64_t v = v_desc + static_cast<uint64_t>((h & 1) * (4 * kChunk >> 4));
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_f16_warp(tm + kColO, p_desc + static_cast<uint64_t>(2 * kk), v + static_cast<uint64_t>(kk * 2048 >> 4), id_pv,
-                     !first || kk != 0);
-      mma_commit_warp(&M.kv_free[h & 1]);
-      if (lane == 0) mbar_arrive_expect_tx(&M.p_other, kQChunk);
-      w = wait_cluster(&M.p_other, h & 1, abort_v, p.status) && mbar_wait_spin(&M.vo_full, h & 1, abort_v, p.status);
-      if (!all(w)) return false;
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_f16_warp(tm + kColO, po_desc + static_cast<uint64_t>(2 * kk), vo_desc + static_cast<uint64_t>(kk * 2048 >> 4), id_pv, 1);
-      mma_commit_warp(&M.vo_free);
-      commit_pair_warp(&M.pv_done);
-      return true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xFFFFFFFFu, wait_poll<false>(bar, parity, abort_v));
     };
     while (ok && next_piece(p, wline, pc, false)) {
-      if (!all(mbar_wait(&M.q_full, n & 1, abort_v, p.status))) break;
-      for (int t = pc.t0; t < pc.t1; ++t, ++g) {
-        const bool w = mbar_wait_spin(&M.ko_full, g & 1, abort_v, p.status) &&
-                       (g == 0 || mbar_wait_spin(&M.s_free, (g - 1) & 1, abort_v, p.status));
-        if (!all(w)) { ok = false; break; }
-        tc_fence_after();
+      if (!wait(&M.q_full, n & 1)) break;
+      const int t0 = __shfl_sync(0xFFFFFFFFu, pc.t0, 0), t1 = __shfl_sync(0xFFFFFFFFu, pc.t1, 0);
+      // step t: the logits of tile t, then the product of tile t - 1
+      for (int t = t0; t <= t1; ++t) {
+        if (t < t1) {
+          if (!wait(&M.ko_full, g & 1) || (g > 0 && !wait(&M.s_free, (g - 1) & 1))) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // Q chunk of slot i: 4 (1 - rank) + i
-          if (rk == 0) qk(4 + i, ko_desc + static_cast<uint64_t>(i * kChunk >> 4), i == 0);
-          else qk(i, ko_desc + static_cast<uint64_t>(i * kChunk >> 4), i == 0);
-        }
-        qk(8, ko_desc + static_cast<uint64_t>(4 * kChunk >> 4), false);
-        mma_commit_warp(&M.ko_free);
-        if (!all(mbar_wait_spin(&M.kv_full[g & 1], (g >> 1) & 1, abort_v, p.status))) { ok = false; break; }
-        tc_fence_after();
-        const uint64_t kd = kv_desc + static_cast<uint64_t>((g & 1) * (4 * kChunk >> 4));
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (rk == 0) qk(i, kd + static_cast<uint64_t>(i * kChunk >> 4), false);
-          else qk(4 + i, kd + static_cast<uint64_t>(i * kChunk >> 4), false);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(tm + kColS, tm + kColQ + 32 * i + 8 * kk, ko_desc + static_cast<uint64_t>((i * kChunk >> 4) + 2 * kk), id_qk,
+                       i != 0 || kk != 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16(tm + kColS, q_desc + static_cast<uint64_t>(2 * kk), ko_desc + static_cast<uint64_t>((4 * kChunk >> 4) + 2 * kk),
+                      id_qk, 1);
+            mma_commit(&M.ko_free);
+          }
+          __syncwarp();
+          if (!wait(&M.kv_full[g & 1], (g >> 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t kd = kv_desc + static_cast<uint64_t>((g & 1) * (4 * kChunk >> 4));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(tm + kColS, tm + kColQ + 128 + 32 * i + 8 * kk, kd + static_cast<uint64_t>((i * kChunk >> 4) + 2 * kk), id_qk, 1);
+#pragma unroll
+            for (int i = 2; i < 4; ++i)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f16(tm + kColS, q_desc + static_cast<uint64_t>(((i - 1) * kQChunk >> 4) + 2 * kk),
+                        kd + static_cast<uint64_t>((i * kChunk >> 4) + 2 * kk), id_qk, 1);
+            mma_commit(&M.s_full);
+          }
+          __syncwarp();
+          ++g;
         }
-        mma_commit_warp(&M.s_full);
-        if (t > pc.t0 && !pv(g - 1, t - 1 == pc.t0)) { ok = false; break; }
+        if (t > t0) {
+          const uint32_t h = t < t1 ? g - 2 : g - 1;  // the tile before
+          const uint32_t first = t - 1 == t0;
+          if (!wait(&M.p_own, h & 1) || (first && n > 0 && !wait(&M.o_free, (n - 1) & 1))) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            // own page first: its V slots are the next to be refilled
+            const uint64_t v = v_desc + static_cast<uint64_t>((h & 1) * (4 * kChunk >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16(tm + kColO, p_desc + static_cast<uint64_t>(2 * kk), v + static_cast<uint64_t>(kk * 2048 >> 4), id_pv,
+                      kk != 0 ? 1 : first ^ 1);
+            mma_commit(&M.kv_free[h & 1]);
+            mbar_arrive_expect_tx(&M.p_other, kQChunk);
+          }
+          __syncwarp();
+          if (!__all_sync(0xFFFFFFFFu, wait_poll<true>(&M.p_other, h & 1, abort_v)) || !wait(&M.vo_full, h & 1)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16(tm + kColO, po_desc + static_cast<uint64_t>(2 * kk), vo_desc + static_cast<uint64_t>(kk * 2048 >> 4), id_pv, 1);
+            mma_commit(&M.vo_free);
+            commit_pair(&M.pv_done);
+          }
+          __syncwarp();
+        }
       }
-      if (!ok || !pv(g - 1, pc.t1 - 1 == pc.t0)) break;
       ++n;
     }
   } else if (FMT != kBf16) {
@@ -813,30 +909,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_v, p.status)); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, abort_v, p.status)); };
     Tiles cur;
     cur.line = line;
     bool more = cur.next(p, rank, true);
     Group ko, kv, vo;  // each group's next load is in flight while the others are stored
     if (more) {
-      fetch(ko, cur.own, kc0, 5);
-      fetch(kv, cur.own, vc0, 4);
+      fetch(ko, Tiles::pool_page(p, cur.own_id), kc0, 5);
+      fetch(kv, Tiles::pool_page(p, cur.own_id), vc0, 4);
     }
     uint32_t g = 0;
     bool ok = true;
     for (; more && ok; ++g) {
-      const int other = cur.other;
-      if (cur.bad && lane == 0) set_status(p.status, kStatusBounds);
+      const int other = Tiles::pool_page(p, cur.other_id);
+      if (cur.bad(p) && lane == 0) set_status(p.status, kStatusBounds);
       more = cur.next(p, rank, false);
       if (g > 0 && !wait(&M.ko_free, (g - 1) & 1)) { ok = false; break; }
       store(ko, kOffKO, kc0, 5);
       filled(&M.ko_full);
-      if (more) fetch(ko, cur.own, kc0, 5);
+      if (more) fetch(ko, Tiles::pool_page(p, cur.own_id), kc0, 5);
       const int buf = g & 1;
       if (g > 1 && !wait(&M.kv_free[buf], ((g >> 1) - 1) & 1)) { ok = false; break; }
       store(kv, kOffKV + 4 * buf * kChunk, vc0, 4);
       filled(&M.kv_full[buf]);
-      if (more) fetch(kv, cur.own, vc0, 4);
+      if (more) fetch(kv, Tiles::pool_page(p, cur.own_id), vc0, 4);
       if (g > 0) {
         if (g > 1 && !wait(&M.vo_free, (g - 2) & 1)) { ok = false; break; }
         store(vo, kOffVO, vc0, 4);
@@ -852,6 +948,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
   }
 
   __syncwarp();
+  if (*abort_v == 2) set_status(p.status, kStatusTimeout);
   if (*abort_v) {  // a wait gave up: let copies that are still under way land before the memory goes
     const long long t0 = clock64();
     while (clock64() - t0 < 4000000) __nanosleep(1000);
@@ -966,19 +1063,51 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
 }
 
 template <int FMT>
-int launch(const CUtensorMap& map, const PrefixParams& p, cudaStream_t st) {
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(prefix_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
-  if (attr != cudaSuccess) return SMLA_ERR_CUDA;
-  prefix_kernel<FMT><<<2 * p.pairs, kThreadsOf<FMT>, kSmemBytes, st>>>(map, p);
+bool set_smem() {
+  return cudaFuncSetAttribute(prefix_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) == cudaSuccess;
+}
+
+template <int FMT>
+int launch(const CUtensorMap& map, const CUtensorMap& rope, const PrefixParams& p, cudaStream_t st) {
+  if (!set_smem<FMT>()) return SMLA_ERR_CUDA;
+  prefix_kernel<FMT><<<2 * p.pairs, kThreadsOf<FMT>, kSmemBytes, st>>>(map, rope, p);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
   merge_kernel<<<p.n_rows / kMergeRows, kMergeThreads, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
-size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+template <int FMT>
+int resident_pairs() {
+  if (!set_smem<FMT>()) return 0;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * num_sms());
+  cfg.blockDim = dim3(kThreadsOf<FMT>);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.attrs = &at, cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, prefix_kernel<FMT>, &cfg) == cudaSuccess ? n : 0;
+}
 
-int pairs_of_device() { return std::max(1, std::min(num_sms() / 2, kMaxPairs)); }
+// CTA pairs that run at the same time: fewer than half of the SMs where a GPC has
+// an odd number of them. One pair more than that starts when the others end, and the
+// call takes nearly twice as long (64x2 on a 64K prompt: 1.16 ms with 76 pairs).
+int pairs_of_device() {
+  static std::mutex mutex;
+  static int known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (known[dev] == 0) {
+    const int n = std::min({resident_pairs<kBf16>(), resident_pairs<kTokenFp8>(), resident_pairs<kTileFp8>()});
+    known[dev] = std::max(1, std::min(n > 0 ? n : num_sms() / 2, kMaxPairs));
+  }
+  return known[dev];
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Row blocks and segments; false: more than 32-bit counts hold.
 bool plan(PrefixParams& p) {
@@ -1051,14 +1180,13 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
   p.status = static_cast<uint32_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
-  CUtensorMap map{};
+  CUtensorMap map{}, rope{};
   if (cache->kv_dtype == SMLA_BF16) {
-    if (!encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cache->kv, kDqk, static_cast<uint64_t>(cache->num_pages) * kPage, kDqk * 2,
-                   64, kPage, CU_TENSOR_MAP_SWIZZLE_128B))
-      return SMLA_ERR_CUDA;
-    return launch<kBf16>(map, p, st);
+    const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * kPage;
+    if (!encode_chunks(&map, cache->kv, rows, kDqk, 4) || !encode_chunks(&rope, cache->kv, rows, kDqk, 1)) return SMLA_ERR_CUDA;
+    return launch<kBf16>(map, rope, p, st);
   }
-  return cache->kv_dtype == SMLA_FP8_E4M3 ? launch<kTokenFp8>(map, p, st) : launch<kTileFp8>(map, p, st);
+  return cache->kv_dtype == SMLA_FP8_E4M3 ? launch<kTokenFp8>(map, rope, p, st) : launch<kTileFp8>(map, rope, p, st);
 }
 
 }  // extern "C"

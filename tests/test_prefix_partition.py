@@ -7,7 +7,7 @@ import random
 
 import pytest
 
-OVERHEAD = 2
+OVERHEAD = 6
 
 
 def pieces(tiles, pairs):
