@@ -82,7 +82,8 @@ struct PrefixParams {
   int32_t n_rb, n_pt; // row blocks and tiles of the shared part (n_rb = 0: nothing shared)
   int32_t rb_s;       // row blocks of one request
   int32_t n_seg, pairs;
-  long long* seg_off; // [0] length of the line, [1 + i] where own segment i starts
+  long long* seg_off; // [i] where own segment i starts on the line
+  long long* bounds;  // [pairs + 1] where each pair's stretch starts
   float* part_m;      // [slot][128]
   float* part_l;      // [slot][2][128]
   float4* part_o;     // [slot][2][64][128]: four output values of a row
@@ -122,7 +123,7 @@ __device__ __noinline__ bool next_piece(const PrefixParams& p, Line& L, Piece& p
     const int s = L.s++;
     const long long a = L.a;
     if (cost == 0) continue;
-    if (writer && s >= p.n_rb && a >= L.x) p.seg_off[1 + s - p.n_rb] = a;
+    if (writer && s >= p.n_rb && a >= L.x) p.seg_off[s - p.n_rb] = a;
     L.a += cost;
     const long long t0 = max(L.x - a - kOverhead, 0LL), t1 = min(L.y - a - kOverhead, static_cast<long long>(tiles));
     if (t1 > t0) {
@@ -446,7 +447,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     for (int w = 0; w < kThreads / 32; ++w) total += M.scan[w];
     line.x = total * pair / p.pairs;
     line.y = total * (pair + 1) / p.pairs;
-    if (pair == 0 && rank == 0 && tid == 0) p.seg_off[0] = total;
+    if (rank == 0 && tid == 0) {
+      p.bounds[pair] = line.x;
+      if (pair == p.pairs - 1) p.bounds[p.pairs] = line.y;
+    }
     if (line.x < line.y) {
       if (line.x < shared_cost) {
         if (tid == 0) {
@@ -501,32 +505,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     const uint32_t peer_pbar = peer_addr(smem_u32(&M.p_other), rank ^ 1);
     const bool writer = rank == 0 && tid == 0;
     bool over = false;
-    // a thread's row of Q: six chunks into its lane of tensor memory, three into shared memory
+    // Q of segment s. A warp brings its 32 rows in 16-byte pieces, eight lanes on one
+    // row's chunk (128 contiguous bytes), kBatch chunks in flight. The three chunks
+    // that stay in shared memory are stored where they belong; the six for tensor
+    // memory pass through those places, from where every lane reads its own row.
+    // (The logits of the previous piece are complete, so both are free.)
     auto load_q = [&](int s) {
+      constexpr int kBatch = FMT == kBf16 ? 3 : 1;
       const bool shared = s < p.n_rb;
       const int i = s - p.n_rb, b = shared ? 0 : i / p.rb_s;
-      const int r = (shared ? s : i - b * p.rb_s) * kRows + row;
-      const int limit = shared ? p.n_rows : p.q_per_seq << p.hshift;
-      const long long flat = (static_cast<long long>(b) * p.q_per_seq << p.hshift) + r;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + flat * kDqk);
+      const int first = (shared ? s : i - b * p.rb_s) * kRows + warp * 32;
+      const int limit = (shared ? p.n_rows : p.q_per_seq << p.hshift) - first;  // rows of the warp that exist
+      const uint16_t* src = p.q + ((static_cast<long long>(b) * p.q_per_seq << p.hshift) + first) * kDqk;
+      const int sub = lane >> 3, pcs = lane & 7;
 #pragma unroll 1
-      for (int c = 0; c < kDqk / 64; ++c) {
-        // c < 6: KO 0-3, KV 0-1; then KO 4, KV 2-3
-        const int chunk = c < 4 ? 4 * (rank ^ 1) + c : c < 6 ? 4 * rank + c - 4 : c == 6 ? 8 : 4 * rank + c - 5;
-        uint4 v[8];
+      for (int c0 = 0; c0 < kDqk / 64; c0 += kBatch) {
+        uint4 v[kBatch][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = r < limit ? __ldg(src + 8 * chunk + j) : make_uint4(0, 0, 0, 0);
-        if (F16) {
+        for (int u = 0; u < kBatch; ++u) {
+          const int c = c0 + u;
+          const int chunk = c < 4 ? 4 * (rank ^ 1) + c : c < 6 ? 4 * rank + c - 4 : c == 6 ? 8 : 4 * rank + c - 5;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            v[j] = make_uint4(to_f16(v[j].x, over), to_f16(v[j].y, over), to_f16(v[j].z, over), to_f16(v[j].w, over));
+          for (int j = 0; j < 8; ++j) {
+            const int r = 4 * j + sub;
+            v[u][j] = r < limit ? __ldg(reinterpret_cast<const uint4*>(src + r * kDqk + chunk * 64 + pcs * 8)) : make_uint4(0, 0, 0, 0);
+          }
         }
-        if (c < kQTmemChunks) {
-          tmem_st_32x32b_x32(tmem + lanes + kColQ + 32 * c, reinterpret_cast<const uint32_t*>(v));
-        } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(smem + kOffQ + (c - kQTmemChunks) * kQChunk + piece_off(row, j)) = v[j];
+        for (int u = 0; u < kBatch; ++u) {
+          const int c = c0 + u;
+          uint8_t* at = smem + kOffQ + (c % 3) * kQChunk;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint4 w = v[u][j];
+            if (F16) w = make_uint4(to_f16(w.x, over), to_f16(w.y, over), to_f16(w.z, over), to_f16(w.w, over));
+            *reinterpret_cast<uint4*>(at + piece_off(warp * 32 + 4 * j + sub, pcs)) = w;
+          }
+        }
+        if (c0 < kQTmemChunks) {
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            const int c = c0 + u;
+            uint4 w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint4*>(smem + kOffQ + (c % 3) * kQChunk + piece_off(row, j));
+            tmem_st_32x32b_x32(tmem + lanes + kColQ + 32 * c, reinterpret_cast<const uint32_t*>(w));
+          }
+          __syncwarp();
         }
       }
       tmem_wait_st();
@@ -535,11 +561,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&M.q_full);
     };
+    // the rows of a later segment's Q into L2
+    auto prefetch_q = [&](int s) {
+      const bool shared = s < p.n_rb;
+      const int i = s - p.n_rb, b = shared ? 0 : i / p.rb_s;
+      const int r = (shared ? s : i - b * p.rb_s) * kRows + row;
+      if (r < (shared ? p.n_rows : p.q_per_seq << p.hshift))
+        prefetch_l2_lines(p.q + ((static_cast<long long>(b) * p.q_per_seq << p.hshift) + r) * kDqk, 2 * kDqk);
+    };
 
     Line wline = line;
     Piece pc, nx;
     nx.s = 0;
     bool have = next_piece(p, wline, nx, writer), started = false;
+    Limits next_lim;
+    if (have) next_lim = limits(p, nx.s, row);
     Tiles cur;
     cur.line = line;
     bool more = cur.next(p, rank, true);
@@ -574,8 +610,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       if (!have) break;
       started = true;
       pc = nx;
-      lim = limits(p, pc.s, row);
+      lim = next_lim;
       m = -INFINITY, l = 0.0f;
+      have = next_piece(p, wline, nx, writer);
+      if (have) {
+        prefetch_q(nx.s);
+        next_lim = limits(p, nx.s, row);
+      }
       for (int t = pc.t0; t < pc.t1; ++t, ++g) {
         const int tile_k = (cur.first_page + 2 * t) * kPage, key0 = tile_k + rank * kPage;
         const int own = Tiles::pool_page(p, cur.own_id);
@@ -701,7 +742,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         }
         __syncwarp();
       }
-      if (ok) have = next_piece(p, wline, nx, writer);
     }
     if (over) set_status(p.status, kStatusOverflow);
   } else if (warp == 4) {
@@ -963,43 +1003,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
 }
 
 // ------------------------------------------------------------------ joining the pieces
-// A block joins 16 rows (one token's or part of one's heads): the pieces of
-// their shared segment and of their own one, weighted by 2^(m - largest m).
-constexpr int kMergeRows = 16, kMergeThreads = 256;
+// A block joins 128 output values of 16 rows (one token's heads or part of them):
+// the pieces of the rows' shared segment and of their own one, weighted by
+// 2^(m - largest m). Reading fp32 partials that were just written, it is bound by
+// L2 and, for few rows, by latency: four blocks share a row's values, and each
+// thread keeps eight 16-byte loads in flight.
+constexpr int kMergeRows = 16, kMergeCols = 128, kMergeThreads = 256;
 
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams p) {
   __shared__ int slots[kMaxPieces];       // slot * 128 + the rows' place in the block
   __shared__ float wgt[kMaxPieces][kMergeRows];
   __shared__ float inv[kMergeRows];
-  __shared__ __align__(16) uint16_t o[kMergeRows][kDv];
+  __shared__ __align__(16) uint16_t o[kMergeRows][kMergeCols];
   __shared__ int s_n;
   const int tid = threadIdx.x, lane = tid & 31;
   const int r0 = blockIdx.x * kMergeRows;
-  const long long total = p.seg_off[0];
+  const int cols = blockIdx.y * kMergeCols;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
   if (tid < 32) {
     int n = 0;
 #pragma unroll 1
     for (int part = 0; part < 2; ++part) {
-      int s, at;
-      long long a;
-      if (part == 0) {
-        if (p.n_rb == 0) continue;
-        s = r0 / kRows;
-        at = r0 % kRows;
-        a = static_cast<long long>(s) * seg_cost(p.n_pt);
-      } else {
+      if (part == 0 && p.n_rb == 0) continue;
+      int s = r0 / kRows, at = r0 % kRows;
+      if (part == 1) {
         const int per = p.q_per_seq << p.hshift, b = r0 / per, in = r0 - b * per;
         s = p.n_rb + b * p.rb_s + in / kRows;
         at = in % kRows;
-        a = 0;
       }
       const int tiles = seg_tiles(p, s);
       if (tiles == 0) continue;
-      if (part == 1) a = p.seg_off[1 + s - p.n_rb];
+      const long long a = part == 1 ? p.seg_off[s - p.n_rb] : static_cast<long long>(s) * seg_cost(p.n_pt);
       const long long t0 = a + kOverhead, t1 = t0 + tiles;
       for (int base = 0; base < p.pairs; base += 32) {
         const int q = base + lane;
-        const bool in = q < p.pairs && max(total * q / p.pairs, t0) < min(total * (q + 1) / p.pairs, t1);
+        const bool in = q < p.pairs && max(p.bounds[q], t0) < min(p.bounds[q + 1], t1);
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, in);
         const int at_n = n + __popc(mask & ((1u << lane) - 1));
         if (in && at_n < kMaxPieces) slots[at_n] = (s + q) * kRows + at;
@@ -1016,7 +1054,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
     for (int i = k; i < n; i += 16) {
       const int slot = slots[i] / kRows, at = slots[i] % kRows + row;
       const float l = p.part_l[(static_cast<long long>(slot) * 2) * kRows + at] + p.part_l[(static_cast<long long>(slot) * 2 + 1) * kRows + at];
-      if (l != 0.0f) top = fmaxf(top, p.part_m[static_cast<long long>(slot) * kRows + at]);
+      const float m = p.part_m[static_cast<long long>(slot) * kRows + at];
+      // a row that saw nothing in a piece (l = 0) has nothing there, whatever its O holds
+      wgt[i][row] = l != 0.0f ? m : -INFINITY;
+      if (l != 0.0f) top = fmaxf(top, m);
     }
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
@@ -1024,8 +1065,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
     for (int i = k; i < n; i += 16) {
       const int slot = slots[i] / kRows, at = slots[i] % kRows + row;
       const float l = p.part_l[(static_cast<long long>(slot) * 2) * kRows + at] + p.part_l[(static_cast<long long>(slot) * 2 + 1) * kRows + at];
-      // a row that saw nothing in a piece (l = 0) has nothing there, whatever its O holds; -1 marks it
-      const float w = l != 0.0f ? exp2_fast(p.part_m[static_cast<long long>(slot) * kRows + at] - top) : -1.0f;
+      const float w = l != 0.0f ? exp2_fast(wgt[i][row] - top) : -1.0f;  // -1: nothing to add
       wgt[i][row] = w;
       if (l != 0.0f) sum += w * l;
     }
@@ -1033,33 +1073,44 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
     for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     if (k == 0) {
       inv[row] = sum != 0.0f ? 1.0f / sum : 0.0f;
-      if (p.lse) p.lse[r0 + row] = sum != 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      if (p.lse && cols == 0) p.lse[r0 + row] = sum != 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     }
   }
   __syncthreads();
-  const int row = tid & 15, c0 = tid >> 4;
-  float4 acc[8];
+  const int row = tid & 15, c0 = tid >> 4;  // two groups of four values: c0 and c0 + 16 of the block's 32
+  float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+  const float4* part = p.part_o + static_cast<long long>(cols / 4 + c0) * kRows + row;
+  for (int i0 = 0; i0 < n; i0 += 4) {
+    float4 v[4][2];
+    float w[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = make_float4(0, 0, 0, 0);
-  for (int i = 0; i < n; ++i) {
-    const float w = wgt[i][row];
-    if (w == -1.0f) continue;
-    const int slot = slots[i] / kRows, at = slots[i] % kRows + row;
-    const float4* src = p.part_o + static_cast<long long>(slot) * 2 * 64 * kRows + at;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float4 v = src[(c0 + 16 * j) * kRows];
-      acc[j].x += w * v.x, acc[j].y += w * v.y, acc[j].z += w * v.z, acc[j].w += w * v.w;
+    for (int u = 0; u < 4; ++u) {
+      w[u] = i0 + u < n ? wgt[i0 + u][row] : -1.0f;
+      if (w[u] != -1.0f) {
+        const int slot = slots[i0 + u] / kRows, at = slots[i0 + u] % kRows;
+        const float4* src = part + static_cast<long long>(slot) * 2 * 64 * kRows + at;
+        v[u][0] = src[0];
+        v[u][1] = src[16 * kRows];
+      }
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (w[u] != -1.0f) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[j].x += w[u] * v[u][j].x, acc[j].y += w[u] * v[u][j].y, acc[j].z += w[u] * v[u][j].z, acc[j].w += w[u] * v[u][j].w;
+      }
   }
   const float f = inv[row];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < 2; ++j)
     *reinterpret_cast<uint2*>(&o[row][4 * (c0 + 16 * j)]) =
         make_uint2(pack2(acc[j].x * f, acc[j].y * f, false), pack2(acc[j].z * f, acc[j].w * f, false));
   __syncthreads();
-  for (int i = tid; i < kMergeRows * kDv / 8; i += kMergeThreads)
-    reinterpret_cast<uint4*>(p.out + static_cast<long long>(r0) * kDv)[i] = reinterpret_cast<const uint4*>(&o[0][0])[i];
+  {
+    const int r = tid >> 4, j = tid & 15;
+    *reinterpret_cast<uint4*>(p.out + static_cast<long long>(r0 + r) * kDv + cols + 8 * j) = *reinterpret_cast<const uint4*>(&o[r][8 * j]);
+  }
 }
 
 template <int FMT>
@@ -1072,8 +1123,16 @@ int launch(const CUtensorMap& map, const CUtensorMap& rope, const PrefixParams& 
   if (!set_smem<FMT>()) return SMLA_ERR_CUDA;
   prefix_kernel<FMT><<<2 * p.pairs, kThreadsOf<FMT>, kSmemBytes, st>>>(map, rope, p);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
-  merge_kernel<<<p.n_rows / kMergeRows, kMergeThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+  // set up while the pieces are computed; it waits for them itself
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.n_rows / kMergeRows, kDv / kMergeCols);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cfg.attrs = &at, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_kernel, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
 template <int FMT>
@@ -1111,6 +1170,7 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Row blocks and segments; false: more than 32-bit counts hold.
 bool plan(PrefixParams& p) {
+  if (p.n_seqs == 1) p.shared_len = 0;  // its table is row 0: one segment per row block instead of two
   const int64_t rows = static_cast<int64_t>(p.n_seqs) * p.q_per_seq << p.hshift;
   const int64_t rb_s = ((static_cast<int64_t>(p.q_per_seq) << p.hshift) + kRows - 1) / kRows;
   const int64_t n_rb = p.shared_len > 0 ? (rows + kRows - 1) / kRows : 0;
@@ -1128,8 +1188,10 @@ bool plan(PrefixParams& p) {
 size_t layout(PrefixParams& p, uint8_t* ws) {
   const size_t slots = static_cast<size_t>(p.n_seg) + p.pairs;
   size_t at = kStatusBytes;
+  p.bounds = reinterpret_cast<long long*>(ws + at);
+  at += up256((static_cast<size_t>(p.pairs) + 1) * 8);
   p.seg_off = reinterpret_cast<long long*>(ws + at);
-  at += up256((static_cast<size_t>(p.n_seg - p.n_rb) + 1) * 8);
+  at += up256(static_cast<size_t>(p.n_seg - p.n_rb) * 8);
   p.part_m = reinterpret_cast<float*>(ws + at);
   at += slots * kRows * 4;
   p.part_l = reinterpret_cast<float*>(ws + at);
