@@ -117,7 +117,7 @@ struct Piece {
   int s, t0, t1;  // tiles [t0, t1) of segment s
 };
 
-__device__ __noinline__ bool next_piece(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
+__device__ __noinline__ bool next_piece_call(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
   while (L.s < p.n_seg && L.a < L.y) {
     const int tiles = seg_tiles(p, L.s), cost = seg_cost(tiles);
     const int s = L.s++;
@@ -134,6 +134,16 @@ __device__ __noinline__ bool next_piece(const PrefixParams& p, Line& L, Piece& p
     }
   }
   return false;
+}
+
+// Through copies, so that the caller's own stay in registers.
+__device__ __forceinline__ bool next_piece(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
+  Line line = L;
+  Piece piece;
+  const bool more = next_piece_call(p, line, piece, writer);
+  L = line;
+  if (more) pc = piece;
+  return more;
 }
 
 // The tiles of a pair's pieces one after another, with the tile's page ids.
@@ -153,7 +163,7 @@ struct Tiles {
   __device__ __forceinline__ bool bad(const PrefixParams& p) const {
     return (own_id != kNoPage && pool_page(p, own_id) < 0) || (other_id != kNoPage && pool_page(p, other_id) < 0);
   }
-  __device__ __noinline__ bool next_segment(const PrefixParams& p) {
+  __device__ __forceinline__ bool next_segment(const PrefixParams& p) {
     if (!next_piece(p, line, pc, false)) return false;
     t = pc.t0;
     if (pc.s < p.n_rb) {
@@ -248,14 +258,15 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, vol
   const uint32_t a = smem_u32(bar);
   return try_bar<true>(a, parity) || wait_long<true>(a, parity, abort, status);
 }
-// Bounded wait without a call, for the MMA role (a call takes its descriptors out of
-// the uniform registers). It polls and never suspends: a try_wait with a time
-// hint took some 300 cycles even on a phase that was complete, seven times a
-// tile. About four seconds of polls at most.
+// Bounded wait of the MMA warp, warp-uniform and without a call (a call takes the
+// descriptors out of the uniform registers). It polls about 2^26 times at most
+// (a second or so). Measured between batches of MMAs on a phase that is complete:
+// 67 cycles; 163 with the loop left by each lane for itself, 300 with a try_wait
+// that has a time hint, and there are six such waits in a tile's 2,400 cycles.
 template <bool kCluster>
-__device__ __forceinline__ bool wait_poll(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait_poll(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
-  for (uint32_t it = 0; it < (1u << 28); ++it) {
+  auto done = [&] {
     uint32_t ok;
     if (kCluster)
       asm volatile(
@@ -273,11 +284,11 @@ __device__ __forceinline__ bool wait_poll(uint64_t* bar, uint32_t parity, volati
           : "=r"(ok)
           : "r"(a), "r"(parity)
           : "memory");
-    if (ok) return true;
-    if ((it & 63u) == 63u && *abort) return false;
-  }
-  *abort = 2;  // reported as a timeout by the end of the kernel
-  return false;
+    return __all_sync(0xFFFFFFFFu, ok != 0) != 0;
+  };
+  bool ok = done();
+  for (uint32_t it = 0; !ok && it < (1u << 26); ++it) ok = done();
+  return ok;
 }
 // true in one thread of the (converged) warp
 __device__ __forceinline__ bool elect_one() {
@@ -346,7 +357,7 @@ struct Meta {
   float mx[2][kRows];         // the other CTA's row maxima
   float ks[4][2][64];         // per softmax warp: scales of the own page (per-token FP8)
   uint64_t q_full, ko_full, kv_full[2], vo_full, ko_free, kv_free[2], vo_free;
-  uint64_t s_full, s_free, p_own, p_other, pv_done, o_free;
+  uint64_t s_full, s_free, p_own, pv_done, o_free;
   uint64_t mx_full[2][4];
   long long scan[34];
   long long start_a;
@@ -415,7 +426,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     mbar_init(&M.s_full, 1);
     mbar_init(&M.s_free, 4);
     mbar_init(&M.p_own, 4);
-    mbar_init(&M.p_other, 1);
     mbar_init(&M.pv_done, 2);
     mbar_init(&M.o_free, 4);
     M.abort_flag = 0;
@@ -502,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     const uint32_t peer_mx = peer_addr(smem_u32(&M.mx[0][0]), rank ^ 1);
     const uint32_t peer_mxbar = peer_addr(smem_u32(&M.mx_full[0][0]), rank ^ 1);
     const uint32_t peer_p = peer_addr(sbase + kOffP + kQChunk, rank ^ 1);
-    const uint32_t peer_pbar = peer_addr(smem_u32(&M.p_other), rank ^ 1);
+    const uint32_t peer_pbar = peer_addr(smem_u32(&M.vo_full), rank ^ 1);
     const bool writer = rank == 0 && tid == 0;
     bool over = false;
     // Q of segment s. A warp brings its 32 rows in 16-byte pieces, eight lanes on one
@@ -707,12 +717,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           *reinterpret_cast<uint4*>(smem + kOffP + piece_off(row, j)) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        // P goes to the other CTA first: the wait below is for its P as well
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) send_bulk(peer_p + warp * 4096, sbase + kOffP + warp * 4096, 4096, peer_pbar);
         // 0 * NaN: V rows that no row of the block sees are zeroed, and rows that
         // only some see are zeroed if they hold a value that is not finite (those
         // that see it have a logit that is not finite either)
         if (tile_k < lim.lo || tile_k + 2 * kPage > lim.min_hi) {
           const bool w_ok = wait_bar(&M.kv_full[g & 1], (g >> 1) & 1, abort_v, p.status) &&
-                            wait_bar(&M.vo_full, g & 1, abort_v, p.status);
+                            wait_cluster(&M.vo_full, g & 1, abort_v, p.status);
           if (!__all_sync(0xFFFFFFFFu, w_ok)) {
             ok = false;
             break;
@@ -732,14 +746,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
           if (zero)
             for (int j = 0; j < 32; ++j)
               *reinterpret_cast<uint4*>(v + (j >> 3) * kChunk + piece_off(r, j & 7)) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          send_bulk(peer_p + warp * 4096, sbase + kOffP + warp * 4096, 4096, peer_pbar);
-          mbar_arrive(&M.p_own);
-        }
+        if (lane == 0) mbar_arrive(&M.p_own);
         __syncwarp();
       }
     }
@@ -756,7 +767,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       auto y = [](int page) { return page >= 0 ? page * kPage : -kPage; };
       auto load_vo = [&](uint32_t h, int page) {
         if (h > 0 && !wait_bar(&M.vo_free, (h - 1) & 1, abort_v, p.status)) return false;
-        mbar_arrive_expect_tx(&M.vo_full, 4 * kChunk);
+        mbar_arrive_expect_tx(&M.vo_full, 4 * kChunk + kQChunk);  // V of the other page and its P
         tma_chunks(smem + kOffVO, &kv_map, &M.vo_full, y(page), v0);
         return true;
       };
@@ -803,11 +814,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     Piece pc;
     uint32_t g = 0, n = 0;
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xFFFFFFFFu, wait_poll<false>(bar, parity, abort_v));
-    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_poll<false>(bar, parity); };
     while (ok && next_piece(p, wline, pc, false)) {
-      if (!wait(&M.q_full, n & 1)) break;
+      if (!wait(&M.q_full, n & 1)) { ok = false; break; }
       const int t0 = __shfl_sync(0xFFFFFFFFu, pc.t0, 0), t1 = __shfl_sync(0xFFFFFFFFu, pc.t1, 0);
       // step t: the logits of tile t, then the product of tile t - 1
       for (int t = t0; t <= t1; ++t) {
@@ -861,10 +870,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
               mma_f16(tm + kColO, p_desc + static_cast<uint64_t>(2 * kk), v + static_cast<uint64_t>(kk * 2048 >> 4), id_pv,
                       kk != 0 ? 1 : first ^ 1);
             mma_commit(&M.kv_free[h & 1]);
-            mbar_arrive_expect_tx(&M.p_other, kQChunk);
           }
           __syncwarp();
-          if (!__all_sync(0xFFFFFFFFu, wait_poll<true>(&M.p_other, h & 1, abort_v)) || !wait(&M.vo_full, h & 1)) { ok = false; break; }
+          if (!wait_poll<true>(&M.vo_full, h & 1)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -878,6 +886,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       }
       ++n;
     }
+    if (!ok) *abort_v = 2;
   } else if (FMT != kBf16) {
     // -------------------------------------------------------------- FP8 rows: load, widen, store
     // Thread u takes 16 codes of row u / 4 in every chunk. Codes are exact in
@@ -947,7 +956,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     auto filled = [&](uint64_t* bar) {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
+      if (lane == 0) {
+        if (bar == &M.vo_full && warp == 6) mbar_arrive_expect_tx(bar, kQChunk);  // and the other page's P
+        else mbar_arrive(bar);
+      }
     };
     auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, abort_v, p.status)); };
     Tiles cur;
