@@ -157,9 +157,12 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
  *   out         [n_seqs * q_per_seq][n_heads][512] bf16.
  *   lse         [n_seqs * q_per_seq][n_heads] fp32 natural log, or NULL. A row
  *               that sees no key gets out = 0 and lse = -inf.
- * Keys of a page outside the pool are skipped and reported. The MMAs run on
- * bf16 operands with fp32 accumulators: q and BF16 rows enter as they are, FP8
- * rows (code * scale) and the probabilities are rounded to bf16.
+ * Keys of a page outside the pool are skipped and reported. The latent cache is
+ * device memory. The MMAs accumulate in fp32. BF16 rows: bf16 operands (q and the
+ * rows as they are, the probabilities rounded to bf16). FP8 rows: f16 operands
+ * (per-token codes are exact, tile-scaled values and the probabilities are
+ * rounded to f16), so |q| and tile-scaled values must stay below 65504; beyond it
+ * smla_read_status gives SMLA_ERR_UNSUPPORTED, as for smla_sparse_mla_fwd.
  * Keys that a row does not see never reach it, whatever they hold (an unused
  * slot of a page may hold NaN).
  * Supported: n_heads 16 and 64; any q_per_seq >= 1; the three cache formats.

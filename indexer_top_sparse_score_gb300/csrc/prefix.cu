@@ -24,8 +24,9 @@
 //   KO  own page, the 5 chunks that only QK reads     (1 tile)
 //   KV  own page, the 4 chunks of this CTA's output   (2 tiles)
 //   VO  other page, the 4 chunks of this CTA's output (1 tile)
-// Warp roles: 0-3 softmax (a thread per row) and results, 4 TMA loads of BF16
-// rows, 5 MMA issue, 6-13 (FP8 caches) load and widen the rows instead of TMA.
+// Warp roles: 0-7 softmax and results (a thread per row and half of the page's
+// keys), 8 TMA loads of BF16 rows, 9 MMA issue, 10-15 (FP8 caches) load and widen
+// the rows instead of TMA, two warps for each of KO, KV and VO.
 // The issue order QK(t + 1), PV(t) keeps the tensor pipe busy during softmax(t).
 //
 // The work is cut evenly: segment after segment on one line (a tile costs 1, a
@@ -61,7 +62,8 @@ constexpr float kRaise = 8.0f;   // log2: the reference maximum is raised only w
 constexpr int kMaxPairs = 128;
 constexpr int kMaxPieces = kMaxPairs + 2;  // of a row: its two segments are walked by distinct pairs, but for one at each border
 constexpr int kTileRowBytes = 656, kTileRope = 528;
-constexpr int kConvWarps = 8;
+constexpr int kSoftWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kConvWarp0 = 10;
+constexpr int kPHalf = kRows * 64;  // P of half a page: 128 rows x 32 keys, 64-byte swizzled
 
 enum { kBf16 = 0, kTokenFp8 = 1, kTileFp8 = 2 };
 
@@ -74,7 +76,8 @@ struct PrefixParams {
   const int32_t* seq_lens;
   int32_t max_seq_len, shared_len, q_per_seq, hshift;  // heads = 1 << hshift
   const uint16_t* q;
-  float scale_log2;
+  float scale_log2;   // |sm_scale| log2 e, not 0
+  uint32_t q_sign;    // flips the sign of Q where sm_scale is negative
   uint16_t* out;
   float* lse;
   uint32_t* status;
@@ -85,7 +88,7 @@ struct PrefixParams {
   long long* seg_off; // [i] where own segment i starts on the line
   long long* bounds;  // [pairs + 1] where each pair's stretch starts
   float* part_m;      // [slot][128]
-  float* part_l;      // [slot][2][128]
+  float* part_l;      // [slot][4][128]: sums of each CTA's two halves
   float4* part_o;     // [slot][2][64][128]: four output values of a row
 };
 
@@ -117,7 +120,7 @@ struct Piece {
   int s, t0, t1;  // tiles [t0, t1) of segment s
 };
 
-__device__ __noinline__ bool next_piece_call(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
+__device__ __forceinline__ bool piece_after(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
   while (L.s < p.n_seg && L.a < L.y) {
     const int tiles = seg_tiles(p, L.s), cost = seg_cost(tiles);
     const int s = L.s++;
@@ -140,7 +143,7 @@ __device__ __noinline__ bool next_piece_call(const PrefixParams& p, Line& L, Pie
 __device__ __forceinline__ bool next_piece(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
   Line line = L;
   Piece piece;
-  const bool more = next_piece_call(p, line, piece, writer);
+  const bool more = piece_after(p, line, piece, writer);
   L = line;
   if (more) pc = piece;
   return more;
@@ -211,9 +214,9 @@ __device__ __forceinline__ void send_bulk(uint32_t dst, uint32_t src, uint32_t b
                "r"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-// Bounded waits. The first try is inline, the rest a call: the kernel's loops have
-// to stay small (114 KB of code ran at 5,800 cycles a tile, most of it waiting for
-// instructions). kCluster: also acquires what the other CTA sent.
+// Bounded waits without calls: across a call the tile loops' values would go to local
+// memory, and next to 225 KB of shared memory there is hardly any L1 to hold it.
+// kCluster: also acquires what the other CTA sent.
 template <bool kCluster>
 __device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -235,28 +238,36 @@ __device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
         : "memory");
   return ok != 0;
 }
+// Gives up after kWaitLimitCycles, or when another role has: false, and *abort is
+// raised (the end of the kernel reports it). One thread.
 template <bool kCluster>
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
-  const long long t0 = clock64();
-  for (uint32_t it = 1;; ++it) {
-    if (try_bar<kCluster>(bar, parity)) return true;
-    if ((it & 15u) == 0) {
-      if (*abort) return false;
-      if (clock64() - t0 > kWaitLimitCycles) {
-        set_status(status, kStatusTimeout);
-        *abort = 1;
-        return false;
-      }
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  long long t0 = 0;
+  for (uint32_t it = 1; !try_bar<kCluster>(a, parity); ++it) {
+    if ((it & 255u) != 0) continue;
+    if (t0 == 0) t0 = clock64();
+    if (*abort || clock64() - t0 > kWaitLimitCycles) {
+      *abort = 2;
+      return false;
     }
   }
+  return true;
 }
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+// The same by a whole warp: every lane sees the phase, all leave together.
+template <bool kCluster>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const uint32_t a = smem_u32(bar);
-  return try_bar<false>(a, parity) || wait_long<false>(a, parity, abort, status);
-}
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
-  const uint32_t a = smem_u32(bar);
-  return try_bar<true>(a, parity) || wait_long<true>(a, parity, abort, status);
+  long long t0 = 0;
+  for (uint32_t it = 1; !__all_sync(0xFFFFFFFFu, try_bar<kCluster>(a, parity)); ++it) {
+    if ((it & 255u) != 0) continue;
+    if (t0 == 0) t0 = clock64();
+    if (__any_sync(0xFFFFFFFFu, *abort != 0 || clock64() - t0 > kWaitLimitCycles)) {
+      *abort = 2;
+      return false;
+    }
+  }
+  return true;
 }
 // Bounded wait of the MMA warp, warp-uniform and without a call (a call takes the
 // descriptors out of the uniform registers). It polls about 2^26 times at most
@@ -289,6 +300,12 @@ __device__ __forceinline__ bool wait_poll(uint64_t* bar, uint32_t parity) {
   bool ok = done();
   for (uint32_t it = 0; !ok && it < (1u << 26); ++it) ok = done();
   return ok;
+}
+// the same box into L2 only
+__device__ __forceinline__ void prefetch_chunks(const CUtensorMap* map, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(0), "r"(y), "r"(z)
+               : "memory");
 }
 // true in one thread of the (converged) warp
 __device__ __forceinline__ bool elect_one() {
@@ -326,6 +343,28 @@ __device__ __forceinline__ float exp2_fast(float x) {  // relative error about 2
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// packed fp32: two independent IEEE operations an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
   if (f16) {
     const __half2 v = __floats2half2_rn(a, b);
@@ -336,13 +375,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-// four e4m3 codes -> four floats
-__device__ __forceinline__ void e4m3x4(uint32_t c, float* f) {
-  uint32_t lo, hi;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(c)));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(c >> 16)));
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+// two e4m3 codes -> two f16 values, exactly
+__device__ __forceinline__ uint32_t e4m3x2(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
 }
 __device__ __forceinline__ uint32_t piece_off(int row, int j) {  // 16-byte piece j of a 128-byte swizzled row
   return static_cast<uint32_t>(row * 128 + ((j ^ (row & 7)) << 4));
@@ -354,8 +391,9 @@ __device__ __forceinline__ uint32_t to_f16(uint32_t w, bool& over) {
 }
 
 struct Meta {
-  float mx[2][kRows];         // the other CTA's row maxima
-  float ks[4][2][64];         // per softmax warp: scales of the own page (per-token FP8)
+  float mx[2][4][kRows];      // row maxima of this CTA's two halves and of the other's
+  float4 ks[kSoftWarps][16];  // per softmax warp and two of its keys: scale * sm_scale * log2 e of both, log2 scale of both (per-token FP8)
+  float rs[kSoftWarps][32];   // and 1 / scale
   uint64_t q_full, ko_full, kv_full[2], vo_full, ko_free, kv_free[2], vo_free;
   uint64_t s_full, s_free, p_own, pv_done, o_free;
   uint64_t mx_full[2][4];
@@ -373,7 +411,7 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 struct Limits {
   int lo, hi, min_hi, max_hi;
 };
-__device__ __noinline__ Limits limits(const PrefixParams& p, int s, int row) {
+__device__ __forceinline__ Limits limits(const PrefixParams& p, int s, int row) {
   Limits m;
   m.hi = 0, m.min_hi = INT_MAX, m.max_hi = 0;
   const bool shared = s < p.n_rb;
@@ -395,16 +433,81 @@ __device__ __noinline__ Limits limits(const PrefixParams& p, int s, int row) {
   return m;
 }
 
+// Q of segment s, by one softmax warp: chunks of its 32 rows in 16-byte pieces,
+// eight lanes on one row's chunk (128 contiguous bytes), a chunk in flight (more
+// push the tile loops' values into local memory, and next to 225 KB of shared
+// memory there is hardly any L1 to hold that). The six for tensor memory pass one by
+// one through a chunk's place in shared memory, from where every lane reads its own
+// row; the other three are stored where they stay. (The logits of the previous piece
+// are complete: all of it is free.) Returns whether a value was outside f16's range.
 template <int FMT>
-constexpr int kThreadsOf = FMT == kBf16 ? 192 : 192 + 32 * kConvWarps;
+__device__ __forceinline__ bool load_q(const PrefixParams& p, int s, uint8_t* q_smem, uint32_t q_tmem, int rank, int quad, int half) {
+  constexpr bool F16 = FMT != kBf16;
+  const int lane = threadIdx.x & 31;
+  const bool shared = s < p.n_rb;
+  const int i = s - p.n_rb, b = shared ? 0 : i / p.rb_s;
+  const int first = (shared ? s : i - b * p.rb_s) * kRows + quad * 32;
+  const int limit = (shared ? p.n_rows : p.q_per_seq << p.hshift) - first;  // rows of the warp that exist
+  const uint16_t* src = p.q + ((static_cast<long long>(b) * p.q_per_seq << p.hshift) + first) * kDqk;
+  const int sub = lane >> 3, pcs = lane & 7;
+  bool over = false;
+  auto bring = [&](int c, int j) {  // piece pcs of row 4 j + sub of the chunk at place c
+    const int chunk = c < 4 ? 4 * (rank ^ 1) + c : c < 6 ? 4 * rank + c - 4 : c == 6 ? 8 : 4 * rank + c - 5;
+    const int r = 4 * j + sub;
+    return r < limit ? __ldg(reinterpret_cast<const uint4*>(src + r * kDqk + chunk * 64 + pcs * 8)) : make_uint4(0, 0, 0, 0);
+  };
+  auto put = [&](int place, int j, uint4 w) {
+    if (F16) w = make_uint4(to_f16(w.x, over), to_f16(w.y, over), to_f16(w.z, over), to_f16(w.w, over));
+    w.x ^= p.q_sign, w.y ^= p.q_sign, w.z ^= p.q_sign, w.w ^= p.q_sign;
+    *reinterpret_cast<uint4*>(q_smem + place * kQChunk + piece_off(quad * 32 + 4 * j + sub, pcs)) = w;
+  };
+  uint4 v[8];
+#pragma unroll 1
+  for (int c = 3 * half; c < 3 * half + 3; ++c) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = bring(c, j);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) put(half, j, v[j]);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const uint4*>(q_smem + half * kQChunk + piece_off(quad * 32 + lane, j));
+    tmem_st_32x32b_x32(q_tmem + 32 * c, reinterpret_cast<const uint32_t*>(v));
+    __syncwarp();
+  }
+  // the chunks of places 6 and 7, one a half, and half of the rows of place 8 each
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = bring(6 + half, j);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) put(half, j, v[j]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = bring(8, 4 * half + j);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) put(2, 4 * half + j, v[j]);
+  tmem_wait_st();
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncwarp();
+  return over;
+}
+// the rows of a later segment's Q into L2
+__device__ __forceinline__ void prefetch_q(const PrefixParams& p, int s, int row) {
+  const bool shared = s < p.n_rb;
+  const int i = s - p.n_rb, b = shared ? 0 : i / p.rb_s;
+  const int r = (shared ? s : i - b * p.rb_s) * kRows + row;
+  if (r < (shared ? p.n_rows : p.q_per_seq << p.hshift))
+    prefetch_l2_lines(p.q + ((static_cast<long long>(b) * p.q_per_seq << p.hshift) + r) * kDqk, 2 * kDqk);
+}
+
+template <int FMT>
+constexpr int kThreadsOf = FMT == kBf16 ? 320 : 512;
 
 template <int FMT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map, const PrefixParams p) {
-  constexpr bool F16 = FMT == kTileFp8;  // operand type of the MMAs
+  constexpr bool F16 = FMT != kBf16;  // operand type of the MMAs: one cvt takes two e4m3 codes to f16, exactly
   constexpr uint32_t kFmt = F16 ? kFmtF16 : kFmtBF16;
   constexpr int kThreads = kThreadsOf<FMT>;
-  constexpr uint32_t kFills = FMT == kBf16 ? 1 : kConvWarps;  // arrivals that fill a slot group
+  constexpr uint32_t kFills = FMT == kBf16 ? 1 : 2;  // arrivals that fill a slot group
   extern __shared__ __align__(1024) uint8_t smem[];
   Meta& M = *reinterpret_cast<Meta*>(smem + kOffMeta);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -413,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
   const bool aligned = (smem_u32(smem) & 1023u) == 0;
 
   if (tid == 0) {
-    mbar_init(&M.q_full, 4);
+    mbar_init(&M.q_full, kSoftWarps);
     mbar_init(&M.ko_full, kFills);
     mbar_init(&M.vo_full, kFills);
     mbar_init(&M.ko_free, 1);
@@ -424,17 +527,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       for (int w = 0; w < 4; ++w) mbar_init(&M.mx_full[i][w], 1);
     }
     mbar_init(&M.s_full, 1);
-    mbar_init(&M.s_free, 4);
-    mbar_init(&M.p_own, 4);
+    mbar_init(&M.s_free, kSoftWarps);
+    mbar_init(&M.p_own, kSoftWarps);
     mbar_init(&M.pv_done, 2);
-    mbar_init(&M.o_free, 4);
+    mbar_init(&M.o_free, kSoftWarps);
     M.abort_flag = 0;
     M.start_s = p.n_seg;
     M.start_a = 0;
     fence_mbar_init();
     if (!aligned) set_status(p.status, kStatusSetup);
   }
-  if (warp == 4) {
+  if (warp == kTmaWarp) {
     tmem_alloc(&M.tmem_slot, 512);
     tmem_relinquish();
   }
@@ -505,81 +608,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
   const uint32_t sbase = smem_u32(smem);
   volatile int* abort_v = &M.abort_flag;
 
-  if (warp < 4) {
+  if (warp < kSoftWarps) {
     // -------------------------------------------------------------- softmax, results
-    const int row = tid;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t peer_mx = peer_addr(smem_u32(&M.mx[0][0]), rank ^ 1);
-    const uint32_t peer_mxbar = peer_addr(smem_u32(&M.mx_full[0][0]), rank ^ 1);
-    const uint32_t peer_p = peer_addr(sbase + kOffP + kQChunk, rank ^ 1);
+    const int quad = warp & 3, half = warp >> 2;
+    const int row = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t mx0 = smem_u32(&M.mx[0][0][0]), mxbar0 = smem_u32(&M.mx_full[0][0]);
+    const uint32_t self_mx = peer_addr(mx0, rank), self_mxbar = peer_addr(mxbar0, rank);
+    const uint32_t peer_mx = peer_addr(mx0, rank ^ 1), peer_mxbar = peer_addr(mxbar0, rank ^ 1);
+    const uint32_t p_at = kOffP + half * kPHalf + quad * 2048;  // the warp's 32 rows of its half
+    const uint32_t peer_p = peer_addr(sbase + kQChunk + p_at, rank ^ 1);
     const uint32_t peer_pbar = peer_addr(smem_u32(&M.vo_full), rank ^ 1);
     const bool writer = rank == 0 && tid == 0;
     bool over = false;
-    // Q of segment s. A warp brings its 32 rows in 16-byte pieces, eight lanes on one
-    // row's chunk (128 contiguous bytes), kBatch chunks in flight. The three chunks
-    // that stay in shared memory are stored where they belong; the six for tensor
-    // memory pass through those places, from where every lane reads its own row.
-    // (The logits of the previous piece are complete, so both are free.)
-    auto load_q = [&](int s) {
-      constexpr int kBatch = FMT == kBf16 ? 3 : 1;
-      const bool shared = s < p.n_rb;
-      const int i = s - p.n_rb, b = shared ? 0 : i / p.rb_s;
-      const int first = (shared ? s : i - b * p.rb_s) * kRows + warp * 32;
-      const int limit = (shared ? p.n_rows : p.q_per_seq << p.hshift) - first;  // rows of the warp that exist
-      const uint16_t* src = p.q + ((static_cast<long long>(b) * p.q_per_seq << p.hshift) + first) * kDqk;
-      const int sub = lane >> 3, pcs = lane & 7;
-#pragma unroll 1
-      for (int c0 = 0; c0 < kDqk / 64; c0 += kBatch) {
-        uint4 v[kBatch][8];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int c = c0 + u;
-          const int chunk = c < 4 ? 4 * (rank ^ 1) + c : c < 6 ? 4 * rank + c - 4 : c == 6 ? 8 : 4 * rank + c - 5;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int r = 4 * j + sub;
-            v[u][j] = r < limit ? __ldg(reinterpret_cast<const uint4*>(src + r * kDqk + chunk * 64 + pcs * 8)) : make_uint4(0, 0, 0, 0);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int c = c0 + u;
-          uint8_t* at = smem + kOffQ + (c % 3) * kQChunk;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint4 w = v[u][j];
-            if (F16) w = make_uint4(to_f16(w.x, over), to_f16(w.y, over), to_f16(w.z, over), to_f16(w.w, over));
-            *reinterpret_cast<uint4*>(at + piece_off(warp * 32 + 4 * j + sub, pcs)) = w;
-          }
-        }
-        if (c0 < kQTmemChunks) {
-          __syncwarp();
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            const int c = c0 + u;
-            uint4 w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint4*>(smem + kOffQ + (c % 3) * kQChunk + piece_off(row, j));
-            tmem_st_32x32b_x32(tmem + lanes + kColQ + 32 * c, reinterpret_cast<const uint32_t*>(w));
-          }
-          __syncwarp();
-        }
-      }
-      tmem_wait_st();
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&M.q_full);
-    };
-    // the rows of a later segment's Q into L2
-    auto prefetch_q = [&](int s) {
-      const bool shared = s < p.n_rb;
-      const int i = s - p.n_rb, b = shared ? 0 : i / p.rb_s;
-      const int r = (shared ? s : i - b * p.rb_s) * kRows + row;
-      if (r < (shared ? p.n_rows : p.q_per_seq << p.hshift))
-        prefetch_l2_lines(p.q + ((static_cast<long long>(b) * p.q_per_seq << p.hshift) + r) * kDqk, 2 * kDqk);
-    };
-
     Line wline = line;
     Piece pc, nx;
     nx.s = 0;
@@ -589,22 +630,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     Tiles cur;
     cur.line = line;
     bool more = cur.next(p, rank, true);
+    auto load_scale = [&] {  // scale of key 32 half + lane of the current tile's own page
+      const int own = Tiles::pool_page(p, cur.own_id);
+      return own >= 0 ? __ldg(p.kv_scale + static_cast<long long>(own) * kPage + half * 32 + lane) : 0.0f;
+    };
+    // the tile that is worked on is one behind `cur`, whose page ids have arrived by the time they are used
+    float scale = 0.0f;
+    if (FMT == kTokenFp8 && more) scale = load_scale();
+    int own_next = more ? Tiles::pool_page(p, cur.own_id) : -1;
+    if (more) more = cur.next(p, rank, false);
     uint32_t g = 0;
     bool ok = true;
     Limits lim;
     float m = 0.0f, l = 0.0f;
     while (ok) {
       // the next piece's Q while the last product of this one runs, then this one's results
-      if (have) load_q(nx.s);
+      if (have) {
+        over |= load_q<FMT>(p, nx.s, smem + kOffQ, tmem + lanes + kColQ, rank, quad, half);
+        if (lane == 0) mbar_arrive(&M.q_full);
+      }
       if (started) {
-        if (!__all_sync(0xFFFFFFFFu, wait_cluster(&M.pv_done, (g - 1) & 1, abort_v, p.status))) break;
+        if (!wait_warp<true>(&M.pv_done, (g - 1) & 1, abort_v)) break;
         tc_fence_after();
         const int slot = pc.s + pair;
-        float4* o = p.part_o + (static_cast<long long>(slot) * 2 + rank) * 64 * kRows + row;
+        float4* o = p.part_o + ((static_cast<long long>(slot) * 2 + rank) * 64 + half * 32) * kRows + row;
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < 4; ++c) {
           float v[32];
-          tmem_ld_32x32b_x32(tmem + lanes + kColO + 32 * c, reinterpret_cast<uint32_t*>(v));
+          tmem_ld_32x32b_x32(tmem + lanes + kColO + 128 * half + 32 * c, reinterpret_cast<uint32_t*>(v));
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 8; ++j) o[(8 * c + j) * kRows] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
@@ -614,63 +667,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         if (lane == 0) mbar_arrive(&M.o_free);
         // a row that sees none of the segment's keys took part in the unmasked tiles: dropped here
         if (lim.hi <= lim.lo) l = 0.0f;
-        if (rank == 0) p.part_m[static_cast<long long>(slot) * kRows + row] = m;
-        p.part_l[(static_cast<long long>(slot) * 2 + rank) * kRows + row] = l;
+        if (rank == 0 && half == 0) p.part_m[static_cast<long long>(slot) * kRows + row] = m;
+        p.part_l[(static_cast<long long>(slot) * 4 + 2 * rank + half) * kRows + row] = l;
       }
       if (!have) break;
       started = true;
       pc = nx;
       lim = next_lim;
+      const int first_page = pc.s < p.n_rb ? 0 : p.shared_len / kPage;
       m = -INFINITY, l = 0.0f;
       have = next_piece(p, wline, nx, writer);
       if (have) {
-        prefetch_q(nx.s);
+        if (half == 0) prefetch_q(p, nx.s, row);
         next_lim = limits(p, nx.s, row);
       }
       for (int t = pc.t0; t < pc.t1; ++t, ++g) {
-        const int tile_k = (cur.first_page + 2 * t) * kPage, key0 = tile_k + rank * kPage;
-        const int own = Tiles::pool_page(p, cur.own_id);
-        const float* ks = M.ks[warp][g & 1];
-        if (FMT == kTokenFp8) {  // scales of the own page, a copy per warp
-          const float2 sc = own >= 0 ? __ldg(reinterpret_cast<const float2*>(p.kv_scale + static_cast<long long>(own) * kPage) + lane)
-                                     : make_float2(0.0f, 0.0f);
-          *reinterpret_cast<float2*>(&M.ks[warp][g & 1][2 * lane]) = sc;
+        const int tile_k = (first_page + 2 * t) * kPage, key0 = tile_k + rank * kPage + half * 32;
+        const int own = own_next;
+        const float4* ks = M.ks[warp];
+        const float2* rs = reinterpret_cast<const float2*>(M.rs[warp]);
+        if (FMT == kTokenFp8) {
+          // Per-token scales: out = sum_j 2^(x_j) s_j code_j with x_j the logit. The
+          // scale goes into the exponent, y_j = x_j + log2 s_j, so that the
+          // probability P_j = 2^(y_j - m) that meets the codes is at most 2^kRaise
+          // whatever the scales are (f16), and l = sum_j P_j / s_j. Scales below
+          // 1e-30 count as that. A warp's 32 keys, loaded a tile ahead. (Keys that no
+          // row of the block sees count as 1; a NaN scale reaches those that see it
+          // through the logit.)
+          const int key = key0 + lane;
+          float sc = scale < 1e-30f ? 1e-30f : scale;
+          if (key < lim.lo || key >= lim.max_hi) sc = 1.0f;
           __syncwarp();
+          float* k = &M.ks[warp][lane >> 1].x + (lane & 1);
+          k[0] = sc * p.scale_log2;
+          k[2] = log2f(sc);
+          M.rs[warp][lane] = sc == sc ? 1.0f / sc : 1.0f;
+          __syncwarp();
+          if (more) scale = load_scale();
         }
+        own_next = more ? Tiles::pool_page(p, cur.own_id) : -1;
         if (more) more = cur.next(p, rank, false);
-        if (!__all_sync(0xFFFFFFFFu, wait_bar(&M.s_full, g & 1, abort_v, p.status))) {
+        if (!wait_warp<false>(&M.s_full, g & 1, abort_v)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        float x[64];
-        tmem_ld_32x32b_x32(tmem + lanes + kColS, reinterpret_cast<uint32_t*>(x));
-        tmem_ld_32x32b_x32(tmem + lanes + kColS + 32, reinterpret_cast<uint32_t*>(x) + 32);
+        float x[32];
+        tmem_ld_32x32b_x32(tmem + lanes + kColS + 32 * half, reinterpret_cast<uint32_t*>(x));
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&M.s_free);
-        const bool edge = own < 0 || key0 < lim.lo || key0 + kPage > lim.min_hi;
+        const bool edge = own < 0 || key0 < lim.lo || key0 + 32 > lim.min_hi;
+        if (FMT == kTokenFp8) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) x[i] *= FMT == kTokenFp8 ? ks[i] * p.scale_log2 : p.scale_log2;
+          for (int i = 0; i < 32; i += 2) {
+            const float4 k = ks[i >> 1];
+            const float2 y = fma2(make_float2(x[i], x[i + 1]), make_float2(k.x, k.y), make_float2(k.z, k.w));
+            x[i] = y.x, x[i + 1] = y.y;
+          }
+        }
         if (edge) {
           const int hi = own < 0 ? 0 : lim.hi;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) x[i] = key0 + i >= lim.lo && key0 + i < hi ? x[i] : -INFINITY;
+          for (int i = 0; i < 32; ++i) x[i] = key0 + i >= lim.lo && key0 + i < hi ? x[i] : -INFINITY;
         }
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mine = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], x[i]);
-        const float mine = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        // the row's maximum over the other CTA's page: both CTAs scale P and O by the same reference
-        const uint32_t par = g & 1;
-        send_float(peer_mx + (par * kRows + row) * 4, mine, peer_mxbar + (par * 4 + warp) * 8);
-        if (lane == 0) mbar_arrive_expect_tx(&M.mx_full[par][warp], 32 * 4);
-        if (!__all_sync(0xFFFFFFFFu, wait_cluster(&M.mx_full[par][warp], (g >> 1) & 1, abort_v, p.status))) {
+        for (int i = 0; i < 32; i += 2) mine = max3(mine, x[i], x[i + 1]);
+        if (FMT != kTokenFp8) mine *= p.scale_log2;
+        // the row's maximum over both halves of both pages, which all scale P by the
+        // same reference: every warp sends its rows' to both CTAs
+        const uint32_t par = g & 1, bar = (par * 4 + quad) * 8;
+        send_float(self_mx + ((par * 4 + half) * kRows + row) * 4, mine, self_mxbar + bar);
+        send_float(peer_mx + ((par * 4 + 2 + half) * kRows + row) * 4, mine, peer_mxbar + bar);
+        if (half == 0 && lane == 0) mbar_arrive_expect_tx(&M.mx_full[par][quad], 4 * 32 * 4);
+        if (!wait_warp<true>(&M.mx_full[par][quad], (g >> 1) & 1, abort_v)) {
           ok = false;
           break;
         }
-        const float top = fmaxf(mine, *reinterpret_cast<volatile float*>(&M.mx[par][row]));
+        const volatile float* mx = &M.mx[par][0][row];
+        const float top = fmaxf(fmaxf(mx[0], mx[kRows]), fmaxf(mx[2 * kRows], mx[3 * kRows]));
         const bool raise = top > m + kRaise || (m == -INFINITY && top > -INFINITY);
         float alpha = 1.0f;
         if (raise) {
@@ -679,72 +756,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
           l *= alpha;
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        uint32_t pk[32];
-        float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t pk[16];
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const float2 factor = make_float2(p.scale_log2, p.scale_log2), minus = make_float2(-ref, -ref);
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          float a = exp2_fast(x[i] - ref), b = exp2_fast(x[i + 1] - ref);
-          l4[(i >> 1) & 3] += a + b;
-          if (FMT == kTokenFp8) {
-            a *= ks[i], b *= ks[i + 1];
-            if (edge) {  // a masked key's scale may be anything
-              if (x[i] == -INFINITY) a = 0.0f;
-              if (x[i + 1] == -INFINITY) b = 0.0f;
-            }
-          }
-          // P is rounded to the operands' type (bf16: 2^-9 of a probability at most); the sum l is not
-          pk[i >> 1] = pack2(a, b, F16);
+        for (int i = 0; i < 32; i += 2) {
+          const float2 v = make_float2(x[i], x[i + 1]);
+          const float2 y = FMT == kTokenFp8 ? add2(v, minus) : fma2(v, factor, minus);
+          const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+          if (FMT == kTokenFp8) sum[(i >> 1) & 1] = fma2(e, rs[i >> 1], sum[(i >> 1) & 1]);
+          else sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
+          // P is rounded to the operands' type (bf16: off by at most 2^-8 of a probability,
+          // f16: 2^-11); the sum l is not
+          pk[i >> 1] = pack2(e.x, e.y, F16);
         }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         // both CTAs are done with the previous tile's P, and O holds it
-        if (g > 0 && !__all_sync(0xFFFFFFFFu, wait_cluster(&M.pv_done, (g - 1) & 1, abort_v, p.status))) {
+        if (g > 0 && !wait_warp<true>(&M.pv_done, (g - 1) & 1, abort_v)) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (t > pc.t0 && __any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < 4; ++c) {
             uint32_t o[32];
-            tmem_ld_32x32b_x32(tmem + lanes + kColO + 32 * c, o);
+            tmem_ld_32x32b_x32(tmem + lanes + kColO + 128 * half + 32 * c, o);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st_32x32b_x32(tmem + lanes + kColO + 32 * c, o);
+            tmem_st_32x32b_x32(tmem + lanes + kColO + 128 * half + 32 * c, o);
           }
           tmem_wait_st();
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(smem + kOffP + piece_off(row, j)) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        for (int j = 0; j < 4; ++j)  // 64-byte rows: piece j of row r sits at j ^ (r / 2 mod 4)
+          *reinterpret_cast<uint4*>(smem + p_at + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
         // P goes to the other CTA first: the wait below is for its P as well
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) send_bulk(peer_p + warp * 4096, sbase + kOffP + warp * 4096, 4096, peer_pbar);
+        if (lane == 0) send_bulk(peer_p, sbase + p_at, 2048, peer_pbar);
         // 0 * NaN: V rows that no row of the block sees are zeroed, and rows that
         // only some see are zeroed if they hold a value that is not finite (those
-        // that see it have a logit that is not finite either)
+        // that see it have a logit that is not finite either). Two chunks a half.
         if (tile_k < lim.lo || tile_k + 2 * kPage > lim.min_hi) {
-          const bool w_ok = wait_bar(&M.kv_full[g & 1], (g >> 1) & 1, abort_v, p.status) &&
-                            wait_cluster(&M.vo_full, g & 1, abort_v, p.status);
-          if (!__all_sync(0xFFFFFFFFu, w_ok)) {
+          if (!wait_warp<false>(&M.kv_full[g & 1], (g >> 1) & 1, abort_v) || !wait_warp<true>(&M.vo_full, g & 1, abort_v)) {
             ok = false;
             break;
           }
           const bool oth = row >= kPage;
           const int r = row & (kPage - 1), key = tile_k + (oth ? rank ^ 1 : rank) * kPage + r;
-          uint8_t* v = smem + (oth ? kOffVO : kOffKV + static_cast<int>(g & 1) * 4 * kChunk);
+          uint8_t* v = smem + (oth ? kOffVO : kOffKV + static_cast<int>(g & 1) * 4 * kChunk) + 2 * half * kChunk;
           bool zero = key < lim.lo || key >= lim.max_hi;
           if (!zero && key >= lim.min_hi) {
             constexpr uint32_t inf = F16 ? 0x7C00u : 0x7F80u;
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < 16; ++j) {
               const uint4 u = *reinterpret_cast<const uint4*>(v + (j >> 3) * kChunk + piece_off(r, j & 7));
               const uint32_t e[4] = {u.x, u.y, u.z, u.w};
               for (int k = 0; k < 4; ++k) zero |= (e[k] & inf) == inf || (e[k] & (inf << 16)) == inf << 16;
             }
           }
           if (zero)
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 16; ++j)
               *reinterpret_cast<uint4*>(v + (j >> 3) * kChunk + piece_off(r, j & 7)) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
@@ -755,7 +829,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       }
     }
     if (over) set_status(p.status, kStatusOverflow);
-  } else if (warp == 4) {
+  } else if (warp == kTmaWarp) {
     // -------------------------------------------------------------- TMA loads
     if (FMT == kBf16 && elect_one()) {
       const int v0 = 4 * rank, k0 = 4 * (rank ^ 1);  // first chunk of this CTA's output values, of the others
@@ -766,7 +840,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       // a page that is missing reads as zeros: a box wholly before the pool
       auto y = [](int page) { return page >= 0 ? page * kPage : -kPage; };
       auto load_vo = [&](uint32_t h, int page) {
-        if (h > 0 && !wait_bar(&M.vo_free, (h - 1) & 1, abort_v, p.status)) return false;
+        if (h > 0 && !wait_one<false>(&M.vo_free, (h - 1) & 1, abort_v)) return false;
         mbar_arrive_expect_tx(&M.vo_full, 4 * kChunk + kQChunk);  // V of the other page and its P
         tma_chunks(smem + kOffVO, &kv_map, &M.vo_full, y(page), v0);
         return true;
@@ -777,20 +851,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         const int own = Tiles::pool_page(p, cur.own_id), other = Tiles::pool_page(p, cur.other_id);
         if (cur.bad(p)) set_status(p.status, kStatusBounds);
         more = cur.next(p, rank, false);
-        if (g > 0 && !wait_bar(&M.ko_free, (g - 1) & 1, abort_v, p.status)) { ok = false; break; }
+        if (g > 0 && !wait_one<false>(&M.ko_free, (g - 1) & 1, abort_v)) { ok = false; break; }
         mbar_arrive_expect_tx(&M.ko_full, 5 * kChunk);
         tma_chunks(smem + kOffKO, &kv_map, &M.ko_full, y(own), k0);
         tma_chunks(smem + kOffKO + 4 * kChunk, &rope_map, &M.ko_full, y(own), 8);
         const int buf = g & 1;
-        if (g > 1 && !wait_bar(&M.kv_free[buf], ((g >> 1) - 1) & 1, abort_v, p.status)) { ok = false; break; }
+        if (g > 1 && !wait_one<false>(&M.kv_free[buf], ((g >> 1) - 1) & 1, abort_v)) { ok = false; break; }
         mbar_arrive_expect_tx(&M.kv_full[buf], 4 * kChunk);
         tma_chunks(smem + kOffKV + 4 * buf * kChunk, &kv_map, &M.kv_full[buf], y(own), v0);
+        if (more) {  // the next tile's own page into L2
+          const int next = Tiles::pool_page(p, cur.own_id);
+          if (next >= 0) {
+            prefetch_chunks(&kv_map, y(next), k0);
+            prefetch_chunks(&rope_map, y(next), 8);
+            prefetch_chunks(&kv_map, y(next), v0);
+          }
+        }
         if (g > 0) ok = load_vo(g - 1, last_other);
         last_other = other;
       }
       if (g > 0 && ok) load_vo(g - 1, last_other);
     }
-  } else if (warp == 5) {
+  } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------- MMA issue
     // tcgen05.mma takes its descriptors from uniform registers. So the loop runs
     // warp-wide on warp-uniform values, each batch of MMAs is unrolled with constant
@@ -808,8 +890,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     const uint64_t kv_desc = smem_desc(sb + kOffKV, 16, 1024);
     const uint64_t v_desc = smem_desc(sb + kOffKV, kChunk, 1024);   // the same chunks read as V: values x keys
     const uint64_t vo_desc = smem_desc(sb + kOffVO, kChunk, 1024);
-    const uint64_t p_desc = smem_desc(sb + kOffP, 16, 1024);
-    const uint64_t po_desc = smem_desc(sb + kOffP + kQChunk, 16, 1024);
+    const uint64_t p_desc = smem_desc(sb + kOffP, 16, 512, kSwizzle64B);  // 32 keys a half: two K = 16 steps each
+    const uint64_t po_desc = smem_desc(sb + kOffP + kQChunk, 16, 512, kSwizzle64B);
     Line wline = line;
     Piece pc;
     uint32_t g = 0, n = 0;
@@ -867,7 +949,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
             const uint64_t v = v_desc + static_cast<uint64_t>((h & 1) * (4 * kChunk >> 4));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f16(tm + kColO, p_desc + static_cast<uint64_t>(2 * kk), v + static_cast<uint64_t>(kk * 2048 >> 4), id_pv,
+              mma_f16(tm + kColO, p_desc + static_cast<uint64_t>((kk >> 1) * (kPHalf >> 4) + 2 * (kk & 1)), v + static_cast<uint64_t>(kk * 2048 >> 4), id_pv,
                       kk != 0 ? 1 : first ^ 1);
             mma_commit(&M.kv_free[h & 1]);
           }
@@ -877,7 +959,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f16(tm + kColO, po_desc + static_cast<uint64_t>(2 * kk), vo_desc + static_cast<uint64_t>(kk * 2048 >> 4), id_pv, 1);
+              mma_f16(tm + kColO, po_desc + static_cast<uint64_t>((kk >> 1) * (kPHalf >> 4) + 2 * (kk & 1)), vo_desc + static_cast<uint64_t>(kk * 2048 >> 4), id_pv, 1);
             mma_commit(&M.vo_free);
             commit_pair(&M.pv_done);
           }
@@ -889,114 +971,96 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     if (!ok) *abort_v = 2;
   } else if (FMT != kBf16) {
     // -------------------------------------------------------------- FP8 rows: load, widen, store
-    // Thread u takes 16 codes of row u / 4 in every chunk. Codes are exact in
-    // bf16 (per-token scales multiply the logits and P in fp32); tile-scaled
-    // values (code * scale) are rounded to f16.
-    const int u = tid - 192, r = u >> 2, pcs = u & 3;
+    // Two warps for each of KO (10, 11), KV (12, 13) and VO (14, 15). Thread u takes
+    // 16 codes of rows u / 4 + 16 i in every chunk (four lanes on a row's 64
+    // contiguous bytes); a tile's pieces are loaded while the tile before is waited
+    // for. Codes are exact in f16 (per-token scales enter the logits and P in
+    // fp32); tile-scaled values (code * scale) are rounded to f16: off by at most
+    // 2^-11 of the value.
+    const int group = (warp - kConvWarp0) >> 1;  // 0 KO, 1 KV, 2 VO
+    const int u = (tid - kConvWarp0 * 32) & 63, r0 = u >> 2, pcs = u & 3;
     constexpr int kRowBytes = FMT == kTokenFp8 ? kDqk : kTileRowBytes;
-    const int kc0 = 4 * (rank ^ 1), vc0 = 4 * rank;
+    const int c0 = group == 0 ? 4 * (rank ^ 1) : 4 * rank;
     bool over = false;
-    struct Group {
-      uint4 v[5];
-      uint4 rope;  // second half of a tile-scaled row's rope piece
-      float4 sc;
-    };
-    auto fetch = [&](Group& gr, int page, int c0, int n) {
-      const uint8_t* src = p.kv + (static_cast<long long>(max(page, 0)) * kPage + r) * kRowBytes;
+    float top = 0.0f;
+    uint4 v[5][4];   // chunks of four rows; the fifth (KO) is the rope (tile-scaled rows: loaded when it is stored)
+    const uint8_t* rope = nullptr;
+    float2 sc[4];    // scales of the two 128-value tiles that the four chunks cover
+    auto fetch = [&](int page) {
       const bool live = page >= 0;
+      const uint8_t* src = p.kv + (static_cast<long long>(max(page, 0)) * kPage + r0) * kRowBytes;
+      const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 5; ++i) {
-        if (i >= n) continue;
-        const int off = i < 4 ? (c0 + i) * 64 + pcs * 16 : FMT == kTokenFp8 ? kDv + pcs * 16 : kTileRope + pcs * 32;
-        gr.v[i] = live ? __ldg(reinterpret_cast<const uint4*>(src + off)) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* row = src + i * 16 * kRowBytes;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c][i] = live ? __ldg(reinterpret_cast<const uint4*>(row + (c0 + c) * 64 + pcs * 16)) : none;
+        if (FMT == kTileFp8) sc[i] = live ? __ldg(reinterpret_cast<const float2*>(row + kDv) + (c0 >> 2)) : make_float2(0, 0);
+        if (FMT == kTokenFp8 && group == 0) v[4][i] = live ? __ldg(reinterpret_cast<const uint4*>(row + kDv + pcs * 16)) : none;
       }
-      if (FMT == kTileFp8) {
-        if (n == 5) gr.rope = live ? __ldg(reinterpret_cast<const uint4*>(src + kTileRope + pcs * 32 + 16)) : make_uint4(0, 0, 0, 0);
-        gr.sc = live ? __ldg(reinterpret_cast<const float4*>(src + kDv)) : make_float4(0, 0, 0, 0);
-      }
+      if (FMT == kTileFp8) rope = live ? src + kTileRope + pcs * 32 : nullptr;
     };
-    auto store = [&](const Group& gr, int off, int c0, int n) {
+    auto store = [&](int off) {
 #pragma unroll
-      for (int i = 0; i < 5; ++i) {
-        if (i >= n) continue;
-        uint8_t* dst = smem + off + i * kChunk;
-        if (FMT == kTileFp8 && i == 4) {  // bf16 rope -> f16
-          const uint4 a = gr.v[4], b = gr.rope;
-          *reinterpret_cast<uint4*>(dst + piece_off(r, 2 * pcs)) =
-              make_uint4(to_f16(a.x, over), to_f16(a.y, over), to_f16(a.z, over), to_f16(a.w, over));
-          *reinterpret_cast<uint4*>(dst + piece_off(r, 2 * pcs + 1)) =
-              make_uint4(to_f16(b.x, over), to_f16(b.y, over), to_f16(b.z, over), to_f16(b.w, over));
-          continue;
-        }
-        float s = 1.0f;
-        if (FMT == kTileFp8) {
-          const int tile = (c0 + i) >> 1;
-          s = tile == 0 ? gr.sc.x : tile == 1 ? gr.sc.y : tile == 2 ? gr.sc.z : gr.sc.w;
-        }
-        const uint32_t w[4] = {gr.v[i].x, gr.v[i].y, gr.v[i].z, gr.v[i].w};
-        uint32_t o[8];
+      for (int c = 0; c < 5; ++c) {
+        if (c == 4 && group != 0) continue;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float f[4];
-          e4m3x4(w[k], f);
-          if (FMT == kTileFp8) {
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + 16 * i;
+          uint8_t* dst = smem + off + c * kChunk;
+          uint32_t o[8];
+          if (FMT == kTileFp8 && c == 4) {  // bf16 rope -> f16
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            const uint4 a = rope ? __ldg(reinterpret_cast<const uint4*>(rope + i * 16 * kRowBytes)) : none;
+            const uint4 b = rope ? __ldg(reinterpret_cast<const uint4*>(rope + i * 16 * kRowBytes + 16)) : none;
+            o[0] = to_f16(a.x, over), o[1] = to_f16(a.y, over), o[2] = to_f16(a.z, over), o[3] = to_f16(a.w, over);
+            o[4] = to_f16(b.x, over), o[5] = to_f16(b.y, over), o[6] = to_f16(b.z, over), o[7] = to_f16(b.w, over);
+          } else {
+            const uint32_t w[4] = {v[c][i].x, v[c][i].y, v[c][i].z, v[c][i].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              f[e] *= s;
-              over |= fabsf(f[e]) > 65504.0f && fabsf(f[e]) < INFINITY;
+            for (int k = 0; k < 4; ++k) {
+              o[2 * k] = e4m3x2(static_cast<uint16_t>(w[k]));
+              o[2 * k + 1] = e4m3x2(static_cast<uint16_t>(w[k] >> 16));
+            }
+            if (FMT == kTileFp8) {
+              const float s = c < 2 ? sc[i].x : sc[i].y;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
+                const float a = f.x * s, b = f.y * s;
+                top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
+                o[k] = pack2(a, b, true);
+              }
             }
           }
-          o[2 * k] = pack2(f[0], f[1], F16);
-          o[2 * k + 1] = pack2(f[2], f[3], F16);
+          *reinterpret_cast<uint4*>(dst + piece_off(r, 2 * pcs)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(dst + piece_off(r, 2 * pcs + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        *reinterpret_cast<uint4*>(dst + piece_off(r, 2 * pcs)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(dst + piece_off(r, 2 * pcs + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
     };
-    auto filled = [&](uint64_t* bar) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if (bar == &M.vo_full && warp == 6) mbar_arrive_expect_tx(bar, kQChunk);  // and the other page's P
-        else mbar_arrive(bar);
-      }
-    };
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, abort_v, p.status)); };
     Tiles cur;
     cur.line = line;
     bool more = cur.next(p, rank, true);
-    Group ko, kv, vo;  // each group's next load is in flight while the others are stored
-    if (more) {
-      fetch(ko, Tiles::pool_page(p, cur.own_id), kc0, 5);
-      fetch(kv, Tiles::pool_page(p, cur.own_id), vc0, 4);
-    }
-    uint32_t g = 0;
-    bool ok = true;
-    for (; more && ok; ++g) {
-      const int other = Tiles::pool_page(p, cur.other_id);
-      if (cur.bad(p) && lane == 0) set_status(p.status, kStatusBounds);
+    if (more) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
+    for (uint32_t g = 0; more; ++g) {
+      if (group == 0 && cur.bad(p) && lane == 0) set_status(p.status, kStatusBounds);
       more = cur.next(p, rank, false);
-      if (g > 0 && !wait(&M.ko_free, (g - 1) & 1)) { ok = false; break; }
-      store(ko, kOffKO, kc0, 5);
-      filled(&M.ko_full);
-      if (more) fetch(ko, Tiles::pool_page(p, cur.own_id), kc0, 5);
-      const int buf = g & 1;
-      if (g > 1 && !wait(&M.kv_free[buf], ((g >> 1) - 1) & 1)) { ok = false; break; }
-      store(kv, kOffKV + 4 * buf * kChunk, vc0, 4);
-      filled(&M.kv_full[buf]);
-      if (more) fetch(kv, Tiles::pool_page(p, cur.own_id), vc0, 4);
-      if (g > 0) {
-        if (g > 1 && !wait(&M.vo_free, (g - 2) & 1)) { ok = false; break; }
-        store(vo, kOffVO, vc0, 4);
-        filled(&M.vo_full);
+      // the slots' previous tile: g - 1, or g - 2 for KV's two buffers
+      const uint32_t back = group == 1 ? 2 : 1;
+      if (g >= back) {
+        uint64_t* bar = group == 0 ? &M.ko_free : group == 1 ? &M.kv_free[g & 1] : &M.vo_free;
+        if (!wait_warp<false>(bar, group == 1 ? ((g >> 1) - 1) & 1 : (g - 1) & 1, abort_v)) break;
       }
-      fetch(vo, other, vc0, 4);
+      store(group == 0 ? kOffKO : group == 1 ? kOffKV + static_cast<int>(g & 1) * 4 * kChunk : kOffVO);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (warp == kConvWarp0 + 4) mbar_arrive_expect_tx(&M.vo_full, kQChunk);  // and the other page's P
+        else mbar_arrive(group == 0 ? &M.ko_full : group == 1 ? &M.kv_full[g & 1] : &M.vo_full);
+      }
+      if (more) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
     }
-    if (ok && g > 0 && (g == 1 || wait(&M.vo_free, (g - 2) & 1))) {
-      store(vo, kOffVO, vc0, 4);
-      filled(&M.vo_full);
-    }
-    if (over) set_status(p.status, kStatusOverflow);
+    if (over || top > 65504.0f) set_status(p.status, kStatusOverflow);
   }
 
   __syncwarp();
@@ -1008,7 +1072,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the peer may still read or signal this CTA's shared memory until here
-  if (warp == 4) {
+  if (warp == kTmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1020,6 +1084,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
 // 2^(m - largest m). Reading fp32 partials that were just written, it is bound by
 // L2 and, for few rows, by latency: four blocks share a row's values, and each
 // thread keeps eight 16-byte loads in flight.
+__device__ __forceinline__ float piece_sum(const PrefixParams& p, int slot, int at) {
+  const float* l = p.part_l + static_cast<long long>(slot) * 4 * kRows + at;
+  return (l[0] + l[kRows]) + (l[2 * kRows] + l[3 * kRows]);
+}
+
 constexpr int kMergeRows = 16, kMergeCols = 128, kMergeThreads = 256;
 
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams p) {
@@ -1065,7 +1134,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
     float top = -INFINITY;
     for (int i = k; i < n; i += 16) {
       const int slot = slots[i] / kRows, at = slots[i] % kRows + row;
-      const float l = p.part_l[(static_cast<long long>(slot) * 2) * kRows + at] + p.part_l[(static_cast<long long>(slot) * 2 + 1) * kRows + at];
+      const float l = piece_sum(p, slot, at);
       const float m = p.part_m[static_cast<long long>(slot) * kRows + at];
       // a row that saw nothing in a piece (l = 0) has nothing there, whatever its O holds
       wgt[i][row] = l != 0.0f ? m : -INFINITY;
@@ -1076,7 +1145,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
     float sum = 0.0f;
     for (int i = k; i < n; i += 16) {
       const int slot = slots[i] / kRows, at = slots[i] % kRows + row;
-      const float l = p.part_l[(static_cast<long long>(slot) * 2) * kRows + at] + p.part_l[(static_cast<long long>(slot) * 2 + 1) * kRows + at];
+      const float l = piece_sum(p, slot, at);
       const float w = l != 0.0f ? exp2_fast(wgt[i][row] - top) : -1.0f;  // -1: nothing to add
       wgt[i][row] = w;
       if (l != 0.0f) sum += w * l;
@@ -1207,7 +1276,7 @@ size_t layout(PrefixParams& p, uint8_t* ws) {
   p.part_m = reinterpret_cast<float*>(ws + at);
   at += slots * kRows * 4;
   p.part_l = reinterpret_cast<float*>(ws + at);
-  at += slots * 2 * kRows * 4;
+  at += slots * 4 * kRows * 4;
   p.part_o = reinterpret_cast<float4*>(ws + at);
   return at + slots * 2 * 64 * kRows * 16;
 }
@@ -1249,7 +1318,9 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
   p.kv = static_cast<const uint8_t*>(cache->kv), p.kv_scale = cache->kv_scale, p.num_pages = cache->num_pages;
   p.page_tables = page_tables, p.max_pages = max_pages, p.seq_lens = seq_lens, p.max_seq_len = max_seq_len;
   p.q = static_cast<const uint16_t*>(q);
-  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  // the logits' scale as a positive factor: the maximum can be taken before it
+  p.scale_log2 = std::max(std::fabs(sm_scale) * 1.4426950408889634f, 1e-37f);
+  p.q_sign = sm_scale < 0.0f ? 0x80008000u : 0u;
   p.out = static_cast<uint16_t*>(out), p.lse = lse;
   p.status = static_cast<uint32_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
