@@ -24,9 +24,9 @@
 //   KO  own page, the 5 chunks that only QK reads     (1 tile)
 //   KV  own page, the 4 chunks of this CTA's output   (2 tiles)
 //   VO  other page, the 4 chunks of this CTA's output (1 tile)
-// Warp roles: 0-7 softmax and results (a thread per row and half of the page's
-// keys), 8 TMA loads of BF16 rows, 9 MMA issue, 10-15 (FP8 caches) load and widen
-// the rows instead of TMA, two warps for each of KO, KV and VO.
+// Warp roles: 0 MMA issue, 1 TMA loads of BF16 rows, 4-11 softmax and results (a
+// thread per row and half of the page's keys); FP8 caches: 2-3 and 12-15 load and
+// widen the rows instead of TMA, two warps for each of KO, KV and VO.
 // The issue order QK(t + 1), PV(t) keeps the tensor pipe busy during softmax(t).
 //
 // The work is cut evenly: segment after segment on one line (a tile costs 1, a
@@ -62,7 +62,7 @@ constexpr float kRaise = 8.0f;   // log2: the reference maximum is raised only w
 constexpr int kMaxPairs = 128;
 constexpr int kMaxPieces = kMaxPairs + 2;  // of a row: its two segments are walked by distinct pairs, but for one at each border
 constexpr int kTileRowBytes = 656, kTileRope = 528;
-constexpr int kSoftWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kConvWarp0 = 10;
+constexpr int kSoftWarps = 8, kMmaWarp = 0, kTmaWarp = 1, kSoftWarp0 = 4;
 constexpr int kPHalf = kRows * 64;  // P of half a page: 128 rows x 32 keys, 64-byte swizzled
 
 enum { kBf16 = 0, kTokenFp8 = 1, kTileFp8 = 2 };
@@ -499,7 +499,7 @@ __device__ __forceinline__ void prefetch_q(const PrefixParams& p, int s, int row
 }
 
 template <int FMT>
-constexpr int kThreadsOf = FMT == kBf16 ? 320 : 512;
+constexpr int kThreadsOf = FMT == kBf16 ? 384 : 512;
 
 template <int FMT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
@@ -608,9 +608,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
   const uint32_t sbase = smem_u32(smem);
   volatile int* abort_v = &M.abort_flag;
 
-  if (warp < kSoftWarps) {
+  if (warp >= kSoftWarp0 && warp < kSoftWarp0 + kSoftWarps) {
     // -------------------------------------------------------------- softmax, results
-    const int quad = warp & 3, half = warp >> 2;
+    const int sw = warp - kSoftWarp0, quad = sw & 3, half = sw >> 2;
     const int row = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t mx0 = smem_u32(&M.mx[0][0][0]), mxbar0 = smem_u32(&M.mx_full[0][0]);
@@ -619,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     const uint32_t p_at = kOffP + half * kPHalf + quad * 2048;  // the warp's 32 rows of its half
     const uint32_t peer_p = peer_addr(sbase + kQChunk + p_at, rank ^ 1);
     const uint32_t peer_pbar = peer_addr(smem_u32(&M.vo_full), rank ^ 1);
-    const bool writer = rank == 0 && tid == 0;
+    const bool writer = rank == 0 && sw == 0 && lane == 0;
     bool over = false;
     Line wline = line;
     Piece pc, nx;
@@ -684,8 +684,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       for (int t = pc.t0; t < pc.t1; ++t, ++g) {
         const int tile_k = (first_page + 2 * t) * kPage, key0 = tile_k + rank * kPage + half * 32;
         const int own = own_next;
-        const float4* ks = M.ks[warp];
-        const float2* rs = reinterpret_cast<const float2*>(M.rs[warp]);
+        const float4* ks = M.ks[sw];
+        const float2* rs = reinterpret_cast<const float2*>(M.rs[sw]);
         if (FMT == kTokenFp8) {
           // Per-token scales: out = sum_j 2^(x_j) s_j code_j with x_j the logit. The
           // scale goes into the exponent, y_j = x_j + log2 s_j, so that the
@@ -698,10 +698,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
           float sc = scale < 1e-30f ? 1e-30f : scale;
           if (key < lim.lo || key >= lim.max_hi) sc = 1.0f;
           __syncwarp();
-          float* k = &M.ks[warp][lane >> 1].x + (lane & 1);
+          float* k = &M.ks[sw][lane >> 1].x + (lane & 1);
           k[0] = sc * p.scale_log2;
           k[2] = log2f(sc);
-          M.rs[warp][lane] = sc == sc ? 1.0f / sc : 1.0f;
+          M.rs[sw][lane] = sc == sc ? 1.0f / sc : 1.0f;
           __syncwarp();
           if (more) scale = load_scale();
         }
@@ -971,14 +971,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     if (!ok) *abort_v = 2;
   } else if (FMT != kBf16) {
     // -------------------------------------------------------------- FP8 rows: load, widen, store
-    // Two warps for each of KO (10, 11), KV (12, 13) and VO (14, 15). Thread u takes
+    // Two warps for each of KO (2, 3), KV (12, 13) and VO (14, 15). Thread u takes
     // 16 codes of rows u / 4 + 16 i in every chunk (four lanes on a row's 64
     // contiguous bytes); a tile's pieces are loaded while the tile before is waited
     // for. Codes are exact in f16 (per-token scales enter the logits and P in
     // fp32); tile-scaled values (code * scale) are rounded to f16: off by at most
     // 2^-11 of the value.
-    const int group = (warp - kConvWarp0) >> 1;  // 0 KO, 1 KV, 2 VO
-    const int u = (tid - kConvWarp0 * 32) & 63, r0 = u >> 2, pcs = u & 3;
+    const int cw = warp < kSoftWarp0 ? warp - 2 : warp - 10;
+    const int group = cw >> 1;  // 0 KO, 1 KV, 2 VO
+    const int u = (cw & 1) * 32 + lane, r0 = u >> 2, pcs = u & 3;
     constexpr int kRowBytes = FMT == kTokenFp8 ? kDqk : kTileRowBytes;
     const int c0 = group == 0 ? 4 * (rank ^ 1) : 4 * rank;
     bool over = false;
@@ -1055,7 +1056,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (warp == kConvWarp0 + 4) mbar_arrive_expect_tx(&M.vo_full, kQChunk);  // and the other page's P
+        if (cw == 4) mbar_arrive_expect_tx(&M.vo_full, kQChunk);  // and the other page's P
         else mbar_arrive(group == 0 ? &M.ko_full : group == 1 ? &M.kv_full[g & 1] : &M.vo_full);
       }
       if (more) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
