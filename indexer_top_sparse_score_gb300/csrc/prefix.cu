@@ -321,12 +321,30 @@ __device__ __forceinline__ void tma_chunks(void* dst, const CUtensorMap* map, ui
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(y), "r"(z)
       : "memory");
 }
+// Shared-memory operand of an MMA: the low word of its descriptor holds the address
+// (in 16 bytes), the high word is the same wherever the operand starts.
+struct Operand {
+  uint32_t lo, hi;
+  __device__ __forceinline__ Operand operator+(int bytes) const { return {lo + static_cast<uint32_t>(bytes >> 4), hi}; }
+};
+__device__ __forceinline__ Operand operand(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout = kSwizzle128B) {
+  const uint64_t d = smem_desc(saddr, lbo, sbo, layout);
+  return {static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)};
+}
 // A from tensor memory
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, Operand b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A from shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, Operand a, Operand b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // arrives on the barrier at this address in both CTAs of the pair
@@ -885,87 +903,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     constexpr uint32_t id_pv = instr_desc(128, 256, kFmt, kFmt, false, true);
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const uint32_t sb = __shfl_sync(0xFFFFFFFFu, sbase, 0);
-    const uint64_t q_desc = smem_desc(sb + kOffQ, 16, 1024);
-    const uint64_t ko_desc = smem_desc(sb + kOffKO, 16, 1024);
-    const uint64_t kv_desc = smem_desc(sb + kOffKV, 16, 1024);
-    const uint64_t v_desc = smem_desc(sb + kOffKV, kChunk, 1024);   // the same chunks read as V: values x keys
-    const uint64_t vo_desc = smem_desc(sb + kOffVO, kChunk, 1024);
-    const uint64_t p_desc = smem_desc(sb + kOffP, 16, 512, kSwizzle64B);  // 32 keys a half: two K = 16 steps each
-    const uint64_t po_desc = smem_desc(sb + kOffP + kQChunk, 16, 512, kSwizzle64B);
+    const Operand q_desc = operand(sb + kOffQ, 16, 1024);
+    const Operand ko_desc = operand(sb + kOffKO, 16, 1024);
+    const Operand kv_desc = operand(sb + kOffKV, 16, 1024);
+    const Operand v_desc = operand(sb + kOffKV, kChunk, 1024);   // the same chunks read as V: values x keys
+    const Operand vo_desc = operand(sb + kOffVO, kChunk, 1024);
+    const Operand p_desc = operand(sb + kOffP, 16, 512, kSwizzle64B);  // 32 keys a half: two K = 16 steps each
+    const Operand po_desc = operand(sb + kOffP + kQChunk, 16, 512, kSwizzle64B);
     Line wline = line;
     Piece pc;
     uint32_t g = 0, n = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_poll<false>(bar, parity); };
+    // logits of tile g
+    auto qk = [&] {
+      if (!wait(&M.ko_full, g & 1) || (g > 0 && !wait(&M.s_free, (g - 1) & 1))) return false;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(tm + kColS, tm + kColQ + 32 * i + 8 * kk, ko_desc + (i * kChunk + 32 * kk), id_qk, i != 0 || kk != 0);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) mma_ss(tm + kColS, q_desc + 32 * kk, ko_desc + (4 * kChunk + 32 * kk), id_qk, 1);
+        mma_commit(&M.ko_free);
+      }
+      __syncwarp();
+      if (!wait(&M.kv_full[g & 1], (g >> 1) & 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const Operand kd = kv_desc + static_cast<int>(g & 1) * 4 * kChunk;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_ts(tm + kColS, tm + kColQ + 128 + 32 * i + 8 * kk, kd + (i * kChunk + 32 * kk), id_qk, 1);
+#pragma unroll
+        for (int i = 2; i < 4; ++i)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss(tm + kColS, q_desc + ((i - 1) * kQChunk + 32 * kk), kd + (i * kChunk + 32 * kk), id_qk, 1);
+        mma_commit(&M.s_full);
+      }
+      __syncwarp();
+      ++g;
+      return true;
+    };
+    // O (+)= P V of tile h, own page first: its V slots are the next to be refilled
+    auto pv = [&](uint32_t h, uint32_t first) {
+      if (!wait(&M.p_own, h & 1) || (first && n > 0 && !wait(&M.o_free, (n - 1) & 1))) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const Operand v = v_desc + static_cast<int>(h & 1) * 4 * kChunk;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ss(tm + kColO, p_desc + ((kk >> 1) * kPHalf + 32 * (kk & 1)), v + kk * 2048, id_pv, kk != 0 ? 1 : first ^ 1);
+        mma_commit(&M.kv_free[h & 1]);
+      }
+      __syncwarp();
+      if (!wait_poll<true>(&M.vo_full, h & 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ss(tm + kColO, po_desc + ((kk >> 1) * kPHalf + 32 * (kk & 1)), vo_desc + kk * 2048, id_pv, 1);
+        mma_commit(&M.vo_free);
+        commit_pair(&M.pv_done);
+      }
+      __syncwarp();
+      return true;
+    };
     while (ok && next_piece(p, wline, pc, false)) {
       if (!wait(&M.q_full, n & 1)) { ok = false; break; }
       const int t0 = __shfl_sync(0xFFFFFFFFu, pc.t0, 0), t1 = __shfl_sync(0xFFFFFFFFu, pc.t1, 0);
-      // step t: the logits of tile t, then the product of tile t - 1
-      for (int t = t0; t <= t1; ++t) {
-        if (t < t1) {
-          if (!wait(&M.ko_full, g & 1) || (g > 0 && !wait(&M.s_free, (g - 1) & 1))) { ok = false; break; }
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ts(tm + kColS, tm + kColQ + 32 * i + 8 * kk, ko_desc + static_cast<uint64_t>((i * kChunk >> 4) + 2 * kk), id_qk,
-                       i != 0 || kk != 0);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16(tm + kColS, q_desc + static_cast<uint64_t>(2 * kk), ko_desc + static_cast<uint64_t>((4 * kChunk >> 4) + 2 * kk),
-                      id_qk, 1);
-            mma_commit(&M.ko_free);
-          }
-          __syncwarp();
-          if (!wait(&M.kv_full[g & 1], (g >> 1) & 1)) { ok = false; break; }
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t kd = kv_desc + static_cast<uint64_t>((g & 1) * (4 * kChunk >> 4));
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ts(tm + kColS, tm + kColQ + 128 + 32 * i + 8 * kk, kd + static_cast<uint64_t>((i * kChunk >> 4) + 2 * kk), id_qk, 1);
-#pragma unroll
-            for (int i = 2; i < 4; ++i)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_f16(tm + kColS, q_desc + static_cast<uint64_t>(((i - 1) * kQChunk >> 4) + 2 * kk),
-                        kd + static_cast<uint64_t>((i * kChunk >> 4) + 2 * kk), id_qk, 1);
-            mma_commit(&M.s_full);
-          }
-          __syncwarp();
-          ++g;
-        }
-        if (t > t0) {
-          const uint32_t h = t < t1 ? g - 2 : g - 1;  // the tile before
-          const uint32_t first = t - 1 == t0;
-          if (!wait(&M.p_own, h & 1) || (first && n > 0 && !wait(&M.o_free, (n - 1) & 1))) { ok = false; break; }
-          tc_fence_after();
-          if (elect_one()) {
-            // own page first: its V slots are the next to be refilled
-            const uint64_t v = v_desc + static_cast<uint64_t>((h & 1) * (4 * kChunk >> 4));
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16(tm + kColO, p_desc + static_cast<uint64_t>((kk >> 1) * (kPHalf >> 4) + 2 * (kk & 1)), v + static_cast<uint64_t>(kk * 2048 >> 4), id_pv,
-                      kk != 0 ? 1 : first ^ 1);
-            mma_commit(&M.kv_free[h & 1]);
-          }
-          __syncwarp();
-          if (!wait_poll<true>(&M.vo_full, h & 1)) { ok = false; break; }
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16(tm + kColO, po_desc + static_cast<uint64_t>((kk >> 1) * (kPHalf >> 4) + 2 * (kk & 1)), vo_desc + static_cast<uint64_t>(kk * 2048 >> 4), id_pv, 1);
-            mma_commit(&M.vo_free);
-            commit_pair(&M.pv_done);
-          }
-          __syncwarp();
-        }
-      }
+      // the logits of a tile are issued before the product of the tile before it
+      ok = qk();
+      for (int t = t0 + 1; ok && t < t1; ++t) ok = qk() && pv(g - 2, t - 1 == t0);
+      ok = ok && pv(g - 1, t1 - 1 == t0);
       ++n;
     }
     if (!ok) *abort_v = 2;
