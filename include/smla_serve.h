@@ -9,8 +9,8 @@
  * enqueued on `stream`, no allocation and no synchronisation, argument checks
  * on the host before anything is enqueued, device-side errors as bits of the
  * status word at the head of the workspace (smla_read_status). Arrays of int32
- * and float need their natural alignment only; rows of bf16 or e4m3 values
- * start on 16-byte boundaries.
+ * and float need their natural alignment only; rows of bf16 or e4m3 values, norm
+ * weights and cos_sin start on 16-byte boundaries.
  */
 #ifndef SMLA_SERVE_H_
 #define SMLA_SERVE_H_
@@ -84,8 +84,8 @@ typedef struct smla_rope {
  *               NULL: y = x), values 512..575: the rotated rope values.
  *             Written as cache->kv_dtype says: bf16; e4m3 with one scale over
  *             the 576 values into kv_scale; or the 656-byte row with a scale per
- *             128 latent values and bf16 rope. scale = amax / 448 (1 if all are
- *             zero), code = e4m3(y / scale), rounded to nearest even.
+ *             128 latent values and bf16 rope. scale = amax / 448 (at least 2^-126; 1 if
+ *             all are zero), code = e4m3(y / scale), rounded to nearest even.
  *   k_raw     [rows] rows of d_idx bf16 values, k_stride apart (a multiple of
  *             8), or NULL: leave cache->k_idx alone.
  *               idx_norm and idx_bias ([d_idx] fp32): layer norm

@@ -174,8 +174,15 @@ def make_cache(cache) -> PagedCache:
                       idx_dtype=_dtype_code(cache.idx_dtype), d_idx=cache.k_idx.shape[-1])
 
 
+# torch's current stream as an integer, without the Stream object that
+# torch.cuda.current_stream() builds (where this torch has the call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -401,9 +408,20 @@ def sparse_mla_decode(cache, page_tables, seq_lens, max_seq_len, q_per_seq, q, q
 
 
 # ---------------------------------------------------------------------------- serving steps
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+# The checks here are plain ifs on attributes: at decode sizes a call costs the host
+# about as much as the GPU.
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+
+
+def _int32(*tensors):
+    for t in tensors:
+        if t is not None and (t.dtype is not _I32 or not t.is_contiguous()):
+            raise ValueError("lengths, tables, positions and maps are contiguous int32 tensors")
+
+
+def _fp32(t, n, what):
+    if t is not None and (t.dtype is not _F32 or t.numel() != n or not t.is_contiguous()):
+        raise ValueError(f"{what} is a contiguous fp32 tensor of {n} values")
 
 
 def build_tables(ctx_lens, new_lens, page_tables, free_pages, max_new, *, seq_lens=None, cu_new=None,
@@ -412,32 +430,44 @@ def build_tables(ctx_lens, new_lens, page_tables, free_pages, max_new, *, seq_le
     page_tables is updated in place. Returns (seq_lens, cu_new, positions, slots,
     row_seq, pages_used, ws)."""
     L = lib()
+    _int32(ctx_lens, new_lens, page_tables, free_pages, seq_lens, cu_new, positions, slots, row_seq, pages_used)
     n, max_pages = page_tables.shape
+    if ctx_lens.numel() != n or new_lens.numel() != n:
+        raise ValueError("ctx_lens and new_lens have one length per row of page_tables")
     dev = page_tables.device
-    for t in (ctx_lens, new_lens, page_tables, free_pages, seq_lens, cu_new, positions, slots, row_seq, pages_used):
-        _need(t is None or (t.dtype == torch.int32 and t.is_contiguous()), "lengths, tables and maps are contiguous int32")
-    _need(ctx_lens.numel() == n and new_lens.numel() == n, "one length per row of page_tables")
 
     def out(t, k):
-        _need(t is None or t.numel() >= k, "an output is too small")
-        return torch.empty(k, dtype=torch.int32, device=dev) if t is None else t
+        if t is None:
+            return torch.empty(k, dtype=_I32, device=dev)
+        if t.numel() < k:
+            raise ValueError("an output is too small")
+        return t
 
     seq_lens, cu_new, pages_used = out(seq_lens, n), out(cu_new, n + 1), out(pages_used, 1)
     positions, slots, row_seq = out(positions, max_new), out(slots, max_new), out(row_seq, max_new)
     if ws is None:
         ws = workspace(STATUS_BYTES, dev)
-    rc = L.smla_build_tables(_p(ctx_lens), _p(new_lens), n, _p(page_tables), max_pages, _p(free_pages),
-                             0 if free_pages is None else free_pages.numel(), max_new, _p(seq_lens), _p(cu_new),
-                             _p(positions), _p(slots), _p(row_seq), _p(pages_used), _p(ws), ws.numel(),
-                             _stream(stream))
+    rc = L.smla_build_tables(ctx_lens.data_ptr(), new_lens.data_ptr(), n, page_tables.data_ptr(), max_pages,
+                             _p(free_pages), 0 if free_pages is None else free_pages.numel(), max_new,
+                             seq_lens.data_ptr(), cu_new.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+                             row_seq.data_ptr(), pages_used.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(rc, "smla_build_tables")
     return seq_lens, cu_new, positions, slots, row_seq, pages_used, ws
 
 
 def _rope(table, kv_interleaved, idx_interleaved) -> RopeTable:
-    _need(table.dtype == torch.float32 and table.dim() == 2 and table.shape[1] == 64 and table.is_contiguous(),
-          "rope is a contiguous fp32 [max_pos, 64] table")
-    return RopeTable(_p(table), table.shape[0], int(kv_interleaved), int(idx_interleaved))
+    if table.dtype is not _F32 or table.dim() != 2 or table.shape[1] != 64 or not table.is_contiguous():
+        raise ValueError("rope is a contiguous fp32 [max_pos, 64] table")
+    return RopeTable(table.data_ptr(), table.shape[0], int(kv_interleaved), int(idx_interleaved))
+
+
+def _bf16_rows(t, rows, width):
+    """Row stride of a [rows, width] bf16 matrix whose rows are dense."""
+    if t is None:
+        return 0
+    if t.dtype is not _BF16 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width or t.stride(1) != 1:
+        raise ValueError(f"rows are bf16 [{rows}, {width}] with a row's values next to each other")
+    return t.stride(0) if rows > 1 else -(-width // 8) * 8
 
 
 def cache_append(cache, slots, positions, rope, *, ckv=None, kv_norm=None, k_idx=None, idx_norm=None, idx_bias=None,
@@ -447,20 +477,20 @@ def cache_append(cache, slots, positions, rope, *, ckv=None, kv_norm=None, k_idx
     (see smla_cache_append). Rows may be strided. Returns ws."""
     L = lib()
     rows = slots.numel()
-    _need(slots.dtype == torch.int32 and positions.dtype == torch.int32 and positions.numel() == rows,
-          "slots and positions are int32, one per row")
-    for x, d in ((ckv, D_QK), (k_idx, cache.k_idx.shape[-1])):
-        _need(x is None or (x.dtype == torch.bfloat16 and x.shape == (rows, d) and x.stride(1) == 1),
-              "rows are bf16 [rows, width] with values next to each other")
-    for t, d in ((kv_norm, D_V), (idx_norm, cache.k_idx.shape[-1]), (idx_bias, cache.k_idx.shape[-1])):
-        _need(t is None or (t.dtype == torch.float32 and t.numel() == d and t.is_contiguous()), "norm weights are fp32")
+    _int32(slots, positions)
+    if positions.numel() != rows:
+        raise ValueError("positions and slots have one entry per row")
+    d = cache.k_idx.shape[-1]
+    kv_stride, k_stride = _bf16_rows(ckv, rows, D_QK), _bf16_rows(k_idx, rows, d)
+    _fp32(kv_norm, D_V, "kv_norm")
+    _fp32(idx_norm, d, "idx_norm")
+    _fp32(idx_bias, d, "idx_bias")
     if ws is None:
         ws = workspace(STATUS_BYTES, slots.device)
     c, r = make_cache(cache), _rope(rope, kv_interleaved, idx_interleaved)
-    rc = L.smla_cache_append(ctypes.byref(c), ctypes.byref(r), rows, _p(slots), _p(positions), _p(ckv),
-                             0 if ckv is None else ckv.stride(0), _p(kv_norm), _p(k_idx),
-                             0 if k_idx is None else k_idx.stride(0), _p(idx_norm), _p(idx_bias), float(eps), _p(ws),
-                             ws.numel(), _stream(stream))
+    rc = L.smla_cache_append(ctypes.byref(c), ctypes.byref(r), rows, slots.data_ptr(), positions.data_ptr(), _p(ckv),
+                             kv_stride, _p(kv_norm), _p(k_idx), k_stride, _p(idx_norm), _p(idx_bias), eps,
+                             ws.data_ptr(), ws.numel(), _stream(stream))
     _check(rc, "smla_cache_append")
     return ws
 
@@ -475,40 +505,44 @@ def query_prep(positions, rope, *, q_pe=None, q=None, q_idx_raw=None, w=None, id
     w_out, ws)."""
     L = lib()
     rows = positions.numel()
-    _need(positions.dtype == torch.int32, "positions are int32")
+    _int32(positions)
     n_heads = h_idx = d_idx = pe_row = pe_head = raw_row = 0
     if q_pe is not None:
-        n_heads = q_pe.shape[1]
-        _need(q_pe.dtype == torch.bfloat16 and q_pe.shape == (rows, n_heads, D_QK - D_V) and q_pe.stride(2) == 1,
-              "q_pe is bf16 [rows, heads, 64] with values next to each other")
+        n, n_heads, d = q_pe.shape
+        pe_row, pe_head, unit = q_pe.stride()
+        if q_pe.dtype is not _BF16 or n != rows or d != D_QK - D_V or unit != 1:
+            raise ValueError("q_pe is bf16 [rows, heads, 64] with a head's values next to each other")
+        if rows == 1:
+            pe_row = 0
         if q is None:
-            q = torch.empty((rows, n_heads, D_QK), dtype=torch.bfloat16, device=q_pe.device)
-        _need(q.dtype == torch.bfloat16 and q.shape == (rows, n_heads, D_QK) and q.is_contiguous(),
-              "q is contiguous bf16 [rows, heads, 576]")
-        pe_row, pe_head = q_pe.stride(0), q_pe.stride(1)
+            q = torch.empty((rows, n_heads, D_QK), dtype=_BF16, device=q_pe.device)
+        elif q.dtype is not _BF16 or q.numel() != rows * n_heads * D_QK or not q.is_contiguous():
+            raise ValueError("q is contiguous bf16 [rows, heads, 576]")
     if q_idx_raw is not None:
-        h_idx, d_idx = q_idx_raw.shape[1:]
-        _need(q_idx_raw.dtype == torch.bfloat16 and q_idx_raw.shape[0] == rows and q_idx_raw.stride(2) == 1
-              and q_idx_raw.stride(1) == d_idx, "q_idx_raw is bf16 [rows, h_idx, d_idx], each row dense")
-        _need(w is not None and w.dtype == torch.float32 and w.shape == (rows, h_idx) and w.is_contiguous(),
-              "w is contiguous fp32 [rows, h_idx]")
-        raw_row = q_idx_raw.stride(0)
+        n, h_idx, d_idx = q_idx_raw.shape
+        raw_row, head, unit = q_idx_raw.stride()
+        values = rows * h_idx * d_idx
+        if q_idx_raw.dtype is not _BF16 or n != rows or unit != 1 or (head != d_idx and h_idx > 1):
+            raise ValueError("q_idx_raw is bf16 [rows, h_idx, d_idx], each row dense")
+        if rows == 1:
+            raw_row = h_idx * d_idx
+        if w is None:
+            raise ValueError("indexer queries need their head weights w")
+        _fp32(w, rows * h_idx, "w")
+        _fp32(w_out, rows * h_idx, "w_out")
+        _fp32(idx_norm, d_idx, "idx_norm")
         if q_idx is None:
-            q_idx = torch.empty((rows, h_idx, d_idx), device=w.device,
-                                dtype=torch.bfloat16 if idx_dtype == "bf16" else torch.uint8)
-        _need(q_idx.shape == (rows, h_idx, d_idx) and q_idx.is_contiguous()
-              and q_idx.element_size() == (2 if idx_dtype == "bf16" else 1), "q_idx does not fit idx_dtype")
+            q_idx = torch.empty((rows, h_idx, d_idx), device=w.device, dtype=_BF16 if idx_dtype == "bf16" else torch.uint8)
+        elif q_idx.numel() != values or q_idx.element_size() != (2 if idx_dtype == "bf16" else 1) or not q_idx.is_contiguous():
+            raise ValueError("q_idx is contiguous [rows, h_idx, d_idx] of idx_dtype")
         if w_out is None:
             w_out = torch.empty_like(w)
-        _need(w_out.dtype == torch.float32 and w_out.shape == w.shape and w_out.is_contiguous(), "w_out is like w")
-        _need(idx_norm is None or (idx_norm.dtype == torch.float32 and idx_norm.numel() == d_idx
-                                   and idx_norm.is_contiguous()), "idx_norm is fp32 [d_idx]")
     if ws is None:
         ws = workspace(STATUS_BYTES, positions.device)
     r = _rope(rope, kv_interleaved, idx_interleaved)
-    rc = L.smla_query_prep(ctypes.byref(r), rows, _p(positions), _p(q_pe), pe_row, pe_head, n_heads, _p(q),
-                           _p(q_idx_raw), raw_row, h_idx, d_idx, _dtype_code(idx_dtype), _p(idx_norm), float(eps),
-                           _p(w), float(w_scale), _p(q_idx), _p(w_out), _p(ws), ws.numel(), _stream(stream))
+    rc = L.smla_query_prep(ctypes.byref(r), rows, positions.data_ptr(), _p(q_pe), pe_row, pe_head, n_heads, _p(q),
+                           _p(q_idx_raw), raw_row, h_idx, d_idx, _dtype_code(idx_dtype), _p(idx_norm), eps, _p(w),
+                           w_scale, _p(q_idx), _p(w_out), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(rc, "smla_query_prep")
     return q, q_idx, w_out, ws
 
@@ -525,23 +559,25 @@ def shared_prefix_fwd(cache, page_tables, seq_lens, max_seq_len, shared_len, q_p
     L = lib()
     n_seqs, max_pages = page_tables.shape
     rows, H, _ = q.shape
-    _need(q.dtype == torch.bfloat16 and q.is_contiguous() and q.shape[2] == D_QK and rows == n_seqs * q_per_seq,
-          "q is contiguous bf16 [n_seqs * q_per_seq, heads, 576]")
-    _need(page_tables.dtype == torch.int32 and page_tables.is_contiguous() and seq_lens.dtype == torch.int32
-          and seq_lens.numel() == n_seqs and seq_lens.is_contiguous(), "page_tables and seq_lens are contiguous int32")
+    _int32(page_tables, seq_lens)
+    if q.dtype is not _BF16 or not q.is_contiguous() or q.shape[2] != D_QK or rows != n_seqs * q_per_seq:
+        raise ValueError("q is contiguous bf16 [n_seqs * q_per_seq, heads, 576]")
+    if seq_lens.numel() != n_seqs:
+        raise ValueError("seq_lens has one length per row of page_tables")
     if out is None:
-        out = torch.empty((rows, H, D_V), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((rows, H, D_V), dtype=_BF16, device=q.device)
+    elif out.dtype is not _BF16 or out.numel() != rows * H * D_V or not out.is_contiguous():
+        raise ValueError("out is contiguous bf16 [rows, heads, 512]")
     if lse is None:
-        lse = torch.empty((rows, H), dtype=torch.float32, device=q.device)
-    _need(out.dtype == torch.bfloat16 and out.shape == (rows, H, D_V) and out.is_contiguous()
-          and lse.dtype == torch.float32 and lse.shape == (rows, H) and lse.is_contiguous(),
-          "out is contiguous bf16 [rows, heads, 512], lse fp32 [rows, heads]")
+        lse = torch.empty((rows, H), dtype=_F32, device=q.device)
+    else:
+        _fp32(lse, rows * H, "lse")
     if ws is None:
         ws = workspace(shared_prefix_workspace_bytes(n_seqs, max_seq_len, shared_len, q_per_seq, H), q.device)
     c = make_cache(cache)
-    rc = L.smla_shared_prefix_fwd(ctypes.byref(c), _p(page_tables), max_pages, n_seqs, _p(seq_lens), max_seq_len,
-                                  shared_len, q_per_seq, _p(q), H, float(sm_scale), _p(out), _p(lse), _p(ws),
-                                  ws.numel(), _stream(stream))
+    rc = L.smla_shared_prefix_fwd(ctypes.byref(c), page_tables.data_ptr(), max_pages, n_seqs, seq_lens.data_ptr(),
+                                  max_seq_len, shared_len, q_per_seq, q.data_ptr(), H, sm_scale, out.data_ptr(),
+                                  lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(rc, "smla_shared_prefix_fwd")
     return out, lse, ws
 

@@ -452,7 +452,7 @@ __device__ __forceinline__ Limits limits(const PrefixParams& p, int s, int row) 
 }
 
 // Q of segment s, by one softmax warp: chunks of its 32 rows in 16-byte pieces,
-// eight lanes on one row's chunk (128 contiguous bytes), a chunk in flight (more
+// eight lanes on one row's chunk (128 contiguous bytes), two chunks in flight (FP8: one; more
 // push the tile loops' values into local memory, and next to 225 KB of shared
 // memory there is hardly any L1 to hold that). The six for tensor memory pass one by
 // one through a chunk's place in shared memory, from where every lane reads its own
@@ -479,28 +479,36 @@ __device__ __forceinline__ bool load_q(const PrefixParams& p, int s, uint8_t* q_
     w.x ^= p.q_sign, w.y ^= p.q_sign, w.z ^= p.q_sign, w.w ^= p.q_sign;
     *reinterpret_cast<uint4*>(q_smem + place * kQChunk + piece_off(quad * 32 + 4 * j + sub, pcs)) = w;
   };
-  uint4 v[8];
+  // step c < 3: chunk 3 half + c to tensor memory; step 3: the chunk of place 6 or 7;
+  // step 4: half of the rows of place 8
+  constexpr int kBatch = FMT == kBf16 ? 2 : 1;
+  uint4 v[kBatch][8];
 #pragma unroll 1
-  for (int c = 3 * half; c < 3 * half + 3; ++c) {
+  for (int c0 = 0; c0 < 5; c0 += kBatch) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = bring(c, j);
+    for (int u = 0; u < kBatch; ++u) {
+      const int c = c0 + u;
+      if (c < 5)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) put(half, j, v[j]);
-    __syncwarp();
+        for (int j = 0; j < 8; ++j)
+          if (c < 4 || j < 4) v[u][j] = bring(c < 3 ? 3 * half + c : c == 3 ? 6 + half : 8, c < 4 ? j : 4 * half + j);
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const uint4*>(q_smem + half * kQChunk + piece_off(quad * 32 + lane, j));
-    tmem_st_32x32b_x32(q_tmem + 32 * c, reinterpret_cast<const uint32_t*>(v));
-    __syncwarp();
+    for (int u = 0; u < kBatch; ++u) {
+      const int c = c0 + u;
+      if (c < 5)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c < 4 || j < 4) put(c < 4 ? half : 2, c < 4 ? j : 4 * half + j, v[u][j]);
+      if (c < 3) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[u][j] = *reinterpret_cast<const uint4*>(q_smem + half * kQChunk + piece_off(quad * 32 + lane, j));
+        tmem_st_32x32b_x32(q_tmem + 32 * (3 * half + c), reinterpret_cast<const uint32_t*>(v[u]));
+        __syncwarp();
+      }
+    }
   }
-  // the chunks of places 6 and 7, one a half, and half of the rows of place 8 each
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = bring(6 + half, j);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) put(half, j, v[j]);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = bring(8, 4 * half + j);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) put(2, 4 * half + j, v[j]);
   tmem_wait_st();
   fence_proxy_async_smem();
   tc_fence_before();

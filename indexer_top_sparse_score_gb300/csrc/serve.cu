@@ -3,6 +3,7 @@
 // (smla_query_prep). All three move little or stream their data once, so their
 // floors are launch latency (decode-sized calls) and memory bandwidth
 // (prefill-sized calls).
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 
@@ -17,7 +18,7 @@ namespace smla {
 namespace {
 
 // ---------------------------------------------------------------------------- tables
-constexpr int kTabThreads = 256;
+constexpr int kTabThreads = 1024;
 
 struct TablesParams {
   const int32_t* ctx;
@@ -42,21 +43,24 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
   __syncthreads();  // the previous use of warp_sums is over
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  long long before = 0;
-  total = 0;
+  long long w = warp_sums[lane];  // as many warps as lanes: every warp scans the warps' sums
+  static_assert(kTabThreads == 1024, "32 warps");
 #pragma unroll
-  for (int w = 0; w < kTabThreads / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    total += warp_sums[w];
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, w, d);
+    if (lane >= d) w += o;
   }
-  return v + before;
+  total = __shfl_sync(0xFFFFFFFFu, w, 31);
+  const long long before = __shfl_sync(0xFFFFFFFFu, w, (warp + 31) & 31);
+  return v + (warp ? before : 0);
 }
 
-// Every block scans all requests' lengths (a few KB that stay in L2; no block
-// waits for another, so one launch does the whole job) and writes the rows
-// [first, last) of the per-token outputs that are its share; block 0 also
-// writes the per-request outputs and the status word, which needs no clearing
-// launch because block 0 sees every condition that can set it.
+// Every block scans all requests' lengths, 1,024 at a time (a few KB that stay in
+// L2; no block waits for another, so one launch does the whole job), and writes
+// the rows [first, last) of the per-token outputs that are its share; block 0
+// also writes the per-request outputs and the status word, which needs no clearing
+// launch because block 0 sees every condition that can set it. Bound by latency:
+// a load, two block scans and a search per 1,024 requests.
 __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesParams p) {
   __shared__ long long warp_sums[kTabThreads / 32];
   __shared__ int s_cu[kTabThreads + 1];   // first row of each request of the chunk
@@ -168,6 +172,10 @@ __device__ __forceinline__ void unpack(const void* p, float* v) {
     v[2 * i + 1] = bf_hi(w[i]);
   }
 }
+__device__ __forceinline__ void load8(const float* p, float* v) {  // 16-byte aligned
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
 template <int W>
 __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
@@ -180,45 +188,65 @@ __device__ __forceinline__ float lanes_max(float v) {
   for (int d = W / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
   return v;
 }
-__device__ __forceinline__ float scale_of(float top) { return top > 0.0f ? top / 448.0f : 1.0f; }
+// scale = amax / 448 (at least 2^-126; 1 where all are zero) and its reciprocal, as
+// products with rounded reciprocals: each off by a few 2^-24, and a value by as much
+// before it is rounded to a code's three bits, for a tenth of the instructions
+// of two divisions and one a value. (NaN does not show in amax: its code is NaN.)
+struct Scale {
+  float s, inv;
+  __device__ __forceinline__ explicit Scale(float top) : s(1.0f), inv(1.0f) {
+    if (top > 0.0f) {
+      s = fmaxf(top * (1.0f / 448.0f), FLT_MIN);
+      inv = __fdividef(1.0f, s);
+    }
+  }
+  __device__ __forceinline__ uint32_t pack(float a, float b) const { return e4m3_pack(a * inv, b * inv); }
+  __device__ __forceinline__ uint32_t pack4(const float* v) const { return pack(v[0], v[1]) | (pack(v[2], v[3]) << 16); }
+};
 
-// Rotation of 8 neighbouring values (first value's index i0 within the 64) held
-// by a lane; the other half of a half-split pair sits 4 lanes away.
-__device__ __forceinline__ void load_turn8(const float* cs, int i0, bool inter, float* c, float* s) {
-  if (inter) {  // pairs i0/2 .. i0/2 + 3
-    const float4 a = *reinterpret_cast<const float4*>(cs + i0 / 2), b = *reinterpret_cast<const float4*>(cs + 32 + i0 / 2);
-    c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
-    s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
-  } else {
-    const int j = i0 & 31;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 a = *reinterpret_cast<const float4*>(cs + j + 4 * h), b = *reinterpret_cast<const float4*>(cs + 32 + j + 4 * h);
-      c[4 * h] = a.x, c[4 * h + 1] = a.y, c[4 * h + 2] = a.z, c[4 * h + 3] = a.w;
-      s[4 * h] = b.x, s[4 * h + 1] = b.y, s[4 * h + 2] = b.z, s[4 * h + 3] = b.w;
+// How a head's or key's values lie in its lanes: eight a lane in two groups of four,
+// so that both values of every rotated pair are in one lane under either pairing.
+// Rotated lanes (sub < 8): pairs 4 sub .. 4 sub + 3.
+struct Places {
+  int a, b;  // first value of each group
+  __device__ __forceinline__ Places(int sub, bool inter) {
+    const bool halves = !inter && sub < 8;
+    a = halves ? 4 * sub : 8 * sub;
+    b = halves ? 32 + 4 * sub : 8 * sub + 4;
+  }
+};
+struct Turn {  // cosines and sines of a lane's four pairs
+  float4 c, s;
+  __device__ __forceinline__ Turn(const float* cos_sin, int pos, int sub) {
+    const float* at = cos_sin + static_cast<long long>(pos) * 64 + 4 * (sub & 7);
+    c = __ldg(reinterpret_cast<const float4*>(at));
+    s = __ldg(reinterpret_cast<const float4*>(at + 32));
+  }
+  static __device__ __forceinline__ void pair(float& a, float& b, float c, float s) {
+    const float x = a, y = b;
+    a = x * c - y * s;
+    b = x * s + y * c;
+  }
+  __device__ __forceinline__ void apply(float* v, bool inter) const {
+    if (inter) {
+      pair(v[0], v[1], c.x, s.x), pair(v[2], v[3], c.y, s.y), pair(v[4], v[5], c.z, s.z), pair(v[6], v[7], c.w, s.w);
+    } else {
+      pair(v[0], v[4], c.x, s.x), pair(v[1], v[5], c.y, s.y), pair(v[2], v[6], c.z, s.z), pair(v[3], v[7], c.w, s.w);
     }
   }
+};
+// the lane's eight bf16 values of a head at p, and the way back
+__device__ __forceinline__ uint4 load_groups(const uint16_t* p, const Places& at) {
+  const uint2 a = __ldg(reinterpret_cast<const uint2*>(p + at.a)), b = __ldg(reinterpret_cast<const uint2*>(p + at.b));
+  return make_uint4(a.x, a.y, b.x, b.y);
 }
-// (a, b) -> (a c - b s, a s + b c); `act`: the lane holds rotated values (the
-// whole warp takes part in the exchange)
-__device__ __forceinline__ void turn8(float* v, const float* c, const float* s, int i0, bool inter, bool act) {
-  if (inter) {
-    if (act) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = v[2 * i], b = v[2 * i + 1];
-        v[2 * i] = a * c[i] - b * s[i];
-        v[2 * i + 1] = a * s[i] + b * c[i];
-      }
-    }
-  } else {
-    const float sign = i0 < 32 ? -1.0f : 1.0f;  // first half: a c - b s; second: b c + a s
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_xor_sync(0xFFFFFFFFu, v[i], 4);
-      if (act) v[i] = v[i] * c[i] + sign * o * s[i];
-    }
-  }
+__device__ __forceinline__ void store_groups(uint16_t* p, const Places& at, const float* v) {
+  *reinterpret_cast<uint2*>(p + at.a) = make_uint2(bf_pack(v[0], v[1]), bf_pack(v[2], v[3]));
+  *reinterpret_cast<uint2*>(p + at.b) = make_uint2(bf_pack(v[4], v[5]), bf_pack(v[6], v[7]));
+}
+__device__ __forceinline__ void load_weights(const float* p, const Places& at, float* w) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p + at.a)), b = __ldg(reinterpret_cast<const float4*>(p + at.b));
+  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
 }
 
 struct AppendParams {
@@ -237,41 +265,58 @@ struct AppendParams {
   const float *idx_norm, *idx_bias;
   float eps;
   const float* cos_sin;
-  int32_t max_pos, kv_inter, idx_inter;
+  int32_t max_pos, kv_inter, idx_inter, first_reports;
   uint32_t* status;
 };
 
-// The row's slot, or -1 to skip it; what is out of range is reported.
-__device__ __forceinline__ int row_slot(const AppendParams& p, int row, int& pos) {
-  const int slot = p.slots[row];
-  pos = p.positions[row];
-  if (slot == -1) return -1;
-  if (slot < 0 || slot >= p.pool_rows || pos < 0 || pos >= p.max_pos) {
-    if ((threadIdx.x & 31) == 0) set_status(p.status, kStatusBounds);
-    return -1;
+// The row's slot, or -1 to skip it (a row that is not written, or out of range).
+__device__ __forceinline__ int usable_slot(const AppendParams& p, int slot, int pos) {
+  const bool ok = slot >= 0 && slot < p.pool_rows && pos >= 0 && pos < p.max_pos;
+  if (!ok && slot != -1 && !p.first_reports) set_status(p.status, kStatusBounds);
+  return ok ? slot : -1;
+}
+// How a launch reports rows that it skips as out of range. Up to kReportRows rows
+// its first block only looks all of them over and writes the status word, so that
+// the call needs no launch to clear it (about 2 us of an 8 us call); with more rows
+// that block would end last, the word is cleared by a memset, and the warps report.
+constexpr int kReportRows = 4096;
+
+template <typename Bad>
+__device__ __forceinline__ void report_rows(int rows, uint32_t* status, Bad bad) {
+  bool any = false;
+  for (int r0 = threadIdx.x; r0 < rows; r0 += 8 * blockDim.x) {
+    bool b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = bad(min(r0 + i * static_cast<int>(blockDim.x), rows - 1));  // loads of all eight in flight
+#pragma unroll
+    for (int i = 0; i < 8; ++i) any |= b[i];
   }
-  return slot;
+  const int found = __syncthreads_or(any);
+  if (threadIdx.x == 0) *status = found ? kStatusBounds : 0u;
 }
 
-// One warp per latent row and one per four indexer keys (a key takes 8 or 16
-// lanes of 8 values): a row is read once in 16-byte pieces, reduced in
-// registers and written once.
+// One warp per latent row and one per two or four indexer keys (a key takes 16 or 8
+// lanes of 8 values): a row is read once in 16-byte pieces, reduced in registers
+// and written once. Its values are requested before the slot and position are
+// looked at, so a row costs two memory latencies (position, then its angles)
+// and not three.
 constexpr int kRowThreads = 128;
 
 __device__ __forceinline__ void append_latent(const AppendParams& p, int row) {
   const int lane = threadIdx.x & 31;
-  int pos;
-  const int slot = row_slot(p, row, pos);
-  if (slot < 0) return;
   const uint16_t* x = p.ckv + row * p.ckv_stride;
+  const int pos = __ldg(p.positions + row), id = __ldg(p.slots + row);
   // values 8 lane .. 8 lane + 7 and 256 + 8 lane .. of the latent part, two rope values
-  const uint4 w0 = *reinterpret_cast<const uint4*>(x + 8 * lane);
-  const uint4 w1 = *reinterpret_cast<const uint4*>(x + 256 + 8 * lane);
-  const float* cs = p.cos_sin + static_cast<long long>(pos) * 64;
-  const float c = cs[lane], s = cs[32 + lane];
+  const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(x + 8 * lane));
+  const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(x + 256 + 8 * lane));
   const int ia = p.kv_inter ? 2 * lane : lane, ib = p.kv_inter ? 2 * lane + 1 : lane + 32;
-  const float a = __uint_as_float(static_cast<uint32_t>(x[kDv + ia]) << 16);
-  const float b = __uint_as_float(static_cast<uint32_t>(x[kDv + ib]) << 16);
+  const uint16_t xa = __ldg(x + kDv + ia), xb = __ldg(x + kDv + ib);
+  const int slot = usable_slot(p, id, pos);
+  if (slot < 0) return;
+  const float* cs = p.cos_sin + static_cast<long long>(pos) * 64;
+  const float c = __ldg(cs + lane), s = __ldg(cs + 32 + lane);
+  const float a = __uint_as_float(static_cast<uint32_t>(xa) << 16);
+  const float b = __uint_as_float(static_cast<uint32_t>(xb) << 16);
   const float ra = a * c - b * s, rb = a * s + b * c;
   float v[16];
   unpack<8>(&w0, v);
@@ -280,11 +325,14 @@ __device__ __forceinline__ void append_latent(const AppendParams& p, int row) {
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) sq += v[i] * v[i];
-    const float r = 1.0f / sqrtf(lanes_sum<32>(sq) / kDv + p.eps);
+    const float r = rsqrtf(lanes_sum<32>(sq) / kDv + p.eps);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      float w[8];
+      load8(p.kv_norm + 256 * h + 8 * lane, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[8 * h + i] = v[8 * h + i] * r * p.kv_norm[256 * h + 8 * lane + i];
+      for (int i = 0; i < 8; ++i) v[8 * h + i] = v[8 * h + i] * r * w[i];
+    }
   }
   if (p.kv_dtype == SMLA_BF16) {
     uint16_t* o = reinterpret_cast<uint16_t*>(p.kv) + static_cast<long long>(slot) * kDqk;
@@ -302,42 +350,40 @@ __device__ __forceinline__ void append_latent(const AppendParams& p, int row) {
   float top[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < 16; ++i) top[i >> 3] = fmaxf(top[i >> 3], fabsf(v[i]));
-  float sc[2];
   if (tile) {  // 16 lanes hold a tile of 128 values
-    sc[0] = scale_of(lanes_max<16>(top[0]));
-    sc[1] = scale_of(lanes_max<16>(top[1]));
+    top[0] = lanes_max<16>(top[0]);
+    top[1] = lanes_max<16>(top[1]);
   } else {
-    sc[0] = sc[1] = scale_of(lanes_max<32>(fmaxf(fmaxf(top[0], top[1]), fmaxf(fabsf(ra), fabsf(rb)))));
+    top[0] = top[1] = lanes_max<32>(fmaxf(fmaxf(top[0], top[1]), fmaxf(fabsf(ra), fabsf(rb))));
   }
+  const Scale by[2] = {Scale(top[0]), Scale(top[1])};
   uint8_t* o = p.kv + static_cast<long long>(slot) * (tile ? 656 : kDqk);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = e4m3_pack(v[8 * h + 2 * i] / sc[h], v[8 * h + 2 * i + 1] / sc[h]);
-    *reinterpret_cast<uint2*>(o + 256 * h + 8 * lane) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+    *reinterpret_cast<uint2*>(o + 256 * h + 8 * lane) = make_uint2(by[h].pack4(v + 8 * h), by[h].pack4(v + 8 * h + 4));
   }
   if (tile) {
     if ((lane & 15) == 0) {
-      reinterpret_cast<float*>(o + kDv)[lane >> 4] = sc[0];
-      reinterpret_cast<float*>(o + kDv)[2 + (lane >> 4)] = sc[1];
+      reinterpret_cast<float*>(o + kDv)[lane >> 4] = by[0].s;
+      reinterpret_cast<float*>(o + kDv)[2 + (lane >> 4)] = by[1].s;
     }
     uint16_t* ro = reinterpret_cast<uint16_t*>(o + kDv + 16);
     const uint32_t pr = bf_pack(ra, rb);
     ro[ia] = static_cast<uint16_t>(pr);
     ro[ib] = static_cast<uint16_t>(pr >> 16);
   } else {
-    const uint32_t q = e4m3_pack(ra / sc[0], rb / sc[0]);
+    const uint32_t q = by[0].pack(ra, rb);
     o[kDv + ia] = static_cast<uint8_t>(q);
     o[kDv + ib] = static_cast<uint8_t>(q >> 8);
-    if (lane == 0) p.kv_scale[slot] = sc[0];
+    if (lane == 0) p.kv_scale[slot] = by[0].s;
   }
 }
 
-// Norm of 8 values a lane over the L lanes of one head or key of 8 L values.
+// Norm of 8 values a lane over the L lanes of one head or key of 8 L values; w and b:
+// the lane's weights and biases.
 template <int L>
-__device__ __forceinline__ void head_norm(float* v, const float* w, const float* bias, float eps, int sub) {
-  if (!w) return;
+__device__ __forceinline__ void head_norm(float* v, bool norm, const float* w, bool bias, const float* b, float eps) {
+  if (!norm) return;
   if (bias) {
     float sum = 0.0f;
 #pragma unroll
@@ -349,9 +395,9 @@ __device__ __forceinline__ void head_norm(float* v, const float* w, const float*
   float sq = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) sq += v[i] * v[i];
-  const float r = 1.0f / sqrtf(lanes_sum<L>(sq) / (8 * L) + eps);
+  const float r = rsqrtf(lanes_sum<L>(sq) / (8 * L) + eps);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[8 * sub + i] + (bias ? bias[8 * sub + i] : 0.0f);
+  for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i] + (bias ? b[i] : 0.0f);
 }
 
 // L lanes of 8 values a key: 16 (e4m3, 128 values) or 8 (bf16, 64 values).
@@ -359,51 +405,50 @@ template <int L>
 __device__ __forceinline__ void append_keys(const AppendParams& p, int unit) {
   const int lane = threadIdx.x & 31, sub = lane % L;
   const int row = unit * (32 / L) + lane / L;
+  const Places at(sub, p.idx_inter);
   int pos = 0, slot = -1;
+  uint4 w = make_uint4(0, 0, 0, 0);
   if (row < p.rows) {
-    slot = p.slots[row];
-    pos = p.positions[row];
-    if (slot != -1 && (slot < 0 || slot >= p.pool_rows || pos < 0 || pos >= p.max_pos)) {
-      set_status(p.status, kStatusBounds);
-      slot = -1;
-    }
+    w = load_groups(p.k_raw + row * p.k_stride, at);
+    pos = __ldg(p.positions + row);
+    slot = usable_slot(p, __ldg(p.slots + row), pos);
   }
   const bool live = slot >= 0;
-  if (!live) pos = 0;
-  uint4 w = make_uint4(0, 0, 0, 0);
-  if (live) w = *reinterpret_cast<const uint4*>(p.k_raw + row * p.k_stride + 8 * sub);
-  float c[8], s[8], v[8];
-  const bool act = sub < 8;
-  const int i0 = 8 * (sub & 7);
-  load_turn8(p.cos_sin + static_cast<long long>(pos) * 64, i0, p.idx_inter, c, s);
+  const Turn turn(p.cos_sin, live ? pos : 0, sub);
+  float v[8], nw[8], nb[8];
+  if (p.idx_norm) load_weights(p.idx_norm, at, nw);
+  if (p.idx_bias) load_weights(p.idx_bias, at, nb);
   unpack<8>(&w, v);
-  head_norm<L>(v, p.idx_norm, p.idx_bias, p.eps, sub);
-  turn8(v, c, s, i0, p.idx_inter, act);
+  head_norm<L>(v, p.idx_norm != nullptr, nw, p.idx_bias != nullptr, nb, p.eps);
+  if (sub < 8) turn.apply(v, p.idx_inter);
+  uint8_t* o = p.k_idx + static_cast<long long>(max(slot, 0)) * 128;
   if (L == 8) {
-    if (live)
-      *reinterpret_cast<uint4*>(p.k_idx + static_cast<long long>(slot) * 128 + 16 * sub) =
-          make_uint4(bf_pack(v[0], v[1]), bf_pack(v[2], v[3]), bf_pack(v[4], v[5]), bf_pack(v[6], v[7]));
+    if (live) store_groups(reinterpret_cast<uint16_t*>(o), at, v);
     return;
   }
-  float sc = 1.0f;
+  float top = 0.0f;
   if (p.k_idx_scale) {
-    float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
-    sc = scale_of(lanes_max<L>(top));
-    if (live && sub == 0) p.k_idx_scale[slot] = sc;
+    top = lanes_max<L>(top);
   }
+  const Scale by(top);  // (without a scale array: 1)
   if (live) {
-    uint32_t q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = e4m3_pack(v[2 * i] / sc, v[2 * i + 1] / sc);
-    *reinterpret_cast<uint2*>(p.k_idx + static_cast<long long>(slot) * 128 + 8 * sub) =
-        make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+    if (p.k_idx_scale && sub == 0) p.k_idx_scale[slot] = by.s;
+    *reinterpret_cast<uint32_t*>(o + at.a) = by.pack4(v);
+    *reinterpret_cast<uint32_t*>(o + at.b) = by.pack4(v + 4);
   }
 }
 
 __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const AppendParams p, int latent_warps) {
-  const int warp = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (p.first_reports && blockIdx.x == 0) {
+    report_rows(p.rows, p.status, [&](int r) {
+      const int slot = __ldg(p.slots + r), pos = __ldg(p.positions + r);
+      return slot != -1 && (slot < 0 || slot >= p.pool_rows || pos < 0 || pos >= p.max_pos);
+    });
+    return;
+  }
+  const int warp = (blockIdx.x - p.first_reports) * (kRowThreads / 32) + (threadIdx.x >> 5);
   if (warp < latent_warps) {
     append_latent(p, warp);
   } else if (p.k_raw) {
@@ -434,83 +479,105 @@ struct QueryParams {
   uint8_t* q_idx;
   float* w_out;
   uint32_t* status;
-  int32_t pe_units, units;  // warps per row: 16 attention heads or 8 (fp8) / 16 (bf16) indexer heads each
+  int32_t pe_units, units;  // warps per row: up to 32 attention heads or 16 (fp8) / 32 (bf16) indexer heads each
+  int32_t first_reports;
 };
 
+// A warp takes four steps of 4 (8 lanes a head) or 2 (16 lanes) heads of one row,
+// all loaded before the row's position and angles, which are two latencies away.
+constexpr int kSteps = 4;
+
 template <int L>
-__device__ __forceinline__ void query_heads(const QueryParams& p, int row, int pos, int unit) {
+__device__ __forceinline__ void query_heads(const QueryParams& p, int row, int unit) {
   constexpr int kPer = 32 / L;  // heads per step
   const int lane = threadIdx.x & 31, sub = lane % L;
-  const int i0 = 8 * (sub & 7);
-  float c[8], s[8];
-  load_turn8(p.cos_sin + static_cast<long long>(pos) * 64, i0, p.idx_inter, c, s);
-  uint4 w[4];
+  const Places at(sub, p.idx_inter);
+  uint4 w[kSteps];
+  float head_w[kSteps];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int h = (unit * 4 + j) * kPer + lane / L;
-    if (h < p.h_idx) w[j] = *reinterpret_cast<const uint4*>(p.q_raw + row * p.raw_stride + h * (8 * L) + 8 * sub);
-    else w[j] = make_uint4(0, 0, 0, 0);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int h = (unit * 4 + j) * kPer + lane / L;
+  for (int j = 0; j < kSteps; ++j) {
+    const int h = (unit * kSteps + j) * kPer + lane / L;
     const bool live = h < p.h_idx;
-    const long long at = static_cast<long long>(row) * p.h_idx + h;
+    w[j] = live ? load_groups(p.q_raw + row * p.raw_stride + h * (8 * L), at) : make_uint4(0, 0, 0, 0);
+    head_w[j] = live && sub == 0 ? p.w[static_cast<long long>(row) * p.h_idx + h] : 0.0f;  // (w_out may be w)
+  }
+  float nw[8];
+  if (p.idx_norm) load_weights(p.idx_norm, at, nw);
+  const int pos = __ldg(p.positions + row);
+  if (pos < 0 || pos >= p.max_pos) {
+    if (!p.first_reports) set_status(p.status, kStatusBounds);
+    return;
+  }
+  const Turn turn(p.cos_sin, pos, sub);
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    const int h = (unit * kSteps + j) * kPer + lane / L;
+    const bool live = h < p.h_idx;
+    if (j > 0 && (unit * kSteps + j) * kPer >= p.h_idx) break;
+    const long long head = static_cast<long long>(row) * p.h_idx + h;
     float v[8];
     unpack<8>(&w[j], v);
-    head_norm<L>(v, p.idx_norm, nullptr, p.eps, sub);
-    turn8(v, c, s, i0, p.idx_inter, sub < 8);
-    float sc = 1.0f;
-    if (L == 8) {
-      if (live)
-        *reinterpret_cast<uint4*>(p.q_idx + at * 128 + 16 * sub) =
-            make_uint4(bf_pack(v[0], v[1]), bf_pack(v[2], v[3]), bf_pack(v[4], v[5]), bf_pack(v[6], v[7]));
-    } else {
-      float top = 0.0f;
+    head_norm<L>(v, p.idx_norm != nullptr, nw, false, nw, p.eps);
+    if (sub < 8) turn.apply(v, p.idx_inter);
+    float top = 0.0f;
+    if (L == 16) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
-      sc = scale_of(lanes_max<L>(top));
-      uint32_t q[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = e4m3_pack(v[2 * i] / sc, v[2 * i + 1] / sc);
-      if (live) *reinterpret_cast<uint2*>(p.q_idx + at * 128 + 8 * sub) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+      top = lanes_max<L>(top);
     }
-    if (live && sub == 0) p.w_out[at] = p.w[at] * (sc * p.w_scale);
+    const Scale by(top);  // (bf16: 1)
+    if (live) {
+      uint8_t* o = p.q_idx + head * 128;
+      if (L == 8) {
+        store_groups(reinterpret_cast<uint16_t*>(o), at, v);
+      } else {
+        *reinterpret_cast<uint32_t*>(o + at.a) = by.pack4(v);
+        *reinterpret_cast<uint32_t*>(o + at.b) = by.pack4(v + 4);
+      }
+      if (sub == 0) p.w_out[head] = head_w[j] * (by.s * p.w_scale);
+    }
   }
 }
 
 __global__ void __launch_bounds__(kRowThreads) query_prep_kernel(const QueryParams p) {
-  const long long warp = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (p.first_reports && blockIdx.x == 0) {
+    report_rows(p.rows, p.status, [&](int r) {
+      const int pos = __ldg(p.positions + r);
+      return pos < 0 || pos >= p.max_pos;
+    });
+    return;
+  }
+  const long long warp = static_cast<long long>(blockIdx.x - p.first_reports) * (kRowThreads / 32) + (threadIdx.x >> 5);
   const int row = static_cast<int>(warp / p.units), unit = static_cast<int>(warp - static_cast<long long>(row) * p.units);
   if (row >= p.rows) return;
   const int lane = threadIdx.x & 31;
-  const int pos = p.positions[row];
-  if (pos < 0 || pos >= p.max_pos) {
-    if (lane == 0) set_status(p.status, kStatusBounds);
-    return;
-  }
   if (unit >= p.pe_units) {
-    if (p.idx_fp8) query_heads<16>(p, row, pos, unit - p.pe_units);
-    else query_heads<8>(p, row, pos, unit - p.pe_units);
+    if (p.idx_fp8) query_heads<16>(p, row, unit - p.pe_units);
+    else query_heads<8>(p, row, unit - p.pe_units);
     return;
   }
-  const int sub = lane & 7, i0 = 8 * sub;
-  float c[8], s[8];
-  load_turn8(p.cos_sin + static_cast<long long>(pos) * 64, i0, p.kv_inter, c, s);
-  uint4 w[4];
+  const int sub = lane & 7;
+  const Places at(sub, p.kv_inter);
+  uint4 w[kSteps];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int h = unit * 16 + j * 4 + (lane >> 3);
-    w[j] = *reinterpret_cast<const uint4*>(p.q_pe + row * p.pe_row + h * p.pe_head + i0);
+  for (int j = 0; j < kSteps; ++j) {
+    const int h = (unit * kSteps + j) * 4 + (lane >> 3);
+    if (h < p.n_heads) w[j] = load_groups(p.q_pe + row * p.pe_row + h * p.pe_head, at);
   }
+  const int pos = __ldg(p.positions + row);
+  if (pos < 0 || pos >= p.max_pos) {
+    if (!p.first_reports) set_status(p.status, kStatusBounds);
+    return;
+  }
+  const Turn turn(p.cos_sin, pos, sub);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int h = unit * 16 + j * 4 + (lane >> 3);
+  for (int j = 0; j < kSteps; ++j) {
+    const int h = (unit * kSteps + j) * 4 + (lane >> 3);
+    if (h >= p.n_heads) break;  // (heads are a multiple of 4: the whole warp)
     float v[8];
     unpack<8>(&w[j], v);
-    turn8(v, c, s, i0, p.kv_inter, true);
-    *reinterpret_cast<uint4*>(p.q + (static_cast<long long>(row) * p.n_heads + h) * kDqk + kDv + i0) =
-        make_uint4(bf_pack(v[0], v[1]), bf_pack(v[2], v[3]), bf_pack(v[4], v[5]), bf_pack(v[6], v[7]));
+    turn.apply(v, p.kv_inter);
+    store_groups(p.q + (static_cast<long long>(row) * p.n_heads + h) * kDqk + kDv, at, v);
   }
 }
 
@@ -548,7 +615,7 @@ int smla_build_tables(const int32_t* ctx_lens, const int32_t* new_lens, int32_t 
     if (!al(a, 4)) return SMLA_ERR_INVALID_ARG;
   if (seq_lens == ctx_lens || seq_lens == new_lens) return SMLA_ERR_INVALID_ARG;  // other blocks still read the lengths
   if (const int rc = check_ws(workspace, workspace_bytes)) return rc;
-  const int rows_per_block = 2 * kTabThreads;
+  const int rows_per_block = std::max(kTabThreads, (max_new + 2 * num_sms() - 1) / (2 * num_sms()));
   TablesParams p{ctx_lens, new_lens, n_seqs, max_pages, page_tables, free_pages, n_free, max_new, seq_lens, cu_new, positions,
                  slots, row_seq, pages_used, static_cast<uint32_t*>(workspace), rows_per_block};
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(max_new) + rows_per_block - 1) / rows_per_block);
@@ -565,13 +632,12 @@ int smla_cache_append(const smla_paged_cache* cache, const smla_rope* rope, int3
   if (rc) return rc;
   if ((rc = check_rope(rope))) return rc;
   if (rows <= 0 || !slots || !positions || !al(slots, 4) || !al(positions, 4) || !(eps >= 0.0f)) return SMLA_ERR_INVALID_ARG;
-  if (ckv && (!al(ckv, 16) || ckv_stride < kDqk || ckv_stride % 8 || !al(kv_norm, 4))) return SMLA_ERR_INVALID_ARG;
-  if (k_raw && (!al(k_raw, 16) || k_stride < cache->d_idx || k_stride % 8 || !al(idx_norm, 4) || !al(idx_bias, 4) ||
+  if (ckv && (!al(ckv, 16) || ckv_stride < kDqk || ckv_stride % 8 || !al(kv_norm, 16))) return SMLA_ERR_INVALID_ARG;
+  if (k_raw && (!al(k_raw, 16) || k_stride < cache->d_idx || k_stride % 8 || !al(idx_norm, 16) || !al(idx_bias, 16) ||
                 (idx_bias && !idx_norm)))
     return SMLA_ERR_INVALID_ARG;
   if ((rc = check_ws(workspace, workspace_bytes))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
   AppendParams p{};
   p.kv = static_cast<uint8_t*>(const_cast<void*>(cache->kv));
   p.kv_scale = const_cast<float*>(cache->kv_scale);
@@ -588,9 +654,11 @@ int smla_cache_append(const smla_paged_cache* cache, const smla_rope* rope, int3
   p.cos_sin = rope->cos_sin, p.max_pos = rope->max_pos;
   p.kv_inter = rope->kv_interleaved, p.idx_inter = rope->idx_interleaved;
   p.status = static_cast<uint32_t*>(workspace);
+  p.first_reports = rows <= kReportRows;
+  if (!p.first_reports && cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
   const int latent = ckv ? rows : 0;
   const long long warps = latent + (k_raw ? (static_cast<long long>(rows) + 1) / (p.idx_fp8 ? 2 : 4) + 1 : 0);
-  const unsigned blocks = static_cast<unsigned>((warps + kRowThreads / 32 - 1) / (kRowThreads / 32));
+  const unsigned blocks = static_cast<unsigned>((warps + kRowThreads / 32 - 1) / (kRowThreads / 32)) + p.first_reports;
   cache_append_kernel<<<blocks, kRowThreads, 0, st>>>(p, latent);
   return launched();
 }
@@ -610,7 +678,7 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
     if (n_heads != 16 && n_heads != 64) return SMLA_ERR_UNSUPPORTED;
   }
   if (q_raw) {
-    if (!w || !q_idx || !w_out || !al(q_raw, 16) || !al(q_idx, 16) || !al(w, 4) || !al(w_out, 4) || !al(idx_norm, 4) ||
+    if (!w || !q_idx || !w_out || !al(q_raw, 16) || !al(q_idx, 16) || !al(w, 4) || !al(w_out, 4) || !al(idx_norm, 16) ||
         q_raw_stride % 8 || d_idx <= 0 || h_idx <= 0 || q_raw_stride < static_cast<int64_t>(h_idx) * d_idx || !(eps >= 0.0f))
       return SMLA_ERR_INVALID_ARG;
     if (idx_dtype != SMLA_BF16 && idx_dtype != SMLA_FP8_E4M3) return SMLA_ERR_INVALID_ARG;
@@ -619,7 +687,6 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
   }
   if ((rc = check_ws(workspace, workspace_bytes))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
   QueryParams p{};
   p.cos_sin = rope->cos_sin, p.max_pos = rope->max_pos;
   p.kv_inter = rope->kv_interleaved, p.idx_inter = rope->idx_interleaved;
@@ -630,11 +697,13 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
   p.idx_fp8 = idx_dtype == SMLA_FP8_E4M3, p.idx_norm = idx_norm, p.eps = eps;
   p.w = w, p.w_scale = w_scale, p.q_idx = static_cast<uint8_t*>(q_idx), p.w_out = w_out;
   p.status = static_cast<uint32_t*>(workspace);
-  p.pe_units = q_pe ? n_heads / 16 : 0;
-  const int per = p.idx_fp8 ? 8 : 16;
+  p.pe_units = q_pe ? (n_heads + 4 * kSteps - 1) / (4 * kSteps) : 0;
+  const int per = (p.idx_fp8 ? 2 : 4) * kSteps;
   p.units = p.pe_units + (q_raw ? (h_idx + per - 1) / per : 0);
+  p.first_reports = rows <= kReportRows;
+  if (!p.first_reports && cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
   const long long warps = static_cast<long long>(rows) * p.units;
-  const unsigned blocks = static_cast<unsigned>((warps + kRowThreads / 32 - 1) / (kRowThreads / 32));
+  const unsigned blocks = static_cast<unsigned>((warps + kRowThreads / 32 - 1) / (kRowThreads / 32)) + p.first_reports;
   query_prep_kernel<<<blocks, kRowThreads, 0, st>>>(p);
   return launched();
 }

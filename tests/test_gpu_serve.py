@@ -42,7 +42,8 @@ def _random_tables(n, ctx_max, new_max, seed, n_free=None, extra_cols=1):
 
 
 @pytest.mark.parametrize("n,ctx_max,new_max", [(1, 0, 1), (1, 63, 1), (1, 64, 1), (3, 200, 130), (64, 131000, 2), (255, 300, 3),
-                                               (256, 300, 3), (257, 300, 3), (1000, 5000, 70), (2, 100, 9000)])
+                                               (256, 300, 3), (257, 300, 3), (1000, 5000, 70), (2, 100, 9000),
+                                               (1023, 90, 5), (1024, 90, 5), (1025, 90, 5), (3001, 200, 40)])
 def test_tables(n, ctx_max, new_max):
     ctx, new, tables, free = _random_tables(n, ctx_max, new_max, n + ctx_max)
     for max_new in (max(1, int(new.sum())), int(new.sum()) + 777):
@@ -302,6 +303,47 @@ def test_attention_new_tokens_nan_stays_with_those_that_see_it():
     assert out[3::4].isnan().all() and lse[3::4].isnan().all()
 
 
+@pytest.mark.parametrize("scale", [-0.04, 0.0, 1e-6, 0.5])
+def test_attention_softmax_scales(scale):
+    c, tab, sl, qt = sc.attention_case(2, 2, 16, "bf16", 130, [300, 211], seed=14)
+    out, lse = _run_attention(c, tab, sl, 2, qt, 130, scale=scale)
+    ref = sc.attention_reference(c, tab, sl, 2, qt, 130, scale)
+    sc.check_attention(out, lse, ref[:3] + (np.abs(ref[3]),), "bf16")
+
+
+@pytest.mark.parametrize("factor", [1e-25, 1e-12, 1e12])
+def test_attention_per_token_scales_of_any_size(factor):
+    """Scales far outside f16's range, and some that are zero (a row of zeros)."""
+    c, tab, sl, qt = sc.attention_case(2, 1, 16, "fp8", 200, [420, 333], seed=15)
+    live = torch.isfinite(c.kv_scale)
+    c.kv_scale[live] *= factor * (1 + torch.arange(c.kv_scale.numel()).view_as(c.kv_scale) % 7)[live]
+    c.kv_scale[torch.logical_and(live, torch.arange(64)[None] % 5 == 0)] = 0.0
+    scale = sc.SM_SCALE / max(factor, 1.0)
+    out, lse = _run_attention(c, tab, sl, 1, qt, 200, scale=scale)
+    sc.check_attention(out.float() / 1.0, lse, sc.attention_reference(c, tab, sl, 1, qt, 200, scale), "fp8")
+
+
+def test_attention_nan_scale_reaches_only_those_that_see_it():
+    c, tab, sl, qt = sc.attention_case(1, 3, 16, "fp8", 0, [150], seed=16)
+    ref = sc.attention_reference(c, tab, sl, 3, qt, 0, sc.SM_SCALE)
+    c.kv_scale[tab[0, 149 // 64], 149 % 64] = float("nan")
+    out, lse = _run_attention(c, tab, sl, 3, qt, 0)
+    sc.check_attention(out[:2], lse[:2], tuple(a[:2] for a in ref), "fp8")
+    assert out[2].isnan().all() and lse[2].isnan().all()
+
+
+@pytest.mark.parametrize("kv_dtype,what", [("fp8", "query"), ("fp8_ds_mla", "query"), ("fp8_ds_mla", "row")])
+def test_attention_reports_values_outside_f16(kv_dtype, what):
+    c, tab, sl, qt = sc.attention_case(1, 1, 16, kv_dtype, 0, [100], seed=17)
+    if what == "query":
+        qt[0, 3, 5] = 1e5
+    else:
+        c.kv[tab[0, 0], 7, 512:516] = torch.tensor([1e4], dtype=torch.float32).view(torch.uint8)
+        c.kv[tab[0, 0], 7, 0] = 0x7E  # 448
+    _, _, ws = smla.shared_prefix_fwd(c.to("cuda"), tab.cuda(), sl.cuda(), 100, 0, 1, qt.cuda(), sc.SM_SCALE)
+    assert smla.read_status(ws)[0] == 2
+
+
 def test_attention_bad_page_is_skipped_and_reported():
     c, tab, sl, qt = sc.attention_case(2, 1, 64, "bf16", 256, [500, 470], seed=7)
     tab[0, 1], tab[1, 6] = 10 ** 6, -3
@@ -357,3 +399,23 @@ def test_attention_agrees_with_sparse_over_all_keys():
     ref = sc.attention_reference(c, tab, sl, q, qt, shared, sc.SM_SCALE)
     sc.check_attention(out, lse, ref, "bf16")
     sc.check_attention(so, sl_, ref, "bf16")
+
+
+def test_many_rows_report_bad_rows_too():
+    """Past the size up to which one block reports: the same skips, the same status."""
+    rows, c, rope = 5000, sc.empty_cache(80, "bf16", "fp8").to("cuda"), sc.rope_table(10)
+    slots = torch.arange(rows, dtype=torch.int32)
+    slots[4321] = 10 ** 6
+    pos = torch.zeros(rows, dtype=torch.int32)
+    ws = smla.cache_append(c, _cu(slots), _cu(pos), _cu(rope), ckv=_cu(_rows(rows, 576, 1)), k_idx=_cu(_rows(rows, 128, 2)))
+    assert smla.read_status(ws)[0] == 5
+    assert c.kv.cpu().reshape(80 * 64, -1).any(1).sum() == rows - 1
+    pos[77] = 10
+    q = torch.zeros(rows, 16, 576, dtype=torch.bfloat16, device="cuda")
+    pe = torch.ones(rows, 16, 64, dtype=torch.bfloat16, device="cuda")
+    _, _, _, ws = smla.query_prep(_cu(pos), _cu(rope), q_pe=pe, q=q)
+    assert smla.read_status(ws)[0] == 5
+    assert q.any(2).all(1).sum() == rows - 1
+    pos[77] = 9
+    _, _, _, ws = smla.query_prep(_cu(pos), _cu(rope), q_pe=pe, q=q, ws=ws)
+    assert smla.read_status(ws)[0] == 0 and q.any(2).all()

@@ -65,7 +65,7 @@ def _append(L, cache=None, rope=None, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(ckv=None, k=None), INVALID), (dict(rows=0), INVALID), (dict(slots=None), INVALID), (dict(pos=None), INVALID),
     (dict(ckv=FAKE + 8), INVALID), (dict(cs=570), INVALID), (dict(cs=580), INVALID), (dict(ks=120), INVALID),
-    (dict(ks=129), INVALID), (dict(w=None), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
+    (dict(ks=129), INVALID), (dict(w=None), INVALID), (dict(kn=FAKE + 4), INVALID), (dict(b=FAKE + 8), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
     (dict(ws=None), WORKSPACE), (dict(wsb=0), WORKSPACE), (dict(cache=_cache(page_size=32)), UNSUPPORTED),
     (dict(cache=_cache(kv=None)), INVALID), (dict(cache=_cache(kv_scale=None)), INVALID),
     (dict(cache=_cache(k_idx=None)), INVALID), (dict(cache=_cache(d_idx=64)), UNSUPPORTED),
