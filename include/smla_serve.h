@@ -166,11 +166,12 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
  * Keys that a row does not see never reach it, whatever they hold (an unused
  * slot of a page may hold NaN).
  * Supported: n_heads 16 and 64; any q_per_seq >= 1; the three cache formats.
- * Workspace: the returned size (status word, then the partial results of the
- * pieces that the keys are cut into).
+ * Workspace: the returned size (status word, the partial results of the pieces that
+ * the keys are cut into and, for FP8 caches whose shared part is read by more than
+ * 128 query rows, an f16 copy of the shared rows, 1,152 bytes a token).
  * ------------------------------------------------------------------------- */
 size_t smla_shared_prefix_fwd_workspace_size(int32_t n_seqs, int32_t max_seq_len, int32_t shared_len,
-                                             int32_t q_per_seq, int32_t n_heads);
+                                             int32_t q_per_seq, int32_t n_heads, int32_t kv_dtype);
 int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_tables, int32_t max_pages,
                            int32_t n_seqs, const int32_t* seq_lens, int32_t max_seq_len, int32_t shared_len,
                            int32_t q_per_seq, const void* q, int32_t n_heads, float sm_scale, void* out, float* lse,

@@ -127,7 +127,7 @@ _SERVE_SIGS = {
                                          _sz, _vp]),
     "smla_query_prep": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp,
                                        _f32, _vp, _f32, _vp, _vp, _vp, _sz, _vp]),
-    "smla_shared_prefix_fwd_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "smla_shared_prefix_fwd_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
     "smla_shared_prefix_fwd": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _f32, _vp, _vp,
                                               _vp, _sz, _vp]),
 }
@@ -547,8 +547,9 @@ def query_prep(positions, rope, *, q_pe=None, q=None, q_idx_raw=None, w=None, id
     return q, q_idx, w_out, ws
 
 
-def shared_prefix_workspace_bytes(n_seqs, max_seq_len, shared_len, q_per_seq, n_heads) -> int:
-    return lib().smla_shared_prefix_fwd_workspace_size(n_seqs, max_seq_len, shared_len, q_per_seq, n_heads)
+def shared_prefix_workspace_bytes(n_seqs, max_seq_len, shared_len, q_per_seq, n_heads, kv_dtype="bf16") -> int:
+    return lib().smla_shared_prefix_fwd_workspace_size(n_seqs, max_seq_len, shared_len, q_per_seq, n_heads,
+                                                       _dtype_code(kv_dtype))
 
 
 def shared_prefix_fwd(cache, page_tables, seq_lens, max_seq_len, shared_len, q_per_seq, q, sm_scale, *, out=None,
@@ -573,7 +574,8 @@ def shared_prefix_fwd(cache, page_tables, seq_lens, max_seq_len, shared_len, q_p
     else:
         _fp32(lse, rows * H, "lse")
     if ws is None:
-        ws = workspace(shared_prefix_workspace_bytes(n_seqs, max_seq_len, shared_len, q_per_seq, H), q.device)
+        ws = workspace(shared_prefix_workspace_bytes(n_seqs, max_seq_len, shared_len, q_per_seq, H, cache.kv_dtype),
+                       q.device)
     c = make_cache(cache)
     rc = L.smla_shared_prefix_fwd(ctypes.byref(c), page_tables.data_ptr(), max_pages, n_seqs, seq_lens.data_ptr(),
                                   max_seq_len, shared_len, q_per_seq, q.data_ptr(), H, sm_scale, out.data_ptr(),

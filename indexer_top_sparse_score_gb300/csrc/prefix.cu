@@ -24,9 +24,11 @@
 //   KO  own page, the 5 chunks that only QK reads     (1 tile)
 //   KV  own page, the 4 chunks of this CTA's output   (2 tiles)
 //   VO  other page, the 4 chunks of this CTA's output (1 tile)
-// Warp roles: 0 MMA issue, 1 TMA loads of BF16 rows, 4-11 softmax and results (a
-// thread per row and half of the page's keys); FP8 caches: 2-3 and 12-15 load and
-// widen the rows instead of TMA, two warps for each of KO, KV and VO.
+// Warp roles: 0 MMA issue, 1 TMA loads, 4-11 softmax and results (a thread per row
+// and half of the page's keys); FP8 caches: 2-3 and 12-15 load and widen rows, two
+// warps for each of KO, KV and VO. FP8 rows that several row blocks read (the shared
+// part, where there are two row blocks or more) are widened once by widen_kernel and
+// come by TMA like BF16 rows; the widening warps then only pass the tile on.
 // The issue order QK(t + 1), PV(t) keeps the tensor pipe busy during softmax(t).
 //
 // The work is cut evenly: segment after segment on one line (a tile costs 1, a
@@ -85,6 +87,8 @@ struct PrefixParams {
   int32_t n_rb, n_pt; // row blocks and tiles of the shared part (n_rb = 0: nothing shared)
   int32_t rb_s;       // row blocks of one request
   int32_t n_seg, pairs;
+  int32_t wide;       // FP8: the shared rows are read from their f16 copy
+  uint16_t* wide_rows;  // [shared pages * 64][576]
   long long* seg_off; // [i] where own segment i starts on the line
   long long* bounds;  // [pairs + 1] where each pair's stretch starts
   float* part_m;      // [slot][128]
@@ -430,24 +434,31 @@ struct Limits {
   int lo, hi, min_hi, max_hi;
 };
 __device__ __forceinline__ Limits limits(const PrefixParams& p, int s, int row) {
-  Limits m;
-  m.hi = 0, m.min_hi = INT_MAX, m.max_hi = 0;
+  const int lane = threadIdx.x & 31;
   const bool shared = s < p.n_rb;
   const int i = s - p.n_rb, b0 = shared ? 0 : i / p.rb_s;
   const int r0 = (shared ? s : i - b0 * p.rb_s) * kRows;
   const int last = shared ? p.n_rows >> p.hshift : p.q_per_seq;  // tokens of the batch or of the request
+  const int n = kRows >> p.hshift;  // tokens of the block (at most 8): one a lane
+  Limits m;
   m.lo = shared ? 0 : p.shared_len;
-  const int mine = (r0 + row) >> p.hshift;
-  for (int k = r0 >> p.hshift; k < min(last, (r0 + kRows) >> p.hshift); ++k) {
+  const int k = (r0 >> p.hshift) + lane;
+  int hi = 0;
+  if (lane < n && k < last) {
     const int b = shared ? k / p.q_per_seq : b0, j = shared ? k - b * p.q_per_seq : k;
-    int hi = max(0, length_of(p, b) - p.q_per_seq + j + 1);
+    hi = max(0, length_of(p, b) - p.q_per_seq + j + 1);
     if (shared) hi = min(hi, p.shared_len);
-    if (hi > m.lo) {
-      m.min_hi = min(m.min_hi, hi);
-      m.max_hi = max(m.max_hi, hi);
-    }
-    if (k == mine) m.hi = hi;
   }
+  m.min_hi = hi > m.lo ? hi : INT_MAX;
+  m.max_hi = hi > m.lo ? hi : 0;
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1) {
+    m.min_hi = min(m.min_hi, __shfl_xor_sync(0xFFFFFFFFu, m.min_hi, d));
+    m.max_hi = max(m.max_hi, __shfl_xor_sync(0xFFFFFFFFu, m.max_hi, d));
+  }
+  m.min_hi = __shfl_sync(0xFFFFFFFFu, m.min_hi, 0);
+  m.max_hi = __shfl_sync(0xFFFFFFFFu, m.max_hi, 0);
+  m.hi = __shfl_sync(0xFFFFFFFFu, hi, row >> p.hshift);
   return m;
 }
 
@@ -533,7 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
   constexpr bool F16 = FMT != kBf16;  // operand type of the MMAs: one cvt takes two e4m3 codes to f16, exactly
   constexpr uint32_t kFmt = F16 ? kFmtF16 : kFmtBF16;
   constexpr int kThreads = kThreadsOf<FMT>;
-  constexpr uint32_t kFills = FMT == kBf16 ? 1 : 2;  // arrivals that fill a slot group
+  constexpr uint32_t kFills = FMT == kBf16 ? 1 : 3;  // arrivals that fill a slot group: TMA and the widening warps
   extern __shared__ __align__(1024) uint8_t smem[];
   Meta& M = *reinterpret_cast<Meta*>(smem + kOffMeta);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -857,46 +868,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     if (over) set_status(p.status, kStatusOverflow);
   } else if (warp == kTmaWarp) {
     // -------------------------------------------------------------- TMA loads
-    if (FMT == kBf16 && elect_one()) {
+    if (elect_one()) {
       const int v0 = 4 * rank, k0 = 4 * (rank ^ 1);  // first chunk of this CTA's output values, of the others
       Tiles cur;
       cur.line = line;
       bool more = cur.next(p, rank, true);
-      int last_other = 0;
-      // a page that is missing reads as zeros: a box wholly before the pool
-      auto y = [](int page) { return page >= 0 ? page * kPage : -kPage; };
-      auto load_vo = [&](uint32_t h, int page) {
+      // where a page's rows lie in the map: pool rows, or (FP8) rows of the shared part's
+      // copy; -64 for a page that is missing: a box wholly before the rows reads as zeros
+      auto place = [&](int id, int i) {
+        if (FMT != kBf16) return id != Tiles::kNoPage ? (cur.first_page + 2 * cur.t + i) * kPage : -kPage;
+        const int page = Tiles::pool_page(p, id);
+        return page >= 0 ? page * kPage : -kPage;
+      };
+      auto load_vo = [&](uint32_t h, bool by_tma, int y) {
         if (h > 0 && !wait_one<false>(&M.vo_free, (h - 1) & 1, abort_v)) return false;
-        mbar_arrive_expect_tx(&M.vo_full, 4 * kChunk + kQChunk);  // V of the other page and its P
-        tma_chunks(smem + kOffVO, &kv_map, &M.vo_full, y(page), v0);
+        if (FMT != kBf16 && !by_tma) {
+          mbar_arrive(&M.vo_full);
+          return true;
+        }
+        // V of the other page and (BF16; else a widening warp expects it) its P
+        mbar_arrive_expect_tx(&M.vo_full, 4 * kChunk + (FMT == kBf16 ? kQChunk : 0));
+        tma_chunks(smem + kOffVO, &kv_map, &M.vo_full, y, v0);
         return true;
       };
       uint32_t g = 0;
-      bool ok = true;
+      bool ok = true, last_tma = false;
+      int last_y = 0;
       for (; more && ok; ++g) {
-        const int own = Tiles::pool_page(p, cur.own_id), other = Tiles::pool_page(p, cur.other_id);
-        if (cur.bad(p)) set_status(p.status, kStatusBounds);
+        const bool by_tma = FMT == kBf16 || (p.wide && cur.pc.s < p.n_rb);
+        const int y = place(cur.own_id, rank), other_y = place(cur.other_id, rank ^ 1);
+        if (FMT == kBf16 && cur.bad(p)) set_status(p.status, kStatusBounds);
         more = cur.next(p, rank, false);
         if (g > 0 && !wait_one<false>(&M.ko_free, (g - 1) & 1, abort_v)) { ok = false; break; }
-        mbar_arrive_expect_tx(&M.ko_full, 5 * kChunk);
-        tma_chunks(smem + kOffKO, &kv_map, &M.ko_full, y(own), k0);
-        tma_chunks(smem + kOffKO + 4 * kChunk, &rope_map, &M.ko_full, y(own), 8);
+        if (by_tma) {
+          mbar_arrive_expect_tx(&M.ko_full, 5 * kChunk);
+          tma_chunks(smem + kOffKO, &kv_map, &M.ko_full, y, k0);
+          tma_chunks(smem + kOffKO + 4 * kChunk, &rope_map, &M.ko_full, y, 8);
+        } else {
+          mbar_arrive(&M.ko_full);
+        }
         const int buf = g & 1;
         if (g > 1 && !wait_one<false>(&M.kv_free[buf], ((g >> 1) - 1) & 1, abort_v)) { ok = false; break; }
-        mbar_arrive_expect_tx(&M.kv_full[buf], 4 * kChunk);
-        tma_chunks(smem + kOffKV + 4 * buf * kChunk, &kv_map, &M.kv_full[buf], y(own), v0);
-        if (more) {  // the next tile's own page into L2
-          const int next = Tiles::pool_page(p, cur.own_id);
+        if (by_tma) {
+          mbar_arrive_expect_tx(&M.kv_full[buf], 4 * kChunk);
+          tma_chunks(smem + kOffKV + 4 * buf * kChunk, &kv_map, &M.kv_full[buf], y, v0);
+        } else {
+          mbar_arrive(&M.kv_full[buf]);
+        }
+        if (more && (FMT == kBf16 || (p.wide && cur.pc.s < p.n_rb))) {  // the next tile's own page into L2
+          const int next = place(cur.own_id, rank);
           if (next >= 0) {
-            prefetch_chunks(&kv_map, y(next), k0);
-            prefetch_chunks(&rope_map, y(next), 8);
-            prefetch_chunks(&kv_map, y(next), v0);
+            prefetch_chunks(&kv_map, next, k0);
+            prefetch_chunks(&rope_map, next, 8);
+            prefetch_chunks(&kv_map, next, v0);
           }
         }
-        if (g > 0) ok = load_vo(g - 1, last_other);
-        last_other = other;
+        if (g > 0) ok = load_vo(g - 1, last_tma, last_y);
+        last_tma = by_tma;
+        last_y = other_y;
       }
-      if (g > 0 && ok) load_vo(g - 1, last_other);
+      if (g > 0 && ok) load_vo(g - 1, last_tma, last_y);
     }
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------- MMA issue
@@ -1064,24 +1095,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     Tiles cur;
     cur.line = line;
     bool more = cur.next(p, rank, true);
-    if (more) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
+    auto mine = [&] { return !(p.wide && cur.pc.s < p.n_rb); };  // not a tile of the copy
+    bool here = more && mine();
+    if (here) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
     for (uint32_t g = 0; more; ++g) {
-      if (group == 0 && cur.bad(p) && lane == 0) set_status(p.status, kStatusBounds);
+      const bool stores = here;
+      if (stores && group == 0 && cur.bad(p) && lane == 0) set_status(p.status, kStatusBounds);
       more = cur.next(p, rank, false);
+      here = more && mine();
       // the slots' previous tile: g - 1, or g - 2 for KV's two buffers
       const uint32_t back = group == 1 ? 2 : 1;
       if (g >= back) {
         uint64_t* bar = group == 0 ? &M.ko_free : group == 1 ? &M.kv_free[g & 1] : &M.vo_free;
         if (!wait_warp<false>(bar, group == 1 ? ((g >> 1) - 1) & 1 : (g - 1) & 1, abort_v)) break;
       }
-      store(group == 0 ? kOffKO : group == 1 ? kOffKV + static_cast<int>(g & 1) * 4 * kChunk : kOffVO);
-      fence_proxy_async_smem();
+      if (stores) {
+        store(group == 0 ? kOffKO : group == 1 ? kOffKV + static_cast<int>(g & 1) * 4 * kChunk : kOffVO);
+        fence_proxy_async_smem();
+      }
       __syncwarp();
       if (lane == 0) {
         if (cw == 4) mbar_arrive_expect_tx(&M.vo_full, kQChunk);  // and the other page's P
         else mbar_arrive(group == 0 ? &M.ko_full : group == 1 ? &M.kv_full[g & 1] : &M.vo_full);
       }
-      if (more) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
+      if (here) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
     }
     if (over || top > 65504.0f) set_status(p.status, kStatusOverflow);
   }
@@ -1099,6 +1136,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// ------------------------------------------------------------------ the shared rows, widened
+// f16 rows of the shared pages in logical order: per-token codes exactly, tile-scaled
+// values (code * scale) rounded (off by at most 2^-11 of the value). One block a page:
+// reads 37 or 42 KB, writes 74 KB, bound by memory. Each row block of the batch would
+// widen them again otherwise (64x2 on a 16K prompt, FP8: 64 times, 329 us against
+// 243 with the copy).
+template <int FMT>
+__global__ void __launch_bounds__(256) widen_kernel(const PrefixParams p) {
+  constexpr int kRowBytes = FMT == kTokenFp8 ? kDqk : kTileRowBytes;
+  constexpr int kPieces = FMT == kTokenFp8 ? kDqk / 16 : kDv / 16 + 8;  // 16 codes each, then (tile-scaled) 8 rope values
+  const int id = p.page_tables[blockIdx.x];
+  const bool live = id >= 0 && id < p.num_pages;
+  if (!live && threadIdx.x == 0) set_status(p.status, kStatusBounds);
+  const uint8_t* src = p.kv + static_cast<long long>(live ? id : 0) * kPage * kRowBytes;
+  uint16_t* dst = p.wide_rows + static_cast<long long>(blockIdx.x) * kPage * kDqk;
+  bool over = false;
+  float top = 0.0f;
+#pragma unroll 4
+  for (int u = threadIdx.x; u < kPage * kPieces; u += 256) {
+    const int r = u / kPieces, j = u - r * kPieces;
+    const uint8_t* row = src + r * kRowBytes;
+    uint16_t* out = dst + r * kDqk;
+    if (FMT == kTileFp8 && j >= kDv / 16) {
+      const int i = j - kDv / 16;
+      const uint4 w = live ? __ldg(reinterpret_cast<const uint4*>(row + kTileRope + 16 * i)) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(out + kDv + 8 * i) = make_uint4(to_f16(w.x, over), to_f16(w.y, over), to_f16(w.z, over), to_f16(w.w, over));
+      continue;
+    }
+    const uint4 c = live ? __ldg(reinterpret_cast<const uint4*>(row + 16 * j)) : make_uint4(0, 0, 0, 0);
+    const float s = FMT == kTileFp8 && live ? __ldg(reinterpret_cast<const float*>(row + kDv) + (j >> 3)) : 1.0f;
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      o[k] = e4m3x2(static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1))));
+      if (FMT == kTileFp8) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
+        top = fmaxf(top, fmaxf(fabsf(f.x * s), fabsf(f.y * s)));
+        o[k] = pack2(f.x * s, f.y * s, true);
+      }
+    }
+    *reinterpret_cast<uint4*>(out + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(out + 16 * j + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  if (over || top > 65504.0f) set_status(p.status, kStatusOverflow);
 }
 
 // ------------------------------------------------------------------ joining the pieces
@@ -1289,7 +1373,7 @@ bool plan(PrefixParams& p) {
   return true;
 }
 
-size_t layout(PrefixParams& p, uint8_t* ws) {
+size_t layout(PrefixParams& p, uint8_t* ws, int32_t kv_dtype) {
   const size_t slots = static_cast<size_t>(p.n_seg) + p.pairs;
   size_t at = kStatusBytes;
   p.bounds = reinterpret_cast<long long*>(ws + at);
@@ -1301,7 +1385,13 @@ size_t layout(PrefixParams& p, uint8_t* ws) {
   p.part_l = reinterpret_cast<float*>(ws + at);
   at += slots * 4 * kRows * 4;
   p.part_o = reinterpret_cast<float4*>(ws + at);
-  return at + slots * 2 * 64 * kRows * 16;
+  at += slots * 2 * 64 * kRows * 16;
+  p.wide = kv_dtype != SMLA_BF16 && p.n_rb >= 2;
+  if (p.wide) {
+    p.wide_rows = reinterpret_cast<uint16_t*>(ws + at);
+    at += static_cast<size_t>((p.shared_len + kPage - 1) / kPage) * kPage * kDqk * 2;
+  }
+  return at;
 }
 
 }  // namespace
@@ -1312,12 +1402,12 @@ using namespace smla;
 extern "C" {
 
 size_t smla_shared_prefix_fwd_workspace_size(int32_t n_seqs, int32_t max_seq_len, int32_t shared_len,
-                                             int32_t q_per_seq, int32_t n_heads) {
+                                             int32_t q_per_seq, int32_t n_heads, int32_t kv_dtype) {
   if (n_seqs <= 0 || q_per_seq <= 0 || max_seq_len <= 0 || shared_len < 0 || (n_heads != 16 && n_heads != 64)) return kStatusBytes;
   PrefixParams p{};
   p.n_seqs = n_seqs, p.q_per_seq = q_per_seq, p.shared_len = shared_len, p.hshift = n_heads == 64 ? 6 : 4;
   if (!plan(p)) return kStatusBytes;
-  return layout(p, nullptr);
+  return layout(p, nullptr, kv_dtype);
 }
 
 int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_tables, int32_t max_pages,
@@ -1337,7 +1427,7 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
   PrefixParams p{};
   p.n_seqs = n_seqs, p.q_per_seq = q_per_seq, p.shared_len = shared_len, p.hshift = n_heads == 64 ? 6 : 4;
   if (!plan(p)) return SMLA_ERR_UNSUPPORTED;
-  if (!workspace || !al(workspace, 16) || workspace_bytes < layout(p, static_cast<uint8_t*>(workspace))) return SMLA_ERR_WORKSPACE;
+  if (!workspace || !al(workspace, 16) || workspace_bytes < layout(p, static_cast<uint8_t*>(workspace), cache->kv_dtype)) return SMLA_ERR_WORKSPACE;
   p.kv = static_cast<const uint8_t*>(cache->kv), p.kv_scale = cache->kv_scale, p.num_pages = cache->num_pages;
   p.page_tables = page_tables, p.max_pages = max_pages, p.seq_lens = seq_lens, p.max_seq_len = max_seq_len;
   p.q = static_cast<const uint16_t*>(q);
@@ -1349,12 +1439,20 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
   CUtensorMap map{}, rope{};
-  if (cache->kv_dtype == SMLA_BF16) {
-    const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * kPage;
-    if (!encode_chunks(&map, cache->kv, rows, kDqk, 4) || !encode_chunks(&rope, cache->kv, rows, kDqk, 1)) return SMLA_ERR_CUDA;
-    return launch<kBf16>(map, rope, p, st);
+  const bool bf16 = cache->kv_dtype == SMLA_BF16, token = cache->kv_dtype == SMLA_FP8_E4M3;
+  if (bf16 || p.wide) {  // (16-bit values of either type)
+    const int pages = (p.shared_len + kPage - 1) / kPage;
+    const void* base = bf16 ? cache->kv : p.wide_rows;
+    const uint64_t rows = static_cast<uint64_t>(bf16 ? cache->num_pages : pages) * kPage;
+    if (!encode_chunks(&map, base, rows, kDqk, 4) || !encode_chunks(&rope, base, rows, kDqk, 1)) return SMLA_ERR_CUDA;
+    if (!bf16) {
+      if (token) widen_kernel<kTokenFp8><<<pages, 256, 0, st>>>(p);
+      else widen_kernel<kTileFp8><<<pages, 256, 0, st>>>(p);
+      if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
+    }
   }
-  return cache->kv_dtype == SMLA_FP8_E4M3 ? launch<kTokenFp8>(map, rope, p, st) : launch<kTileFp8>(map, rope, p, st);
+  if (bf16) return launch<kBf16>(map, rope, p, st);
+  return token ? launch<kTokenFp8>(map, rope, p, st) : launch<kTileFp8>(map, rope, p, st);
 }
 
 }  // extern "C"

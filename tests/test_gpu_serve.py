@@ -344,11 +344,14 @@ def test_attention_reports_values_outside_f16(kv_dtype, what):
     assert smla.read_status(ws)[0] == 2
 
 
-def test_attention_bad_page_is_skipped_and_reported():
-    c, tab, sl, qt = sc.attention_case(2, 1, 64, "bf16", 256, [500, 470], seed=7)
-    tab[0, 1], tab[1, 6] = 10 ** 6, -3
-    out, lse = _run_attention(c, tab, sl, 1, qt, 256, status=5)
-    sc.check_attention(out, lse, sc.attention_reference(c, tab, sl, 1, qt, 256, sc.SM_SCALE), "bf16")
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8", "fp8_ds_mla"])
+@pytest.mark.parametrize("q", [1, 2])
+def test_attention_bad_page_is_skipped_and_reported(kv_dtype, q):
+    for bad in ((0, 1), (1, 6)):  # in the shared part; in a request's own
+        c, tab, sl, qt = sc.attention_case(2, q, 64, kv_dtype, 256, [500, 470], seed=7)
+        tab[bad] = 10 ** 6 if q == 1 else -3
+        out, lse = _run_attention(c, tab, sl, q, qt, 256, status=5)
+        sc.check_attention(out, lse, sc.attention_reference(c, tab, sl, q, qt, 256, sc.SM_SCALE), kv_dtype)
 
 
 def test_attention_length_above_its_bound_is_reported():

@@ -96,7 +96,7 @@ def _attention(L, cache=None, **kw):
     a = dict(pt=FAKE, mp=40, n=3, lens=FAKE, mx=2500, sh=1000, q=2, qp=FAKE, h=64, sm=0.04, out=FAKE, lse=FAKE, ws=FAKE, wsb=None)
     a.update(kw)
     if a["wsb"] is None:
-        a["wsb"] = L.smla_shared_prefix_fwd_workspace_size(a["n"], a["mx"], a["sh"], a["q"], a["h"])
+        a["wsb"] = L.smla_shared_prefix_fwd_workspace_size(a["n"], a["mx"], a["sh"], a["q"], a["h"], 1)
     return L.smla_shared_prefix_fwd(ctypes.byref(cache or _cache()), *a.values(), None)
 
 
@@ -109,6 +109,18 @@ def _attention(L, cache=None, **kw):
     (dict(cache=_cache(kv_dtype=9)), INVALID), (dict(cache=_cache(page_size=16)), UNSUPPORTED)])
 def test_attention_refusals(L, kw, code):
     assert _attention(L, **kw) == code
+
+
+def test_attention_workspace_holds_the_wide_copy(L):
+    size = lambda *a: L.smla_shared_prefix_fwd_workspace_size(*a)  # noqa: E731
+    # 3 x 2 tokens x 64 heads = 3 row blocks share 1,000 tokens (16 pages of 64 rows of 1,152 bytes)
+    for fp8 in (smla.SMLA_FP8_E4M3, smla.SMLA_FP8_DS_MLA):
+        assert size(3, 2500, 1000, 2, 64, fp8) == size(3, 2500, 1000, 2, 64, smla.SMLA_BF16) + 16 * 64 * 1152
+        # one row block, or one request (nothing is shared), has none
+        assert size(2, 2500, 1000, 1, 64, fp8) == size(2, 2500, 1000, 1, 64, smla.SMLA_BF16)
+        assert size(1, 2500, 1000, 9, 64, fp8) == size(1, 2500, 1000, 9, 64, smla.SMLA_BF16)
+    need = size(3, 2500, 1000, 2, 64, smla.SMLA_FP8_E4M3)
+    assert _attention(L, wsb=need - 1) == WORKSPACE
 
 
 def test_binding_refuses_wrong_tensors(L):
