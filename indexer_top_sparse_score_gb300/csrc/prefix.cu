@@ -31,10 +31,11 @@
 // come by TMA like BF16 rows; the widening warps then only pass the tile on.
 // The issue order QK(t + 1), PV(t) keeps the tensor pipe busy during softmax(t).
 //
-// The work is cut evenly: segment after segment on one line (a tile costs 1, a
-// segment's start kOverhead more), and pair i of P walks the i-th of P equal
-// stretches. A segment that is cut leaves several partial results (fp32 O with
-// its maximum and sums) that merge_kernel joins; no pair waits for another.
+// The work is cut evenly: segment after segment on one line (each tile and each
+// segment's start has a cost), and pair i of P walks the i-th of P equal stretches.
+// A segment that is cut leaves several partial results (fp32 O with its maximum
+// and sums) that merge_kernel joins; no pair waits for another. Rows whose keys are
+// one uncut segment get their results at once.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -51,12 +52,19 @@ namespace smla {
 namespace {
 
 constexpr int kRows = 128;       // rows of a block (MMA M)
-constexpr int kOverhead = 6;     // cost of starting a segment (Q in, results out), in tiles
+// Costs on the line of work, in quarters of a tile that comes by TMA (2,900 cycles
+// with BF16 rows, 3,100 to 3,900 with the f16 copy). Measured per CTA: starting a
+// segment (Q in, results out) 14,000 cycles with BF16 rows, 25,000 with FP8 ones; a
+// tile that is widened on the way 5,500 (per-token scales) and 7,800 (tile scales).
+// With equal weights the pairs that walk short segments end last: 64x2 on a 16K
+// prompt, FP8, at 345 us while the others end at 238.
+struct Costs {
+  int32_t start, shared_tile, own_tile;
+};
 constexpr int kChunk = 64 * 128; // 64 keys x 64 values
 constexpr int kQChunk = kRows * 128;
 // Q chunks follow the key slots they meet (KO 0-4, KV 0-3, below): those of KO 0-3
 // and KV 0-1 are in tensor memory, those of KO 4 and KV 2-3 in shared memory.
-constexpr int kQTmemChunks = 6;
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 constexpr int kOffQ = 0, kOffKO = 3 * kQChunk, kOffKV = kOffKO + 5 * kChunk, kOffVO = kOffKV + 8 * kChunk,
               kOffP = kOffVO + 4 * kChunk, kOffMeta = kOffP + 2 * kQChunk;
@@ -87,6 +95,7 @@ struct PrefixParams {
   int32_t n_rb, n_pt; // row blocks and tiles of the shared part (n_rb = 0: nothing shared)
   int32_t rb_s;       // row blocks of one request
   int32_t n_seg, pairs;
+  Costs costs;
   int32_t wide;       // FP8: the shared rows are read from their f16 copy
   uint16_t* wide_rows;  // [shared pages * 64][576]
   long long* seg_off; // [i] where own segment i starts on the line
@@ -114,7 +123,17 @@ __device__ __forceinline__ int own_tiles(const PrefixParams& p, int i) {
 __device__ __forceinline__ int seg_tiles(const PrefixParams& p, int s) {
   return s < p.n_rb ? p.n_pt : own_tiles(p, s - p.n_rb);
 }
-__device__ __forceinline__ int seg_cost(int tiles) { return tiles > 0 ? tiles + kOverhead : 0; }
+__device__ __forceinline__ int seg_cost(const PrefixParams& p, int s, int tiles) {
+  return tiles > 0 ? p.costs.start + tiles * (s < p.n_rb ? p.costs.shared_tile : p.costs.own_tile) : 0;
+}
+// Tiles [t0, t1) of segment s, which starts at a, that begin inside the stretch [x, y).
+__device__ __forceinline__ void stretch_tiles(const PrefixParams& p, int s, int tiles, long long a, long long x, long long y, int& t0,
+                                              int& t1) {
+  const int one = s < p.n_rb ? p.costs.shared_tile : p.costs.own_tile;
+  const long long from = a + p.costs.start;
+  t0 = static_cast<int>((max(x - from, 0LL) + one - 1) / one);
+  t1 = static_cast<int>(min((max(y - from, 0LL) + one - 1) / one, static_cast<long long>(tiles)));
+}
 
 struct Line {  // a pair's stretch [x, y) and where it stands: segment s starts at a
   long long x, y, a;
@@ -122,21 +141,21 @@ struct Line {  // a pair's stretch [x, y) and where it stands: segment s starts 
 };
 struct Piece {
   int s, t0, t1;  // tiles [t0, t1) of segment s
+  bool whole;     // all of them
 };
 
 __device__ __forceinline__ bool piece_after(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
   while (L.s < p.n_seg && L.a < L.y) {
-    const int tiles = seg_tiles(p, L.s), cost = seg_cost(tiles);
     const int s = L.s++;
+    const int tiles = seg_tiles(p, s), cost = seg_cost(p, s, tiles);
     const long long a = L.a;
     if (cost == 0) continue;
     if (writer && s >= p.n_rb && a >= L.x) p.seg_off[s - p.n_rb] = a;
     L.a += cost;
-    const long long t0 = max(L.x - a - kOverhead, 0LL), t1 = min(L.y - a - kOverhead, static_cast<long long>(tiles));
-    if (t1 > t0) {
+    stretch_tiles(p, s, tiles, a, L.x, L.y, pc.t0, pc.t1);
+    if (pc.t1 > pc.t0) {
       pc.s = s;
-      pc.t0 = static_cast<int>(t0);
-      pc.t1 = static_cast<int>(t1);
+      pc.whole = pc.t0 == 0 && pc.t1 == tiles;
       return true;
     }
   }
@@ -583,9 +602,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
   Line line;
   {
     const int n_own = p.n_seg - p.n_rb;
-    const long long shared_cost = static_cast<long long>(p.n_rb) * seg_cost(p.n_pt);
+    const long long shared_cost = static_cast<long long>(p.n_rb) * seg_cost(p, 0, p.n_pt);
     long long sum = 0;
-    for (int i = tid; i < n_own; i += kThreads) sum += seg_cost(own_tiles(p, i));
+    for (int i = tid; i < n_own; i += kThreads) sum += seg_cost(p, p.n_rb + i, own_tiles(p, i));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     if (lane == 0) M.scan[warp] = sum;
@@ -604,14 +623,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     if (line.x < line.y) {
       if (line.x < shared_cost) {
         if (tid == 0) {
-          M.start_s = static_cast<int>(line.x / seg_cost(p.n_pt));
-          M.start_a = static_cast<long long>(M.start_s) * seg_cost(p.n_pt);
+          M.start_s = static_cast<int>(line.x / seg_cost(p, 0, p.n_pt));
+          M.start_a = static_cast<long long>(M.start_s) * seg_cost(p, 0, p.n_pt);
         }
       } else {
         long long before = shared_cost;
         for (int c0 = 0; c0 < n_own && before <= line.x; c0 += kThreads) {
           const int i = c0 + tid;
-          const long long cost = i < n_own ? seg_cost(own_tiles(p, i)) : 0;
+          const long long cost = i < n_own ? seg_cost(p, p.n_rb + i, own_tiles(p, i)) : 0;
           long long v = cost;
 #pragma unroll
           for (int d = 1; d < 32; d <<= 1) {
@@ -676,10 +695,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     if (FMT == kTokenFp8 && more) scale = load_scale();
     int own_next = more ? Tiles::pool_page(p, cur.own_id) : -1;
     if (more) more = cur.next(p, rank, false);
-    uint32_t g = 0;
+    uint32_t g = 0, sent = 0;  // tiles; exchanges between the warps of a row
     bool ok = true;
     Limits lim;
     float m = 0.0f, l = 0.0f;
+    // A value of a row from each of the four warps that hold the row (both halves,
+    // both CTAs; own CTA's first), in the same order everywhere but for the CTA.
+    auto exchange = [&](float value, float4& got) {
+      const uint32_t par = sent & 1, bar = (par * 4 + quad) * 8;
+      send_float(self_mx + ((par * 4 + half) * kRows + row) * 4, value, self_mxbar + bar);
+      send_float(peer_mx + ((par * 4 + 2 + half) * kRows + row) * 4, value, peer_mxbar + bar);
+      if (half == 0 && lane == 0) mbar_arrive_expect_tx(&M.mx_full[par][quad], 4 * 32 * 4);
+      if (!wait_warp<true>(&M.mx_full[par][quad], (sent >> 1) & 1, abort_v)) return false;
+      ++sent;
+      const volatile float* v = &M.mx[par][0][row];
+      got = make_float4(v[0], v[kRows], v[2 * kRows], v[3 * kRows]);
+      return true;
+    };
     while (ok) {
       // the next piece's Q while the last product of this one runs, then this one's results
       if (have) {
@@ -689,23 +721,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       if (started) {
         if (!wait_warp<true>(&M.pv_done, (g - 1) & 1, abort_v)) break;
         tc_fence_after();
-        const int slot = pc.s + pair;
-        float4* o = p.part_o + ((static_cast<long long>(slot) * 2 + rank) * 64 + half * 32) * kRows + row;
+        // a row that sees none of the segment's keys took part in the unmasked tiles: dropped here
+        if (lim.hi <= lim.lo) l = 0.0f;
+        const bool whole = pc.whole && p.n_rb == 0;  // no other piece has keys of these rows: their results
+        if (whole) {
+          float4 of;
+          if (!exchange(l, of)) break;
+          // summed in the same order by both CTAs
+          const float sum = rank == 0 ? (of.x + of.y) + (of.z + of.w) : (of.z + of.w) + (of.x + of.y);
+          const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+          const int i = pc.s, b = i / p.rb_s, r = (i - b * p.rb_s) * kRows + row;
+          const bool exists = r < p.q_per_seq << p.hshift;
+          const long long flat = (static_cast<long long>(b) * p.q_per_seq << p.hshift) + r;
+          uint16_t* o = p.out + flat * kDv + 256 * rank + 128 * half;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld_32x32b_x32(tmem + lanes + kColO + 128 * half + 32 * c, reinterpret_cast<uint32_t*>(v));
-          tmem_wait_ld();
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld_32x32b_x32(tmem + lanes + kColO + 128 * half + 32 * c, reinterpret_cast<uint32_t*>(v));
+            tmem_wait_ld();
+            if (exists) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[(8 * c + j) * kRows] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  w[k] = sum != 0.0f ? pack2(v[8 * j + 2 * k] * inv, v[8 * j + 2 * k + 1] * inv, false) : 0u;
+                *reinterpret_cast<uint4*>(o + 32 * c + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+          if (exists && rank == 0 && half == 0 && p.lse) p.lse[flat] = sum != 0.0f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        } else {
+          const int slot = pc.s + pair;
+          float4* o = p.part_o + ((static_cast<long long>(slot) * 2 + rank) * 64 + half * 32) * kRows + row;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld_32x32b_x32(tmem + lanes + kColO + 128 * half + 32 * c, reinterpret_cast<uint32_t*>(v));
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[(8 * c + j) * kRows] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          }
+          if (rank == 0 && half == 0) p.part_m[static_cast<long long>(slot) * kRows + row] = m;
+          p.part_l[(static_cast<long long>(slot) * 4 + 2 * rank + half) * kRows + row] = l;
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&M.o_free);
-        // a row that sees none of the segment's keys took part in the unmasked tiles: dropped here
-        if (lim.hi <= lim.lo) l = 0.0f;
-        if (rank == 0 && half == 0) p.part_m[static_cast<long long>(slot) * kRows + row] = m;
-        p.part_l[(static_cast<long long>(slot) * 4 + 2 * rank + half) * kRows + row] = l;
       }
       if (!have) break;
       started = true;
@@ -737,8 +799,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
           __syncwarp();
           float* k = &M.ks[sw][lane >> 1].x + (lane & 1);
           k[0] = sc * p.scale_log2;
-          k[2] = log2f(sc);
-          M.rs[sw][lane] = sc == sc ? 1.0f / sc : 1.0f;
+          k[2] = __log2f(sc);  // off by 2^-22 at most: so is P, which is rounded to 2^-11 next
+          M.rs[sw][lane] = sc == sc ? __fdividef(1.0f, sc) : 1.0f;
           __syncwarp();
           if (more) scale = load_scale();
         }
@@ -775,16 +837,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         if (FMT != kTokenFp8) mine *= p.scale_log2;
         // the row's maximum over both halves of both pages, which all scale P by the
         // same reference: every warp sends its rows' to both CTAs
-        const uint32_t par = g & 1, bar = (par * 4 + quad) * 8;
-        send_float(self_mx + ((par * 4 + half) * kRows + row) * 4, mine, self_mxbar + bar);
-        send_float(peer_mx + ((par * 4 + 2 + half) * kRows + row) * 4, mine, peer_mxbar + bar);
-        if (half == 0 && lane == 0) mbar_arrive_expect_tx(&M.mx_full[par][quad], 4 * 32 * 4);
-        if (!wait_warp<true>(&M.mx_full[par][quad], (g >> 1) & 1, abort_v)) {
+        float4 of;
+        if (!exchange(mine, of)) {
           ok = false;
           break;
         }
-        const volatile float* mx = &M.mx[par][0][row];
-        const float top = fmaxf(fmaxf(mx[0], mx[kRows]), fmaxf(mx[2 * kRows], mx[3 * kRows]));
+        const float top = fmaxf(fmaxf(of.x, of.y), fmaxf(of.z, of.w));
         const bool raise = top > m + kRaise || (m == -INFINITY && top > -INFINITY);
         float alpha = 1.0f;
         if (raise) {
@@ -1189,7 +1247,7 @@ __global__ void __launch_bounds__(256) widen_kernel(const PrefixParams p) {
 // A block joins 128 output values of 16 rows (one token's heads or part of them):
 // the pieces of the rows' shared segment and of their own one, weighted by
 // 2^(m - largest m). Reading fp32 partials that were just written, it is bound by
-// L2 and, for few rows, by latency: four blocks share a row's values, and each
+// L2 and, for few rows, by latency: up to four blocks share a row's values, and each
 // thread keeps eight 16-byte loads in flight.
 __device__ __forceinline__ float piece_sum(const PrefixParams& p, int slot, int at) {
   const float* l = p.part_l + static_cast<long long>(slot) * 4 * kRows + at;
@@ -1206,7 +1264,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
   __shared__ int s_n;
   const int tid = threadIdx.x, lane = tid & 31;
   const int r0 = blockIdx.x * kMergeRows;
-  const int cols = blockIdx.y * kMergeCols;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
   if (tid < 32) {
     int n = 0;
@@ -1221,11 +1278,12 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
       }
       const int tiles = seg_tiles(p, s);
       if (tiles == 0) continue;
-      const long long a = part == 1 ? p.seg_off[s - p.n_rb] : static_cast<long long>(s) * seg_cost(p.n_pt);
-      const long long t0 = a + kOverhead, t1 = t0 + tiles;
+      const long long a = part == 1 ? p.seg_off[s - p.n_rb] : static_cast<long long>(s) * seg_cost(p, 0, p.n_pt);
       for (int base = 0; base < p.pairs; base += 32) {
         const int q = base + lane;
-        const bool in = q < p.pairs && max(p.bounds[q], t0) < min(p.bounds[q + 1], t1);
+        int t0 = 0, t1 = 0;
+        if (q < p.pairs) stretch_tiles(p, s, tiles, a, p.bounds[q], p.bounds[q + 1], t0, t1);
+        const bool in = t1 > t0;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, in);
         const int at_n = n + __popc(mask & ((1u << lane) - 1));
         if (in && at_n < kMaxPieces) slots[at_n] = (s + q) * kRows + at;
@@ -1236,6 +1294,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
   }
   __syncthreads();
   const int n = s_n;
+  if (n == 1 && p.n_rb == 0) return;  // one piece that walked all of the rows' keys: it wrote the results itself
   {  // 16 threads per row
     const int row = tid >> 4, k = tid & 15;
     float top = -INFINITY;
@@ -1261,43 +1320,47 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
     for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     if (k == 0) {
       inv[row] = sum != 0.0f ? 1.0f / sum : 0.0f;
-      if (p.lse && cols == 0) p.lse[r0 + row] = sum != 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      if (p.lse && blockIdx.y == 0) p.lse[r0 + row] = sum != 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     }
   }
   __syncthreads();
-  const int row = tid & 15, c0 = tid >> 4;  // two groups of four values: c0 and c0 + 16 of the block's 32
-  float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
-  const float4* part = p.part_o + static_cast<long long>(cols / 4 + c0) * kRows + row;
-  for (int i0 = 0; i0 < n; i0 += 4) {
-    float4 v[4][2];
-    float w[4];
+  const int row = tid & 15, c0 = tid >> 4;  // two groups of four values: c0 and c0 + 16 of the 32
+#pragma unroll 1
+  for (int cols = blockIdx.y * kMergeCols; cols < kDv; cols += gridDim.y * kMergeCols) {
+    float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+    const float4* part = p.part_o + static_cast<long long>(cols / 4 + c0) * kRows + row;
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      float4 v[4][2];
+      float w[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      w[u] = i0 + u < n ? wgt[i0 + u][row] : -1.0f;
-      if (w[u] != -1.0f) {
-        const int slot = slots[i0 + u] / kRows, at = slots[i0 + u] % kRows;
-        const float4* src = part + static_cast<long long>(slot) * 2 * 64 * kRows + at;
-        v[u][0] = src[0];
-        v[u][1] = src[16 * kRows];
+      for (int u = 0; u < 4; ++u) {
+        w[u] = i0 + u < n ? wgt[i0 + u][row] : -1.0f;
+        if (w[u] != -1.0f) {
+          const int slot = slots[i0 + u] / kRows, at = slots[i0 + u] % kRows;
+          const float4* src = part + static_cast<long long>(slot) * 2 * 64 * kRows + at;
+          v[u][0] = src[0];
+          v[u][1] = src[16 * kRows];
+        }
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (w[u] != -1.0f) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[j].x += w[u] * v[u][j].x, acc[j].y += w[u] * v[u][j].y, acc[j].z += w[u] * v[u][j].z, acc[j].w += w[u] * v[u][j].w;
+        }
     }
+    const float f = inv[row];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (w[u] != -1.0f) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[j].x += w[u] * v[u][j].x, acc[j].y += w[u] * v[u][j].y, acc[j].z += w[u] * v[u][j].z, acc[j].w += w[u] * v[u][j].w;
-      }
-  }
-  const float f = inv[row];
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    *reinterpret_cast<uint2*>(&o[row][4 * (c0 + 16 * j)]) =
-        make_uint2(pack2(acc[j].x * f, acc[j].y * f, false), pack2(acc[j].z * f, acc[j].w * f, false));
-  __syncthreads();
-  {
-    const int r = tid >> 4, j = tid & 15;
-    *reinterpret_cast<uint4*>(p.out + static_cast<long long>(r0 + r) * kDv + cols + 8 * j) = *reinterpret_cast<const uint4*>(&o[r][8 * j]);
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<uint2*>(&o[row][4 * (c0 + 16 * j)]) =
+          make_uint2(pack2(acc[j].x * f, acc[j].y * f, false), pack2(acc[j].z * f, acc[j].w * f, false));
+    __syncthreads();
+    {
+      const int r = tid >> 4, j = tid & 15;
+      *reinterpret_cast<uint4*>(p.out + static_cast<long long>(r0 + r) * kDv + cols + 8 * j) = *reinterpret_cast<const uint4*>(&o[r][8 * j]);
+    }
+    __syncthreads();
   }
 }
 
@@ -1316,7 +1379,8 @@ int launch(const CUtensorMap& map, const CUtensorMap& rope, const PrefixParams& 
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.n_rows / kMergeRows, kDv / kMergeCols);
+  // few rows: four blocks share a row's values; from 1,024 blocks on the GPU is full without
+  cfg.gridDim = dim3(p.n_rows / kMergeRows, p.n_rows / kMergeRows < 1024 ? kDv / kMergeCols : 1);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cfg.attrs = &at, cfg.numAttrs = 1;
@@ -1356,6 +1420,12 @@ int pairs_of_device() {
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
+Costs costs_of(int32_t kv_dtype, bool wide) {
+  if (kv_dtype == SMLA_BF16) return {20, 4, 4};
+  const int own = kv_dtype == SMLA_FP8_E4M3 ? 6 : 10;
+  return {kv_dtype == SMLA_FP8_E4M3 ? 26 : 34, wide ? 4 : own, own};
+}
+
 // Row blocks and segments; false: more than 32-bit counts hold.
 bool plan(PrefixParams& p) {
   if (p.n_seqs == 1) p.shared_len = 0;  // its table is row 0: one segment per row block instead of two
@@ -1387,6 +1457,7 @@ size_t layout(PrefixParams& p, uint8_t* ws, int32_t kv_dtype) {
   p.part_o = reinterpret_cast<float4*>(ws + at);
   at += slots * 2 * 64 * kRows * 16;
   p.wide = kv_dtype != SMLA_BF16 && p.n_rb >= 2;
+  p.costs = costs_of(kv_dtype, p.wide);
   if (p.wide) {
     p.wide_rows = reinterpret_cast<uint16_t*>(ws + at);
     at += static_cast<size_t>((p.shared_len + kPage - 1) / kPage) * kPage * kDqk * 2;
