@@ -681,23 +681,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     Piece pc, nx;
     nx.s = 0;
     bool have = next_piece(p, wline, nx, writer), started = false;
-    Limits next_lim;
-    if (have) next_lim = limits(p, nx.s, row);
-    Tiles cur;
+    if (have && half == 0) prefetch_q(p, nx.s, row);
+    Tiles cur;  // one ahead of the tile that is worked on: its page ids have arrived when they are used
     cur.line = line;
-    bool more = cur.next(p, rank, true);
-    auto load_scale = [&] {  // scale of key 32 half + lane of the current tile's own page
+    bool more = false;
+    int own_next = -1;  // own page of the next tile to be worked on
+    auto load_scale = [&] {  // scale of key 32 half + lane of the own page of tile `cur`
       const int own = Tiles::pool_page(p, cur.own_id);
       return own >= 0 ? __ldg(p.kv_scale + static_cast<long long>(own) * kPage + half * 32 + lane) : 0.0f;
     };
-    // the tile that is worked on is one behind `cur`, whose page ids have arrived by the time they are used
     float scale = 0.0f;
-    if (FMT == kTokenFp8 && more) scale = load_scale();
-    int own_next = more ? Tiles::pool_page(p, cur.own_id) : -1;
-    if (more) more = cur.next(p, rank, false);
     uint32_t g = 0, sent = 0;  // tiles; exchanges between the warps of a row
     bool ok = true;
-    Limits lim;
+    Limits lim, next_lim;
     float m = 0.0f, l = 0.0f;
     // A value of a row from each of the four warps that hold the row (both halves,
     // both CTAs; own CTA's first), in the same order everywhere but for the CTA.
@@ -768,6 +764,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&M.o_free);
+      } else if (have) {
+        next_lim = limits(p, nx.s, row);
+        more = cur.next(p, rank, true);
+        own_next = Tiles::pool_page(p, cur.own_id);
+        if (FMT == kTokenFp8) scale = load_scale();
+        more = cur.next(p, rank, false);
       }
       if (!have) break;
       started = true;
@@ -1110,7 +1112,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         if (FMT == kTileFp8) sc[i] = live ? __ldg(reinterpret_cast<const float2*>(row + kDv) + (c0 >> 2)) : make_float2(0, 0);
         if (FMT == kTokenFp8 && group == 0) v[4][i] = live ? __ldg(reinterpret_cast<const uint4*>(row + kDv + pcs * 16)) : none;
       }
-      if (FMT == kTileFp8) rope = live ? src + kTileRope + pcs * 32 : nullptr;
+      if (FMT == kTileFp8 && group == 0) {
+        rope = live ? src + kTileRope + pcs * 32 : nullptr;
+        if (live && pcs == 0)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) prefetch_l2_lines(rope + i * 16 * kRowBytes, 128);
+      }
     };
     auto store = [&](int off) {
 #pragma unroll
@@ -1371,7 +1378,6 @@ bool set_smem() {
 
 template <int FMT>
 int launch(const CUtensorMap& map, const CUtensorMap& rope, const PrefixParams& p, cudaStream_t st) {
-  if (!set_smem<FMT>()) return SMLA_ERR_CUDA;
   prefix_kernel<FMT><<<2 * p.pairs, kThreadsOf<FMT>, kSmemBytes, st>>>(map, rope, p);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
   // set up while the pieces are computed; it waits for them itself
@@ -1402,9 +1408,9 @@ int resident_pairs() {
   return cudaOccupancyMaxActiveClusters(&n, prefix_kernel<FMT>, &cfg) == cudaSuccess ? n : 0;
 }
 
-// CTA pairs that run at the same time: fewer than half of the SMs where a GPC has
-// an odd number of them. One pair more than that starts when the others end, and the
-// call takes nearly twice as long (64x2 on a 64K prompt: 1.16 ms with 76 pairs).
+// CTA pairs that run at the same time (76 on a 152-SM part; fewer than half of the
+// SMs where a GPC has an odd number of them: a pair too many would start when the
+// others end). Looked up once per device, with the kernels' shared memory limit set.
 int pairs_of_device() {
   static std::mutex mutex;
   static int known[64] = {};

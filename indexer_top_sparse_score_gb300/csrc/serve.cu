@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
         // written by the row that opens it), a continued page's from the table
         const int id = page < held_b ? row[page] : p.free_pages[s_free[lo] + page - held_b];
         if (page >= held_b && pos % kPage == 0) row[page] = id;
-        if (id >= 0) slot = id * kPage + pos % kPage;
+        if (id >= 0 && id < (1 << 25)) slot = id * kPage + pos % kPage;  // (a pool has at most 2^25 pages)
       }
       p.slots[r] = slot;
       if (p.positions) p.positions[r] = pos;
