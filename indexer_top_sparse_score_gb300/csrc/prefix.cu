@@ -98,8 +98,9 @@ struct PrefixParams {
   Costs costs;
   int32_t wide;       // FP8: the shared rows are read from their f16 copy
   uint16_t* wide_rows;  // [shared pages * 64][576]
-  long long* seg_off; // [i] where own segment i starts on the line
+  long long* seg_off; // [i] where own segment i starts on the line; -1: one piece walks it and writes the results itself
   long long* bounds;  // [pairs + 1] where each pair's stretch starts
+  uint32_t* errors;   // [2 * pairs] status bits of each CTA
   float* part_m;      // [slot][128]
   float* part_l;      // [slot][4][128]: sums of each CTA's two halves
   float4* part_o;     // [slot][2][64][128]: four output values of a row
@@ -129,10 +130,10 @@ __device__ __forceinline__ int seg_cost(const PrefixParams& p, int s, int tiles)
 // Tiles [t0, t1) of segment s, which starts at a, that begin inside the stretch [x, y).
 __device__ __forceinline__ void stretch_tiles(const PrefixParams& p, int s, int tiles, long long a, long long x, long long y, int& t0,
                                               int& t1) {
-  const int one = s < p.n_rb ? p.costs.shared_tile : p.costs.own_tile;
-  const long long from = a + p.costs.start;
-  t0 = static_cast<int>((max(x - from, 0LL) + one - 1) / one);
-  t1 = static_cast<int>(min((max(y - from, 0LL) + one - 1) / one, static_cast<long long>(tiles)));
+  const uint32_t one = s < p.n_rb ? p.costs.shared_tile : p.costs.own_tile;
+  const long long from = a + p.costs.start, most = static_cast<long long>(tiles) * one;  // (below 2^31: a tile has 128 keys)
+  t0 = static_cast<int>((static_cast<uint32_t>(min(max(x - from, 0LL), most)) + one - 1) / one);
+  t1 = static_cast<int>((static_cast<uint32_t>(min(max(y - from, 0LL), most)) + one - 1) / one);
 }
 
 struct Line {  // a pair's stretch [x, y) and where it stands: segment s starts at a
@@ -150,12 +151,13 @@ __device__ __forceinline__ bool piece_after(const PrefixParams& p, Line& L, Piec
     const int tiles = seg_tiles(p, s), cost = seg_cost(p, s, tiles);
     const long long a = L.a;
     if (cost == 0) continue;
-    if (writer && s >= p.n_rb && a >= L.x) p.seg_off[s - p.n_rb] = a;
     L.a += cost;
     stretch_tiles(p, s, tiles, a, L.x, L.y, pc.t0, pc.t1);
     if (pc.t1 > pc.t0) {
       pc.s = s;
       pc.whole = pc.t0 == 0 && pc.t1 == tiles;
+      // (the pair with the first tile writes it)
+      if (writer && s >= p.n_rb && pc.t0 == 0) p.seg_off[s - p.n_rb] = pc.whole && p.n_rb == 0 ? -1 : a;
       return true;
     }
   }
@@ -441,7 +443,7 @@ struct Meta {
   long long scan[34];
   long long start_a;
   int start_s;
-  uint32_t tmem_slot;
+  uint32_t tmem_slot, status;
   int abort_flag;
 };
 constexpr size_t kSmemBytes = kOffMeta + sizeof(Meta);
@@ -571,6 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
   const int pair = blockIdx.x >> 1;
   const bool aligned = (smem_u32(smem) & 1023u) == 0;
 
+  asm volatile("griddepcontrol.launch_dependents;");  // merge_kernel may take an SM as soon as there is room
   if (tid == 0) {
     mbar_init(&M.q_full, kSoftWarps);
     mbar_init(&M.ko_full, kFills);
@@ -588,10 +591,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     mbar_init(&M.pv_done, 2);
     mbar_init(&M.o_free, kSoftWarps);
     M.abort_flag = 0;
+    M.status = 0;
     M.start_s = p.n_seg;
     M.start_a = 0;
     fence_mbar_init();
-    if (!aligned) set_status(p.status, kStatusSetup);
+    if (!aligned) set_status(&M.status, kStatusSetup);
   }
   if (warp == kTmaWarp) {
     tmem_alloc(&M.tmem_slot, 512);
@@ -610,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     if (lane == 0) M.scan[warp] = sum;
     if (pair == 0 && rank == 0)
       for (int b = tid; b < p.n_seqs; b += kThreads)
-        if (__ldg(p.seq_lens + b) > p.max_seq_len) set_status(p.status, kStatusBounds);
+        if (__ldg(p.seq_lens + b) > p.max_seq_len) set_status(&M.status, kStatusBounds);
     __syncthreads();
     long long total = shared_cost;
     for (int w = 0; w < kThreads / 32; ++w) total += M.scan[w];
@@ -925,7 +929,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         __syncwarp();
       }
     }
-    if (over) set_status(p.status, kStatusOverflow);
+    if (over) set_status(&M.status, kStatusOverflow);
   } else if (warp == kTmaWarp) {
     // -------------------------------------------------------------- TMA loads
     if (elect_one()) {
@@ -957,7 +961,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       for (; more && ok; ++g) {
         const bool by_tma = FMT == kBf16 || (p.wide && cur.pc.s < p.n_rb);
         const int y = place(cur.own_id, rank), other_y = place(cur.other_id, rank ^ 1);
-        if (FMT == kBf16 && cur.bad(p)) set_status(p.status, kStatusBounds);
+        if (FMT == kBf16 && cur.bad(p)) set_status(&M.status, kStatusBounds);
         more = cur.next(p, rank, false);
         if (g > 0 && !wait_one<false>(&M.ko_free, (g - 1) & 1, abort_v)) { ok = false; break; }
         if (by_tma) {
@@ -1165,7 +1169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     if (here) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
     for (uint32_t g = 0; more; ++g) {
       const bool stores = here;
-      if (stores && group == 0 && cur.bad(p) && lane == 0) set_status(p.status, kStatusBounds);
+      if (stores && group == 0 && cur.bad(p) && lane == 0) set_status(&M.status, kStatusBounds);
       more = cur.next(p, rank, false);
       here = more && mine();
       // the slots' previous tile: g - 1, or g - 2 for KV's two buffers
@@ -1185,17 +1189,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       }
       if (here) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
     }
-    if (over || top > 65504.0f) set_status(p.status, kStatusOverflow);
+    if (over || top > 65504.0f) set_status(&M.status, kStatusOverflow);
   }
 
   __syncwarp();
-  if (*abort_v == 2) set_status(p.status, kStatusTimeout);
+  if (*abort_v == 2) set_status(&M.status, kStatusTimeout);
   if (*abort_v) {  // a wait gave up: let copies that are still under way land before the memory goes
     const long long t0 = clock64();
     while (clock64() - t0 < 4000000) __nanosleep(1000);
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0) p.errors[blockIdx.x] = M.status;
   cluster_sync();  // the peer may still read or signal this CTA's shared memory until here
   if (warp == kTmaWarp) {
     tc_fence_after();
@@ -1205,8 +1210,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
 
 // ------------------------------------------------------------------ the shared rows, widened
 // f16 rows of the shared pages in logical order: per-token codes exactly, tile-scaled
-// values (code * scale) rounded (off by at most 2^-11 of the value). One block a page:
-// reads 37 or 42 KB, writes 74 KB, bound by memory. Each row block of the batch would
+// values (code * scale) rounded (off by at most 2^-11 of the value). Four blocks a
+// page, which read 37 or 42 KB and write 74 KB: bound by memory. Each row block of the batch would
 // widen them again otherwise (64x2 on a 16K prompt, FP8: 64 times, 329 us against
 // 243 with the copy).
 template <int FMT>
@@ -1215,13 +1220,14 @@ __global__ void __launch_bounds__(256) widen_kernel(const PrefixParams p) {
   constexpr int kPieces = FMT == kTokenFp8 ? kDqk / 16 : kDv / 16 + 8;  // 16 codes each, then (tile-scaled) 8 rope values
   const int id = p.page_tables[blockIdx.x];
   const bool live = id >= 0 && id < p.num_pages;
-  if (!live && threadIdx.x == 0) set_status(p.status, kStatusBounds);
-  const uint8_t* src = p.kv + static_cast<long long>(live ? id : 0) * kPage * kRowBytes;
-  uint16_t* dst = p.wide_rows + static_cast<long long>(blockIdx.x) * kPage * kDqk;
+  if (!live && blockIdx.y == 0 && threadIdx.x == 0) set_status(p.status, kStatusBounds);
+  constexpr int kPart = kPage / 4;
+  const uint8_t* src = p.kv + (static_cast<long long>(live ? id : 0) * kPage + blockIdx.y * kPart) * kRowBytes;
+  uint16_t* dst = p.wide_rows + (static_cast<long long>(blockIdx.x) * kPage + blockIdx.y * kPart) * kDqk;
   bool over = false;
   float top = 0.0f;
 #pragma unroll 4
-  for (int u = threadIdx.x; u < kPage * kPieces; u += 256) {
+  for (int u = threadIdx.x; u < kPart * kPieces; u += 256) {
     const int r = u / kPieces, j = u - r * kPieces;
     const uint8_t* row = src + r * kRowBytes;
     uint16_t* out = dst + r * kDqk;
@@ -1265,35 +1271,57 @@ constexpr int kMergeRows = 16, kMergeCols = 128, kMergeThreads = 256;
 
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams p) {
   __shared__ int slots[kMaxPieces];       // slot * 128 + the rows' place in the block
-  __shared__ float wgt[kMaxPieces][kMergeRows];
+  __shared__ float wgt[kMaxPieces][kMergeRows], sums[kMaxPieces][kMergeRows];
   __shared__ float inv[kMergeRows];
+  __shared__ long long bounds[kMaxPairs + 1];
+  __shared__ uint32_t warp_bits[kMergeThreads / 32];
   __shared__ __align__(16) uint16_t o[kMergeRows][kMergeCols];
   __shared__ int s_n;
   const int tid = threadIdx.x, lane = tid & 31;
   const int r0 = blockIdx.x * kMergeRows;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
+  // what does not depend on the pieces, then wait until they are written
+  int seg[2], at[2], tiles[2];  // the rows' shared and own segment
+  {
+    const int per = p.q_per_seq << p.hshift, b = r0 / per, in = r0 - b * per;
+    seg[0] = r0 / kRows, at[0] = r0 % kRows;
+    seg[1] = p.n_rb + b * p.rb_s + in / kRows, at[1] = in % kRows;
+    tiles[0] = p.n_rb > 0 ? p.n_pt : 0;
+    tiles[1] = seg_tiles(p, seg[1]);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long own_at = tiles[1] > 0 ? p.seg_off[seg[1] - p.n_rb] : 0;
+  const bool done = own_at < 0;
+  if (done && blockIdx.x != 0) return;
+  for (int q = tid; q <= p.pairs; q += kMergeThreads) bounds[q] = p.bounds[q];
+  if (blockIdx.x == 0 && blockIdx.y == 0) {  // the call's status
+    uint32_t bits = 0;
+    for (int q = tid; q < 2 * p.pairs; q += kMergeThreads) bits |= p.errors[q];
+    bits = __reduce_or_sync(0xFFFFFFFFu, bits);
+    if (lane == 0) warp_bits[tid >> 5] = bits;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
+    uint32_t bits = 0;
+    for (int w = 0; w < kMergeThreads / 32; ++w) bits |= warp_bits[w];
+    if (p.wide) set_status(p.status, bits);  // (widen_kernel may have set some)
+    else *p.status = bits;
+  }
+  if (done) return;
   if (tid < 32) {
     int n = 0;
-#pragma unroll 1
+#pragma unroll
     for (int part = 0; part < 2; ++part) {
-      if (part == 0 && p.n_rb == 0) continue;
-      int s = r0 / kRows, at = r0 % kRows;
-      if (part == 1) {
-        const int per = p.q_per_seq << p.hshift, b = r0 / per, in = r0 - b * per;
-        s = p.n_rb + b * p.rb_s + in / kRows;
-        at = in % kRows;
-      }
-      const int tiles = seg_tiles(p, s);
-      if (tiles == 0) continue;
-      const long long a = part == 1 ? p.seg_off[s - p.n_rb] : static_cast<long long>(s) * seg_cost(p, 0, p.n_pt);
+      if (tiles[part] == 0) continue;
+      const int s = seg[part];
+      const long long a = part == 1 ? own_at : static_cast<long long>(s) * seg_cost(p, 0, p.n_pt);
       for (int base = 0; base < p.pairs; base += 32) {
         const int q = base + lane;
         int t0 = 0, t1 = 0;
-        if (q < p.pairs) stretch_tiles(p, s, tiles, a, p.bounds[q], p.bounds[q + 1], t0, t1);
+        if (q < p.pairs) stretch_tiles(p, s, tiles[part], a, bounds[q], bounds[q + 1], t0, t1);
         const bool in = t1 > t0;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, in);
         const int at_n = n + __popc(mask & ((1u << lane) - 1));
-        if (in && at_n < kMaxPieces) slots[at_n] = (s + q) * kRows + at;
+        if (in && at_n < kMaxPieces) slots[at_n] = (s + q) * kRows + at[part];
         n += __popc(mask);
       }
     }
@@ -1301,7 +1329,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
   }
   __syncthreads();
   const int n = s_n;
-  if (n == 1 && p.n_rb == 0) return;  // one piece that walked all of the rows' keys: it wrote the results itself
   {  // 16 threads per row
     const int row = tid >> 4, k = tid & 15;
     float top = -INFINITY;
@@ -1310,15 +1337,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
       const float l = piece_sum(p, slot, at);
       const float m = p.part_m[static_cast<long long>(slot) * kRows + at];
       // a row that saw nothing in a piece (l = 0) has nothing there, whatever its O holds
-      wgt[i][row] = l != 0.0f ? m : -INFINITY;
+      wgt[i][row] = m;
+      sums[i][row] = l;
       if (l != 0.0f) top = fmaxf(top, m);
     }
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     float sum = 0.0f;
     for (int i = k; i < n; i += 16) {
-      const int slot = slots[i] / kRows, at = slots[i] % kRows + row;
-      const float l = piece_sum(p, slot, at);
+      const float l = sums[i][row];
       const float w = l != 0.0f ? exp2_fast(wgt[i][row] - top) : -1.0f;  // -1: nothing to add
       wgt[i][row] = w;
       if (l != 0.0f) sum += w * l;
@@ -1454,6 +1481,8 @@ size_t layout(PrefixParams& p, uint8_t* ws, int32_t kv_dtype) {
   size_t at = kStatusBytes;
   p.bounds = reinterpret_cast<long long*>(ws + at);
   at += up256((static_cast<size_t>(p.pairs) + 1) * 8);
+  p.errors = reinterpret_cast<uint32_t*>(ws + at);
+  at += up256(static_cast<size_t>(p.pairs) * 2 * 4);
   p.seg_off = reinterpret_cast<long long*>(ws + at);
   at += up256(static_cast<size_t>(p.n_seg - p.n_rb) * 8);
   p.part_m = reinterpret_cast<float*>(ws + at);
@@ -1514,7 +1543,6 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
   p.out = static_cast<uint16_t*>(out), p.lse = lse;
   p.status = static_cast<uint32_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
   CUtensorMap map{}, rope{};
   const bool bf16 = cache->kv_dtype == SMLA_BF16, token = cache->kv_dtype == SMLA_FP8_E4M3;
   if (bf16 || p.wide) {  // (16-bit values of either type)
@@ -1523,8 +1551,10 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
     const uint64_t rows = static_cast<uint64_t>(bf16 ? cache->num_pages : pages) * kPage;
     if (!encode_chunks(&map, base, rows, kDqk, 4) || !encode_chunks(&rope, base, rows, kDqk, 1)) return SMLA_ERR_CUDA;
     if (!bf16) {
-      if (token) widen_kernel<kTokenFp8><<<pages, 256, 0, st>>>(p);
-      else widen_kernel<kTileFp8><<<pages, 256, 0, st>>>(p);
+      // (without the copy merge_kernel writes the status word; with it, it adds to widen_kernel's)
+      if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
+      if (token) widen_kernel<kTokenFp8><<<dim3(pages, 4), 256, 0, st>>>(p);
+      else widen_kernel<kTileFp8><<<dim3(pages, 4), 256, 0, st>>>(p);
       if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
     }
   }

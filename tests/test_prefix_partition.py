@@ -32,12 +32,12 @@ def pieces(tiles, n_shared, cost, pairs):
             s += 1
         while s < len(tiles) and a < y:
             if whole[s]:
-                if a >= x:
-                    assert s not in start
-                    start[s] = a
                 t0, t1 = stretch(cost, one[s], tiles[s], a, x, y)
                 if t1 > t0:
                     got[s, p] = (t0, t1)
+                    if t0 == 0:  # the pair with the first tile says where the segment starts
+                        assert s not in start
+                        start[s] = a
                 a += whole[s]
             s += 1
     return got, start, total, one
