@@ -60,11 +60,14 @@ def peaks():
 
 
 def kernel_sources_digest():
-    """SHA-256 (first 16 hex digits) of the kernel sources and the C header,
-    each file hashed as its repository path then its bytes, in path order."""
+    """SHA-256 (first 16 hex digits) of the kernel sources of the measured path and
+    its C header, each file hashed as its repository path then its bytes, in path
+    order. (The serving calls' sources are not on that path.)"""
     csrc = os.path.join("indexer_top_sparse_score_gb300", "csrc")
+    serving = ("prefix.cu", "serve.cu", "serve.h")
     rel = sorted([os.path.join(csrc, f) for f in os.listdir(os.path.join(ROOT, csrc))
-                  if os.path.isfile(os.path.join(ROOT, csrc, f))] + [os.path.join("include", "smla.h")])
+                  if os.path.isfile(os.path.join(ROOT, csrc, f)) and f not in serving]
+                 + [os.path.join("include", "smla.h")])
     h = hashlib.sha256()
     for r in rel:
         h.update(r.replace(os.sep, "/").encode())

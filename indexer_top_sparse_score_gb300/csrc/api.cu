@@ -33,16 +33,6 @@ EncodeTiledFn encode_fn() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-bool valid_h_idx(int h) { return h == 4 || h == 8 || h == 16 || h == 32 || h == 64; }
-
-size_t round256(size_t b) { return (b + 255) / 256 * 256; }
-
-int reset_status(void* ws, cudaStream_t st) {
-  return cudaMemsetAsync(ws, 0, 4, st) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
-}
-
-}  // namespace
-
 int check_cache(const smla_paged_cache* c, bool need_kv, bool need_idx) {
   if (!c) return SMLA_ERR_INVALID_ARG;
   if (c->page_size != kPage || c->num_pages <= 0) return c->page_size != kPage && c->page_size > 0
@@ -65,6 +55,16 @@ int check_cache(const smla_paged_cache* c, bool need_kv, bool need_idx) {
   return SMLA_OK;
 }
 
+bool valid_h_idx(int h) { return h == 4 || h == 8 || h == 16 || h == 32 || h == 64; }
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+int reset_status(void* ws, cudaStream_t st) {
+  return cudaMemsetAsync(ws, 0, 4, st) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+}  // namespace
+
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner_elems,
                uint64_t rows, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows,
                CUtensorMapSwizzle swizzle) {
@@ -76,18 +76,6 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, ui
   cuuint32_t es[2] = {1, 1};
   return fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool encode_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint32_t width, uint32_t chunks) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {64, rows, width / 64};
-  cuuint64_t strides[2] = {width * 2, 128};
-  cuuint32_t box[3] = {64, kPage, chunks};
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t prefill_min_workspace(int32_t n_tokens, int32_t topk) {

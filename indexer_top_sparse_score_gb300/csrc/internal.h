@@ -83,9 +83,6 @@ size_t mla_shadow_bytes(int32_t n_keys, int32_t kv_dtype);
 // Fills the shadow from the pool through the page table (one sequence).
 int launch_shadow_convert(const MlaLaunch& L);
 
-// Argument checks of a cache whose latent rows / indexer keys the call uses.
-int check_cache(const smla_paged_cache* c, bool need_kv, bool need_idx);
-
 // Whether the indexer runs token groups over the full key range (prefill) or
 // splits each sequence's keys into blocks merged afterwards (decode).
 bool indexer_split_mode(int32_t q_per_seq, int32_t h_idx);
@@ -107,10 +104,6 @@ int launch_mla(const MlaLaunch& L);           // returns smla_status
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner_elems,
                uint64_t rows, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows,
                CUtensorMapSwizzle swizzle);
-
-// Rows of `width` 16-bit values as [width / 64 chunks][rows][64 values], loaded in
-// boxes of one page (64 rows) and `chunks` chunks, each chunk 128-byte swizzled.
-bool encode_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint32_t width, uint32_t chunks);
 
 int num_sms();
 

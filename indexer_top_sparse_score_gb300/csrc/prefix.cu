@@ -44,9 +44,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "../../include/smla_serve.h"
 #include "common.cuh"
-#include "internal.h"
+#include "serve.h"
 
 namespace smla {
 namespace {
@@ -1451,6 +1450,26 @@ int pairs_of_device() {
   return known[dev];
 }
 
+// Rows of 576 16-bit values as [9 chunks][rows][64 values], loaded in boxes of one
+// page (64 rows) and `chunks` chunks, each chunk 128-byte swizzled.
+bool encode_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint32_t chunks) {
+  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+    return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(f) : nullptr;
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {64, rows, kDqk / 64}, strides[2] = {kDqk * 2, 128};
+  const cuuint32_t box[3] = {64, kPage, chunks}, steps[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 Costs costs_of(int32_t kv_dtype, bool wide) {
@@ -1520,10 +1539,9 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
                            int32_t n_seqs, const int32_t* seq_lens, int32_t max_seq_len, int32_t shared_len,
                            int32_t q_per_seq, const void* q, int32_t n_heads, float sm_scale, void* out, float* lse,
                            void* workspace, size_t workspace_bytes, void* stream) {
-  int rc = check_cache(cache, true, false);
+  int rc = check_serve_cache(cache, true, false);
   if (rc) return rc;
-  auto al = [](const void* a, uintptr_t n) { return (reinterpret_cast<uintptr_t>(a) & (n - 1)) == 0; };
-  if (!page_tables || !seq_lens || !q || !out || !al(page_tables, 4) || !al(seq_lens, 4) || !al(q, 16) || !al(out, 16) || !al(lse, 4))
+  if (!page_tables || !seq_lens || !q || !out || !aligned_to(page_tables, 4) || !aligned_to(seq_lens, 4) || !aligned_to(q, 16) || !aligned_to(out, 16) || !aligned_to(lse, 4))
     return SMLA_ERR_INVALID_ARG;
   if (n_seqs <= 0 || q_per_seq <= 0 || max_pages <= 0 || max_seq_len <= 0 || shared_len < 0 || shared_len > max_seq_len)
     return SMLA_ERR_INVALID_ARG;
@@ -1533,7 +1551,7 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
   PrefixParams p{};
   p.n_seqs = n_seqs, p.q_per_seq = q_per_seq, p.shared_len = shared_len, p.hshift = n_heads == 64 ? 6 : 4;
   if (!plan(p)) return SMLA_ERR_UNSUPPORTED;
-  if (!workspace || !al(workspace, 16) || workspace_bytes < layout(p, static_cast<uint8_t*>(workspace), cache->kv_dtype)) return SMLA_ERR_WORKSPACE;
+  if (!workspace || !aligned_to(workspace, 16) || workspace_bytes < layout(p, static_cast<uint8_t*>(workspace), cache->kv_dtype)) return SMLA_ERR_WORKSPACE;
   p.kv = static_cast<const uint8_t*>(cache->kv), p.kv_scale = cache->kv_scale, p.num_pages = cache->num_pages;
   p.page_tables = page_tables, p.max_pages = max_pages, p.seq_lens = seq_lens, p.max_seq_len = max_seq_len;
   p.q = static_cast<const uint16_t*>(q);
@@ -1549,7 +1567,7 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
     const int pages = (p.shared_len + kPage - 1) / kPage;
     const void* base = bf16 ? cache->kv : p.wide_rows;
     const uint64_t rows = static_cast<uint64_t>(bf16 ? cache->num_pages : pages) * kPage;
-    if (!encode_chunks(&map, base, rows, kDqk, 4) || !encode_chunks(&rope, base, rows, kDqk, 1)) return SMLA_ERR_CUDA;
+    if (!encode_chunks(&map, base, rows, 4) || !encode_chunks(&rope, base, rows, 1)) return SMLA_ERR_CUDA;
     if (!bf16) {
       // (without the copy merge_kernel writes the status word; with it, it adds to widen_kernel's)
       if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;

@@ -10,9 +10,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "../../include/smla_serve.h"
 #include "common.cuh"
-#include "internal.h"
+#include "serve.h"
 
 namespace smla {
 namespace {
@@ -581,15 +580,13 @@ __global__ void __launch_bounds__(kRowThreads) query_prep_kernel(const QueryPara
   }
 }
 
-bool al(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 int check_rope(const smla_rope* r) {
-  if (!r || !r->cos_sin || !al(r->cos_sin, 16) || r->max_pos <= 0) return SMLA_ERR_INVALID_ARG;
+  if (!r || !r->cos_sin || !aligned_to(r->cos_sin, 16) || r->max_pos <= 0) return SMLA_ERR_INVALID_ARG;
   return SMLA_OK;
 }
 
 int check_ws(void* workspace, size_t bytes) {
-  return !workspace || !al(workspace, 16) || bytes < kStatusBytes ? SMLA_ERR_WORKSPACE : SMLA_OK;
+  return !workspace || !aligned_to(workspace, 16) || bytes < kStatusBytes ? SMLA_ERR_WORKSPACE : SMLA_OK;
 }
 
 int launched() { return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA; }
@@ -612,7 +609,7 @@ int smla_build_tables(const int32_t* ctx_lens, const int32_t* new_lens, int32_t 
                         static_cast<const void*>(free_pages), static_cast<const void*>(seq_lens), static_cast<const void*>(cu_new),
                         static_cast<const void*>(positions), static_cast<const void*>(slots), static_cast<const void*>(row_seq),
                         static_cast<const void*>(pages_used)})
-    if (!al(a, 4)) return SMLA_ERR_INVALID_ARG;
+    if (!aligned_to(a, 4)) return SMLA_ERR_INVALID_ARG;
   if (seq_lens == ctx_lens || seq_lens == new_lens) return SMLA_ERR_INVALID_ARG;  // other blocks still read the lengths
   if (const int rc = check_ws(workspace, workspace_bytes)) return rc;
   const int rows_per_block = std::max(kTabThreads, (max_new + 2 * num_sms() - 1) / (2 * num_sms()));
@@ -628,12 +625,12 @@ int smla_cache_append(const smla_paged_cache* cache, const smla_rope* rope, int3
                       const void* k_raw, int64_t k_stride, const float* idx_norm, const float* idx_bias, float eps,
                       void* workspace, size_t workspace_bytes, void* stream) {
   if (!ckv && !k_raw) return SMLA_ERR_INVALID_ARG;
-  int rc = check_cache(cache, ckv != nullptr, k_raw != nullptr);
+  int rc = check_serve_cache(cache, ckv != nullptr, k_raw != nullptr);
   if (rc) return rc;
   if ((rc = check_rope(rope))) return rc;
-  if (rows <= 0 || !slots || !positions || !al(slots, 4) || !al(positions, 4) || !(eps >= 0.0f)) return SMLA_ERR_INVALID_ARG;
-  if (ckv && (!al(ckv, 16) || ckv_stride < kDqk || ckv_stride % 8 || !al(kv_norm, 16))) return SMLA_ERR_INVALID_ARG;
-  if (k_raw && (!al(k_raw, 16) || k_stride < cache->d_idx || k_stride % 8 || !al(idx_norm, 16) || !al(idx_bias, 16) ||
+  if (rows <= 0 || !slots || !positions || !aligned_to(slots, 4) || !aligned_to(positions, 4) || !(eps >= 0.0f)) return SMLA_ERR_INVALID_ARG;
+  if (ckv && (!aligned_to(ckv, 16) || ckv_stride < kDqk || ckv_stride % 8 || !aligned_to(kv_norm, 16))) return SMLA_ERR_INVALID_ARG;
+  if (k_raw && (!aligned_to(k_raw, 16) || k_stride < cache->d_idx || k_stride % 8 || !aligned_to(idx_norm, 16) || !aligned_to(idx_bias, 16) ||
                 (idx_bias && !idx_norm)))
     return SMLA_ERR_INVALID_ARG;
   if ((rc = check_ws(workspace, workspace_bytes))) return rc;
@@ -671,14 +668,14 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
   if (!q_pe && !q_raw) return SMLA_ERR_INVALID_ARG;
   int rc = check_rope(rope);
   if (rc) return rc;
-  if (rows <= 0 || !positions || !al(positions, 4)) return SMLA_ERR_INVALID_ARG;
+  if (rows <= 0 || !positions || !aligned_to(positions, 4)) return SMLA_ERR_INVALID_ARG;
   if (q_pe) {
-    if (!q || !al(q, 16) || !al(q_pe, 16) || pe_row_stride % 8 || pe_head_stride % 8 || pe_head_stride < 64 || pe_row_stride < 0)
+    if (!q || !aligned_to(q, 16) || !aligned_to(q_pe, 16) || pe_row_stride % 8 || pe_head_stride % 8 || pe_head_stride < 64 || pe_row_stride < 0)
       return SMLA_ERR_INVALID_ARG;
     if (n_heads != 16 && n_heads != 64) return SMLA_ERR_UNSUPPORTED;
   }
   if (q_raw) {
-    if (!w || !q_idx || !w_out || !al(q_raw, 16) || !al(q_idx, 16) || !al(w, 4) || !al(w_out, 4) || !al(idx_norm, 16) ||
+    if (!w || !q_idx || !w_out || !aligned_to(q_raw, 16) || !aligned_to(q_idx, 16) || !aligned_to(w, 4) || !aligned_to(w_out, 4) || !aligned_to(idx_norm, 16) ||
         q_raw_stride % 8 || d_idx <= 0 || h_idx <= 0 || q_raw_stride < static_cast<int64_t>(h_idx) * d_idx || !(eps >= 0.0f))
       return SMLA_ERR_INVALID_ARG;
     if (idx_dtype != SMLA_BF16 && idx_dtype != SMLA_FP8_E4M3) return SMLA_ERR_INVALID_ARG;
