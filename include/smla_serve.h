@@ -158,17 +158,18 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
  *   lse         [n_seqs * q_per_seq][n_heads] fp32 natural log, or NULL. A row
  *               that sees no key gets out = 0 and lse = -inf.
  * Keys of a page outside the pool are skipped and reported. The latent cache is
- * device memory. The MMAs accumulate in fp32. BF16 rows: bf16 operands (q and the
- * rows as they are, the probabilities rounded to bf16). FP8 rows: f16 operands
- * (per-token codes are exact, tile-scaled values and the probabilities are
- * rounded to f16), so |q| and tile-scaled values must stay below 65504; beyond it
- * smla_read_status gives SMLA_ERR_UNSUPPORTED, as for smla_sparse_mla_fwd.
+ * device memory. The MMAs accumulate in fp32. BF16 rows and per-token FP8 codes:
+ * bf16 operands (q, rows and codes as they are, the probabilities rounded to bf16;
+ * the scales multiply logits and probabilities in fp32). Tile-scaled FP8 rows: f16
+ * operands (values and probabilities rounded to f16), so |q| and the values must
+ * stay below 65504; beyond it smla_read_status gives SMLA_ERR_UNSUPPORTED, as for
+ * smla_sparse_mla_fwd.
  * Keys that a row does not see never reach it, whatever they hold (an unused
  * slot of a page may hold NaN).
  * Supported: n_heads 16 and 64; any q_per_seq >= 1; the three cache formats.
  * Workspace: the returned size (status word, the partial results of the pieces that
  * the keys are cut into and, for FP8 caches whose shared part is read by more than
- * 128 query rows, an f16 copy of the shared rows, 1,152 bytes a token).
+ * 128 query rows, a 16-bit copy of the shared rows, 1,152 bytes a token).
  * ------------------------------------------------------------------------- */
 size_t smla_shared_prefix_fwd_workspace_size(int32_t n_seqs, int32_t max_seq_len, int32_t shared_len,
                                              int32_t q_per_seq, int32_t n_heads, int32_t kv_dtype);

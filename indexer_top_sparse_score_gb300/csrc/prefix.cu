@@ -52,7 +52,7 @@ namespace {
 
 constexpr int kRows = 128;       // rows of a block (MMA M)
 // Costs on the line of work, in quarters of a tile that comes by TMA (2,900 cycles
-// with BF16 rows, 3,100 to 3,900 with the f16 copy). Measured per CTA: starting a
+// with BF16 rows, 3,100 with the 16-bit copy). Measured per CTA: starting a
 // segment (Q in, results out) 14,000 cycles with BF16 rows, 25,000 with FP8 ones; a
 // tile that is widened on the way 5,500 (per-token scales) and 7,800 (tile scales).
 // With equal weights the pairs that walk short segments end last: 64x2 on a 16K
@@ -95,7 +95,7 @@ struct PrefixParams {
   int32_t rb_s;       // row blocks of one request
   int32_t n_seg, pairs;
   Costs costs;
-  int32_t wide;       // FP8: the shared rows are read from their f16 copy
+  int32_t wide;       // FP8: the shared rows are read from their 16-bit copy
   uint16_t* wide_rows;  // [shared pages * 64][576]
   long long* seg_off; // [i] where own segment i starts on the line; -1: one piece walks it and writes the results itself
   long long* bounds;  // [pairs + 1] where each pair's stretch starts
@@ -394,6 +394,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
@@ -426,6 +434,12 @@ __device__ __forceinline__ uint32_t e4m3x2(uint16_t c) {
 __device__ __forceinline__ uint32_t piece_off(int row, int j) {  // 16-byte piece j of a 128-byte swizzled row
   return static_cast<uint32_t>(row * 128 + ((j ^ (row & 7)) << 4));
 }
+// ... -> two bf16 values, exactly
+__device__ __forceinline__ uint32_t e4m3x2_bf16(uint16_t c) {
+  const uint32_t h = e4m3x2(c);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack2(f.x, f.y, false);
+}
 // bf16 pair -> f16 pair; `over`: a value outside f16's range
 __device__ __forceinline__ uint32_t to_f16(uint32_t w, bool& over) {
   over |= ((w & 0x7FFFu) > 0x477Fu && (w & 0x7FFFu) < 0x7F80u) || ((w & 0x7FFF0000u) > 0x477F0000u && (w & 0x7FFF0000u) < 0x7F800000u);
@@ -434,8 +448,8 @@ __device__ __forceinline__ uint32_t to_f16(uint32_t w, bool& over) {
 
 struct Meta {
   float mx[2][4][kRows];      // row maxima of this CTA's two halves and of the other's
-  float4 ks[kSoftWarps][16];  // per softmax warp and two of its keys: scale * sm_scale * log2 e of both, log2 scale of both (per-token FP8)
-  float rs[kSoftWarps][32];   // and 1 / scale
+  float4 ks[kSoftWarps][8];   // per softmax warp: the scales of its 32 keys (per-token FP8),
+  float4 vs[kSoftWarps][8];   // and as they meet the probabilities
   uint64_t q_full, ko_full, kv_full[2], vo_full, ko_free, kv_free[2], vo_free;
   uint64_t s_full, s_free, p_own, pv_done, o_free;
   uint64_t mx_full[2][4];
@@ -491,7 +505,7 @@ __device__ __forceinline__ Limits limits(const PrefixParams& p, int s, int row) 
 // are complete: all of it is free.) Returns whether a value was outside f16's range.
 template <int FMT>
 __device__ __forceinline__ bool load_q(const PrefixParams& p, int s, uint8_t* q_smem, uint32_t q_tmem, int rank, int quad, int half) {
-  constexpr bool F16 = FMT != kBf16;
+  constexpr bool F16 = FMT == kTileFp8;
   const int lane = threadIdx.x & 31;
   const bool shared = s < p.n_rb;
   const int i = s - p.n_rb, b = shared ? 0 : i / p.rb_s;
@@ -561,7 +575,7 @@ constexpr int kThreadsOf = FMT == kBf16 ? 384 : 512;
 template <int FMT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map, const PrefixParams p) {
-  constexpr bool F16 = FMT != kBf16;  // operand type of the MMAs: one cvt takes two e4m3 codes to f16, exactly
+  constexpr bool F16 = FMT == kTileFp8;  // operand type of the MMAs: bf16 holds BF16 rows and e4m3 codes as they are
   constexpr uint32_t kFmt = F16 ? kFmtF16 : kFmtBF16;
   constexpr int kThreads = kThreadsOf<FMT>;
   constexpr uint32_t kFills = FMT == kBf16 ? 1 : 3;  // arrivals that fill a slot group: TMA and the widening warps
@@ -788,24 +802,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       for (int t = pc.t0; t < pc.t1; ++t, ++g) {
         const int tile_k = (first_page + 2 * t) * kPage, key0 = tile_k + rank * kPage + half * 32;
         const int own = own_next;
-        const float4* ks = M.ks[sw];
-        const float2* rs = reinterpret_cast<const float2*>(M.rs[sw]);
         if (FMT == kTokenFp8) {
-          // Per-token scales: out = sum_j 2^(x_j) s_j code_j with x_j the logit. The
-          // scale goes into the exponent, y_j = x_j + log2 s_j, so that the
-          // probability P_j = 2^(y_j - m) that meets the codes is at most 2^kRaise
-          // whatever the scales are (f16), and l = sum_j P_j / s_j. Scales below
-          // 1e-30 count as that. A warp's 32 keys, loaded a tile ahead. (Keys that no
-          // row of the block sees count as 1; a NaN scale reaches those that see it
-          // through the logit.)
+          // Per-token scales multiply the logits, and the probabilities on their way to
+          // V's codes, in fp32. A warp's 32 keys, loaded a tile ahead. (Keys that no row
+          // of the block sees may have any scale: they count as 1. One that is not finite
+          // reaches the rows that see its key through the logit alone: 0 * NaN.)
           const int key = key0 + lane;
-          float sc = scale < 1e-30f ? 1e-30f : scale;
-          if (key < lim.lo || key >= lim.max_hi) sc = 1.0f;
+          const float sc = key < lim.lo || key >= lim.max_hi ? 1.0f : scale;
           __syncwarp();
-          float* k = &M.ks[sw][lane >> 1].x + (lane & 1);
-          k[0] = sc * p.scale_log2;
-          k[2] = __log2f(sc);  // off by 2^-22 at most: so is P, which is rounded to 2^-11 next
-          M.rs[sw][lane] = sc == sc ? __fdividef(1.0f, sc) : 1.0f;
+          reinterpret_cast<float*>(M.ks[sw])[lane] = sc;
+          reinterpret_cast<float*>(M.vs[sw])[lane] = fabsf(sc) < INFINITY ? sc : 1.0f;
           __syncwarp();
           if (more) scale = load_scale();
         }
@@ -825,10 +831,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         const bool edge = own < 0 || key0 < lim.lo || key0 + 32 > lim.min_hi;
         if (FMT == kTokenFp8) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float4 k = ks[i >> 1];
-            const float2 y = fma2(make_float2(x[i], x[i + 1]), make_float2(k.x, k.y), make_float2(k.z, k.w));
-            x[i] = y.x, x[i + 1] = y.y;
+          for (int i = 0; i < 32; i += 4) {
+            const float4 k = M.ks[sw][i >> 2];
+            const float2 y = mul2(make_float2(x[i], x[i + 1]), make_float2(k.x, k.y));
+            const float2 z = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k.z, k.w));
+            x[i] = y.x, x[i + 1] = y.y, x[i + 2] = z.x, x[i + 3] = z.y;
           }
         }
         if (edge) {
@@ -839,7 +846,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         float mine = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 32; i += 2) mine = max3(mine, x[i], x[i + 1]);
-        if (FMT != kTokenFp8) mine *= p.scale_log2;
+        mine *= p.scale_log2;
         // the row's maximum over both halves of both pages, which all scale P by the
         // same reference: every warp sends its rows' to both CTAs
         float4 of;
@@ -861,11 +868,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         const float2 factor = make_float2(p.scale_log2, p.scale_log2), minus = make_float2(-ref, -ref);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const float2 v = make_float2(x[i], x[i + 1]);
-          const float2 y = FMT == kTokenFp8 ? add2(v, minus) : fma2(v, factor, minus);
-          const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-          if (FMT == kTokenFp8) sum[(i >> 1) & 1] = fma2(e, rs[i >> 1], sum[(i >> 1) & 1]);
-          else sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
+          const float2 y = fma2(make_float2(x[i], x[i + 1]), factor, minus);
+          float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+          sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
+          if (FMT == kTokenFp8) e = mul2(e, reinterpret_cast<const float2*>(M.vs[sw])[i >> 1]);
           // P is rounded to the operands' type (bf16: off by at most 2^-8 of a probability,
           // f16: 2^-11); the sum l is not
           pk[i >> 1] = pack2(e.x, e.y, F16);
@@ -1090,9 +1096,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     // Two warps for each of KO (2, 3), KV (12, 13) and VO (14, 15). Thread u takes
     // 16 codes of rows u / 4 + 16 i in every chunk (four lanes on a row's 64
     // contiguous bytes); a tile's pieces are loaded while the tile before is waited
-    // for. Codes are exact in f16 (per-token scales enter the logits and P in
-    // fp32); tile-scaled values (code * scale) are rounded to f16: off by at most
-    // 2^-11 of the value.
+    // for. Per-token codes are exact in bf16; tile-scaled values (code * scale) are
+    // rounded to f16: off by at most 2^-11 of the value.
     const int cw = warp < kSoftWarp0 ? warp - 2 : warp - 10;
     const int group = cw >> 1;  // 0 KO, 1 KV, 2 VO
     const int u = (cw & 1) * 32 + lane, r0 = u >> 2, pcs = u & 3;
@@ -1141,8 +1146,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
             const uint32_t w[4] = {v[c][i].x, v[c][i].y, v[c][i].z, v[c][i].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              o[2 * k] = e4m3x2(static_cast<uint16_t>(w[k]));
-              o[2 * k + 1] = e4m3x2(static_cast<uint16_t>(w[k] >> 16));
+              const uint16_t lo = static_cast<uint16_t>(w[k]), hi = static_cast<uint16_t>(w[k] >> 16);
+              o[2 * k] = F16 ? e4m3x2(lo) : e4m3x2_bf16(lo);
+              o[2 * k + 1] = F16 ? e4m3x2(hi) : e4m3x2_bf16(hi);
             }
             if (FMT == kTileFp8) {
               const float s = c < 2 ? sc[i].x : sc[i].y;
@@ -1208,8 +1214,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
 }
 
 // ------------------------------------------------------------------ the shared rows, widened
-// f16 rows of the shared pages in logical order: per-token codes exactly, tile-scaled
-// values (code * scale) rounded (off by at most 2^-11 of the value). Four blocks a
+// The shared pages' rows in logical order, as the MMAs take them: per-token codes in
+// bf16, exactly; tile-scaled values (code * scale) in f16, rounded (off by at most
+// 2^-11 of the value). Four blocks a
 // page, which read 37 or 42 KB and write 74 KB: bound by memory. Each row block of the batch would
 // widen them again otherwise (64x2 on a 16K prompt, FP8: 64 times, 329 us against
 // 243 with the copy).
@@ -1242,7 +1249,8 @@ __global__ void __launch_bounds__(256) widen_kernel(const PrefixParams p) {
     uint32_t o[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      o[k] = e4m3x2(static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1))));
+      const uint16_t pair = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+      o[k] = FMT == kTileFp8 ? e4m3x2(pair) : e4m3x2_bf16(pair);
       if (FMT == kTileFp8) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
         top = fmaxf(top, fmaxf(fabsf(f.x * s), fabsf(f.y * s)));

@@ -313,7 +313,7 @@ def test_attention_softmax_scales(scale):
 
 @pytest.mark.parametrize("factor", [1e-25, 1e-12, 1e12])
 def test_attention_per_token_scales_of_any_size(factor):
-    """Scales far outside f16's range, and some that are zero (a row of zeros)."""
+    """Scales far from one, and some that are zero (a row of zeros)."""
     c, tab, sl, qt = sc.attention_case(2, 1, 16, "fp8", 200, [420, 333], seed=15)
     live = torch.isfinite(c.kv_scale)
     c.kv_scale[live] *= factor * (1 + torch.arange(c.kv_scale.numel()).view_as(c.kv_scale) % 7)[live]
@@ -332,7 +332,7 @@ def test_attention_nan_scale_reaches_only_those_that_see_it():
     assert out[2].isnan().all() and lse[2].isnan().all()
 
 
-@pytest.mark.parametrize("kv_dtype,what", [("fp8", "query"), ("fp8_ds_mla", "query"), ("fp8_ds_mla", "row")])
+@pytest.mark.parametrize("kv_dtype,what", [("fp8_ds_mla", "query"), ("fp8_ds_mla", "row")])
 def test_attention_reports_values_outside_f16(kv_dtype, what):
     c, tab, sl, qt = sc.attention_case(1, 1, 16, kv_dtype, 0, [100], seed=17)
     if what == "query":
