@@ -95,6 +95,8 @@ struct PrefixParams {
   int32_t rb_s;       // row blocks of one request
   int32_t n_seg, pairs;
   Costs costs;
+  int32_t q_tma;      // Q's chunks for shared memory come by TMA
+  int32_t q_sectors;  // q starts on a 32-byte boundary
   int32_t wide;       // FP8: the shared rows are read from their 16-bit copy
   uint16_t* wide_rows;  // [shared pages * 64][576]
   long long* seg_off; // [i] where own segment i starts on the line; -1: one piece walks it and writes the results itself
@@ -496,77 +498,103 @@ __device__ __forceinline__ Limits limits(const PrefixParams& p, int s, int row) 
   return m;
 }
 
-// Q of segment s, by one softmax warp: chunks of its 32 rows in 16-byte pieces,
-// eight lanes on one row's chunk (128 contiguous bytes), two chunks in flight (FP8: one; more
-// push the tile loops' values into local memory, and next to 225 KB of shared
-// memory there is hardly any L1 to hold that). The six for tensor memory pass one by
-// one through a chunk's place in shared memory, from where every lane reads its own
-// row; the other three are stored where they stay. (The logits of the previous piece
-// are complete: all of it is free.) Returns whether a value was outside f16's range.
+// First row of segment s in q, and how many of the rows from there on are its own.
+__device__ __forceinline__ long long first_row(const PrefixParams& p, int s, int& rows) {
+  if (s < p.n_rb) {
+    rows = p.n_rows - s * kRows;
+    return static_cast<long long>(s) * kRows;
+  }
+  const int i = s - p.n_rb, b = i / p.rb_s, in = (i - b * p.rb_s) * kRows;
+  rows = (p.q_per_seq << p.hshift) - in;
+  return (static_cast<long long>(b) * p.q_per_seq << p.hshift) + in;
+}
+// 32 bytes, a whole sector, at once (aligned to 32)
+__device__ __forceinline__ void ldg32(const void* p, uint32_t* v) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p));
+}
+// Q of segment s, by one softmax warp (the logits of the previous piece are complete:
+// all of Q's places are free). The six chunks for tensor memory: every lane reads its
+// own row's 128 bytes a chunk in whole sectors. The three for shared memory come by
+// TMA unless their values change on the way (f16, a negative scale): then eight lanes
+// bring a row's chunk in 16-byte pieces. More chunks in flight push the tile
+// loops' values into local memory, and next to 225 KB of shared memory there is
+// hardly any L1 to hold that. Returns whether a value was outside f16's range.
 template <int FMT>
 __device__ __forceinline__ bool load_q(const PrefixParams& p, int s, uint8_t* q_smem, uint32_t q_tmem, int rank, int quad, int half) {
   constexpr bool F16 = FMT == kTileFp8;
+  constexpr int kBatch = FMT == kBf16 ? 3 : 1;
   const int lane = threadIdx.x & 31;
-  const bool shared = s < p.n_rb;
-  const int i = s - p.n_rb, b = shared ? 0 : i / p.rb_s;
-  const int first = (shared ? s : i - b * p.rb_s) * kRows + quad * 32;
-  const int limit = (shared ? p.n_rows : p.q_per_seq << p.hshift) - first;  // rows of the warp that exist
-  const uint16_t* src = p.q + ((static_cast<long long>(b) * p.q_per_seq << p.hshift) + first) * kDqk;
-  const int sub = lane >> 3, pcs = lane & 7;
-  bool over = false;
-  auto bring = [&](int c, int j) {  // piece pcs of row 4 j + sub of the chunk at place c
-    const int chunk = c < 4 ? 4 * (rank ^ 1) + c : c < 6 ? 4 * rank + c - 4 : c == 6 ? 8 : 4 * rank + c - 5;
-    const int r = 4 * j + sub;
-    return r < limit ? __ldg(reinterpret_cast<const uint4*>(src + r * kDqk + chunk * 64 + pcs * 8)) : make_uint4(0, 0, 0, 0);
-  };
-  auto put = [&](int place, int j, uint4 w) {
-    if (F16) w = make_uint4(to_f16(w.x, over), to_f16(w.y, over), to_f16(w.z, over), to_f16(w.w, over));
-    w.x ^= p.q_sign, w.y ^= p.q_sign, w.z ^= p.q_sign, w.w ^= p.q_sign;
-    *reinterpret_cast<uint4*>(q_smem + place * kQChunk + piece_off(quad * 32 + 4 * j + sub, pcs)) = w;
-  };
-  // step c < 3: chunk 3 half + c to tensor memory; step 3: the chunk of place 6 or 7;
-  // step 4: half of the rows of place 8
-  constexpr int kBatch = FMT == kBf16 ? 2 : 1;
-  uint4 v[kBatch][8];
-#pragma unroll 1
-  for (int c0 = 0; c0 < 5; c0 += kBatch) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int c = c0 + u;
-      if (c < 5)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c < 4 || j < 4) v[u][j] = bring(c < 3 ? 3 * half + c : c == 3 ? 6 + half : 8, c < 4 ? j : 4 * half + j);
+  int rows;
+  const uint16_t* src = p.q + (first_row(p, s, rows) + quad * 32) * kDqk;
+  const int limit = rows - quad * 32;  // rows of the warp that exist
+  float top = 0.0f;
+  auto change = [&](uint32_t w) {
+    if (F16) {
+      const float a = bf_lo(w), b = bf_hi(w);
+      top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
+      w = pack2(a, b, true);
     }
+    return w ^ p.q_sign;
+  };
+  // chunk of values at place c: 0-5 in tensor memory (KO 0-3, KV 0-1), 6-8 in shared memory (KO 4, KV 2-3)
+  auto chunk_of = [&](int c) { return c < 4 ? 4 * (rank ^ 1) + c : c < 6 ? 4 * rank + c - 4 : c == 6 ? 8 : 4 * rank + c - 5; };
+  uint32_t v[kBatch][32];
+#pragma unroll 1
+  for (int c0 = 3 * half; c0 < 3 * half + 3; c0 += kBatch) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int c = c0 + u;
-      if (c < 5)
+      const uint16_t* at = src + lane * kDqk + chunk_of(c0 + u) * 64;
+      if (lane >= limit) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c < 4 || j < 4) put(c < 4 ? half : 2, c < 4 ? j : 4 * half + j, v[u][j]);
-      if (c < 3) {
-        __syncwarp();
+        for (int j = 0; j < 32; ++j) v[u][j] = 0;
+      } else if (p.q_sectors) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[u][j] = *reinterpret_cast<const uint4*>(q_smem + half * kQChunk + piece_off(quad * 32 + lane, j));
-        tmem_st_32x32b_x32(q_tmem + 32 * (3 * half + c), reinterpret_cast<const uint32_t*>(v[u]));
-        __syncwarp();
+        for (int j = 0; j < 4; ++j) ldg32(at + 16 * j, v[u] + 8 * j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(at) + j);
+          v[u][4 * j] = w.x, v[u][4 * j + 1] = w.y, v[u][4 * j + 2] = w.z, v[u][4 * j + 3] = w.w;
+        }
       }
     }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[u][j] = change(v[u][j]);
+      tmem_st_32x32b_x32(q_tmem + 32 * (c0 + u), v[u]);
+    }
+  }
+  if (!p.q_tma) {
+    const int sub = lane >> 3, pcs = lane & 7;
+#pragma unroll 1
+    for (int c = 6; c < 9; ++c) {  // half of the warp's rows each
+      uint4 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 16 * half + 4 * j + sub;
+        w[j] = r < limit ? __ldg(reinterpret_cast<const uint4*>(src + r * kDqk + chunk_of(c) * 64 + pcs * 8)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(q_smem + (c - 6) * kQChunk + piece_off(quad * 32 + 16 * half + 4 * j + sub, pcs)) =
+            make_uint4(change(w[j].x), change(w[j].y), change(w[j].z), change(w[j].w));
+    }
+    fence_proxy_async_smem();
   }
   tmem_wait_st();
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncwarp();
-  return over;
+  return top > 65504.0f;
 }
 // the rows of a later segment's Q into L2
 __device__ __forceinline__ void prefetch_q(const PrefixParams& p, int s, int row) {
-  const bool shared = s < p.n_rb;
-  const int i = s - p.n_rb, b = shared ? 0 : i / p.rb_s;
-  const int r = (shared ? s : i - b * p.rb_s) * kRows + row;
-  if (r < (shared ? p.n_rows : p.q_per_seq << p.hshift))
-    prefetch_l2_lines(p.q + ((static_cast<long long>(b) * p.q_per_seq << p.hshift) + r) * kDqk, 2 * kDqk);
+  int rows;
+  const long long first = first_row(p, s, rows);
+  if (row < rows) prefetch_l2_lines(p.q + (first + row) * kDqk, 2 * kDqk);
 }
 
 template <int FMT>
@@ -574,7 +602,8 @@ constexpr int kThreadsOf = FMT == kBf16 ? 384 : 512;
 
 template <int FMT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
-    prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map, const PrefixParams p) {
+    prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
+                  const __grid_constant__ CUtensorMap q_map, const PrefixParams p) {
   constexpr bool F16 = FMT == kTileFp8;  // operand type of the MMAs: bf16 holds BF16 rows and e4m3 codes as they are
   constexpr uint32_t kFmt = F16 ? kFmtF16 : kFmtBF16;
   constexpr int kThreads = kThreadsOf<FMT>;
@@ -588,7 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
 
   asm volatile("griddepcontrol.launch_dependents;");  // merge_kernel may take an SM as soon as there is room
   if (tid == 0) {
-    mbar_init(&M.q_full, kSoftWarps);
+    mbar_init(&M.q_full, kSoftWarps + (p.q_tma ? 1 : 0));
     mbar_init(&M.ko_full, kFills);
     mbar_init(&M.vo_full, kFills);
     mbar_init(&M.ko_free, 1);
@@ -963,10 +992,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       uint32_t g = 0;
       bool ok = true, last_tma = false;
       int last_y = 0;
+      if (more && p.q_tma) prefetch_tensormap(&q_map);
       for (; more && ok; ++g) {
         const bool by_tma = FMT == kBf16 || (p.wide && cur.pc.s < p.n_rb);
         const int y = place(cur.own_id, rank), other_y = place(cur.other_id, rank ^ 1);
         if (FMT == kBf16 && cur.bad(p)) set_status(&M.status, kStatusBounds);
+        const bool new_piece = cur.t == cur.pc.t0;
+        int rows;
+        const int q_row = static_cast<int>(first_row(p, cur.pc.s, rows));
         more = cur.next(p, rank, false);
         if (g > 0 && !wait_one<false>(&M.ko_free, (g - 1) & 1, abort_v)) { ok = false; break; }
         if (by_tma) {
@@ -993,6 +1026,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
           }
         }
         if (g > 0) ok = load_vo(g - 1, last_tma, last_y);
+        if (p.q_tma && new_piece) {  // its Q, once the logits of the piece before are complete
+          if (g > 0 && !wait_one<false>(&M.s_full, (g - 1) & 1, abort_v)) { ok = false; break; }
+          mbar_arrive_expect_tx(&M.q_full, 3 * kQChunk);
+          tma_chunks(smem + kOffQ, &q_map, &M.q_full, q_row, 8);
+          tma_chunks(smem + kOffQ + kQChunk, &q_map, &M.q_full, q_row, v0 + 2);
+          tma_chunks(smem + kOffQ + 2 * kQChunk, &q_map, &M.q_full, q_row, v0 + 3);
+        }
         last_tma = by_tma;
         last_y = other_y;
       }
@@ -1411,8 +1451,8 @@ bool set_smem() {
 }
 
 template <int FMT>
-int launch(const CUtensorMap& map, const CUtensorMap& rope, const PrefixParams& p, cudaStream_t st) {
-  prefix_kernel<FMT><<<2 * p.pairs, kThreadsOf<FMT>, kSmemBytes, st>>>(map, rope, p);
+int launch(const CUtensorMap& map, const CUtensorMap& rope, const CUtensorMap& q, const PrefixParams& p, cudaStream_t st) {
+  prefix_kernel<FMT><<<2 * p.pairs, kThreadsOf<FMT>, kSmemBytes, st>>>(map, rope, q, p);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
   // set up while the pieces are computed; it waits for them itself
   cudaLaunchAttribute at{};
@@ -1458,9 +1498,9 @@ int pairs_of_device() {
   return known[dev];
 }
 
-// Rows of 576 16-bit values as [9 chunks][rows][64 values], loaded in boxes of one
-// page (64 rows) and `chunks` chunks, each chunk 128-byte swizzled.
-bool encode_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint32_t chunks) {
+// Rows of 576 16-bit values as [9 chunks][rows][64 values], loaded in boxes of
+// `box_rows` rows and `chunks` chunks, each chunk 128-byte swizzled.
+bool encode_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows, uint32_t chunks) {
   typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -1472,7 +1512,7 @@ bool encode_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint32_t c
   }();
   if (!encode) return false;
   const cuuint64_t dims[3] = {64, rows, kDqk / 64}, strides[2] = {kDqk * 2, 128};
-  const cuuint32_t box[3] = {64, kPage, chunks}, steps[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, box_rows, chunks}, steps[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, steps,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1483,7 +1523,7 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 Costs costs_of(int32_t kv_dtype, bool wide) {
   if (kv_dtype == SMLA_BF16) return {20, 4, 4};
   const int own = kv_dtype == SMLA_FP8_E4M3 ? 6 : 10;
-  return {kv_dtype == SMLA_FP8_E4M3 ? 26 : 34, wide ? 4 : own, own};
+  return {kv_dtype == SMLA_FP8_E4M3 ? 32 : 34, wide ? 4 : own, own};
 }
 
 // Row blocks and segments; false: more than 32-bit counts hold.
@@ -1569,13 +1609,13 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
   p.out = static_cast<uint16_t*>(out), p.lse = lse;
   p.status = static_cast<uint32_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  CUtensorMap map{}, rope{};
+  CUtensorMap map{}, rope{}, q_map{};
   const bool bf16 = cache->kv_dtype == SMLA_BF16, token = cache->kv_dtype == SMLA_FP8_E4M3;
   if (bf16 || p.wide) {  // (16-bit values of either type)
     const int pages = (p.shared_len + kPage - 1) / kPage;
     const void* base = bf16 ? cache->kv : p.wide_rows;
     const uint64_t rows = static_cast<uint64_t>(bf16 ? cache->num_pages : pages) * kPage;
-    if (!encode_chunks(&map, base, rows, 4) || !encode_chunks(&rope, base, rows, 1)) return SMLA_ERR_CUDA;
+    if (!encode_chunks(&map, base, rows, kPage, 4) || !encode_chunks(&rope, base, rows, kPage, 1)) return SMLA_ERR_CUDA;
     if (!bf16) {
       // (without the copy merge_kernel writes the status word; with it, it adds to widen_kernel's)
       if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
@@ -1584,8 +1624,11 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
       if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
     }
   }
-  if (bf16) return launch<kBf16>(map, rope, p, st);
-  return token ? launch<kTokenFp8>(map, rope, p, st) : launch<kTileFp8>(map, rope, p, st);
+  p.q_tma = cache->kv_dtype != SMLA_FP8_DS_MLA && p.q_sign == 0;
+  p.q_sectors = aligned_to(q, 32);
+  if (p.q_tma && !encode_chunks(&q_map, q, static_cast<uint64_t>(p.n_rows), kRows, 1)) return SMLA_ERR_CUDA;
+  if (bf16) return launch<kBf16>(map, rope, q_map, p, st);
+  return token ? launch<kTokenFp8>(map, rope, q_map, p, st) : launch<kTileFp8>(map, rope, q_map, p, st);
 }
 
 }  // extern "C"
