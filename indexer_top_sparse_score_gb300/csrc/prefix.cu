@@ -1522,8 +1522,8 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 Costs costs_of(int32_t kv_dtype, bool wide) {
   if (kv_dtype == SMLA_BF16) return {20, 4, 4};
-  const int own = kv_dtype == SMLA_FP8_E4M3 ? 6 : 10;
-  return {kv_dtype == SMLA_FP8_E4M3 ? 32 : 34, wide ? 4 : own, own};
+  const int own = kv_dtype == SMLA_FP8_E4M3 ? 7 : 10;
+  return {kv_dtype == SMLA_FP8_E4M3 ? 40 : 34, wide ? 4 : own, own};
 }
 
 // Row blocks and segments; false: more than 32-bit counts hold.

@@ -8,7 +8,7 @@ import random
 
 import pytest
 
-COSTS = [(20, 4, 4), (32, 4, 6), (34, 4, 10), (34, 10, 10)]  # start, shared tile, own tile
+COSTS = [(20, 4, 4), (40, 4, 7), (34, 4, 10), (34, 10, 10)]  # start, shared tile, own tile
 
 
 def stretch(cost, one, tiles, a, x, y):
