@@ -169,7 +169,7 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
  * Supported: n_heads 16 and 64; any q_per_seq >= 1; the three cache formats.
  * Workspace: the returned size (status word, the partial results of the pieces that
  * the keys are cut into and, for FP8 caches whose shared part is read by more than
- * 128 query rows, a 16-bit copy of the shared rows, 1,152 bytes a token).
+ * 128 query rows, a 16-bit copy of the shared rows, 1,152 bytes a token and 16 a page).
  * ------------------------------------------------------------------------- */
 size_t smla_shared_prefix_fwd_workspace_size(int32_t n_seqs, int32_t max_seq_len, int32_t shared_len,
                                              int32_t q_per_seq, int32_t n_heads, int32_t kv_dtype);

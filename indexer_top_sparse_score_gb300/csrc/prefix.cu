@@ -102,6 +102,7 @@ struct PrefixParams {
   long long* seg_off; // [i] where own segment i starts on the line; -1: one piece walks it and writes the results itself
   long long* bounds;  // [pairs + 1] where each pair's stretch starts
   uint32_t* errors;   // [2 * pairs] status bits of each CTA
+  uint4* wide_errors; // [shared pages] of each page's four blocks of widen_kernel
   float* part_m;      // [slot][128]
   float* part_l;      // [slot][4][128]: sums of each CTA's two halves
   float4* part_o;     // [slot][2][64][128]: four output values of a row
@@ -700,6 +701,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       }
     }
   }
+  if (FMT != kBf16) asm volatile("griddepcontrol.wait;" ::: "memory");  // widen_kernel's rows
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the pair's barriers are set up before either CTA sends to the other
@@ -992,6 +994,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       uint32_t g = 0;
       bool ok = true, last_tma = false;
       int last_y = 0;
+      if (FMT != kBf16) asm volatile("fence.proxy.async.global;" ::: "memory");  // the copy was written by plain stores
       if (more && p.q_tma) prefetch_tensormap(&q_map);
       for (; more && ok; ++g) {
         const bool by_tma = FMT == kBf16 || (p.wide && cur.pc.s < p.n_rb);
@@ -1264,9 +1267,9 @@ template <int FMT>
 __global__ void __launch_bounds__(256) widen_kernel(const PrefixParams p) {
   constexpr int kRowBytes = FMT == kTokenFp8 ? kDqk : kTileRowBytes;
   constexpr int kPieces = FMT == kTokenFp8 ? kDqk / 16 : kDv / 16 + 8;  // 16 codes each, then (tile-scaled) 8 rope values
+  asm volatile("griddepcontrol.launch_dependents;");  // prefix_kernel may set up; it waits for the rows
   const int id = p.page_tables[blockIdx.x];
   const bool live = id >= 0 && id < p.num_pages;
-  if (!live && blockIdx.y == 0 && threadIdx.x == 0) set_status(p.status, kStatusBounds);
   constexpr int kPart = kPage / 4;
   const uint8_t* src = p.kv + (static_cast<long long>(live ? id : 0) * kPage + blockIdx.y * kPart) * kRowBytes;
   uint16_t* dst = p.wide_rows + (static_cast<long long>(blockIdx.x) * kPage + blockIdx.y * kPart) * kDqk;
@@ -1300,7 +1303,9 @@ __global__ void __launch_bounds__(256) widen_kernel(const PrefixParams p) {
     *reinterpret_cast<uint4*>(out + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(out + 16 * j + 8) = make_uint4(o[4], o[5], o[6], o[7]);
   }
-  if (over || top > 65504.0f) set_status(p.status, kStatusOverflow);
+  over = __syncthreads_or(over || top > 65504.0f);
+  if (threadIdx.x == 0)
+    reinterpret_cast<uint32_t*>(p.wide_errors)[4 * blockIdx.x + blockIdx.y] = (over ? kStatusOverflow : 0u) | (live ? 0u : kStatusBounds);
 }
 
 // ------------------------------------------------------------------ joining the pieces
@@ -1343,6 +1348,14 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
   if (blockIdx.x == 0 && blockIdx.y == 0) {  // the call's status
     uint32_t bits = 0;
     for (int q = tid; q < 2 * p.pairs; q += kMergeThreads) bits |= p.errors[q];
+    if (p.wide) {
+      const int pages = (p.shared_len + kPage - 1) / kPage;
+#pragma unroll 8
+      for (int i = tid; i < pages; i += kMergeThreads) {
+        const uint4 e = p.wide_errors[i];
+        bits |= e.x | e.y | e.z | e.w;
+      }
+    }
     bits = __reduce_or_sync(0xFFFFFFFFu, bits);
     if (lane == 0) warp_bits[tid >> 5] = bits;
   }
@@ -1350,8 +1363,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
   if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
     uint32_t bits = 0;
     for (int w = 0; w < kMergeThreads / 32; ++w) bits |= warp_bits[w];
-    if (p.wide) set_status(p.status, bits);  // (widen_kernel may have set some)
-    else *p.status = bits;
+    *p.status = bits;
   }
   if (done) return;
   if (tid < 32) {
@@ -1452,13 +1464,18 @@ bool set_smem() {
 
 template <int FMT>
 int launch(const CUtensorMap& map, const CUtensorMap& rope, const CUtensorMap& q, const PrefixParams& p, cudaStream_t st) {
-  prefix_kernel<FMT><<<2 * p.pairs, kThreadsOf<FMT>, kSmemBytes, st>>>(map, rope, q, p);
-  if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
-  // set up while the pieces are computed; it waits for them itself
+  // each kernel but the call's first is set up while the one before runs, and waits for it itself
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * p.pairs);
+  cfg.blockDim = dim3(kThreadsOf<FMT>);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = &at, cfg.numAttrs = p.wide ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, prefix_kernel<FMT>, map, rope, q, p) != cudaSuccess) return SMLA_ERR_CUDA;
+  cfg = cudaLaunchConfig_t{};
   // few rows: four blocks share a row's values; from 1,024 blocks on the GPU is full without
   cfg.gridDim = dim3(p.n_rows / kMergeRows, p.n_rows / kMergeRows < 1024 ? kDv / kMergeCols : 1);
   cfg.blockDim = dim3(kMergeThreads);
@@ -1562,7 +1579,10 @@ size_t layout(PrefixParams& p, uint8_t* ws, int32_t kv_dtype) {
   p.costs = costs_of(kv_dtype, p.wide);
   if (p.wide) {
     p.wide_rows = reinterpret_cast<uint16_t*>(ws + at);
-    at += static_cast<size_t>((p.shared_len + kPage - 1) / kPage) * kPage * kDqk * 2;
+    const size_t pages = (static_cast<size_t>(p.shared_len) + kPage - 1) / kPage;
+    at += pages * kPage * kDqk * 2;
+    p.wide_errors = reinterpret_cast<uint4*>(ws + at);
+    at += pages * sizeof(uint4);
   }
   return at;
 }
@@ -1617,8 +1637,6 @@ int smla_shared_prefix_fwd(const smla_paged_cache* cache, const int32_t* page_ta
     const uint64_t rows = static_cast<uint64_t>(bf16 ? cache->num_pages : pages) * kPage;
     if (!encode_chunks(&map, base, rows, kPage, 4) || !encode_chunks(&rope, base, rows, kPage, 1)) return SMLA_ERR_CUDA;
     if (!bf16) {
-      // (without the copy merge_kernel writes the status word; with it, it adds to widen_kernel's)
-      if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
       if (token) widen_kernel<kTokenFp8><<<dim3(pages, 4), 256, 0, st>>>(p);
       else widen_kernel<kTileFp8><<<dim3(pages, 4), 256, 0, st>>>(p);
       if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;

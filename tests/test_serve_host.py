@@ -113,9 +113,10 @@ def test_attention_refusals(L, kw, code):
 
 def test_attention_workspace_holds_the_wide_copy(L):
     size = lambda *a: L.smla_shared_prefix_fwd_workspace_size(*a)  # noqa: E731
-    # 3 x 2 tokens x 64 heads = 3 row blocks share 1,000 tokens (16 pages of 64 rows of 1,152 bytes)
+    # 3 x 2 tokens x 64 heads = 3 row blocks share 1,000 tokens (16 pages of 64 rows of 1,152 bytes,
+    # and four status words a page)
     for fp8 in (smla.SMLA_FP8_E4M3, smla.SMLA_FP8_DS_MLA):
-        assert size(3, 2500, 1000, 2, 64, fp8) == size(3, 2500, 1000, 2, 64, smla.SMLA_BF16) + 16 * 64 * 1152
+        assert size(3, 2500, 1000, 2, 64, fp8) == size(3, 2500, 1000, 2, 64, smla.SMLA_BF16) + 16 * (64 * 1152 + 16)
         # one row block, or one request (nothing is shared), has none
         assert size(2, 2500, 1000, 1, 64, fp8) == size(2, 2500, 1000, 1, 64, smla.SMLA_BF16)
         assert size(1, 2500, 1000, 9, 64, fp8) == size(1, 2500, 1000, 9, 64, smla.SMLA_BF16)
