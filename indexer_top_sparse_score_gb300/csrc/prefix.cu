@@ -36,6 +36,15 @@
 // A segment that is cut leaves several partial results (fp32 O with its maximum
 // and sums) that merge_kernel joins; no pair waits for another. Rows whose keys are
 // one uncut segment get their results at once.
+//
+// Bound by the tensor pipe: a tile's 44 MMAs take 2,376 cycles issued back to back,
+// a tile here 2,900 (BF16), the rest being the row maxima's way across the pair and
+// the starts of segments. 64 x 2 tokens of 64 heads on a 64K prompt: 735 us and 20 to
+// join, 1,620 TFLOP/s in this kernel, 85% of cuBLAS's bf16 rate (the tensor pipe is
+// active in 72% of the cycles of a call half that size). 1,024 tokens after 8K: 740 us and 20.
+// Per-token FP8, 64 x 2 on 16K: 216 us, 8 to widen, 20 to join, 1,250 TFLOP/s in all:
+// the requests' own keys, 6% of all, are 15% of the line's cost. One token
+// on 1,100 keys: 14.7 us, a chain of latencies: Q, three tiles a pair, results, join.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -52,11 +61,14 @@ namespace {
 
 constexpr int kRows = 128;       // rows of a block (MMA M)
 // Costs on the line of work, in quarters of a tile that comes by TMA (2,900 cycles
-// with BF16 rows, 3,100 with the 16-bit copy). Measured per CTA: starting a
-// segment (Q in, results out) 14,000 cycles with BF16 rows, 25,000 with FP8 ones; a
-// tile that is widened on the way 5,500 (per-token scales) and 7,800 (tile scales).
-// With equal weights the pairs that walk short segments end last: 64x2 on a 16K
-// prompt, FP8, at 345 us while the others end at 238.
+// with BF16 rows, 3,100 with the 16-bit copy): a segment's start (the pipeline
+// drains, Q in, results out), a tile of the shared part, a tile of a request's own
+// keys (FP8: widened on the way, 5,500 cycles with per-token scales, 7,800 with tile
+// scales). Starts and own tiles weighed too lightly leave the pairs that walk short
+// segments to end last. Measured over the start's cost: 64 x 2 tokens of 64 heads on
+// a 64K prompt, BF16, 850 / 834 / 825 / 842 us at 12 / 16 / 20 / 24; on a 16K prompt,
+// per-token FP8, 284 / 275 / 266 / 259 us at 20 / 26 / 32 / 38 with own tiles at 6, and
+// 254 / 253 / 258 at 38 / 44 / 56 with own tiles at 7.
 struct Costs {
   int32_t start, shared_tile, own_tile;
 };
@@ -1259,10 +1271,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
 // ------------------------------------------------------------------ the shared rows, widened
 // The shared pages' rows in logical order, as the MMAs take them: per-token codes in
 // bf16, exactly; tile-scaled values (code * scale) in f16, rounded (off by at most
-// 2^-11 of the value). Four blocks a
-// page, which read 37 or 42 KB and write 74 KB: bound by memory. Each row block of the batch would
-// widen them again otherwise (64x2 on a 16K prompt, FP8: 64 times, 329 us against
-// 243 with the copy).
+// 2^-11 of the value). Four blocks a page, which read 37 or 42 KB and write 74 KB:
+// bound by memory and, for short prompts, by latency (7.5 us for 16K tokens, 29 MB,
+// 3.8 TB/s; 4.2 us for 5K). Each row block of the batch would widen them again
+// otherwise: 64 x 2 tokens of 64 heads on 16K per-token rows (64 row blocks), 382 us
+// against 253 with the copy; 37 x 2 of 16 heads on 5K tile-scaled rows (10 row
+// blocks) 72 against 69.
 template <int FMT>
 __global__ void __launch_bounds__(256) widen_kernel(const PrefixParams p) {
   constexpr int kRowBytes = FMT == kTokenFp8 ? kDqk : kTileRowBytes;
@@ -1313,7 +1327,8 @@ __global__ void __launch_bounds__(256) widen_kernel(const PrefixParams p) {
 // the pieces of the rows' shared segment and of their own one, weighted by
 // 2^(m - largest m). Reading fp32 partials that were just written, it is bound by
 // L2 and, for few rows, by latency: up to four blocks share a row's values, and each
-// thread keeps eight 16-byte loads in flight.
+// thread keeps eight 16-byte loads in flight. It ends 20 us after prefix_kernel for
+// 8,192 rows of three or four pieces, 9 us after it for 1,184 rows, 5 us for 64.
 __device__ __forceinline__ float piece_sum(const PrefixParams& p, int slot, int at) {
   const float* l = p.part_l + static_cast<long long>(slot) * 4 * kRows + at;
   return (l[0] + l[kRows]) + (l[2 * kRows] + l[3 * kRows]);
