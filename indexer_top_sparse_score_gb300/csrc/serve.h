@@ -1,4 +1,4 @@
-// Host-side helpers of the serving calls (serve.cu, prefix.cu).
+// Helpers of the serving calls (serve.cu, prefix.cu).
 #pragma once
 #include <cstdint>
 
@@ -27,6 +27,24 @@ inline int check_serve_cache(const smla_paged_cache* c, bool need_kv, bool need_
     if (c->d_idx * (bf16 ? 2 : 1) != kIdxRowBytes) return SMLA_ERR_UNSUPPORTED;
   }
   return SMLA_OK;
+}
+
+// packed fp32: two independent IEEE operations an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 }  // namespace smla
