@@ -37,7 +37,7 @@ extern "C" {
  *               pages are written, all others are left as they are.
  *   free_pages  [n_free] int32: page ids to hand out (may be NULL if n_free = 0).
  *   max_new     rows of the per-token outputs (host bound on the sum of new_lens).
- *   seq_lens    [n_seqs] int32 out: tokens of b that have a slot afterwards
+ *   seq_lens    [n_seqs] int32 out: tokens of b that have a page afterwards
  *               (ctx + new); what smla_sparse_mla_decode and
  *               smla_shared_prefix_fwd take. Not the same array as ctx_lens.
  *   cu_new      [n_seqs + 1] int32 out: first output row of each request, and
@@ -51,8 +51,10 @@ extern "C" {
  * Device errors (SMLA_ERR_DEVICE_BOUNDS): negative lengths, or more than
  * max_pages * 64 tokens: the request counts as empty (seq_lens 0, no rows).
  * Rows past max_new: dropped, as if new_lens were smaller. Free list exhausted:
- * the tokens without a page get slot -1 and seq_lens stops before them. A
- * continued page whose table entry is negative: slot -1.
+ * the tokens without a page get slot -1 and seq_lens stops before them. A page id
+ * that no pool can have (negative, or 2^25 and more), of a continued page or taken
+ * from free_pages: the page's tokens get slot -1; the id stays in the table and
+ * seq_lens counts the tokens (the attention skips and reports the page again).
  * Workspace: 256 bytes.
  * ------------------------------------------------------------------------- */
 int smla_build_tables(const int32_t* ctx_lens, const int32_t* new_lens, int32_t n_seqs, int32_t* page_tables,

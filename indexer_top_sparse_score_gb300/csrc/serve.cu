@@ -31,6 +31,9 @@ struct TablesParams {
   int32_t rows_per_block;
 };
 
+// A page id that a pool can have (pool rows are int32).
+__device__ __forceinline__ bool page_id(int id) { return id >= 0 && id < (1 << 25); }
+
 // Inclusive sum over the block's threads; every thread also gets the total.
 __device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
       p.seq_lens[b] = static_cast<int>(ctx + got);
       p.cu[b] = cu0;
       if (b == p.n_seqs - 1) p.cu[p.n_seqs] = cu1;
-      if (got > 0 && ctx % kPage && p.tables[static_cast<long long>(b) * p.max_pages + ctx / kPage] < 0)
+      if (got > 0 && ctx % kPage && !page_id(p.tables[static_cast<long long>(b) * p.max_pages + ctx / kPage]))
         bad = kStatusBounds;
     }
     __syncthreads();
@@ -126,7 +129,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
         // written by the row that opens it), a continued page's from the table
         const int id = page < held_b ? row[page] : p.free_pages[s_free[lo] + page - held_b];
         if (page >= held_b && pos % kPage == 0) row[page] = id;
-        if (id >= 0 && id < (1 << 25)) slot = id * kPage + pos % kPage;  // (a pool has at most 2^25 pages)
+        if (page_id(id)) slot = id * kPage + pos % kPage;
       }
       p.slots[r] = slot;
       if (p.positions) p.positions[r] = pos;
@@ -142,10 +145,14 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
     if (p.row_seq) p.row_seq[r] = -1;
   }
   if (lead) {
+    const int taken = static_cast<int>(min(pages_before, static_cast<long long>(p.n_free)));
+#pragma unroll 4
+    for (int i = tid; i < taken; i += kTabThreads)
+      if (!page_id(p.free_pages[i])) bad = kStatusBounds;
     const int any = __syncthreads_or(bad != 0);
     if (tid == 0) {
       *p.status = any ? kStatusBounds : 0u;
-      *p.pages_used = static_cast<int>(min(pages_before, static_cast<long long>(p.n_free)));
+      *p.pages_used = taken;
     }
   }
 }

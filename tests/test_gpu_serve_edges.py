@@ -70,3 +70,40 @@ def test_query_codes_are_the_rounded_quotients(rows):
     scale, codes = _codes(raw.float().numpy())
     assert np.array_equal(wo.cpu().numpy(), scale)
     assert np.array_equal(qi.cpu().view(torch.float8_e4m3fn).float().numpy(), codes)
+
+
+# ---------------------------------------------------------------------------- tables
+def _tables(ctx, new, tables, free, max_new):
+    i = lambda a: torch.as_tensor(a, dtype=torch.int32).cuda()  # noqa: E731
+    tab = i(tables)
+    seq, cu, pos, slots, own, used, ws = smla.build_tables(i(ctx), i(new), tab, i(free), max_new)
+    return seq.tolist(), slots.tolist(), tab.tolist(), int(used), smla.read_status(ws)[0]
+
+
+@pytest.mark.parametrize("bad", [-1, -7, 1 << 25, 2 ** 31 - 1])
+def test_tables_report_unusable_ids_of_the_free_list(bad):
+    # 64 tokens and 70 more: pages free[0], free[1]; an empty request with 3: free[2]
+    for at in range(3):
+        free = [10, 11, 12, -1]  # (the last one is not taken)
+        free[at] = bad
+        seq, slots, tab, used, status = _tables([64, 0], [70, 3], [[5, -1, -1], [-1, -1, -1]], free, 73)
+        assert status == 5 and used == 3 and seq == [134, 3]
+        page = lambda i, rows: [-1] * rows if i == at else [free[i] * 64 + r for r in range(rows)]  # noqa: E731
+        assert slots == page(0, 64) + page(1, 6) + page(2, 3)
+        assert tab == [[5, free[0], free[1]], [free[2], -1, -1]]
+    assert _tables([64, 0], [70, 3], [[5, -1, -1], [-1, -1, -1]], [10, 11, 12, -1], 73)[4] == 0
+
+
+def test_tables_report_an_unusable_id_far_down_the_free_list():
+    free = np.arange(5000)
+    n, lens = 2000, [64] * 2000
+    assert _tables([0] * n, lens, [[-1]] * n, free, 64 * n)[4] == 0
+    free[1999] = -1
+    seq, slots, _, used, status = _tables([0] * n, lens, [[-1]] * n, free, 64 * n)
+    assert status == 5 and used == 2000 and slots[-65:] == [1998 * 64 + 63] + [-1] * 64
+
+
+@pytest.mark.parametrize("bad", [-1, 1 << 25])
+def test_tables_report_an_unusable_page_in_use(bad):
+    seq, slots, _, used, status = _tables([70], [60], [[5, bad, -1]], [9], 60)
+    assert status == 5 and slots == [-1] * 58 + [9 * 64, 9 * 64 + 1] and seq == [130] and used == 1
