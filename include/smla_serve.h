@@ -49,7 +49,7 @@ extern "C" {
  * Rows past cu_new[n_seqs] get -1 in all three (a batch padded to a captured
  * size: smla_cache_append skips slot -1).
  * Device errors (SMLA_ERR_DEVICE_BOUNDS): negative lengths, or more than
- * max_pages * 64 tokens: the request counts as empty (seq_lens 0, no rows).
+ * max_pages * 64 tokens (or 2^31 - 64): the request counts as empty (seq_lens 0, no rows).
  * Rows past max_new: dropped, as if new_lens were smaller. Free list exhausted:
  * the tokens without a page get slot -1 and seq_lens stops before them. A page id
  * that no pool can have (negative, or 2^25 and more), of a continued page or taken

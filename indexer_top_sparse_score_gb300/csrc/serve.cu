@@ -5,6 +5,7 @@
 // (prefill-sized calls).
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -74,6 +75,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
   const bool lead = blockIdx.x == 0;
   const long long first_row = static_cast<long long>(blockIdx.x) * p.rows_per_block;
   const long long last_row = min(first_row + p.rows_per_block, static_cast<long long>(p.max_new));
+  const long long most = min(static_cast<long long>(p.max_pages) * kPage, static_cast<long long>(INT_MAX) - (kPage - 1));
   long long rows_before = 0, pages_before = 0;  // of the chunks before this one
   uint32_t bad = 0;
   for (int c0 = 0; c0 < p.n_seqs; c0 += kTabThreads) {
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
     if (b < p.n_seqs) {
       ctx = p.ctx[b];
       add = p.add[b];
-      valid = ctx >= 0 && add >= 0 && ctx + add <= static_cast<long long>(p.max_pages) * kPage;
+      valid = ctx >= 0 && add >= 0 && ctx + add <= most;
       if (!valid) ctx = add = 0;
     }
     long long rows_total, pages_total;
@@ -644,7 +646,7 @@ int smla_build_tables(const int32_t* ctx_lens, const int32_t* new_lens, int32_t 
     if (!aligned_to(a, 4)) return SMLA_ERR_INVALID_ARG;
   if (seq_lens == ctx_lens || seq_lens == new_lens) return SMLA_ERR_INVALID_ARG;  // other blocks still read the lengths
   if (const int rc = check_ws(workspace, workspace_bytes)) return rc;
-  const int rows_per_block = std::max(kTabThreads, (max_new + 2 * num_sms() - 1) / (2 * num_sms()));
+  const int rows_per_block = std::max(kTabThreads, static_cast<int>((max_new + 2LL * num_sms() - 1) / (2 * num_sms())));
   TablesParams p{ctx_lens, new_lens, n_seqs, max_pages, page_tables, free_pages, n_free, max_new, seq_lens, cu_new, positions,
                  slots, row_seq, pages_used, static_cast<uint32_t*>(workspace), rows_per_block};
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(max_new) + rows_per_block - 1) / rows_per_block);

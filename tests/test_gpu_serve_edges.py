@@ -107,3 +107,19 @@ def test_tables_report_an_unusable_id_far_down_the_free_list():
 def test_tables_report_an_unusable_page_in_use(bad):
     seq, slots, _, used, status = _tables([70], [60], [[5, bad, -1]], [9], 60)
     assert status == 5 and slots == [-1] * 58 + [9 * 64, 9 * 64 + 1] and seq == [130] and used == 1
+
+
+def test_tables_lengths_next_to_the_end_of_int32():
+    """Positions and page numbers stay in 32 bits: 2^31 - 64 tokens are the most that a request can have."""
+    width, last = 1 << 25, 2 ** 31 - 64
+    tab = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    tab[0, last // 64 - 1] = 7
+    free = torch.tensor([9], dtype=torch.int32, device="cuda")
+    i = lambda a: torch.tensor([a], dtype=torch.int32, device="cuda")  # noqa: E731
+    seq, cu, pos, slots, _, used, ws = smla.build_tables(i(last - 3), i(3), tab, free, 4)
+    assert smla.read_status(ws)[0] == 0 and int(seq) == last and int(used) == 0
+    assert pos.tolist() == [last - 3, last - 2, last - 1, -1] and slots.tolist() == [7 * 64 + 61, 7 * 64 + 62, 7 * 64 + 63, -1]
+    for ctx, new in ((last - 3, 4), (last, 1), (last + 50, 1), (2 ** 31 - 1, 1), (2 ** 31 - 1, 0), (5, 2 ** 31 - 1)):
+        seq, cu, pos, slots, _, used, ws = smla.build_tables(i(ctx), i(new), tab, free, 4)
+        assert smla.read_status(ws)[0] == 5 and int(seq) == 0 and cu.tolist() == [0, 0] and int(used) == 0
+        assert slots.tolist() == [-1] * 4 and (tab == -1).sum() == width - 1
