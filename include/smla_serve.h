@@ -47,7 +47,7 @@ extern "C" {
  *   row_seq     [max_new] int32 out or NULL: its request.
  *   pages_used  [1] int32 out: entries of free_pages that were taken.
  * Rows past cu_new[n_seqs] get -1 in all three (a batch padded to a captured
- * size: smla_cache_append skips slot -1).
+ * size: smla_cache_append skips slot -1, smla_query_prep position -1).
  * Device errors (SMLA_ERR_DEVICE_BOUNDS): negative lengths, or more than
  * max_pages * 64 tokens (or 2^31 - 64): the request counts as empty (seq_lens 0, no rows).
  * Rows past max_new: dropped, as if new_lens were smaller. Free list exhausted:
@@ -110,6 +110,7 @@ int smla_cache_append(const smla_paged_cache* cache, const smla_rope* rope, int3
  * smla_query_prep — the queries of new tokens as the attention and the indexer
  * take them, every head in one pass.
  *
+ *   positions [rows] int32 (row of cos_sin); -1: the row is skipped (padding).
  *   q_pe      the 64 rope values of each attention head, bf16: head h of row i
  *             at q_pe + i * pe_row_stride + h * pe_head_stride values (multiples
  *             of 8), or NULL: no attention queries. Rotated and written to
@@ -124,7 +125,7 @@ int smla_cache_append(const smla_paged_cache* cache, const smla_rope* rope, int3
  *   w_out     [rows][h_idx] fp32 = w * (scale * w_scale) (bf16: w * w_scale),
  *             so that w_out * ReLU(q_idx . k) is the score's term: a positive
  *             scale passes through the ReLU. w [rows][h_idx] fp32; w_out may be w.
- * Device errors: a position outside [0, max_pos): the row is skipped.
+ * Device errors: another position outside [0, max_pos): the row is skipped.
  * Workspace: 256 bytes. Supported: n_heads 16 and 64, h_idx 4, 8, 16, 32, 64,
  * d_idx 128 (e4m3) and 64 (bf16).
  * ------------------------------------------------------------------------- */

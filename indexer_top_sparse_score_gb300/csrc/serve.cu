@@ -538,7 +538,7 @@ __device__ __forceinline__ void query_heads(const QueryParams& p, int row, int u
   if (p.idx_norm) load_weights(p.idx_norm, at, nw);
   const int pos = __ldg(p.positions + row);
   if (pos < 0 || pos >= p.max_pos) {
-    if (!p.first_reports) set_status(p.status, kStatusBounds);
+    if (pos != -1 && !p.first_reports) set_status(p.status, kStatusBounds);
     return;
   }
   const Turn turn(p.cos_sin, pos, sub);
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kRowThreads) query_prep_kernel(const QueryPara
   if (p.first_reports && blockIdx.x == 0) {
     report_rows(p.rows, p.status, [&](int r) {
       const int pos = __ldg(p.positions + r);
-      return pos < 0 || pos >= p.max_pos;
+      return pos != -1 && (pos < 0 || pos >= p.max_pos);
     });
     return;
   }
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kRowThreads) query_prep_kernel(const QueryPara
   }
   const int pos = __ldg(p.positions + row);
   if (pos < 0 || pos >= p.max_pos) {
-    if (!p.first_reports) set_status(p.status, kStatusBounds);
+    if (pos != -1 && !p.first_reports) set_status(p.status, kStatusBounds);
     return;
   }
   const Turn turn(p.cos_sin, pos, sub);

@@ -123,3 +123,27 @@ def test_tables_lengths_next_to_the_end_of_int32():
         seq, cu, pos, slots, _, used, ws = smla.build_tables(i(ctx), i(new), tab, free, 4)
         assert smla.read_status(ws)[0] == 5 and int(seq) == 0 and cu.tolist() == [0, 0] and int(used) == 0
         assert slots.tolist() == [-1] * 4 and (tab == -1).sum() == width - 1
+
+
+# ---------------------------------------------------------------------------- padding
+def test_query_skips_the_padding_of_the_tables():
+    """Rows past a batch's own have position -1 (build_tables): nothing is written, nothing reported."""
+    rope = sc.rope_table(100).cuda()
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    _, _, pos, slots, _, _, ws = smla.build_tables(i([3, 0]), i([2, 1]), i([[4], [-1]]), i([7]), 8)
+    assert smla.read_status(ws)[0] == 0 and pos.tolist() == [3, 4, 0] + [-1] * 5
+    for rows in (8, 5000):  # (past 4,096 rows the warps report)
+        p = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+        p[:8] = pos
+        q = torch.full((rows, 16, 576), 7.0, dtype=torch.bfloat16, device="cuda")
+        qi = torch.full((rows, 4, 128), 9, dtype=torch.uint8, device="cuda")
+        wo = torch.full((rows, 4), 5.0, device="cuda")
+        _, _, _, ws = smla.query_prep(p, rope, q_pe=torch.ones(rows, 16, 64, dtype=torch.bfloat16, device="cuda"), q=q, q_idx=qi, w_out=wo,
+                                      q_idx_raw=torch.ones(rows, 4, 128, dtype=torch.bfloat16, device="cuda"), w=torch.ones(rows, 4, device="cuda"))
+        assert smla.read_status(ws)[0] == 0
+        assert (q[3:] == 7).all() and (qi[3:] == 9).all() and (wo[3:] == 5).all()
+        assert (q[:3, :, 512:] != 7).any(-1).all() and (wo[:3] != 5).all()
+        for bad in (-2, 100):
+            p[5] = bad
+            _, _, _, ws = smla.query_prep(p, rope, q_pe=torch.ones(rows, 16, 64, dtype=torch.bfloat16, device="cuda"), q=q)
+            assert smla.read_status(ws)[0] == 5
