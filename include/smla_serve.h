@@ -142,7 +142,9 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
  * values, PV over the first 512, as smla_sparse_mla_fwd).
  *
  * Tokens 0 .. shared_len - 1 are the same for every request. They are read
- * through page_tables[0] only, once for all query rows of the batch together;
+ * through page_tables[0] only, once for all query rows of the batch together
+ * (so row 0 lists the shared pages even where request 0 is idle; pages past every
+ * request's length are not looked at);
  * tokens from shared_len on are read through each request's own table. The two
  * parts are joined by their log-sum-exp. shared_len need not end on a page: the
  * page that holds the border is read through row 0 before it and through

@@ -82,6 +82,7 @@ constexpr int kOffQ = 0, kOffKO = 3 * kQChunk, kOffKV = kOffKO + 5 * kChunk, kOf
 constexpr float kRaise = 8.0f;   // log2: the reference maximum is raised only when exceeded by this much
 constexpr int kMaxPairs = 128;
 constexpr int kMaxPieces = kMaxPairs + 2;  // of a row: its two segments are walked by distinct pairs, but for one at each border
+constexpr int kEnds = 768, kGroups = 512;
 constexpr int kTileRowBytes = 656, kTileRope = 528;
 constexpr int kSoftWarps = 8, kMmaWarp = 0, kTmaWarp = 1, kSoftWarp0 = 4;
 constexpr int kPHalf = kRows * 64;  // P of half a page: 128 rows x 32 keys, 64-byte swizzled
@@ -103,7 +104,9 @@ struct PrefixParams {
   float* lse;
   uint32_t* status;
   int32_t n_rows;     // tokens * heads
-  int32_t n_rb, n_pt; // row blocks and tiles of the shared part (n_rb = 0: nothing shared)
+  int32_t n_rb;       // row blocks of the shared part (0: nothing shared)
+  int32_t end_shift;  // 2^end_shift row blocks form a group with one end of the shared part
+  int32_t n_groups;   // (kGroups at most)
   int32_t rb_s;       // row blocks of one request
   int32_t n_seg, pairs;
   Costs costs;
@@ -111,7 +114,7 @@ struct PrefixParams {
   int32_t q_sectors;  // q starts on a 32-byte boundary
   int32_t wide;       // FP8: the shared rows are read from their 16-bit copy
   uint16_t* wide_rows;  // [shared pages * 64][576]
-  long long* seg_off; // [i] where own segment i starts on the line; -1: one piece walks it and writes the results itself
+  long long* seg_off; // [s] where segment s starts on the line; -1: one piece walks it and writes the results itself
   long long* bounds;  // [pairs + 1] where each pair's stretch starts
   uint32_t* errors;   // [2 * pairs] status bits of each CTA
   uint4* wide_errors; // [shared pages] of each page's four blocks of widen_kernel
@@ -124,19 +127,37 @@ struct PrefixParams {
 __device__ __forceinline__ int length_of(const PrefixParams& p, int b) {
   return max(0, min(__ldg(p.seq_lens + b), p.max_seq_len));
 }
+// Keys of the shared part that some token of the row blocks of group g sees: a block of
+// idle requests, or of requests that end before the shared part does, walks no more.
+__device__ __forceinline__ int shared_end(const PrefixParams& p, int g) {
+  const int n = (kRows >> p.hshift) << p.end_shift, first = g * n, last = min(first + n, p.n_rows >> p.hshift);  // its tokens
+  int b = first / p.q_per_seq, j = first - b * p.q_per_seq, end = 0;
+#pragma unroll 4
+  for (int k = first; k < last; ++k) {
+    end = max(end, length_of(p, b) - p.q_per_seq + j + 1);
+    if (++j == p.q_per_seq) j = 0, ++b;
+  }
+  return min(end, p.shared_len);
+}
 // Keys that the last token of own segment i sees.
 __device__ __forceinline__ int own_end(const PrefixParams& p, int i) {
   const int b = i / p.rb_s, rb = i - b * p.rb_s;
   const int j = min(p.q_per_seq - 1, (rb * kRows + kRows - 1) >> p.hshift);
   return length_of(p, b) - p.q_per_seq + j + 1;
 }
-__device__ __forceinline__ int own_tiles(const PrefixParams& p, int i) {
-  const int end = own_end(p, i);
+__device__ __forceinline__ int own_tiles(const PrefixParams& p, int end) {
   if (end <= p.shared_len) return 0;
   return ((end + kPage - 1) / kPage - p.shared_len / kPage + 1) >> 1;
 }
-__device__ __forceinline__ int seg_tiles(const PrefixParams& p, int s) {
-  return s < p.n_rb ? p.n_pt : own_tiles(p, s - p.n_rb);
+__device__ __forceinline__ int shared_tiles(int end) { return (end + 2 * kPage - 1) / (2 * kPage); }
+// The same from the CTA's table: the groups' ends, then those of the own segments as far as it reaches.
+__device__ __forceinline__ int seg_end(const PrefixParams& p, const int* ends, int s) {
+  const int at = s < p.n_rb ? s >> p.end_shift : s - p.n_rb + p.n_groups;
+  return at < kEnds ? ends[at] : own_end(p, s - p.n_rb);
+}
+__device__ __forceinline__ int seg_tiles(const PrefixParams& p, const int* ends, int s) {
+  const int end = seg_end(p, ends, s);
+  return s < p.n_rb ? shared_tiles(end) : own_tiles(p, end);
 }
 __device__ __forceinline__ int seg_cost(const PrefixParams& p, int s, int tiles) {
   return tiles > 0 ? p.costs.start + tiles * (s < p.n_rb ? p.costs.shared_tile : p.costs.own_tile) : 0;
@@ -159,10 +180,10 @@ struct Piece {
   bool whole;     // all of them
 };
 
-__device__ __forceinline__ bool piece_after(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
+__device__ __forceinline__ bool piece_after(const PrefixParams& p, const int* ends, Line& L, Piece& pc, bool writer) {
   while (L.s < p.n_seg && L.a < L.y) {
     const int s = L.s++;
-    const int tiles = seg_tiles(p, s), cost = seg_cost(p, s, tiles);
+    const int tiles = seg_tiles(p, ends, s), cost = seg_cost(p, s, tiles);
     const long long a = L.a;
     if (cost == 0) continue;
     L.a += cost;
@@ -171,7 +192,7 @@ __device__ __forceinline__ bool piece_after(const PrefixParams& p, Line& L, Piec
       pc.s = s;
       pc.whole = pc.t0 == 0 && pc.t1 == tiles;
       // (the pair with the first tile writes it)
-      if (writer && s >= p.n_rb && pc.t0 == 0) p.seg_off[s - p.n_rb] = pc.whole && p.n_rb == 0 ? -1 : a;
+      if (writer && pc.t0 == 0) p.seg_off[s] = pc.whole && p.n_rb == 0 ? -1 : a;
       return true;
     }
   }
@@ -179,10 +200,10 @@ __device__ __forceinline__ bool piece_after(const PrefixParams& p, Line& L, Piec
 }
 
 // Through copies, so that the caller's own stay in registers.
-__device__ __forceinline__ bool next_piece(const PrefixParams& p, Line& L, Piece& pc, bool writer) {
+__device__ __forceinline__ bool next_piece(const PrefixParams& p, const int* ends, Line& L, Piece& pc, bool writer) {
   Line line = L;
   Piece piece;
-  const bool more = piece_after(p, line, piece, writer);
+  const bool more = piece_after(p, ends, line, piece, writer);
   L = line;
   if (more) pc = piece;
   return more;
@@ -195,6 +216,7 @@ struct Tiles {
   int t;
   const int32_t* table;
   int first_page, end_page;  // of the segment
+  int seen_page;             // end of the pages that some row of the segment sees
   int own_id, other_id;      // table entries of the tile's page `rank` and of the other one (kNoPage past the end);
                              // loaded a tile ahead and looked at when the tile is
   static constexpr int kNoPage = INT_MIN;
@@ -202,26 +224,30 @@ struct Tiles {
   __device__ __forceinline__ int entry(int i) const { return i < end_page ? __ldg(table + i) : kNoPage; }
   // pool page of an entry, -1: none
   static __device__ __forceinline__ int pool_page(const PrefixParams& p, int id) { return id >= 0 && id < p.num_pages ? id : -1; }
-  __device__ __forceinline__ bool bad(const PrefixParams& p) const {
-    return (own_id != kNoPage && pool_page(p, own_id) < 0) || (other_id != kNoPage && pool_page(p, other_id) < 0);
+  // a page that a row sees is missing
+  __device__ __forceinline__ bool bad(const PrefixParams& p, int rank) const {
+    const int page = first_page + 2 * t;
+    return (page + rank < seen_page && pool_page(p, own_id) < 0) || (page + (rank ^ 1) < seen_page && pool_page(p, other_id) < 0);
   }
-  __device__ __forceinline__ bool next_segment(const PrefixParams& p) {
-    if (!next_piece(p, line, pc, false)) return false;
+  __device__ __forceinline__ bool next_segment(const PrefixParams& p, const int* ends) {
+    if (!next_piece(p, ends, line, pc, false)) return false;
     t = pc.t0;
+    const int end = seg_end(p, ends, pc.s);
     if (pc.s < p.n_rb) {
       table = p.page_tables;
       first_page = 0;
       end_page = (p.shared_len + kPage - 1) / kPage;
+      seen_page = (end + kPage - 1) / kPage;
     } else {
       const int i = pc.s - p.n_rb;
       table = p.page_tables + static_cast<long long>(i / p.rb_s) * p.max_pages;
       first_page = p.shared_len / kPage;
-      end_page = (own_end(p, i) + kPage - 1) / kPage;
+      end_page = seen_page = (end + kPage - 1) / kPage;
     }
     return true;
   }
-  __device__ __forceinline__ bool next(const PrefixParams& p, int rank, bool fresh) {
-    if ((fresh || ++t >= pc.t1) && !next_segment(p)) return false;
+  __device__ __forceinline__ bool next(const PrefixParams& p, const int* ends, int rank, bool fresh) {
+    if ((fresh || ++t >= pc.t1) && !next_segment(p, ends)) return false;
     own_id = entry(first_page + 2 * t + rank);
     other_id = entry(first_page + 2 * t + (rank ^ 1));
     return true;
@@ -452,6 +478,7 @@ struct Meta {
   uint64_t s_full, s_free, p_own, pv_done, o_free;
   uint64_t mx_full[2][4];
   long long scan[34];
+  int ends[kEnds];            // seg_end
   long long start_a;
   int start_s;
   uint32_t tmem_slot, status;
@@ -643,10 +670,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
   // ---- the length of the line, this pair's stretch, and the segment it begins in
   Line line;
   {
-    const int n_own = p.n_seg - p.n_rb;
-    const long long shared_cost = static_cast<long long>(p.n_rb) * seg_cost(p, 0, p.n_pt);
-    long long sum = 0;
-    for (int i = tid; i < n_own; i += kThreads) sum += seg_cost(p, p.n_rb + i, own_tiles(p, i));
+    for (int i = tid; i < min(p.n_groups + p.n_seg - p.n_rb, kEnds); i += kThreads)
+      M.ends[i] = i < p.n_groups ? shared_end(p, i) : own_end(p, i - p.n_groups);
+    if (p.end_shift > 0) __syncthreads();  // (otherwise a thread reads the ends that it wrote)
+    const long long first_cost = tid < p.n_seg ? seg_cost(p, tid, seg_tiles(p, M.ends, tid)) : 0;
+    long long sum = first_cost;
+    for (int i = tid + kThreads; i < p.n_seg; i += kThreads) sum += seg_cost(p, i, seg_tiles(p, M.ends, i));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     if (lane == 0) M.scan[warp] = sum;
@@ -654,7 +683,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       for (int b = tid; b < p.n_seqs; b += kThreads)
         if (__ldg(p.seq_lens + b) > p.max_seq_len) set_status(&M.status, kStatusBounds);
     __syncthreads();
-    long long total = shared_cost;
+    long long total = 0;
     for (int w = 0; w < kThreads / 32; ++w) total += M.scan[w];
     line.x = total * pair / p.pairs;
     line.y = total * (pair + 1) / p.pairs;
@@ -663,36 +692,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       if (pair == p.pairs - 1) p.bounds[p.pairs] = line.y;
     }
     if (line.x < line.y) {
-      if (line.x < shared_cost) {
-        if (tid == 0) {
-          M.start_s = static_cast<int>(line.x / seg_cost(p, 0, p.n_pt));
-          M.start_a = static_cast<long long>(M.start_s) * seg_cost(p, 0, p.n_pt);
-        }
-      } else {
-        long long before = shared_cost;
-        for (int c0 = 0; c0 < n_own && before <= line.x; c0 += kThreads) {
-          const int i = c0 + tid;
-          const long long cost = i < n_own ? seg_cost(p, p.n_rb + i, own_tiles(p, i)) : 0;
-          long long v = cost;
+      long long before = 0;
+      for (int c0 = 0; c0 < p.n_seg && before <= line.x; c0 += kThreads) {
+        const int i = c0 + tid;
+        const long long cost = c0 == 0 ? first_cost : i < p.n_seg ? seg_cost(p, i, seg_tiles(p, M.ends, i)) : 0;
+        long long v = cost;
 #pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-            if (lane >= d) v += o;
-          }
-          __syncthreads();
-          if (lane == 31) M.scan[warp] = v;
-          __syncthreads();
-          long long all = 0;
-          for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) v += M.scan[w];
-            all += M.scan[w];
-          }
-          if (before + v - cost <= line.x && line.x < before + v) {
-            M.start_s = p.n_rb + i;
-            M.start_a = before + v - cost;
-          }
-          before += all;
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+          if (lane >= d) v += o;
         }
+        __syncthreads();
+        if (lane == 31) M.scan[warp] = v;
+        __syncthreads();
+        long long all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+          if (w < warp) v += M.scan[w];
+          all += M.scan[w];
+        }
+        if (before + v - cost <= line.x && line.x < before + v) {
+          M.start_s = i;
+          M.start_a = before + v - cost;
+        }
+        before += all;
       }
     }
   }
@@ -723,7 +745,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     Line wline = line;
     Piece pc, nx;
     nx.s = 0;
-    bool have = next_piece(p, wline, nx, writer), started = false;
+    bool have = next_piece(p, M.ends, wline, nx, writer), started = false;
     if (have && half == 0) prefetch_q(p, nx.s, row);
     Tiles cur;  // one ahead of the tile that is worked on: its page ids have arrived when they are used
     cur.line = line;
@@ -809,10 +831,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         if (lane == 0) mbar_arrive(&M.o_free);
       } else if (have) {
         next_lim = limits(p, nx.s, row);
-        more = cur.next(p, rank, true);
+        more = cur.next(p, M.ends, rank, true);
         own_next = Tiles::pool_page(p, cur.own_id);
         if (FMT == kTokenFp8) scale = load_scale();
-        more = cur.next(p, rank, false);
+        more = cur.next(p, M.ends, rank, false);
       }
       if (!have) break;
       started = true;
@@ -820,7 +842,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       lim = next_lim;
       const int first_page = pc.s < p.n_rb ? 0 : p.shared_len / kPage;
       m = -INFINITY, l = 0.0f;
-      have = next_piece(p, wline, nx, writer);
+      have = next_piece(p, M.ends, wline, nx, writer);
       if (have) {
         if (half == 0) prefetch_q(p, nx.s, row);
         next_lim = limits(p, nx.s, row);
@@ -842,7 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
           if (more) scale = load_scale();
         }
         own_next = more ? Tiles::pool_page(p, cur.own_id) : -1;
-        if (more) more = cur.next(p, rank, false);
+        if (more) more = cur.next(p, M.ends, rank, false);
         if (!wait_warp<false>(&M.s_full, g & 1, abort_v)) {
           ok = false;
           break;
@@ -967,7 +989,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       const int v0 = 4 * rank, k0 = 4 * (rank ^ 1);  // first chunk of this CTA's output values, of the others
       Tiles cur;
       cur.line = line;
-      bool more = cur.next(p, rank, true);
+      bool more = cur.next(p, M.ends, rank, true);
       // where a page's rows lie in the map: pool rows, or (FP8) rows of the shared part's
       // copy; -64 for a page that is missing: a box wholly before the rows reads as zeros
       auto place = [&](int id, int i) {
@@ -994,11 +1016,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       for (; more && ok; ++g) {
         const bool by_tma = FMT == kBf16 || (p.wide && cur.pc.s < p.n_rb);
         const int y = place(cur.own_id, rank), other_y = place(cur.other_id, rank ^ 1);
-        if (FMT == kBf16 && cur.bad(p)) set_status(&M.status, kStatusBounds);
+        if (FMT == kBf16 && cur.bad(p, rank)) set_status(&M.status, kStatusBounds);
         const bool new_piece = cur.t == cur.pc.t0;
         int rows;
         const int q_row = static_cast<int>(first_row(p, cur.pc.s, rows));
-        more = cur.next(p, rank, false);
+        more = cur.next(p, M.ends, rank, false);
         if (g > 0 && !wait_one<false>(&M.ko_free, (g - 1) & 1, abort_v)) { ok = false; break; }
         if (by_tma) {
           mbar_arrive_expect_tx(&M.ko_full, 5 * kChunk);
@@ -1119,7 +1141,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
       __syncwarp();
       return true;
     };
-    while (ok && next_piece(p, wline, pc, false)) {
+    while (ok && next_piece(p, M.ends, wline, pc, false)) {
       if (!wait(&M.q_full, n & 1)) { ok = false; break; }
       const int t0 = __shfl_sync(0xFFFFFFFFu, pc.t0, 0), t1 = __shfl_sync(0xFFFFFFFFu, pc.t1, 0);
       // the logits of a tile are issued before the product of the tile before it
@@ -1206,14 +1228,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     };
     Tiles cur;
     cur.line = line;
-    bool more = cur.next(p, rank, true);
+    bool more = cur.next(p, M.ends, rank, true);
     auto mine = [&] { return !(p.wide && cur.pc.s < p.n_rb); };  // not a tile of the copy
     bool here = more && mine();
     if (here) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
     for (uint32_t g = 0; more; ++g) {
       const bool stores = here;
-      if (stores && group == 0 && cur.bad(p) && lane == 0) set_status(&M.status, kStatusBounds);
-      more = cur.next(p, rank, false);
+      if (group == 0 && cur.bad(p, rank) && lane == 0) set_status(&M.status, kStatusBounds);
+      more = cur.next(p, M.ends, rank, false);
       here = more && mine();
       // the slots' previous tile: g - 1, or g - 2 for KV's two buffers
       const uint32_t back = group == 1 ? 2 : 1;
@@ -1302,7 +1324,7 @@ __global__ void __launch_bounds__(256) widen_kernel(const PrefixParams p) {
   }
   over = __syncthreads_or(over || top > 65504.0f);
   if (threadIdx.x == 0)
-    reinterpret_cast<uint32_t*>(p.wide_errors)[4 * blockIdx.x + blockIdx.y] = (over ? kStatusOverflow : 0u) | (live ? 0u : kStatusBounds);
+    reinterpret_cast<uint32_t*>(p.wide_errors)[4 * blockIdx.x + blockIdx.y] = over ? kStatusOverflow : 0u;
 }
 
 // ------------------------------------------------------------------ joining the pieces
@@ -1335,11 +1357,11 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
     const int per = p.q_per_seq << p.hshift, b = r0 / per, in = r0 - b * per;
     seg[0] = r0 / kRows, at[0] = r0 % kRows;
     seg[1] = p.n_rb + b * p.rb_s + in / kRows, at[1] = in % kRows;
-    tiles[0] = p.n_rb > 0 ? p.n_pt : 0;
-    tiles[1] = seg_tiles(p, seg[1]);
+    tiles[0] = p.n_rb > 0 ? shared_tiles(shared_end(p, seg[0] >> p.end_shift)) : 0;
+    tiles[1] = own_tiles(p, own_end(p, seg[1] - p.n_rb));
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long own_at = tiles[1] > 0 ? p.seg_off[seg[1] - p.n_rb] : 0;
+  const long long own_at = tiles[1] > 0 ? p.seg_off[seg[1]] : 0, shared_at = tiles[0] > 0 ? p.seg_off[seg[0]] : 0;
   const bool done = own_at < 0;
   if (done && blockIdx.x != 0) return;
   for (int q = tid; q <= p.pairs; q += kMergeThreads) bounds[q] = p.bounds[q];
@@ -1370,7 +1392,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
     for (int part = 0; part < 2; ++part) {
       if (tiles[part] == 0) continue;
       const int s = seg[part];
-      const long long a = part == 1 ? own_at : static_cast<long long>(s) * seg_cost(p, 0, p.n_pt);
+      const long long a = part == 1 ? own_at : shared_at;
       for (int base = 0; base < p.pairs; base += 32) {
         const int q = base + lane;
         int t0 = 0, t1 = 0;
@@ -1552,8 +1574,10 @@ bool plan(PrefixParams& p) {
   p.n_rows = static_cast<int32_t>(rows);
   p.rb_s = static_cast<int32_t>(rb_s);
   p.n_rb = static_cast<int32_t>(n_rb);
+  p.end_shift = 0;
+  while (((n_rb - 1) >> p.end_shift) >= kGroups) ++p.end_shift;
+  p.n_groups = n_rb > 0 ? static_cast<int32_t>((n_rb - 1) >> p.end_shift) + 1 : 0;
   p.n_seg = static_cast<int32_t>(n_seg);
-  p.n_pt = (p.shared_len + 2 * kPage - 1) / (2 * kPage);
   p.pairs = pairs_of_device();
   return true;
 }
@@ -1566,7 +1590,7 @@ size_t layout(PrefixParams& p, uint8_t* ws, int32_t kv_dtype) {
   p.errors = reinterpret_cast<uint32_t*>(ws + at);
   at += up256(static_cast<size_t>(p.pairs) * 2 * 4);
   p.seg_off = reinterpret_cast<long long*>(ws + at);
-  at += up256(static_cast<size_t>(p.n_seg - p.n_rb) * 8);
+  at += up256(static_cast<size_t>(p.n_seg) * 8);
   p.part_m = reinterpret_cast<float*>(ws + at);
   at += slots * kRows * 4;
   p.part_l = reinterpret_cast<float*>(ws + at);

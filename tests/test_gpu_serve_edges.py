@@ -72,6 +72,58 @@ def test_query_codes_are_the_rounded_quotients(rows):
     assert np.array_equal(qi.cpu().view(torch.float8_e4m3fn).float().numpy(), codes)
 
 
+# ---------------------------------------------------------------------------- idle requests
+def _attend(c, tab, sl, q, qt, shared, max_len=None, scale=sc.SM_SCALE):
+    m = max(1, int(sl.max()), shared) if max_len is None else max_len
+    out, lse, ws = smla.shared_prefix_fwd(c.to("cuda"), tab.cuda(), sl.cuda(), m, shared, q, qt.cuda(), scale)
+    return out, lse, smla.read_status(ws)[0]
+
+
+@pytest.mark.parametrize("kv_dtype", FORMATS)
+@pytest.mark.parametrize("n,q,heads", [(2, 1, 16), (5, 2, 64)])  # one and several row blocks
+def test_attention_of_an_idle_batch_looks_at_no_page(kv_dtype, n, q, heads):
+    c, tab, sl, qt = sc.attention_case(n, q, heads, kv_dtype, 200, [0] * n, seed=26)
+    tab[:] = -1
+    out, lse, status = _attend(c, tab, sl, q, qt, 200, max_len=256)
+    assert status == 0 and (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("kv_dtype", FORMATS)
+@pytest.mark.parametrize("n,q,heads", [(3, 1, 16), (6, 2, 64)])
+def test_attention_pages_past_every_length_need_not_exist(kv_dtype, n, q, heads):
+    lens = [130, 70, 0, 5, 129, 0][:n]
+    c, tab, sl, qt = sc.attention_case(n, q, heads, kv_dtype, 700, lens, seed=27)
+    tab[:, 3:] = -1
+    out, lse, status = _attend(c, tab, sl, q, qt, 700)
+    assert status == 0
+    sc.check_attention(out, lse, sc.attention_reference(c, tab, sl, q, qt, 700, sc.SM_SCALE), kv_dtype)
+    tab[0, 2] = -1  # keys 128 and 129: seen by request 0 (and 4)
+    out, lse, status = _attend(c, tab, sl, q, qt, 700)
+    assert status == 5
+    sc.check_attention(out, lse, sc.attention_reference(c, tab, sl, q, qt, 700, sc.SM_SCALE), kv_dtype)
+
+
+@pytest.mark.parametrize("kv_dtype", FORMATS)
+def test_attention_idle_requests_among_others(kv_dtype):
+    """Row blocks of idle requests between others, the first among them: its table lists the prompt all the same."""
+    lens = [0, 0, 0, 900, 0, 650, 0, 0, 0, 0, 701, 0, 40, 0]
+    c, tab, sl, qt = sc.attention_case(14, 1, 64, kv_dtype, 640, lens, seed=28)
+    out, lse, status = _attend(c, tab, sl, 1, qt, 640)
+    assert status == 0
+    sc.check_attention(out, lse, sc.attention_reference(c, tab, sl, 1, qt, 640, sc.SM_SCALE), kv_dtype)
+
+
+@pytest.mark.parametrize("kv_dtype", FORMATS)
+def test_attention_more_row_blocks_than_the_table_of_ends_holds(kv_dtype):
+    """1,040 requests of 64 heads: 520 row blocks share 130 keys, two of them an end; whole blocks of them are idle."""
+    rng = np.random.default_rng(29)
+    lens = np.where(np.arange(1040) % 37 < 9, rng.integers(0, 190, 1040), 0).tolist()
+    c, tab, sl, qt = sc.attention_case(1040, 1, 64, kv_dtype, 130, lens, seed=29)
+    out, lse, status = _attend(c, tab, sl, 1, qt, 130)
+    assert status == 0
+    sc.check_attention(out, lse, sc.attention_reference(c, tab, sl, 1, qt, 130, sc.SM_SCALE), kv_dtype)
+
+
 # ---------------------------------------------------------------------------- tables
 def _tables(ctx, new, tables, free, max_new):
     i = lambda a: torch.as_tensor(a, dtype=torch.int32).cuda()  # noqa: E731
