@@ -167,8 +167,8 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
  * bf16 operands (q, rows and codes as they are, the probabilities rounded to bf16;
  * the scales multiply logits and probabilities in fp32). Tile-scaled FP8 rows: f16
  * operands (values and probabilities rounded to f16), so |q| and the values must
- * stay below 65504; beyond it smla_read_status gives SMLA_ERR_UNSUPPORTED, as for
- * smla_sparse_mla_fwd.
+ * stay below 65504; beyond it, in a row that sees a key or a key that a row sees,
+ * smla_read_status gives SMLA_ERR_UNSUPPORTED, as for smla_sparse_mla_fwd.
  * Keys that a row does not see never reach it, whatever they hold (an unused
  * slot of a page may hold NaN).
  * Supported: n_heads 16 and 64; any q_per_seq >= 1; the three cache formats.

@@ -117,7 +117,7 @@ struct PrefixParams {
   long long* seg_off; // [s] where segment s starts on the line; -1: one piece walks it and writes the results itself
   long long* bounds;  // [pairs + 1] where each pair's stretch starts
   uint32_t* errors;   // [2 * pairs] status bits of each CTA
-  uint4* wide_errors; // [shared pages] of each page's four blocks of widen_kernel
+  uint4* wide_over;   // [shared pages] tile-scaled: which of each page's 4 x 16 keys hold a value outside f16's range
   float* part_m;      // [slot][128]
   float* part_l;      // [slot][4][128]: sums of each CTA's two halves
   float4* part_o;     // [slot][2][64][128]: four output values of a row
@@ -217,6 +217,7 @@ struct Tiles {
   const int32_t* table;
   int first_page, end_page;  // of the segment
   int seen_page;             // end of the pages that some row of the segment sees
+  int first_key, end_key;    // keys that some row sees
   int own_id, other_id;      // table entries of the tile's page `rank` and of the other one (kNoPage past the end);
                              // loaded a tile ahead and looked at when the tile is
   static constexpr int kNoPage = INT_MIN;
@@ -233,15 +234,17 @@ struct Tiles {
     if (!next_piece(p, ends, line, pc, false)) return false;
     t = pc.t0;
     const int end = seg_end(p, ends, pc.s);
+    end_key = end;
     if (pc.s < p.n_rb) {
       table = p.page_tables;
-      first_page = 0;
+      first_page = first_key = 0;
       end_page = (p.shared_len + kPage - 1) / kPage;
       seen_page = (end + kPage - 1) / kPage;
     } else {
       const int i = pc.s - p.n_rb;
       table = p.page_tables + static_cast<long long>(i / p.rb_s) * p.max_pages;
       first_page = p.shared_len / kPage;
+      first_key = p.shared_len;
       end_page = seen_page = (end + kPage - 1) / kPage;
     }
     return true;
@@ -543,9 +546,12 @@ __device__ __forceinline__ void ldg32(const void* p, uint32_t* v) {
 // TMA unless their values change on the way (f16, a negative scale): then eight lanes
 // bring a row's chunk in 16-byte pieces. More chunks in flight push the tile
 // loops' values into local memory, and next to 225 KB of shared memory there is
-// hardly any L1 to hold that. Returns whether a value was outside f16's range.
+// hardly any L1 to hold that. Returns whether a value was outside f16's range. f16:
+// rows that are not in `live` (they see no key of the segment) count as zeros, whatever
+// they hold.
 template <int FMT>
-__device__ __forceinline__ bool load_q(const PrefixParams& p, int s, uint8_t* q_smem, uint32_t q_tmem, int rank, int quad, int half) {
+__device__ __forceinline__ bool load_q(const PrefixParams& p, int s, uint8_t* q_smem, uint32_t q_tmem, int rank, int quad, int half,
+                                       uint32_t live) {
   constexpr bool F16 = FMT == kTileFp8;
   constexpr int kBatch = FMT == kBf16 ? 3 : 1;
   const int lane = threadIdx.x & 31;
@@ -569,7 +575,7 @@ __device__ __forceinline__ bool load_q(const PrefixParams& p, int s, uint8_t* q_
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const uint16_t* at = src + lane * kDqk + chunk_of(c0 + u) * 64;
-      if (lane >= limit) {
+      if (lane >= limit || (F16 && !(live >> lane & 1))) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[u][j] = 0;
       } else if (p.q_sectors) {
@@ -599,7 +605,7 @@ __device__ __forceinline__ bool load_q(const PrefixParams& p, int s, uint8_t* q_
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = 16 * half + 4 * j + sub;
-        w[j] = r < limit ? __ldg(reinterpret_cast<const uint4*>(src + r * kDqk + chunk_of(c) * 64 + pcs * 8)) : make_uint4(0, 0, 0, 0);
+        w[j] = r < limit && (!F16 || (live >> r & 1)) ? __ldg(reinterpret_cast<const uint4*>(src + r * kDqk + chunk_of(c) * 64 + pcs * 8)) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -776,7 +782,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     while (ok) {
       // the next piece's Q while the last product of this one runs, then this one's results
       if (have) {
-        over |= load_q<FMT>(p, nx.s, smem + kOffQ, tmem + lanes + kColQ, rank, quad, half);
+        if (F16 && !started) next_lim = limits(p, nx.s, row);
+        const uint32_t live = F16 ? __ballot_sync(0xFFFFFFFFu, next_lim.hi > next_lim.lo) : 0;
+        over |= load_q<FMT>(p, nx.s, smem + kOffQ, tmem + lanes + kColQ, rank, quad, half, live);
         if (lane == 0) mbar_arrive(&M.q_full);
       }
       if (started) {
@@ -830,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&M.o_free);
       } else if (have) {
-        next_lim = limits(p, nx.s, row);
+        if (!F16) next_lim = limits(p, nx.s, row);
         more = cur.next(p, M.ends, rank, true);
         own_next = Tiles::pool_page(p, cur.own_id);
         if (FMT == kTokenFp8) scale = load_scale();
@@ -1157,7 +1165,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     // 16 codes of rows u / 4 + 16 i in every chunk (four lanes on a row's 64
     // contiguous bytes); a tile's pieces are loaded while the tile before is waited
     // for. Per-token codes are exact in bf16; tile-scaled values (code * scale) are
-    // rounded to f16: off by at most 2^-11 of the value.
+    // rounded to f16: off by at most 2^-11 of the value (at least 2^-25). Tile-scaled
+    // rows that no row of the segment sees count as zeros: their values may be outside
+    // f16's range.
     const int cw = warp < kSoftWarp0 ? warp - 2 : warp - 10;
     const int group = cw >> 1;  // 0 KO, 1 KV, 2 VO
     const int u = (cw & 1) * 32 + lane, r0 = u >> 2, pcs = u & 3;
@@ -1168,24 +1178,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     uint4 v[5][4];   // chunks of four rows; the fifth (KO) is the rope (tile-scaled rows: loaded when it is stored)
     const uint8_t* rope = nullptr;
     float2 sc[4];    // scales of the two 128-value tiles that the four chunks cover
-    auto fetch = [&](int page) {
-      const bool live = page >= 0;
+    uint32_t seen = 0;  // which of the four rows (tile-scaled)
+    auto fetch = [&](int page, int key0, int first_key, int end_key) {
       const uint8_t* src = p.kv + (static_cast<long long>(max(page, 0)) * kPage + r0) * kRowBytes;
       const uint4 none = make_uint4(0, 0, 0, 0);
+      seen = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const int key = key0 + r0 + 16 * i;
+        const bool live = page >= 0 && (FMT != kTileFp8 || (key >= first_key && key < end_key));
         const uint8_t* row = src + i * 16 * kRowBytes;
 #pragma unroll
         for (int c = 0; c < 4; ++c) v[c][i] = live ? __ldg(reinterpret_cast<const uint4*>(row + (c0 + c) * 64 + pcs * 16)) : none;
         if (FMT == kTileFp8) sc[i] = live ? __ldg(reinterpret_cast<const float2*>(row + kDv) + (c0 >> 2)) : make_float2(0, 0);
         if (FMT == kTokenFp8 && group == 0) v[4][i] = live ? __ldg(reinterpret_cast<const uint4*>(row + kDv + pcs * 16)) : none;
+        if (FMT == kTileFp8 && live) {
+          seen |= 1u << i;
+          if (group == 0 && pcs == 0) prefetch_l2_lines(row + kTileRope, 128);
+        }
       }
-      if (FMT == kTileFp8 && group == 0) {
-        rope = live ? src + kTileRope + pcs * 32 : nullptr;
-        if (live && pcs == 0)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) prefetch_l2_lines(rope + i * 16 * kRowBytes, 128);
-      }
+      if (FMT == kTileFp8 && group == 0) rope = src + kTileRope + pcs * 32;
     };
     auto store = [&](int off) {
 #pragma unroll
@@ -1198,8 +1210,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
           uint32_t o[8];
           if (FMT == kTileFp8 && c == 4) {  // bf16 rope -> f16
             const uint4 none = make_uint4(0, 0, 0, 0);
-            const uint4 a = rope ? __ldg(reinterpret_cast<const uint4*>(rope + i * 16 * kRowBytes)) : none;
-            const uint4 b = rope ? __ldg(reinterpret_cast<const uint4*>(rope + i * 16 * kRowBytes + 16)) : none;
+            const bool live = seen >> i & 1;
+            const uint4 a = live ? __ldg(reinterpret_cast<const uint4*>(rope + i * 16 * kRowBytes)) : none;
+            const uint4 b = live ? __ldg(reinterpret_cast<const uint4*>(rope + i * 16 * kRowBytes + 16)) : none;
             o[0] = to_f16(a.x, over), o[1] = to_f16(a.y, over), o[2] = to_f16(a.z, over), o[3] = to_f16(a.w, over);
             o[4] = to_f16(b.x, over), o[5] = to_f16(b.y, over), o[6] = to_f16(b.z, over), o[7] = to_f16(b.w, over);
           } else {
@@ -1231,7 +1244,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
     bool more = cur.next(p, M.ends, rank, true);
     auto mine = [&] { return !(p.wide && cur.pc.s < p.n_rb); };  // not a tile of the copy
     bool here = more && mine();
-    if (here) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
+    auto fetch_tile = [&] {
+      const int side = group == 2 ? rank ^ 1 : rank;
+      fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id), (cur.first_page + 2 * cur.t + side) * kPage, cur.first_key, cur.end_key);
+    };
+    if (here) fetch_tile();
     for (uint32_t g = 0; more; ++g) {
       const bool stores = here;
       if (group == 0 && cur.bad(p, rank) && lane == 0) set_status(&M.status, kStatusBounds);
@@ -1252,7 +1269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FMT>, 1)
         if (cw == 4) mbar_arrive_expect_tx(&M.vo_full, kQChunk);  // and the other page's P
         else mbar_arrive(group == 0 ? &M.ko_full : group == 1 ? &M.kv_full[g & 1] : &M.vo_full);
       }
-      if (here) fetch(Tiles::pool_page(p, group == 2 ? cur.other_id : cur.own_id));
+      if (here) fetch_tile();
     }
     if (over || top > 65504.0f) set_status(&M.status, kStatusOverflow);
   }
@@ -1292,17 +1309,23 @@ __global__ void __launch_bounds__(256) widen_kernel(const PrefixParams p) {
   constexpr int kPart = kPage / 4;
   const uint8_t* src = p.kv + (static_cast<long long>(live ? id : 0) * kPage + blockIdx.y * kPart) * kRowBytes;
   uint16_t* dst = p.wide_rows + (static_cast<long long>(blockIdx.x) * kPage + blockIdx.y * kPart) * kDqk;
-  bool over = false;
-  float top = 0.0f;
+  __shared__ uint32_t over_keys;
+  if (FMT == kTileFp8) {
+    if (threadIdx.x == 0) over_keys = 0;
+    __syncthreads();
+  }
 #pragma unroll 4
   for (int u = threadIdx.x; u < kPart * kPieces; u += 256) {
     const int r = u / kPieces, j = u - r * kPieces;
     const uint8_t* row = src + r * kRowBytes;
     uint16_t* out = dst + r * kDqk;
+    bool over = false;
+    float top = 0.0f;
     if (FMT == kTileFp8 && j >= kDv / 16) {
       const int i = j - kDv / 16;
       const uint4 w = live ? __ldg(reinterpret_cast<const uint4*>(row + kTileRope + 16 * i)) : make_uint4(0, 0, 0, 0);
       *reinterpret_cast<uint4*>(out + kDv + 8 * i) = make_uint4(to_f16(w.x, over), to_f16(w.y, over), to_f16(w.z, over), to_f16(w.w, over));
+      if (over) atomicOr(&over_keys, 1u << r);
       continue;
     }
     const uint4 c = live ? __ldg(reinterpret_cast<const uint4*>(row + 16 * j)) : make_uint4(0, 0, 0, 0);
@@ -1321,10 +1344,12 @@ __global__ void __launch_bounds__(256) widen_kernel(const PrefixParams p) {
     }
     *reinterpret_cast<uint4*>(out + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(out + 16 * j + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+    if (FMT == kTileFp8 && top > 65504.0f) atomicOr(&over_keys, 1u << r);
   }
-  over = __syncthreads_or(over || top > 65504.0f);
-  if (threadIdx.x == 0)
-    reinterpret_cast<uint32_t*>(p.wide_errors)[4 * blockIdx.x + blockIdx.y] = over ? kStatusOverflow : 0u;
+  if (FMT == kTileFp8) {
+    __syncthreads();
+    if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(p.wide_over)[4 * blockIdx.x + blockIdx.y] = over_keys;
+  }
 }
 
 // ------------------------------------------------------------------ joining the pieces
@@ -1360,27 +1385,39 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixParams
     tiles[0] = p.n_rb > 0 ? shared_tiles(shared_end(p, seg[0] >> p.end_shift)) : 0;
     tiles[1] = own_tiles(p, own_end(p, seg[1] - p.n_rb));
   }
+  const bool reports = blockIdx.x == 0 && blockIdx.y == 0;  // the call's status
+  int seen = 0;  // keys of the shared part that some row sees
+  if (reports && p.wide_over) {
+#pragma unroll 4
+    for (int b = tid; b < p.n_seqs; b += kMergeThreads) seen = max(seen, length_of(p, b));
+    seen = __reduce_max_sync(0xFFFFFFFFu, seen);
+    if (lane == 0) warp_bits[tid >> 5] = seen;
+    __syncthreads();
+    for (int w = 0; w < kMergeThreads / 32; ++w) seen = max(seen, static_cast<int>(warp_bits[w]));
+    seen = min(seen, p.shared_len);
+    __syncthreads();
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long own_at = tiles[1] > 0 ? p.seg_off[seg[1]] : 0, shared_at = tiles[0] > 0 ? p.seg_off[seg[0]] : 0;
   const bool done = own_at < 0;
   if (done && blockIdx.x != 0) return;
   for (int q = tid; q <= p.pairs; q += kMergeThreads) bounds[q] = p.bounds[q];
-  if (blockIdx.x == 0 && blockIdx.y == 0) {  // the call's status
+  if (reports) {
     uint32_t bits = 0;
     for (int q = tid; q < 2 * p.pairs; q += kMergeThreads) bits |= p.errors[q];
-    if (p.wide) {
-      const int pages = (p.shared_len + kPage - 1) / kPage;
-#pragma unroll 8
-      for (int i = tid; i < pages; i += kMergeThreads) {
-        const uint4 e = p.wide_errors[i];
-        bits |= e.x | e.y | e.z | e.w;
+    if (p.wide_over) {
+#pragma unroll 4
+      for (int i = tid; i < 4 * ((seen + kPage - 1) / kPage); i += kMergeThreads) {  // 16 keys each
+        const uint32_t over = reinterpret_cast<const uint32_t*>(p.wide_over)[i];
+        const int n = seen - 16 * i;
+        if (n > 0 && (over & ((1u << min(n, 16)) - 1))) bits |= kStatusOverflow;
       }
     }
     bits = __reduce_or_sync(0xFFFFFFFFu, bits);
     if (lane == 0) warp_bits[tid >> 5] = bits;
   }
   __syncthreads();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
+  if (reports && tid == 0) {
     uint32_t bits = 0;
     for (int w = 0; w < kMergeThreads / 32; ++w) bits |= warp_bits[w];
     *p.status = bits;
@@ -1603,7 +1640,7 @@ size_t layout(PrefixParams& p, uint8_t* ws, int32_t kv_dtype) {
     p.wide_rows = reinterpret_cast<uint16_t*>(ws + at);
     const size_t pages = (static_cast<size_t>(p.shared_len) + kPage - 1) / kPage;
     at += pages * kPage * kDqk * 2;
-    p.wide_errors = reinterpret_cast<uint4*>(ws + at);
+    if (kv_dtype == SMLA_FP8_DS_MLA) p.wide_over = reinterpret_cast<uint4*>(ws + at);
     at += pages * sizeof(uint4);
   }
   return at;

@@ -72,13 +72,59 @@ def test_query_codes_are_the_rounded_quotients(rows):
     assert np.array_equal(qi.cpu().view(torch.float8_e4m3fn).float().numpy(), codes)
 
 
-# ---------------------------------------------------------------------------- idle requests
+# ---------------------------------------------------------------------------- memory that no row sees
 def _attend(c, tab, sl, q, qt, shared, max_len=None, scale=sc.SM_SCALE):
     m = max(1, int(sl.max()), shared) if max_len is None else max_len
     out, lse, ws = smla.shared_prefix_fwd(c.to("cuda"), tab.cuda(), sl.cuda(), m, shared, q, qt.cuda(), scale)
     return out, lse, smla.read_status(ws)[0]
 
 
+def _huge(c, dead):
+    """Tile-scaled rows whose values are finite and far outside f16's range."""
+    c.kv[dead] = torch.cat([torch.full((512,), 0x7E, dtype=torch.uint8), torch.full((4,), 1e30).view(torch.uint8),
+                            torch.full((64,), 1e30, dtype=torch.bfloat16).view(torch.uint8)])
+
+
+@pytest.mark.parametrize("n,q,heads,shared,lens", [
+    (1, 1, 64, 0, [100]),                   # past the length
+    (1, 5, 64, 0, [77]),
+    (2, 1, 16, 130, [200, 333]),            # and before the border of the second request's page (one row block)
+    (3, 2, 64, 200, [260, 410, 777]),       # the shared part's copy (three row blocks)
+])
+def test_attention_unseen_values_outside_f16_are_not_reported(n, q, heads, shared, lens):
+    c, tab, sl, qt = sc.attention_case(n, q, heads, "fp8_ds_mla", shared, lens, seed=n + 20)
+    _huge(c, (c.kv == 0xFF).all(-1))
+    ref = sc.attention_reference(c, tab, sl, q, qt, shared, sc.SM_SCALE)
+    out, lse, status = _attend(c, tab, sl, q, qt, shared)
+    assert status == 0
+    sc.check_attention(out, lse, ref, "fp8_ds_mla")
+
+
+@pytest.mark.parametrize("q,heads", [(1, 16), (2, 64)])
+def test_attention_shared_values_past_every_length_are_not_reported(q, heads):
+    """All requests end before the shared part does."""
+    c, tab, sl, qt = sc.attention_case(3, q, heads, "fp8_ds_mla", 333, [100, 90, 70], seed=24)
+    for s in range(100, 333):
+        _huge(c, (tab[0, s // 64], s % 64))
+    ref = sc.attention_reference(c, tab, sl, q, qt, 333, sc.SM_SCALE)
+    out, lse, status = _attend(c, tab, sl, q, qt, 333)
+    assert status == 0
+    sc.check_attention(out, lse, ref, "fp8_ds_mla")
+    _huge(c, (tab[0, 1], 99 % 64))  # the last one that a row sees
+    assert _attend(c, tab, sl, q, qt, 333)[2] == 2
+
+
+@pytest.mark.parametrize("shared", [0, 130])
+def test_attention_queries_that_see_nothing_are_not_reported(shared):
+    c, tab, sl, qt = sc.attention_case(3, 2, 64, "fp8_ds_mla", shared, [0, 180, 1], seed=25)
+    qt[0:2], qt[4] = 1e30, -1e30  # an idle request, and a token before the first key
+    out, lse, status = _attend(c, tab, sl, 2, qt, shared)
+    assert status == 0
+    qt[0:2], qt[4] = 0, 0
+    sc.check_attention(out, lse, sc.attention_reference(c, tab, sl, 2, qt, shared, sc.SM_SCALE), "fp8_ds_mla")
+
+
+# ---------------------------------------------------------------------------- idle requests
 @pytest.mark.parametrize("kv_dtype", FORMATS)
 @pytest.mark.parametrize("n,q,heads", [(2, 1, 16), (5, 2, 64)])  # one and several row blocks
 def test_attention_of_an_idle_batch_looks_at_no_page(kv_dtype, n, q, heads):
