@@ -173,8 +173,11 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
  * slot of a page may hold NaN).
  * Supported: n_heads 16 and 64; any q_per_seq >= 1; the three cache formats.
  * Workspace: the returned size (status word, the partial results of the pieces that
- * the keys are cut into and, for FP8 caches whose shared part is read by more than
- * 128 query rows, a 16-bit copy of the shared rows, 1,152 bytes a token and 16 a page).
+ * the keys are cut into, 265 KB each: two pieces for each pair of SMs where nothing is
+ * shared, else one for each 128 rows of the batch, one for each 128 rows or part
+ * of them of each request, and one for each pair; and, for FP8 caches whose shared part
+ * is read by more than 128 query rows of several requests, a 16-bit copy of the shared
+ * rows, 1,152 bytes a token and 16 a page). The size is that of the current device.
  * ------------------------------------------------------------------------- */
 size_t smla_shared_prefix_fwd_workspace_size(int32_t n_seqs, int32_t max_seq_len, int32_t shared_len,
                                              int32_t q_per_seq, int32_t n_heads, int32_t kv_dtype);

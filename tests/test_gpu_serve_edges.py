@@ -170,6 +170,35 @@ def test_attention_more_row_blocks_than_the_table_of_ends_holds(kv_dtype):
     sc.check_attention(out, lse, sc.attention_reference(c, tab, sl, 1, qt, 130, sc.SM_SCALE), kv_dtype)
 
 
+# ---------------------------------------------------------------------------- nothing shared, many segments
+def _sample(tab, sl, q, qt, rows):
+    """Rows of a batch as requests of one token each (row 0 first: its table holds the shared part)."""
+    rows = [0] + sorted(rows)
+    b = [r // q for r in rows]
+    lens = [max(0, int(sl[r // q]) - q + r % q + 1) for r in rows]
+    return rows, tab[b], torch.tensor(lens, dtype=torch.int32), qt[rows]
+
+
+@pytest.mark.parametrize("kv_dtype", FORMATS)
+@pytest.mark.parametrize("n,q,heads,longest", [
+    (1, 1101, 64, 1500),  # a chunk of prompt: 551 segments of up to 12 tiles, most of them uncut
+    (1, 700, 16, 5003),   # 88 segments of 34 to 40 tiles: a pair walks one and a bit
+    (90, 3, 64, 700),     # 180 segments, two a request
+    (601, 1, 64, 150),    # more segments than threads
+])
+def test_attention_nothing_shared_many_segments(kv_dtype, n, q, heads, longest):
+    rng = np.random.default_rng(n)
+    lens = [longest] if n == 1 else rng.integers(0, longest + 1, n).tolist()
+    c, tab, sl, qt = sc.attention_case(n, q, heads, kv_dtype, 0, lens, seed=30)
+    need = smla.shared_prefix_workspace_bytes(n, longest, 0, q, heads, kv_dtype)
+    raw = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse, ws = smla.shared_prefix_fwd(c.to("cuda"), tab.cuda(), sl.cuda(), longest, 0, q, qt.cuda(), sc.SM_SCALE, ws=raw[:need])
+    assert smla.read_status(ws)[0] == 0 and (raw[need:] == 0xA5).all()
+    assert out.isfinite().all()
+    rows, t, l, x = _sample(tab, sl, q, qt, rng.choice(n * q, 60, replace=False).tolist())
+    sc.check_attention(out[rows], lse[rows], sc.attention_reference(c, t, l, 1, x, 0, sc.SM_SCALE), kv_dtype)
+
+
 # ---------------------------------------------------------------------------- tables
 def _tables(ctx, new, tables, free, max_new):
     i = lambda a: torch.as_tensor(a, dtype=torch.int32).cuda()  # noqa: E731
