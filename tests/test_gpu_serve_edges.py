@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import indexer_top_sparse_score_gb300 as smla
+import serve_bounds as sb
 import serve_common as sc
 
 pytestmark = pytest.mark.gpu
@@ -197,6 +198,110 @@ def test_attention_nothing_shared_many_segments(kv_dtype, n, q, heads, longest):
     assert out.isfinite().all()
     rows, t, l, x = _sample(tab, sl, q, qt, rng.choice(n * q, 60, replace=False).tolist())
     sc.check_attention(out[rows], lse[rows], sc.attention_reference(c, t, l, 1, x, 0, sc.SM_SCALE), kv_dtype)
+
+
+# ---------------------------------------------------------------------------- long rows, small values, other inputs
+@pytest.mark.parametrize("kv_dtype", FORMATS)
+def test_attention_long_rows_as_a_whole(kv_dtype):
+    """Bounds that a lost tile of keys does not pass (one row block's keys in pieces; the copy of shared rows)."""
+    for n, q, shared, lens in ((1, 1, 0, [38000]), (3, 2, 30011, [38000, 9000, 30200])):
+        c, tab, sl, qt = sc.attention_case(n, q, 64, kv_dtype, shared, lens, seed=31)
+        out, lse, status = _attend(c, tab, sl, q, qt, shared)
+        assert status == 0
+        ro, rl, _, _ = sc.attention_reference(c, tab, sl, q, qt, shared, sc.SM_SCALE)
+        sb.check_rows(out.double().cpu().numpy(), lse.double().cpu().numpy(), ro, rl)
+
+
+@pytest.mark.parametrize("factor", [1e-3, 1e-5, 1e-7, 1e-9])
+def test_attention_small_tile_scaled_values(factor):
+    """Values below f16's normals (2^-14) are held to 2^-25: the results' error grows by that, and a logit's by
+    that much of each |q|."""
+    c, tab, sl, qt = sc.attention_case(2, 1, 16, "fp8_ds_mla", 200, [420, 333], seed=32)
+    live = ~(c.kv == 0xFF).all(-1)
+    scales = c.kv[..., 512:528].contiguous().view(torch.float32)
+    scales[live] *= factor
+    c.kv[..., 512:528] = scales.view(torch.uint8)
+    out, lse, status = _attend(c, tab, sl, 1, qt, 200)
+    assert status == 0
+    ro, rl, mag, top = sc.attention_reference(c, tab, sl, 1, qt, 200, sc.SM_SCALE)
+    delta = top * (576 * 2.0 ** -24 + 2.0 ** -11) + 2.0 ** -18 + 2.0 ** -25 * sc.SM_SCALE * qt.double().abs().sum(-1).numpy()
+    rel = (2.0 ** -10 + 2.0 ** -14 + 2 * delta)[..., None]
+    bound = rel * mag + 2.0 ** -25 * (1 + rel)
+    assert (np.abs(out.double().cpu().numpy() - ro) <= bound + 2.0 ** -8 * (np.abs(ro) + bound)).all()
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= delta + 2.0 ** -20 * np.abs(rl)).all()
+
+
+@pytest.mark.parametrize("kv_dtype", FORMATS)
+@pytest.mark.parametrize("n", [2, 5])
+def test_attention_queries_on_a_16_byte_boundary(kv_dtype, n):
+    c, tab, sl, qt = sc.attention_case(n, 2, 64, kv_dtype, 130, [300, 411, 129, 0, 257][:n], seed=33)
+    base = torch.empty(qt.numel() + 8, dtype=torch.bfloat16, device="cuda")
+    q = base[8:].view(qt.shape)
+    q.copy_(qt)
+    assert q.data_ptr() % 32 == 16
+    m = int(sl.max())
+    out, lse, ws = smla.shared_prefix_fwd(c.to("cuda"), tab.cuda(), sl.cuda(), m, 130, 2, q, sc.SM_SCALE)
+    assert smla.read_status(ws)[0] == 0
+    sc.check_attention(out, lse, sc.attention_reference(c, tab, sl, 2, qt, 130, sc.SM_SCALE), kv_dtype)
+
+
+@pytest.mark.parametrize("kv_dtype", ["fp8", "fp8_ds_mla"])
+@pytest.mark.parametrize("n", [1, 4])
+def test_attention_negative_scale_of_fp8_rows(kv_dtype, n):
+    c, tab, sl, qt = sc.attention_case(n, 2, 64, kv_dtype, 130, [300, 211, 140, 500][:n], seed=34)
+    out, lse, status = _attend(c, tab, sl, 2, qt, 130, scale=-0.04)
+    assert status == 0
+    ref = sc.attention_reference(c, tab, sl, 2, qt, 130, -0.04)
+    sc.check_attention(out, lse, ref[:3] + (np.abs(ref[3]),), kv_dtype)
+
+
+@pytest.mark.parametrize("kv_dtype", ["fp8", "fp8_ds_mla"])
+def test_attention_copy_of_shared_rows_on_streams_and_in_graphs(kv_dtype):
+    """The 16-bit copy is made anew by every call: in a workspace full of NaN, after another prompt, on a side stream
+    and by a replayed graph, the same bits."""
+    a, b = (sc.attention_case(4, 2, 64, kv_dtype, 450, [600, 451, 777, 500], seed=s) for s in (35, 36))
+    ref = sc.attention_reference(*a[:3], 2, a[3], 450, sc.SM_SCALE)
+    (ca, ta, la, qa), (cb, tb, lb, qb) = ((c.to("cuda"), t.cuda(), sl.cuda(), q.cuda()) for c, t, sl, q in (a, b))
+    ws = smla.workspace(smla.shared_prefix_workspace_bytes(4, 777, 450, 2, 64, kv_dtype)).fill_(0xFF)
+    out, lse = torch.empty(8, 64, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(8, 64, device="cuda")
+    call = lambda c, t, sl, q: smla.shared_prefix_fwd(c, t, sl, 777, 450, 2, q, sc.SM_SCALE, out=out, lse=lse, ws=ws)  # noqa: E731
+    call(ca, ta, la, qa)
+    assert smla.read_status(ws)[0] == 0
+    sc.check_attention(out, lse, ref, kv_dtype)
+    first, flse = out.clone(), lse.clone()
+    same = lambda: torch.equal(out, first) and torch.equal(lse, flse)  # noqa: E731
+    call(cb, tb, lb, qb)
+    assert not same()
+    call(ca, ta, la, qa)
+    assert same()
+    call(cb, tb, lb, qb)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(ca, ta, la, qa)
+    side.synchronize()
+    assert same()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(cb, tb, lb, qb)
+        call(ca, ta, la, qa)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert same()
+
+
+@pytest.mark.parametrize("kv_dtype", FORMATS)
+def test_attention_many_rows_on_a_shared_prompt(kv_dtype):
+    """38,464 rows of 601 requests: each block of the joining kernel takes all of its rows' values."""
+    rng = np.random.default_rng(37)
+    lens = (200 + rng.integers(0, 70, 601)).tolist()
+    c, tab, sl, qt = sc.attention_case(601, 1, 64, kv_dtype, 200, lens, seed=37)
+    out, lse, status = _attend(c, tab, sl, 1, qt, 200)
+    assert status == 0 and out.isfinite().all()
+    rows, t, l, x = _sample(tab, sl, 1, qt, rng.choice(601, 80, replace=False).tolist())
+    sc.check_attention(out[rows], lse[rows], sc.attention_reference(c, t, l, 1, x, 200, sc.SM_SCALE), kv_dtype)
 
 
 # ---------------------------------------------------------------------------- tables
