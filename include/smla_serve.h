@@ -23,7 +23,9 @@ extern "C" {
 
 /* ---------------------------------------------------------------------------
  * smla_build_tables — pages and slots of the next new_lens[b] tokens of every
- * request, from lengths that live on the device (no host round trip).
+ * request, from lengths that live on the device. (free_pages begins with the page to
+ * be handed out first: a caller that keeps one list for many calls moves it on by
+ * pages_used.)
  *
  * Request b holds ctx_lens[b] tokens in ceil(ctx / 64) pages, listed first in
  * page_tables[b]. Its new tokens continue its last page and then take pages
@@ -95,7 +97,7 @@ typedef struct smla_rope {
  *               idx_norm alone: y = x * rsqrt(mean(x^2) + eps) * idx_norm;
  *               neither: y = x.
  *             The first 64 values are then rotated. bf16 keys are rounded; e4m3
- *             keys get scale = amax / 448 in k_idx_scale, or, where that array
+ *             keys get such a scale in k_idx_scale, or, where that array
  *             is NULL, are rounded as they are (beyond +-448: saturated).
  * All arithmetic in fp32, rounded once. Device errors: a slot outside the pool
  * or a position outside [0, max_pos): the row is skipped. Workspace: 256 bytes.
@@ -120,8 +122,8 @@ int smla_cache_append(const smla_paged_cache* cache, const smla_rope* rope, int3
  *             values apart (a multiple of 8), or NULL: no indexer queries. Each
  *             head: y = x * rsqrt(mean(x^2) + eps) * idx_norm ([d_idx] fp32;
  *             NULL: y = x), first 64 values rotated, then
- *   q_idx     [rows][h_idx][d_idx]: bf16, or e4m3 with scale = amax / 448 (1 if
- *             all are zero) of the head, which goes into
+ *   q_idx     [rows][h_idx][d_idx]: bf16, or e4m3 with scale and codes of the head
+ *             as smla_cache_append makes them; the scale goes into
  *   w_out     [rows][h_idx] fp32 = w * (scale * w_scale) (bf16: w * w_scale),
  *             so that w_out * ReLU(q_idx . k) is the score's term: a positive
  *             scale passes through the ReLU. w [rows][h_idx] fp32; w_out may be w.
@@ -168,7 +170,8 @@ int smla_query_prep(const smla_rope* rope, int32_t rows, const int32_t* position
  * the scales multiply logits and probabilities in fp32). Tile-scaled FP8 rows: f16
  * operands (values and probabilities rounded to f16), so |q| and the values must
  * stay below 65504; beyond it, in a row that sees a key or a key that a row sees,
- * smla_read_status gives SMLA_ERR_UNSUPPORTED, as for smla_sparse_mla_fwd.
+ * smla_read_status gives SMLA_ERR_UNSUPPORTED, as for smla_sparse_mla_fwd. Values
+ * below f16's normals (2^-14) are off by up to 2^-25 (and below that zero).
  * Keys that a row does not see never reach it, whatever they hold (an unused
  * slot of a page may hold NaN).
  * Supported: n_heads 16 and 64; any q_per_seq >= 1; the three cache formats.

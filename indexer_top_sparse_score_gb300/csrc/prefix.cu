@@ -42,9 +42,12 @@
 // the starts of segments. 64 x 2 tokens of 64 heads on a 64K prompt: 735 us and 20 to
 // join, 1,620 TFLOP/s in this kernel, 85% of cuBLAS's bf16 rate (the tensor pipe is
 // active in 72% of the cycles of a call half that size). 1,024 tokens after 8K: 740 us and 20.
-// Per-token FP8, 64 x 2 on 16K: 216 us, 8 to widen, 20 to join, 1,250 TFLOP/s in all:
-// the requests' own keys, 6% of all, are 15% of the line's cost. One token
-// on 1,100 keys: 14.7 us, a chain of latencies: Q, three tiles a pair, results, join.
+// Per-token FP8, 64 x 2 on 16K: 218 us, 8 to widen, 25 to join, 1,240 TFLOP/s in all:
+// the requests' own keys, 6% of all, are 15% of the line's cost. A single request's
+// FP8 rows have no copy: each of its row blocks widens them (1,024 tokens after 8K: 1.34
+// ms with per-token scales, 2.27 ms with tile scales, 0.78 ms from BF16 rows). One token
+// on 1,100 keys: 13 us, 17 on cold caches, a chain of latencies: Q, three tiles a pair,
+// results, join.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -68,7 +71,8 @@ constexpr int kRows = 128;       // rows of a block (MMA M)
 // segments to end last. Measured over the start's cost: 64 x 2 tokens of 64 heads on
 // a 64K prompt, BF16, 850 / 834 / 825 / 842 us at 12 / 16 / 20 / 24; on a 16K prompt,
 // per-token FP8, 284 / 275 / 266 / 259 us at 20 / 26 / 32 / 38 with own tiles at 6, and
-// 254 / 253 / 258 at 38 / 44 / 56 with own tiles at 7.
+// 254 / 253 / 258 at 38 / 44 / 56 with own tiles at 7; later 255 at 40 and 7, 256 / 257 /
+// 260 at 32 / 40 / 48 with own tiles at 8.
 struct Costs {
   int32_t start, shared_tile, own_tile;
 };

@@ -63,8 +63,9 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
 // the rows [first, last) of the per-token outputs that are its share; block 0
 // also writes the per-request outputs and the status word, which needs no clearing
 // launch because block 0 sees every condition that can set it. Bound by latency:
-// a load, two block scans and a search per 1,024 requests. 1,000 requests with up to
-// 257 new tokens: 7.2 us on cold caches; 64 requests: 5 us, within the launch of a call.
+// a load, two block scans and a search per 1,024 requests, and block 0's look at the
+// ids that were taken. 1,000 requests with up to 257 new tokens: 7.4 us on cold
+// caches; 64 requests: 5.5 us, within the launch of a call.
 __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesParams p) {
   __shared__ long long warp_sums[kTabThreads / 32];
   __shared__ int s_cu[kTabThreads + 1];   // first row of each request of the chunk
@@ -323,8 +324,9 @@ __device__ __forceinline__ void report_rows(int rows, uint32_t* status, Bad bad)
 // lanes of 8 values): a row is read once in 16-byte pieces, reduced in registers
 // and written once. Its values are requested before the slot and position are
 // looked at, so a row costs two memory latencies (position, then its angles)
-// and not three. Cold caches: 128 rows 3.0 us; 8,192 BF16 rows with FP8 keys 8.8 us,
-// 24 MB, 2.8 TB/s; 5,003 tile-scaled rows 6.4 us: latency, one or two waves of warps.
+// and not three. Cold caches: 128 rows 3.3 us; 8,192 BF16 rows with FP8 keys 8.7 us,
+// 24 MB, 2.8 TB/s; 5,003 tile-scaled rows 6.7 us: two to four times what the bytes
+// take, in one or two waves of warps. (More rows a warp have not been measured.)
 constexpr int kRowThreads = 128;
 
 __device__ __forceinline__ void append_latent(const AppendParams& p, int row) {
@@ -514,10 +516,11 @@ struct QueryParams {
 
 // A warp takes four steps of 4 (8 lanes a head) or 2 (16 lanes) heads of one row,
 // all loaded before the row's position and angles, which are two latencies away.
-// Bound by memory: 8,192 rows of 64 attention and 32 indexer heads move 239 MB in
-// 48.6 us, 4.9 TB/s or 72% of a plain copy's rate (the rope values are written as
-// 128 bytes of every 1,152); 128 rows take 4.3 us. With two or eight steps 58 us, in
-// blocks of 256 threads 53, in 51 or 42 registers (more warps) 53 or 55.
+// Bound by memory and instructions: 8,192 rows of 64 attention and 32 indexer heads
+// move 239 MB in 51.4 us, 4.7 TB/s or 69% of a plain copy's rate (the rope values are
+// written as 128 bytes of every 1,152); 128 rows take 4.7 us. Measured when codes were
+// products without a step of correction and four steps took 48.6 us: two or eight
+// steps 58 us, blocks of 256 threads 53, 51 or 42 registers (more warps) 53 or 55.
 constexpr int kSteps = 4;
 
 template <int L>

@@ -73,6 +73,28 @@ def test_query_codes_are_the_rounded_quotients(rows):
     assert np.array_equal(qi.cpu().view(torch.float8_e4m3fn).float().numpy(), codes)
 
 
+def test_append_codes_of_the_ends_of_fp32():
+    """An infinite amax, NaN, zeros, and rows whose scale would fall below 2^-126."""
+    inf, nan = float("inf"), float("nan")
+    x = torch.zeros(6, 128, dtype=torch.bfloat16)  # (values from 64 on are not rotated)
+    x[0, 64:68] = torch.tensor([inf, -inf, 3.0, -3e38])
+    x[1, 64:67] = torch.tensor([nan, 2.0, -448.0])
+    x[2, 64:68] = torch.tensor([2.0 ** -118, -3 * 2.0 ** -121, 2.0 ** -126, 2.0 ** -130])
+    x[3, 64:67] = torch.tensor([2.0 ** -126, -(2.0 ** -128), 2.0 ** -133])
+    x[4, 64:67] = torch.tensor([3.3e38, -1e38, 1e36])
+    c = sc.empty_cache(1, "bf16", "fp8").to("cuda")
+    pos, rope = _unturned(6)
+    smla.cache_append(c, torch.arange(6, dtype=torch.int32, device="cuda"), pos, rope, k_idx=x.cuda())
+    scale = c.k_idx_scale.cpu().numpy()[0, :6]
+    got = c.k_idx.cpu()[0, :6].view(torch.float8_e4m3fn).float().numpy()
+    with np.errstate(invalid="ignore"):
+        want_scale, want = _codes(np.nan_to_num(x.float().numpy(), nan=0.0, posinf=np.inf, neginf=-np.inf))
+    want[0, 64:68] = [nan, nan, 0, 0]  # infinity by infinity; finite by infinity
+    want[1, 64] = nan
+    assert np.array_equal(scale, want_scale) and np.isinf(scale[0]) and scale[3] == 2.0 ** -126 and scale[5] == 1
+    np.testing.assert_array_equal(got, want)
+
+
 # ---------------------------------------------------------------------------- memory that no row sees
 def _attend(c, tab, sl, q, qt, shared, max_len=None, scale=sc.SM_SCALE):
     m = max(1, int(sl.max()), shared) if max_len is None else max_len
