@@ -22,7 +22,7 @@ _CSRC = os.path.join(_HERE, "csrc")
 _INCLUDE = os.path.join(os.path.dirname(_HERE), "include")
 _BUILD = os.path.join(_HERE, "_build")
 LIB_PATH = os.path.join(_BUILD, "libsmla.so")
-SOURCES = ["api.cu", "indexer.cu", "mla.cu", "noalloc.cu", "prefix.cu", "serve.cu"]
+SOURCES = ["api.cu", "indexer.cu", "mla.cu", "noalloc.cu", "prefix.cu", "prompt.cu", "rows.cu", "serve.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC"]
 
@@ -133,6 +133,25 @@ _SERVE_SIGS = {
 }
 
 
+class Heads(ctypes.Structure):
+    """smla_heads: heads of packed tokens by their strides (in values)."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+_f64 = ctypes.c_double
+# include/smla_prompt.h
+_PROMPT_SIGS = {
+    "smla_rope_table": (ctypes.c_int, [_vp, _i64, _i32, _i32, _f64, _f64, _i32, _f64, _f64, _f32, _vp]),
+    "smla_rope_apply": (ctypes.c_int, [_vp, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _sz,
+                                       _vp]),
+    "smla_cache_read": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz,
+                                       _vp]),
+    "smla_prompt_fwd_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "smla_prompt_fwd": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _f32,
+                                       _vp, _vp, _vp, _i32, _vp, _vp, _sz, _vp]),
+}
+
+
 def lib(build_if_missing: bool = False):
     """The loaded libsmla.so. Raises if it has not been built (no fallback)."""
     global _lib
@@ -144,7 +163,7 @@ def lib(build_if_missing: bool = False):
                 raise RuntimeError(f"libsmla.so is not built ({LIB_PATH}); run "
                                    "indexer_top_sparse_score_gb300.build() first")
             L = ctypes.CDLL(LIB_PATH)
-            for name, (res, args) in {**_SIGS, **_SERVE_SIGS}.items():
+            for name, (res, args) in {**_SIGS, **_SERVE_SIGS, **_PROMPT_SIGS}.items():
                 f = getattr(L, name)
                 f.restype = res
                 f.argtypes = args
@@ -581,6 +600,147 @@ def shared_prefix_fwd(cache, page_tables, seq_lens, max_seq_len, shared_len, q_p
                                   max_seq_len, shared_len, q_per_seq, q.data_ptr(), H, sm_scale, out.data_ptr(),
                                   lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(rc, "smla_shared_prefix_fwd")
+    return out, lse, ws
+
+
+# ---------------------------------------------------------------------------- expanded prompts
+def _here(*tensors):
+    """The kernels run on the current device's stream: every tensor has to be there."""
+    now = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors are on the GPU")
+        if now is None:
+            now = torch.cuda.current_device()
+        if t.get_device() != now:
+            raise ValueError("tensors are on the current CUDA device (torch.cuda.device sets it)")
+
+
+def rope_table(n, dim=64, *, first=0, base=10000.0, factor=1.0, original=0, beta_fast=32.0, beta_slow=1.0,
+               magnitude=1.0, out=None, stream=None):
+    """cos and sin of the angles of positions first .. first + n - 1: fp32 [n, dim], a
+    row's dim / 2 cosines before its sines. factor > 1 slows the turns for long
+    contexts: all alike (original = 0), or by how often they turn over `original`
+    positions (see smla_rope_table). Returns the table."""
+    if out is None:
+        out = torch.empty((n, dim), dtype=_F32, device="cuda")
+    elif out.dtype is not _F32 or out.shape != (n, dim) or not out.is_contiguous():
+        raise ValueError("out is a contiguous fp32 [n, dim] table")
+    _here(out)
+    rc = lib().smla_rope_table(out.data_ptr(), first, n, dim, base, factor, original, beta_fast, beta_slow, magnitude,
+                               _stream(stream))
+    _check(rc, "smla_rope_table")
+    return out
+
+
+def _strides(t, what):
+    """Row and head stride of a bf16 [rows, heads, width] tensor whose heads' values lie next to each other."""
+    if t.dtype is not _BF16 or t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{what} is bf16 [rows, heads, width] with a head's values next to each other")
+    rows, heads, width = t.shape
+    head = t.stride(1) if heads > 1 else -(-width // 8) * 8
+    return (t.stride(0) if rows > 1 else max(heads * head, -(-width // 8) * 8)), head
+
+
+def rope_apply(x, positions, table, *, interleaved=True, out=None, ws=None, stream=None):
+    """Rotation of x [rows, heads, dim] bf16 (strided: a part of wider heads, for
+    instance) by the rows `positions` of table [max_pos, dim], into out (a new tensor
+    if None; x itself: in place). Position -1 skips a row (see smla_rope_apply).
+    Returns (out, ws)."""
+    L = lib()
+    _int32(positions)
+    x_row, x_head = _strides(x, "x")
+    rows, heads, dim = x.shape
+    if positions.numel() != rows:
+        raise ValueError("positions has one entry per row of x")
+    if table.dtype is not _F32 or table.dim() != 2 or table.shape[1] != dim or not table.is_contiguous():
+        raise ValueError("table is a contiguous fp32 [max_pos, dim] table of x's dim")
+    if out is None:
+        out = torch.empty((rows, heads, dim), dtype=_BF16, device=x.device)
+    elif out.shape != x.shape:
+        raise ValueError("out has x's shape")
+    o_row, o_head = _strides(out, "out")
+    _here(x, positions, table, out, ws)
+    if ws is None:
+        ws = workspace(STATUS_BYTES, x.device)
+    rc = L.smla_rope_apply(table.data_ptr(), table.shape[0], dim, int(interleaved), rows, positions.data_ptr(), x.data_ptr(),
+                           x_row, x_head, heads, out.data_ptr(), o_row, o_head, ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(rc, "smla_rope_apply")
+    return out, ws
+
+
+def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, pe=None, keys=None, want_keys=False, ws=None,
+               stream=None):
+    """Tokens starts[b] .. of every request b out of `cache` into the packed rows
+    cu_rows[b] .. cu_rows[b + 1] - 1, as bf16: latent [rows, 512], pe [rows, 64] and, if wanted or
+    given, keys [rows, d_idx] (see smla_cache_read). Given outputs may be strided; rows past
+    cu_rows[n] are left as they are. Returns (latent, pe, keys, ws)."""
+    L = lib()
+    _int32(page_tables, cu_rows, starts)
+    n_seqs, max_pages = page_tables.shape
+    if cu_rows.numel() != n_seqs + 1 or (starts is not None and starts.numel() != n_seqs):
+        raise ValueError("cu_rows has n_seqs + 1 entries, starts n_seqs")
+    _here(cache.kv, cache.kv_scale, cache.k_idx, cache.k_idx_scale, page_tables, cu_rows, starts, latent, pe, keys, ws)
+    dev, d = page_tables.device, cache.k_idx.shape[-1]
+    if latent is None:
+        latent = torch.empty((rows, D_V), dtype=_BF16, device=dev)
+    if pe is None:
+        pe = torch.empty((rows, D_QK - D_V), dtype=_BF16, device=dev)
+    if keys is None and want_keys:
+        keys = torch.empty((rows, d), dtype=_BF16, device=dev)
+    strides = _bf16_rows(latent, rows, D_V), _bf16_rows(pe, rows, D_QK - D_V), _bf16_rows(keys, rows, d)
+    if ws is None:
+        ws = workspace(STATUS_BYTES, dev)
+    c = make_cache(cache)
+    rc = L.smla_cache_read(ctypes.byref(c), page_tables.data_ptr(), max_pages, n_seqs, cu_rows.data_ptr(), rows, _p(starts),
+                           latent.data_ptr(), strides[0], pe.data_ptr(), strides[1], _p(keys), strides[2], ws.data_ptr(),
+                           ws.numel(), _stream(stream))
+    _check(rc, "smla_cache_read")
+    return latent, pe, keys, ws
+
+
+def prompt_workspace_bytes(total_q, total_k, n_seqs, n_heads, n_kv_heads) -> int:
+    return lib().smla_prompt_fwd_workspace_size(total_q, total_k, n_seqs, n_heads, n_kv_heads)
+
+
+D_HEAD = 128  # values of an expanded head's v
+
+
+def prompt_fwd(q, k, v, cu_q, cu_k, sm_scale, *, k_pe=None, causal=True, prev_out=None, prev_lse=None, out=None, lse=None,
+               out_dtype=torch.bfloat16, ws=None, stream=None):
+    """Attention over packed prompts: q [total_q, H, 128 or 192], k [total_k, Hk, the same] (or
+    64 less, with the rope part k_pe [total_k, 64] of all heads), v [total_k, Hk, 128], all bf16 and
+    possibly strided; cu_q and cu_k [n + 1] where each request's tokens and keys begin. causal: the
+    tokens are the last ones of their keys. prev_out and prev_lse (fp32): the result over other keys, to
+    be joined with (see smla_prompt_fwd). Returns (out, lse, ws)."""
+    L = lib()
+    _int32(cu_q, cu_k)
+    n_seqs = cu_q.numel() - 1
+    tq, heads, d = q.shape
+    tk, kv_heads, dk = k.shape
+    hq, hk, hv = (Heads(t.data_ptr(), *_strides(t, w)) for t, w in ((q, "q"), (k, "k"), (v, "v")))
+    if cu_k.numel() != n_seqs + 1 or dk != (d if k_pe is None else d - 64) or v.shape != (tk, kv_heads, D_HEAD):
+        raise ValueError("k and v are [total_k, kv heads, ..] with k as wide as q (64 less beside k_pe) and v of 128; cu_q and cu_k are alike")
+    pe_row = _bf16_rows(k_pe, tk, 64)
+    if out is None:
+        out = torch.empty((tq, heads, D_HEAD), dtype=out_dtype, device=q.device)
+    if out.dtype not in (_BF16, _F32) or out.numel() != tq * heads * D_HEAD or not out.is_contiguous():
+        raise ValueError("out is contiguous bf16 or fp32 [total_q, heads, 128]")
+    if lse is None:
+        lse = torch.empty((tq, heads), dtype=_F32, device=q.device)
+    _fp32(lse, tq * heads, "lse")
+    _fp32(prev_out, tq * heads * D_HEAD, "prev_out")
+    _fp32(prev_lse, tq * heads, "prev_lse")
+    _here(q, k, v, k_pe, cu_q, cu_k, prev_out, prev_lse, out, lse, ws)
+    if ws is None:
+        ws = workspace(prompt_workspace_bytes(tq, tk, n_seqs, heads, kv_heads), q.device)
+    rc = L.smla_prompt_fwd(ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv), _p(k_pe), pe_row, tq, tk, n_seqs,
+                           cu_q.data_ptr(), cu_k.data_ptr(), heads, kv_heads, d, int(causal), sm_scale, _p(prev_out),
+                           _p(prev_lse), out.data_ptr(), int(out.dtype is _F32), lse.data_ptr(), ws.data_ptr(), ws.numel(),
+                           _stream(stream))
+    _check(rc, "smla_prompt_fwd")
     return out, lse, ws
 
 

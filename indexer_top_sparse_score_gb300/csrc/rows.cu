@@ -1,0 +1,379 @@
+// Rows around the expanded form of latent attention: rotation tables
+// (smla_rope_table), rotation of a part of each head (smla_rope_apply), rows of the
+// paged cache back as bf16 values (smla_cache_read). Each value is read and written
+// once: bound by memory, and by latency for few rows.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "../../include/smla_prompt.h"
+#include "rows.cuh"
+
+namespace smla {
+namespace {
+
+// ---------------------------------------------------------------------------- rotation tables
+constexpr int kMaxDim = 256;
+constexpr int kTableThreads = 256;
+
+struct TableParams {
+  float* out;
+  uint64_t first;
+  int32_t n, dim;
+  float magnitude;
+  uint64_t turns[kMaxDim / 2];  // of each pair per position, in 2^-64 turns
+};
+
+// cos and sin of s / 2^64 turns. The angle goes to the float nearest to its upper half,
+// exactly reduced by sincospif, and what that leaves out (under 2^-24 of a turn) is
+// added to first order: c - s d, s + c d.
+__device__ __forceinline__ void cos_sin_of(uint64_t angle, float& c, float& s) {
+  const int32_t hi = static_cast<int32_t>(angle >> 32);
+  const float x = static_cast<float>(hi);
+  const float rest = static_cast<float>(hi - __float2int_rn(x)) + static_cast<float>(static_cast<uint32_t>(angle)) * 0x1p-32f;
+  float s0, c0;
+  sincospif(x * 0x1p-31f, &s0, &c0);
+  const float d = rest * (0x1p-31f * 3.14159265358979f);
+  c = fmaf(-s0, d, c0);
+  s = fmaf(c0, d, s0);
+}
+
+// A thread keeps four pairs and walks the rows: position * turns wraps at whole
+// turns by itself in 64-bit integers, so the angle needs no reduction.
+__global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_constant__ TableParams p) {
+  const int groups = p.dim / 8, half = p.dim / 2;  // groups of four pairs
+  const int g = threadIdx.x % groups, r0 = threadIdx.x / groups, per = kTableThreads / groups;
+  if (r0 >= per) return;
+  uint64_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = p.turns[4 * g + i];
+  for (long long r = static_cast<long long>(blockIdx.x) * per + r0; r < p.n; r += static_cast<long long>(gridDim.x) * per) {
+    float c[4], s[4];
+    const uint64_t pos = p.first + static_cast<uint64_t>(r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cos_sin_of(pos * w[i], c[i], s[i]);
+      c[i] *= p.magnitude;
+      s[i] *= p.magnitude;
+    }
+    float* o = p.out + r * p.dim + 4 * g;
+    *reinterpret_cast<float4*>(o) = make_float4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<float4*>(o + half) = make_float4(s[0], s[1], s[2], s[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------- rotation
+constexpr int kRopeThreads = 128;
+constexpr int kRopeSteps = 4;  // heads a thread
+
+struct RopeParams {
+  const float* cos_sin;
+  int32_t max_pos, dim, inter, rows;
+  const int32_t* positions;
+  const uint16_t* x;
+  long long x_row, x_head;
+  uint16_t* out;
+  long long o_row, o_head;
+  int32_t n_heads, subs, heads_a;  // threads a head, heads a step
+  uint32_t* status;
+  int32_t first_reports;
+};
+
+// A thread takes eight values (four pairs) of up to four heads of one row, all requested
+// before the row's position and angles, which are two latencies away.
+__global__ void __launch_bounds__(kRopeThreads) rope_apply_kernel(const RopeParams p) {
+  if (p.first_reports && blockIdx.x == 0) {
+    report_rows(p.rows, p.status, [&](int r) {
+      const int pos = __ldg(p.positions + r);
+      return pos != -1 && (pos < 0 || pos >= p.max_pos);
+    });
+    return;
+  }
+  const long long id = static_cast<long long>(blockIdx.x - p.first_reports) * kRopeThreads + threadIdx.x;
+  const int per_row = p.subs * p.heads_a;
+  const long long row = id / per_row;
+  if (row >= p.rows) return;
+  const int in = static_cast<int>(id - row * per_row), h0 = in / p.subs, sub = in - h0 * p.subs;
+  const int a = p.inter ? 8 * sub : 4 * sub, b = p.inter ? 8 * sub + 4 : p.dim / 2 + 4 * sub;
+  const uint16_t* x = p.x + row * p.x_row;
+  uint2 wa[kRopeSteps], wb[kRopeSteps];
+#pragma unroll
+  for (int j = 0; j < kRopeSteps; ++j) {
+    const int h = h0 + j * p.heads_a;
+    if (h < p.n_heads) {
+      wa[j] = *reinterpret_cast<const uint2*>(x + h * p.x_head + a);
+      wb[j] = *reinterpret_cast<const uint2*>(x + h * p.x_head + b);
+    }
+  }
+  const int pos = __ldg(p.positions + row);
+  if (pos < 0 || pos >= p.max_pos) {
+    if (pos != -1 && !p.first_reports) set_status(p.status, kStatusBounds);
+    return;
+  }
+  const float* cs = p.cos_sin + static_cast<long long>(pos) * p.dim + 4 * sub;
+  const float4 c = __ldg(reinterpret_cast<const float4*>(cs)), s = __ldg(reinterpret_cast<const float4*>(cs + p.dim / 2));
+  auto turn = [](float& u, float& v, float co, float si) {
+    const float t = u * co - v * si;
+    v = u * si + v * co;
+    u = t;
+  };
+#pragma unroll
+  for (int j = 0; j < kRopeSteps; ++j) {
+    const int h = h0 + j * p.heads_a;
+    if (h >= p.n_heads) break;
+    float v[8] = {bf_lo(wa[j].x), bf_hi(wa[j].x), bf_lo(wa[j].y), bf_hi(wa[j].y),
+                  bf_lo(wb[j].x), bf_hi(wb[j].x), bf_lo(wb[j].y), bf_hi(wb[j].y)};
+    if (p.inter) {
+      turn(v[0], v[1], c.x, s.x), turn(v[2], v[3], c.y, s.y), turn(v[4], v[5], c.z, s.z), turn(v[6], v[7], c.w, s.w);
+    } else {
+      turn(v[0], v[4], c.x, s.x), turn(v[1], v[5], c.y, s.y), turn(v[2], v[6], c.z, s.z), turn(v[3], v[7], c.w, s.w);
+    }
+    uint16_t* o = p.out + row * p.o_row + h * p.o_head;
+    *reinterpret_cast<uint2*>(o + a) = make_uint2(bf_pack(v[0], v[1]), bf_pack(v[2], v[3]));
+    *reinterpret_cast<uint2*>(o + b) = make_uint2(bf_pack(v[4], v[5]), bf_pack(v[6], v[7]));
+  }
+}
+
+// ---------------------------------------------------------------------------- cache rows
+constexpr int kReadThreads = 256, kReadRows = 32;
+constexpr int kTileRow = 656, kTileRopeAt = 528;
+
+struct ReadParams {
+  const uint8_t* kv;
+  const float* kv_scale;
+  const uint8_t* k_idx;
+  const float* k_idx_scale;
+  int32_t num_pages, kv_dtype, idx_fp8, d_idx;
+  const int32_t* tables;
+  int32_t max_pages, n_seqs;
+  const int32_t* cu;
+  int32_t rows;
+  const int32_t* starts;
+  uint16_t* latent;
+  long long latent_stride;
+  uint16_t* pe;
+  long long pe_stride;
+  uint16_t* keys;
+  long long keys_stride;
+  uint32_t* status;
+};
+
+// eight e4m3 codes times a scale, as bf16
+__device__ __forceinline__ uint4 widen8(uint2 c, float s) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint16_t pair = static_cast<uint16_t>((i < 2 ? c.x : c.y) >> (16 * (i & 1)));
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(pair));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    o[i] = bf_pack(f.x * s, f.y * s);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// A block finds the pool rows of 32 output rows: every request's first row is loaded once
+// and counted against them (one latency, no search), then the rows' pieces
+// of 16 output bytes go round the block's threads.
+__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadParams p) {
+  __shared__ int begun[kReadRows + 1];      // requests that begin at or before the block's first row, then at each row
+  __shared__ long long place[kReadRows];    // pool row; -1: zeros; -2: left as it is
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int r0 = blockIdx.x * kReadRows;
+  for (int i = tid; i <= kReadRows; i += kReadThreads) begun[i] = 0;
+  __syncthreads();
+  int before = 0;
+  for (int i = tid; i <= p.n_seqs; i += kReadThreads) {
+    const int c = __ldg(p.cu + i);
+    if (c <= r0) ++before;
+    else if (c - r0 < kReadRows) atomicAdd(&begun[1 + c - r0], 1);
+  }
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  if (lane == 0 && before) atomicAdd(&begun[0], before);
+  __syncthreads();
+  if (tid < kReadRows) {
+    const int r = r0 + tid;
+    int n = begun[1 + tid];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, n, d);
+      if (tid >= d) n += o;
+    }
+    const int b = begun[0] + n - 1;
+    long long at = -2;
+    bool bad = false;
+    if (r < p.rows && b >= 0 && b < p.n_seqs) {
+      const int first = __ldg(p.cu + b), last = __ldg(p.cu + b + 1);
+      if (r < first || r >= last) {  // (an order that runs backwards: the counts do not fit)
+        bad = true;
+      } else {
+        const long long t = static_cast<long long>(p.starts ? __ldg(p.starts + b) : 0) + (r - first);
+        at = -1;
+        if (t >= 0 && t / kPage < p.max_pages) {
+          const int id = __ldg(p.tables + static_cast<long long>(b) * p.max_pages + t / kPage);
+          if (id >= 0 && id < p.num_pages) at = static_cast<long long>(id) * kPage + t % kPage;
+        }
+        bad = at < 0;
+      }
+    }
+    place[tid] = at;
+    if (bad) set_status(p.status, kStatusBounds);
+  }
+  if (blockIdx.x == 0) {  // what no row shows: the list's order and its end
+    bool bad = false;
+    for (int i = tid; i <= p.n_seqs; i += kReadThreads) {
+      const int c = __ldg(p.cu + i);
+      bad |= c < 0 || c > p.rows || (i > 0 && c < __ldg(p.cu + i - 1));
+    }
+    if (bad) set_status(p.status, kStatusBounds);
+  }
+  __syncthreads();
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  // pieces of eight values of a row: 64 latent ones, 8 of the rope part, then the indexer key's
+  const int key_pieces = p.keys ? p.d_idx / 8 : 0, pieces = 72 + key_pieces;
+#pragma unroll 4
+  for (int u = tid; u < kReadRows * pieces; u += kReadThreads) {
+    const int r = u / pieces, j = u - r * pieces;
+    const long long at = place[r];
+    if (at == -2) continue;
+    uint4 v = none;
+    if (j < 72) {
+      if (!(j < 64 ? p.latent : p.pe)) continue;
+      if (at >= 0) {
+        if (p.kv_dtype == SMLA_BF16) {
+          v = __ldg(reinterpret_cast<const uint4*>(p.kv + at * (2 * kDqk)) + j);
+        } else if (p.kv_dtype == SMLA_FP8_E4M3) {
+          v = widen8(__ldg(reinterpret_cast<const uint2*>(p.kv + at * kDqk) + j), __ldg(p.kv_scale + at));
+        } else if (j < 64) {
+          const uint8_t* row = p.kv + at * kTileRow;
+          v = widen8(__ldg(reinterpret_cast<const uint2*>(row) + j), __ldg(reinterpret_cast<const float*>(row + kDv) + (j >> 4)));
+        } else {
+          v = __ldg(reinterpret_cast<const uint4*>(p.kv + at * kTileRow + kTileRopeAt) + (j - 64));
+        }
+      }
+      uint16_t* o = j < 64 ? p.latent + (r0 + r) * p.latent_stride + 8 * j : p.pe + (r0 + r) * p.pe_stride + 8 * (j - 64);
+      *reinterpret_cast<uint4*>(o) = v;
+    } else {
+      const int k = j - 72;
+      if (at >= 0) {
+        const uint8_t* row = p.k_idx + at * kIdxRowBytes;
+        const float s = p.k_idx_scale ? __ldg(p.k_idx_scale + at) : 1.0f;
+        if (p.idx_fp8) {
+          v = widen8(__ldg(reinterpret_cast<const uint2*>(row) + k), s);
+        } else {
+          v = __ldg(reinterpret_cast<const uint4*>(row) + k);
+          if (p.k_idx_scale) {
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = bf_pack(bf_lo(w[i]) * s, bf_hi(w[i]) * s);
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      *reinterpret_cast<uint4*>(p.keys + (r0 + r) * p.keys_stride + 8 * k) = v;
+    }
+  }
+}
+
+bool strided(const void* p, int64_t stride, int64_t width) { return aligned_to(p, 16) && stride % 8 == 0 && stride >= width; }
+
+}  // namespace
+}  // namespace smla
+
+using namespace smla;
+
+extern "C" {
+
+int smla_rope_table(float* cos_sin, int64_t first, int32_t n, int32_t dim, double base, double factor,
+                    int32_t original, double beta_fast, double beta_slow, float magnitude, void* stream) {
+  if (!cos_sin || !aligned_to(cos_sin, 16) || n <= 0 || first < 0 || dim <= 0 || original < 0) return SMLA_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !(factor >= 1.0) || !std::isfinite(base) || !std::isfinite(factor) || !std::isfinite(magnitude)) return SMLA_ERR_INVALID_ARG;
+  if (original > 0 && (!(beta_slow > 0.0) || !(beta_fast >= beta_slow) || !std::isfinite(beta_fast))) return SMLA_ERR_INVALID_ARG;
+  if (dim % 8 || dim > kMaxDim || first > (1LL << 31) - n) return SMLA_ERR_UNSUPPORTED;
+  TableParams p{};
+  p.out = cos_sin, p.first = static_cast<uint64_t>(first), p.n = n, p.dim = dim, p.magnitude = magnitude;
+  const double two_pi = 6.283185307179586476925;
+  double low = 0.0, high = 0.0;
+  if (original > 0) {
+    const double at_fast = dim * std::log(original / (beta_fast * two_pi)) / (2.0 * std::log(base));
+    const double at_slow = dim * std::log(original / (beta_slow * two_pi)) / (2.0 * std::log(base));
+    low = std::max(std::floor(at_fast), 0.0);
+    high = std::min(std::ceil(at_slow), dim - 1.0);
+  }
+  for (int i = 0; i < dim / 2; ++i) {
+    double w = std::pow(base, -2.0 * i / dim);
+    if (original > 0) {
+      const double r = std::min(1.0, std::max(0.0, (i - low) / std::max(high - low, 0.001)));
+      w = w * (1.0 - r) + w / factor * r;
+    } else {
+      w /= factor;
+    }
+    // w / (2 pi) < 1/6 of a turn
+    p.turns[i] = static_cast<uint64_t>(std::ldexp(static_cast<long double>(w) / 6.283185307179586476925286766559L, 64) + 0.5L);
+  }
+  const int per = kTableThreads / (dim / 8);
+  const long long blocks = (static_cast<long long>(n) + per - 1) / per;
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(blocks, 8LL * num_sms()));
+  rope_table_kernel<<<grid, kTableThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return launched();
+}
+
+int smla_rope_apply(const float* cos_sin, int32_t max_pos, int32_t dim, int32_t interleaved, int32_t rows,
+                    const int32_t* positions, const void* x, int64_t x_row, int64_t x_head, int32_t n_heads,
+                    void* out, int64_t out_row, int64_t out_head, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!cos_sin || !positions || !x || !out || !aligned_to(cos_sin, 16) || !aligned_to(positions, 4) || !aligned_to(x, 16) || !aligned_to(out, 16))
+    return SMLA_ERR_INVALID_ARG;
+  if (max_pos <= 0 || rows <= 0 || n_heads <= 0 || dim <= 0) return SMLA_ERR_INVALID_ARG;
+  if (dim % 8 || dim > kMaxDim) return SMLA_ERR_UNSUPPORTED;
+  if (x_row % 8 || x_head % 8 || out_row % 8 || out_head % 8 || x_row < 0 || out_row < 0) return SMLA_ERR_INVALID_ARG;
+  if (n_heads > 1 && (x_head < dim || out_head < dim)) return SMLA_ERR_INVALID_ARG;
+  if (rows > 1 && out_row < dim) return SMLA_ERR_INVALID_ARG;  // rows of the output do not share their place
+  if (out == x && (x_row != out_row || x_head != out_head)) return SMLA_ERR_INVALID_ARG;
+  if (const int rc = check_ws(workspace, workspace_bytes)) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  RopeParams p{};
+  p.cos_sin = cos_sin, p.max_pos = max_pos, p.dim = dim, p.inter = interleaved, p.rows = rows, p.positions = positions;
+  p.x = static_cast<const uint16_t*>(x), p.x_row = x_row, p.x_head = x_head;
+  p.out = static_cast<uint16_t*>(out), p.o_row = out_row, p.o_head = out_head;
+  p.n_heads = n_heads, p.subs = dim / 8, p.heads_a = (n_heads + kRopeSteps - 1) / kRopeSteps;
+  p.status = static_cast<uint32_t*>(workspace);
+  p.first_reports = rows <= kReportRows;
+  if (static_cast<long long>(p.subs) * p.heads_a > INT_MAX) return SMLA_ERR_UNSUPPORTED;
+  const long long threads = static_cast<long long>(rows) * p.subs * p.heads_a;
+  const long long blocks = (threads + kRopeThreads - 1) / kRopeThreads + p.first_reports;
+  if (blocks > INT_MAX) return SMLA_ERR_UNSUPPORTED;
+  if (!p.first_reports && cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
+  rope_apply_kernel<<<static_cast<unsigned>(blocks), kRopeThreads, 0, st>>>(p);
+  return launched();
+}
+
+int smla_cache_read(const smla_paged_cache* cache, const int32_t* page_tables, int32_t max_pages, int32_t n_seqs,
+                    const int32_t* cu_rows, int32_t rows, const int32_t* starts, void* latent, int64_t latent_stride,
+                    void* pe, int64_t pe_stride, void* keys, int64_t keys_stride, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!latent && !pe && !keys) return SMLA_ERR_INVALID_ARG;
+  int rc = check_serve_cache(cache, latent || pe, keys != nullptr);
+  if (rc) return rc;
+  if (!page_tables || !cu_rows || !aligned_to(page_tables, 4) || !aligned_to(cu_rows, 4) || !aligned_to(starts, 4)) return SMLA_ERR_INVALID_ARG;
+  if (max_pages <= 0 || n_seqs <= 0 || rows <= 0) return SMLA_ERR_INVALID_ARG;
+  if ((latent && !strided(latent, latent_stride, kDv)) || (pe && !strided(pe, pe_stride, kDqk - kDv)) ||
+      (keys && !strided(keys, keys_stride, cache->d_idx)))
+    return SMLA_ERR_INVALID_ARG;
+  if (rows > INT_MAX - kReadRows || n_seqs == INT_MAX) return SMLA_ERR_UNSUPPORTED;
+  if ((rc = check_ws(workspace, workspace_bytes))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ReadParams p{};
+  p.kv = static_cast<const uint8_t*>(cache->kv), p.kv_scale = cache->kv_scale;
+  p.k_idx = static_cast<const uint8_t*>(cache->k_idx), p.k_idx_scale = cache->k_idx_scale;
+  p.num_pages = cache->num_pages, p.kv_dtype = cache->kv_dtype, p.idx_fp8 = cache->idx_dtype == SMLA_FP8_E4M3, p.d_idx = cache->d_idx;
+  p.tables = page_tables, p.max_pages = max_pages, p.n_seqs = n_seqs, p.cu = cu_rows, p.rows = rows, p.starts = starts;
+  p.latent = static_cast<uint16_t*>(latent), p.latent_stride = latent_stride;
+  p.pe = static_cast<uint16_t*>(pe), p.pe_stride = pe_stride;
+  p.keys = static_cast<uint16_t*>(keys), p.keys_stride = keys_stride;
+  p.status = static_cast<uint32_t*>(workspace);
+  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
+  cache_read_kernel<<<static_cast<unsigned>((rows + kReadRows - 1) / kReadRows), kReadThreads, 0, st>>>(p);
+  return launched();
+}
+
+}  // extern "C"

@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "rows.cuh"
 #include "serve.h"
 
 namespace smla {
@@ -161,26 +162,11 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const TablesP
 }
 
 // ---------------------------------------------------------------------------- rows
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t bf_pack(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 // two values -> two e4m3 codes (nearest even, saturating), the first in the low byte
 __device__ __forceinline__ uint32_t e4m3_pack(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
-}
-template <int N>
-__device__ __forceinline__ void unpack(const void* p, float* v) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
-    v[2 * i] = bf_lo(w[i]);
-    v[2 * i + 1] = bf_hi(w[i]);
-  }
 }
 __device__ __forceinline__ void load8(const float* p, float* v) {  // 16-byte aligned
   const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
@@ -300,26 +286,6 @@ __device__ __forceinline__ int usable_slot(const AppendParams& p, int slot, int 
   if (!ok && slot != -1 && !p.first_reports) set_status(p.status, kStatusBounds);
   return ok ? slot : -1;
 }
-// How a launch reports rows that it skips as out of range. Up to kReportRows rows
-// its first block only looks all of them over and writes the status word, so that
-// the call needs no launch to clear it (about 2 us of an 8 us call); with more rows
-// that block would end last, the word is cleared by a memset, and the warps report.
-constexpr int kReportRows = 4096;
-
-template <typename Bad>
-__device__ __forceinline__ void report_rows(int rows, uint32_t* status, Bad bad) {
-  bool any = false;
-  for (int r0 = threadIdx.x; r0 < rows; r0 += 8 * blockDim.x) {
-    bool b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = bad(min(r0 + i * static_cast<int>(blockDim.x), rows - 1));  // loads of all eight in flight
-#pragma unroll
-    for (int i = 0; i < 8; ++i) any |= b[i];
-  }
-  const int found = __syncthreads_or(any);
-  if (threadIdx.x == 0) *status = found ? kStatusBounds : 0u;
-}
-
 // One warp per latent row and one per two or four indexer keys (a key takes 16 or 8
 // lanes of 8 values): a row is read once in 16-byte pieces, reduced in registers
 // and written once. Its values are requested before the slot and position are
@@ -621,12 +587,6 @@ int check_rope(const smla_rope* r) {
   if (!r || !r->cos_sin || !aligned_to(r->cos_sin, 16) || r->max_pos <= 0) return SMLA_ERR_INVALID_ARG;
   return SMLA_OK;
 }
-
-int check_ws(void* workspace, size_t bytes) {
-  return !workspace || !aligned_to(workspace, 16) || bytes < kStatusBytes ? SMLA_ERR_WORKSPACE : SMLA_OK;
-}
-
-int launched() { return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA; }
 
 }  // namespace
 }  // namespace smla
