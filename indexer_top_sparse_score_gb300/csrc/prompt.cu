@@ -1,6 +1,34 @@
 // Attention over packed prompts in the expanded form (smla_prompt_fwd):
 //   o = softmax(sm_scale q K^T) V,  lse = ln sum exp(sm_scale q k)
-// a warp for each (token, head), which walks the token's keys with a running maximum and sum.
+// in one pass over the keys with a running maximum and sum.
+//
+// Rows are (token, query head of one key head) pairs: G heads that share a key head (the
+// largest power of two that divides their number, at most 128) lie side by side, so that
+// few tokens of many grouped heads still fill a tile. A block is 256 rows of one request
+// and head group, two tiles of 128 rows; K and V come in tiles of 128 keys that both
+// row tiles use. While the softmax of one row tile runs, the tensor cores work for the
+// other:  PV0(t) QK0(t+1) | PV1(t) QK1(t+1) | PV0(t+1) ...
+//
+// Tensor memory (512 columns): S0 | S1 | O0 | O1, 128 fp32 columns each; P takes the
+// place of its logits as bf16 (64 columns), as MMA operand A. Products of one tile are
+// issued in order, so S(t+1) overwrites P(t) only after PV(t) has read it, and when S(t+1) is
+// complete O holds everything up to t.
+// Shared memory: Q of both tiles, and a ring of 16 KB slots (128 keys x 64 values, 128-byte
+// swizzled) that K and V tiles go through in turn.
+// Warps: 0 TMA loads and the schedule, 1 MMA issue, 2 looks V over (below), 4-7 and 8-11
+// softmax and results of the two row tiles, a thread a row.
+//
+// 0 * NaN. V rows that a row does not see meet its zero probabilities. Tiles that
+// some row of the block sees only in part are looked over before they are used: values
+// that are not finite are zeroed in shared memory, and the first key that holds +inf, -inf or
+// NaN is noted for each of the 128 columns; rows that see it get it added to their result.
+//
+// The plan. A small kernel turns the requests' bounds into a list of blocks. Where blocks
+// are many, CTAs take them one by one, longest first, a few key heads at a time (so that
+// their K and V stay in L2). Where the longest would end late (few rows, many keys), all
+// tiles lie on one line that is cut into equal stretches, one per CTA; blocks that are cut
+// leave fp32 partial results, and the warp that ends a row group's last piece joins them, in
+// the order of the pieces. No CTA waits for another.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -13,92 +41,1032 @@ namespace {
 
 constexpr int kVal = 128;   // values of a head's v
 constexpr int kPe = 64;
+constexpr int kTile = 128;  // rows of a row tile, keys of a key tile
+constexpr int kBlock = 2 * kTile;
+constexpr int kSlot = kTile * 128;
+constexpr int kThreads = 384;
+constexpr int kTmaWarp = 0, kMmaWarp = 1, kScanWarp = 2, kSoftWarp0 = 4;
+constexpr float kRaise = 8.0f;  // log2: the reference maximum is raised only when exceeded by this much
+constexpr int kStart = 2;       // a piece's start and end on the line of work, in tiles
+constexpr int kLongTiles = 8;   // blocks of no more tiles are never cut
+constexpr uint32_t kColS = 0, kColO = 256;
+
+struct Block {      // of the plan
+  int32_t tok0, n_tok;    // rows of q
+  int32_t key0, lim0;     // first key's row; keys that its first token sees (causal: may be <= 0)
+  int32_t n_keys, tiles;  // keys that its last token sees; tiles of them, at least one
+  int32_t pad[2];
+};
+struct Plan {
+  unsigned long long next;  // item to be taken
+  long long line;           // length of the line of work
+  int32_t n_blocks, even;   // even: the line is cut evenly
+  int32_t ctas;             // stretches of the line
+};
 
 struct PromptParams {
-  const uint16_t *q, *k, *v, *pe;
-  long long q_row, q_head, k_row, k_head, v_row, v_head, pe_row;
   int32_t total_q, total_k, n_seqs;
   const int32_t *cu_q, *cu_k;
-  int32_t n_heads, group, d_qk, d_k, causal;
-  float sm_scale;
+  int32_t n_heads, group, causal;
+  int32_t gshift;     // G = 1 << gshift heads of a row tile's tokens
+  int32_t units;      // head groups: n_heads >> gshift
+  int32_t units_a;    // of those that are worked on at a time
+  int32_t d_k;        // values of k (the others of a key are k_pe's)
+  int32_t max_blocks, ctas, can_cut;
+  float scale_log2;   // sm_scale log2 e, not 0
   const float *prev_out, *prev_lse;
   void* out;
   int32_t out_fp32;
   float* lse;
   uint32_t* status;
+  Plan* plan;
+  Block* blocks;
+  int32_t* order;       // blocks, longest first
+  long long* line_at;   // where each block starts on the line
+  int32_t* block_at;    // first block of each request
+  int32_t* tickets;     // [ctas][8]: pieces that have ended
+  float2* part_ml;      // [2 * ctas][256]
+  float4* part_o;       // [2 * ctas][256][32]
 };
 
-__device__ __forceinline__ float bf_at(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
+// ------------------------------------------------------------------ the plan
+constexpr int kPlanThreads = 1024;
 
-__global__ void __launch_bounds__(128) prompt_kernel(const PromptParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long id = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const long long rows = static_cast<long long>(p.total_q) * p.n_heads;
-  if (blockIdx.x == 0) {
-    for (int b = threadIdx.x; b < p.n_seqs; b += 128) {
-      const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
-      if (q0 < 0 || q1 < q0 || q1 > p.total_q || k0 < 0 || k1 < k0 || k1 > p.total_k) set_status(p.status, kStatusBounds);
-    }
-  }
-  if (id >= rows) return;
-  const int token = static_cast<int>(id / p.n_heads), h = static_cast<int>(id - static_cast<long long>(token) * p.n_heads);
-  int b = -1, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-  for (int i = 0; i < p.n_seqs; ++i) {
-    q0 = p.cu_q[i], q1 = p.cu_q[i + 1], k0 = p.cu_k[i], k1 = p.cu_k[i + 1];
-    if (q0 < 0 || q1 < q0 || q1 > p.total_q || k0 < 0 || k1 < k0 || k1 > p.total_k) continue;
-    if (token >= q0 && token < q1) {
-      b = i;
-      break;
-    }
-  }
-  if (b < 0) return;
-  const int seen = p.causal ? max(0, k1 - k0 - (q1 - q0) + token - q0 + 1) : k1 - k0;
-  const int g = h / p.group;
-  float x[6];
+__device__ __forceinline__ long long plan_scan(long long v, long long* warp_sums, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int i = 0; i < 6; ++i) x[i] = 32 * i + lane < p.d_qk ? bf_at(p.q + token * p.q_row + h * p.q_head + 32 * i + lane) : 0.0f;
-  float m = -INFINITY, l = 0.0f, o[4] = {0, 0, 0, 0};
-  for (int j = 0; j < seen; ++j) {
-    const long long kj = k0 + j;
-    float dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      const int d = 32 * i + lane;
-      if (d < p.d_k) dot += x[i] * bf_at(p.k + kj * p.k_row + g * p.k_head + d);
-      else if (d < p.d_qk) dot += x[i] * bf_at(p.pe + kj * p.pe_row + d - p.d_k);
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, s);
-    dot *= p.sm_scale;
-    const float top = fmaxf(m, dot);
-    const float alpha = m == -INFINITY ? 0.0f : expf(m - top), w = top == -INFINITY ? 0.0f : expf(dot - top);
-    m = top;
-    l = l * alpha + w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * alpha + w * bf_at(p.v + kj * p.v_row + g * p.v_head + 32 * i + lane);
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v += o;
   }
-  float lse = l != 0.0f ? m + logf(l) : -INFINITY, f = l != 0.0f ? 1.0f / l : 0.0f, fp = 0.0f;
-  if (p.prev_lse) {
-    const float was = p.prev_lse[id], top = fmaxf(was, lse);
-    if (was != -INFINITY) {
-      const float both = l != 0.0f ? top + logf(expf(was - top) + expf(lse - top)) : was;
-      f *= expf(lse - both);
-      fp = expf(was - both);
-      lse = both;
-    }
-  }
-  __syncwarp();
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  long long w = warp_sums[lane];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long long at = id * kVal + 32 * i + lane;
-    float y = l != 0.0f ? o[i] * f : 0.0f;
-    if (fp != 0.0f) y += fp * p.prev_out[at];
-    if (p.out_fp32) static_cast<float*>(p.out)[at] = y;
-    else static_cast<uint16_t*>(p.out)[at] = static_cast<uint16_t>(bf_pack(y, 0.0f));
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, w, d);
+    if (lane >= d) w += o;
   }
-  if (lane == 0 && p.lse) p.lse[id] = lse;
+  total = __shfl_sync(0xFFFFFFFFu, w, 31);
+  const long long before = __shfl_sync(0xFFFFFFFFu, w, (warp + 31) & 31);
+  return v + (warp ? before : 0);
 }
 
+// One block of threads: requests -> blocks -> longest first, and whether the line is cut.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p) {
+  __shared__ long long warp_sums[32];
+  __shared__ int bins[1024];
+  __shared__ int s_most, s_bad;
+  __shared__ long long s_bound;
+  const int tid = threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;");  // prompt_kernel may set up
+  if (tid == 0) s_most = 1, s_bad = 0, s_bound = 0;
+  for (int i = tid; i < 1024; i += kPlanThreads) bins[i] = 0;
+  for (int i = tid; i < p.ctas * 8; i += kPlanThreads) p.tickets[i] = 0;
+  const int per = kBlock >> p.gshift;  // tokens of a block
+  // blocks of each request
+  long long before = 0;
+  bool bad = false;
+  for (int c0 = 0; c0 < p.n_seqs; c0 += kPlanThreads) {
+    const int b = c0 + tid;
+    int n = 0;
+    if (b < p.n_seqs) {
+      const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
+      if (q0 < 0 || q1 < q0 || q1 > p.total_q || k0 < 0 || k1 < k0 || k1 > p.total_k) bad = true;
+      else n = (q1 - q0 + per - 1) / per;
+    }
+    long long total;
+    const long long upto = before + plan_scan(n, warp_sums, total);
+    if (b < p.n_seqs) {  // (bounds that overlap can make more blocks than there is room for)
+      if (upto > p.max_blocks) bad = true;
+      p.block_at[b] = static_cast<int>(min(upto - n, static_cast<long long>(p.max_blocks)));
+    }
+    before += total;
+  }
+  if (bad) s_bad = 1;
+  const int n_blocks = static_cast<int>(min(before, static_cast<long long>(p.max_blocks)));
+  if (tid == 0) p.block_at[p.n_seqs] = n_blocks;
+  __syncthreads();
+  // the blocks, and where each lies on the line
+  long long line = 0;
+  for (int c0 = 0; c0 < n_blocks; c0 += kPlanThreads) {
+    const int i = c0 + tid;
+    long long cost = 0;
+    if (i < n_blocks) {
+      int lo = 0, hi = p.n_seqs;  // block_at[lo] <= i < block_at[hi], empty requests passed over
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.block_at[mid] <= i) lo = mid; else hi = mid;
+      }
+      const int q0 = p.cu_q[lo], nq = p.cu_q[lo + 1] - q0, k0 = p.cu_k[lo], nk = p.cu_k[lo + 1] - k0;
+      const int i0 = (i - p.block_at[lo]) * per;
+      Block k;
+      k.tok0 = q0 + i0;
+      k.n_tok = min(per, nq - i0);
+      k.key0 = k0;
+      k.lim0 = p.causal ? nk - nq + i0 + 1 : nk;
+      k.n_keys = p.causal ? max(0, k.lim0 + k.n_tok - 1) : nk;
+      k.tiles = max(1, static_cast<int>((static_cast<uint32_t>(k.n_keys) + kTile - 1) / kTile));
+      k.pad[0] = k.pad[1] = 0;
+      p.blocks[i] = k;
+      atomicMax(&s_most, k.tiles);
+      cost = static_cast<long long>(k.tiles + kStart) * p.units;
+    }
+    long long total;
+    const long long upto = line + plan_scan(cost, warp_sums, total);
+    if (i < n_blocks) p.line_at[i] = upto - cost;
+    line += total;
+  }
+  __syncthreads();
+  // longest first, by bins of tiles
+  int shift = 0;
+  while ((s_most >> shift) >= 1024) ++shift;
+  for (int i = tid; i < n_blocks; i += kPlanThreads) atomicAdd(&bins[1023 - (p.blocks[i].tiles >> shift)], 1);
+  __syncthreads();
+  const int count = bins[tid];
+  const long long t = (static_cast<long long>(1023 - tid) << shift) + (shift ? (1 << shift) - 1 : 0) + kStart;  // of the bin's longest
+  long long all;
+  const long long first = plan_scan(count, warp_sums, all) - count;
+  // Taken one by one in this order, an item ends by (work before it) / CTAs + its own: the
+  // last of a bin's is the latest of the bin.
+  const long long work = plan_scan(t * count * p.units, warp_sums, all);
+  if (count > 0) atomicMax(reinterpret_cast<unsigned long long*>(&s_bound), static_cast<unsigned long long>((work - t) / p.ctas + t));
+  __syncthreads();
+  bins[tid] = static_cast<int>(first);
+  __syncthreads();
+  for (int i = tid; i < n_blocks; i += kPlanThreads) p.order[atomicAdd(&bins[1023 - (p.blocks[i].tiles >> shift)], 1)] = i;
+  if (tid == 0) {
+    const long long even = line / p.ctas;
+    p.plan->next = 0;
+    p.plan->line = line;
+    p.plan->n_blocks = n_blocks;
+    p.plan->even = p.can_cut && s_most > kLongTiles && s_bound > even + even / 10 + 6;
+    p.plan->ctas = static_cast<int>(max(1LL, min(static_cast<long long>(p.ctas), line / 4)));
+    *p.status = s_bad ? kStatusBounds : 0u;
+  }
+}
+
+// ------------------------------------------------------------------ waits, TMA, MMA
+// Bounded waits without calls (a call would move the tile loops' values to local memory).
+__device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Gives up after kWaitLimitCycles, or when another role has: false, and *abort is raised
+// (the end of the kernel reports it). One thread.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  long long t0 = 0;
+  for (uint32_t it = 1; !try_bar(a, parity); ++it) {
+    if ((it & 255u) != 0) continue;
+    if (t0 == 0) t0 = clock64();
+    if (*abort || clock64() - t0 > kWaitLimitCycles) {
+      *abort = 2;
+      return false;
+    }
+  }
+  return true;
+}
+// The same by a whole warp: every lane sees the phase, all leave together.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  long long t0 = 0;
+  for (uint32_t it = 1; !__all_sync(0xFFFFFFFFu, try_bar(a, parity)); ++it) {
+    if ((it & 255u) != 0) continue;
+    if (t0 == 0) t0 = clock64();
+    if (__any_sync(0xFFFFFFFFu, *abort != 0 || clock64() - t0 > kWaitLimitCycles)) {
+      *abort = 2;
+      return false;
+    }
+  }
+  return true;
+}
+// true in one thread of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// Shared-memory operand of an MMA: the low word of its descriptor holds the address
+// (in 16 bytes), the high word is the same wherever the operand starts.
+struct Operand {
+  uint32_t lo, hi;
+  __device__ __forceinline__ Operand operator+(int bytes) const { return {lo + static_cast<uint32_t>(bytes >> 4), hi}; }
+};
+__device__ __forceinline__ Operand operand(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  const uint64_t d = smem_desc(saddr, lbo, sbo);
+  return {static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)};
+}
+// A from tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, Operand b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A from shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, Operand a, Operand b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {  // relative error about 2^-22; 2^-inf = 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// ------------------------------------------------------------------ items
+struct Item {        // tiles [t0, t1) of a block and head group; t1 = 0: no more
+  int32_t tok0, n_tok, key0, lim0, n_keys, t0, t1;
+  int32_t unit;
+  int32_t whole;     // all tiles of the block
+  int32_t slot;      // where its partial results go
+  int32_t first_cta, pieces;
+};
+// Tiles that row tile x takes part in: [t0, end), none where end <= t0.
+__device__ __forceinline__ int tokens_of(const PromptParams& p, const Item& it, int x) {
+  return min(it.n_tok - x * (kTile >> p.gshift), kTile >> p.gshift);
+}
+__device__ __forceinline__ int seen_by(const PromptParams& p, const Item& it, int token) {  // keys that a token of the block sees
+  return p.causal ? max(0, it.lim0 + token) : it.n_keys;
+}
+__device__ __forceinline__ int end_of(const PromptParams& p, const Item& it, int x) {
+  const int n = tokens_of(p, it, x);
+  if (n <= 0) return 0;
+  const int seen = seen_by(p, it, x * (kTile >> p.gshift) + n - 1);
+  return min(it.t1, max(1, static_cast<int>((static_cast<uint32_t>(seen) + kTile - 1) / kTile)));
+}
+
+#define SMLA_W4(i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      SMLA_W4(0), SMLA_W4(4), SMLA_W4(8), SMLA_W4(12)
+      : "memory");
+}
+#undef SMLA_W4
+
+template <int D>
+struct Sizes {
+  static constexpr int kChunks = D / 64;                // of a row of q or k
+  static constexpr int kSlots = D == 192 ? 8 : 10;
+  static constexpr int kQTile = kChunks * kSlot;
+  static constexpr int kOffRing = 2 * kQTile, kOffMeta = kOffRing + kSlots * kSlot;
+};
+// Ring positions: K takes kChunks slots, each for itself; V two that lie next to each
+// other (its tile is one operand), so it passes over the ring's last slot.
+template <int D>
+__device__ __forceinline__ int after_k(int pos) {
+  pos += Sizes<D>::kChunks;
+  if (pos >= Sizes<D>::kSlots) pos -= Sizes<D>::kSlots;
+  return pos == Sizes<D>::kSlots - 1 ? 0 : pos;  // where V goes
+}
+template <int D>
+__device__ __forceinline__ int after_v(int pos) {
+  pos += 2;
+  return pos >= Sizes<D>::kSlots ? pos - Sizes<D>::kSlots : pos;
+}
+
+struct Meta {
+  Item items[2];
+  uint64_t item_full[2], item_free[2];
+  uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2];
+  uint64_t k_full[4], v_full[4], v_ok[4];
+  uint64_t slot_free[10];
+  uint64_t scanned, ended;
+  int odd[3][kVal];  // first key whose value in this column is +inf, -inf, NaN
+  int any_odd;
+  uint32_t tmem_slot, status;
+  int abort_flag;
+};
+template <int D>
+constexpr size_t kSmemBytes = Sizes<D>::kOffMeta + sizeof(Meta);
+static_assert(kSmemBytes<192> <= 232448 && kSmemBytes<128> <= 232448, "shared memory budget");
+
+// ------------------------------------------------------------------ results
+struct Joined {  // how a row's sum goes into its result: out = own * f + prev_out * fp
+  float f, fp, lse;
+};
+__device__ __forceinline__ Joined join_prev(const PromptParams& p, long long flat, float m, float l) {
+  Joined j;
+  j.f = l != 0.0f ? 1.0f / l : 0.0f;
+  j.fp = 0.0f;
+  j.lse = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (p.prev_lse) {
+    const float was = p.prev_lse[flat];
+    if (was != -INFINITY) {
+      const float top = fmaxf(was, j.lse);
+      const float both = l != 0.0f ? top + logf(expf(was - top) + expf(j.lse - top)) : was;
+      j.f *= expf(j.lse - both);
+      j.fp = expf(was - both);
+      j.lse = both;
+    }
+  }
+  return j;
+}
+__device__ __forceinline__ void store4(const PromptParams& p, long long flat, int col, float4 v) {
+  const long long at = flat * kVal + col;
+  if (p.out_fp32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;
+  else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(bf_pack(v.x, v.y), bf_pack(v.z, v.w));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                  const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap pe_map, const PromptParams p) {
+  using Z = Sizes<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Meta& M = *reinterpret_cast<Meta*>(smem + Z::kOffMeta);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool aligned = (smem_u32(smem) & 1023u) == 0;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&M.item_full[i], 1);
+      mbar_init(&M.item_free[i], 10);
+      mbar_init(&M.q_full[i], 1);
+      mbar_init(&M.q_free[i], 1);
+      mbar_init(&M.s_full[i], 1);
+      mbar_init(&M.p_full[i], 4);
+      mbar_init(&M.o_full[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&M.k_full[i], 1);
+      mbar_init(&M.v_full[i], 1);
+      mbar_init(&M.v_ok[i], 1);
+    }
+    for (int i = 0; i < Z::kSlots; ++i) mbar_init(&M.slot_free[i], 1);
+    mbar_init(&M.scanned, 1);
+    mbar_init(&M.ended, 8);
+    M.any_odd = 0;
+    M.abort_flag = aligned ? 0 : 2;
+    M.status = aligned ? 0 : kStatusSetup;
+    fence_mbar_init();
+  }
+  for (int i = tid; i < 3 * kVal; i += kThreads) (&M.odd[0][0])[i] = INT_MAX;
+  if (warp == kMmaWarp) {
+    tmem_alloc(&M.tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    prefetch_tensormap(&q_map);
+    prefetch_tensormap(&k_map);
+    prefetch_tensormap(&v_map);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
+  const uint32_t tmem = M.tmem_slot;
+  const uint32_t sbase = smem_u32(smem);
+  volatile int* abort_v = &M.abort_flag;
+
+  if (!aligned) {
+    // nothing: the status says so
+  } else if (warp == kTmaWarp) {
+    // -------------------------------------------------------------- schedule and TMA loads
+    if (lane == 0) {
+      const Plan plan = *p.plan;
+      const int cta = blockIdx.x;
+      const long long items = static_cast<long long>(plan.n_blocks) * p.units;
+      // even: this CTA's stretch [x, y) of the line and where it stands
+      long long x = 0, y = 0, at = 0;
+      int blk = 0, unit = 0;
+      if (plan.even && cta < plan.ctas) {
+        x = plan.line * cta / plan.ctas;
+        y = plan.line * (cta + 1) / plan.ctas;
+        int hi = plan.n_blocks;
+        while (hi - blk > 1) {
+          const int mid = (blk + hi) >> 1;
+          if (p.line_at[mid] <= x) blk = mid; else hi = mid;
+        }
+        const int cost = p.blocks[blk].tiles + kStart;
+        unit = static_cast<int>((x - p.line_at[blk]) / cost);
+        at = p.line_at[blk] + static_cast<long long>(unit) * cost;
+      }
+      auto cta_of = [&](long long pos) {  // that has this place of the line
+        return static_cast<int>(((pos + 1) * plan.ctas + plan.line - 1) / plan.line) - 1;
+      };
+      auto next = [&](Item& it) {
+        if (plan.even) {
+          while (at < y) {
+            const Block b = p.blocks[blk];
+            const long long from = at + kStart;
+            const int t0 = static_cast<int>(min(max(x - from, 0LL), static_cast<long long>(b.tiles)));
+            const int t1 = static_cast<int>(min(max(y - from, 0LL), static_cast<long long>(b.tiles)));
+            const int u = unit;
+            at += b.tiles + kStart;
+            if (++unit == p.units) unit = 0, ++blk;
+            if (t1 <= t0) continue;
+            it = Item{b.tok0, b.n_tok, b.key0, b.lim0, b.n_keys, t0, t1, u, t0 == 0 && t1 == b.tiles, 2 * cta + (t0 == 0), 0, 0};
+            it.first_cta = cta_of(from);
+            it.pieces = cta_of(from + b.tiles - 1) - it.first_cta + 1;
+            return true;
+          }
+          return false;
+        }
+        const long long i = static_cast<long long>(atomicAdd(&p.plan->next, 1ULL));
+        if (i >= items) return false;
+        const long long per = static_cast<long long>(plan.n_blocks) * p.units_a;
+        const int g = static_cast<int>(i / per), u0 = g * p.units_a, n = min(p.units_a, p.units - u0);
+        const long long r = i - g * per;
+        const int rank = static_cast<int>(r / n);
+        const Block b = p.blocks[p.order[rank]];
+        it = Item{b.tok0, b.n_tok, b.key0, b.lim0, b.n_keys, 0, b.tiles, u0 + static_cast<int>(r - static_cast<long long>(rank) * n), 1, 0, 0, 1};
+        return true;
+      };
+      uint32_t n = 0, kg = 0, vg = 0, used = 0;  // items, K tiles, V tiles, parity of each slot's use
+      uint32_t nq[2] = {0, 0};
+      int pos = 0;
+      bool ok = true, more = true;
+      auto take_slot = [&](int s) {
+        const bool got = wait_one(&M.slot_free[s], ((used >> s) & 1u) ^ 1u, abort_v);
+        used ^= 1u << s;
+        return got;
+      };
+      while (ok && more) {
+        Item it{};
+        more = next(it);
+        if (n >= 2 && !wait_one(&M.item_free[n & 1], ((n >> 1) - 1) & 1, abort_v)) break;
+        M.items[n & 1] = it;
+        mbar_arrive(&M.item_full[n & 1]);
+        ++n;
+        if (!more) break;
+        const int kv_head = static_cast<int>((static_cast<long long>(it.unit) << p.gshift) / p.group);
+        auto load_q = [&](int x) {
+          if (end_of(p, it, x) <= it.t0) return true;
+          if (nq[x] > 0 && !wait_one(&M.q_free[x], (nq[x] - 1) & 1, abort_v)) return false;
+          ++nq[x];
+          mbar_arrive_expect_tx(&M.q_full[x], Z::kQTile);
+          const int token = it.tok0 + x * (kTile >> p.gshift);
+          for (int c = 0; c < Z::kChunks; ++c)
+            tma_box(smem + x * Z::kQTile + c * kSlot, &q_map, &M.q_full[x], 64 * c, it.unit << p.gshift, token);
+          return true;
+        };
+        auto load_k = [&](int t) {
+          uint64_t* bar = &M.k_full[kg++ & 3];
+          for (int c = 0; c < Z::kChunks; ++c) {
+            const int s = pos + c >= Z::kSlots ? pos + c - Z::kSlots : pos + c;
+            if (!take_slot(s)) return false;
+            if (c == 0) mbar_arrive_expect_tx(bar, Z::kChunks * kSlot);
+            const bool shared = 64 * c >= p.d_k;
+            tma_box(smem + Z::kOffRing + s * kSlot, shared ? &pe_map : &k_map, bar, shared ? 0 : 64 * c, shared ? 0 : kv_head, it.key0 + t * kTile);
+          }
+          pos = after_k<D>(pos);
+          return true;
+        };
+        auto load_v = [&](int t) {
+          uint64_t* bar = &M.v_full[vg++ & 3];
+          for (int c = 0; c < 2; ++c) {
+            if (!take_slot(pos + c)) return false;
+            if (c == 0) mbar_arrive_expect_tx(bar, 2 * kSlot);
+            tma_box(smem + Z::kOffRing + (pos + c) * kSlot, &v_map, bar, 64 * c, kv_head, it.key0 + t * kTile);
+          }
+          pos = after_v<D>(pos);
+          return true;
+        };
+        ok = load_q(0) && load_k(it.t0) && load_q(1) && load_v(it.t0);
+        for (int t = it.t0 + 1; ok && t < it.t1; ++t) ok = load_k(t) && load_v(t);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // -------------------------------------------------------------- MMA issue
+    // Warp-wide on warp-uniform values, each batch of MMAs unrolled and issued by one
+    // elected thread: descriptors come from uniform registers.
+    constexpr uint32_t id_qk = instr_desc(128, 128, kFmtBF16, kFmtBF16, false, false);
+    constexpr uint32_t id_pv = instr_desc(128, 128, kFmtBF16, kFmtBF16, false, true);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const uint32_t sb = __shfl_sync(0xFFFFFFFFu, sbase, 0);
+    const Operand q_desc = operand(sb, 16, 1024);
+    const Operand k_desc = operand(sb + Z::kOffRing, 16, 1024);
+    const Operand v_desc = operand(sb + Z::kOffRing, kSlot, 1024);  // read as values x keys
+    uint32_t n = 0, kg = 0, vg = 0;
+    uint32_t nq[2] = {0, 0}, ns[2] = {0, 0};  // row tiles begun, P tiles used
+    int pos = 0;
+    bool ok = true;
+    auto qk = [&](int x, int kpos) {
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < Z::kChunks; ++c) {
+          const int s = kpos + c >= Z::kSlots ? kpos + c - Z::kSlots : kpos + c;
+          const Operand k = k_desc + s * kSlot;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss(tm + kColS + kTile * x, q_desc + (x * Z::kQTile + c * kSlot + 32 * kk), k + 32 * kk, id_qk, c != 0 || kk != 0);
+        }
+        mma_commit(&M.s_full[x]);
+      }
+      __syncwarp();
+    };
+    auto pv = [&](int x, int vpos, bool first) {
+      tc_fence_after();
+      if (elect_one()) {
+        const Operand v = v_desc + vpos * kSlot;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tm + kColO + kVal * x, tm + kColS + kTile * x + 8 * kk, v + 2048 * kk, id_pv, kk != 0 || !first);
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) mma_commit(bar);
+      __syncwarp();
+    };
+    auto free_k = [&](int kpos) {
+      for (int c = 0; c < Z::kChunks; ++c) commit(&M.slot_free[kpos + c >= Z::kSlots ? kpos + c - Z::kSlots : kpos + c]);
+    };
+    while (ok) {
+      if (!wait_warp(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) { ok = false; break; }
+      const Item it = M.items[n & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&M.item_free[n & 1]);
+      ++n;
+      if (it.t1 == 0) break;
+      const int t0 = __shfl_sync(0xFFFFFFFFu, it.t0, 0), t1 = __shfl_sync(0xFFFFFFFFu, it.t1, 0);
+      const int end[2] = {__shfl_sync(0xFFFFFFFFu, end_of(p, it, 0), 0), __shfl_sync(0xFFFFFFFFu, end_of(p, it, 1), 0)};
+      ok = wait_warp(&M.k_full[kg & 3], (kg >> 2) & 1, abort_v);
+      ++kg;
+      int kpos = pos;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (!ok || end[x] <= t0) continue;
+        ok = wait_warp(&M.q_full[x], nq[x] & 1, abort_v);
+        if (!ok) break;
+        ++nq[x];
+        qk(x, kpos);
+        if (t0 + 1 == end[x]) commit(&M.q_free[x]);
+      }
+      if (!ok) break;
+      free_k(kpos);
+      for (int t = t0; ok && t < t1; ++t) {
+        const int vpos = after_k<D>(kpos);
+        const bool next = t + 1 < t1;
+        kpos = after_v<D>(vpos);
+        bool have_k = false;
+        ok = wait_warp(&M.v_ok[vg & 3], (vg >> 2) & 1, abort_v);
+        ++vg;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || t >= end[x]) continue;
+          ok = wait_warp(&M.p_full[x], ns[x] & 1, abort_v);
+          if (!ok) break;
+          ++ns[x];
+          pv(x, vpos, t == t0);
+          if (t + 1 == end[x]) {
+            commit(&M.o_full[x]);
+            continue;
+          }
+          if (!have_k) {
+            ok = wait_warp(&M.k_full[kg & 3], (kg >> 2) & 1, abort_v);
+            ++kg;
+            have_k = true;
+            if (!ok) break;
+          }
+          qk(x, kpos);
+          if (t + 2 == end[x]) commit(&M.q_free[x]);
+        }
+        if (!ok) break;
+        commit(&M.slot_free[vpos]);
+        commit(&M.slot_free[vpos + 1]);
+        if (next) free_k(kpos);
+      }
+      pos = kpos;
+    }
+    if (!ok) *abort_v = 2;
+  } else if (warp == kScanWarp) {
+    // -------------------------------------------------------------- V rows that some row does not see
+    uint32_t n = 0, vg = 0;
+    int pos = 0;
+    bool ok = true;
+    while (ok) {
+      if (!wait_warp(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) break;
+      const Item it = M.items[n & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&M.item_free[n & 1]);
+      if (it.t1 == 0) break;
+      if (n > 0) {  // the results of the item before are out: what was noted for it goes
+        if (!wait_warp(&M.ended, (n - 1) & 1, abort_v)) break;
+        const int any = *const_cast<volatile int*>(&M.any_odd);
+        __syncwarp();
+        if (any) {
+          for (int i = lane; i < 3 * kVal; i += 32) (&M.odd[0][0])[i] = INT_MAX;
+          if (lane == 0) M.any_odd = 0;
+          __syncwarp();
+        }
+      }
+      ++n;
+      const int all_see = seen_by(p, it, 0);  // keys before this one are seen by every row
+      for (int t = it.t0; t < it.t1; ++t) {
+        const int vpos = after_k<D>(pos);
+        pos = after_v<D>(vpos);
+        if (!wait_warp(&M.v_full[vg & 3], (vg >> 2) & 1, abort_v)) { ok = false; break; }
+        if ((t + 1) * kTile > all_see) {
+          bool changed = false;
+          for (int r = lane; r < kTile; r += 32) {
+            const int key = t * kTile + r;
+            if (key < all_see) continue;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              uint8_t* row = smem + Z::kOffRing + (vpos + c) * kSlot + r * 128;
+              uint32_t hit = 0;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * j);
+                auto odd = [](uint32_t v) { return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u; };
+                hit |= static_cast<uint32_t>(odd(w.x) || odd(w.y) || odd(w.z) || odd(w.w)) << j;
+              }
+              for (; hit; hit &= hit - 1) {
+                const int j = __ffs(hit) - 1, col = 64 * c + 8 * (j ^ (r & 7));
+                uint16_t* v = reinterpret_cast<uint16_t*>(row + 16 * j);
+                for (int e = 0; e < 8; ++e) {
+                  const uint16_t w = v[e];
+                  if ((w & 0x7F80u) != 0x7F80u) continue;
+                  v[e] = 0;
+                  const int kind = w == 0x7F80u ? 0 : w == 0xFF80u ? 1 : 2;
+                  if (key < it.n_keys) atomicMin(&M.odd[kind][col + e], key);
+                }
+                changed = true;
+              }
+            }
+          }
+          if (changed) {
+            M.any_odd = 1;
+            fence_proxy_async_smem();
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&M.v_ok[vg & 3]);
+        ++vg;
+      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&M.scanned);
+    }
+  } else if (warp >= kSoftWarp0) {
+    // -------------------------------------------------------------- softmax, results
+    const int x = (warp - kSoftWarp0) >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;  // of the row tile
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t s_col = tmem + lanes + kColS + kTile * x, o_col = tmem + lanes + kColO + kVal * x;
+    const bool negative = p.scale_log2 < 0.0f;
+    const float hidden = negative ? INFINITY : -INFINITY;
+    uint32_t n = 0, g = 0, no = 0;  // items, tiles, results
+    bool ok = true;
+    while (ok) {
+      if (!wait_warp(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) break;
+      const Item it = M.items[n & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&M.item_free[n & 1]);
+      if (it.t1 == 0) break;
+      const int per = kTile >> p.gshift, end = end_of(p, it, x), n_tok = tokens_of(p, it, x);
+      const int token = x * per + (row >> p.gshift);  // of the block
+      const bool exists = (row >> p.gshift) < n_tok;
+      const int seen = seen_by(p, it, token);
+      float m = -INFINITY, l = 0.0f;
+      for (int t = it.t0; t < end; ++t, ++g) {
+        if (!wait_warp(&M.s_full[x], g & 1, abort_v)) { ok = false; break; }
+        tc_fence_after();
+        float s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_col + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
+        tmem_wait_ld();
+        const int left = seen - t * kTile;  // keys of the tile that the row sees
+        if (__any_sync(0xFFFFFFFFu, left < kTile)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] = i < left ? s[i] : hidden;
+        }
+        float top = hidden;
+        if (negative) {
+#pragma unroll
+          for (int i = 0; i < 128; i += 2) top = min3(top, s[i], s[i + 1]);
+        } else {
+          float other = hidden;
+#pragma unroll
+          for (int i = 0; i < 128; i += 4) {
+            top = max3(top, s[i], s[i + 1]);
+            other = max3(other, s[i + 2], s[i + 3]);
+          }
+          top = fmaxf(top, other);
+        }
+        top *= p.scale_log2;
+        const bool raise = top > m + kRaise || (m == -INFINITY && top > -INFINITY);
+        float alpha = 1.0f;
+        if (raise) {
+          alpha = m == -INFINITY ? 0.0f : exp2_fast(m - top);
+          m = top;
+          l *= alpha;
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        if (t > it.t0 && __any_sync(0xFFFFFFFFu, raise)) {  // O holds every tile before this one
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(o_col + 16 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st_x16(o_col + 16 * c, o);
+          }
+        }
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const float2 factor = make_float2(p.scale_log2, p.scale_log2), minus = make_float2(-ref, -ref);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 y = fma2(make_float2(s[32 * h + i], s[32 * h + i + 1]), factor, minus);
+            const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
+            // P is rounded to bf16 (off by at most 2^-8 of a probability); the sum l is not
+            pk[i >> 1] = bf_pack(e.x, e.y);
+          }
+          tmem_st_x16(s_col + 16 * h, pk);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&M.p_full[x]);
+      }
+      if (!ok) break;
+      // ---- results
+      const int head = it.unit << p.gshift;
+      const long long flat = (static_cast<long long>(it.tok0) + token) * p.n_heads + head + (row & ((1 << p.gshift) - 1));
+      const bool some = end > it.t0;
+      if (!wait_warp(&M.scanned, n & 1, abort_v)) break;
+      if (some) {
+        if (!wait_warp(&M.o_full[x], no & 1, abort_v)) break;
+        ++no;
+        tc_fence_after();
+      }
+      const int any_odd = *const_cast<volatile int*>(&M.any_odd);
+      auto odd_value = [&](int col, float v) {  // what the row sees of values that are not finite
+        const bool up = M.odd[0][col] < seen, down = M.odd[1][col] < seen, nan = M.odd[2][col] < seen;
+        return nan || (up && down) ? NAN : up ? v + INFINITY : down ? v - INFINITY : v;
+      };
+      if (n_tok > 0 && it.whole) {
+        Joined j{0.0f, 0.0f, -INFINITY};
+        if (exists) {
+          j = join_prev(p, flat, m, l);
+          if (p.lse) p.lse[flat] = j.lse;
+        }
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld_32x32b_x32(o_col + 32 * c, reinterpret_cast<uint32_t*>(v));
+          tmem_wait_ld();
+          if (exists) {
+            if (any_odd) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = odd_value(32 * c + i, v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = l != 0.0f ? v[i] * j.f : 0.0f;
+            if (j.fp != 0.0f) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 was = *reinterpret_cast<const float4*>(p.prev_out + flat * kVal + 32 * c + i);
+                v[i] += j.fp * was.x, v[i + 1] += j.fp * was.y, v[i + 2] += j.fp * was.z, v[i + 3] += j.fp * was.w;
+              }
+            }
+            if (p.out_fp32) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) store4(p, flat, 32 * c + i, make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+            } else {
+              uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + flat * kVal + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                o[i] = make_uint4(bf_pack(v[8 * i], v[8 * i + 1]), bf_pack(v[8 * i + 2], v[8 * i + 3]), bf_pack(v[8 * i + 4], v[8 * i + 5]),
+                                  bf_pack(v[8 * i + 6], v[8 * i + 7]));
+            }
+          }
+          __syncwarp();
+        }
+      } else if (quad * 32 >> p.gshift < n_tok) {  // a piece: some row of the warp exists
+        const int r0 = x * kTile + quad * 32;      // the warp's first row in the block
+        const long long at = static_cast<long long>(it.slot) * kBlock + r0 + lane;
+#pragma unroll 1
+        for (int c = 0; c < 4 && some; ++c) {
+          float v[32];
+          tmem_ld_32x32b_x32(o_col + 32 * c, reinterpret_cast<uint32_t*>(v));
+          tmem_wait_ld();
+          if (exists) {
+            if (any_odd) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = odd_value(32 * c + i, v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p.part_o[at * 32 + 8 * c + i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+          __syncwarp();
+        }
+        if (exists) p.part_ml[at] = make_float2(m, some ? l : 0.0f);
+        __threadfence();
+        __syncwarp();
+        int ended = 0;
+        if (lane == 0) ended = atomicAdd(p.tickets + it.first_cta * 8 + (warp - kSoftWarp0), 1);
+        ended = __shfl_sync(0xFFFFFFFFu, ended, 0);
+        if (ended == it.pieces - 1) {
+          // The last of the pieces of these 32 rows: join them, by their maxima and sums, in
+          // the order of the pieces. A lane's row for the weights, then a row's 128 values
+          // over the lanes, eight rows at a time.
+          __threadfence();
+          auto slot_of = [&](int i) { return static_cast<long long>(2 * (it.first_cta + i) + (i == 0)) * kBlock + r0; };
+          float best = -INFINITY, sum = 0.0f;
+          if (exists) {
+            for (int i = 0; i < it.pieces; ++i) {
+              const float2 ml = __ldcg(p.part_ml + slot_of(i) + lane);
+              if (ml.y != 0.0f) best = fmaxf(best, ml.x);
+            }
+            for (int i = 0; i < it.pieces; ++i) {
+              const float2 ml = __ldcg(p.part_ml + slot_of(i) + lane);
+              if (ml.y != 0.0f) sum += ml.y * exp2_fast(ml.x - best);
+            }
+          }
+          Joined j{0.0f, 0.0f, -INFINITY};
+          if (exists) {
+            j = join_prev(p, flat, best, sum);
+            if (p.lse) p.lse[flat] = j.lse;
+          }
+          const uint32_t rows = __ballot_sync(0xFFFFFFFFu, exists);
+#pragma unroll 1
+          for (int b = 0; b < 32; b += 8) {
+            if (!(rows >> b & 0xFFu)) continue;
+            float4 acc[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+            for (int i = 0; i < it.pieces; ++i) {
+              const long long s = slot_of(i);
+              float w = -1.0f;  // nothing to add
+              if (exists) {
+                const float2 ml = __ldcg(p.part_ml + s + lane);
+                if (ml.y != 0.0f) w = exp2_fast(ml.x - best);
+              }
+              float4 v[8];
+              float wr[8];
+#pragma unroll
+              for (int r = 0; r < 8; ++r) {
+                wr[r] = __shfl_sync(0xFFFFFFFFu, w, b + r);
+                if (wr[r] != -1.0f) v[r] = __ldcg(p.part_o + (s + b + r) * 32 + lane);
+              }
+#pragma unroll
+              for (int r = 0; r < 8; ++r)
+                if (wr[r] != -1.0f)
+                  acc[r].x += wr[r] * v[r].x, acc[r].y += wr[r] * v[r].y, acc[r].z += wr[r] * v[r].z, acc[r].w += wr[r] * v[r].w;
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const float f = __shfl_sync(0xFFFFFFFFu, j.f, b + r), fp = __shfl_sync(0xFFFFFFFFu, j.fp, b + r);
+              const long long to = __shfl_sync(0xFFFFFFFFu, flat, b + r);
+              if (!(rows >> (b + r) & 1u)) continue;
+              float4 v = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
+              if (fp != 0.0f) {
+                const float4 was = *reinterpret_cast<const float4*>(p.prev_out + to * kVal + 4 * lane);
+                v.x += fp * was.x, v.y += fp * was.y, v.z += fp * was.z, v.w += fp * was.w;
+              }
+              store4(p, to, 4 * lane, v);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&M.ended);
+      ++n;
+    }
+    if (!ok) *abort_v = 2;
+  }
+
+  __syncwarp();
+  if (*abort_v == 2 && !M.status) set_status(&M.status, kStatusTimeout);
+  if (*abort_v) {  // a wait gave up: let copies that are still under way land before the memory goes
+    const long long t0 = clock64();
+    while (clock64() - t0 < 4000000) __nanosleep(1000);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && M.status) set_status(p.status, M.status);
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ host
+// Heads as [rows][heads][width] 16-bit values, loaded in boxes of 64 values, `heads` heads and
+// `rows` rows, 128-byte swizzled.
+bool encode_heads(CUtensorMap* map, const smla_heads& t, uint64_t width, uint64_t n_heads, uint64_t rows, uint32_t box_heads, uint32_t box_rows) {
+  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+    return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(f) : nullptr;
+  }();
+  if (!encode) return false;
+  // (one head's or one row's stride is never used)
+  const uint64_t row = rows > 1 ? t.row_stride : std::max<int64_t>(t.row_stride, width);
+  const uint64_t head = n_heads > 1 ? t.head_stride : (width + 7) / 8 * 8;
+  const cuuint64_t dims[3] = {width, n_heads, rows}, strides[2] = {head * 2, row * 2};
+  const cuuint32_t box[3] = {64, box_heads, box_rows}, steps[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(t.data), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& pe, const PromptParams& p, cudaStream_t st) {
+  if (cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes<D>)) != cudaSuccess)
+    return SMLA_ERR_CUDA;
+  plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
+  cudaLaunchAttribute at{};  // set up while the plan is made
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes<D>;
+  cfg.stream = st;
+  cfg.attrs = &at, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_kernel<D>, q, k, v, pe, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Sizes that follow from the shape, and the workspace's parts; its bytes.
+size_t layout(PromptParams& p, uint8_t* ws) {
+  p.gshift = 0;
+  while (p.gshift < 7 && p.group % (2 << p.gshift) == 0) ++p.gshift;
+  p.units = p.n_heads >> p.gshift;
+  p.max_blocks = p.total_q / (kBlock >> p.gshift) + p.n_seqs;
+  p.ctas = num_sms();
+  p.can_cut = p.total_k > kLongTiles * kTile;
+  size_t at = kStatusBytes;
+  p.plan = reinterpret_cast<Plan*>(ws + at);
+  at += up256(sizeof(Plan));
+  p.tickets = reinterpret_cast<int32_t*>(ws + at);
+  at += up256(static_cast<size_t>(p.ctas) * 8 * 4);
+  p.blocks = reinterpret_cast<Block*>(ws + at);
+  at += up256(static_cast<size_t>(p.max_blocks) * sizeof(Block));
+  p.line_at = reinterpret_cast<long long*>(ws + at);
+  at += up256(static_cast<size_t>(p.max_blocks) * 8);
+  p.order = reinterpret_cast<int32_t*>(ws + at);
+  at += up256(static_cast<size_t>(p.max_blocks) * 4);
+  p.block_at = reinterpret_cast<int32_t*>(ws + at);
+  at += up256((static_cast<size_t>(p.n_seqs) + 1) * 4);
+  if (p.can_cut) {
+    p.part_ml = reinterpret_cast<float2*>(ws + at);
+    at += static_cast<size_t>(p.ctas) * 2 * kBlock * 8;
+    p.part_o = reinterpret_cast<float4*>(ws + at);
+    at += static_cast<size_t>(p.ctas) * 2 * kBlock * kVal * 4;
+  }
+  return at;
+}
+
+bool sizes_ok(const PromptParams& p) {  // 32-bit rows and counts
+  return p.n_heads <= 1024 && p.n_seqs <= (1 << 24) && p.total_q <= INT_MAX / 2 && p.total_k <= INT_MAX - 1024;
+}
 bool heads_ok(const smla_heads* t, int64_t width, int32_t n) {
   return t && t->data && aligned_to(t->data, 16) && t->row_stride % 8 == 0 && t->head_stride % 8 == 0 && t->row_stride >= width &&
          t->row_stride < (1LL << 35) && t->head_stride < (1LL << 35) && (n == 1 || t->head_stride >= width);
@@ -112,8 +1080,11 @@ using namespace smla;
 extern "C" {
 
 size_t smla_prompt_fwd_workspace_size(int32_t total_q, int32_t total_k, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads) {
-  (void)total_q, (void)total_k, (void)n_seqs, (void)n_heads, (void)n_kv_heads;
-  return kStatusBytes;
+  if (total_q <= 0 || total_k <= 0 || n_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads) return kStatusBytes;
+  PromptParams p{};
+  p.total_q = total_q, p.total_k = total_k, p.n_seqs = n_seqs, p.n_heads = n_heads, p.group = n_heads / n_kv_heads;
+  if (!sizes_ok(p)) return kStatusBytes;
+  return layout(p, nullptr);
 }
 
 int smla_prompt_fwd(const smla_heads* q, const smla_heads* k, const smla_heads* v, const void* k_pe,
@@ -124,29 +1095,33 @@ int smla_prompt_fwd(const smla_heads* q, const smla_heads* k, const smla_heads* 
   if (total_q <= 0 || total_k <= 0 || n_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || d_qk <= 0 || n_heads % n_kv_heads) return SMLA_ERR_INVALID_ARG;
   const int d_k = k_pe ? d_qk - kPe : d_qk;
   if (d_qk != 128 && d_qk != 192) return SMLA_ERR_UNSUPPORTED;
-  if (n_heads > 1024 || n_seqs > (1 << 24) || total_q > INT_MAX - 1024 || total_k > INT_MAX - 1024) return SMLA_ERR_UNSUPPORTED;
+  PromptParams p{};
+  p.total_q = total_q, p.total_k = total_k, p.n_seqs = n_seqs, p.n_heads = n_heads, p.group = n_heads / n_kv_heads;
+  if (!sizes_ok(p)) return SMLA_ERR_UNSUPPORTED;
   if (!heads_ok(q, d_qk, n_heads) || !heads_ok(k, d_k, n_kv_heads) || !heads_ok(v, kVal, n_kv_heads)) return SMLA_ERR_INVALID_ARG;
   if (k_pe && (!aligned_to(k_pe, 16) || k_pe_stride % 8 || k_pe_stride < kPe || k_pe_stride >= (1LL << 35))) return SMLA_ERR_INVALID_ARG;
   if (!cu_q || !cu_k || !out || !aligned_to(cu_q, 4) || !aligned_to(cu_k, 4) || !aligned_to(out, 16) || !aligned_to(lse, 4)) return SMLA_ERR_INVALID_ARG;
   if ((prev_out == nullptr) != (prev_lse == nullptr) || !aligned_to(prev_out, 16) || !aligned_to(prev_lse, 4) || !std::isfinite(sm_scale))
     return SMLA_ERR_INVALID_ARG;
   if (static_cast<const void*>(prev_out) == out && out && !out_fp32) return SMLA_ERR_INVALID_ARG;
-  if (const int rc = check_ws(workspace, workspace_bytes)) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  PromptParams p{};
-  p.q = static_cast<const uint16_t*>(q->data), p.q_row = q->row_stride, p.q_head = q->head_stride;
-  p.k = static_cast<const uint16_t*>(k->data), p.k_row = k->row_stride, p.k_head = k->head_stride;
-  p.v = static_cast<const uint16_t*>(v->data), p.v_row = v->row_stride, p.v_head = v->head_stride;
-  p.pe = static_cast<const uint16_t*>(k_pe), p.pe_row = k_pe_stride;
-  p.total_q = total_q, p.total_k = total_k, p.n_seqs = n_seqs, p.cu_q = cu_q, p.cu_k = cu_k;
-  p.n_heads = n_heads, p.group = n_heads / n_kv_heads, p.d_qk = d_qk, p.d_k = d_k, p.causal = causal, p.sm_scale = sm_scale;
+  if (!workspace || !aligned_to(workspace, 16) || workspace_bytes < layout(p, static_cast<uint8_t*>(workspace))) return SMLA_ERR_WORKSPACE;
+  p.cu_q = cu_q, p.cu_k = cu_k, p.causal = causal != 0, p.d_k = d_k;
+  // never 0: masked logits are infinities, and 0 times those is not
+  const float s = sm_scale * 1.4426950408889634f;
+  p.scale_log2 = s < 0.0f ? std::min(s, -1e-37f) : std::max(s, 1e-37f);
   p.prev_out = prev_out, p.prev_lse = prev_lse, p.out = out, p.out_fp32 = out_fp32, p.lse = lse;
   p.status = static_cast<uint32_t*>(workspace);
-  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
-  const long long warps = static_cast<long long>(total_q) * n_heads;
-  if ((warps + 3) / 4 > INT_MAX) return SMLA_ERR_UNSUPPORTED;
-  prompt_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, st>>>(p);
-  return launched();
+  // heads worked on at a time: K and V of their keys in some 40 MB of L2
+  const int64_t kv_bytes = static_cast<int64_t>(total_k) * (d_k + kVal) * 2, at_once = std::max<int64_t>(1, (40LL << 20) / kv_bytes);
+  p.units_a = static_cast<int32_t>(std::min<int64_t>(p.units, at_once * (p.group >> p.gshift)));
+  CUtensorMap q_map{}, k_map{}, v_map{}, pe_map{};
+  const int g = 1 << p.gshift;
+  const smla_heads pe{k_pe, k_pe_stride, kPe};
+  if (!encode_heads(&q_map, *q, d_qk, n_heads, total_q, g, kTile / g) || !encode_heads(&k_map, *k, d_k, n_kv_heads, total_k, 1, kTile) ||
+      !encode_heads(&v_map, *v, kVal, n_kv_heads, total_k, 1, kTile) || (k_pe && !encode_heads(&pe_map, pe, kPe, 1, total_k, 1, kTile)))
+    return SMLA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return d_qk == 192 ? launch<192>(q_map, k_map, v_map, pe_map, p, st) : launch<128>(q_map, k_map, v_map, pe_map, p, st);
 }
 
 }  // extern "C"
