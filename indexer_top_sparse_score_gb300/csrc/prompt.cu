@@ -15,7 +15,7 @@
 // complete O holds everything up to t.
 // Shared memory: Q of both tiles, and a ring of 16 KB slots (128 keys x 64 values, 128-byte
 // swizzled) that K and V tiles go through in turn.
-// Warps: 0 TMA loads and the schedule, 1 MMA issue, 2 looks V over (below), 4-7 and 8-11
+// Warps: 0 TMA loads and the schedule, 1 MMA issue, 2-3 look V over (below), 4-7 and 8-11
 // softmax and results of the two row tiles, a thread a row.
 //
 // 0 * NaN. V rows that a row does not see meet its zero probabilities. Tiles that
@@ -45,7 +45,7 @@ constexpr int kTile = 128;  // rows of a row tile, keys of a key tile
 constexpr int kBlock = 2 * kTile;
 constexpr int kSlot = kTile * 128;
 constexpr int kThreads = 384;
-constexpr int kTmaWarp = 0, kMmaWarp = 1, kScanWarp = 2, kSoftWarp0 = 4;
+constexpr int kTmaWarp = 0, kMmaWarp = 1, kScanWarp0 = 2, kSoftWarp0 = 4;
 constexpr float kRaise = 8.0f;  // log2: the reference maximum is raised only when exceeded by this much
 constexpr int kStart = 2;       // a piece's start and end on the line of work, in tiles
 constexpr int kLongTiles = 8;   // blocks of no more tiles are never cut
@@ -76,12 +76,12 @@ struct PromptParams {
   float scale_log2;   // sm_scale log2 e, not 0
   const float *prev_out, *prev_lse;
   void* out;
-  int32_t out_fp32;
+  int32_t out_fp32, out_sectors;  // fp32; on a 32-byte boundary
   float* lse;
   uint32_t* status;
   Plan* plan;
   Block* blocks;
-  int32_t* order;       // blocks, longest first
+  Block* sorted;        // longest first
   long long* line_at;   // where each block starts on the line
   int32_t* block_at;    // first block of each request
   int32_t* tickets;     // [ctas][8]: pieces that have ended
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
   __syncthreads();
   bins[tid] = static_cast<int>(first);
   __syncthreads();
-  for (int i = tid; i < n_blocks; i += kPlanThreads) p.order[atomicAdd(&bins[1023 - (p.blocks[i].tiles >> shift)], 1)] = i;
+  for (int i = tid; i < n_blocks; i += kPlanThreads) p.sorted[atomicAdd(&bins[1023 - (p.blocks[i].tiles >> shift)], 1)] = p.blocks[i];
   if (tid == 0) {
     const long long even = line / p.ctas;
     p.plan->next = 0;
@@ -240,6 +240,27 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   const uint32_t a = smem_u32(bar);
   long long t0 = 0;
   for (uint32_t it = 1; !__all_sync(0xFFFFFFFFu, try_bar(a, parity)); ++it) {
+    if ((it & 255u) != 0) continue;
+    if (t0 == 0) t0 = clock64();
+    if (__any_sync(0xFFFFFFFFu, *abort != 0 || clock64() - t0 > kWaitLimitCycles)) {
+      *abort = 2;
+      return false;
+    }
+  }
+  return true;
+}
+// Counters in shared memory that only grow: a waiter may lag behind by any number of steps.
+__device__ __forceinline__ void count_up(uint32_t* counter) {  // one thread
+  asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_u32(counter)) : "memory");
+}
+__device__ __forceinline__ bool wait_count(const uint32_t* counter, uint32_t n, volatile int* abort) {  // a whole warp
+  auto there = [&] {
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(counter)) : "memory");
+    return __all_sync(0xFFFFFFFFu, static_cast<int32_t>(v - n) >= 0);
+  };
+  long long t0 = 0;
+  for (uint32_t it = 1; !there(); ++it) {
     if ((it & 255u) != 0) continue;
     if (t0 == 0) t0 = clock64();
     if (__any_sync(0xFFFFFFFFu, *abort != 0 || clock64() - t0 > kWaitLimitCycles)) {
@@ -370,9 +391,11 @@ struct Meta {
   uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2];
   uint64_t k_full[4], v_full[4], v_ok[4];
   uint64_t slot_free[10];
-  uint64_t scanned, ended;
   int odd[3][kVal];  // first key whose value in this column is +inf, -inf, NaN
-  int any_odd;
+  uint32_t odd_item;    // the item (from 1 on) that they are of
+  uint32_t odd_lock;
+  uint32_t scanned[2];  // V tiles that each of the two warps has looked over
+  uint32_t ended;       // warps that are done with what was noted for an item
   uint32_t tmem_slot, status;
   int abort_flag;
 };
@@ -381,6 +404,12 @@ constexpr size_t kSmemBytes = Sizes<D>::kOffMeta + sizeof(Meta);
 static_assert(kSmemBytes<192> <= 232448 && kSmemBytes<128> <= 232448, "shared memory budget");
 
 // ------------------------------------------------------------------ results
+// 32 bytes, a whole sector, at once (aligned to 32)
+__device__ __forceinline__ void stg32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 struct Joined {  // how a row's sum goes into its result: out = own * f + prev_out * fp
   float f, fp, lse;
 };
@@ -419,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&M.item_full[i], 1);
-      mbar_init(&M.item_free[i], 10);
+      mbar_init(&M.item_free[i], 11);
       mbar_init(&M.q_full[i], 1);
       mbar_init(&M.q_free[i], 1);
       mbar_init(&M.s_full[i], 1);
@@ -429,12 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) {
       mbar_init(&M.k_full[i], 1);
       mbar_init(&M.v_full[i], 1);
-      mbar_init(&M.v_ok[i], 1);
+      mbar_init(&M.v_ok[i], 2);
     }
     for (int i = 0; i < Z::kSlots; ++i) mbar_init(&M.slot_free[i], 1);
-    mbar_init(&M.scanned, 1);
-    mbar_init(&M.ended, 8);
-    M.any_odd = 0;
+    M.odd_item = M.odd_lock = 0;
+    M.scanned[0] = M.scanned[1] = M.ended = 0;
     M.abort_flag = aligned ? 0 : 2;
     M.status = aligned ? 0 : kStatusSetup;
     fence_mbar_init();
@@ -457,9 +485,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   volatile int* abort_v = &M.abort_flag;
 
+  // 168 registers a thread at launch, for three warpgroups: 88 + 2 x 208 of them are used. The
+  // softmax threads hold a row's 128 logits.
   if (!aligned) {
     // nothing: the status says so
-  } else if (warp == kTmaWarp) {
+  } else if (warp < kSoftWarp0) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+   if (warp == kTmaWarp) {
     // -------------------------------------------------------------- schedule and TMA loads
     if (lane == 0) {
       const Plan plan = *p.plan;
@@ -507,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g = static_cast<int>(i / per), u0 = g * p.units_a, n = min(p.units_a, p.units - u0);
         const long long r = i - g * per;
         const int rank = static_cast<int>(r / n);
-        const Block b = p.blocks[p.order[rank]];
+        const Block b = p.sorted[rank];
         it = Item{b.tok0, b.n_tok, b.key0, b.lim0, b.n_keys, 0, b.tiles, u0 + static_cast<int>(r - static_cast<long long>(rank) * n), 1, 0, 0, 1};
         return true;
       };
@@ -520,9 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         used ^= 1u << s;
         return got;
       };
-      while (ok && more) {
-        Item it{};
-        more = next(it);
+      Item it{}, after{};  // the next item is looked up while this one's first loads are under way
+      more = next(after);
+      while (ok) {
+        it = more ? after : Item{};
         if (n >= 2 && !wait_one(&M.item_free[n & 1], ((n >> 1) - 1) & 1, abort_v)) break;
         M.items[n & 1] = it;
         mbar_arrive(&M.item_full[n & 1]);
@@ -562,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         ok = load_q(0) && load_k(it.t0) && load_q(1) && load_v(it.t0);
+        more = next(after);
         for (int t = it.t0 + 1; ok && t < it.t1; ++t) ok = load_k(t) && load_v(t);
       }
     }
@@ -670,8 +704,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       pos = kpos;
     }
     if (!ok) *abort_v = 2;
-  } else if (warp == kScanWarp) {
+  } else {
     // -------------------------------------------------------------- V rows that some row does not see
+    const int mine = warp - kScanWarp0;
     uint32_t n = 0, vg = 0;
     int pos = 0;
     bool ok = true;
@@ -681,16 +716,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&M.item_free[n & 1]);
       if (it.t1 == 0) break;
-      if (n > 0) {  // the results of the item before are out: what was noted for it goes
-        if (!wait_warp(&M.ended, (n - 1) & 1, abort_v)) break;
-        const int any = *const_cast<volatile int*>(&M.any_odd);
-        __syncwarp();
-        if (any) {
-          for (int i = lane; i < 3 * kVal; i += 32) (&M.odd[0][0])[i] = INT_MAX;
-          if (lane == 0) M.any_odd = 0;
-          __syncwarp();
-        }
-      }
       ++n;
       const int all_see = seen_by(p, it, 0);  // keys before this one are seen by every row
       for (int t = it.t0; t < it.t1; ++t) {
@@ -698,23 +723,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         pos = after_v<D>(vpos);
         if (!wait_warp(&M.v_full[vg & 3], (vg >> 2) & 1, abort_v)) { ok = false; break; }
         if ((t + 1) * kTile > all_see) {
-          bool changed = false;
-          for (int r = lane; r < kTile; r += 32) {
-            const int key = t * kTile + r;
-            if (key < all_see) continue;
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              uint8_t* row = smem + Z::kOffRing + (vpos + c) * kSlot + r * 128;
-              uint32_t hit = 0;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * j);
-                auto odd = [](uint32_t v) { return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u; };
-                hit |= static_cast<uint32_t>(odd(w.x) || odd(w.y) || odd(w.z) || odd(w.w)) << j;
-              }
-              for (; hit; hit &= hit - 1) {
-                const int j = __ffs(hit) - 1, col = 64 * c + 8 * (j ^ (r & 7));
-                uint16_t* v = reinterpret_cast<uint16_t*>(row + 16 * j);
+          // Eight lanes read the eight pieces of a row; the rows that every row sees left out.
+          const int first = (max(0, all_see - t * kTile) & ~7) + 4 * mine;
+          uint32_t hit = 0;
+#pragma unroll 4
+          for (int r = first; r < kTile; r += 8) {
+            const uint8_t* at = smem + Z::kOffRing + vpos * kSlot + (r + (lane >> 3)) * 128 + (lane & 7) * 16;
+            const uint4 w = *reinterpret_cast<const uint4*>(at), u = *reinterpret_cast<const uint4*>(at + kSlot);
+            // an exponent of all ones carries into the sign's place
+            auto odd = [](uint32_t v) { return (v & 0x7F807F80u) + 0x00800080u; };
+            const uint32_t any = odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w) | odd(u.x) | odd(u.y) | odd(u.z) | odd(u.w);
+            hit |= static_cast<uint32_t>((any & 0x80008000u) != 0) << (r >> 3);
+          }
+          if (__any_sync(0xFFFFFFFFu, hit != 0)) {
+            // The results of the items before are out: what was noted for them goes, once.
+            if (!wait_count(&M.ended, 8 * (n - 1), abort_v)) { ok = false; break; }
+            if (lane == 0)
+              for (uint32_t i = 0; atomicCAS(&M.odd_lock, 0u, 1u) != 0 && i < (1u << 24); ++i) __nanosleep(32);
+            __syncwarp();
+            if (*const_cast<volatile uint32_t*>(&M.odd_item) != n) {
+              for (int i = lane; i < 3 * kVal; i += 32) (&M.odd[0][0])[i] = INT_MAX;
+              __syncwarp();
+              if (lane == 0) *const_cast<volatile uint32_t*>(&M.odd_item) = n;
+            }
+            __threadfence_block();
+            __syncwarp();
+            if (lane == 0) atomicExch(&M.odd_lock, 0u);
+            for (; hit; hit &= hit - 1) {
+              const int r = 8 * (__ffs(hit) - 1) + 4 * mine + (lane >> 3), key = t * kTile + r;
+              if (key < all_see) continue;
+              for (int c = 0; c < 2; ++c) {
+                uint16_t* v = reinterpret_cast<uint16_t*>(smem + Z::kOffRing + (vpos + c) * kSlot + r * 128 + (lane & 7) * 16);
+                const int col = 64 * c + 8 * ((lane & 7) ^ (r & 7));
                 for (int e = 0; e < 8; ++e) {
                   const uint16_t w = v[e];
                   if ((w & 0x7F80u) != 0x7F80u) continue;
@@ -722,31 +762,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const int kind = w == 0x7F80u ? 0 : w == 0xFF80u ? 1 : 2;
                   if (key < it.n_keys) atomicMin(&M.odd[kind][col + e], key);
                 }
-                changed = true;
               }
             }
-          }
-          if (changed) {
-            M.any_odd = 1;
             fence_proxy_async_smem();
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&M.v_ok[vg & 3]);
+        if (lane == 0) {
+          mbar_arrive(&M.v_ok[vg & 3]);
+          count_up(&M.scanned[mine]);
+        }
         ++vg;
       }
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&M.scanned);
     }
-  } else if (warp >= kSoftWarp0) {
+   }
+  } else {
     // -------------------------------------------------------------- softmax, results
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int x = (warp - kSoftWarp0) >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;  // of the row tile
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_col = tmem + lanes + kColS + kTile * x, o_col = tmem + lanes + kColO + kVal * x;
     const bool negative = p.scale_log2 < 0.0f;
     const float hidden = negative ? INFINITY : -INFINITY;
-    uint32_t n = 0, g = 0, no = 0;  // items, tiles, results
+    uint32_t n = 0, g = 0, no = 0, vg = 0;  // items, tiles, results, V tiles
     bool ok = true;
     while (ok) {
       if (!wait_warp(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) break;
@@ -830,13 +870,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int head = it.unit << p.gshift;
       const long long flat = (static_cast<long long>(it.tok0) + token) * p.n_heads + head + (row & ((1 << p.gshift) - 1));
       const bool some = end > it.t0;
-      if (!wait_warp(&M.scanned, n & 1, abort_v)) break;
+      bool any_odd = false;
       if (some) {
         if (!wait_warp(&M.o_full[x], no & 1, abort_v)) break;
         ++no;
         tc_fence_after();
+        const uint32_t used = vg + static_cast<uint32_t>(end - it.t0);
+        if (!wait_count(&M.scanned[0], used, abort_v) || !wait_count(&M.scanned[1], used, abort_v)) break;
+        any_odd = *const_cast<volatile uint32_t*>(&M.odd_item) == n + 1;
       }
-      const int any_odd = *const_cast<volatile int*>(&M.any_odd);
+      vg += it.t1 - it.t0;
+      // (nothing was noted that this warp needs: no need to wait for its stores)
+      const bool done = !__any_sync(0xFFFFFFFFu, any_odd);
+      if (done && lane == 0) count_up(&M.ended);
       auto odd_value = [&](int col, float v) {  // what the row sees of values that are not finite
         const bool up = M.odd[0][col] < seen, down = M.odd[1][col] < seen, nan = M.odd[2][col] < seen;
         return nan || (up && down) ? NAN : up ? v + INFINITY : down ? v - INFINITY : v;
@@ -848,33 +894,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.lse) p.lse[flat] = j.lse;
         }
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld_32x32b_x32(o_col + 32 * c, reinterpret_cast<uint32_t*>(v));
+        for (int c = 0; c < 2; ++c) {
+          float v[64];
+#pragma unroll
+          for (int i = 0; i < 64; i += 32) tmem_ld_32x32b_x32(o_col + 64 * c + i, reinterpret_cast<uint32_t*>(v + i));
           tmem_wait_ld();
           if (exists) {
             if (any_odd) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = odd_value(32 * c + i, v[i]);
+              for (int i = 0; i < 64; ++i) v[i] = odd_value(64 * c + i, v[i]);
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = l != 0.0f ? v[i] * j.f : 0.0f;
+            for (int i = 0; i < 64; ++i) v[i] = l != 0.0f ? v[i] * j.f : 0.0f;
+            const long long at = flat * kVal + 64 * c;
             if (j.fp != 0.0f) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 was = *reinterpret_cast<const float4*>(p.prev_out + flat * kVal + 32 * c + i);
+              for (int i = 0; i < 64; i += 4) {
+                const float4 was = *reinterpret_cast<const float4*>(p.prev_out + at + i);
                 v[i] += j.fp * was.x, v[i + 1] += j.fp * was.y, v[i + 2] += j.fp * was.z, v[i + 3] += j.fp * was.w;
               }
             }
             if (p.out_fp32) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) store4(p, flat, 32 * c + i, make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+              for (int i = 0; i < 64; i += 4)
+                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             } else {
-              uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + flat * kVal + 32 * c);
+              uint16_t* o = static_cast<uint16_t*>(p.out) + at;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                o[i] = make_uint4(bf_pack(v[8 * i], v[8 * i + 1]), bf_pack(v[8 * i + 2], v[8 * i + 3]), bf_pack(v[8 * i + 4], v[8 * i + 5]),
-                                  bf_pack(v[8 * i + 6], v[8 * i + 7]));
+              for (int i = 0; i < 64; i += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] = bf_pack(v[i + 2 * k], v[i + 2 * k + 1]);
+                if (p.out_sectors) {
+                  stg32(o + i, w);
+                } else {
+                  *reinterpret_cast<uint4*>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                  *reinterpret_cast<uint4*>(o + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+              }
             }
           }
           __syncwarp();
@@ -969,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&M.ended);
+      if (!done && lane == 0) count_up(&M.ended);
       ++n;
     }
     if (!ok) *abort_v = 2;
@@ -1051,8 +1107,8 @@ size_t layout(PromptParams& p, uint8_t* ws) {
   at += up256(static_cast<size_t>(p.max_blocks) * sizeof(Block));
   p.line_at = reinterpret_cast<long long*>(ws + at);
   at += up256(static_cast<size_t>(p.max_blocks) * 8);
-  p.order = reinterpret_cast<int32_t*>(ws + at);
-  at += up256(static_cast<size_t>(p.max_blocks) * 4);
+  p.sorted = reinterpret_cast<Block*>(ws + at);
+  at += up256(static_cast<size_t>(p.max_blocks) * sizeof(Block));
   p.block_at = reinterpret_cast<int32_t*>(ws + at);
   at += up256((static_cast<size_t>(p.n_seqs) + 1) * 4);
   if (p.can_cut) {
@@ -1109,7 +1165,7 @@ int smla_prompt_fwd(const smla_heads* q, const smla_heads* k, const smla_heads* 
   // never 0: masked logits are infinities, and 0 times those is not
   const float s = sm_scale * 1.4426950408889634f;
   p.scale_log2 = s < 0.0f ? std::min(s, -1e-37f) : std::max(s, 1e-37f);
-  p.prev_out = prev_out, p.prev_lse = prev_lse, p.out = out, p.out_fp32 = out_fp32, p.lse = lse;
+  p.prev_out = prev_out, p.prev_lse = prev_lse, p.out = out, p.out_fp32 = out_fp32, p.out_sectors = aligned_to(out, 32), p.lse = lse;
   p.status = static_cast<uint32_t*>(workspace);
   // heads worked on at a time: K and V of their keys in some 40 MB of L2
   const int64_t kv_bytes = static_cast<int64_t>(total_k) * (d_k + kVal) * 2, at_once = std::max<int64_t>(1, (40LL << 20) / kv_bytes);
