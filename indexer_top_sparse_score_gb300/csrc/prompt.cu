@@ -404,11 +404,20 @@ constexpr size_t kSmemBytes = Sizes<D>::kOffMeta + sizeof(Meta);
 static_assert(kSmemBytes<192> <= 232448 && kSmemBytes<128> <= 232448, "shared memory budget");
 
 // ------------------------------------------------------------------ results
-// 32 bytes, a whole sector, at once (aligned to 32)
-__device__ __forceinline__ void stg32(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
-               "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+// 32 bytes, a whole sector, at once where they lie on a 32-byte boundary
+__device__ __forceinline__ void store8(float* p, const float* v, bool sector) {
+  if (sector) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+                 "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float* v) {  // (no .nc: it may be the output)
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 struct Joined {  // how a row's sum goes into its result: out = own * f + prev_out * fp
   float f, fp, lse;
@@ -430,13 +439,26 @@ __device__ __forceinline__ Joined join_prev(const PromptParams& p, long long fla
   }
   return j;
 }
+__device__ __forceinline__ void add_prev(const PromptParams& p, long long at, float f, float* v) {
+  float was[16];
+  load8(p.prev_out + at, was);
+  load8(p.prev_out + at + 8, was + 8);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] += f * was[i];
+}
+// What a row that sees `seen` keys gets in a column from values that are not finite: added to its
+// finite sum, +inf, -inf or NaN; 0: nothing.
+__device__ __forceinline__ float odd_of(const int (&odd)[3][kVal], int col, int seen) {
+  const bool up = odd[0][col] < seen, down = odd[1][col] < seen, nan = odd[2][col] < seen;
+  return nan || (up && down) ? NAN : up ? INFINITY : down ? -INFINITY : 0.0f;
+}
 __device__ __forceinline__ void store4(const PromptParams& p, long long flat, int col, float4 v) {
   const long long at = flat * kVal + col;
   if (p.out_fp32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;
   else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(bf_pack(v.x, v.y), bf_pack(v.z, v.w));
 }
 
-template <int D>
+template <int D, bool NEG>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap pe_map, const PromptParams p) {
@@ -784,8 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quad * 32 + lane;  // of the row tile
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_col = tmem + lanes + kColS + kTile * x, o_col = tmem + lanes + kColO + kVal * x;
-    const bool negative = p.scale_log2 < 0.0f;
-    const float hidden = negative ? INFINITY : -INFINITY;
+    const float hidden = NEG ? INFINITY : -INFINITY;  // times a negative scale: -inf
     uint32_t n = 0, g = 0, no = 0, vg = 0;  // items, tiles, results, V tiles
     bool ok = true;
     while (ok) {
@@ -797,7 +818,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int per = kTile >> p.gshift, end = end_of(p, it, x), n_tok = tokens_of(p, it, x);
       const int token = x * per + (row >> p.gshift);  // of the block
       const bool exists = (row >> p.gshift) < n_tok;
-      const int seen = seen_by(p, it, token);
+      // (rows that do not exist count like the last one that does)
+      const int seen = seen_by(p, it, min(token, it.n_tok - 1));
+      const int least_seen = __reduce_min_sync(0xFFFFFFFFu, seen);
       float m = -INFINITY, l = 0.0f;
       for (int t = it.t0; t < end; ++t, ++g) {
         if (!wait_warp(&M.s_full[x], g & 1, abort_v)) { ok = false; break; }
@@ -806,24 +829,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_col + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
         tmem_wait_ld();
-        const int left = seen - t * kTile;  // keys of the tile that the row sees
-        if (__any_sync(0xFFFFFFFFu, left < kTile)) {
+        // Keys of the tile that the row sees; chunks of 32 keys that every row of the warp sees
+        // are left as they are.
+        const int left = seen - t * kTile, least = least_seen - t * kTile;
+        if (least < kTile) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) s[i] = i < left ? s[i] : hidden;
+          for (int c = 0; c < 4; ++c)
+            if (least < 32 * c + 32) {
+#pragma unroll
+              for (int i = 32 * c; i < 32 * c + 32; ++i) s[i] = i < left ? s[i] : hidden;
+            }
         }
-        float top = hidden;
-        if (negative) {
+        float top = hidden, other = hidden;
 #pragma unroll
-          for (int i = 0; i < 128; i += 2) top = min3(top, s[i], s[i + 1]);
-        } else {
-          float other = hidden;
-#pragma unroll
-          for (int i = 0; i < 128; i += 4) {
-            top = max3(top, s[i], s[i + 1]);
-            other = max3(other, s[i + 2], s[i + 3]);
-          }
-          top = fmaxf(top, other);
+        for (int i = 0; i < 128; i += 4) {
+          top = NEG ? min3(top, s[i], s[i + 1]) : max3(top, s[i], s[i + 1]);
+          other = NEG ? min3(other, s[i + 2], s[i + 3]) : max3(other, s[i + 2], s[i + 3]);
         }
+        top = NEG ? fminf(top, other) : fmaxf(top, other);
         top *= p.scale_log2;
         const bool raise = top > m + kRaise || (m == -INFINITY && top > -INFINITY);
         float alpha = 1.0f;
@@ -883,75 +906,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (nothing was noted that this warp needs: no need to wait for its stores)
       const bool done = !__any_sync(0xFFFFFFFFu, any_odd);
       if (done && lane == 0) count_up(&M.ended);
-      auto odd_value = [&](int col, float v) {  // what the row sees of values that are not finite
-        const bool up = M.odd[0][col] < seen, down = M.odd[1][col] < seen, nan = M.odd[2][col] < seen;
-        return nan || (up && down) ? NAN : up ? v + INFINITY : down ? v - INFINITY : v;
-      };
       if (n_tok > 0 && it.whole) {
         Joined j{0.0f, 0.0f, -INFINITY};
         if (exists) {
           j = join_prev(p, flat, m, l);
           if (p.lse) p.lse[flat] = j.lse;
         }
+        // (a short loop: the tile loop's code fills the instruction cache, and what runs once an item
+        // is fetched anew. 128 columns unrolled took 5,000 cycles, most of them waiting for code.)
+        const float f = l != 0.0f ? j.f : 0.0f;
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          float v[64];
-#pragma unroll
-          for (int i = 0; i < 64; i += 32) tmem_ld_32x32b_x32(o_col + 64 * c + i, reinterpret_cast<uint32_t*>(v + i));
+        for (int c = 0; c < kVal; c += 16) {
+          float v[16];
+          tmem_ld_32x32b_x16(o_col + c, reinterpret_cast<uint32_t*>(v));
           tmem_wait_ld();
           if (exists) {
-            if (any_odd) {
-              for (int i = 0; i < 64; ++i) v[i] = odd_value(64 * c + i, v[i]);
-            }
+            const long long at = flat * kVal + c;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) v[i] = l != 0.0f ? v[i] * j.f : 0.0f;
-            const long long at = flat * kVal + 64 * c;
-            if (j.fp != 0.0f) {
-#pragma unroll
-              for (int i = 0; i < 64; i += 4) {
-                const float4 was = *reinterpret_cast<const float4*>(p.prev_out + at + i);
-                v[i] += j.fp * was.x, v[i + 1] += j.fp * was.y, v[i + 2] += j.fp * was.z, v[i + 3] += j.fp * was.w;
-              }
-            }
+            for (int i = 0; i < 16; ++i) v[i] = l != 0.0f ? v[i] * f : 0.0f;
+            if (j.fp != 0.0f) add_prev(p, at, j.fp, v);
             if (p.out_fp32) {
-#pragma unroll
-              for (int i = 0; i < 64; i += 4)
-                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              store8(static_cast<float*>(p.out) + at, v, p.out_sectors);
+              store8(static_cast<float*>(p.out) + at + 8, v + 8, p.out_sectors);
             } else {
-              uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+              uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 64; i += 16) {
-                uint32_t w[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] = bf_pack(v[i + 2 * k], v[i + 2 * k + 1]);
-                if (p.out_sectors) {
-                  stg32(o + i, w);
-                } else {
-                  *reinterpret_cast<uint4*>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                  *reinterpret_cast<uint4*>(o + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-              }
+              for (int i = 0; i < 8; ++i) w[i] = bf_pack(v[2 * i], v[2 * i + 1]);
+              store8(reinterpret_cast<float*>(static_cast<uint16_t*>(p.out) + at), reinterpret_cast<const float*>(w), p.out_sectors);
             }
           }
           __syncwarp();
         }
+        if (any_odd && exists) {
+          for (int c = 0; c < kVal; ++c) {
+            const float o = odd_of(M.odd, c, seen);
+            if (o == 0.0f) continue;
+            const long long at = flat * kVal + c;
+            if (p.out_fp32) {
+              static_cast<float*>(p.out)[at] += o;
+            } else {
+              uint16_t* to = static_cast<uint16_t*>(p.out) + at;
+              *to = static_cast<uint16_t>(bf_pack(bf_lo(*to) + o, 0.0f));
+            }
+          }
+        }
+        __syncwarp();
       } else if (quad * 32 >> p.gshift < n_tok) {  // a piece: some row of the warp exists
         const int r0 = x * kTile + quad * 32;      // the warp's first row in the block
         const long long at = static_cast<long long>(it.slot) * kBlock + r0 + lane;
+        float* part = reinterpret_cast<float*>(p.part_o + at * 32);
 #pragma unroll 1
-        for (int c = 0; c < 4 && some; ++c) {
-          float v[32];
-          tmem_ld_32x32b_x32(o_col + 32 * c, reinterpret_cast<uint32_t*>(v));
+        for (int c = 0; c < kVal && some; c += 16) {
+          float v[16];
+          tmem_ld_32x32b_x16(o_col + c, reinterpret_cast<uint32_t*>(v));
           tmem_wait_ld();
           if (exists) {
-            if (any_odd) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = odd_value(32 * c + i, v[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p.part_o[at * 32 + 8 * c + i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            store8(part + c, v, true);
+            store8(part + c + 8, v + 8, true);
           }
           __syncwarp();
+        }
+        if (any_odd && exists) {
+          for (int c = 0; c < kVal; ++c) {
+            const float o = odd_of(M.odd, c, seen);
+            if (o != 0.0f) part[c] += o;
+          }
         }
         if (exists) p.part_ml[at] = make_float2(m, some ? l : 0.0f);
         __threadfence();
@@ -1070,9 +1089,9 @@ bool encode_heads(CUtensorMap* map, const smla_heads& t, uint64_t width, uint64_
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool NEG>
 int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& pe, const PromptParams& p, cudaStream_t st) {
-  if (cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes<D>)) != cudaSuccess)
+  if (cudaFuncSetAttribute(prompt_kernel<D, NEG>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes<D>)) != cudaSuccess)
     return SMLA_ERR_CUDA;
   plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
@@ -1085,7 +1104,7 @@ int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, con
   cfg.dynamicSmemBytes = kSmemBytes<D>;
   cfg.stream = st;
   cfg.attrs = &at, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_kernel<D>, q, k, v, pe, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, prompt_kernel<D, NEG>, q, k, v, pe, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
@@ -1177,7 +1196,8 @@ int smla_prompt_fwd(const smla_heads* q, const smla_heads* k, const smla_heads* 
       !encode_heads(&v_map, *v, kVal, n_kv_heads, total_k, 1, kTile) || (k_pe && !encode_heads(&pe_map, pe, kPe, 1, total_k, 1, kTile)))
     return SMLA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d_qk == 192 ? launch<192>(q_map, k_map, v_map, pe_map, p, st) : launch<128>(q_map, k_map, v_map, pe_map, p, st);
+  const auto go = d_qk == 192 ? (p.scale_log2 < 0.0f ? launch<192, true> : launch<192, false>) : (p.scale_log2 < 0.0f ? launch<128, true> : launch<128, false>);
+  return go(q_map, k_map, v_map, pe_map, p, st);
 }
 
 }  // extern "C"
