@@ -221,13 +221,12 @@ __device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Gives up after kWaitLimitCycles, or when another role has: false, and *abort is raised
-// (the end of the kernel reports it). One thread.
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const uint32_t a = smem_u32(bar);
-  long long t0 = 0;
-  for (uint32_t it = 1; !try_bar(a, parity); ++it) {
-    if ((it & 255u) != 0) continue;
-    if (t0 == 0) t0 = clock64();
+// (the end of the kernel reports it). The loops are functions of their own: in line at every
+// wait they made the kernel too long for the instruction cache. One thread:
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const long long t0 = clock64();
+  for (uint32_t it = 1; !try_bar(bar, parity); ++it) {
+    if ((it & 63u) != 0) continue;
     if (*abort || clock64() - t0 > kWaitLimitCycles) {
       *abort = 2;
       return false;
@@ -235,8 +234,28 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatil
   }
   return true;
 }
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  return try_bar(a, parity) || wait_on(a, parity, abort);
+}
 // The same by a whole warp: every lane sees the phase, all leave together.
+__device__ __noinline__ bool wait_on_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const long long t0 = clock64();
+  for (uint32_t it = 1; !__all_sync(0xFFFFFFFFu, try_bar(bar, parity)); ++it) {
+    if ((it & 63u) != 0) continue;
+    if (__any_sync(0xFFFFFFFFu, *abort != 0 || clock64() - t0 > kWaitLimitCycles)) {
+      *abort = 2;
+      return false;
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  return __all_sync(0xFFFFFFFFu, try_bar(a, parity)) || wait_on_warp(a, parity, abort);
+}
+// The same without a call, for the softmax warps (a call would move their values to local memory).
+__device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const uint32_t a = smem_u32(bar);
   long long t0 = 0;
   for (uint32_t it = 1; !__all_sync(0xFFFFFFFFu, try_bar(a, parity)); ++it) {
@@ -403,6 +422,41 @@ template <int D>
 constexpr size_t kSmemBytes = Sizes<D>::kOffMeta + sizeof(Meta);
 static_assert(kSmemBytes<192> <= 232448 && kSmemBytes<128> <= 232448, "shared memory budget");
 
+// Values that are not finite in the rows of a V tile that `hit` names (bit i: row 8 i + 4 mine + lane / 8):
+// zeroed, and where some row of the block sees them noted.
+__device__ __noinline__ bool note_odd(Meta& M, uint8_t* tile, uint32_t hit, int mine, uint32_t n, int key0, int all_see, int n_keys,
+                                      volatile int* abort) {
+  const int lane = threadIdx.x & 31;
+  // The results of the items before are out: what was noted for them goes, once.
+  if (!wait_count(&M.ended, 8 * (n - 1), abort)) return false;
+  if (lane == 0)
+    for (uint32_t i = 0; atomicCAS(&M.odd_lock, 0u, 1u) != 0 && i < (1u << 24); ++i) __nanosleep(32);
+  __syncwarp();
+  if (*const_cast<volatile uint32_t*>(&M.odd_item) != n) {
+    for (int i = lane; i < 3 * kVal; i += 32) (&M.odd[0][0])[i] = INT_MAX;
+    __syncwarp();
+    if (lane == 0) *const_cast<volatile uint32_t*>(&M.odd_item) = n;
+  }
+  __threadfence_block();
+  __syncwarp();
+  if (lane == 0) atomicExch(&M.odd_lock, 0u);
+  for (; hit; hit &= hit - 1) {
+    const int r = 8 * (__ffs(hit) - 1) + 4 * mine + (lane >> 3), key = key0 + r;
+    if (key < all_see) continue;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      uint16_t* v = reinterpret_cast<uint16_t*>(tile + (i >> 3) * kSlot + r * 128 + (lane & 7) * 16) + (i & 7);
+      const uint16_t w = *v;
+      if ((w & 0x7F80u) != 0x7F80u) continue;
+      *v = 0;
+      const int kind = w == 0x7F80u ? 0 : w == 0xFF80u ? 1 : 2, col = 64 * (i >> 3) + 8 * ((lane & 7) ^ (r & 7)) + (i & 7);
+      if (key < n_keys) atomicMin(&M.odd[kind][col], key);
+    }
+  }
+  __syncwarp();
+  return true;
+}
+
 // ------------------------------------------------------------------ results
 // 32 bytes, a whole sector, at once where they lie on a 32-byte boundary
 __device__ __forceinline__ void store8(float* p, const float* v, bool sector) {
@@ -422,21 +476,20 @@ __device__ __forceinline__ void load8(const float* p, float* v) {  // (no .nc: i
 struct Joined {  // how a row's sum goes into its result: out = own * f + prev_out * fp
   float f, fp, lse;
 };
+__device__ __noinline__ void join_with(float was, float l, Joined& j) {
+  if (was == -INFINITY) return;
+  const float top = fmaxf(was, j.lse);
+  const float both = l != 0.0f ? top + logf(expf(was - top) + expf(j.lse - top)) : was;
+  j.f *= expf(j.lse - both);
+  j.fp = expf(was - both);
+  j.lse = both;
+}
 __device__ __forceinline__ Joined join_prev(const PromptParams& p, long long flat, float m, float l) {
   Joined j;
   j.f = l != 0.0f ? 1.0f / l : 0.0f;
   j.fp = 0.0f;
   j.lse = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-  if (p.prev_lse) {
-    const float was = p.prev_lse[flat];
-    if (was != -INFINITY) {
-      const float top = fmaxf(was, j.lse);
-      const float both = l != 0.0f ? top + logf(expf(was - top) + expf(j.lse - top)) : was;
-      j.f *= expf(j.lse - both);
-      j.fp = expf(was - both);
-      j.lse = both;
-    }
-  }
+  if (p.prev_lse) join_with(p.prev_lse[flat], l, j);
   return j;
 }
 __device__ __forceinline__ void add_prev(const PromptParams& p, long long at, float f, float* v) {
@@ -590,35 +643,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nq[x];
           mbar_arrive_expect_tx(&M.q_full[x], Z::kQTile);
           const int token = it.tok0 + x * (kTile >> p.gshift);
+#pragma unroll 1
           for (int c = 0; c < Z::kChunks; ++c)
             tma_box(smem + x * Z::kQTile + c * kSlot, &q_map, &M.q_full[x], 64 * c, it.unit << p.gshift, token);
           return true;
         };
-        auto load_k = [&](int t) {
-          uint64_t* bar = &M.k_full[kg++ & 3];
+        for (int t = it.t0; ok && t < it.t1; ++t) {
+          if (t == it.t0 && !load_q(0)) { ok = false; break; }
+          const int key = it.key0 + t * kTile;
+          uint64_t* k_bar = &M.k_full[kg++ & 3];
+#pragma unroll
           for (int c = 0; c < Z::kChunks; ++c) {
-            const int s = pos + c >= Z::kSlots ? pos + c - Z::kSlots : pos + c;
-            if (!take_slot(s)) return false;
-            if (c == 0) mbar_arrive_expect_tx(bar, Z::kChunks * kSlot);
+            ok = ok && take_slot(pos);
+            if (!ok) break;
+            if (c == 0) mbar_arrive_expect_tx(k_bar, Z::kChunks * kSlot);
             const bool shared = 64 * c >= p.d_k;
-            tma_box(smem + Z::kOffRing + s * kSlot, shared ? &pe_map : &k_map, bar, shared ? 0 : 64 * c, shared ? 0 : kv_head, it.key0 + t * kTile);
+            tma_box(smem + Z::kOffRing + pos * kSlot, shared ? &pe_map : &k_map, k_bar, shared ? 0 : 64 * c, shared ? 0 : kv_head, key);
+            if (++pos == Z::kSlots) pos = 0;
           }
-          pos = after_k<D>(pos);
-          return true;
-        };
-        auto load_v = [&](int t) {
-          uint64_t* bar = &M.v_full[vg++ & 3];
+          ok = ok && (t != it.t0 || load_q(1));
+          uint64_t* v_bar = &M.v_full[vg++ & 3];
+          if (pos == Z::kSlots - 1) pos = 0;
+#pragma unroll
           for (int c = 0; c < 2; ++c) {
-            if (!take_slot(pos + c)) return false;
-            if (c == 0) mbar_arrive_expect_tx(bar, 2 * kSlot);
-            tma_box(smem + Z::kOffRing + (pos + c) * kSlot, &v_map, bar, 64 * c, kv_head, it.key0 + t * kTile);
+            ok = ok && take_slot(pos);
+            if (!ok) break;
+            if (c == 0) mbar_arrive_expect_tx(v_bar, 2 * kSlot);
+            tma_box(smem + Z::kOffRing + pos * kSlot, &v_map, v_bar, 64 * c, kv_head, key);
+            if (++pos == Z::kSlots) pos = 0;
           }
-          pos = after_v<D>(pos);
-          return true;
-        };
-        ok = load_q(0) && load_k(it.t0) && load_q(1) && load_v(it.t0);
-        more = next(after);
-        for (int t = it.t0 + 1; ok && t < it.t1; ++t) ok = load_k(t) && load_v(t);
+          if (t == it.t0) more = next(after);
+        }
       }
     }
   } else if (warp == kMmaWarp) {
@@ -636,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t nq[2] = {0, 0}, ns[2] = {0, 0};  // row tiles begun, P tiles used
     int pos = 0;
     bool ok = true;
-    auto qk = [&](int x, int kpos) {
+    auto qk = [&](int x, int kpos, bool last) {
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -648,25 +703,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ss(tm + kColS + kTile * x, q_desc + (x * Z::kQTile + c * kSlot + 32 * kk), k + 32 * kk, id_qk, c != 0 || kk != 0);
         }
         mma_commit(&M.s_full[x]);
+        if (last) mma_commit(&M.q_free[x]);
       }
       __syncwarp();
     };
-    auto pv = [&](int x, int vpos, bool first) {
+    auto pv = [&](int x, int vpos, bool first, bool last) {
       tc_fence_after();
       if (elect_one()) {
         const Operand v = v_desc + vpos * kSlot;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(tm + kColO + kVal * x, tm + kColS + kTile * x + 8 * kk, v + 2048 * kk, id_pv, kk != 0 || !first);
+        if (last) mma_commit(&M.o_full[x]);
       }
       __syncwarp();
     };
-    auto commit = [&](uint64_t* bar) {
-      if (elect_one()) mma_commit(bar);
+    // slots whose products are all issued: V's two (vpos >= 0), K's
+    auto free_slots = [&](int vpos, int kpos, bool k) {
+      if (elect_one()) {
+        if (vpos >= 0) {
+          mma_commit(&M.slot_free[vpos]);
+          mma_commit(&M.slot_free[vpos + 1]);
+        }
+        if (k)
+#pragma unroll
+          for (int c = 0; c < Z::kChunks; ++c) mma_commit(&M.slot_free[kpos + c >= Z::kSlots ? kpos + c - Z::kSlots : kpos + c]);
+      }
       __syncwarp();
-    };
-    auto free_k = [&](int kpos) {
-      for (int c = 0; c < Z::kChunks; ++c) commit(&M.slot_free[kpos + c >= Z::kSlots ? kpos + c - Z::kSlots : kpos + c]);
     };
     while (ok) {
       if (!wait_warp(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) { ok = false; break; }
@@ -677,23 +740,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.t1 == 0) break;
       const int t0 = __shfl_sync(0xFFFFFFFFu, it.t0, 0), t1 = __shfl_sync(0xFFFFFFFFu, it.t1, 0);
       const int end[2] = {__shfl_sync(0xFFFFFFFFu, end_of(p, it, 0), 0), __shfl_sync(0xFFFFFFFFu, end_of(p, it, 1), 0)};
+      int kpos = pos;
       ok = wait_warp(&M.k_full[kg & 3], (kg >> 2) & 1, abort_v);
       ++kg;
-      int kpos = pos;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (!ok || end[x] <= t0) continue;
         ok = wait_warp(&M.q_full[x], nq[x] & 1, abort_v);
-        if (!ok) break;
         ++nq[x];
-        qk(x, kpos);
-        if (t0 + 1 == end[x]) commit(&M.q_free[x]);
+        if (ok) qk(x, kpos, t0 + 1 == end[x]);
       }
       if (!ok) break;
-      free_k(kpos);
-      for (int t = t0; ok && t < t1; ++t) {
+      free_slots(-1, kpos, true);
+#pragma unroll 1
+      for (int t = t0; t < t1; ++t) {
         const int vpos = after_k<D>(kpos);
-        const bool next = t + 1 < t1;
         kpos = after_v<D>(vpos);
         bool have_k = false;
         ok = wait_warp(&M.v_ok[vg & 3], (vg >> 2) & 1, abort_v);
@@ -702,26 +763,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 2; ++x) {
           if (!ok || t >= end[x]) continue;
           ok = wait_warp(&M.p_full[x], ns[x] & 1, abort_v);
-          if (!ok) break;
           ++ns[x];
-          pv(x, vpos, t == t0);
-          if (t + 1 == end[x]) {
-            commit(&M.o_full[x]);
-            continue;
-          }
+          if (!ok) continue;
+          const bool last = t + 1 == end[x];
+          pv(x, vpos, t == t0, last);
+          if (last) continue;
           if (!have_k) {
             ok = wait_warp(&M.k_full[kg & 3], (kg >> 2) & 1, abort_v);
             ++kg;
             have_k = true;
-            if (!ok) break;
           }
-          qk(x, kpos);
-          if (t + 2 == end[x]) commit(&M.q_free[x]);
+          if (ok) qk(x, kpos, t + 2 == end[x]);
         }
         if (!ok) break;
-        commit(&M.slot_free[vpos]);
-        commit(&M.slot_free[vpos + 1]);
-        if (next) free_k(kpos);
+        free_slots(vpos, kpos, t + 1 < t1);
       }
       pos = kpos;
     }
@@ -758,34 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             hit |= static_cast<uint32_t>((any & 0x80008000u) != 0) << (r >> 3);
           }
           if (__any_sync(0xFFFFFFFFu, hit != 0)) {
-            // The results of the items before are out: what was noted for them goes, once.
-            if (!wait_count(&M.ended, 8 * (n - 1), abort_v)) { ok = false; break; }
-            if (lane == 0)
-              for (uint32_t i = 0; atomicCAS(&M.odd_lock, 0u, 1u) != 0 && i < (1u << 24); ++i) __nanosleep(32);
-            __syncwarp();
-            if (*const_cast<volatile uint32_t*>(&M.odd_item) != n) {
-              for (int i = lane; i < 3 * kVal; i += 32) (&M.odd[0][0])[i] = INT_MAX;
-              __syncwarp();
-              if (lane == 0) *const_cast<volatile uint32_t*>(&M.odd_item) = n;
-            }
-            __threadfence_block();
-            __syncwarp();
-            if (lane == 0) atomicExch(&M.odd_lock, 0u);
-            for (; hit; hit &= hit - 1) {
-              const int r = 8 * (__ffs(hit) - 1) + 4 * mine + (lane >> 3), key = t * kTile + r;
-              if (key < all_see) continue;
-              for (int c = 0; c < 2; ++c) {
-                uint16_t* v = reinterpret_cast<uint16_t*>(smem + Z::kOffRing + (vpos + c) * kSlot + r * 128 + (lane & 7) * 16);
-                const int col = 64 * c + 8 * ((lane & 7) ^ (r & 7));
-                for (int e = 0; e < 8; ++e) {
-                  const uint16_t w = v[e];
-                  if ((w & 0x7F80u) != 0x7F80u) continue;
-                  v[e] = 0;
-                  const int kind = w == 0x7F80u ? 0 : w == 0xFF80u ? 1 : 2;
-                  if (key < it.n_keys) atomicMin(&M.odd[kind][col + e], key);
-                }
-              }
-            }
+            if (!note_odd(M, smem + Z::kOffRing + vpos * kSlot, hit, mine, n, t * kTile, all_see, it.n_keys, abort_v)) { ok = false; break; }
             fence_proxy_async_smem();
           }
         }
@@ -810,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n = 0, g = 0, no = 0, vg = 0;  // items, tiles, results, V tiles
     bool ok = true;
     while (ok) {
-      if (!wait_warp(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) break;
+      if (!wait_here(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) break;
       const Item it = M.items[n & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&M.item_free[n & 1]);
@@ -823,23 +851,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int least_seen = __reduce_min_sync(0xFFFFFFFFu, seen);
       float m = -INFINITY, l = 0.0f;
       for (int t = it.t0; t < end; ++t, ++g) {
-        if (!wait_warp(&M.s_full[x], g & 1, abort_v)) { ok = false; break; }
+        if (!wait_here(&M.s_full[x], g & 1, abort_v)) { ok = false; break; }
         tc_fence_after();
+        // Keys that the row does not see: their logits are replaced where they lie, 32 keys at a time (a
+        // short loop: it runs once or twice an item, and unrolled over the tile it would
+        // push the tile's own code out of the instruction cache).
+        const int left = seen - t * kTile, least = least_seen - t * kTile;
+        if (least < kTile) {
+#pragma unroll 1
+          for (int c = max(0, least) & ~31; c < kTile; c += 32) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(s_col + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = c + i < left ? v[i] : __float_as_uint(hidden);
+            tmem_st_32x32b_x32(s_col + c, v);
+          }
+          tmem_wait_st();
+        }
         float s[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_col + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
         tmem_wait_ld();
-        // Keys of the tile that the row sees; chunks of 32 keys that every row of the warp sees
-        // are left as they are.
-        const int left = seen - t * kTile, least = least_seen - t * kTile;
-        if (least < kTile) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (least < 32 * c + 32) {
-#pragma unroll
-              for (int i = 32 * c; i < 32 * c + 32; ++i) s[i] = i < left ? s[i] : hidden;
-            }
-        }
         float top = hidden, other = hidden;
 #pragma unroll
         for (int i = 0; i < 128; i += 4) {
@@ -895,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool some = end > it.t0;
       bool any_odd = false;
       if (some) {
-        if (!wait_warp(&M.o_full[x], no & 1, abort_v)) break;
+        if (!wait_here(&M.o_full[x], no & 1, abort_v)) break;
         ++no;
         tc_fence_after();
         const uint32_t used = vg + static_cast<uint32_t>(end - it.t0);
@@ -916,23 +949,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         // is fetched anew. 128 columns unrolled took 5,000 cycles, most of them waiting for code.)
         const float f = l != 0.0f ? j.f : 0.0f;
 #pragma unroll 1
-        for (int c = 0; c < kVal; c += 16) {
-          float v[16];
-          tmem_ld_32x32b_x16(o_col + c, reinterpret_cast<uint32_t*>(v));
+        for (int c = 0; c < kVal; c += 32) {
+          float v[32];
+          tmem_ld_32x32b_x32(o_col + c, reinterpret_cast<uint32_t*>(v));
           tmem_wait_ld();
           if (exists) {
             const long long at = flat * kVal + c;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = l != 0.0f ? v[i] * f : 0.0f;
-            if (j.fp != 0.0f) add_prev(p, at, j.fp, v);
+            for (int i = 0; i < 32; ++i) v[i] = l != 0.0f ? v[i] * f : 0.0f;
+            if (j.fp != 0.0f) {
+              add_prev(p, at, j.fp, v);
+              add_prev(p, at + 16, j.fp, v + 16);
+            }
             if (p.out_fp32) {
-              store8(static_cast<float*>(p.out) + at, v, p.out_sectors);
-              store8(static_cast<float*>(p.out) + at + 8, v + 8, p.out_sectors);
-            } else {
-              uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = bf_pack(v[2 * i], v[2 * i + 1]);
-              store8(reinterpret_cast<float*>(static_cast<uint16_t*>(p.out) + at), reinterpret_cast<const float*>(w), p.out_sectors);
+              for (int i = 0; i < 32; i += 8) store8(static_cast<float*>(p.out) + at + i, v + i, p.out_sectors);
+            } else {
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = bf_pack(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+              for (int i = 0; i < 16; i += 8)
+                store8(reinterpret_cast<float*>(static_cast<uint16_t*>(p.out) + at + 2 * i), reinterpret_cast<const float*>(w + i), p.out_sectors);
             }
           }
           __syncwarp();
