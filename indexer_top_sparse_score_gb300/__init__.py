@@ -606,16 +606,14 @@ def shared_prefix_fwd(cache, page_tables, seq_lens, max_seq_len, shared_len, q_p
 # ---------------------------------------------------------------------------- expanded prompts
 def _here(*tensors):
     """The kernels run on the current device's stream: every tensor has to be there."""
-    now = None
+    now = -2
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors are on the GPU")
-        if now is None:
-            now = torch.cuda.current_device()
-        if t.get_device() != now:
-            raise ValueError("tensors are on the current CUDA device (torch.cuda.device sets it)")
+        if t is not None:
+            at = t.get_device()  # -1: not on a GPU
+            if at != now:
+                if at < 0 or now >= 0 or at != torch.cuda.current_device():
+                    raise ValueError("tensors are on the current CUDA device (torch.cuda.device sets it)")
+                now = at
 
 
 def rope_table(n, dim=64, *, first=0, base=10000.0, factor=1.0, original=0, beta_fast=32.0, beta_slow=1.0,

@@ -32,6 +32,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <mutex>
 
 #include "../../include/smla_prompt.h"
 #include "rows.cuh"
@@ -1129,8 +1130,6 @@ bool encode_heads(CUtensorMap* map, const smla_heads& t, uint64_t width, uint64_
 
 template <int D, bool NEG>
 int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& pe, const PromptParams& p, cudaStream_t st) {
-  if (cudaFuncSetAttribute(prompt_kernel<D, NEG>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes<D>)) != cudaSuccess)
-    return SMLA_ERR_CUDA;
   plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
   cudaLaunchAttribute at{};  // set up while the plan is made
@@ -1145,6 +1144,22 @@ int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, con
   return cudaLaunchKernelEx(&cfg, prompt_kernel<D, NEG>, q, k, v, pe, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
+template <int D, bool NEG>
+bool set_smem() {
+  return cudaFuncSetAttribute(prompt_kernel<D, NEG>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes<D>)) == cudaSuccess;
+}
+// CTAs of the current device, one per SM; looked up once per device, with the kernels' shared
+// memory limit set. 0: no device.
+int ctas_of_device() {
+  static std::mutex mutex;
+  static int known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (known[dev] == 0 && set_smem<192, false>() && set_smem<192, true>() && set_smem<128, false>() && set_smem<128, true>()) known[dev] = num_sms();
+  return known[dev];
+}
+
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Sizes that follow from the shape, and the workspace's parts; its bytes.
@@ -1153,7 +1168,7 @@ size_t layout(PromptParams& p, uint8_t* ws) {
   while (p.gshift < 7 && p.group % (2 << p.gshift) == 0) ++p.gshift;
   p.units = p.n_heads >> p.gshift;
   p.max_blocks = p.total_q / (kBlock >> p.gshift) + p.n_seqs;
-  p.ctas = num_sms();
+  p.ctas = std::max(1, ctas_of_device());
   p.can_cut = p.total_k > kLongTiles * kTile;
   size_t at = kStatusBytes;
   p.plan = reinterpret_cast<Plan*>(ws + at);

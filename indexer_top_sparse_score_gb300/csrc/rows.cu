@@ -24,39 +24,47 @@ struct TableParams {
   uint64_t turns[kMaxDim / 2];  // of each pair per position, in 2^-64 turns
 };
 
-// cos and sin of s / 2^64 turns. The angle goes to the float nearest to its upper half,
-// exactly reduced by sincospif, and what that leaves out (under 2^-24 of a turn) is
-// added to first order: c - s d, s + c d.
+// cos and sin of angle / 2^64 turns. The nearest quarter of a turn is taken off, exactly; what is left, at most
+// an eighth, goes to the nearest float (2^-24 of it) and into the Taylor series of sin and cos
+// up to x^9 and x^10, which are off by 2^-29 there: within 2^-23 altogether.
 __device__ __forceinline__ void cos_sin_of(uint64_t angle, float& c, float& s) {
-  const int32_t hi = static_cast<int32_t>(angle >> 32);
-  const float x = static_cast<float>(hi);
-  const float rest = static_cast<float>(hi - __float2int_rn(x)) + static_cast<float>(static_cast<uint32_t>(angle)) * 0x1p-32f;
-  float s0, c0;
-  sincospif(x * 0x1p-31f, &s0, &c0);
-  const float d = rest * (0x1p-31f * 3.14159265358979f);
-  c = fmaf(-s0, d, c0);
-  s = fmaf(c0, d, s0);
+  const uint64_t up = angle + (1ull << 61);
+  const int32_t rest = static_cast<int32_t>(static_cast<uint32_t>((up << 2) >> 32) ^ 0x80000000u);  // - 1/8 .. 1/8 turn in 2^-34 turns
+  const float x = static_cast<float>(rest) * (0x1p-34f * 6.28318530717958648f), t = x * x;
+  const float sn = x * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), 1.0f);
+  const float cs = fmaf(t, fmaf(t, fmaf(t, fmaf(t, fmaf(t, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+  const uint32_t quarter = static_cast<uint32_t>(up >> 62);
+  const float a = quarter & 1 ? sn : cs, b = quarter & 1 ? cs : sn;
+  c = __uint_as_float(__float_as_uint(a) ^ ((quarter + 1 & 2) << 30));  // quarters 1 and 2
+  s = __uint_as_float(__float_as_uint(b) ^ ((quarter & 2) << 30));      // quarters 2 and 3
 }
 
 // A thread keeps four pairs and walks the rows: position * turns wraps at whole
-// turns by itself in 64-bit integers, so the angle needs no reduction.
+// turns by itself in 64-bit integers, so the angle needs no reduction and goes on by additions.
 __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_constant__ TableParams p) {
   const int groups = p.dim / 8, half = p.dim / 2;  // groups of four pairs
   const int g = threadIdx.x % groups, r0 = threadIdx.x / groups, per = kTableThreads / groups;
   if (r0 >= per) return;
-  uint64_t w[4];
+  const long long step = static_cast<long long>(gridDim.x) * per;
+  long long r = static_cast<long long>(blockIdx.x) * per + r0;
+  uint64_t w[4], at[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = p.turns[4 * g + i];
-  for (long long r = static_cast<long long>(blockIdx.x) * per + r0; r < p.n; r += static_cast<long long>(gridDim.x) * per) {
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t turns = p.turns[4 * g + i];
+    at[i] = (p.first + static_cast<uint64_t>(r)) * turns;
+    w[i] = static_cast<uint64_t>(step) * turns;
+  }
+  float* o = p.out + r * p.dim + 4 * g;
+#pragma unroll 2
+  for (; r < p.n; r += step, o += step * p.dim) {
     float c[4], s[4];
-    const uint64_t pos = p.first + static_cast<uint64_t>(r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      cos_sin_of(pos * w[i], c[i], s[i]);
+      cos_sin_of(at[i], c[i], s[i]);
+      at[i] += w[i];
       c[i] *= p.magnitude;
       s[i] *= p.magnitude;
     }
-    float* o = p.out + r * p.dim + 4 * g;
     *reinterpret_cast<float4*>(o) = make_float4(c[0], c[1], c[2], c[3]);
     *reinterpret_cast<float4*>(o + half) = make_float4(s[0], s[1], s[2], s[3]);
   }
@@ -173,8 +181,38 @@ __device__ __forceinline__ uint4 widen8(uint2 c, float s) {
 }
 
 // A block finds the pool rows of 32 output rows: every request's first row is loaded once
-// and counted against them (one latency, no search), then the rows' pieces
-// of 16 output bytes go round the block's threads.
+// and counted against them (one latency, no search), then the rows' pieces of 16 bytes of the pool
+// go round the block's threads, each thread's requested together.
+// Programmatic launch after clear_kernel: only who reports waits for it.
+__global__ void clear_kernel(uint32_t* status) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  *status = 0;
+}
+__device__ __forceinline__ void report(uint32_t* status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  set_status(status, kStatusBounds);
+}
+
+// `pieces` pieces a row of the block's rows: load(place, piece) -> T, store(row, piece, T)
+template <int BATCH, typename T, typename Load, typename Store>
+__device__ __forceinline__ void each_piece(int pieces, const long long* place, Load load, Store store) {
+  const int total = kReadRows * pieces;
+  for (int u0 = threadIdx.x; u0 < total; u0 += BATCH * kReadThreads) {
+    T v[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int u = u0 + i * kReadThreads, r = u / pieces;
+      if (u < total && place[r] >= 0) v[i] = load(place[r], u - r * pieces);
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int u = u0 + i * kReadThreads, r = u / pieces;
+      if (u < total && place[r] != -2) store(r, u - r * pieces, v[i], place[r] >= 0);
+    }
+  }
+}
+
+template <int FMT>
 __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadParams p) {
   __shared__ int begun[kReadRows + 1];      // requests that begin at or before the block's first row, then at each row
   __shared__ long long place[kReadRows];    // pool row; -1: zeros; -2: left as it is
@@ -217,7 +255,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
       }
     }
     place[tid] = at;
-    if (bad) set_status(p.status, kStatusBounds);
+    if (bad) report(p.status);
   }
   if (blockIdx.x == 0) {  // what no row shows: the list's order and its end
     bool bad = false;
@@ -225,54 +263,84 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
       const int c = __ldg(p.cu + i);
       bad |= c < 0 || c > p.rows || (i > 0 && c < __ldg(p.cu + i - 1));
     }
-    if (bad) set_status(p.status, kStatusBounds);
+    if (bad) report(p.status);
   }
   __syncthreads();
   const uint4 none = make_uint4(0, 0, 0, 0);
-  // pieces of eight values of a row: 64 latent ones, 8 of the rope part, then the indexer key's
-  const int key_pieces = p.keys ? p.d_idx / 8 : 0, pieces = 72 + key_pieces;
-#pragma unroll 4
-  for (int u = tid; u < kReadRows * pieces; u += kReadThreads) {
-    const int r = u / pieces, j = u - r * pieces;
-    const long long at = place[r];
-    if (at == -2) continue;
-    uint4 v = none;
-    if (j < 72) {
-      if (!(j < 64 ? p.latent : p.pe)) continue;
-      if (at >= 0) {
-        if (p.kv_dtype == SMLA_BF16) {
-          v = __ldg(reinterpret_cast<const uint4*>(p.kv + at * (2 * kDqk)) + j);
-        } else if (p.kv_dtype == SMLA_FP8_E4M3) {
-          v = widen8(__ldg(reinterpret_cast<const uint2*>(p.kv + at * kDqk) + j), __ldg(p.kv_scale + at));
-        } else if (j < 64) {
-          const uint8_t* row = p.kv + at * kTileRow;
-          v = widen8(__ldg(reinterpret_cast<const uint2*>(row) + j), __ldg(reinterpret_cast<const float*>(row + kDv) + (j >> 4)));
-        } else {
-          v = __ldg(reinterpret_cast<const uint4*>(p.kv + at * kTileRow + kTileRopeAt) + (j - 64));
-        }
-      }
-      uint16_t* o = j < 64 ? p.latent + (r0 + r) * p.latent_stride + 8 * j : p.pe + (r0 + r) * p.pe_stride + 8 * (j - 64);
-      *reinterpret_cast<uint4*>(o) = v;
-    } else {
-      const int k = j - 72;
-      if (at >= 0) {
-        const uint8_t* row = p.k_idx + at * kIdxRowBytes;
-        const float s = p.k_idx_scale ? __ldg(p.k_idx_scale + at) : 1.0f;
-        if (p.idx_fp8) {
-          v = widen8(__ldg(reinterpret_cast<const uint2*>(row) + k), s);
-        } else {
-          v = __ldg(reinterpret_cast<const uint4*>(row) + k);
-          if (p.k_idx_scale) {
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = bf_pack(bf_lo(w[i]) * s, bf_hi(w[i]) * s);
-            v = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
-      *reinterpret_cast<uint4*>(p.keys + (r0 + r) * p.keys_stride + 8 * k) = v;
-    }
+  auto to_latent = [&](int r, int j, uint4 v) { *reinterpret_cast<uint4*>(p.latent + (r0 + r) * p.latent_stride + 8 * j) = v; };
+  auto to_pe = [&](int r, int j, uint4 v) { *reinterpret_cast<uint4*>(p.pe + (r0 + r) * p.pe_stride + 8 * j) = v; };
+  if (FMT == SMLA_BF16) {
+    const int first = p.latent ? 0 : 64, pieces = (p.pe ? 72 : 64) - first;  // of those that are wanted
+    if (pieces > 0)
+      each_piece<5, uint4>(pieces, place, [&](long long at, int j) { return __ldg(reinterpret_cast<const uint4*>(p.kv + at * (2 * kDqk)) + first + j); },
+                           [&](int r, int j, uint4 v, bool there) {
+                             j += first;
+                             if (j < 64) to_latent(r, j, there ? v : none);
+                             else to_pe(r, j - 64, there ? v : none);
+                           });
+  } else if (FMT == SMLA_FP8_E4M3) {
+    const int first = p.latent ? 0 : 32, pieces = (p.pe ? 36 : 32) - first;  // sixteen codes each
+    struct Got {
+      uint4 c;
+      float s;
+    };
+    if (pieces > 0)
+      each_piece<5, Got>(pieces, place,
+                         [&](long long at, int j) {
+                           return Got{__ldg(reinterpret_cast<const uint4*>(p.kv + at * kDqk) + first + j), __ldg(p.kv_scale + at)};
+                         },
+                         [&](int r, int j, Got v, bool there) {
+                           j += first;
+                           const uint4 a = there ? widen8(make_uint2(v.c.x, v.c.y), v.s) : none, b = there ? widen8(make_uint2(v.c.z, v.c.w), v.s) : none;
+                           if (j < 32) to_latent(r, 2 * j, a), to_latent(r, 2 * j + 1, b);
+                           else to_pe(r, 2 * (j - 32), a), to_pe(r, 2 * (j - 32) + 1, b);
+                         });
+  } else if (FMT == SMLA_FP8_DS_MLA) {
+    struct Got {
+      uint4 c;
+      float s;
+    };
+    const int first = p.latent ? 0 : 32, pieces = (p.pe ? 40 : 32) - first;  // sixteen codes or eight rope values each
+    if (pieces > 0)
+      each_piece<5, Got>(pieces, place,
+                         [&](long long at, int j) {
+                           const uint8_t* row = p.kv + at * kTileRow;
+                           j += first;
+                           return Got{__ldg(reinterpret_cast<const uint4*>(row + (j < 32 ? 0 : 16)) + j),
+                                      j < 32 ? __ldg(reinterpret_cast<const float*>(row + kDv) + (j >> 3)) : 1.0f};
+                         },
+                         [&](int r, int j, Got v, bool there) {
+                           j += first;
+                           if (j < 32) {
+                             to_latent(r, 2 * j, there ? widen8(make_uint2(v.c.x, v.c.y), v.s) : none);
+                             to_latent(r, 2 * j + 1, there ? widen8(make_uint2(v.c.z, v.c.w), v.s) : none);
+                           } else {
+                             to_pe(r, j - 32, there ? v.c : none);
+                           }
+                         });
   }
+  if (!p.keys) return;
+  auto to_keys = [&](int r, int j, uint4 v) { *reinterpret_cast<uint4*>(p.keys + (r0 + r) * p.keys_stride + 8 * j) = v; };
+  struct Got {
+    uint4 c;
+    float s;
+  };
+  each_piece<2, Got>(8, place,
+                     [&](long long at, int j) {
+                       return Got{__ldg(reinterpret_cast<const uint4*>(p.k_idx + at * kIdxRowBytes) + j), p.k_idx_scale ? __ldg(p.k_idx_scale + at) : 1.0f};
+                     },
+                     [&](int r, int j, Got v, bool there) {
+                       if (p.idx_fp8) {
+                         to_keys(r, 2 * j, there ? widen8(make_uint2(v.c.x, v.c.y), v.s) : none);
+                         to_keys(r, 2 * j + 1, there ? widen8(make_uint2(v.c.z, v.c.w), v.s) : none);
+                         return;
+                       }
+                       uint32_t w[4] = {v.c.x, v.c.y, v.c.z, v.c.w};
+                       if (p.k_idx_scale)
+#pragma unroll
+                         for (int i = 0; i < 4; ++i) w[i] = bf_pack(bf_lo(w[i]) * v.s, bf_hi(w[i]) * v.s);
+                       to_keys(r, j, there ? make_uint4(w[0], w[1], w[2], w[3]) : none);
+                     });
 }
 
 bool strided(const void* p, int64_t stride, int64_t width) { return aligned_to(p, 16) && stride % 8 == 0 && stride >= width; }
@@ -371,9 +439,19 @@ int smla_cache_read(const smla_paged_cache* cache, const int32_t* page_tables, i
   p.pe = static_cast<uint16_t*>(pe), p.pe_stride = pe_stride;
   p.keys = static_cast<uint16_t*>(keys), p.keys_stride = keys_stride;
   p.status = static_cast<uint32_t*>(workspace);
-  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SMLA_ERR_CUDA;
-  cache_read_kernel<<<static_cast<unsigned>((rows + kReadRows - 1) / kReadRows), kReadThreads, 0, st>>>(p);
-  return launched();
+  clear_kernel<<<1, 1, 0, st>>>(p.status);
+  if (launched()) return SMLA_ERR_CUDA;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kReadRows - 1) / kReadRows));
+  cfg.blockDim = dim3(kReadThreads);
+  cfg.stream = st;
+  cfg.attrs = &at, cfg.numAttrs = 1;
+  const int fmt = latent || pe ? cache->kv_dtype : SMLA_BF16;  // (keys alone: no latent pieces)
+  const auto kernel = fmt == SMLA_BF16 ? cache_read_kernel<SMLA_BF16> : fmt == SMLA_FP8_E4M3 ? cache_read_kernel<SMLA_FP8_E4M3> : cache_read_kernel<SMLA_FP8_DS_MLA>;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
 }  // extern "C"
