@@ -4,19 +4,25 @@
 //
 // Rows are (token, query head of one key head) pairs: G heads that share a key head (the
 // largest power of two that divides their number, at most 128) lie side by side, so that
-// few tokens of many grouped heads still fill a tile. A block is 256 rows of one request
-// and head group, two tiles of 128 rows; K and V come in tiles of 128 keys that both
-// row tiles use. While the softmax of one row tile runs, the tensor cores work for the
-// other:  PV0(t) QK0(t+1) | PV1(t) QK1(t+1) | PV0(t+1) ...
+// few tokens of many grouped heads still fill a tile. A block is 512 rows of one request
+// and head group, worked on by a pair of CTAs in two row tiles of 256 rows, 128 in each CTA.
+// K and V come in tiles of 128 keys that both row tiles use. While the softmax of one row
+// tile runs, the tensor cores work for the other:  PV0(t) QK0(t+1) | PV1(t) QK1(t+1) | PV0(t+1) ...
+//
+// Why a pair. A 128 x 128 x 16 product of one CTA reads 8 KB of shared memory in the 64 cycles that it
+// takes, all that shared memory gives, and the loads of K and V come on top (80 KB a tile pair, 640 cycles of
+// 2,560: QK and PV measured 3,000-3,200 together). With cta_group::2 each CTA holds half of the keys of
+// K and half of the values of V: 6 KB a product and half of the loads.
 //
 // Tensor memory (512 columns): S0 | S1 | O0 | O1, 128 fp32 columns each; P takes the
 // place of its logits as bf16 (64 columns), as MMA operand A. Products of one tile are
 // issued in order, so S(t+1) overwrites P(t) only after PV(t) has read it, and when S(t+1) is
 // complete O holds everything up to t.
-// Shared memory: Q of both tiles, and a ring of 16 KB slots (128 keys x 64 values, 128-byte
-// swizzled) that K and V tiles go through in turn.
-// Warps: 0 TMA loads and the schedule, 1 MMA issue, 2-3 look V over (below), 4-7 and 8-11
-// softmax and results of the two row tiles, a thread a row.
+// Shared memory: Q of both tiles, and a ring of 8 KB slots (64 keys x 64 values of K; two slots for
+// 128 keys x 64 values of V; 128-byte swizzled) that K and V tiles go through in turn.
+// Warps of each CTA: 0 TMA loads (CTA 0: and the schedule), 1 MMA issue (CTA 1: tells CTA 0 what has
+// arrived), 2-3 look V over (below), 4-7 and 8-11 softmax and results of the two row tiles, a
+// thread a row.
 //
 // 0 * NaN. V rows that a row does not see meet its zero probabilities. Tiles that
 // some row of the block sees only in part are looked over before they are used: values
@@ -24,11 +30,11 @@
 // NaN is noted for each of the 128 columns; rows that see it get it added to their result.
 //
 // The plan. A small kernel turns the requests' bounds into a list of blocks. Where blocks
-// are many, CTAs take them one by one, longest first, a few key heads at a time (so that
+// are many, pairs take them one by one, longest first, a few key heads at a time (so that
 // their K and V stay in L2). Where the longest would end late (few rows, many keys), all
-// tiles lie on one line that is cut into equal stretches, one per CTA; blocks that are cut
+// tiles lie on one line that is cut into equal stretches, one per pair; blocks that are cut
 // leave fp32 partial results, and the warp that ends a row group's last piece joins them, in
-// the order of the pieces. No CTA waits for another.
+// the order of the pieces. No pair waits for another.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -42,9 +48,11 @@ namespace {
 
 constexpr int kVal = 128;   // values of a head's v
 constexpr int kPe = 64;
-constexpr int kTile = 128;  // rows of a row tile, keys of a key tile
-constexpr int kBlock = 2 * kTile;
-constexpr int kSlot = kTile * 128;
+constexpr int kTile = 128;  // rows of a row tile in each CTA, keys of a key tile
+constexpr int kBlock = 4 * kTile;
+constexpr int kQChunk = kTile * 128;  // bytes of 128 rows x 64 values
+constexpr int kSlot = 64 * 128;       // of 64 keys x 64 values
+constexpr int kAhead = 8;             // tiles of the ring at most, and barriers for them
 constexpr int kThreads = 384;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kScanWarp0 = 2, kSoftWarp0 = 4;
 constexpr float kRaise = 8.0f;  // log2: the reference maximum is raised only when exceeded by this much
@@ -62,7 +70,7 @@ struct Plan {
   unsigned long long next;  // item to be taken
   long long line;           // length of the line of work
   int32_t n_blocks, even;   // even: the line is cut evenly
-  int32_t ctas;             // stretches of the line
+  int32_t pairs;            // stretches of the line
 };
 
 struct PromptParams {
@@ -73,7 +81,7 @@ struct PromptParams {
   int32_t units;      // head groups: n_heads >> gshift
   int32_t units_a;    // of those that are worked on at a time
   int32_t d_k;        // values of k (the others of a key are k_pe's)
-  int32_t max_blocks, ctas, can_cut;
+  int32_t max_blocks, pairs, can_cut;
   float scale_log2;   // sm_scale log2 e, not 0
   const float *prev_out, *prev_lse;
   void* out;
@@ -85,9 +93,9 @@ struct PromptParams {
   Block* sorted;        // longest first
   long long* line_at;   // where each block starts on the line
   int32_t* block_at;    // first block of each request
-  int32_t* tickets;     // [ctas][8]: pieces that have ended
-  float2* part_ml;      // [2 * ctas][256]
-  float4* part_o;       // [2 * ctas][256][32]
+  int32_t* tickets;     // [pairs][16]: pieces that have ended
+  float2* part_ml;      // [2 * pairs][512]
+  float4* part_o;       // [2 * pairs][512][32]
 };
 
 // ------------------------------------------------------------------ the plan
@@ -124,7 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
   asm volatile("griddepcontrol.launch_dependents;");  // prompt_kernel may set up
   if (tid == 0) s_most = 1, s_bad = 0, s_bound = 0;
   for (int i = tid; i < 1024; i += kPlanThreads) bins[i] = 0;
-  for (int i = tid; i < p.ctas * 8; i += kPlanThreads) p.tickets[i] = 0;
+  for (int i = tid; i < p.pairs * 16; i += kPlanThreads) p.tickets[i] = 0;
   const int per = kBlock >> p.gshift;  // tokens of a block
   // blocks of each request
   long long before = 0;
@@ -189,21 +197,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
   const long long t = (static_cast<long long>(1023 - tid) << shift) + (shift ? (1 << shift) - 1 : 0) + kStart;  // of the bin's longest
   long long all;
   const long long first = plan_scan(count, warp_sums, all) - count;
-  // Taken one by one in this order, an item ends by (work before it) / CTAs + its own: the
+  // Taken one by one in this order, an item ends by (work before it) / pairs + its own: the
   // last of a bin's is the latest of the bin.
   const long long work = plan_scan(t * count * p.units, warp_sums, all);
-  if (count > 0) atomicMax(reinterpret_cast<unsigned long long*>(&s_bound), static_cast<unsigned long long>((work - t) / p.ctas + t));
+  if (count > 0) atomicMax(reinterpret_cast<unsigned long long*>(&s_bound), static_cast<unsigned long long>((work - t) / p.pairs + t));
   __syncthreads();
   bins[tid] = static_cast<int>(first);
   __syncthreads();
   for (int i = tid; i < n_blocks; i += kPlanThreads) p.sorted[atomicAdd(&bins[1023 - (p.blocks[i].tiles >> shift)], 1)] = p.blocks[i];
   if (tid == 0) {
-    const long long even = line / p.ctas;
+    const long long even = line / p.pairs;
     p.plan->next = 0;
     p.plan->line = line;
     p.plan->n_blocks = n_blocks;
     p.plan->even = p.can_cut && s_most > kLongTiles && s_bound > even + even / 10 + 6;
-    p.plan->ctas = static_cast<int>(max(1LL, min(static_cast<long long>(p.ctas), line / 4)));
+    p.plan->pairs = static_cast<int>(max(1LL, min(static_cast<long long>(p.pairs), line / 4)));
     *p.status = s_bad ? kStatusBounds : 0u;
   }
 }
@@ -214,7 +222,7 @@ __device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -269,14 +277,39 @@ __device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity, volati
   }
   return true;
 }
-// Counters in shared memory that only grow: a waiter may lag behind by any number of steps.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t addr_in(uint32_t saddr, uint32_t rank) {  // the same place in CTA `rank` of the pair
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Arrivals across the pair speak of tensor memory and of TMA's bytes, not of what this thread wrote to memory:
+// they carry no release at cluster scope, which waits for the warp's memory operations (1,000
+// cycles a tile at the end of the softmax). Where memory was written for the other CTA, cluster_fence comes first.
+__device__ __forceinline__ void arrive_in(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr_in(smem_u32(bar), rank)) : "memory");
+}
+__device__ __forceinline__ void cluster_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+__device__ __forceinline__ void store_in(const void* at, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr_in(smem_u32(at), rank)), "r"(v) : "memory");
+}
+// Counters in shared memory that only grow, in both CTAs: a waiter may lag behind by any number of steps.
 __device__ __forceinline__ void count_up(uint32_t* counter) {  // one thread
-  asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_u32(counter)) : "memory");
+#pragma unroll
+  for (uint32_t r = 0; r < 2; ++r)
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], 1;" ::"r"(addr_in(smem_u32(counter), r)) : "memory");
 }
 __device__ __forceinline__ bool wait_count(const uint32_t* counter, uint32_t n, volatile int* abort) {  // a whole warp
   auto there = [&] {
     uint32_t v;
-    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(counter)) : "memory");
+    asm volatile("ld.relaxed.cluster.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(counter)) : "memory");
     return __all_sync(0xFFFFFFFFu, static_cast<int32_t>(v - n) >= 0);
   };
   long long t0 = 0;
@@ -289,6 +322,13 @@ __device__ __forceinline__ bool wait_count(const uint32_t* counter, uint32_t n, 
     }
   }
   return true;
+}
+template <typename M>
+__device__ __forceinline__ bool wait_scanned(const M& m, uint32_t n, volatile int* abort) {
+  bool ok = true;
+#pragma unroll 1
+  for (int i = 0; ok && i < 4; ++i) ok = wait_count(&m.scanned[i], n, abort);
+  return ok;
 }
 // true in one thread of the (converged) warp
 __device__ __forceinline__ bool elect_one() {
@@ -317,7 +357,7 @@ __device__ __forceinline__ Operand operand(uint32_t saddr, uint32_t lbo, uint32_
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, Operand b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -325,8 +365,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, Operand
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, Operand a, Operand b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
       "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrives on the barrier at this address in both CTAs when the products issued so far are done
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ float exp2_fast(float x) {  // relative error about 2^-22; 2^-inf = 0
@@ -359,11 +407,11 @@ struct Item {        // tiles [t0, t1) of a block and head group; t1 = 0: no mor
   int32_t unit;
   int32_t whole;     // all tiles of the block
   int32_t slot;      // where its partial results go
-  int32_t first_cta, pieces;
+  int32_t first_pair, pieces;
 };
-// Tiles that row tile x takes part in: [t0, end), none where end <= t0.
+// Tiles that row tile x takes part in: [t0, end), none where end <= t0. (Both CTAs alike.)
 __device__ __forceinline__ int tokens_of(const PromptParams& p, const Item& it, int x) {
-  return min(it.n_tok - x * (kTile >> p.gshift), kTile >> p.gshift);
+  return min(it.n_tok - x * (2 * kTile >> p.gshift), 2 * kTile >> p.gshift);
 }
 __device__ __forceinline__ int seen_by(const PromptParams& p, const Item& it, int token) {  // keys that a token of the block sees
   return p.causal ? max(0, it.lim0 + token) : it.n_keys;
@@ -371,7 +419,7 @@ __device__ __forceinline__ int seen_by(const PromptParams& p, const Item& it, in
 __device__ __forceinline__ int end_of(const PromptParams& p, const Item& it, int x) {
   const int n = tokens_of(p, it, x);
   if (n <= 0) return 0;
-  const int seen = seen_by(p, it, x * (kTile >> p.gshift) + n - 1);
+  const int seen = seen_by(p, it, x * (2 * kTile >> p.gshift) + n - 1);
   return min(it.t1, max(1, static_cast<int>((static_cast<uint32_t>(seen) + kTile - 1) / kTile)));
 }
 
@@ -387,8 +435,8 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
 template <int D>
 struct Sizes {
   static constexpr int kChunks = D / 64;                // of a row of q or k
-  static constexpr int kSlots = D == 192 ? 8 : 10;
-  static constexpr int kQTile = kChunks * kSlot;
+  static constexpr int kSlots = D == 192 ? 16 : 20;
+  static constexpr int kQTile = kChunks * kQChunk;
   static constexpr int kOffRing = 2 * kQTile, kOffMeta = kOffRing + kSlots * kSlot;
 };
 // Ring positions: K takes kChunks slots, each for itself; V two that lie next to each
@@ -409,13 +457,13 @@ struct Meta {
   Item items[2];
   uint64_t item_full[2], item_free[2];
   uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2];
-  uint64_t k_full[4], v_full[4], v_ok[4];
-  uint64_t slot_free[10];
-  int odd[3][kVal];  // first key whose value in this column is +inf, -inf, NaN
-  uint32_t odd_item;    // the item (from 1 on) that they are of
+  uint64_t k_full[kAhead], v_full[kAhead], v_ok[kAhead];
+  uint64_t slot_free[20];
+  int odd[3][kVal];     // first key whose value in this column is +inf, -inf, NaN; noted by the CTA that has the column
+  uint32_t odd_item[2]; // the item (from 1 on) that they are of, for each CTA's columns
   uint32_t odd_lock;
-  uint32_t scanned[2];  // V tiles that each of the two warps has looked over
-  uint32_t ended;       // warps that are done with what was noted for an item
+  uint32_t scanned[4];  // V tiles that each of the four warps has looked over
+  uint32_t ended;       // warps (of both CTAs) that are done with what was noted for an item
   uint32_t tmem_slot, status;
   int abort_flag;
 };
@@ -423,37 +471,44 @@ template <int D>
 constexpr size_t kSmemBytes = Sizes<D>::kOffMeta + sizeof(Meta);
 static_assert(kSmemBytes<192> <= 232448 && kSmemBytes<128> <= 232448, "shared memory budget");
 
-// Values that are not finite in the rows of a V tile that `hit` names (bit i: row 8 i + 4 mine + lane / 8):
-// zeroed, and where some row of the block sees them noted.
-__device__ __noinline__ bool note_odd(Meta& M, uint8_t* tile, uint32_t hit, int mine, uint32_t n, int key0, int all_see, int n_keys,
-                                      volatile int* abort) {
+// Values that are not finite in the rows of this CTA's half of a V tile that `hit` names (bit i: row
+// 8 i + 4 mine + lane / 8): zeroed, and where some row of the block sees them noted in both CTAs.
+__device__ __noinline__ bool note_odd(Meta& M, uint8_t* tile, uint32_t hit, int mine, uint32_t rank, uint32_t n, int key0, int all_see,
+                                      int n_keys, volatile int* abort) {
   const int lane = threadIdx.x & 31;
   // The results of the items before are out: what was noted for them goes, once.
-  if (!wait_count(&M.ended, 8 * (n - 1), abort)) return false;
+  if (!wait_count(&M.ended, 16 * (n - 1), abort)) return false;
   if (lane == 0)
     for (uint32_t i = 0; atomicCAS(&M.odd_lock, 0u, 1u) != 0 && i < (1u << 24); ++i) __nanosleep(32);
   __syncwarp();
-  if (*const_cast<volatile uint32_t*>(&M.odd_item) != n) {
-    for (int i = lane; i < 3 * kVal; i += 32) (&M.odd[0][0])[i] = INT_MAX;
+  if (*const_cast<volatile uint32_t*>(&M.odd_item[rank]) != n) {
+    for (int i = lane; i < 3 * 64; i += 32)
+      for (uint32_t r = 0; r < 2; ++r) store_in(&M.odd[i >> 6][64 * rank + (i & 63)], r, INT_MAX);
     __syncwarp();
-    if (lane == 0) *const_cast<volatile uint32_t*>(&M.odd_item) = n;
+    if (lane == 0) {
+      cluster_fence();
+      for (uint32_t r = 0; r < 2; ++r) store_in(&M.odd_item[rank], r, n);
+    }
   }
-  __threadfence_block();
+  cluster_fence();
   __syncwarp();
   if (lane == 0) atomicExch(&M.odd_lock, 0u);
   for (; hit; hit &= hit - 1) {
     const int r = 8 * (__ffs(hit) - 1) + 4 * mine + (lane >> 3), key = key0 + r;
     if (key < all_see) continue;
 #pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-      uint16_t* v = reinterpret_cast<uint16_t*>(tile + (i >> 3) * kSlot + r * 128 + (lane & 7) * 16) + (i & 7);
+    for (int i = 0; i < 8; ++i) {
+      uint16_t* v = reinterpret_cast<uint16_t*>(tile + r * 128 + (lane & 7) * 16) + i;
       const uint16_t w = *v;
       if ((w & 0x7F80u) != 0x7F80u) continue;
       *v = 0;
-      const int kind = w == 0x7F80u ? 0 : w == 0xFF80u ? 1 : 2, col = 64 * (i >> 3) + 8 * ((lane & 7) ^ (r & 7)) + (i & 7);
-      if (key < n_keys) atomicMin(&M.odd[kind][col], key);
+      const int kind = w == 0x7F80u ? 0 : w == 0xFF80u ? 1 : 2, col = 64 * rank + 8 * ((lane & 7) ^ (r & 7)) + i;
+      if (key < n_keys)
+        for (uint32_t c = 0; c < 2; ++c)
+          asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(addr_in(smem_u32(&M.odd[kind][col]), c)), "r"(key) : "memory");
     }
   }
+  cluster_fence();  // before the counters and barriers that say so
   __syncwarp();
   return true;
 }
@@ -502,8 +557,9 @@ __device__ __forceinline__ void add_prev(const PromptParams& p, long long at, fl
 }
 // What a row that sees `seen` keys gets in a column from values that are not finite: added to its
 // finite sum, +inf, -inf or NaN; 0: nothing.
-__device__ __forceinline__ float odd_of(const int (&odd)[3][kVal], int col, int seen) {
-  const bool up = odd[0][col] < seen, down = odd[1][col] < seen, nan = odd[2][col] < seen;
+__device__ __forceinline__ float odd_of(const Meta& M, uint32_t item, int col, int seen) {
+  if (M.odd_item[col >> 6] != item) return 0.0f;
+  const bool up = M.odd[0][col] < seen, down = M.odd[1][col] < seen, nan = M.odd[2][col] < seen;
   return nan || (up && down) ? NAN : up ? INFINITY : down ? -INFINITY : 0.0f;
 }
 __device__ __forceinline__ void store4(const PromptParams& p, long long flat, int col, float4 v) {
@@ -513,40 +569,41 @@ __device__ __forceinline__ void store4(const PromptParams& p, long long flat, in
 }
 
 template <int D, bool NEG>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap pe_map, const PromptParams p) {
   using Z = Sizes<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Meta& M = *reinterpret_cast<Meta*>(smem + Z::kOffMeta);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool aligned = (smem_u32(smem) & 1023u) == 0;
+  const uint32_t rank = cluster_rank();
+  const bool aligned = (smem_u32(smem) & 1023u) == 0;  // (alike in both CTAs)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&M.item_full[i], 1);
-      mbar_init(&M.item_free[i], 11);
-      mbar_init(&M.q_full[i], 1);
+      mbar_init(&M.item_free[i], 11 + 12);  // in CTA 0: the warps of both but its own that writes
+      mbar_init(&M.q_full[i], rank == 0 ? 2 : 1);
       mbar_init(&M.q_free[i], 1);
       mbar_init(&M.s_full[i], 1);
-      mbar_init(&M.p_full[i], 4);
+      mbar_init(&M.p_full[i], 8);
       mbar_init(&M.o_full[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&M.k_full[i], 1);
+    for (int i = 0; i < kAhead; ++i) {
+      mbar_init(&M.k_full[i], rank == 0 ? 2 : 1);  // CTA 0's: its own half, and the other's is there
       mbar_init(&M.v_full[i], 1);
-      mbar_init(&M.v_ok[i], 2);
+      mbar_init(&M.v_ok[i], 4);
     }
     for (int i = 0; i < Z::kSlots; ++i) mbar_init(&M.slot_free[i], 1);
-    M.odd_item = M.odd_lock = 0;
-    M.scanned[0] = M.scanned[1] = M.ended = 0;
+    M.odd_item[0] = M.odd_item[1] = M.odd_lock = M.ended = 0;
+    for (int i = 0; i < 4; ++i) M.scanned[i] = 0;
     M.abort_flag = aligned ? 0 : 2;
     M.status = aligned ? 0 : kStatusSetup;
     fence_mbar_init();
   }
   for (int i = tid; i < 3 * kVal; i += kThreads) (&M.odd[0][0])[i] = INT_MAX;
   if (warp == kMmaWarp) {
-    tmem_alloc(&M.tmem_slot, 512);
-    tmem_relinquish();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&M.tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
     prefetch_tensormap(&q_map);
@@ -555,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // the pair's barriers are set up before either CTA signals the other
   tc_fence_after();
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
   const uint32_t tmem = M.tmem_slot;
@@ -571,14 +629,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- schedule and TMA loads
     if (lane == 0) {
       const Plan plan = *p.plan;
-      const int cta = blockIdx.x;
+      const int pair = blockIdx.x >> 1;
       const long long items = static_cast<long long>(plan.n_blocks) * p.units;
-      // even: this CTA's stretch [x, y) of the line and where it stands
+      // even: this pair's stretch [x, y) of the line and where it stands
       long long x = 0, y = 0, at = 0;
       int blk = 0, unit = 0;
-      if (plan.even && cta < plan.ctas) {
-        x = plan.line * cta / plan.ctas;
-        y = plan.line * (cta + 1) / plan.ctas;
+      if (plan.even && pair < plan.pairs) {
+        x = plan.line * pair / plan.pairs;
+        y = plan.line * (pair + 1) / plan.pairs;
         int hi = plan.n_blocks;
         while (hi - blk > 1) {
           const int mid = (blk + hi) >> 1;
@@ -588,8 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         unit = static_cast<int>((x - p.line_at[blk]) / cost);
         at = p.line_at[blk] + static_cast<long long>(unit) * cost;
       }
-      auto cta_of = [&](long long pos) {  // that has this place of the line
-        return static_cast<int>(((pos + 1) * plan.ctas + plan.line - 1) / plan.line) - 1;
+      auto pair_of = [&](long long pos) {  // that has this place of the line
+        return static_cast<int>(((pos + 1) * plan.pairs + plan.line - 1) / plan.line) - 1;
       };
       auto next = [&](Item& it) {
         if (plan.even) {
@@ -602,9 +660,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             at += b.tiles + kStart;
             if (++unit == p.units) unit = 0, ++blk;
             if (t1 <= t0) continue;
-            it = Item{b.tok0, b.n_tok, b.key0, b.lim0, b.n_keys, t0, t1, u, t0 == 0 && t1 == b.tiles, 2 * cta + (t0 == 0), 0, 0};
-            it.first_cta = cta_of(from);
-            it.pieces = cta_of(from + b.tiles - 1) - it.first_cta + 1;
+            it = Item{b.tok0, b.n_tok, b.key0, b.lim0, b.n_keys, t0, t1, u, t0 == 0 && t1 == b.tiles, 2 * pair + (t0 == 0), 0, 0};
+            it.first_pair = pair_of(from);
+            it.pieces = pair_of(from + b.tiles - 1) - it.first_pair + 1;
             return true;
           }
           return false;
@@ -614,9 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long per = static_cast<long long>(plan.n_blocks) * p.units_a;
         const int g = static_cast<int>(i / per), u0 = g * p.units_a, n = min(p.units_a, p.units - u0);
         const long long r = i - g * per;
-        const int rank = static_cast<int>(r / n);
-        const Block b = p.sorted[rank];
-        it = Item{b.tok0, b.n_tok, b.key0, b.lim0, b.n_keys, 0, b.tiles, u0 + static_cast<int>(r - static_cast<long long>(rank) * n), 1, 0, 0, 1};
+        const int place = static_cast<int>(r / n);
+        const Block b = p.sorted[place];
+        it = Item{b.tok0, b.n_tok, b.key0, b.lim0, b.n_keys, 0, b.tiles, u0 + static_cast<int>(r - static_cast<long long>(place) * n), 1, 0, 0, 1};
         return true;
       };
       uint32_t n = 0, kg = 0, vg = 0, used = 0;  // items, K tiles, V tiles, parity of each slot's use
@@ -629,65 +687,100 @@ __global__ void __launch_bounds__(kThreads, 1)
         return got;
       };
       Item it{}, after{};  // the next item is looked up while this one's first loads are under way
-      more = next(after);
+      if (rank == 0) more = next(after);
       while (ok) {
-        it = more ? after : Item{};
-        if (n >= 2 && !wait_one(&M.item_free[n & 1], ((n >> 1) - 1) & 1, abort_v)) break;
-        M.items[n & 1] = it;
-        mbar_arrive(&M.item_full[n & 1]);
+        if (rank == 0) {
+          it = more ? after : Item{};
+          if (n >= 2 && !wait_one(&M.item_free[n & 1], ((n >> 1) - 1) & 1, abort_v)) break;
+          for (uint32_t r = 0; r < 2; ++r) {
+#pragma unroll
+            for (uint32_t i = 0; i < sizeof(Item) / 4; ++i) store_in(reinterpret_cast<uint32_t*>(&M.items[n & 1]) + i, r, reinterpret_cast<uint32_t*>(&it)[i]);
+            cluster_fence();
+            arrive_in(&M.item_full[n & 1], r);
+          }
+        } else {
+          if (!wait_one(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) break;
+          it = M.items[n & 1];
+          arrive_in(&M.item_free[n & 1], 0);
+        }
         ++n;
-        if (!more) break;
+        if (it.t1 == 0) break;
         const int kv_head = static_cast<int>((static_cast<long long>(it.unit) << p.gshift) / p.group);
         auto load_q = [&](int x) {
           if (end_of(p, it, x) <= it.t0) return true;
           if (nq[x] > 0 && !wait_one(&M.q_free[x], (nq[x] - 1) & 1, abort_v)) return false;
           ++nq[x];
           mbar_arrive_expect_tx(&M.q_full[x], Z::kQTile);
-          const int token = it.tok0 + x * (kTile >> p.gshift);
+          const int token = it.tok0 + (2 * x + static_cast<int>(rank)) * (kTile >> p.gshift);
 #pragma unroll 1
           for (int c = 0; c < Z::kChunks; ++c)
-            tma_box(smem + x * Z::kQTile + c * kSlot, &q_map, &M.q_full[x], 64 * c, it.unit << p.gshift, token);
+            tma_box(smem + x * Z::kQTile + c * kQChunk, &q_map, &M.q_full[x], 64 * c, it.unit << p.gshift, token);
           return true;
         };
         for (int t = it.t0; ok && t < it.t1; ++t) {
           if (t == it.t0 && !load_q(0)) { ok = false; break; }
           const int key = it.key0 + t * kTile;
-          uint64_t* k_bar = &M.k_full[kg++ & 3];
+          uint64_t* k_bar = &M.k_full[kg++ & (kAhead - 1)];
 #pragma unroll
           for (int c = 0; c < Z::kChunks; ++c) {
             ok = ok && take_slot(pos);
             if (!ok) break;
             if (c == 0) mbar_arrive_expect_tx(k_bar, Z::kChunks * kSlot);
             const bool shared = 64 * c >= p.d_k;
-            tma_box(smem + Z::kOffRing + pos * kSlot, shared ? &pe_map : &k_map, k_bar, shared ? 0 : 64 * c, shared ? 0 : kv_head, key);
+            tma_box(smem + Z::kOffRing + pos * kSlot, shared ? &pe_map : &k_map, k_bar, shared ? 0 : 64 * c, shared ? 0 : kv_head, key + 64 * static_cast<int>(rank));
             if (++pos == Z::kSlots) pos = 0;
           }
           ok = ok && (t != it.t0 || load_q(1));
-          uint64_t* v_bar = &M.v_full[vg++ & 3];
+          uint64_t* v_bar = &M.v_full[vg++ & (kAhead - 1)];
           if (pos == Z::kSlots - 1) pos = 0;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            ok = ok && take_slot(pos);
-            if (!ok) break;
-            if (c == 0) mbar_arrive_expect_tx(v_bar, 2 * kSlot);
-            tma_box(smem + Z::kOffRing + pos * kSlot, &v_map, v_bar, 64 * c, kv_head, key);
-            if (++pos == Z::kSlots) pos = 0;
-          }
-          if (t == it.t0) more = next(after);
+          ok = ok && take_slot(pos) && take_slot(pos + 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(v_bar, 2 * kSlot);
+          tma_box(smem + Z::kOffRing + pos * kSlot, &v_map, v_bar, 64 * static_cast<int>(rank), kv_head, key);
+          pos = after_v<D>(pos);
+          if (rank == 0 && t == it.t0) more = next(after);
         }
       }
     }
-  } else if (warp == kMmaWarp) {
+   } else if (warp == kMmaWarp && rank == 1) {
+    // -------------------------------------------------------------- what has arrived here, told to CTA 0
+    uint32_t n = 0, kg = 0;
+    uint32_t nq[2] = {0, 0};
+    bool ok = true;
+    while (ok) {
+      if (!wait_warp(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) break;
+      const Item it = M.items[n & 1];
+      __syncwarp();
+      if (lane == 0) arrive_in(&M.item_free[n & 1], 0);
+      ++n;
+      if (it.t1 == 0) break;
+      auto tell_q = [&](int x) {
+        if (end_of(p, it, x) <= it.t0) return true;
+        if (!wait_warp(&M.q_full[x], nq[x] & 1, abort_v)) return false;
+        ++nq[x];
+        if (lane == 0) arrive_in(&M.q_full[x], 0);
+        return true;
+      };
+      ok = tell_q(0);
+      for (int t = it.t0; ok && t < it.t1; ++t) {
+        ok = wait_warp(&M.k_full[kg & (kAhead - 1)], (kg / kAhead) & 1, abort_v);
+        if (!ok) break;
+        if (lane == 0) arrive_in(&M.k_full[kg & (kAhead - 1)], 0);
+        ++kg;
+        if (t == it.t0) ok = tell_q(1);
+      }
+    }
+   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------- MMA issue
     // Warp-wide on warp-uniform values, each batch of MMAs unrolled and issued by one
     // elected thread: descriptors come from uniform registers.
-    constexpr uint32_t id_qk = instr_desc(128, 128, kFmtBF16, kFmtBF16, false, false);
-    constexpr uint32_t id_pv = instr_desc(128, 128, kFmtBF16, kFmtBF16, false, true);
+    constexpr uint32_t id_qk = instr_desc(256, 128, kFmtBF16, kFmtBF16, false, false);
+    constexpr uint32_t id_pv = instr_desc(256, 128, kFmtBF16, kFmtBF16, false, true);
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const uint32_t sb = __shfl_sync(0xFFFFFFFFu, sbase, 0);
     const Operand q_desc = operand(sb, 16, 1024);
     const Operand k_desc = operand(sb + Z::kOffRing, 16, 1024);
-    const Operand v_desc = operand(sb + Z::kOffRing, kSlot, 1024);  // read as values x keys
+    const Operand v_desc = operand(sb + Z::kOffRing, 2 * kSlot, 1024);  // read as values x keys
     uint32_t n = 0, kg = 0, vg = 0;
     uint32_t nq[2] = {0, 0}, ns[2] = {0, 0};  // row tiles begun, P tiles used
     int pos = 0;
@@ -701,10 +794,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Operand k = k_desc + s * kSlot;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss(tm + kColS + kTile * x, q_desc + (x * Z::kQTile + c * kSlot + 32 * kk), k + 32 * kk, id_qk, c != 0 || kk != 0);
+            mma_ss(tm + kColS + kTile * x, q_desc + (x * Z::kQTile + c * kQChunk + 32 * kk), k + 32 * kk, id_qk, c != 0 || kk != 0);
         }
-        mma_commit(&M.s_full[x]);
-        if (last) mma_commit(&M.q_free[x]);
+        commit_pair(&M.s_full[x]);
+        if (last) commit_pair(&M.q_free[x]);
       }
       __syncwarp();
     };
@@ -715,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(tm + kColO + kVal * x, tm + kColS + kTile * x + 8 * kk, v + 2048 * kk, id_pv, kk != 0 || !first);
-        if (last) mma_commit(&M.o_full[x]);
+        if (last) commit_pair(&M.o_full[x]);
       }
       __syncwarp();
     };
@@ -723,12 +816,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto free_slots = [&](int vpos, int kpos, bool k) {
       if (elect_one()) {
         if (vpos >= 0) {
-          mma_commit(&M.slot_free[vpos]);
-          mma_commit(&M.slot_free[vpos + 1]);
+          commit_pair(&M.slot_free[vpos]);
+          commit_pair(&M.slot_free[vpos + 1]);
         }
         if (k)
 #pragma unroll
-          for (int c = 0; c < Z::kChunks; ++c) mma_commit(&M.slot_free[kpos + c >= Z::kSlots ? kpos + c - Z::kSlots : kpos + c]);
+          for (int c = 0; c < Z::kChunks; ++c) commit_pair(&M.slot_free[kpos + c >= Z::kSlots ? kpos + c - Z::kSlots : kpos + c]);
       }
       __syncwarp();
     };
@@ -736,13 +829,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_warp(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) { ok = false; break; }
       const Item it = M.items[n & 1];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&M.item_free[n & 1]);
+      if (lane == 0) arrive_in(&M.item_free[n & 1], 0);
       ++n;
       if (it.t1 == 0) break;
       const int t0 = __shfl_sync(0xFFFFFFFFu, it.t0, 0), t1 = __shfl_sync(0xFFFFFFFFu, it.t1, 0);
       const int end[2] = {__shfl_sync(0xFFFFFFFFu, end_of(p, it, 0), 0), __shfl_sync(0xFFFFFFFFu, end_of(p, it, 1), 0)};
       int kpos = pos;
-      ok = wait_warp(&M.k_full[kg & 3], (kg >> 2) & 1, abort_v);
+      ok = wait_warp(&M.k_full[kg & (kAhead - 1)], (kg / kAhead) & 1, abort_v);
       ++kg;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -758,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int vpos = after_k<D>(kpos);
         kpos = after_v<D>(vpos);
         bool have_k = false;
-        ok = wait_warp(&M.v_ok[vg & 3], (vg >> 2) & 1, abort_v);
+        ok = wait_warp(&M.v_ok[vg & (kAhead - 1)], (vg / kAhead) & 1, abort_v);
         ++vg;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -770,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           pv(x, vpos, t == t0, last);
           if (last) continue;
           if (!have_k) {
-            ok = wait_warp(&M.k_full[kg & 3], (kg >> 2) & 1, abort_v);
+            ok = wait_warp(&M.k_full[kg & (kAhead - 1)], (kg / kAhead) & 1, abort_v);
             ++kg;
             have_k = true;
           }
@@ -792,14 +885,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_warp(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) break;
       const Item it = M.items[n & 1];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&M.item_free[n & 1]);
+      if (lane == 0) arrive_in(&M.item_free[n & 1], 0);
       if (it.t1 == 0) break;
       ++n;
       const int all_see = seen_by(p, it, 0);  // keys before this one are seen by every row
       for (int t = it.t0; t < it.t1; ++t) {
         const int vpos = after_k<D>(pos);
         pos = after_v<D>(vpos);
-        if (!wait_warp(&M.v_full[vg & 3], (vg >> 2) & 1, abort_v)) { ok = false; break; }
+        if (!wait_warp(&M.v_full[vg & (kAhead - 1)], (vg / kAhead) & 1, abort_v)) { ok = false; break; }
         if ((t + 1) * kTile > all_see) {
           // Eight lanes read the eight pieces of a row; the rows that every row sees left out.
           const int first = (max(0, all_see - t * kTile) & ~7) + 4 * mine;
@@ -807,21 +900,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
           for (int r = first; r < kTile; r += 8) {
             const uint8_t* at = smem + Z::kOffRing + vpos * kSlot + (r + (lane >> 3)) * 128 + (lane & 7) * 16;
-            const uint4 w = *reinterpret_cast<const uint4*>(at), u = *reinterpret_cast<const uint4*>(at + kSlot);
+            const uint4 w = *reinterpret_cast<const uint4*>(at);
             // an exponent of all ones carries into the sign's place
             auto odd = [](uint32_t v) { return (v & 0x7F807F80u) + 0x00800080u; };
-            const uint32_t any = odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w) | odd(u.x) | odd(u.y) | odd(u.z) | odd(u.w);
+            const uint32_t any = odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w);
             hit |= static_cast<uint32_t>((any & 0x80008000u) != 0) << (r >> 3);
           }
           if (__any_sync(0xFFFFFFFFu, hit != 0)) {
-            if (!note_odd(M, smem + Z::kOffRing + vpos * kSlot, hit, mine, n, t * kTile, all_see, it.n_keys, abort_v)) { ok = false; break; }
+            if (!note_odd(M, smem + Z::kOffRing + vpos * kSlot, hit, mine, rank, n, t * kTile, all_see, it.n_keys, abort_v)) { ok = false; break; }
             fence_proxy_async_smem();
           }
         }
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&M.v_ok[vg & 3]);
-          count_up(&M.scanned[mine]);
+          arrive_in(&M.v_ok[vg & (kAhead - 1)], 0);
+          count_up(&M.scanned[2 * rank + mine]);
         }
         ++vg;
       }
@@ -842,10 +935,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_here(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) break;
       const Item it = M.items[n & 1];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&M.item_free[n & 1]);
+      if (lane == 0) arrive_in(&M.item_free[n & 1], 0);
       if (it.t1 == 0) break;
-      const int per = kTile >> p.gshift, end = end_of(p, it, x), n_tok = tokens_of(p, it, x);
-      const int token = x * per + (row >> p.gshift);  // of the block
+      const int first = (2 * x + static_cast<int>(rank)) * (kTile >> p.gshift);  // this CTA's first token in the tile
+      const int end = end_of(p, it, x), n_tok = min(it.n_tok - first, kTile >> p.gshift);
+      const int token = first + (row >> p.gshift);  // of the block
       const bool exists = (row >> p.gshift) < n_tok;
       // (rows that do not exist count like the last one that does)
       const int seen = seen_by(p, it, min(token, it.n_tok - 1));
@@ -920,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&M.p_full[x]);
+        if (lane == 0) arrive_in(&M.p_full[x], 0);
       }
       if (!ok) break;
       // ---- results
@@ -933,8 +1027,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++no;
         tc_fence_after();
         const uint32_t used = vg + static_cast<uint32_t>(end - it.t0);
-        if (!wait_count(&M.scanned[0], used, abort_v) || !wait_count(&M.scanned[1], used, abort_v)) break;
-        any_odd = *const_cast<volatile uint32_t*>(&M.odd_item) == n + 1;
+        if (!wait_scanned(M, used, abort_v)) break;
+        any_odd = *const_cast<volatile uint32_t*>(&M.odd_item[0]) == n + 1 || *const_cast<volatile uint32_t*>(&M.odd_item[1]) == n + 1;
+        if (any_odd) cluster_fence();
       }
       vg += it.t1 - it.t0;
       // (nothing was noted that this warp needs: no need to wait for its stores)
@@ -978,7 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (any_odd && exists) {
           for (int c = 0; c < kVal; ++c) {
-            const float o = odd_of(M.odd, c, seen);
+            const float o = odd_of(M, n + 1, c, seen);
             if (o == 0.0f) continue;
             const long long at = flat * kVal + c;
             if (p.out_fp32) {
@@ -991,7 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       } else if (quad * 32 >> p.gshift < n_tok) {  // a piece: some row of the warp exists
-        const int r0 = x * kTile + quad * 32;      // the warp's first row in the block
+        const int r0 = (2 * x + static_cast<int>(rank)) * kTile + quad * 32;  // the warp's first row in the block
         const long long at = static_cast<long long>(it.slot) * kBlock + r0 + lane;
         float* part = reinterpret_cast<float*>(p.part_o + at * 32);
 #pragma unroll 1
@@ -1007,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (any_odd && exists) {
           for (int c = 0; c < kVal; ++c) {
-            const float o = odd_of(M.odd, c, seen);
+            const float o = odd_of(M, n + 1, c, seen);
             if (o != 0.0f) part[c] += o;
           }
         }
@@ -1015,14 +1110,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __threadfence();
         __syncwarp();
         int ended = 0;
-        if (lane == 0) ended = atomicAdd(p.tickets + it.first_cta * 8 + (warp - kSoftWarp0), 1);
+        if (lane == 0) ended = atomicAdd(p.tickets + it.first_pair * 16 + 8 * rank + (warp - kSoftWarp0), 1);
         ended = __shfl_sync(0xFFFFFFFFu, ended, 0);
         if (ended == it.pieces - 1) {
           // The last of the pieces of these 32 rows: join them, by their maxima and sums, in
           // the order of the pieces. A lane's row for the weights, then a row's 128 values
           // over the lanes, eight rows at a time.
           __threadfence();
-          auto slot_of = [&](int i) { return static_cast<long long>(2 * (it.first_cta + i) + (i == 0)) * kBlock + r0; };
+          auto slot_of = [&](int i) { return static_cast<long long>(2 * (it.first_pair + i) + (i == 0)) * kBlock + r0; };
           float best = -INFINITY, sum = 0.0f;
           if (exists) {
             for (int i = 0; i < it.pieces; ++i) {
@@ -1098,9 +1193,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && M.status) set_status(p.status, M.status);
+  cluster_sync();  // the other CTA may still signal this one's shared memory until here
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
@@ -1136,7 +1232,7 @@ int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, con
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.ctas);
+  cfg.gridDim = dim3(2 * p.pairs);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes<D>;
   cfg.stream = st;
@@ -1148,15 +1244,30 @@ template <int D, bool NEG>
 bool set_smem() {
   return cudaFuncSetAttribute(prompt_kernel<D, NEG>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes<D>)) == cudaSuccess;
 }
-// CTAs of the current device, one per SM; looked up once per device, with the kernels' shared
-// memory limit set. 0: no device.
-int ctas_of_device() {
+template <int D, bool NEG>
+int resident_pairs() {
+  if (!set_smem<D, NEG>()) return 0;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * num_sms());
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes<D>;
+  cfg.attrs = &at, cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, prompt_kernel<D, NEG>, &cfg) == cudaSuccess ? n : 0;
+}
+// CTA pairs that run at the same time (76 on a 152-SM part; fewer where a GPC has an odd number of
+// SMs). Looked up once per device, with the kernels' shared memory limit set. 0: no device.
+int pairs_of_device() {
   static std::mutex mutex;
   static int known[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mutex);
-  if (known[dev] == 0 && set_smem<192, false>() && set_smem<192, true>() && set_smem<128, false>() && set_smem<128, true>()) known[dev] = num_sms();
+  if (known[dev] == 0)
+    known[dev] = std::min({resident_pairs<192, false>(), resident_pairs<192, true>(), resident_pairs<128, false>(), resident_pairs<128, true>(), num_sms() / 2});
   return known[dev];
 }
 
@@ -1168,13 +1279,13 @@ size_t layout(PromptParams& p, uint8_t* ws) {
   while (p.gshift < 7 && p.group % (2 << p.gshift) == 0) ++p.gshift;
   p.units = p.n_heads >> p.gshift;
   p.max_blocks = p.total_q / (kBlock >> p.gshift) + p.n_seqs;
-  p.ctas = std::max(1, ctas_of_device());
+  p.pairs = std::max(1, pairs_of_device());
   p.can_cut = p.total_k > kLongTiles * kTile;
   size_t at = kStatusBytes;
   p.plan = reinterpret_cast<Plan*>(ws + at);
   at += up256(sizeof(Plan));
   p.tickets = reinterpret_cast<int32_t*>(ws + at);
-  at += up256(static_cast<size_t>(p.ctas) * 8 * 4);
+  at += up256(static_cast<size_t>(p.pairs) * 16 * 4);
   p.blocks = reinterpret_cast<Block*>(ws + at);
   at += up256(static_cast<size_t>(p.max_blocks) * sizeof(Block));
   p.line_at = reinterpret_cast<long long*>(ws + at);
@@ -1185,9 +1296,9 @@ size_t layout(PromptParams& p, uint8_t* ws) {
   at += up256((static_cast<size_t>(p.n_seqs) + 1) * 4);
   if (p.can_cut) {
     p.part_ml = reinterpret_cast<float2*>(ws + at);
-    at += static_cast<size_t>(p.ctas) * 2 * kBlock * 8;
+    at += static_cast<size_t>(p.pairs) * 2 * kBlock * 8;
     p.part_o = reinterpret_cast<float4*>(ws + at);
-    at += static_cast<size_t>(p.ctas) * 2 * kBlock * kVal * 4;
+    at += static_cast<size_t>(p.pairs) * 2 * kBlock * kVal * 4;
   }
   return at;
 }
@@ -1245,8 +1356,8 @@ int smla_prompt_fwd(const smla_heads* q, const smla_heads* k, const smla_heads* 
   CUtensorMap q_map{}, k_map{}, v_map{}, pe_map{};
   const int g = 1 << p.gshift;
   const smla_heads pe{k_pe, k_pe_stride, kPe};
-  if (!encode_heads(&q_map, *q, d_qk, n_heads, total_q, g, kTile / g) || !encode_heads(&k_map, *k, d_k, n_kv_heads, total_k, 1, kTile) ||
-      !encode_heads(&v_map, *v, kVal, n_kv_heads, total_k, 1, kTile) || (k_pe && !encode_heads(&pe_map, pe, kPe, 1, total_k, 1, kTile)))
+  if (!encode_heads(&q_map, *q, d_qk, n_heads, total_q, g, kTile / g) || !encode_heads(&k_map, *k, d_k, n_kv_heads, total_k, 1, kTile / 2) ||
+      !encode_heads(&v_map, *v, kVal, n_kv_heads, total_k, 1, kTile) || (k_pe && !encode_heads(&pe_map, pe, kPe, 1, total_k, 1, kTile / 2)))
     return SMLA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const auto go = d_qk == 192 ? (p.scale_log2 < 0.0f ? launch<192, true> : launch<192, false>) : (p.scale_log2 < 0.0f ? launch<128, true> : launch<128, false>);
