@@ -416,7 +416,12 @@ __device__ __forceinline__ int tokens_of(const PromptParams& p, const Item& it, 
 __device__ __forceinline__ int seen_by(const PromptParams& p, const Item& it, int token) {  // keys that a token of the block sees
   return p.causal ? max(0, it.lim0 + token) : it.n_keys;
 }
+// A block of one row tile: its key tiles go to both halves of the pipeline in turn, which hold the
+// same rows and are joined at the end. (One row tile alone leaves the tensor cores waiting for its softmax:
+// 5 x 3 tokens of 64 heads on 9K keys, 530 us, against 290 with both halves at work.)
+__device__ __forceinline__ bool two_halves(const PromptParams& p, const Item& it) { return tokens_of(p, it, 1) <= 0 && it.t1 - it.t0 >= 2; }
 __device__ __forceinline__ int end_of(const PromptParams& p, const Item& it, int x) {
+  if (two_halves(p, it)) return it.t1;
   const int n = tokens_of(p, it, x);
   if (n <= 0) return 0;
   const int seen = seen_by(p, it, x * (2 * kTile >> p.gshift) + n - 1);
@@ -456,16 +461,18 @@ __device__ __forceinline__ int after_v(int pos) {
 struct Meta {
   Item items[2];
   uint64_t item_full[2], item_free[2];
-  uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], q_free[2], s_full[2], p_half[2], p_full[2], o_full[2];
+  uint64_t ml_full, ml_free;
   uint64_t k_full[kAhead], v_full[kAhead], v_ok[kAhead];
   uint64_t slot_free[20];
-  int odd[3][kVal];     // first key whose value in this column is +inf, -inf, NaN; noted by the CTA that has the column
+  int odd[2][kVal];     // first key whose value in this column is +inf or NaN, -inf or NaN; noted by the CTA that has the column
   uint32_t odd_item[2]; // the item (from 1 on) that they are of, for each CTA's columns
   uint32_t odd_lock;
   uint32_t scanned[4];  // V tiles that each of the four warps has looked over
   uint32_t ended;       // warps (of both CTAs) that are done with what was noted for an item
   uint32_t tmem_slot, status;
   int abort_flag;
+  float2 ml[kTile];     // maximum and sum of the second row tile's half of the keys (two_halves)
 };
 template <int D>
 constexpr size_t kSmemBytes = Sizes<D>::kOffMeta + sizeof(Meta);
@@ -482,7 +489,7 @@ __device__ __noinline__ bool note_odd(Meta& M, uint8_t* tile, uint32_t hit, int 
     for (uint32_t i = 0; atomicCAS(&M.odd_lock, 0u, 1u) != 0 && i < (1u << 24); ++i) __nanosleep(32);
   __syncwarp();
   if (*const_cast<volatile uint32_t*>(&M.odd_item[rank]) != n) {
-    for (int i = lane; i < 3 * 64; i += 32)
+    for (int i = lane; i < 2 * 64; i += 32)
       for (uint32_t r = 0; r < 2; ++r) store_in(&M.odd[i >> 6][64 * rank + (i & 63)], r, INT_MAX);
     __syncwarp();
     if (lane == 0) {
@@ -502,10 +509,11 @@ __device__ __noinline__ bool note_odd(Meta& M, uint8_t* tile, uint32_t hit, int 
       const uint16_t w = *v;
       if ((w & 0x7F80u) != 0x7F80u) continue;
       *v = 0;
-      const int kind = w == 0x7F80u ? 0 : w == 0xFF80u ? 1 : 2, col = 64 * rank + 8 * ((lane & 7) ^ (r & 7)) + i;
+      const int col = 64 * rank + 8 * ((lane & 7) ^ (r & 7)) + i;
       if (key < n_keys)
-        for (uint32_t c = 0; c < 2; ++c)
-          asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(addr_in(smem_u32(&M.odd[kind][col]), c)), "r"(key) : "memory");
+        for (uint32_t c = 0; c < 4; ++c)
+          if (w != ((c & 1) ? 0x7F80u : 0xFF80u))  // a NaN counts as both
+            asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(addr_in(smem_u32(&M.odd[c & 1][col]), c >> 1)), "r"(key) : "memory");
     }
   }
   cluster_fence();  // before the counters and barriers that say so
@@ -559,8 +567,8 @@ __device__ __forceinline__ void add_prev(const PromptParams& p, long long at, fl
 // finite sum, +inf, -inf or NaN; 0: nothing.
 __device__ __forceinline__ float odd_of(const Meta& M, uint32_t item, int col, int seen) {
   if (M.odd_item[col >> 6] != item) return 0.0f;
-  const bool up = M.odd[0][col] < seen, down = M.odd[1][col] < seen, nan = M.odd[2][col] < seen;
-  return nan || (up && down) ? NAN : up ? INFINITY : down ? -INFINITY : 0.0f;
+  const bool up = M.odd[0][col] < seen, down = M.odd[1][col] < seen;
+  return up && down ? NAN : up ? INFINITY : down ? -INFINITY : 0.0f;
 }
 __device__ __forceinline__ void store4(const PromptParams& p, long long flat, int col, float4 v) {
   const long long at = flat * kVal + col;
@@ -585,6 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&M.q_full[i], rank == 0 ? 2 : 1);
       mbar_init(&M.q_free[i], 1);
       mbar_init(&M.s_full[i], 1);
+      mbar_init(&M.p_half[i], 8);
       mbar_init(&M.p_full[i], 8);
       mbar_init(&M.o_full[i], 1);
     }
@@ -594,13 +603,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&M.v_ok[i], 4);
     }
     for (int i = 0; i < Z::kSlots; ++i) mbar_init(&M.slot_free[i], 1);
+    mbar_init(&M.ml_full, 4);
+    mbar_init(&M.ml_free, 4);
     M.odd_item[0] = M.odd_item[1] = M.odd_lock = M.ended = 0;
     for (int i = 0; i < 4; ++i) M.scanned[i] = 0;
     M.abort_flag = aligned ? 0 : 2;
     M.status = aligned ? 0 : kStatusSetup;
     fence_mbar_init();
   }
-  for (int i = tid; i < 3 * kVal; i += kThreads) (&M.odd[0][0])[i] = INT_MAX;
+  for (int i = tid; i < 2 * kVal; i += kThreads) (&M.odd[0][0])[i] = INT_MAX;
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&M.tmem_slot)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -711,7 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (nq[x] > 0 && !wait_one(&M.q_free[x], (nq[x] - 1) & 1, abort_v)) return false;
           ++nq[x];
           mbar_arrive_expect_tx(&M.q_full[x], Z::kQTile);
-          const int token = it.tok0 + (2 * x + static_cast<int>(rank)) * (kTile >> p.gshift);
+          const int token = it.tok0 + ((two_halves(p, it) ? 0 : 2 * x) + static_cast<int>(rank)) * (kTile >> p.gshift);
 #pragma unroll 1
           for (int c = 0; c < Z::kChunks; ++c)
             tma_box(smem + x * Z::kQTile + c * kQChunk, &q_map, &M.q_full[x], 64 * c, it.unit << p.gshift, token);
@@ -801,12 +812,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    auto pv = [&](int x, int vpos, bool first, bool last) {
+    auto pv = [&](int x, int vpos, int k0, bool first, bool last) {  // four steps of 16 keys from step k0 on
       tc_fence_after();
       if (elect_one()) {
         const Operand v = v_desc + vpos * kSlot;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
+        for (int kk = k0; kk < k0 + 4; ++kk)
           mma_ts(tm + kColO + kVal * x, tm + kColS + kTile * x + 8 * kk, v + 2048 * kk, id_pv, kk != 0 || !first);
         if (last) commit_pair(&M.o_full[x]);
       }
@@ -835,6 +846,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int t0 = __shfl_sync(0xFFFFFFFFu, it.t0, 0), t1 = __shfl_sync(0xFFFFFFFFu, it.t1, 0);
       const int end[2] = {__shfl_sync(0xFFFFFFFFu, end_of(p, it, 0), 0), __shfl_sync(0xFFFFFFFFu, end_of(p, it, 1), 0)};
       int kpos = pos;
+      if (__shfl_sync(0xFFFFFFFFu, two_halves(p, it), 0)) {
+        // QK0(t0) QK1(t0+1) | PV0(t0) QK0(t0+2) | PV1(t0+1) QK1(t0+3) ...
+        int kn = kpos;  // where the next K tile is
+#pragma unroll 1
+        for (int t = t0 - 2; ok && t < t1; ++t) {
+          const int x = (t - t0) & 1;
+          if (t >= t0) {
+            const int vpos = after_k<D>(kpos);
+            kpos = after_v<D>(vpos);
+            ok = wait_warp(&M.v_ok[vg & (kAhead - 1)], (vg / kAhead) & 1, abort_v) && wait_warp(&M.p_half[x], ns[x] & 1, abort_v);
+            ++vg;
+            if (!ok) break;
+            pv(x, vpos, 0, t < t0 + 2, false);
+            ok = wait_warp(&M.p_full[x], ns[x] & 1, abort_v);
+            ++ns[x];
+            if (!ok) break;
+            pv(x, vpos, 4, false, t + 2 >= t1);
+            free_slots(vpos, 0, false);
+          }
+          if (t + 2 < t1) {
+            if (t < t0) {
+              ok = wait_warp(&M.q_full[x], nq[x] & 1, abort_v);
+              ++nq[x];
+            }
+            ok = ok && wait_warp(&M.k_full[kg & (kAhead - 1)], (kg / kAhead) & 1, abort_v);
+            ++kg;
+            if (!ok) break;
+            qk(x, kn, t + 4 >= t1);
+            free_slots(-1, kn, true);
+            kn = after_v<D>(after_k<D>(kn));
+          }
+        }
+        pos = kpos;
+        if (!ok) break;
+        continue;
+      }
       ok = wait_warp(&M.k_full[kg & (kAhead - 1)], (kg / kAhead) & 1, abort_v);
       ++kg;
 #pragma unroll
@@ -856,11 +903,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (!ok || t >= end[x]) continue;
+          ok = wait_warp(&M.p_half[x], ns[x] & 1, abort_v);
+          if (!ok) continue;
+          const bool last = t + 1 == end[x];
+          pv(x, vpos, 0, t == t0, false);
           ok = wait_warp(&M.p_full[x], ns[x] & 1, abort_v);
           ++ns[x];
           if (!ok) continue;
-          const bool last = t + 1 == end[x];
-          pv(x, vpos, t == t0, last);
+          pv(x, vpos, 4, false, last);
           if (last) continue;
           if (!have_k) {
             ok = wait_warp(&M.k_full[kg & (kAhead - 1)], (kg / kAhead) & 1, abort_v);
@@ -929,7 +979,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_col = tmem + lanes + kColS + kTile * x, o_col = tmem + lanes + kColO + kVal * x;
     const float hidden = NEG ? INFINITY : -INFINITY;  // times a negative scale: -inf
-    uint32_t n = 0, g = 0, no = 0, vg = 0;  // items, tiles, results, V tiles
+    uint32_t n = 0, g = 0, no = 0, vg = 0, nh = 0;  // items, tiles, results, V tiles, items in two halves
     bool ok = true;
     while (ok) {
       if (!wait_here(&M.item_full[n & 1], (n >> 1) & 1, abort_v)) break;
@@ -937,7 +987,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) arrive_in(&M.item_free[n & 1], 0);
       if (it.t1 == 0) break;
-      const int first = (2 * x + static_cast<int>(rank)) * (kTile >> p.gshift);  // this CTA's first token in the tile
+      const bool halves = two_halves(p, it);
+      const int first = ((halves ? 0 : 2 * x) + static_cast<int>(rank)) * (kTile >> p.gshift);  // this CTA's first token in the tile
       const int end = end_of(p, it, x), n_tok = min(it.n_tok - first, kTile >> p.gshift);
       const int token = first + (row >> p.gshift);  // of the block
       const bool exists = (row >> p.gshift) < n_tok;
@@ -945,7 +996,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int seen = seen_by(p, it, min(token, it.n_tok - 1));
       const int least_seen = __reduce_min_sync(0xFFFFFFFFu, seen);
       float m = -INFINITY, l = 0.0f;
-      for (int t = it.t0; t < end; ++t, ++g) {
+      const int t_first = it.t0 + (halves ? x : 0), t_step = halves ? 2 : 1;
+      for (int t = t_first; t < end; t += t_step, ++g) {
         if (!wait_here(&M.s_full[x], g & 1, abort_v)) { ok = false; break; }
         tc_fence_after();
         // Keys that the row does not see: their logits are replaced where they lie, 32 keys at a time (a
@@ -984,7 +1036,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           l *= alpha;
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        if (t > it.t0 && __any_sync(0xFFFFFFFFu, raise)) {  // O holds every tile before this one
+        if (t > t_first && __any_sync(0xFFFFFFFFu, raise)) {  // O holds every tile before this one
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t o[16];
@@ -1009,6 +1061,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             pk[i >> 1] = bf_pack(e.x, e.y);
           }
           tmem_st_x16(s_col + 16 * h, pk);
+          if (h == 1) {  // the product with the first 64 keys may begin
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_in(&M.p_half[x], 0);
+          }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
@@ -1020,7 +1078,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---- results
       const int head = it.unit << p.gshift;
       const long long flat = (static_cast<long long>(it.tok0) + token) * p.n_heads + head + (row & ((1 << p.gshift) - 1));
-      const bool some = end > it.t0;
+      const bool some = end > it.t0;  // (the items' tiles, or this half's)
       bool any_odd = false;
       if (some) {
         if (!wait_here(&M.o_full[x], no & 1, abort_v)) break;
@@ -1035,7 +1093,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // (nothing was noted that this warp needs: no need to wait for its stores)
       const bool done = !__any_sync(0xFFFFFFFFu, any_odd);
       if (done && lane == 0) count_up(&M.ended);
-      if (n_tok > 0 && it.whole) {
+      // Two halves: the first one's warps join both and write the results.
+      float w0 = 1.0f, w1 = 0.0f;
+      if (halves) {
+        if (x == 1) {
+          M.ml[row] = make_float2(m, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&M.ml_full);
+          if (!wait_here(&M.ml_free, nh & 1, abort_v)) break;  // it has read this half's O
+        } else {
+          if (!wait_here(&M.ml_full, nh & 1, abort_v)) break;
+          tc_fence_after();
+          const float2 other = M.ml[row];
+          const float top = fmaxf(l != 0.0f ? m : -INFINITY, other.y != 0.0f ? other.x : -INFINITY);
+          w0 = l != 0.0f ? exp2_fast(m - top) : 0.0f;
+          w1 = other.y != 0.0f ? exp2_fast(other.x - top) : 0.0f;
+          l = (l != 0.0f ? w0 * l : 0.0f) + (other.y != 0.0f ? w1 * other.y : 0.0f);
+          m = top;
+        }
+        ++nh;
+      }
+      const bool writes = !(halves && x == 1);
+      // 16 values of the row's sum
+      auto sums = [&](int c, float* v) {
+        tmem_ld_32x32b_x16(o_col + c, reinterpret_cast<uint32_t*>(v));
+        if (halves) {
+          float u[16];
+          tmem_ld_32x32b_x16(o_col + kVal + c, reinterpret_cast<uint32_t*>(u));
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = (w0 != 0.0f ? w0 * v[i] : 0.0f) + (w1 != 0.0f ? w1 * u[i] : 0.0f);
+        } else {
+          tmem_wait_ld();
+        }
+      };
+      if (writes && n_tok > 0 && it.whole) {
         Joined j{0.0f, 0.0f, -INFINITY};
         if (exists) {
           j = join_prev(p, flat, m, l);
@@ -1045,28 +1138,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // is fetched anew. 128 columns unrolled took 5,000 cycles, most of them waiting for code.)
         const float f = l != 0.0f ? j.f : 0.0f;
 #pragma unroll 1
-        for (int c = 0; c < kVal; c += 32) {
-          float v[32];
-          tmem_ld_32x32b_x32(o_col + c, reinterpret_cast<uint32_t*>(v));
-          tmem_wait_ld();
+        for (int c = 0; c < kVal; c += 16) {
+          float v[16];
+          sums(c, v);
           if (exists) {
             const long long at = flat * kVal + c;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = l != 0.0f ? v[i] * f : 0.0f;
-            if (j.fp != 0.0f) {
-              add_prev(p, at, j.fp, v);
-              add_prev(p, at + 16, j.fp, v + 16);
-            }
+            for (int i = 0; i < 16; ++i) v[i] = l != 0.0f ? v[i] * f : 0.0f;
+            if (j.fp != 0.0f) add_prev(p, at, j.fp, v);
             if (p.out_fp32) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 8) store8(static_cast<float*>(p.out) + at + i, v + i, p.out_sectors);
+              store8(static_cast<float*>(p.out) + at, v, p.out_sectors);
+              store8(static_cast<float*>(p.out) + at + 8, v + 8, p.out_sectors);
             } else {
-              uint32_t w[16];
+              uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = bf_pack(v[2 * i], v[2 * i + 1]);
-#pragma unroll
-              for (int i = 0; i < 16; i += 8)
-                store8(reinterpret_cast<float*>(static_cast<uint16_t*>(p.out) + at + 2 * i), reinterpret_cast<const float*>(w + i), p.out_sectors);
+              for (int i = 0; i < 8; ++i) w[i] = bf_pack(v[2 * i], v[2 * i + 1]);
+              store8(reinterpret_cast<float*>(static_cast<uint16_t*>(p.out) + at), reinterpret_cast<const float*>(w), p.out_sectors);
             }
           }
           __syncwarp();
@@ -1085,15 +1172,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-      } else if (quad * 32 >> p.gshift < n_tok) {  // a piece: some row of the warp exists
+      } else if (writes && quad * 32 >> p.gshift < n_tok) {  // a piece: some row of the warp exists
         const int r0 = (2 * x + static_cast<int>(rank)) * kTile + quad * 32;  // the warp's first row in the block
         const long long at = static_cast<long long>(it.slot) * kBlock + r0 + lane;
         float* part = reinterpret_cast<float*>(p.part_o + at * 32);
 #pragma unroll 1
         for (int c = 0; c < kVal && some; c += 16) {
           float v[16];
-          tmem_ld_32x32b_x16(o_col + c, reinterpret_cast<uint32_t*>(v));
-          tmem_wait_ld();
+          sums(c, v);
           if (exists) {
             store8(part + c, v, true);
             store8(part + c + 8, v + 8, true);
@@ -1178,6 +1264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
+      if (halves && x == 0 && lane == 0) mbar_arrive(&M.ml_free);
       if (!done && lane == 0) count_up(&M.ended);
       ++n;
     }
