@@ -33,8 +33,7 @@
 // are many, pairs take them one by one, longest first, a few key heads at a time (so that
 // their K and V stay in L2). Where the longest would end late (few rows, many keys), all
 // tiles lie on one line that is cut into equal stretches, one per pair; blocks that are cut
-// leave fp32 partial results, and the warp that ends a row group's last piece joins them, in
-// the order of the pieces. No pair waits for another.
+// leave fp32 partial results, which join_kernel joins. No pair waits for another.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -66,6 +65,9 @@ struct Block {      // of the plan
   int32_t n_keys, tiles;  // keys that its last token sees; tiles of them, at least one
   int32_t pad[2];
 };
+struct Cut {              // a block and head group whose pieces lie with the pairs from this one on (pieces 0: none)
+  int32_t tok0, n_tok, unit, pieces;
+};
 struct Plan {
   unsigned long long next;  // item to be taken
   long long line;           // length of the line of work
@@ -93,7 +95,7 @@ struct PromptParams {
   Block* sorted;        // longest first
   long long* line_at;   // where each block starts on the line
   int32_t* block_at;    // first block of each request
-  int32_t* tickets;     // [pairs][16]: pieces that have ended
+  Cut* cuts;            // [pairs]
   float2* part_ml;      // [2 * pairs][512]
   float4* part_o;       // [2 * pairs][512][32]
 };
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
   asm volatile("griddepcontrol.launch_dependents;");  // prompt_kernel may set up
   if (tid == 0) s_most = 1, s_bad = 0, s_bound = 0;
   for (int i = tid; i < 1024; i += kPlanThreads) bins[i] = 0;
-  for (int i = tid; i < p.pairs * 16; i += kPlanThreads) p.tickets[i] = 0;
+  for (int i = tid; i < p.pairs; i += kPlanThreads) p.cuts[i] = Cut{0, 0, 0, 0};
   const int per = kBlock >> p.gshift;  // tokens of a block
   // blocks of each request
   long long before = 0;
@@ -407,7 +409,6 @@ struct Item {        // tiles [t0, t1) of a block and head group; t1 = 0: no mor
   int32_t unit;
   int32_t whole;     // all tiles of the block
   int32_t slot;      // where its partial results go
-  int32_t first_pair, pieces;
 };
 // Tiles that row tile x takes part in: [t0, end), none where end <= t0. (Both CTAs alike.)
 __device__ __forceinline__ int tokens_of(const PromptParams& p, const Item& it, int x) {
@@ -625,6 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();  // the pair's barriers are set up before either CTA signals the other
   tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
   const uint32_t tmem = M.tmem_slot;
   const uint32_t sbase = smem_u32(smem);
@@ -671,9 +673,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             at += b.tiles + kStart;
             if (++unit == p.units) unit = 0, ++blk;
             if (t1 <= t0) continue;
-            it = Item{b.tok0, b.n_tok, b.key0, b.lim0, b.n_keys, t0, t1, u, t0 == 0 && t1 == b.tiles, 2 * pair + (t0 == 0), 0, 0};
-            it.first_pair = pair_of(from);
-            it.pieces = pair_of(from + b.tiles - 1) - it.first_pair + 1;
+            it = Item{b.tok0, b.n_tok, b.key0, b.lim0, b.n_keys, t0, t1, u, t0 == 0 && t1 == b.tiles, 2 * pair + (t0 == 0)};
+            if (t0 == 0 && !it.whole)  // (a pair has one such piece at most, its last)
+              p.cuts[pair] = Cut{b.tok0, b.n_tok, u, pair_of(from + b.tiles - 1) - pair + 1};
             return true;
           }
           return false;
@@ -685,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const long long r = i - g * per;
         const int place = static_cast<int>(r / n);
         const Block b = p.sorted[place];
-        it = Item{b.tok0, b.n_tok, b.key0, b.lim0, b.n_keys, 0, b.tiles, u0 + static_cast<int>(r - static_cast<long long>(place) * n), 1, 0, 0, 1};
+        it = Item{b.tok0, b.n_tok, b.key0, b.lim0, b.n_keys, 0, b.tiles, u0 + static_cast<int>(r - static_cast<long long>(place) * n), 1, 0};
         return true;
       };
       uint32_t n = 0, kg = 0, vg = 0, used = 0;  // items, K tiles, V tiles, parity of each slot's use
@@ -994,7 +996,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool exists = (row >> p.gshift) < n_tok;
       // (rows that do not exist count like the last one that does)
       const int seen = seen_by(p, it, min(token, it.n_tok - 1));
-      const int least_seen = __reduce_min_sync(0xFFFFFFFFu, seen);
+      const int least_seen = __reduce_min_sync(0xFFFFFFFFu, seen), most_seen = __reduce_max_sync(0xFFFFFFFFu, seen);
       float m = -INFINITY, l = 0.0f;
       const int t_first = it.t0 + (halves ? x : 0), t_step = halves ? 2 : 1;
       for (int t = t_first; t < end; t += t_step, ++g) {
@@ -1003,13 +1005,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Keys that the row does not see: their logits are replaced where they lie, 32 keys at a time (a
         // short loop: it runs once or twice an item, and unrolled over the tile it would
         // push the tile's own code out of the instruction cache).
-        const int left = seen - t * kTile, least = least_seen - t * kTile;
+        const int left = seen - t * kTile, least = least_seen - t * kTile, most = most_seen - t * kTile;
         if (least < kTile) {
 #pragma unroll 1
           for (int c = max(0, least) & ~31; c < kTile; c += 32) {
             uint32_t v[32];
-            tmem_ld_32x32b_x32(s_col + c, v);
-            tmem_wait_ld();
+            if (most > c) {  // (else no row of the warp sees any of them)
+              tmem_ld_32x32b_x32(s_col + c, v);
+              tmem_wait_ld();
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = c + i < left ? v[i] : __float_as_uint(hidden);
             tmem_st_32x32b_x32(s_col + c, v);
@@ -1079,6 +1083,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int head = it.unit << p.gshift;
       const long long flat = (static_cast<long long>(it.tok0) + token) * p.n_heads + head + (row & ((1 << p.gshift) - 1));
       const bool some = end > it.t0;  // (the items' tiles, or this half's)
+      // What needs no product is done while the last one runs.
+      Joined j{0.0f, 0.0f, -INFINITY};
+      const bool alone = exists && it.whole && !halves;
+      if (alone) {
+        j = join_prev(p, flat, m, l);
+        if (p.lse) p.lse[flat] = j.lse;
+      }
       bool any_odd = false;
       if (some) {
         if (!wait_here(&M.o_full[x], no & 1, abort_v)) break;
@@ -1129,8 +1140,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       };
       if (writes && n_tok > 0 && it.whole) {
-        Joined j{0.0f, 0.0f, -INFINITY};
-        if (exists) {
+        if (exists && !alone) {
           j = join_prev(p, flat, m, l);
           if (p.lse) p.lse[flat] = j.lse;
         }
@@ -1193,74 +1203,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if (exists) p.part_ml[at] = make_float2(m, some ? l : 0.0f);
-        __threadfence();
-        __syncwarp();
-        int ended = 0;
-        if (lane == 0) ended = atomicAdd(p.tickets + it.first_pair * 16 + 8 * rank + (warp - kSoftWarp0), 1);
-        ended = __shfl_sync(0xFFFFFFFFu, ended, 0);
-        if (ended == it.pieces - 1) {
-          // The last of the pieces of these 32 rows: join them, by their maxima and sums, in
-          // the order of the pieces. A lane's row for the weights, then a row's 128 values
-          // over the lanes, eight rows at a time.
-          __threadfence();
-          auto slot_of = [&](int i) { return static_cast<long long>(2 * (it.first_pair + i) + (i == 0)) * kBlock + r0; };
-          float best = -INFINITY, sum = 0.0f;
-          if (exists) {
-            for (int i = 0; i < it.pieces; ++i) {
-              const float2 ml = __ldcg(p.part_ml + slot_of(i) + lane);
-              if (ml.y != 0.0f) best = fmaxf(best, ml.x);
-            }
-            for (int i = 0; i < it.pieces; ++i) {
-              const float2 ml = __ldcg(p.part_ml + slot_of(i) + lane);
-              if (ml.y != 0.0f) sum += ml.y * exp2_fast(ml.x - best);
-            }
-          }
-          Joined j{0.0f, 0.0f, -INFINITY};
-          if (exists) {
-            j = join_prev(p, flat, best, sum);
-            if (p.lse) p.lse[flat] = j.lse;
-          }
-          const uint32_t rows = __ballot_sync(0xFFFFFFFFu, exists);
-#pragma unroll 1
-          for (int b = 0; b < 32; b += 8) {
-            if (!(rows >> b & 0xFFu)) continue;
-            float4 acc[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r) acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-            for (int i = 0; i < it.pieces; ++i) {
-              const long long s = slot_of(i);
-              float w = -1.0f;  // nothing to add
-              if (exists) {
-                const float2 ml = __ldcg(p.part_ml + s + lane);
-                if (ml.y != 0.0f) w = exp2_fast(ml.x - best);
-              }
-              float4 v[8];
-              float wr[8];
-#pragma unroll
-              for (int r = 0; r < 8; ++r) {
-                wr[r] = __shfl_sync(0xFFFFFFFFu, w, b + r);
-                if (wr[r] != -1.0f) v[r] = __ldcg(p.part_o + (s + b + r) * 32 + lane);
-              }
-#pragma unroll
-              for (int r = 0; r < 8; ++r)
-                if (wr[r] != -1.0f)
-                  acc[r].x += wr[r] * v[r].x, acc[r].y += wr[r] * v[r].y, acc[r].z += wr[r] * v[r].z, acc[r].w += wr[r] * v[r].w;
-            }
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const float f = __shfl_sync(0xFFFFFFFFu, j.f, b + r), fp = __shfl_sync(0xFFFFFFFFu, j.fp, b + r);
-              const long long to = __shfl_sync(0xFFFFFFFFu, flat, b + r);
-              if (!(rows >> (b + r) & 1u)) continue;
-              float4 v = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
-              if (fp != 0.0f) {
-                const float4 was = *reinterpret_cast<const float4*>(p.prev_out + to * kVal + 4 * lane);
-                v.x += fp * was.x, v.y += fp * was.y, v.z += fp * was.z, v.w += fp * was.w;
-              }
-              store4(p, to, 4 * lane, v);
-            }
-          }
-        }
       }
       tc_fence_before();
       __syncwarp();
@@ -1284,6 +1226,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ joining the pieces
+// Rows of the blocks that the line's cuts went through: their pieces' partial results, weighted by their maxima and
+// sums, in the order of the pieces. A warp takes eight rows, a row's 128 values over its lanes. (In
+// prompt_kernel, by the warp that ends last, it saved a launch and cost the tile loop its registers: 16,384 tokens
+// 3.10 ms against 2.95.) 5 x 3 tokens on 9K keys: 76 blocks of up to three pieces, 3 us.
+constexpr int kJoinThreads = 512;
+
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const PromptParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Cut cut = p.cuts[blockIdx.x];
+  const int lane = threadIdx.x & 31, r0 = (blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5)) * 8;
+  const int n = min(8, (cut.n_tok << p.gshift) - r0);  // rows of the block are its tokens' heads
+  if (cut.pieces == 0 || n <= 0) return;
+  auto slot_of = [&](int i) { return static_cast<long long>(2 * (blockIdx.x + i) + (i == 0)) * kBlock + r0; };
+  float best = -INFINITY, sum = 0.0f;  // of row lane mod 8
+  const int mine = min(lane & 7, n - 1);
+  for (int i = 0; i < cut.pieces; ++i) {
+    const float2 ml = p.part_ml[slot_of(i) + mine];
+    if (ml.y != 0.0f) best = fmaxf(best, ml.x);
+  }
+  for (int i = 0; i < cut.pieces; ++i) {
+    const float2 ml = p.part_ml[slot_of(i) + mine];
+    if (ml.y != 0.0f) sum += ml.y * exp2_fast(ml.x - best);
+  }
+  const int row = r0 + mine;
+  const long long flat = (static_cast<long long>(cut.tok0) + (row >> p.gshift)) * p.n_heads + (cut.unit << p.gshift) + (row & ((1 << p.gshift) - 1));
+  const Joined j = join_prev(p, flat, best, sum);
+  __syncwarp();  // (lse may be prev_lse: every lane has read it)
+  if (p.lse && lane < n) p.lse[flat] = j.lse;
+  float4 acc[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+  for (int i = 0; i < cut.pieces; ++i) {
+    const long long s = slot_of(i);
+    const float2 ml = p.part_ml[s + mine];
+    const float w = ml.y != 0.0f ? exp2_fast(ml.x - best) : -1.0f;  // -1: nothing to add, whatever its O holds
+    float4 v[8];
+    float wr[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      wr[r] = r < n ? __shfl_sync(0xFFFFFFFFu, w, r) : -1.0f;
+      if (wr[r] != -1.0f) v[r] = p.part_o[(s + r) * 32 + lane];
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      if (wr[r] != -1.0f) acc[r].x += wr[r] * v[r].x, acc[r].y += wr[r] * v[r].y, acc[r].z += wr[r] * v[r].z, acc[r].w += wr[r] * v[r].w;
+  }
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    if (r >= n) break;
+    const float f = __shfl_sync(0xFFFFFFFFu, j.f, r), fp = __shfl_sync(0xFFFFFFFFu, j.fp, r);
+    const long long to = __shfl_sync(0xFFFFFFFFu, flat, r);
+    float4 v = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
+    if (fp != 0.0f) {
+      const float4 was = *reinterpret_cast<const float4*>(p.prev_out + to * kVal + 4 * lane);
+      v.x += fp * was.x, v.y += fp * was.y, v.z += fp * was.z, v.w += fp * was.w;
+    }
+    store4(p, to, 4 * lane, v);
   }
 }
 
@@ -1324,7 +1328,12 @@ int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, con
   cfg.dynamicSmemBytes = kSmemBytes<D>;
   cfg.stream = st;
   cfg.attrs = &at, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_kernel<D, NEG>, q, k, v, pe, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, prompt_kernel<D, NEG>, q, k, v, pe, p) != cudaSuccess) return SMLA_ERR_CUDA;
+  if (!p.can_cut) return SMLA_OK;
+  cfg.gridDim = dim3(p.pairs, kBlock / (8 * kJoinThreads / 32));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
 template <int D, bool NEG>
@@ -1371,8 +1380,8 @@ size_t layout(PromptParams& p, uint8_t* ws) {
   size_t at = kStatusBytes;
   p.plan = reinterpret_cast<Plan*>(ws + at);
   at += up256(sizeof(Plan));
-  p.tickets = reinterpret_cast<int32_t*>(ws + at);
-  at += up256(static_cast<size_t>(p.pairs) * 16 * 4);
+  p.cuts = reinterpret_cast<Cut*>(ws + at);
+  at += up256(static_cast<size_t>(p.pairs) * sizeof(Cut));
   p.blocks = reinterpret_cast<Block*>(ws + at);
   at += up256(static_cast<size_t>(p.max_blocks) * sizeof(Block));
   p.line_at = reinterpret_cast<long long*>(ws + at);
