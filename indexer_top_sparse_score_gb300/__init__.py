@@ -627,19 +627,22 @@ def rope_table(n, dim=64, *, first=0, base=10000.0, factor=1.0, original=0, beta
     elif out.dtype is not _F32 or out.shape != (n, dim) or not out.is_contiguous():
         raise ValueError("out is a contiguous fp32 [n, dim] table")
     _here(out)
-    rc = lib().smla_rope_table(out.data_ptr(), first, n, dim, base, factor, original, beta_fast, beta_slow, magnitude,
-                               _stream(stream))
-    _check(rc, "smla_rope_table")
+    rc = (_lib or lib()).smla_rope_table(out.data_ptr(), first, n, dim, base, factor, original, beta_fast, beta_slow, magnitude,
+                                         _stream(stream))
+    if rc:
+        raise SmlaError(rc, "smla_rope_table")
     return out
 
 
 def _strides(t, what):
-    """Row and head stride of a bf16 [rows, heads, width] tensor whose heads' values lie next to each other."""
+    """Rows, heads and width of a bf16 tensor whose heads' values lie next to each other, its row and head stride."""
     if t.dtype is not _BF16 or t.dim() != 3 or t.stride(2) != 1:
         raise ValueError(f"{what} is bf16 [rows, heads, width] with a head's values next to each other")
     rows, heads, width = t.shape
-    head = t.stride(1) if heads > 1 else -(-width // 8) * 8
-    return (t.stride(0) if rows > 1 else max(heads * head, -(-width // 8) * 8)), head
+    row, head, _ = t.stride()
+    if heads == 1:
+        head = -(-width // 8) * 8
+    return rows, heads, width, row if rows > 1 else max(heads * head, -(-width // 8) * 8), head
 
 
 def rope_apply(x, positions, table, *, interleaved=True, out=None, ws=None, stream=None):
@@ -647,25 +650,24 @@ def rope_apply(x, positions, table, *, interleaved=True, out=None, ws=None, stre
     instance) by the rows `positions` of table [max_pos, dim], into out (a new tensor
     if None; x itself: in place). Position -1 skips a row (see smla_rope_apply).
     Returns (out, ws)."""
-    L = lib()
     _int32(positions)
-    x_row, x_head = _strides(x, "x")
-    rows, heads, dim = x.shape
+    rows, heads, dim, x_row, x_head = _strides(x, "x")
     if positions.numel() != rows:
         raise ValueError("positions has one entry per row of x")
     if table.dtype is not _F32 or table.dim() != 2 or table.shape[1] != dim or not table.is_contiguous():
         raise ValueError("table is a contiguous fp32 [max_pos, dim] table of x's dim")
     if out is None:
         out = torch.empty((rows, heads, dim), dtype=_BF16, device=x.device)
-    elif out.shape != x.shape:
+    o = _strides(out, "out")
+    if o[:3] != (rows, heads, dim):
         raise ValueError("out has x's shape")
-    o_row, o_head = _strides(out, "out")
     _here(x, positions, table, out, ws)
     if ws is None:
         ws = workspace(STATUS_BYTES, x.device)
-    rc = L.smla_rope_apply(table.data_ptr(), table.shape[0], dim, int(interleaved), rows, positions.data_ptr(), x.data_ptr(),
-                           x_row, x_head, heads, out.data_ptr(), o_row, o_head, ws.data_ptr(), ws.numel(), _stream(stream))
-    _check(rc, "smla_rope_apply")
+    rc = (_lib or lib()).smla_rope_apply(table.data_ptr(), table.shape[0], dim, int(interleaved), rows, positions.data_ptr(), x.data_ptr(),
+                                         x_row, x_head, heads, out.data_ptr(), o[3], o[4], ws.data_ptr(), ws.numel(), _stream(stream))
+    if rc:
+        raise SmlaError(rc, "smla_rope_apply")
     return out, ws
 
 
@@ -675,7 +677,6 @@ def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, p
     cu_rows[b] .. cu_rows[b + 1] - 1, as bf16: latent [rows, 512], pe [rows, 64] and, if wanted or
     given, keys [rows, d_idx] (see smla_cache_read). Given outputs may be strided; rows past
     cu_rows[n] are left as they are. Returns (latent, pe, keys, ws)."""
-    L = lib()
     _int32(page_tables, cu_rows, starts)
     n_seqs, max_pages = page_tables.shape
     if cu_rows.numel() != n_seqs + 1 or (starts is not None and starts.numel() != n_seqs):
@@ -692,10 +693,11 @@ def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, p
     if ws is None:
         ws = workspace(STATUS_BYTES, dev)
     c = make_cache(cache)
-    rc = L.smla_cache_read(ctypes.byref(c), page_tables.data_ptr(), max_pages, n_seqs, cu_rows.data_ptr(), rows, _p(starts),
-                           latent.data_ptr(), strides[0], pe.data_ptr(), strides[1], _p(keys), strides[2], ws.data_ptr(),
-                           ws.numel(), _stream(stream))
-    _check(rc, "smla_cache_read")
+    rc = (_lib or lib()).smla_cache_read(ctypes.byref(c), page_tables.data_ptr(), max_pages, n_seqs, cu_rows.data_ptr(), rows, _p(starts),
+                                         latent.data_ptr(), strides[0], pe.data_ptr(), strides[1], _p(keys), strides[2], ws.data_ptr(),
+                                         ws.numel(), _stream(stream))
+    if rc:
+        raise SmlaError(rc, "smla_cache_read")
     return latent, pe, keys, ws
 
 
@@ -704,6 +706,7 @@ def prompt_workspace_bytes(total_q, total_k, n_seqs, n_heads, n_kv_heads) -> int
 
 
 D_HEAD = 128  # values of an expanded head's v
+_HeadsOfThree = Heads * 3
 
 
 def prompt_fwd(q, k, v, cu_q, cu_k, sm_scale, *, k_pe=None, causal=True, prev_out=None, prev_lse=None, out=None, lse=None,
@@ -713,32 +716,36 @@ def prompt_fwd(q, k, v, cu_q, cu_k, sm_scale, *, k_pe=None, causal=True, prev_ou
     possibly strided; cu_q and cu_k [n + 1] where each request's tokens and keys begin. causal: the
     tokens are the last ones of their keys. prev_out and prev_lse (fp32): the result over other keys, to
     be joined with (see smla_prompt_fwd). Returns (out, lse, ws)."""
-    L = lib()
     _int32(cu_q, cu_k)
     n_seqs = cu_q.numel() - 1
-    tq, heads, d = q.shape
-    tk, kv_heads, dk = k.shape
-    hq, hk, hv = (Heads(t.data_ptr(), *_strides(t, w)) for t, w in ((q, "q"), (k, "k"), (v, "v")))
-    if cu_k.numel() != n_seqs + 1 or dk != (d if k_pe is None else d - 64) or v.shape != (tk, kv_heads, D_HEAD):
+    tq, heads, d, q_row, q_head = _strides(q, "q")
+    tk, kv_heads, dk, k_row, k_head = _strides(k, "k")
+    nv, v_heads, dv, v_row, v_head = _strides(v, "v")
+    if cu_k.numel() != n_seqs + 1 or dk != (d if k_pe is None else d - 64) or nv != tk or v_heads != kv_heads or dv != D_HEAD:
         raise ValueError("k and v are [total_k, kv heads, ..] with k as wide as q (64 less beside k_pe) and v of 128; cu_q and cu_k are alike")
-    pe_row = _bf16_rows(k_pe, tk, 64)
+    pe_row = 0 if k_pe is None else _bf16_rows(k_pe, tk, 64)
     if out is None:
         out = torch.empty((tq, heads, D_HEAD), dtype=out_dtype, device=q.device)
-    if out.dtype not in (_BF16, _F32) or out.numel() != tq * heads * D_HEAD or not out.is_contiguous():
+    fp32 = out.dtype is _F32
+    if not (fp32 or out.dtype is _BF16) or out.numel() != tq * heads * D_HEAD or not out.is_contiguous():
         raise ValueError("out is contiguous bf16 or fp32 [total_q, heads, 128]")
     if lse is None:
         lse = torch.empty((tq, heads), dtype=_F32, device=q.device)
-    _fp32(lse, tq * heads, "lse")
-    _fp32(prev_out, tq * heads * D_HEAD, "prev_out")
-    _fp32(prev_lse, tq * heads, "prev_lse")
+    else:
+        _fp32(lse, tq * heads, "lse")
+    if prev_out is not None or prev_lse is not None:
+        _fp32(prev_out, tq * heads * D_HEAD, "prev_out")
+        _fp32(prev_lse, tq * heads, "prev_lse")
     _here(q, k, v, k_pe, cu_q, cu_k, prev_out, prev_lse, out, lse, ws)
     if ws is None:
         ws = workspace(prompt_workspace_bytes(tq, tk, n_seqs, heads, kv_heads), q.device)
-    rc = L.smla_prompt_fwd(ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv), _p(k_pe), pe_row, tq, tk, n_seqs,
-                           cu_q.data_ptr(), cu_k.data_ptr(), heads, kv_heads, d, int(causal), sm_scale, _p(prev_out),
-                           _p(prev_lse), out.data_ptr(), int(out.dtype is _F32), lse.data_ptr(), ws.data_ptr(), ws.numel(),
-                           _stream(stream))
-    _check(rc, "smla_prompt_fwd")
+    h = _HeadsOfThree((q.data_ptr(), q_row, q_head), (k.data_ptr(), k_row, k_head), (v.data_ptr(), v_row, v_head))
+    at = ctypes.addressof(h)
+    rc = (_lib or lib()).smla_prompt_fwd(at, at + 24, at + 48, _p(k_pe), pe_row, tq, tk, n_seqs, cu_q.data_ptr(), cu_k.data_ptr(), heads,
+                                         kv_heads, d, int(causal), sm_scale, _p(prev_out), _p(prev_lse), out.data_ptr(), int(fp32),
+                                         lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if rc:
+        raise SmlaError(rc, "smla_prompt_fwd")
     return out, lse, ws
 
 

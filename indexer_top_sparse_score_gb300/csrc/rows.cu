@@ -376,8 +376,8 @@ int smla_rope_table(float* cos_sin, int64_t first, int32_t n, int32_t dim, doubl
     } else {
       w /= factor;
     }
-    // w / (2 pi) < 1/6 of a turn
-    p.turns[i] = static_cast<uint64_t>(std::ldexp(static_cast<long double>(w) / 6.283185307179586476925286766559L, 64) + 0.5L);
+    // w / (2 pi) < 1/6 of a turn; off by 2^-52 of it, as w itself may be
+    p.turns[i] = static_cast<uint64_t>(w * (0.15915494309189533577 * 0x1p64));
   }
   const int per = kTableThreads / (dim / 8);
   const long long blocks = (static_cast<long long>(n) + per - 1) / per;
