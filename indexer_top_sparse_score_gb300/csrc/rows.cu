@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
   if (FMT == SMLA_BF16) {
     const int first = p.latent ? 0 : 64, pieces = (p.pe ? 72 : 64) - first;  // of those that are wanted
     if (pieces > 0)
-      each_piece<5, uint4>(pieces, place, [&](long long at, int j) { return __ldg(reinterpret_cast<const uint4*>(p.kv + at * (2 * kDqk)) + first + j); },
+      each_piece<3, uint4>(pieces, place, [&](long long at, int j) { return __ldg(reinterpret_cast<const uint4*>(p.kv + at * (2 * kDqk)) + first + j); },
                            [&](int r, int j, uint4 v, bool there) {
                              j += first;
                              if (j < 64) to_latent(r, j, there ? v : none);
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
       float s;
     };
     if (pieces > 0)
-      each_piece<5, Got>(pieces, place,
+      each_piece<3, Got>(pieces, place,
                          [&](long long at, int j) {
                            return Got{__ldg(reinterpret_cast<const uint4*>(p.kv + at * kDqk) + first + j), __ldg(p.kv_scale + at)};
                          },
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
     };
     const int first = p.latent ? 0 : 32, pieces = (p.pe ? 40 : 32) - first;  // sixteen codes or eight rope values each
     if (pieces > 0)
-      each_piece<5, Got>(pieces, place,
+      each_piece<3, Got>(pieces, place,
                          [&](long long at, int j) {
                            const uint8_t* row = p.kv + at * kTileRow;
                            j += first;
