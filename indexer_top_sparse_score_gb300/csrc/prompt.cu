@@ -437,7 +437,7 @@ __device__ __forceinline__ int seen_by(const PromptParams& p, const Item& it, in
 }
 // A block of one row tile: its key tiles go to both halves of the pipeline in turn, which hold the
 // same rows and are joined at the end. (One row tile alone leaves the tensor cores waiting for its softmax:
-// 5 x 3 tokens of 64 heads on 9K keys, 530 us, against 290 with both halves at work.)
+// 5 x 3 tokens of 64 heads on 9K keys, 531 us, against 322 with both halves at work.)
 __device__ __forceinline__ bool two_halves(const PromptParams& p, const Item& it) { return tokens_of(p, it, 1) <= 0 && it.t1 - it.t0 >= 2; }
 __device__ __forceinline__ int end_of(const PromptParams& p, const Item& it, int x) {
   if (two_halves(p, it)) return it.t1;

@@ -387,6 +387,69 @@ def test_prompt_two_calls_at_once():
     assert all(torch.equal(a, b) for a, b in zip(alone, outs)) and all(smla.read_status(w)[0] == 0 for w in ws)
 
 
+@pytest.mark.parametrize("d,pe,heads,kv_heads,scale", [(192, True, 4, 4, 0.07), (128, False, 8, 1, 0.09), (192, False, 6, 2, -0.07), (128, True, 2, 2, 0.09)])
+def test_prompt_cut_keys_joined_in_place(d, pe, heads, kv_heads, scale):
+    """Few rows whose keys are cut into pieces, joined with an earlier result in its own buffers."""
+    ql, kl = [2, 1, 5], [9000, 3, 17000]
+    c = pc.prompt_case(ql, kl, heads, kv_heads, d, pe, seed=30)
+    g = torch.Generator().manual_seed(31)
+    po, pl = torch.randn(8, heads, 128, generator=g), torch.randn(8, heads, generator=g) + 8
+    pl[4] = float("-inf")
+    ref = pc.prompt_reference(*(None if t is None else t.cuda() for t in c), scale, True, prev=(po.cuda(), pl.cuda()))
+    out, lse = po.cuda(), pl.cuda()
+    _run(*c, scale, True, prev_out=out, prev_lse=lse, out=out, lse=lse)
+    pc.check_prompt(out, lse, ref)
+
+
+@pytest.mark.parametrize("n,length", [(3, 6000), (2, 300), (300, 9000)])
+def test_prompt_cut_keys_and_values_that_are_not_finite(n, length):
+    """Late values that only some tokens see, where key tiles go to two halves of the pipeline and are cut."""
+    q, k, v, pe, cq, ck = pc.prompt_case([n], [length], 2, 1, 192, True, seed=32)
+    for i, j in enumerate((length - 1, length - n // 2, length - n)):  # the last token's, some tokens', every token's
+        v[j, 0, 5 + 40 * i] = [float("nan"), float("inf"), float("-inf")][i]
+    v[length - 1, 0, 45] = float("-inf")  # against the +inf of an earlier key
+    out, lse = _run(q, k, v, pe, cq, ck, 0.07, True)
+    ref = pc.prompt_reference(*(t.cuda() for t in (q, k, torch.nan_to_num(v, 0.0, 0.0, 0.0), pe, cq, ck)), 0.07, True)
+    want = ref[0].clone()
+    pos = torch.arange(n, device="cuda") + length - n
+    for j in sorted({length - 1, length - n // 2, length - n}):
+        bad = ~torch.isfinite(v[j, 0]).cuda()
+        sees = pos >= j
+        add = torch.where(bad, v[j, 0].cuda().double(), 0.0)
+        want[sees] = torch.where(bad, want[sees] + add, want[sees])
+    pc.check_prompt(out, lse, (want, *ref[1:]))
+
+
+def test_prompt_many_requests():
+    """More requests than the plan's threads, most of them short, some empty."""
+    rng = np.random.default_rng(33)
+    ql = rng.integers(0, 4, 2500).tolist()
+    kl = (np.array(ql) + rng.integers(0, 5, 2500)).tolist()
+    c = pc.prompt_case(ql, kl, 2, 1, 192, True, seed=34)
+    out, lse = _run(*c, 0.07, True)
+    pc.check_prompt(out, lse, pc.prompt_reference(*c, 0.07, True))
+
+
+def test_prompt_very_many_keys():
+    """More key tiles than the plan's bins."""
+    c = pc.prompt_case([2, 70], [140000, 300], 1, 1, 192, True, seed=35)
+    out, lse = _run(*c, 0.07, True)
+    pc.check_prompt(out, lse, pc.prompt_reference(*(t.cuda() for t in c), 0.07, True))
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+def test_prompt_results_on_a_16_byte_boundary(fp32):
+    c = pc.prompt_case([70, 300], [90, 300], 3, 3, 192, True, seed=36)
+    t = torch.float32 if fp32 else torch.bfloat16
+    pad = 4 if fp32 else 8
+    raw = torch.full((370 * 3 * 128 + 64,), 3.0, dtype=t, device="cuda")
+    out = raw[pad:pad + 370 * 384].view(370, 3, 128)
+    assert out.data_ptr() % 32 == 16
+    _, lse = _run(*c, 0.07, True, out=out)
+    pc.check_prompt(out, lse, pc.prompt_reference(*c, 0.07, True))
+    assert (raw[:pad] == 3).all() and (raw[pad + 370 * 384:] == 3).all()
+
+
 @pytest.mark.parametrize("kv_dtype", ["bf16", "fp8", "fp8_ds_mla"])
 def test_expanded_equals_latent_attention(kv_dtype):
     """The calls as a prompt step uses them: new rows appended to the cache, context and new rows read back, expanded by
