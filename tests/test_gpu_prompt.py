@@ -182,6 +182,57 @@ def test_cache_read_reports_what_is_not_there():
     assert rc == 5 and (got[0] == 0).all() and torch.equal(got[1], x[0, :512].float())
 
 
+def test_row_calls_on_a_stream_and_in_a_graph():
+    """Captured, replayed on changed inputs and on a side stream: what a plain call gives; the status of a bad replay, and
+    of a good one after it."""
+    c = _filled(6, "fp8", "fp8", 40).to("cuda")
+    tab = torch.tensor([[0, 1, 2], [3, 4, 5]], dtype=torch.int32).cuda()
+    cu, starts = pc.cu([70, 30], "cuda"), torch.tensor([0, 64], dtype=torch.int32).cuda()
+    pos, table = torch.arange(100, dtype=torch.int32, device="cuda"), torch.empty(200, 64, device="cuda")
+    lat, pe, out = (torch.zeros(100, *w, dtype=torch.bfloat16, device="cuda") for w in ((512,), (64,), (1, 64)))
+    ws = [smla.workspace(256) for _ in range(2)]
+
+    def call():
+        smla.rope_table(200, out=table)
+        smla.cache_read(c, tab, cu, 100, starts=starts, latent=lat, pe=pe, ws=ws[0])
+        smla.rope_apply(pe[:, None], pos, table, out=out, ws=ws[1])
+
+    def expect():
+        x, _ = _bf16_rows(c.to("cpu"))
+        b, t = (torch.arange(100) >= 70).long(), torch.cat([torch.arange(70), torch.arange(30)]) + starts.cpu().repeat_interleave(torch.tensor([70, 30]))
+        rows = x[tab.cpu()[b, t // 64].long() * 64 + t % 64]
+        assert torch.equal(lat.cpu(), rows[:, :512]) and torch.equal(pe.cpu(), rows[:, 512:])
+        ref, mag = pc.rotate(rows[:, 512:].double(), table.cpu()[pos.cpu().long()], True)
+        pc.check_rotated(out.cpu()[:, 0], ref, mag)
+
+    call()
+    expect()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    tab.copy_(tab.flip(0).clone())
+    starts.copy_(torch.tensor([100, 3], dtype=torch.int32))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            g.replay()
+    side.synchronize()
+    expect()
+    assert smla.read_status(ws[0])[0] == 0 and smla.read_status(ws[1])[0] == 0
+    held = int(tab[1, 0])
+    tab[1, 0] = 77
+    pos[5] = 200
+    g.replay()
+    assert smla.read_status(ws[0])[0] == 5 and smla.read_status(ws[1])[0] == 5
+    tab[1, 0] = held
+    pos[5] = 5
+    g.replay()
+    torch.cuda.synchronize()
+    expect()
+    assert smla.read_status(ws[0])[0] == 0 and smla.read_status(ws[1])[0] == 0
+
+
 # ---------------------------------------------------------------------------- attention
 def _run(q, k, v, pe, cq, ck, scale, causal, status=0, **kw):
     kv = k._base.cuda() if k._base is not None else None  # keys and values side by side, as they are here
