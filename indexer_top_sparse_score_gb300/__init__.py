@@ -692,7 +692,9 @@ def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, p
     strides = _bf16_rows(latent, rows, D_V), _bf16_rows(pe, rows, D_QK - D_V), _bf16_rows(keys, rows, d)
     if ws is None:
         ws = workspace(STATUS_BYTES, dev)
-    c = make_cache(cache)
+    kv = cache.kv
+    c = PagedCache(kv.data_ptr(), _p(cache.kv_scale), cache.k_idx.data_ptr(), _p(cache.k_idx_scale), *kv.shape[:2], _dtype_code(cache.kv_dtype),
+                   _dtype_code(cache.idx_dtype), d)
     rc = (_lib or lib()).smla_cache_read(ctypes.byref(c), page_tables.data_ptr(), max_pages, n_seqs, cu_rows.data_ptr(), rows, _p(starts),
                                          latent.data_ptr(), strides[0], pe.data_ptr(), strides[1], _p(keys), strides[2], ws.data_ptr(),
                                          ws.numel(), _stream(stream))

@@ -345,9 +345,13 @@ __device__ __forceinline__ bool wait_count(const uint32_t* counter, uint32_t n, 
 }
 template <typename M>
 __device__ __forceinline__ bool wait_scanned(const M& m, uint32_t n, volatile int* abort) {
+  // all four at a look; one after the other where that does not do
+  uint32_t a, b, c, d;
+  asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(smem_u32(m.scanned)) : "memory");
   bool ok = true;
+  if (!__all_sync(0xFFFFFFFFu, min(min(static_cast<int32_t>(a - n), static_cast<int32_t>(b - n)), min(static_cast<int32_t>(c - n), static_cast<int32_t>(d - n))) >= 0))
 #pragma unroll 1
-  for (int i = 0; ok && i < 4; ++i) ok = wait_count(&m.scanned[i], n, abort);
+    for (int i = 0; ok && i < 4; ++i) ok = wait_count(&m.scanned[i], n, abort);
   return ok;
 }
 // true in one thread of the (converged) warp
@@ -487,7 +491,7 @@ struct Meta {
   int odd[2][kVal];     // first key whose value in this column is +inf or NaN, -inf or NaN; noted by the CTA that has the column
   uint32_t odd_item[2]; // the item (from 1 on) that they are of, for each CTA's columns
   uint32_t odd_lock;
-  uint32_t scanned[4];  // V tiles that each of the four warps has looked over
+  alignas(16) uint32_t scanned[4];  // V tiles that each of the four warps has looked over
   uint32_t ended;       // warps (of both CTAs) that are done with what was noted for an item
   uint32_t tmem_slot, status;
   int abort_flag;
@@ -1191,8 +1195,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // (a short loop: the tile loop's code fills the instruction cache, and what runs once an item
         // is fetched anew. 128 columns unrolled took 5,000 cycles, most of them waiting for code.)
         const float f = l != 0.0f ? j.f : 0.0f;
+        const bool plain = !halves && !p.prev_lse && !p.out_fp32 && p.out_sectors;
 #pragma unroll 1
-        for (int c = 0; c < kVal; c += 16) {
+        for (int c = 0; plain && c < kVal; c += 32) {  // the usual case by itself: less code to fetch
+          float v[32];
+          tmem_ld_32x32b_x32(o_col + c, reinterpret_cast<uint32_t*>(v));
+          tmem_wait_ld();
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = l != 0.0f ? bf_pack(v[2 * i] * f, v[2 * i + 1] * f) : 0u;
+          if (exists) {
+            float* to = reinterpret_cast<float*>(static_cast<uint16_t*>(p.out) + flat * kVal + c);
+            store8(to, reinterpret_cast<const float*>(w), true);
+            store8(to + 8, reinterpret_cast<const float*>(w + 8), true);
+          }
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int c = 0; !plain && c < kVal; c += 16) {
           float v[16];
           sums(c, v);
           if (exists) {
