@@ -164,6 +164,7 @@ struct ReadParams {
   uint16_t* keys;
   long long keys_stride;
   uint32_t* status;
+  int32_t first_reports;
 };
 
 // eight e4m3 codes times a scale, as bf16
@@ -193,6 +194,47 @@ __device__ __forceinline__ void report(uint32_t* status) {
   set_status(status, kStatusBounds);
 }
 
+// Pool row of token t of request b; -1: there is none.
+__device__ __forceinline__ long long pool_row(const ReadParams& p, int b, long long t) {
+  if (t < 0 || t / kPage >= p.max_pages) return -1;
+  const int id = __ldg(p.tables + static_cast<long long>(b) * p.max_pages + t / kPage);
+  return id >= 0 && id < p.num_pages ? static_cast<long long>(id) * kPage + t % kPage : -1;
+}
+
+// What no row shows: the list's order and its end.
+__device__ __forceinline__ bool bad_bounds(const ReadParams& p) {
+  bool bad = false;
+  for (int i = threadIdx.x; i <= p.n_seqs; i += kReadThreads) {
+    const int c = __ldg(p.cu + i);
+    bad |= c < 0 || c > p.rows || (i > 0 && c < __ldg(p.cu + i - 1));
+  }
+  return bad;
+}
+
+// Up to kReportedRows rows of kReportedSeqs requests the first block only looks all of them over and writes the
+// status word: no launch to clear it (about 2 us of a 12 us call).
+constexpr int kReportedRows = 1024, kReportedSeqs = 1023;
+
+__device__ __forceinline__ void report_all(const ReadParams& p) {
+  __shared__ int cu[kReportedSeqs + 1];
+  bool bad = bad_bounds(p);
+  for (int i = threadIdx.x; i <= p.n_seqs; i += kReadThreads) cu[i] = __ldg(p.cu + i);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kReportedRows / kReadThreads; ++i) {
+    const int r = threadIdx.x + i * kReadThreads;
+    if (r >= p.rows || r < cu[0] || r >= cu[p.n_seqs]) continue;
+    int lo = 0, hi = p.n_seqs;  // cu[lo] <= r < cu[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cu[mid] <= r) lo = mid; else hi = mid;
+    }
+    bad |= pool_row(p, lo, static_cast<long long>(p.starts ? __ldg(p.starts + lo) : 0) + (r - cu[lo])) < 0;
+  }
+  const int found = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *p.status = found ? kStatusBounds : 0u;
+}
+
 // `pieces` pieces a row of the block's rows: load(place, piece) -> T, store(row, piece, T)
 template <int BATCH, typename T, typename Load, typename Store>
 __device__ __forceinline__ void each_piece(int pieces, const long long* place, Load load, Store store) {
@@ -217,7 +259,11 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
   __shared__ int begun[kReadRows + 1];      // requests that begin at or before the block's first row, then at each row
   __shared__ long long place[kReadRows];    // pool row; -1: zeros; -2: left as it is
   const int tid = threadIdx.x, lane = tid & 31;
-  const int r0 = blockIdx.x * kReadRows;
+  if (p.first_reports && blockIdx.x == 0) {
+    report_all(p);
+    return;
+  }
+  const int r0 = (blockIdx.x - p.first_reports) * kReadRows;
   for (int i = tid; i <= kReadRows; i += kReadThreads) begun[i] = 0;
   __syncthreads();
   int before = 0;
@@ -245,26 +291,14 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
       if (r < first || r >= last) {  // (an order that runs backwards: the counts do not fit)
         bad = true;
       } else {
-        const long long t = static_cast<long long>(p.starts ? __ldg(p.starts + b) : 0) + (r - first);
-        at = -1;
-        if (t >= 0 && t / kPage < p.max_pages) {
-          const int id = __ldg(p.tables + static_cast<long long>(b) * p.max_pages + t / kPage);
-          if (id >= 0 && id < p.num_pages) at = static_cast<long long>(id) * kPage + t % kPage;
-        }
+        at = pool_row(p, b, static_cast<long long>(p.starts ? __ldg(p.starts + b) : 0) + (r - first));
         bad = at < 0;
       }
     }
     place[tid] = at;
-    if (bad) report(p.status);
+    if (bad && !p.first_reports) report(p.status);
   }
-  if (blockIdx.x == 0) {  // what no row shows: the list's order and its end
-    bool bad = false;
-    for (int i = tid; i <= p.n_seqs; i += kReadThreads) {
-      const int c = __ldg(p.cu + i);
-      bad |= c < 0 || c > p.rows || (i > 0 && c < __ldg(p.cu + i - 1));
-    }
-    if (bad) report(p.status);
-  }
+  if (!p.first_reports && blockIdx.x == 0 && bad_bounds(p)) report(p.status);
   __syncthreads();
   const uint4 none = make_uint4(0, 0, 0, 0);
   auto to_latent = [&](int r, int j, uint4 v) { *reinterpret_cast<uint4*>(p.latent + (r0 + r) * p.latent_stride + 8 * j) = v; };
@@ -306,7 +340,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
                          [&](long long at, int j) {
                            const uint8_t* row = p.kv + at * kTileRow;
                            j += first;
-                           return Got{__ldg(reinterpret_cast<const uint4*>(row + (j < 32 ? 0 : 16)) + j),
+                           return Got{__ldg(reinterpret_cast<const uint4*>(row + (j < 32 ? 0 : kTileRopeAt - kDv)) + j),
                                       j < 32 ? __ldg(reinterpret_cast<const float*>(row + kDv) + (j >> 3)) : 1.0f};
                          },
                          [&](int r, int j, Got v, bool there) {
@@ -439,16 +473,19 @@ int smla_cache_read(const smla_paged_cache* cache, const int32_t* page_tables, i
   p.pe = static_cast<uint16_t*>(pe), p.pe_stride = pe_stride;
   p.keys = static_cast<uint16_t*>(keys), p.keys_stride = keys_stride;
   p.status = static_cast<uint32_t*>(workspace);
-  clear_kernel<<<1, 1, 0, st>>>(p.status);
-  if (launched()) return SMLA_ERR_CUDA;
+  p.first_reports = rows <= kReportedRows && n_seqs <= kReportedSeqs;
+  if (!p.first_reports) {
+    clear_kernel<<<1, 1, 0, st>>>(p.status);
+    if (launched()) return SMLA_ERR_CUDA;
+  }
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kReadRows - 1) / kReadRows));
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kReadRows - 1) / kReadRows) + p.first_reports);
   cfg.blockDim = dim3(kReadThreads);
   cfg.stream = st;
-  cfg.attrs = &at, cfg.numAttrs = 1;
+  cfg.attrs = &at, cfg.numAttrs = p.first_reports ? 0 : 1;
   const int fmt = latent || pe ? cache->kv_dtype : SMLA_BF16;  // (keys alone: no latent pieces)
   const auto kernel = fmt == SMLA_BF16 ? cache_read_kernel<SMLA_BF16> : fmt == SMLA_FP8_E4M3 ? cache_read_kernel<SMLA_FP8_E4M3> : cache_read_kernel<SMLA_FP8_DS_MLA>;
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;

@@ -182,6 +182,28 @@ def test_cache_read_reports_what_is_not_there():
     assert rc == 5 and (got[0] == 0).all() and torch.equal(got[1], x[0, :512].float())
 
 
+@pytest.mark.parametrize("n,length", [(1, 1000), (1, 1100), (1200, 1), (40, 25), (41, 25)])
+def test_cache_read_reports_the_same_in_small_and_large_calls(n, length):
+    """One missing page anywhere among the rows; a list that ends past the outputs."""
+    c = _filled(30, "bf16", "fp8", 41).to("cuda")
+    width = -(-length // 64)
+    tables = lambda: (torch.arange(n * width, dtype=torch.int32) % 30).view(n, width)  # noqa: E731
+    cu = pc.cu([length] * n)
+    for at in (0, n * width // 2, n * width - 1):
+        tab = tables()
+        tab.view(-1)[at] = 30
+        lat, _, _, ws = smla.cache_read(c, tab.cuda(), cu.cuda(), n * length)
+        assert smla.read_status(ws)[0] == 5
+        b, p = at // width, at % width
+        gone = slice(b * length + 64 * p, b * length + min(length, 64 * (p + 1)))
+        assert (lat[gone] == 0).all() and (lat != 0).any(1).sum() == n * length - (gone.stop - gone.start)
+    lat, _, _, ws = smla.cache_read(c, tables().cuda(), cu.cuda(), n * length, ws=ws)
+    assert smla.read_status(ws)[0] == 0 and (lat != 0).any(1).all()
+    cu[n] += 1
+    _, _, _, ws = smla.cache_read(c, tables().cuda(), cu.cuda(), n * length, ws=ws)
+    assert smla.read_status(ws)[0] == 5
+
+
 def test_row_calls_on_a_stream_and_in_a_graph():
     """Captured, replayed on changed inputs and on a side stream: what a plain call gives; the status of a bad replay, and
     of a good one after it."""
