@@ -121,7 +121,7 @@ typedef struct smla_heads {
  * Operands are bf16, sums, maxima and partial results fp32; probabilities are rounded
  * to bf16 for their product with V, the sum of them is not. Keys and values that a row does
  * not see never reach it, whatever they hold; a value that is not finite reaches the rows that
- * see it.
+ * see it (an infinity as NaN where its probability is zero in fp32).
  * Supported: d_qk 128 and 192; 1 <= n_heads <= 1024, a multiple of n_kv_heads. sm_scale is finite.
  * Workspace: the returned size (status word, the plan of the work, and partial results of
  * rows whose keys are cut: two pieces of 133 KB for each SM). The size is that of the current device.

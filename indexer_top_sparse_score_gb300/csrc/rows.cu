@@ -41,6 +41,8 @@ __device__ __forceinline__ void cos_sin_of(uint64_t angle, float& c, float& s) {
 
 // A thread keeps four pairs and walks the rows: position * turns wraps at whole
 // turns by itself in 64-bit integers, so the angle needs no reduction and goes on by additions.
+// Bound by memory: 1,048,576 positions of 64 values, 268 MB written in 45 us, 6.0 TB/s (55 us with
+// sincospif, by instructions); 8,192 positions in 2.4 us.
 __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_constant__ TableParams p) {
   const int groups = p.dim / 8, half = p.dim / 2;  // groups of four pairs
   const int g = threadIdx.x % groups, r0 = threadIdx.x / groups, per = kTableThreads / groups;
@@ -88,7 +90,9 @@ struct RopeParams {
 };
 
 // A thread takes eight values (four pairs) of up to four heads of one row, all requested
-// before the row's position and angles, which are two latencies away.
+// before the row's position and angles, which are two latencies away. Bound by memory: 8,192 rows of 64
+// heads (64 of 192 values each), 136 MB in 26.7 us, 5.1 TB/s. On cold caches with two / four / eight heads
+// a thread 32.4 / 28.3 / 28.3 us, in blocks of 256 threads 29.3; 128 rows 2.4 us.
 __global__ void __launch_bounds__(kRopeThreads) rope_apply_kernel(const RopeParams p) {
   if (p.first_reports && blockIdx.x == 0) {
     report_rows(p.rows, p.status, [&](int r) {
@@ -183,7 +187,10 @@ __device__ __forceinline__ uint4 widen8(uint2 c, float s) {
 
 // A block finds the pool rows of 32 output rows: every request's first row is loaded once
 // and counted against them (one latency, no search), then the rows' pieces of 16 bytes of the pool
-// go round the block's threads, each thread's requested together.
+// go round the block's threads, each thread's requested together. Bound by memory: 131,072 FP8 rows, 227 MB in
+// 41 us, 5.6 TB/s; 37 ragged requests of BF16 rows and keys, 102 MB in 22.6 us; few rows by four latencies (600
+// rows: 4.5 us). Batches of three / five / nine pieces a thread: 43.6 / 51.9 / 51.9 us for the FP8 rows on cold
+// caches (registers), blocks of 16 rows 46.8, of 128 threads 44.7 (both with batches of five).
 // Programmatic launch after clear_kernel: only who reports waits for it.
 __global__ void clear_kernel(uint32_t* status) {
   asm volatile("griddepcontrol.launch_dependents;");
