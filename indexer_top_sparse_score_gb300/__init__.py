@@ -604,8 +604,8 @@ def shared_prefix_fwd(cache, page_tables, seq_lens, max_seq_len, shared_len, q_p
 
 
 # ---------------------------------------------------------------------------- expanded prompts
-def _here(*tensors):
-    """The kernels run on the current device's stream: every tensor has to be there."""
+def _stream_of(stream, *tensors):
+    """The stream's handle. The kernels run on the current device: every tensor has to be there."""
     now = -2
     for t in tensors:
         if t is not None:
@@ -614,6 +614,7 @@ def _here(*tensors):
                 if at < 0 or now >= 0 or at != torch.cuda.current_device():
                     raise ValueError("tensors are on the current CUDA device (torch.cuda.device sets it)")
                 now = at
+    return _raw_stream(now) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def rope_table(n, dim=64, *, first=0, base=10000.0, factor=1.0, original=0, beta_fast=32.0, beta_slow=1.0,
@@ -626,9 +627,8 @@ def rope_table(n, dim=64, *, first=0, base=10000.0, factor=1.0, original=0, beta
         out = torch.empty((n, dim), dtype=_F32, device="cuda")
     elif out.dtype is not _F32 or out.shape != (n, dim) or not out.is_contiguous():
         raise ValueError("out is a contiguous fp32 [n, dim] table")
-    _here(out)
-    rc = (_lib or lib()).smla_rope_table(out.data_ptr(), first, n, dim, base, factor, original, beta_fast, beta_slow, magnitude,
-                                         _stream(stream))
+    at = _stream_of(stream, out)
+    rc = (_lib or lib()).smla_rope_table(out.data_ptr(), first, n, dim, base, factor, original, beta_fast, beta_slow, magnitude, at)
     if rc:
         raise SmlaError(rc, "smla_rope_table")
     return out
@@ -636,10 +636,12 @@ def rope_table(n, dim=64, *, first=0, base=10000.0, factor=1.0, original=0, beta
 
 def _strides(t, what):
     """Rows, heads and width of a bf16 tensor whose heads' values lie next to each other, its row and head stride."""
-    if t.dtype is not _BF16 or t.dim() != 3 or t.stride(2) != 1:
+    if t.dtype is not _BF16 or t.dim() != 3:
         raise ValueError(f"{what} is bf16 [rows, heads, width] with a head's values next to each other")
     rows, heads, width = t.shape
-    row, head, _ = t.stride()
+    row, head, unit = t.stride()
+    if unit != 1 and width > 1:
+        raise ValueError(f"{what} is bf16 [rows, heads, width] with a head's values next to each other")
     if heads == 1:
         head = -(-width // 8) * 8
     return rows, heads, width, row if rows > 1 else max(heads * head, -(-width // 8) * 8), head
@@ -661,11 +663,11 @@ def rope_apply(x, positions, table, *, interleaved=True, out=None, ws=None, stre
     o = _strides(out, "out")
     if o[:3] != (rows, heads, dim):
         raise ValueError("out has x's shape")
-    _here(x, positions, table, out, ws)
+    at = _stream_of(stream, x, positions, table, out, ws)
     if ws is None:
         ws = workspace(STATUS_BYTES, x.device)
     rc = (_lib or lib()).smla_rope_apply(table.data_ptr(), table.shape[0], dim, int(interleaved), rows, positions.data_ptr(), x.data_ptr(),
-                                         x_row, x_head, heads, out.data_ptr(), o[3], o[4], ws.data_ptr(), ws.numel(), _stream(stream))
+                                         x_row, x_head, heads, out.data_ptr(), o[3], o[4], ws.data_ptr(), ws.numel(), at)
     if rc:
         raise SmlaError(rc, "smla_rope_apply")
     return out, ws
@@ -681,7 +683,7 @@ def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, p
     n_seqs, max_pages = page_tables.shape
     if cu_rows.numel() != n_seqs + 1 or (starts is not None and starts.numel() != n_seqs):
         raise ValueError("cu_rows has n_seqs + 1 entries, starts n_seqs")
-    _here(cache.kv, cache.kv_scale, cache.k_idx, cache.k_idx_scale, page_tables, cu_rows, starts, latent, pe, keys, ws)
+    at = _stream_of(stream, cache.kv, cache.kv_scale, cache.k_idx, cache.k_idx_scale, page_tables, cu_rows, starts, latent, pe, keys, ws)
     dev, d = page_tables.device, cache.k_idx.shape[-1]
     if latent is None:
         latent = torch.empty((rows, D_V), dtype=_BF16, device=dev)
@@ -697,7 +699,7 @@ def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, p
                    _dtype_code(cache.idx_dtype), d)
     rc = (_lib or lib()).smla_cache_read(ctypes.byref(c), page_tables.data_ptr(), max_pages, n_seqs, cu_rows.data_ptr(), rows, _p(starts),
                                          latent.data_ptr(), strides[0], pe.data_ptr(), strides[1], _p(keys), strides[2], ws.data_ptr(),
-                                         ws.numel(), _stream(stream))
+                                         ws.numel(), at)
     if rc:
         raise SmlaError(rc, "smla_cache_read")
     return latent, pe, keys, ws
@@ -738,14 +740,14 @@ def prompt_fwd(q, k, v, cu_q, cu_k, sm_scale, *, k_pe=None, causal=True, prev_ou
     if prev_out is not None or prev_lse is not None:
         _fp32(prev_out, tq * heads * D_HEAD, "prev_out")
         _fp32(prev_lse, tq * heads, "prev_lse")
-    _here(q, k, v, k_pe, cu_q, cu_k, prev_out, prev_lse, out, lse, ws)
+    handle = _stream_of(stream, q, k, v, k_pe, cu_q, cu_k, prev_out, prev_lse, out, lse, ws)
     if ws is None:
         ws = workspace(prompt_workspace_bytes(tq, tk, n_seqs, heads, kv_heads), q.device)
     h = _HeadsOfThree((q.data_ptr(), q_row, q_head), (k.data_ptr(), k_row, k_head), (v.data_ptr(), v_row, v_head))
     at = ctypes.addressof(h)
     rc = (_lib or lib()).smla_prompt_fwd(at, at + 24, at + 48, _p(k_pe), pe_row, tq, tk, n_seqs, cu_q.data_ptr(), cu_k.data_ptr(), heads,
                                          kv_heads, d, int(causal), sm_scale, _p(prev_out), _p(prev_lse), out.data_ptr(), int(fp32),
-                                         lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+                                         lse.data_ptr(), ws.data_ptr(), ws.numel(), handle)
     if rc:
         raise SmlaError(rc, "smla_prompt_fwd")
     return out, lse, ws
