@@ -1122,7 +1122,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             pk[i >> 1] = bf_pack(e.x, e.y);
           }
           tmem_st_x16(s_col + 16 * h, pk);
-          if (h == 1) {  // the product with the first 64 keys may begin
+          // The product with the first 64 keys may begin. (Handed over after 32, 64 or 96 keys, in quarters, at once: 8,192
+          // tokens of 64 heads on 8 take 719, 661, 684, 709 and 735 us.)
+          if (h == 1) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
