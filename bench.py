@@ -64,7 +64,7 @@ def kernel_sources_digest():
     its C header, each file hashed as its repository path then its bytes, in path
     order. (The serving calls' sources are not on that path.)"""
     csrc = os.path.join("indexer_top_sparse_score_gb300", "csrc")
-    serving = ("prefix.cu", "prompt.cu", "rows.cu", "rows.cuh", "serve.cu", "serve.h")
+    serving = ("prefix.cu", "prompt.cu", "prompt_layout.h", "rows.cu", "rows.cuh", "serve.cu", "serve.h")
     rel = sorted([os.path.join(csrc, f) for f in os.listdir(os.path.join(ROOT, csrc))
                   if os.path.isfile(os.path.join(ROOT, csrc, f)) and f not in serving]
                  + [os.path.join("include", "smla.h")])

@@ -48,15 +48,17 @@
 #include <mutex>
 
 #include "../../include/smla_prompt.h"
+#include "prompt_layout.h"
 #include "rows.cuh"
 
 namespace smla {
 namespace {
 
-constexpr int kVal = 128;   // values of a head's v
+constexpr int kVal = kPromptVal;
 constexpr int kPe = 64;
 constexpr int kTile = 128;  // rows of a row tile in each CTA, keys of a key tile
-constexpr int kBlock = 4 * kTile;
+constexpr int kBlock = kPromptRows;
+static_assert(kBlock == 4 * kTile, "two row tiles of both CTAs");
 constexpr int kQChunk = kTile * 128;  // bytes of 128 rows x 64 values
 constexpr int kSlot = 64 * 128;       // of 64 keys x 64 values
 constexpr int kAhead = 8;             // tiles of the ring at most, and barriers for them
@@ -67,22 +69,6 @@ constexpr int kStart = 2;       // a piece's start and end on the line of work, 
 constexpr int kLongTiles = 8;   // blocks of no more tiles are never cut
 constexpr int kDirectSeqs = 8;  // requests that a thread looks through
 constexpr uint32_t kColS = 0, kColO = 256;
-
-struct Block {      // of the plan
-  int32_t tok0, n_tok;    // rows of q
-  int32_t key0, lim0;     // first key's row; keys that its first token sees (causal: may be <= 0)
-  int32_t n_keys, tiles;  // keys that its last token sees; tiles of them, at least one
-  int32_t pad[2];
-};
-struct Cut {              // a block and head group whose pieces lie with the pairs from this one on (pieces 0: none)
-  int32_t tok0, n_tok, unit, pieces;
-};
-struct Plan {
-  unsigned long long next;  // item to be taken
-  long long line;           // length of the line of work
-  int32_t n_blocks, even;   // even: the line is cut evenly
-  int32_t pairs;            // stretches of the line
-};
 
 struct PromptParams {
   int32_t total_q, total_k, n_seqs;
@@ -107,7 +93,7 @@ struct PromptParams {
   int32_t* block_at;    // first block of each request
   Cut* cuts;            // [pairs]
   float2* part_ml;      // [2 * pairs][512]
-  float4* part_o;       // [2 * pairs][512][32]
+  float4* part_o;       // [2 * pairs][512][32], on a 32-byte boundary
 };
 
 // ------------------------------------------------------------------ the plan
@@ -1445,8 +1431,6 @@ int pairs_of_device() {
   return known[dev];
 }
 
-size_t up256(size_t b) { return (b + 255) / 256 * 256; }
-
 // Sizes that follow from the shape, and the workspace's parts; its bytes.
 size_t layout(PromptParams& p, uint8_t* ws) {
   p.gshift = 0;
@@ -1457,26 +1441,16 @@ size_t layout(PromptParams& p, uint8_t* ws) {
   p.can_cut = p.total_k > kLongTiles * kTile;
   // A small call needs no plan: 1 x 100 tokens of 16 heads, 9.5 us of device time against 14.3.
   p.direct = !p.can_cut && p.n_seqs <= kDirectSeqs && static_cast<int64_t>(p.max_blocks) * p.units <= p.pairs;
-  size_t at = kStatusBytes;
-  p.plan = reinterpret_cast<Plan*>(ws + at);
-  at += up256(sizeof(Plan));
-  p.cuts = reinterpret_cast<Cut*>(ws + at);
-  at += up256(static_cast<size_t>(p.pairs) * sizeof(Cut));
-  p.blocks = reinterpret_cast<Block*>(ws + at);
-  at += up256(static_cast<size_t>(p.max_blocks) * sizeof(Block));
-  p.line_at = reinterpret_cast<long long*>(ws + at);
-  at += up256(static_cast<size_t>(p.max_blocks) * 8);
-  p.sorted = reinterpret_cast<Block*>(ws + at);
-  at += up256(static_cast<size_t>(p.max_blocks) * sizeof(Block));
-  p.block_at = reinterpret_cast<int32_t*>(ws + at);
-  at += up256((static_cast<size_t>(p.n_seqs) + 1) * 4);
-  if (p.can_cut) {
-    p.part_ml = reinterpret_cast<float2*>(ws + at);
-    at += static_cast<size_t>(p.pairs) * 2 * kBlock * 8;
-    p.part_o = reinterpret_cast<float4*>(ws + at);
-    at += static_cast<size_t>(p.pairs) * 2 * kBlock * kVal * 4;
-  }
-  return at;
+  const PromptParts w = prompt_parts(reinterpret_cast<uintptr_t>(ws), kStatusBytes, p.max_blocks, p.pairs, p.n_seqs, p.can_cut != 0);
+  p.plan = reinterpret_cast<Plan*>(ws + w.plan);
+  p.cuts = reinterpret_cast<Cut*>(ws + w.cuts);
+  p.blocks = reinterpret_cast<Block*>(ws + w.blocks);
+  p.line_at = reinterpret_cast<long long*>(ws + w.line_at);
+  p.sorted = reinterpret_cast<Block*>(ws + w.sorted);
+  p.block_at = reinterpret_cast<int32_t*>(ws + w.block_at);
+  p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
+  p.part_o = reinterpret_cast<float4*>(ws + w.part_o);
+  return w.bytes;
 }
 
 bool sizes_ok(const PromptParams& p) {  // 32-bit rows and counts
