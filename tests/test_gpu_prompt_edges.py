@@ -4,6 +4,7 @@ import torch
 
 import indexer_top_sparse_score_gb300 as smla
 import prompt_common as pc
+import prompt_tiles as pt
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,67 @@ def test_prompt_workspace_on_any_16_byte_boundary(lead, ql, kl):
     assert smla.read_status(ws)[0] == 0
     assert torch.equal(got, out) and torch.equal(glse, lse)
     assert (raw[:lead] == 171).all() and (raw[lead + need:] == 171).all()
+
+
+# ---------------------------------------------------------------------------- bad bounds
+def _guarded(total_q, total_k, n, heads, kv_heads):
+    need = smla.prompt_workspace_bytes(total_q, total_k, n, heads, kv_heads)
+    raw = torch.full((need + 8192,), 171, dtype=torch.uint8, device="cuda")
+    return raw, raw[4096:4096 + need]
+
+
+def _check_bad(cq, ck, total_q, total_k, heads=2, repeated=False, seed=80):
+    """Valid requests keep their results, nothing else is written, neither outputs nor memory around the workspace."""
+    q, k, v, pe, _, _ = (t.cuda() for t in pc.prompt_case([total_q], [total_k], heads, heads, 192, True, seed=seed))
+    raw, ws = _guarded(total_q, total_k, len(cq) - 1, heads, heads)
+    out, lse = torch.full((total_q, heads, 128), 7.0, device="cuda"), torch.full((total_q, heads), 7.0, device="cuda")
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    smla.prompt_fwd(q, k, v, i(cq), i(ck), 0.07, k_pe=pe, out=out, lse=lse, ws=ws)
+    assert smla.read_status(ws)[0] == 5
+    assert (raw[:4096] == 171).all() and (raw[-4096:] == 171).all()
+    written, done = torch.zeros(total_q, dtype=torch.bool), set()
+    for a, b, c, d in zip(cq, cq[1:], ck, ck[1:]):
+        if not (0 <= a <= b <= total_q and 0 <= c <= d <= total_k) or a == b:
+            continue
+        written[a:b] = True
+        if (a, b, c, d) in done:
+            continue
+        done.add((a, b, c, d))
+        ref = pc.prompt_reference(q[a:b], k[c:d], v[c:d], pe[c:d], pc.cu([b - a]), pc.cu([d - c]), 0.07, True)
+        pt.check_rows(out[a:b], lse[a:b], ref)
+    assert (out[~written] == 7).all() and (lse[~written] == 7).all()
+    ok = smla.prompt_fwd(q, k, v, i([0, total_q]), i([0, total_k]), 0.07, k_pe=pe, ws=ws)  # the workspace is as good as new
+    assert smla.read_status(ws)[0] == 0
+    ref = pc.prompt_reference(q, k, v, pe, pc.cu([total_q]), pc.cu([total_k]), 0.07, True)
+    pt.check_rows(ok[0], ok[1], ref)
+
+
+@pytest.mark.parametrize("bad", ["backwards", "negative", "past q", "past k", "keys backwards", "none"])
+@pytest.mark.parametrize("n,q_len,k_len", [(12, 9, 40), (10, 30, 1100), (3, 2, 9000), (1030, 2, 3)])
+def test_prompt_bad_bounds_in_a_plan(bad, n, q_len, k_len):
+    """More than eight requests, more than 1,024 keys (cut evenly or not), more requests than the plan's threads."""
+    cq, ck = [q_len * i for i in range(n + 1)], [k_len * i for i in range(n + 1)]
+    tq, tk = cq[-1], ck[-1]
+    if bad == "backwards":
+        cq[n // 2] = cq[n // 2 - 1] - 1 if n > 3 else -1
+    elif bad == "negative":
+        cq[0], ck[0] = -5, -1
+    elif bad == "past q":
+        cq[n] = tq + 1
+    elif bad == "past k":
+        ck[n] = tk + 1
+    elif bad == "keys backwards":
+        ck[1] = ck[2] + 1
+    else:
+        cq = [-1 - i for i in range(n + 1)]
+    # (a bound that is moved lengthens a neighbour or makes requests claim the same rows: those are left out by their bounds)
+    if bad == "backwards" and n > 3:
+        cq[n // 2] = tq + 5  # past the end for one request, backwards for the next
+    _check_bad(cq, ck, tq, tk)
+
+
+@pytest.mark.parametrize("total_q,total_k,n", [(1500, 700, 9), (1500, 2000, 25), (1100, 9000, 25), (1100, 2000, 1400)])
+def test_prompt_bounds_that_overlap_make_more_blocks_than_there_is_room_for(total_q, total_k, n):
+    """0 .. total again and again, every other request backwards."""
+    cq, ck = [total_q * (i % 2) for i in range(n + 1)], [total_k * (i % 2) for i in range(n + 1)]
+    _check_bad(cq, ck, total_q, total_k)
