@@ -116,12 +116,13 @@ typedef struct smla_heads {
  *          (where that is fp32) and prev_lse may be lse.
  *   out    [total_q][n_heads][128] bf16, or fp32 (out_fp32 != 0: to be joined by a later call
  *          without rounding in between).
- *   lse    [total_q][n_heads] fp32 natural log, or NULL. A row that sees no key has o = 0 and
- *          lse = -inf.
+ *   lse    [total_q][n_heads] fp32 natural log, or NULL. A row that sees no key, or none whose logit is above
+ *          -inf, has o = 0 and lse = -inf.
  * Operands are bf16, sums, maxima and partial results fp32; probabilities are rounded
  * to bf16 for their product with V, the sum of them is not. Keys and values that a row does
  * not see never reach it, whatever they hold; a value that is not finite reaches the rows that
- * see it (an infinity as NaN where its probability is zero in fp32).
+ * see it, however small its probability: NaN as NaN, an infinity as itself or, where its probability or a joined
+ * part's weight is zero in fp32, as either (how a request's keys are cut decides).
  * Supported: d_qk 128 and 192; 1 <= n_heads <= 1024, a multiple of n_kv_heads. sm_scale is finite.
  * Workspace: the returned size (status word, the plan of the work, and partial results of
  * rows whose keys are cut: two pieces of 133 KB for each SM). The size is that of the current device.

@@ -1179,7 +1179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_ld_32x32b_x16(o_col + kVal + c, reinterpret_cast<uint32_t*>(u));
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = (w0 != 0.0f ? w0 * v[i] : 0.0f) + (w1 != 0.0f ? w1 * u[i] : 0.0f);
+          for (int i = 0; i < 16; ++i) v[i] = w0 * v[i] + w1 * u[i];  // (both halves have tiles; a weight of 0 keeps a NaN)
         } else {
           tmem_wait_ld();
         }
@@ -1229,7 +1229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (any_odd && exists) {
+        if (any_odd && exists && l != 0.0f) {
           for (int c = 0; c < kVal; ++c) {
             const float o = odd_of(M, n + 1, c, seen);
             if (o == 0.0f) continue;

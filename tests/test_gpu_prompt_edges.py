@@ -33,6 +33,60 @@ def test_prompt_workspace_on_any_16_byte_boundary(lead, ql, kl):
     assert (raw[:lead] == 171).all() and (raw[lead + need:] == 171).all()
 
 
+# ---------------------------------------------------------------------------- values that are not finite
+def _levels(nk, low, size=128, even=True, first=None):
+    """Logits by key: `low` in every other tile of 128 keys, or in the keys before `first`; 0 elsewhere."""
+    j = torch.arange(nk)
+    hit = j < first if first is not None else ((j // size) % 2 == 0) == even
+    return torch.where(hit, low, 0.0)
+
+
+def _level_case(nq, level, seed):
+    """One head whose logits with a scale of 1 are `level`, whatever the query; random values."""
+    g = torch.Generator().manual_seed(seed)
+    nk = level.numel()
+    q, k = torch.zeros(nq, 1, 128, dtype=torch.bfloat16), torch.zeros(nk, 1, 128, dtype=torch.bfloat16)
+    q[:, 0, 0], k[:, 0, 0] = 1.0, level.to(torch.bfloat16)
+    return q.cuda(), k.cuda(), torch.randn(nk, 1, 128, generator=g).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("low", [-300.0, -float("inf")])
+@pytest.mark.parametrize("nq,nk,even,first", [
+    (100, 512, True, None), (100, 512, False, None), (1, 1100, True, None),   # key tiles in two halves of the pipeline
+    (300, 512, True, None), (300, 512, True, 200)])                           # two row tiles
+def test_prompt_values_whose_weight_vanishes(nq, nk, even, first, low):
+    """A NaN or an infinity of V at a key that every row sees reaches every row, however small the key's probability."""
+    level = _levels(nk, low, even=even, first=first)
+    q, k, v = _level_case(nq, level, 70)
+    odd = int((level < 0).nonzero()[0])
+    v[odd, 0, 3], v[odd + 1, 0, 7], v[odd + 2, 0, 9] = float("nan"), float("inf"), -float("inf")
+    out, lse, ws = smla.prompt_fwd(q, k, v.cuda(), pc.cu([nq], "cuda"), pc.cu([nk], "cuda"), 1.0, causal=False)
+    assert smla.read_status(ws)[0] == 0
+    live = level == 0
+    assert out[:, 0, 3].isnan().all()
+    assert not torch.isfinite(out[:, 0, [7, 9]]).any()
+    rest = [c for c in range(128) if c not in (3, 7, 9)]
+    want = v[live, 0].double().mean(0)[rest]
+    mag = v[live, 0].double().abs().mean(0)[rest]
+    # equal probabilities: exact but for the sums (2^-23 a key of the mean magnitude) and bf16
+    assert ((out[:, 0, rest].double().cpu() - want).abs() <= pc.BF16 * want.abs() + 2 * pc.FP32 * nk * mag).all()
+    assert ((lse.cpu() - float(live.sum().double().log())).abs() <= 2.0 ** -16).all()
+
+
+def test_prompt_rows_whose_logits_are_all_minus_infinity():
+    """They are as rows that see nothing, whole or cut, alone or joined, whatever V holds."""
+    for nq, nk, odd in ((100, 300, 290), (300, 300, 5), (300, 300, 299), (2, 20000, 9), (2, 20000, 19999)):
+        q, k, v = _level_case(nq, torch.full((nk,), -float("inf")), 73)
+        v[odd, 0, 11] = float("nan")
+        for causal in (False, True):
+            out, lse, ws = smla.prompt_fwd(q, k, v.cuda(), pc.cu([nq], "cuda"), pc.cu([nk], "cuda"), 1.0, causal=causal)
+            assert smla.read_status(ws)[0] == 0 and (out == 0).all() and lse.isneginf().all()
+        po, pl = torch.randn(nq, 1, 128, device="cuda"), torch.zeros(nq, 1, device="cuda")
+        out, lse, ws = smla.prompt_fwd(q, k, v.cuda(), pc.cu([nq], "cuda"), pc.cu([nk], "cuda"), 1.0, causal=False, prev_out=po, prev_lse=pl,
+                                       out_dtype=torch.float32)
+        assert torch.equal(out, po) and torch.equal(lse, pl)
+
+
 # ---------------------------------------------------------------------------- bad bounds
 def _guarded(total_q, total_k, n, heads, kv_heads):
     need = smla.prompt_workspace_bytes(total_q, total_k, n, heads, kv_heads)
