@@ -1263,7 +1263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (o != 0.0f) part[c] += o;
           }
         }
-        if (exists) p.part_ml[at] = make_float2(m, some ? l : 0.0f);
+        if (exists) p.part_ml[at] = make_float2(m, some ? l : -1.0f);  // -1: no tile, no values
       }
       tc_fence_before();
       __syncwarp();
@@ -1308,11 +1308,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PromptParams p
   const int mine = min(lane & 7, n - 1);
   for (int i = 0; i < cut.pieces; ++i) {
     const float2 ml = p.part_ml[slot_of(i) + mine];
-    if (ml.y != 0.0f) best = fmaxf(best, ml.x);
+    if (!(ml.y <= 0.0f)) best = fmaxf(best, ml.x);
   }
   for (int i = 0; i < cut.pieces; ++i) {
     const float2 ml = p.part_ml[slot_of(i) + mine];
-    if (ml.y != 0.0f) sum += ml.y * exp2_fast(ml.x - best);
+    if (!(ml.y <= 0.0f)) sum += ml.y * exp2_fast(ml.x - best);
   }
   const int row = r0 + mine;
   const long long flat = (static_cast<long long>(cut.tok0) + (row >> p.gshift)) * p.n_heads + (cut.unit << p.gshift) + (row & ((1 << p.gshift) - 1));
@@ -1326,7 +1326,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PromptParams p
   for (int i = 0; i < cut.pieces; ++i) {
     const long long s = slot_of(i);
     const float2 ml = p.part_ml[s + mine];
-    const float w = ml.y != 0.0f ? exp2_fast(ml.x - best) : -1.0f;  // -1: nothing to add, whatever its O holds
+    // -1: nothing to add. (A piece with values is added even where its weight is 0: they may be NaN. A row that sees
+    // nothing anywhere is 0.)
+    const float w = sum == 0.0f || ml.y < 0.0f ? -1.0f : exp2_fast(ml.x - best);
     float4 v[8];
     float wr[8];
 #pragma unroll

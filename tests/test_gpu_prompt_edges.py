@@ -53,6 +53,7 @@ def _level_case(nq, level, seed):
 @pytest.mark.parametrize("low", [-300.0, -float("inf")])
 @pytest.mark.parametrize("nq,nk,even,first", [
     (100, 512, True, None), (100, 512, False, None), (1, 1100, True, None),   # key tiles in two halves of the pipeline
+    (2, 30000, True, 15000), (2, 30000, True, 29000), (200, 20000, False, None),  # cut keys
     (300, 512, True, None), (300, 512, True, 200)])                           # two row tiles
 def test_prompt_values_whose_weight_vanishes(nq, nk, even, first, low):
     """A NaN or an infinity of V at a key that every row sees reaches every row, however small the key's probability."""
