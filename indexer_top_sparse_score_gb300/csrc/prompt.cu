@@ -555,7 +555,7 @@ __device__ __forceinline__ void load8(const float* p, float* v) {  // (no .nc: i
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
-struct Joined {  // how a row's sum goes into its result: out = own * f + prev_out * fp
+struct Joined {  // how a row's sum goes into its result: out = own * f + prev_out * fp (fp -1: nothing of prev_out)
   float f, fp, lse;
 };
 __device__ __noinline__ void join_with(float was, float l, Joined& j) {
@@ -569,7 +569,7 @@ __device__ __noinline__ void join_with(float was, float l, Joined& j) {
 __device__ __forceinline__ Joined join_prev(const PromptParams& p, long long flat, float m, float l) {
   Joined j;
   j.f = l != 0.0f ? 1.0f / l : 0.0f;
-  j.fp = 0.0f;
+  j.fp = -1.0f;
   j.lse = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
   if (p.prev_lse) join_with(p.prev_lse[flat], l, j);
   return j;
@@ -1129,7 +1129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const long long flat = (static_cast<long long>(it.tok0) + token) * p.n_heads + head + (row & ((1 << p.gshift) - 1));
       const bool some = end > it.t0;  // (the items' tiles, or this half's)
       // What needs no product is done while the last one runs.
-      Joined j{0.0f, 0.0f, -INFINITY};
+      Joined j{0.0f, -1.0f, -INFINITY};
       const bool alone = exists && it.whole && !halves;
       if (alone) {
         j = join_prev(p, flat, m, l);
@@ -1216,7 +1216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const long long at = flat * kVal + c;
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = l != 0.0f ? v[i] * f : 0.0f;
-            if (j.fp != 0.0f) add_prev(p, at, j.fp, v);
+            if (j.fp != -1.0f) add_prev(p, at, j.fp, v);
             if (p.out_fp32) {
               store8(static_cast<float*>(p.out) + at, v, p.out_sectors);
               store8(static_cast<float*>(p.out) + at + 8, v + 8, p.out_sectors);
@@ -1346,7 +1346,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PromptParams p
     const float f = __shfl_sync(0xFFFFFFFFu, j.f, r), fp = __shfl_sync(0xFFFFFFFFu, j.fp, r);
     const long long to = __shfl_sync(0xFFFFFFFFu, flat, r);
     float4 v = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
-    if (fp != 0.0f) {
+    if (fp != -1.0f) {  // (a weight of 0 keeps a NaN)
       const float4 was = *reinterpret_cast<const float4*>(p.prev_out + to * kVal + 4 * lane);
       v.x += fp * was.x, v.y += fp * was.y, v.z += fp * was.z, v.w += fp * was.w;
     }

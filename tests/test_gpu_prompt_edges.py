@@ -74,6 +74,26 @@ def test_prompt_values_whose_weight_vanishes(nq, nk, even, first, low):
     assert ((lse.cpu() - float(live.sum().double().log())).abs() <= 2.0 ** -16).all()
 
 
+@pytest.mark.parametrize("nq,nk", [(100, 300), (3, 20000)])
+def test_prompt_joined_values_whose_weight_vanishes(nq, nk):
+    """The earlier result's values too, and this call's beside an earlier result that outweighs them; -inf adds nothing."""
+    q, k, v = _level_case(nq, torch.zeros(nk), 71)
+    po, pl = torch.randn(nq, 1, 128, generator=torch.Generator().manual_seed(72)), torch.full((nq, 1), -400.0)
+    po[0, 0, 5], pl[1, 0], pl[2, 0] = float("nan"), 500.0, -float("inf")
+    po[2] = float("nan")
+    v[40, 0, 9] = float("nan")
+    out, lse, ws = smla.prompt_fwd(q, k, v.cuda(), pc.cu([nq], "cuda"), pc.cu([nk], "cuda"), 1.0, causal=False, prev_out=po.cuda(), prev_lse=pl.cuda(),
+                                   out_dtype=torch.float32)
+    assert smla.read_status(ws)[0] == 0
+    bad = out.isnan().cpu()[:, 0]
+    want = torch.zeros_like(bad)
+    want[:, 9] = True
+    want[0, 5] = True
+    assert torch.equal(bad, want)
+    rest = ~want[1]
+    assert torch.equal(out[1, 0].cpu()[rest], po[1, 0][rest]) and lse[1, 0] == 500.0
+
+
 def test_prompt_rows_whose_logits_are_all_minus_infinity():
     """They are as rows that see nothing, whole or cut, alone or joined, whatever V holds."""
     for nq, nk, odd in ((100, 300, 290), (300, 300, 5), (300, 300, 299), (2, 20000, 9), (2, 20000, 19999)):
