@@ -50,7 +50,8 @@ int smla_rope_table(float* cos_sin, int64_t first, int32_t n, int32_t dim, doubl
  *   positions [rows] int32; -1: the row is skipped (padding).
  *   x         head h of row i at x + i * x_row + h * x_head bf16 values.
  *   out       the same with out_row and out_head. out may be x with the same strides (in
- *             place); otherwise the two do not overlap.
+ *             place); otherwise the two do not overlap. No two heads of out share a value
+ *             (SMLA_ERR_INVALID_ARG).
  * dim: a multiple of 8, 8 .. 256. Strides: multiples of 8 values, head strides at
  * least dim (where there are several heads), row strides not negative. Device errors:
  * another position outside [0, max_pos): the row is skipped. Workspace: 256 bytes.

@@ -384,6 +384,20 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
                      });
 }
 
+// Whether two of the places of `dim` values at i * row + h * head (both strides at least dim where they are used) overlap.
+bool places_overlap(int64_t rows, int64_t row, int64_t heads, int64_t head, int64_t dim) {
+  typedef __int128 Wide;
+  if (rows == 1 || heads == 1) return false;
+  const Wide all_rows = static_cast<Wide>(rows - 1) * row, all_heads = static_cast<Wide>(heads - 1) * head;
+  if (row >= all_heads + dim || head >= all_rows + dim) return false;  // heads inside a row, rows inside a head
+  for (int64_t h = 1; h < heads; ++h) {  // the rows on both sides of a head's distance
+    const Wide at = static_cast<Wide>(h) * head, below = at / row, rest = at % row;
+    if (at >= all_rows + dim) break;
+    if ((below < rows && rest < dim) || (below + 1 < rows && row - rest < dim)) return true;
+  }
+  return false;
+}
+
 bool strided(const void* p, int64_t stride, int64_t width) { return aligned_to(p, 16) && stride % 8 == 0 && stride >= width; }
 
 }  // namespace
@@ -436,7 +450,8 @@ int smla_rope_apply(const float* cos_sin, int32_t max_pos, int32_t dim, int32_t 
   if (dim % 8 || dim > kMaxDim) return SMLA_ERR_UNSUPPORTED;
   if (x_row % 8 || x_head % 8 || out_row % 8 || out_head % 8 || x_row < 0 || out_row < 0) return SMLA_ERR_INVALID_ARG;
   if (n_heads > 1 && (x_head < dim || out_head < dim)) return SMLA_ERR_INVALID_ARG;
-  if (rows > 1 && out_row < dim) return SMLA_ERR_INVALID_ARG;  // rows of the output do not share their place
+  if (rows > 1 && out_row < dim) return SMLA_ERR_INVALID_ARG;
+  if (places_overlap(rows, out_row, n_heads, out_head, dim)) return SMLA_ERR_INVALID_ARG;
   if (out == x && (x_row != out_row || x_head != out_head)) return SMLA_ERR_INVALID_ARG;
   if (const int rc = check_ws(workspace, workspace_bytes)) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
