@@ -191,7 +191,8 @@ __device__ __forceinline__ uint4 widen8(uint2 c, float s) {
 // 41 us, 5.6 TB/s; 37 ragged requests of BF16 rows and keys, 102 MB in 22.6 us; few rows by four latencies (600
 // rows: 4.5 us). Batches of three / five / nine pieces a thread: 43.6 / 51.9 / 51.9 us for the FP8 rows on cold
 // caches (registers), blocks of 16 rows 46.8, of 128 threads 44.7 (both with batches of five).
-// Programmatic launch after clear_kernel: only who reports waits for it.
+// Programmatic launch after clear_kernel: who reports waits for it, and the first block does, so that the launch is not
+// over before the word is cleared (what comes next on the stream may write it).
 __global__ void clear_kernel(uint32_t* status) {
   asm volatile("griddepcontrol.launch_dependents;");
   *status = 0;
@@ -305,7 +306,10 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
     place[tid] = at;
     if (bad && !p.first_reports) report(p.status);
   }
-  if (!p.first_reports && blockIdx.x == 0 && bad_bounds(p)) report(p.status);
+  if (!p.first_reports && blockIdx.x == 0) {
+    if (bad_bounds(p)) report(p.status);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
   __syncthreads();
   const uint4 none = make_uint4(0, 0, 0, 0);
   auto to_latent = [&](int r, int j, uint4 v) { *reinterpret_cast<uint4*>(p.latent + (r0 + r) * p.latent_stride + 8 * j) = v; };

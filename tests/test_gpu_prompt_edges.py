@@ -170,3 +170,27 @@ def test_prompt_bounds_that_overlap_make_more_blocks_than_there_is_room_for(tota
     """0 .. total again and again, every other request backwards."""
     cq, ck = [total_q * (i % 2) for i in range(n + 1)], [total_k * (i % 2) for i in range(n + 1)]
     _check_bad(cq, ck, total_q, total_k)
+
+
+# ---------------------------------------------------------------------------- cache rows
+class _Cache:
+    def __init__(self, pages, keys=True, seed=90):
+        g = torch.Generator().manual_seed(seed)
+        self.kv, self.kv_scale, self.kv_dtype = torch.randn(pages, 64, 576, generator=g).to(torch.bfloat16).cuda(), None, "bf16"
+        self.k_idx = torch.randn(pages, 64, 64, generator=g).to(torch.bfloat16).cuda() if keys else None
+        self.k_idx_scale, self.idx_dtype = None, "bf16" if keys else None
+
+
+def test_cache_read_status_of_a_small_call_behind_a_large_one():
+    """A large call clears the status in a launch of its own, a small one writes it: one after the other in one workspace."""
+    c = _Cache(40)
+    big, small = torch.arange(40, dtype=torch.int32, device="cuda")[None], torch.full((1, 1), 77, dtype=torch.int32, device="cuda")
+    cu_big, cu_small, ws = pc.cu([2560], "cuda"), pc.cu([3], "cuda"), smla.workspace(256)
+    lat, pe = (torch.empty(2560, w, dtype=torch.bfloat16, device="cuda") for w in (512, 64))
+    for _ in range(200):
+        smla.cache_read(c, big, cu_big, 2560, latent=lat, pe=pe, ws=ws)
+        smla.cache_read(c, small, cu_small, 3, latent=lat[:3], pe=pe[:3], ws=ws)
+        assert smla.read_status(ws)[0] == 5
+        smla.cache_read(c, big, cu_big, 2560, latent=lat, pe=pe, ws=ws)
+        assert smla.read_status(ws)[0] == 0
+    assert torch.equal(lat, c.kv.flatten(0, 1)[:, :512])
