@@ -186,11 +186,14 @@ def _dtype_code(name: str) -> int:
 
 def make_cache(cache) -> PagedCache:
     """C view of a paged cache object with kv / kv_scale / k_idx / k_idx_scale
-    tensors and kv_dtype / idx_dtype names ("bf16" or "fp8")."""
+    tensors and kv_dtype / idx_dtype names ("bf16" or "fp8"). A dense layer's has no
+    indexer keys: k_idx is None."""
+    keys = cache.k_idx is not None
     return PagedCache(kv=_p(cache.kv), kv_scale=_p(cache.kv_scale), k_idx=_p(cache.k_idx),
                       k_idx_scale=_p(cache.k_idx_scale), num_pages=cache.kv.shape[0],
                       page_size=cache.kv.shape[1], kv_dtype=_dtype_code(cache.kv_dtype),
-                      idx_dtype=_dtype_code(cache.idx_dtype), d_idx=cache.k_idx.shape[-1])
+                      idx_dtype=_dtype_code(cache.idx_dtype) if keys else SMLA_BF16,
+                      d_idx=cache.k_idx.shape[-1] if keys else 0)
 
 
 # torch's current stream as an integer, without the Stream object that
@@ -499,7 +502,9 @@ def cache_append(cache, slots, positions, rope, *, ckv=None, kv_norm=None, k_idx
     _int32(slots, positions)
     if positions.numel() != rows:
         raise ValueError("positions and slots have one entry per row")
-    d = cache.k_idx.shape[-1]
+    d = 0 if cache.k_idx is None else cache.k_idx.shape[-1]
+    if k_idx is not None and d == 0:
+        raise ValueError("the cache has no indexer keys")
     kv_stride, k_stride = _bf16_rows(ckv, rows, D_QK), _bf16_rows(k_idx, rows, d)
     _fp32(kv_norm, D_V, "kv_norm")
     _fp32(idx_norm, d, "idx_norm")
@@ -678,13 +683,17 @@ def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, p
     """Tokens starts[b] .. of every request b out of `cache` into the packed rows
     cu_rows[b] .. cu_rows[b + 1] - 1, as bf16: latent [rows, 512], pe [rows, 64] and, if wanted or
     given, keys [rows, d_idx] (see smla_cache_read). Given outputs may be strided; rows past
-    cu_rows[n] are left as they are. Returns (latent, pe, keys, ws)."""
+    cu_rows[n] are left as they are. A cache without indexer keys has k_idx None. Returns
+    (latent, pe, keys, ws)."""
     _int32(page_tables, cu_rows, starts)
     n_seqs, max_pages = page_tables.shape
     if cu_rows.numel() != n_seqs + 1 or (starts is not None and starts.numel() != n_seqs):
         raise ValueError("cu_rows has n_seqs + 1 entries, starts n_seqs")
     at = _stream_of(stream, cache.kv, cache.kv_scale, cache.k_idx, cache.k_idx_scale, page_tables, cu_rows, starts, latent, pe, keys, ws)
-    dev, d = page_tables.device, cache.k_idx.shape[-1]
+    dev, k_idx = page_tables.device, cache.k_idx
+    d = 0 if k_idx is None else k_idx.shape[-1]
+    if d == 0 and (want_keys or keys is not None):
+        raise ValueError("the cache has no indexer keys")
     if latent is None:
         latent = torch.empty((rows, D_V), dtype=_BF16, device=dev)
     if pe is None:
@@ -695,8 +704,8 @@ def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, p
     if ws is None:
         ws = workspace(STATUS_BYTES, dev)
     kv = cache.kv
-    c = PagedCache(kv.data_ptr(), _p(cache.kv_scale), cache.k_idx.data_ptr(), _p(cache.k_idx_scale), *kv.shape[:2], _dtype_code(cache.kv_dtype),
-                   _dtype_code(cache.idx_dtype), d)
+    c = PagedCache(kv.data_ptr(), _p(cache.kv_scale), _p(k_idx), _p(cache.k_idx_scale), *kv.shape[:2], _dtype_code(cache.kv_dtype),
+                   _dtype_code(cache.idx_dtype) if d else SMLA_BF16, d)
     rc = (_lib or lib()).smla_cache_read(ctypes.byref(c), page_tables.data_ptr(), max_pages, n_seqs, cu_rows.data_ptr(), rows, _p(starts),
                                          latent.data_ptr(), strides[0], pe.data_ptr(), strides[1], _p(keys), strides[2], ws.data_ptr(),
                                          ws.numel(), at)

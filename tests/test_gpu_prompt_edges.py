@@ -194,3 +194,33 @@ def test_cache_read_status_of_a_small_call_behind_a_large_one():
         smla.cache_read(c, big, cu_big, 2560, latent=lat, pe=pe, ws=ws)
         assert smla.read_status(ws)[0] == 0
     assert torch.equal(lat, c.kv.flatten(0, 1)[:, :512])
+
+
+def test_calls_on_a_cache_without_indexer_keys():
+    """A dense layer's cache: rows appended, read back, attended over in both forms."""
+    c = _Cache(6, keys=False)
+    tab, lens = torch.tensor([[3, 1], [5, 0]], dtype=torch.int32, device="cuda"), torch.tensor([70, 64], dtype=torch.int32, device="cuda")
+    t = [torch.arange(int(n), device="cuda") for n in lens]
+    slots = torch.cat([tab[b, i // 64] * 64 + i % 64 for b, i in enumerate(t)]).to(torch.int32)
+    pos, table = torch.cat(t).to(torch.int32), smla.rope_table(100)
+    rows = (torch.randn(134, 576, generator=torch.Generator().manual_seed(91)) * 2).to(torch.bfloat16).cuda()
+    ws = smla.cache_append(c, slots, pos, table, ckv=rows)
+    assert smla.read_status(ws)[0] == 0
+    lat, pe, keys, ws = smla.cache_read(c, tab, pc.cu([70, 64], "cuda"), 134)
+    assert smla.read_status(ws)[0] == 0 and keys is None
+    assert torch.equal(lat, rows[:, :512])
+    turned, mag = pc.rotate(rows[:, 512:].double().cpu(), table.cpu()[pos.cpu().long()], True)
+    pc.check_rotated(pe.cpu(), turned, mag)
+    q = torch.randn(2, 64, 576, generator=torch.Generator().manual_seed(92)).to(torch.bfloat16).cuda()
+    out, _, ws = smla.shared_prefix_fwd(c, tab, lens, 128, 0, 1, q, 0.04)
+    assert smla.read_status(ws)[0] == 0
+    for b, (lo, hi) in enumerate(((0, 70), (70, 134))):
+        z = (q[b].double() @ torch.cat([lat, pe], 1)[lo:hi].double().T) * 0.04
+        ref = torch.softmax(z, 1) @ lat[lo:hi].double()
+        assert ((out[b].double() - ref).norm(dim=-1) <= 2.0 ** -7 * ref.norm(dim=-1)).all()
+    for call in (lambda: smla.cache_read(c, tab, pc.cu([70, 64], "cuda"), 134, want_keys=True),
+                 lambda: smla.cache_append(c, slots, pos, table, ckv=rows, k_idx=rows[:, :64])):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(smla.SmlaError):
+        smla.indexer_topk(c, tab, lens, 128, 1, rows[:2, None, :64].expand(2, 32, 64).contiguous(), torch.ones(2, 32, device="cuda"), 64)

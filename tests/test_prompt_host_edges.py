@@ -2,6 +2,7 @@
 import itertools
 
 import pytest
+import torch
 
 import indexer_top_sparse_score_gb300 as smla
 from test_prompt_host import FAKE, INVALID, L, WORKSPACE, _rope  # noqa: F401
@@ -31,3 +32,13 @@ def test_rope_accepts_large_strides(L):  # noqa: F811
     assert _rope(L, rows=1 << 30, h=1 << 10, outr=64, outh=64 << 30, ws=None) == WORKSPACE
     assert _rope(L, rows=1 << 30, h=1 << 10, outr=64, outh=64, ws=None) == INVALID
     assert _rope(L, rows=1 << 30, h=1 << 20, outr=big, outh=big, ws=None) == INVALID
+
+
+def test_view_of_a_cache_without_indexer_keys():
+    """As the C calls take it: no keys, no width."""
+    class Dense:
+        kv, kv_scale, kv_dtype = torch.zeros(3, 64, 576, dtype=torch.bfloat16), None, "bf16"
+        k_idx = k_idx_scale = idx_dtype = None
+
+    c = smla.make_cache(Dense())
+    assert c.kv == Dense.kv.data_ptr() and not c.k_idx and c.d_idx == 0 and c.num_pages == 3 and c.page_size == 64
