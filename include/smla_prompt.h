@@ -79,7 +79,8 @@ int smla_rope_apply(const float* cos_sin, int32_t max_pos, int32_t dim, int32_t 
  * Strides: multiples of 8, at least the row's width. Device errors: a token outside the
  * request's table or whose page is not in the pool: zeros; rows of an interval that runs
  * backwards: left as they are, as are rows past `rows`. Workspace: 256 bytes. The cache
- * is device memory.
+ * is device memory; a part of it that no output needs may be NULL. One output at least, rows, n_seqs and
+ * max_pages at least 1: a step that has no rows makes no call.
  * ------------------------------------------------------------------------- */
 int smla_cache_read(const smla_paged_cache* cache, const int32_t* page_tables, int32_t max_pages, int32_t n_seqs,
                     const int32_t* cu_rows, int32_t rows, const int32_t* starts, void* latent, int64_t latent_stride,
@@ -124,6 +125,8 @@ typedef struct smla_heads {
  * not see never reach it, whatever they hold; a value that is not finite reaches the rows that
  * see it, however small its probability: NaN as NaN, an infinity as itself or, where its probability or a joined
  * part's weight is zero in fp32, as either (how a request's keys are cut decides).
+ * total_q, total_k and n_seqs are at least 1 (requests of no tokens or keys are fine; where no request has
+ * any, there is no call to make: prev_out and prev_lse are the result).
  * Supported: d_qk 128 and 192; 1 <= n_heads <= 1024, a multiple of n_kv_heads. sm_scale is finite.
  * Workspace: the returned size (status word, the plan of the work, and partial results of
  * rows whose keys are cut: two pieces of 133 KB for each SM). The size is that of the current device.

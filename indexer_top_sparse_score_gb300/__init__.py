@@ -678,13 +678,13 @@ def rope_apply(x, positions, table, *, interleaved=True, out=None, ws=None, stre
     return out, ws
 
 
-def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, pe=None, keys=None, want_keys=False, ws=None,
-               stream=None):
+def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, pe=None, keys=None, want_latent=True, want_pe=True,
+               want_keys=False, ws=None, stream=None):
     """Tokens starts[b] .. of every request b out of `cache` into the packed rows
-    cu_rows[b] .. cu_rows[b + 1] - 1, as bf16: latent [rows, 512], pe [rows, 64] and, if wanted or
-    given, keys [rows, d_idx] (see smla_cache_read). Given outputs may be strided; rows past
+    cu_rows[b] .. cu_rows[b + 1] - 1, as bf16, those that are wanted or given of latent [rows, 512], pe
+    [rows, 64] and keys [rows, d_idx] (see smla_cache_read). Given outputs may be strided; rows past
     cu_rows[n] are left as they are. A cache without indexer keys has k_idx None. Returns
-    (latent, pe, keys, ws)."""
+    (latent, pe, keys, ws), None for what is left out."""
     _int32(page_tables, cu_rows, starts)
     n_seqs, max_pages = page_tables.shape
     if cu_rows.numel() != n_seqs + 1 or (starts is not None and starts.numel() != n_seqs):
@@ -694,9 +694,9 @@ def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, p
     d = 0 if k_idx is None else k_idx.shape[-1]
     if d == 0 and (want_keys or keys is not None):
         raise ValueError("the cache has no indexer keys")
-    if latent is None:
+    if latent is None and want_latent:
         latent = torch.empty((rows, D_V), dtype=_BF16, device=dev)
-    if pe is None:
+    if pe is None and want_pe:
         pe = torch.empty((rows, D_QK - D_V), dtype=_BF16, device=dev)
     if keys is None and want_keys:
         keys = torch.empty((rows, d), dtype=_BF16, device=dev)
@@ -707,8 +707,7 @@ def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, p
     c = PagedCache(kv.data_ptr(), _p(cache.kv_scale), _p(k_idx), _p(cache.k_idx_scale), *kv.shape[:2], _dtype_code(cache.kv_dtype),
                    _dtype_code(cache.idx_dtype) if d else SMLA_BF16, d)
     rc = (_lib or lib()).smla_cache_read(ctypes.byref(c), page_tables.data_ptr(), max_pages, n_seqs, cu_rows.data_ptr(), rows, _p(starts),
-                                         latent.data_ptr(), strides[0], pe.data_ptr(), strides[1], _p(keys), strides[2], ws.data_ptr(),
-                                         ws.numel(), at)
+                                         _p(latent), strides[0], _p(pe), strides[1], _p(keys), strides[2], ws.data_ptr(), ws.numel(), at)
     if rc:
         raise SmlaError(rc, "smla_cache_read")
     return latent, pe, keys, ws
@@ -723,12 +722,13 @@ _HeadsOfThree = Heads * 3
 
 
 def prompt_fwd(q, k, v, cu_q, cu_k, sm_scale, *, k_pe=None, causal=True, prev_out=None, prev_lse=None, out=None, lse=None,
-               out_dtype=torch.bfloat16, ws=None, stream=None):
+               want_lse=True, out_dtype=torch.bfloat16, ws=None, stream=None):
     """Attention over packed prompts: q [total_q, H, 128 or 192], k [total_k, Hk, the same] (or
     64 less, with the rope part k_pe [total_k, 64] of all heads), v [total_k, Hk, 128], all bf16 and
     possibly strided; cu_q and cu_k [n + 1] where each request's tokens and keys begin. causal: the
     tokens are the last ones of their keys. prev_out and prev_lse (fp32): the result over other keys, to
-    be joined with (see smla_prompt_fwd). Returns (out, lse, ws)."""
+    be joined with (see smla_prompt_fwd). Returns (out, lse, ws), lse None where it is neither wanted nor
+    given."""
     _int32(cu_q, cu_k)
     n_seqs = cu_q.numel() - 1
     tq, heads, d, q_row, q_head = _strides(q, "q")
@@ -742,7 +742,7 @@ def prompt_fwd(q, k, v, cu_q, cu_k, sm_scale, *, k_pe=None, causal=True, prev_ou
     fp32 = out.dtype is _F32
     if not (fp32 or out.dtype is _BF16) or out.numel() != tq * heads * D_HEAD or not out.is_contiguous():
         raise ValueError("out is contiguous bf16 or fp32 [total_q, heads, 128]")
-    if lse is None:
+    if lse is None and want_lse:
         lse = torch.empty((tq, heads), dtype=_F32, device=q.device)
     else:
         _fp32(lse, tq * heads, "lse")
@@ -756,7 +756,7 @@ def prompt_fwd(q, k, v, cu_q, cu_k, sm_scale, *, k_pe=None, causal=True, prev_ou
     at = ctypes.addressof(h)
     rc = (_lib or lib()).smla_prompt_fwd(at, at + 24, at + 48, _p(k_pe), pe_row, tq, tk, n_seqs, cu_q.data_ptr(), cu_k.data_ptr(), heads,
                                          kv_heads, d, int(causal), sm_scale, _p(prev_out), _p(prev_lse), out.data_ptr(), int(fp32),
-                                         lse.data_ptr(), ws.data_ptr(), ws.numel(), handle)
+                                         _p(lse), ws.data_ptr(), ws.numel(), handle)
     if rc:
         raise SmlaError(rc, "smla_prompt_fwd")
     return out, lse, ws

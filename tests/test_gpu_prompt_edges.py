@@ -5,6 +5,7 @@ import torch
 import indexer_top_sparse_score_gb300 as smla
 import prompt_common as pc
 import prompt_tiles as pt
+from test_gpu_prompt import _bf16_rows, _filled
 
 pytestmark = pytest.mark.gpu
 
@@ -224,3 +225,56 @@ def test_calls_on_a_cache_without_indexer_keys():
             call()
     with pytest.raises(smla.SmlaError):
         smla.indexer_topk(c, tab, lens, 128, 1, rows[:2, None, :64].expand(2, 32, 64).contiguous(), torch.ones(2, 32, device="cuda"), 64)
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8", "fp8_ds_mla"])
+@pytest.mark.parametrize("idx_dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,length", [(3, 70), (9, 333)])
+def test_cache_read_of_some_outputs(kv_dtype, idx_dtype, n, length):
+    """Every choice of outputs, in small calls and large: the bits of the call for all of them; bad tokens reported alike."""
+    width = -(-length // 64)
+    c = _filled(n * width, kv_dtype, idx_dtype, 93).to("cuda")
+    tab = torch.randperm(n * width, generator=torch.Generator().manual_seed(94)).to(torch.int32).view(n, width).cuda()
+    cu, rows = pc.cu([length] * n, "cuda"), n * length
+    bad = tab.clone()
+    bad[n // 2, 0] = n * width
+    for pages, code in ((tab, 0), (bad, 5)):
+        *whole, ws = smla.cache_read(c, pages, cu, rows, want_keys=True)
+        assert smla.read_status(ws)[0] == code
+        for some in range(1, 8):
+            a, b, k = bool(some & 1), bool(some & 2), bool(some & 4)
+            *got, ws = smla.cache_read(c, pages, cu, rows, want_latent=a, want_pe=b, want_keys=k)
+            assert smla.read_status(ws)[0] == code
+            for g, w, want in zip(got, whole, (a, b, k)):
+                assert torch.equal(g, w) if want else g is None
+    x, k = _bf16_rows(c.to("cpu"))
+    at = torch.cat([tab[b, torch.arange(length) // 64].cpu().long() * 64 + torch.arange(length) % 64 for b in range(n)])
+    good = smla.cache_read(c, tab, cu, rows, want_keys=True)
+    assert torch.equal(good[0].cpu(), x[at, :512]) and torch.equal(good[1].cpu(), x[at, 512:]) and torch.equal(good[2].cpu(), k[at])
+    with pytest.raises(smla.SmlaError):
+        smla.cache_read(c, tab, cu, rows, want_latent=False, want_pe=False)
+
+
+@pytest.mark.parametrize("ql,kl", [([70, 9], [90, 20]), ([300], [900]), ([2, 1], [9000, 300]), ([200], [20000])])
+@pytest.mark.parametrize("join", [False, True])
+def test_prompt_without_lse(ql, kl, join):
+    q, k, v, pe, cq, ck = (t.cuda() for t in pc.prompt_case(ql, kl, 4, 4, 192, True, seed=95))
+    prev = dict(prev_out=torch.randn(sum(ql), 4, 128, device="cuda"), prev_lse=torch.randn(sum(ql), 4, device="cuda") + 5) if join else {}
+    out, lse, _ = smla.prompt_fwd(q, k, v, cq, ck, 0.07, k_pe=pe, **prev)
+    got, none, ws = smla.prompt_fwd(q, k, v, cq, ck, 0.07, k_pe=pe, want_lse=False, **prev)
+    assert smla.read_status(ws)[0] == 0 and none is None and torch.equal(got, out)
+
+
+def test_calls_without_rows_or_keys_are_refused():
+    """As the header says: there is nothing to launch."""
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    c, tab = _Cache(2), i(0, 1)[None]
+    for call in (lambda: smla.prompt_fwd(b(0, 2, 192), b(5, 2, 192), b(5, 2, 128), i(0, 0), i(0, 5), 0.1),
+                 lambda: smla.prompt_fwd(b(5, 2, 192), b(0, 2, 192), b(0, 2, 128), i(0, 5), i(0, 0), 0.1, causal=False),
+                 lambda: smla.prompt_fwd(b(5, 2, 192), b(5, 2, 192), b(5, 2, 128), i(0), i(0), 0.1),
+                 lambda: smla.cache_read(c, tab, i(0, 0), 0), lambda: smla.rope_table(0),
+                 lambda: smla.rope_apply(b(0, 2, 64), torch.zeros(0, dtype=torch.int32, device="cuda"), smla.rope_table(4))):
+        with pytest.raises(smla.SmlaError) as e:
+            call()
+        assert e.value.code == 1
