@@ -2490,7 +2490,9 @@ size_t indexer_workspace_bytes(int32_t n_seqs, int32_t max_seq_len, int32_t q_pe
 }
 
 int launch_indexer(const IndexerLaunch& L) {
-  const bool split = indexer_split_mode(L.q_per_seq, L.h_idx);
+  // (split mode reads the lengths on the device, and its scores need room of their own: a prefill of a few
+  // tokens, which has neither, runs in group mode)
+  const bool split = L.seq_lens != nullptr && indexer_split_mode(L.q_per_seq, L.h_idx);
   const int dense_tq = split ? 0 : indexer_dense_tokens(L.h_idx, L.topk, L.max_seq_len);
   const bool dense = dense_tq > 0;
   const int tq = dense ? dense_tq : indexer_tokens_per_cta(L.h_idx, L.topk, split, L.q_per_seq);
