@@ -213,6 +213,19 @@ def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return torch.empty(max(256, (nbytes + 255) // 256 * 256), dtype=torch.uint8, device=device)
 
 
+def _made(stream, t: torch.Tensor) -> torch.Tensor:
+    """t, an output or workspace that a call on `stream` makes. torch hands its memory out again once
+    nobody holds it, in the order of the current stream: on another one, that
+    stream's work up to then comes first (the caller may drop t right after the call)."""
+    if stream is not None and t.is_cuda:
+        handle = _stream(stream)
+        if handle != torch.cuda.current_stream(t.device).cuda_stream:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(handle, t.device) if handle else torch.cuda.default_stream(t.device)
+            t.record_stream(stream)
+    return t
+
+
 # ---------------------------------------------------------------------------- entry points
 def indexer_topk(cache, page_tables, seq_lens, max_seq_len, q_per_seq, q_idx, w, topk, out_idx=None,
                  out_scores=None, ws=None, stream=None, want_scores=False):
@@ -223,12 +236,12 @@ def indexer_topk(cache, page_tables, seq_lens, max_seq_len, q_per_seq, q_idx, w,
     rows = n_seqs * q_per_seq
     h_idx = q_idx.shape[1]
     if out_idx is None:
-        out_idx = torch.empty((rows, topk), dtype=torch.int32, device=q_idx.device)
+        out_idx = _made(stream, torch.empty((rows, topk), dtype=torch.int32, device=q_idx.device))
     if want_scores and out_scores is None:
-        out_scores = torch.empty((rows, topk), dtype=torch.float32, device=q_idx.device)
+        out_scores = _made(stream, torch.empty((rows, topk), dtype=torch.float32, device=q_idx.device))
     need = L.smla_indexer_topk_workspace_size(n_seqs, max_seq_len, q_per_seq, h_idx, topk)
     if ws is None:
-        ws = workspace(need, q_idx.device)
+        ws = _made(stream, workspace(need, q_idx.device))
     c = make_cache(cache)
     rc = L.smla_indexer_topk(ctypes.byref(c), _p(pt), max_pages, n_seqs, _p(seq_lens), max_seq_len,
                              q_per_seq, _p(q_idx), _p(w), h_idx, topk, _p(out_idx), _p(out_scores),
@@ -248,13 +261,13 @@ def sparse_mla_fwd(cache, page_tables, q, idx, sm_scale, *, prefix_len=0, seq_le
     if q_per_seq is None:
         q_per_seq = rows // n_seqs
     if out is None:
-        out = torch.empty((rows, H, D_V), dtype=torch.bfloat16, device=q.device)
+        out = _made(stream, torch.empty((rows, H, D_V), dtype=torch.bfloat16, device=q.device))
     if lse is None:
-        lse = torch.empty((rows, H), dtype=torch.float32, device=q.device)
+        lse = _made(stream, torch.empty((rows, H), dtype=torch.float32, device=q.device))
     if ws is None:
         max_keys = prefix_len + q_per_seq if seq_lens is None else 0
-        ws = workspace(L.smla_sparse_mla_fwd_workspace_size(max_keys, rows, H, topk, _dtype_code(cache.kv_dtype)),
-                       q.device)
+        need = L.smla_sparse_mla_fwd_workspace_size(max_keys, rows, H, topk, _dtype_code(cache.kv_dtype))
+        ws = _made(stream, workspace(need, q.device))
     c = make_cache(cache)
     rc = L.smla_sparse_mla_fwd(ctypes.byref(c), _p(pt), max_pages, n_seqs, _p(seq_lens), prefix_len,
                                q_per_seq, _p(q), H, _p(idx), topk, float(sm_scale), _p(out), _p(lse),
@@ -275,11 +288,11 @@ def sparse_mla_prefill(cache, page_table, prefix_len, q, q_idx, w, topk, sm_scal
     T, H, _ = q.shape
     h_idx = q_idx.shape[1]
     if out is None:
-        out = torch.empty((T, H, D_V), dtype=torch.bfloat16, device=q.device)
+        out = _made(stream, torch.empty((T, H, D_V), dtype=torch.bfloat16, device=q.device))
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = _made(stream, torch.empty((T, H), dtype=torch.float32, device=q.device))
     if ws is None:
-        ws = workspace(prefill_workspace_bytes(prefix_len, T, H, h_idx, topk, cache.kv_dtype), q.device)
+        ws = _made(stream, workspace(prefill_workspace_bytes(prefix_len, T, H, h_idx, topk, cache.kv_dtype), q.device))
     c = make_cache(cache)
     rc = L.smla_sparse_mla_prefill(ctypes.byref(c), _p(page_table), prefix_len, T, _p(q), H, _p(q_idx), _p(w),
                                    h_idx, topk, float(sm_scale), _p(out), _p(lse), _p(out_idx), _p(ws),
@@ -415,11 +428,11 @@ def sparse_mla_decode(cache, page_tables, seq_lens, max_seq_len, q_per_seq, q, q
     rows, H, _ = q.shape
     h_idx = q_idx.shape[1]
     if out is None:
-        out = torch.empty((rows, H, D_V), dtype=torch.bfloat16, device=q.device)
+        out = _made(stream, torch.empty((rows, H, D_V), dtype=torch.bfloat16, device=q.device))
     if lse is None:
-        lse = torch.empty((rows, H), dtype=torch.float32, device=q.device)
+        lse = _made(stream, torch.empty((rows, H), dtype=torch.float32, device=q.device))
     if ws is None:
-        ws = workspace(decode_workspace_bytes(n_seqs, max_seq_len, q_per_seq, H, h_idx, topk), q.device)
+        ws = _made(stream, workspace(decode_workspace_bytes(n_seqs, max_seq_len, q_per_seq, H, h_idx, topk), q.device))
     c = make_cache(cache)
     rc = L.smla_sparse_mla_decode(ctypes.byref(c), _p(page_tables), max_pages, n_seqs, _p(seq_lens),
                                   max_seq_len, q_per_seq, _p(q), H, _p(q_idx), _p(w), h_idx, topk,
@@ -460,7 +473,7 @@ def build_tables(ctx_lens, new_lens, page_tables, free_pages, max_new, *, seq_le
 
     def out(t, k):
         if t is None:
-            return torch.empty(k, dtype=_I32, device=dev)
+            return _made(stream, torch.empty(k, dtype=_I32, device=dev))
         if t.numel() < k:
             raise ValueError("an output is too small")
         return t
@@ -468,7 +481,7 @@ def build_tables(ctx_lens, new_lens, page_tables, free_pages, max_new, *, seq_le
     seq_lens, cu_new, pages_used = out(seq_lens, n), out(cu_new, n + 1), out(pages_used, 1)
     positions, slots, row_seq = out(positions, max_new), out(slots, max_new), out(row_seq, max_new)
     if ws is None:
-        ws = workspace(STATUS_BYTES, dev)
+        ws = _made(stream, workspace(STATUS_BYTES, dev))
     rc = L.smla_build_tables(ctx_lens.data_ptr(), new_lens.data_ptr(), n, page_tables.data_ptr(), max_pages,
                              _p(free_pages), 0 if free_pages is None else free_pages.numel(), max_new,
                              seq_lens.data_ptr(), cu_new.data_ptr(), positions.data_ptr(), slots.data_ptr(),
@@ -510,7 +523,7 @@ def cache_append(cache, slots, positions, rope, *, ckv=None, kv_norm=None, k_idx
     _fp32(idx_norm, d, "idx_norm")
     _fp32(idx_bias, d, "idx_bias")
     if ws is None:
-        ws = workspace(STATUS_BYTES, slots.device)
+        ws = _made(stream, workspace(STATUS_BYTES, slots.device))
     c, r = make_cache(cache), _rope(rope, kv_interleaved, idx_interleaved)
     rc = L.smla_cache_append(ctypes.byref(c), ctypes.byref(r), rows, slots.data_ptr(), positions.data_ptr(), _p(ckv),
                              kv_stride, _p(kv_norm), _p(k_idx), k_stride, _p(idx_norm), _p(idx_bias), eps,
@@ -539,7 +552,7 @@ def query_prep(positions, rope, *, q_pe=None, q=None, q_idx_raw=None, w=None, id
         if rows == 1:
             pe_row = 0
         if q is None:
-            q = torch.empty((rows, n_heads, D_QK), dtype=_BF16, device=q_pe.device)
+            q = _made(stream, torch.empty((rows, n_heads, D_QK), dtype=_BF16, device=q_pe.device))
         elif q.dtype is not _BF16 or q.numel() != rows * n_heads * D_QK or not q.is_contiguous():
             raise ValueError("q is contiguous bf16 [rows, heads, 576]")
     if q_idx_raw is not None:
@@ -556,13 +569,14 @@ def query_prep(positions, rope, *, q_pe=None, q=None, q_idx_raw=None, w=None, id
         _fp32(w_out, rows * h_idx, "w_out")
         _fp32(idx_norm, d_idx, "idx_norm")
         if q_idx is None:
-            q_idx = torch.empty((rows, h_idx, d_idx), device=w.device, dtype=_BF16 if idx_dtype == "bf16" else torch.uint8)
+            idx_t = _BF16 if idx_dtype == "bf16" else torch.uint8
+            q_idx = _made(stream, torch.empty((rows, h_idx, d_idx), device=w.device, dtype=idx_t))
         elif q_idx.numel() != values or q_idx.element_size() != (2 if idx_dtype == "bf16" else 1) or not q_idx.is_contiguous():
             raise ValueError("q_idx is contiguous [rows, h_idx, d_idx] of idx_dtype")
         if w_out is None:
-            w_out = torch.empty_like(w)
+            w_out = _made(stream, torch.empty_like(w))
     if ws is None:
-        ws = workspace(STATUS_BYTES, positions.device)
+        ws = _made(stream, workspace(STATUS_BYTES, positions.device))
     r = _rope(rope, kv_interleaved, idx_interleaved)
     rc = L.smla_query_prep(ctypes.byref(r), rows, positions.data_ptr(), _p(q_pe), pe_row, pe_head, n_heads, _p(q),
                            _p(q_idx_raw), raw_row, h_idx, d_idx, _dtype_code(idx_dtype), _p(idx_norm), eps, _p(w),
@@ -590,16 +604,16 @@ def shared_prefix_fwd(cache, page_tables, seq_lens, max_seq_len, shared_len, q_p
     if seq_lens.numel() != n_seqs:
         raise ValueError("seq_lens has one length per row of page_tables")
     if out is None:
-        out = torch.empty((rows, H, D_V), dtype=_BF16, device=q.device)
+        out = _made(stream, torch.empty((rows, H, D_V), dtype=_BF16, device=q.device))
     elif out.dtype is not _BF16 or out.numel() != rows * H * D_V or not out.is_contiguous():
         raise ValueError("out is contiguous bf16 [rows, heads, 512]")
     if lse is None:
-        lse = torch.empty((rows, H), dtype=_F32, device=q.device)
+        lse = _made(stream, torch.empty((rows, H), dtype=_F32, device=q.device))
     else:
         _fp32(lse, rows * H, "lse")
     if ws is None:
-        ws = workspace(shared_prefix_workspace_bytes(n_seqs, max_seq_len, shared_len, q_per_seq, H, cache.kv_dtype),
-                       q.device)
+        need = shared_prefix_workspace_bytes(n_seqs, max_seq_len, shared_len, q_per_seq, H, cache.kv_dtype)
+        ws = _made(stream, workspace(need, q.device))
     c = make_cache(cache)
     rc = L.smla_shared_prefix_fwd(ctypes.byref(c), page_tables.data_ptr(), max_pages, n_seqs, seq_lens.data_ptr(),
                                   max_seq_len, shared_len, q_per_seq, q.data_ptr(), H, sm_scale, out.data_ptr(),
@@ -629,7 +643,7 @@ def rope_table(n, dim=64, *, first=0, base=10000.0, factor=1.0, original=0, beta
     contexts: all alike (original = 0), or by how often they turn over `original`
     positions (see smla_rope_table). Returns the table."""
     if out is None:
-        out = torch.empty((n, dim), dtype=_F32, device="cuda")
+        out = _made(stream, torch.empty((n, dim), dtype=_F32, device="cuda"))
     elif out.dtype is not _F32 or out.shape != (n, dim) or not out.is_contiguous():
         raise ValueError("out is a contiguous fp32 [n, dim] table")
     at = _stream_of(stream, out)
@@ -664,13 +678,13 @@ def rope_apply(x, positions, table, *, interleaved=True, out=None, ws=None, stre
     if table.dtype is not _F32 or table.dim() != 2 or table.shape[1] != dim or not table.is_contiguous():
         raise ValueError("table is a contiguous fp32 [max_pos, dim] table of x's dim")
     if out is None:
-        out = torch.empty((rows, heads, dim), dtype=_BF16, device=x.device)
+        out = _made(stream, torch.empty((rows, heads, dim), dtype=_BF16, device=x.device))
     o = _strides(out, "out")
     if o[:3] != (rows, heads, dim):
         raise ValueError("out has x's shape")
     at = _stream_of(stream, x, positions, table, out, ws)
     if ws is None:
-        ws = workspace(STATUS_BYTES, x.device)
+        ws = _made(stream, workspace(STATUS_BYTES, x.device))
     rc = (_lib or lib()).smla_rope_apply(table.data_ptr(), table.shape[0], dim, int(interleaved), rows, positions.data_ptr(), x.data_ptr(),
                                          x_row, x_head, heads, out.data_ptr(), o[3], o[4], ws.data_ptr(), ws.numel(), at)
     if rc:
@@ -695,14 +709,14 @@ def cache_read(cache, page_tables, cu_rows, rows, *, starts=None, latent=None, p
     if d == 0 and (want_keys or keys is not None):
         raise ValueError("the cache has no indexer keys")
     if latent is None and want_latent:
-        latent = torch.empty((rows, D_V), dtype=_BF16, device=dev)
+        latent = _made(stream, torch.empty((rows, D_V), dtype=_BF16, device=dev))
     if pe is None and want_pe:
-        pe = torch.empty((rows, D_QK - D_V), dtype=_BF16, device=dev)
+        pe = _made(stream, torch.empty((rows, D_QK - D_V), dtype=_BF16, device=dev))
     if keys is None and want_keys:
-        keys = torch.empty((rows, d), dtype=_BF16, device=dev)
+        keys = _made(stream, torch.empty((rows, d), dtype=_BF16, device=dev))
     strides = _bf16_rows(latent, rows, D_V), _bf16_rows(pe, rows, D_QK - D_V), _bf16_rows(keys, rows, d)
     if ws is None:
-        ws = workspace(STATUS_BYTES, dev)
+        ws = _made(stream, workspace(STATUS_BYTES, dev))
     kv = cache.kv
     c = PagedCache(kv.data_ptr(), _p(cache.kv_scale), _p(k_idx), _p(cache.k_idx_scale), *kv.shape[:2], _dtype_code(cache.kv_dtype),
                    _dtype_code(cache.idx_dtype) if d else SMLA_BF16, d)
@@ -738,12 +752,12 @@ def prompt_fwd(q, k, v, cu_q, cu_k, sm_scale, *, k_pe=None, causal=True, prev_ou
         raise ValueError("k and v are [total_k, kv heads, ..] with k as wide as q (64 less beside k_pe) and v of 128; cu_q and cu_k are alike")
     pe_row = 0 if k_pe is None else _bf16_rows(k_pe, tk, 64)
     if out is None:
-        out = torch.empty((tq, heads, D_HEAD), dtype=out_dtype, device=q.device)
+        out = _made(stream, torch.empty((tq, heads, D_HEAD), dtype=out_dtype, device=q.device))
     fp32 = out.dtype is _F32
     if not (fp32 or out.dtype is _BF16) or out.numel() != tq * heads * D_HEAD or not out.is_contiguous():
         raise ValueError("out is contiguous bf16 or fp32 [total_q, heads, 128]")
     if lse is None and want_lse:
-        lse = torch.empty((tq, heads), dtype=_F32, device=q.device)
+        lse = _made(stream, torch.empty((tq, heads), dtype=_F32, device=q.device))
     else:
         _fp32(lse, tq * heads, "lse")
     if prev_out is not None or prev_lse is not None:
@@ -751,7 +765,7 @@ def prompt_fwd(q, k, v, cu_q, cu_k, sm_scale, *, k_pe=None, causal=True, prev_ou
         _fp32(prev_lse, tq * heads, "prev_lse")
     handle = _stream_of(stream, q, k, v, k_pe, cu_q, cu_k, prev_out, prev_lse, out, lse, ws)
     if ws is None:
-        ws = workspace(prompt_workspace_bytes(tq, tk, n_seqs, heads, kv_heads), q.device)
+        ws = _made(stream, workspace(prompt_workspace_bytes(tq, tk, n_seqs, heads, kv_heads), q.device))
     h = _HeadsOfThree((q.data_ptr(), q_row, q_head), (k.data_ptr(), k_row, k_head), (v.data_ptr(), v_row, v_head))
     at = ctypes.addressof(h)
     rc = (_lib or lib()).smla_prompt_fwd(at, at + 24, at + 48, _p(k_pe), pe_row, tq, tk, n_seqs, cu_q.data_ptr(), cu_k.data_ptr(), heads,

@@ -278,3 +278,57 @@ def test_calls_without_rows_or_keys_are_refused():
         with pytest.raises(smla.SmlaError) as e:
             call()
         assert e.value.code == 1
+
+
+# ---------------------------------------------------------------------------- another stream
+def _stream_calls():
+    """Every call that makes tensors of its own, by name: call(stream) -> what it made."""
+    g = torch.Generator().manual_seed(96)
+    rn = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    c, tab = _Cache(4), i(0, 1, 2, 3)[None]
+    pos, table = torch.arange(200, dtype=torch.int32, device="cuda"), smla.rope_table(256)
+    q, k, v, cu, ckv, pe = rn(2, 4, 192), rn(3000, 4, 192), rn(3000, 4, 128), pc.cu([2], "cuda"), rn(200, 576), rn(200, 16, 64)
+    ck, qi, w, ql, cu_rows, raw, big = pc.cu([3000], "cuda"), rn(2, 32, 64), torch.ones(2, 32, device="cuda"), rn(2, 64, 576), pc.cu([200], "cuda"), rn(200, 32, 64), rn(200, 4, 64)
+    lens, new, free, idx, w200 = i(200), i(3), i(3, 2, 1), torch.zeros(2, 64, dtype=torch.int32, device="cuda"), torch.ones(200, 32, device="cuda")
+    return {
+        "rope_table": lambda s: [smla.rope_table(256, stream=s)],
+        "rope_apply": lambda s: smla.rope_apply(big, pos, table, stream=s),
+        "cache_read": lambda s: smla.cache_read(c, tab, cu_rows, 200, want_keys=True, stream=s),
+        "prompt_fwd": lambda s: smla.prompt_fwd(q, k, v, cu, ck, 0.07, stream=s),
+        "build_tables": lambda s: smla.build_tables(lens, new, tab, free, 8, stream=s),
+        "cache_append": lambda s: [smla.cache_append(c, pos, pos, table, ckv=ckv, stream=s)],
+        "query_prep": lambda s: smla.query_prep(pos, table, q_pe=pe, q_idx_raw=raw, w=w200, idx_dtype="bf16", stream=s),
+        "shared_prefix_fwd": lambda s: smla.shared_prefix_fwd(c, tab, lens, 256, 0, 2, ql, 0.04, stream=s),
+        "indexer_topk": lambda s: smla.indexer_topk(c, tab, lens, 256, 2, qi, w, 64, want_scores=True, stream=s),
+        "sparse_mla_fwd": lambda s: smla.sparse_mla_fwd(c, tab, ql, idx, 0.04, seq_lens=lens, stream=s),
+        "sparse_mla_prefill": lambda s: [t for t in smla.sparse_mla_prefill(c, tab[0], 198, ql, qi, w, 64, 0.04, stream=s) if t is not None],
+        "sparse_mla_decode": lambda s: [t for t in smla.sparse_mla_decode(c, tab, lens, 256, 2, ql, qi, w, 64, 0.04, stream=s) if t is not None],
+    }
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_what_a_call_on_another_stream_makes_outlives_its_work(handle):
+    """Outputs and workspaces that the caller drops at once are not handed out again while the stream still works on them.
+    (Nothing is written to what is handed out.)"""
+    calls = _stream_calls()
+    side = torch.cuda.Stream()
+    lost = []
+    for name, call in calls.items():
+        call(None)
+        torch.cuda.synchronize()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # some 100 ms
+        made = call(side.cuda_stream if handle else side)
+        held = [(t.data_ptr(), t.numel() * t.element_size()) for t in made]
+        del made
+        fresh = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in held for _ in range(3)]
+        assert not side.query(), "the stream was to be busy until here"
+        for p, n in held:
+            if any(f.data_ptr() < p + n and p < f.data_ptr() + f.numel() for f in fresh):
+                lost.append(name)
+                break
+        torch.cuda.synchronize()
+        del fresh
+    assert not lost, lost
