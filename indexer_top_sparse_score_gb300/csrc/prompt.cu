@@ -36,12 +36,15 @@
 // leave fp32 partial results, which join_kernel joins. No pair waits for another.
 //
 // Bound by the tensor pipe and, in long runs, by power where prompts are long: 16,384 tokens of 64 heads
-// in 2.98 ms, 1,840 TFLOP/s (3.2-3.3 ms, 1,700, in runs of many; cuBLAS: 1,715). Prompts of some thousand
-// tokens wait for their softmax: a tile's chain is 1,500 cycles of softmax, 1,280 of products and 300 of
+// in 3.2-3.3 ms, 1,670-1,700 TFLOP/s (cuBLAS in long runs: 1,715; the first calls on a cool GPU 2.98 ms). Prompts of
+// some thousand tokens wait for their softmax: a tile's chain is 1,500 cycles of softmax, 1,280 of products and 300 of
 // hand-overs against 2,560 of products for both row tiles (8,192 tokens of 64 heads on 8: 669 us, 1,640
-// TFLOP/s). Short ones spend as long on an item's start and results as on its products (37 prompts of up to
-// 2,047 tokens: 1,094 us, 970 TFLOP/s). A few tokens on many keys cost as much tensor time as 256 rows would (5 x 3
-// tokens on 9K keys: 316 us, 4.7 TB/s). 1 x 100 tokens of 16 heads: 9.5 us, a chain of latencies.
+// TFLOP/s). Short ones, 37 prompts of up to 2,047 tokens: 1,094 us for a floor of 542, from products that the
+// mask hides (row tiles of 256 against key tiles of 128: 1.3 to 1.4 times the definition's, some 730 us at the
+// burst rate; 1.03 at 8,192 tokens) and from the starts and results of items, which the softmax warps do
+// themselves (about 8,000 cycles an item against 15,000 of products). A few tokens on many keys cost as much tensor
+// time as 256 rows would (5 x 3 tokens on 9K keys: 316 us, 4.7 TB/s; 244 us of products at the burst rate). 1 x 100
+// tokens of 16 heads: 9.5 us, a chain of latencies.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -66,8 +69,11 @@ constexpr int kThreads = 384;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kScanWarp0 = 2, kSoftWarp0 = 4;
 constexpr float kRaise = 8.0f;  // log2: the reference maximum is raised only when exceeded by this much
 constexpr int kStart = 2;       // a piece's start and end on the line of work, in tiles (1, 2 and 5: within 2%)
-constexpr int kLongTiles = 8;   // blocks of no more tiles are never cut
-constexpr int kDirectSeqs = 8;  // requests that a thread looks through
+// Blocks of no more tiles are never cut, and calls of no more keys have no join to launch. With 4 / 8 / 16 tiles, us on the
+// device: 7 x 100 tokens of 8 heads 16.3 / 10.9 / 10.9, one token on 1,000 keys of 16 heads 20.3 / 16.2 / 16.0, on 2,048 keys
+// 21.9 / 23.4 / 22.6 (64 heads: 31 / 31 / 24), 300 tokens on 4,000 keys of 4 heads 32 with each.
+constexpr int kLongTiles = 8;
+constexpr int kDirectSeqs = 8;  // requests that a thread looks through (8 x 20 tokens of 8 heads: 10.7 us, 14.4 with a plan)
 constexpr uint32_t kColS = 0, kColO = 256;
 
 struct PromptParams {
@@ -226,6 +232,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
     p.plan->next = 0;
     p.plan->line = line;
     p.plan->n_blocks = n_blocks;
+    // Cut evenly where whole blocks would end a tenth and six tiles later: pieces cost a start and a join each, and blocks
+    // in a row on one line do not share K and V in L2. Never / by this rule / always, us: 5 x 3 tokens on 9K keys 346 / 296 /
+    // 296, 300 tokens on 4,000 keys of 4 heads 62 / 32 / 32, 4,096 tokens of 16 heads 93 / 83 / 83, 37 ragged prompts of 64
+    // heads 950 / 952 / 1,035; 2,048 tokens of 16 heads 40 / 44 / 44 and 8,192 of 16 heads 262 / 263 / 224 on the wrong side.
     p.plan->even = p.can_cut && s_most > kLongTiles && s_bound > even + even / 10 + 6;
     p.plan->pairs = static_cast<int>(max(1LL, min(static_cast<long long>(p.pairs), line / 4)));
     *p.status = s_bad ? kStatusBounds : 0u;
@@ -1104,7 +1114,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float2 y = fma2(make_float2(s[32 * h + i], s[32 * h + i + 1]), factor, minus);
             const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
             sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
-            // P is rounded to bf16 (off by at most 2^-8 of a probability); the sum l is not
+            // P is rounded to bf16 (off by at most 2^-8 of a probability): a product's operands have one type, and
+            // V in f16 would lose its range. Rows are off by 2^-8 / sqrt(3) of their length from it, about what rounding
+            // the result to bf16 adds. The sum l is not rounded.
             pk[i >> 1] = bf_pack(e.x, e.y);
           }
           tmem_st_x16(s_col + 16 * h, pk);

@@ -25,8 +25,8 @@ struct TableParams {
 };
 
 // cos and sin of angle / 2^64 turns. The nearest quarter of a turn is taken off, exactly; what is left, at most
-// an eighth, goes to the nearest float (2^-24 of it) and into the Taylor series of sin and cos
-// up to x^9 and x^10, which are off by 2^-29 there: within 2^-23 altogether.
+// an eighth, becomes a float (three roundings) and goes into the Taylor series of sin and cos
+// up to x^9 and x^10, which are off by 2^-29 there: 2.4 * 2^-24 altogether at most (1.8 * 2^-24 over 80 million angles).
 __device__ __forceinline__ void cos_sin_of(uint64_t angle, float& c, float& s) {
   const uint64_t up = angle + (1ull << 61);
   const int32_t rest = static_cast<int32_t>(static_cast<uint32_t>((up << 2) >> 32) ^ 0x80000000u);  // - 1/8 .. 1/8 turn in 2^-34 turns
@@ -186,11 +186,14 @@ __device__ __forceinline__ uint4 widen8(uint2 c, float s) {
 }
 
 // A block finds the pool rows of 32 output rows: every request's first row is loaded once
-// and counted against them (one latency, no search), then the rows' pieces of 16 bytes of the pool
+// and counted against them (one latency up to 255 requests, whose work is requests x rows / 32 loads; a search would
+// be eight latencies one after the other), then the rows' pieces of 16 bytes of the pool
 // go round the block's threads, each thread's requested together. Bound by memory: 131,072 FP8 rows, 227 MB in
-// 41 us, 5.6 TB/s; 37 ragged requests of BF16 rows and keys, 102 MB in 22.6 us; few rows by four latencies (600
-// rows: 4.5 us). Batches of three / five / nine pieces a thread: 43.6 / 51.9 / 51.9 us for the FP8 rows on cold
-// caches (registers), blocks of 16 rows 46.8, of 128 threads 44.7 (both with batches of five).
+// 41 us, 5.6 TB/s; 37 ragged requests of BF16 rows and keys, 102 MB in 22.6 us (1,184 blocks, each a chain of bounds,
+// table, place and data, and the keys a second round); few rows by those latencies (600 rows: 4.5 us).
+// Batches of two / three / five / nine pieces a thread, 131,072 rows on the device: BF16 50.2 / 49.3 / 49.2 / 68.7 us,
+// FP8 38.9 / 38.9 / 47.1 / 47.1, tile-scaled 40.6 / 45.5 / 56.9 / 56.9 (registers); blocks of 16 rows took the FP8
+// rows 46.8 us on cold caches, of 128 threads 44.7 (both with batches of five, which took 51.9).
 // Programmatic launch after clear_kernel: who reports waits for it, and the first block does, so that the launch is not
 // over before the word is cleared (what comes next on the stream may write it).
 __global__ void clear_kernel(uint32_t* status) {

@@ -332,3 +332,20 @@ def test_what_a_call_on_another_stream_makes_outlives_its_work(handle):
         torch.cuda.synchronize()
         del fresh
     assert not lost, lost
+
+
+# ---------------------------------------------------------------------------- rotation tables
+@pytest.mark.parametrize("magnitude", [1.0, -1.0, 1.37])
+@pytest.mark.parametrize("n,dim,first,kw", [(4099, 64, 0, {}), (70, 256, 1000003, {}), (1001, 8, 1 << 26, dict(base=500.0)),
+                                            (2048, 128, 5, dict(base=1e6, factor=8.0, original=8192))])
+def test_rope_table_bound(n, dim, first, kw, magnitude):
+    """The series' bound. The angle, within an eighth of a turn after exact steps, is a float: its integer, the constant
+    2 pi and their product are rounded, 2.5 half steps of 2^-24 relative at most; times an eighth of a turn (0.79) and the slope there
+    (0.71) that is 1.4 * 2^-24. The polynomials' last steps are off by 2^-25 each, two for the sine, which is at most 0.71 there, and the
+    inner ones by less than 2^-26 together: 2.4 * 2^-24; what the series leaves out is 2^-29. 3 * 2^-24, and a magnitude that is no power of two rounds
+    once more. The frequencies (64-bit roundings here and in the reference): 2^-51 of an angle of first + n radians at most."""
+    got = smla.rope_table(n, dim, first=first, magnitude=magnitude, **kw).double().cpu()
+    ref = pc.table_reference(n, dim, first, magnitude=magnitude, **kw)
+    far = (first + n) * 2.0 ** -51
+    steps = 3 if abs(magnitude) == 1 else 4
+    assert ((got - ref).abs() <= (steps * pc.FP32 + far) * abs(magnitude)).all()
