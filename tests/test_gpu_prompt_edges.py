@@ -349,3 +349,126 @@ def test_rope_table_bound(n, dim, first, kw, magnitude):
     far = (first + n) * 2.0 ** -51
     steps = 3 if abs(magnitude) == 1 else 4
     assert ((got - ref).abs() <= (steps * pc.FP32 + far) * abs(magnitude)).all()
+
+
+# ---------------------------------------------------------------------------- sizes
+@pytest.mark.parametrize("heads,kv_heads", [(128, 1), (1024, 8), (384, 1), (96, 1), (7, 7), (1000, 8), (5, 1)])
+@pytest.mark.parametrize("ql,kl", [([1, 6], [1, 300]), ([9], [2000])])
+def test_prompt_head_groups(heads, kv_heads, ql, kl):
+    """Groups of 128 heads in a tile and more, groups that no power of two fills."""
+    c = [t.cuda() for t in pc.prompt_case(ql, kl, heads, kv_heads, 128, True, seed=97)]
+    q, k, v, pe, cq, ck = c
+    out, lse, ws = smla.prompt_fwd(q, k, v, cq, ck, 0.09, k_pe=pe)
+    assert smla.read_status(ws)[0] == 0
+    ref = pc.prompt_reference(*c, 0.09, True)
+    pc.check_prompt(out, lse, ref)
+    pt.check_rows(out, lse, ref)
+
+
+def test_prompt_offsets_that_pass_32_bits():
+    """Queries and results of 2.6e9 values, keys and values of 3.3e9: the first request and the last ones."""
+    n, heads = 5000, 1024
+    g = torch.Generator(device="cuda").manual_seed(98)
+    q = torch.zeros(4 * n, heads, 128, dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros(40 * n, 64, 256, dtype=torch.bfloat16, device="cuda")
+    ends = [slice(0, 4), slice(4 * n - 8, 4 * n)]
+    for r in ends:
+        q[r] = torch.randn(q[r].shape, generator=g, device="cuda").to(torch.bfloat16)
+    keys = [slice(0, 40), slice(40 * n - 80, 40 * n)]
+    for r in keys:
+        kv[r] = torch.randn(kv[r].shape, generator=g, device="cuda").to(torch.bfloat16)
+    assert q.numel() > 2 ** 31 and kv.numel() > 2 ** 31
+    cq, ck = (torch.arange(0, (n + 1) * m, m, dtype=torch.int32, device="cuda") for m in (4, 40))
+    out, lse, ws = smla.prompt_fwd(q, kv[..., :128], kv[..., 128:], cq, ck, 0.09)
+    assert smla.read_status(ws)[0] == 0
+    for r, s, m in zip(ends, keys, (1, 2)):
+        ref = pc.prompt_reference(q[r], kv[s][..., :128], kv[s][..., 128:], None, pc.cu([4] * m), pc.cu([40] * m), 0.09, True)
+        pt.check_rows(out[r], lse[r], ref)
+    assert (out[4:4 * n - 8] == 0).all()
+
+
+def test_row_calls_with_offsets_that_pass_32_bits():
+    g = torch.Generator(device="cuda").manual_seed(99)
+    rows = 180000
+    x = torch.zeros(rows, 64, 192, dtype=torch.bfloat16, device="cuda")
+    assert x.numel() > 2 ** 31
+    for r in (slice(0, 5), slice(rows - 5, rows)):
+        x[r] = torch.randn(5, 64, 192, generator=g, device="cuda").to(torch.bfloat16)
+    was = {i: x[i].clone() for i in (0, rows - 1)}
+    pos, table = torch.full((rows,), 77, dtype=torch.int32, device="cuda"), smla.rope_table(100)
+    _, ws = smla.rope_apply(x[..., 128:], pos, table, out=x[..., 128:])
+    assert smla.read_status(ws)[0] == 0
+    for i, w in was.items():
+        ref, mag = pc.rotate(w[:, 128:].double().cpu(), table[77].cpu()[None], True)
+        pc.check_rotated(x[i][:, 128:].cpu(), ref, mag)
+        assert torch.equal(x[i][:, :128], w[:, :128])
+    del x
+    pages = 70000
+    c = _Cache(1)
+    c.kv = torch.zeros(pages, 64, 576, dtype=torch.bfloat16, device="cuda")
+    assert c.kv.numel() > 2 ** 31
+    c.k_idx = None
+    c.kv[pages - 1] = torch.randn(64, 576, generator=g, device="cuda").to(torch.bfloat16)
+    tab = torch.full((1, 3), pages - 1, dtype=torch.int32, device="cuda")
+    lat, pe, _, ws = smla.cache_read(c, tab, pc.cu([100], "cuda"), 100, starts=torch.tensor([64], dtype=torch.int32, device="cuda"))
+    assert smla.read_status(ws)[0] == 0
+    assert torch.equal(torch.cat([lat, pe], 1), c.kv[pages - 1].repeat(2, 1)[:100])
+
+
+# ---------------------------------------------------------------------------- graphs and threads
+@pytest.mark.parametrize("before,after,total_q,total_k", [
+    (([70, 9], [90, 20]), ([3, 60], [5, 200]), 100, 220),              # without a plan
+    (([300, 40, 0], [900, 60, 0]), ([1, 200, 500], [1, 800, 500]), 800, 1400),
+    (([2, 1, 5], [9000, 3, 17000]), ([5, 0, 1], [40, 0, 25000]), 8, 26100)])  # cut elsewhere
+def test_prompt_graph_replayed_on_other_bounds(before, after, total_q, total_k):
+    """The work is planned on the GPU: a captured call takes the bounds that it finds, bad ones too."""
+    q, k, v, pe, _, _ = (t.cuda() for t in pc.prompt_case([total_q], [total_k], 4, 4, 192, True, seed=100))
+    n = len(before[0])
+    cq, ck = pc.cu(before[0], "cuda"), pc.cu(before[1], "cuda")
+    out, lse = torch.zeros(total_q, 4, 128, device="cuda"), torch.zeros(total_q, 4, device="cuda")
+    ws = smla.workspace(smla.prompt_workspace_bytes(total_q, total_k, n, 4, 4))
+    call = lambda: smla.prompt_fwd(q, k, v, cq, ck, 0.07, k_pe=pe, out=out, lse=lse, ws=ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for ql, kl in (before, after, before):
+        cq.copy_(pc.cu(ql)), ck.copy_(pc.cu(kl))
+        out.fill_(7.0), lse.fill_(7.0)
+        g.replay()
+        assert smla.read_status(ws)[0] == 0
+        rows = sum(ql)
+        ref = pc.prompt_reference(q[:rows], k, v, pe, cq, ck, 0.07, True)
+        pt.check_rows(out[:rows], lse[:rows], ref)
+        assert (out[rows:] == 7).all() and (lse[rows:] == 7).all()
+        cq[0] = -1
+        g.replay()
+        assert smla.read_status(ws)[0] == 5
+
+
+def test_calls_from_several_threads():
+    """Each with a stream and a workspace of its own."""
+    import threading
+    cases = [([200 + 30 * i], [200 + 30 * i]) if i % 2 else ([2, 3], [3000 + 500 * i, 40]) for i in range(6)]
+    data = [[t.cuda() for t in pc.prompt_case(ql, kl, 4, 4, 192, True, seed=101 + i)] for i, (ql, kl) in enumerate(cases)]
+    alone = [smla.prompt_fwd(q, k, v, cq, ck, 0.07, k_pe=pe)[:2] for q, k, v, pe, cq, ck in data]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        q, k, v, pe, cq, ck = data[i]
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                out, lse, ws = smla.prompt_fwd(q, k, v, cq, ck, 0.07, k_pe=pe)
+                if smla.read_status(ws)[0] or not torch.equal(out, alone[i][0]) or not torch.equal(lse, alone[i][1]):
+                    bad.append(i)
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
